@@ -30,7 +30,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_status", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bw
            "fa_set_bwd_kernel",
            "fa_bwd_noalloc", "fa_fwd_mod", "fa_bwd_mod", "fa_fwd_split_count",
            "fa_fwd_split_workspace_bytes", "fa_fwd_split", "fa_lse_merge", "fa_wait_test",
-           "fa_bwd_noalloc_status")
+           "fa_bwd_noalloc_status", "fa_varlen_workspace_bytes", "fa_fwd_varlen",
+           "fa_bwd_varlen")
 
 
 class ScoreMod(ctypes.Structure):
@@ -39,6 +40,12 @@ class ScoreMod(ctypes.Structure):
     (device pointers or None)."""
     _fields_ = [("window_left", ctypes.c_int), ("window_right", ctypes.c_int),
                 ("alibi_slopes", ctypes.c_void_p), ("seqlens_k", ctypes.c_void_p)]
+
+
+class PackedStride(ctypes.Structure):
+    """fa_packed_stride: elements from one token, and from one head, to the next."""
+    _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
 
 _LIB = None
 
@@ -94,6 +101,14 @@ def _bind(lib):
     lib.fa_lse_merge.restype = i
     lib.fa_wait_test.argtypes = [vp, i, vp, vp]
     lib.fa_wait_test.restype = i
+    psp = ctypes.POINTER(PackedStride)
+    lib.fa_varlen_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.fa_varlen_workspace_bytes.restype = sz
+    lib.fa_fwd_varlen.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, psp, psp, psp, i, i, f,
+                                  vp, sz, vp]
+    lib.fa_fwd_varlen.restype = i
+    lib.fa_bwd_varlen.argtypes = [vp] * 10 + [i, i, i, i, i, psp, psp, psp, i, i, f, vp, sz, i, vp]
+    lib.fa_bwd_varlen.restype = i
     return lib
 
 
@@ -377,3 +392,174 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     """
     return _Attention.apply(q, k, v, causal, scale, window, alibi_slopes, deterministic,
                             seqlens_k)
+
+
+def _packed(t, name, heads=None, like=None):
+    """Checks a packed [T, H, D] bf16 CUDA tensor and returns its PackedStride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [T, H, D] with contiguous elements")
+    if like is not None and (t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]
+                             or t.device != like.device):
+        raise ValueError(f"{name} must have q's tokens, head dimension and device")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} must have {heads} heads")
+    # the stride of a dimension of one element is arbitrary: give the kernel a valid one
+    T, H, D = t.shape
+    head = t.stride(1) if H > 1 else D
+    token = t.stride(0) if T > 1 else max(H * D, head)
+    return PackedStride(token, head)
+
+
+def _out(t, shape, dtype, device, name, stream):
+    """A checked output of the caller, or a new one that `stream` may write."""
+    if t is not None:
+        if (not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape)
+                or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {tuple(shape)}")
+        return t
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:  # keep its memory until that stream has passed
+        t.record_stream(stream)
+    return t
+
+
+def _workspace(t, nbytes, device, stream):
+    """The caller's workspace, or a new one of nbytes that `stream` may use."""
+    if t is not None:
+        if not t.is_cuda or t.device != device or not t.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        return t
+    return _out(None, (max(nbytes, 1),), torch.uint8, device, "workspace", stream)
+
+
+def _int32(t, n, device, name):
+    """Checks an int32 CUDA vector of n elements (n None: any number above one)."""
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device
+            or t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != 1):
+        raise TypeError(f"{name} must be a contiguous int32 vector on the inputs' device")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return t
+
+
+def _var_window(causal, window):
+    if window is None:
+        return -1, (0 if causal else -1)
+    if causal:
+        raise ValueError("give the causal mask as window=(-1, 0), not with causal=True")
+    return int(window[0]), int(window[1])
+
+
+def varlen_workspace_bytes(B, T, Hq, Hkv, D, backward=False, deterministic=False) -> int:
+    return int(lib().fa_varlen_workspace_bytes(B, T, Hq, Hkv, D, int(bool(backward)),
+                                               int(bool(deterministic))))
+
+
+def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+               causal: bool = False, scale: float | None = None, window=None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """Forward attention over packed sequences (fa_fwd_varlen).
+
+    q [T,Hq,D], k/v [T,Hkv,D] bf16 CUDA, elements contiguous, tokens and heads at
+    any stride that is a multiple of 8 (slices of a fused projection);
+    ``cu_seqlens`` int32 [B+1]: sequence b is tokens cu_seqlens[b] ..
+    cu_seqlens[b+1]-1.  ``causal`` / ``window`` as in fwd, inside each sequence.
+    Returns (o [T,Hq,D] bf16, lse [Hq,T] fp32); tokens of no sequence are not
+    written.  fwd_status() reports a cu_seqlens that does not ascend in [0, T].
+    """
+    qs = _packed(q, "q")
+    T, Hq, D = q.shape
+    ks = _packed(k, "k", None, q)
+    Hkv = k.shape[1]
+    vs = _packed(v, "v", Hkv, q)
+    wl, wr = _var_window(causal, window)
+    B = _int32(cu_seqlens, None, q.device, "cu_seqlens").numel() - 1
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(q.device):
+        out = _out(out, (T, Hq, D), torch.bfloat16, q.device, "out", stream)
+        lse = _out(lse, (Hq, T), torch.float32, q.device, "lse", stream)
+        workspace = _workspace(workspace, varlen_workspace_bytes(B, T, Hq, Hkv, D), q.device, stream)
+        rc = lib().fa_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
+                                 B, T, Hq, Hkv, D, ctypes.byref(qs), ctypes.byref(ks),
+                                 ctypes.byref(vs), wl, wr, float(scale), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_fwd_varlen", rc)
+    return out, lse
+
+
+def bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal: bool = False, scale: float | None = None,
+               window=None, deterministic: bool = False, workspace: torch.Tensor | None = None,
+               dq=None, dk=None, dv=None, stream=None):
+    """Backward of fwd_varlen (fa_bwd_varlen).  Returns (dq [T,Hq,D], dk, dv
+    [T,Hkv,D]) bf16, contiguous; tokens of no sequence are not written.  o, do
+    and lse are contiguous; the other arguments as in fwd_varlen, and as given
+    to it."""
+    qs = _packed(q, "q")
+    T, Hq, D = q.shape
+    ks = _packed(k, "k", None, q)
+    Hkv = k.shape[1]
+    vs = _packed(v, "v", Hkv, q)
+    for t, n in ((o, "o"), (do, "do")):
+        _packed(t, n, Hq, q)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    _out(lse, (Hq, T), torch.float32, q.device, "lse", None)
+    wl, wr = _var_window(causal, window)
+    B = _int32(cu_seqlens, None, q.device, "cu_seqlens").numel() - 1
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(q.device):
+        need = varlen_workspace_bytes(B, T, Hq, Hkv, D, True, deterministic)
+        workspace = _workspace(workspace, need, q.device, stream)
+        dq = _out(dq, q.shape, torch.bfloat16, q.device, "dq", stream)
+        dk = _out(dk, k.shape, torch.bfloat16, q.device, "dk", stream)
+        dv = _out(dv, v.shape, torch.bfloat16, q.device, "dv", stream)
+        rc = lib().fa_bwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
+                                 _ptr(dk), _ptr(dv), _ptr(cu_seqlens), B, T, Hq, Hkv, D,
+                                 ctypes.byref(qs), ctypes.byref(ks), ctypes.byref(vs), wl, wr,
+                                 float(scale), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(),
+                                 int(bool(deterministic)), _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_bwd_varlen", rc)
+    return dq, dk, dv
+
+
+class _AttentionVarlen(torch.autograd.Function):
+    """fwd_varlen in forward (saving O and LSE), bwd_varlen in backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, causal, scale, window, deterministic):
+        # tokens of no sequence: zeros, so that neither O nor a gradient holds
+        # uninitialised memory
+        o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        _, lse = fwd_varlen(q, k, v, cu_seqlens, causal=causal, scale=scale, window=window, out=o)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        ctx.args = (causal, scale, window, deterministic)
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        causal, scale, window, deterministic = ctx.args
+        grads = [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+        bwd_varlen(q, k, v, o, do.contiguous(), lse, cu_seqlens, causal=causal, scale=scale,
+                   window=window, deterministic=deterministic, dq=grads[0], dk=grads[1],
+                   dv=grads[2])
+        return (*grads, None, None, None, None, None)
+
+
+def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     causal: bool = False, scale: float | None = None, window=None,
+                     deterministic: bool = False) -> torch.Tensor:
+    """attention() over packed sequences: q [T,Hq,D], k/v [T,Hkv,D] bf16 CUDA,
+    ``cu_seqlens`` int32 [B+1] (see fwd_varlen).  Tokens of no sequence get zeros
+    in O and in every gradient.  Returns O [T,Hq,D] bf16."""
+    return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic)

@@ -9,6 +9,7 @@
 
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "var_common.cuh"
 
 namespace fa {
 
@@ -36,8 +37,8 @@ __device__ __forceinline__ int bwd_kv_len(const BwdArgs& a, int b) {
 // batch with kv_len keys): the queries from (first key - wr) to (last key +
 // wl); empty when the tile holds no key of the batch
 template <bool kMod, int QB>
-__device__ __forceinline__ void bwd_qblk_range(const BwdArgs& a, int j, int kv_len, int& lo,
-                                               int& hi) {
+__device__ __forceinline__ void bwd_qblk_range(const BwdArgs& a, int Sq, int j, int kv_len,
+                                               int& lo, int& hi) {
   const int wl = win_left<kMod>(a), wr = win_right<kMod>(a);
   const int k0 = j * kTile;
   if (k0 >= kv_len) {
@@ -46,7 +47,7 @@ __device__ __forceinline__ void bwd_qblk_range(const BwdArgs& a, int j, int kv_l
   }
   const int k1 = min(kv_len, k0 + kTile) - 1;
   const int q_lo = wr >= 0 ? max(0, k0 - wr) : 0;
-  const int q_hi = wl >= 0 ? min(a.Sq - 1, k1 + wl) : a.Sq - 1;
+  const int q_hi = wl >= 0 ? min(Sq - 1, k1 + wl) : Sq - 1;
   lo = q_lo / QB;
   hi = q_hi >= q_lo ? q_hi / QB + 1 : lo;
 }
@@ -64,7 +65,7 @@ __device__ __forceinline__ int qblk_first_contributor(int wl, int iq) {
 template <bool kMod, int QB>
 __device__ __forceinline__ bool tile_adds_to(const BwdArgs& a, int j, int kv_len, int iq) {
   int lo, hi;
-  bwd_qblk_range<kMod, QB>(a, j, kv_len, lo, hi);
+  bwd_qblk_range<kMod, QB>(a, a.Sq, j, kv_len, lo, hi);
   return lo <= iq && iq < hi;
 }
 
@@ -179,6 +180,9 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&w)[N]) 
 struct BwdUnit {
   int bhk, j, b, hk, lo, n_blk, n_it;
   int kv_len;  // keys of batch b
+  // packed calls: the sequence's first row, and its first row where each one
+  // is padded to 64; its queries and keys are kv_len, bhk is the kv head
+  int row0, pad0;
 };
 
 // The r-th unit this CTA processes under static dealing (-1 when it has no
@@ -231,7 +235,26 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u, int group) 
   w.kv_len = bwd_kv_len<kMod>(a, w.b);
   if (a.desc) w.j = a.n_ktiles - 1 - w.j;  // each head's tiles highest first
   int hi;
-  bwd_qblk_range<kMod, QB>(a, w.j, w.kv_len, w.lo, hi);
+  bwd_qblk_range<kMod, QB>(a, a.Sq, w.j, w.kv_len, w.lo, hi);
+  w.n_blk = hi - w.lo;
+  w.n_it = group * w.n_blk;
+  return w;
+}
+
+// Unit u of a packed call: (item, kv head), the head running fastest.
+template <bool kMod, int QB>
+__device__ __forceinline__ BwdUnit bwd_unit_var(const BwdArgs& a, int u, int group) {
+  BwdUnit w;
+  const int item = u / a.Hkv;
+  const VarItem it = load_item(a.items, item);
+  w.hk = w.bhk = u - item * a.Hkv;
+  w.b = it.b;
+  w.j = it.tile;
+  w.kv_len = it.len;
+  w.row0 = it.row0;
+  w.pad0 = a.items[item].pad0;
+  int hi;
+  bwd_qblk_range<kMod, QB>(a, it.len, w.j, it.len, w.lo, hi);
   w.n_blk = hi - w.lo;
   w.n_it = group * w.n_blk;
   return w;
@@ -260,8 +283,8 @@ __device__ __forceinline__ BwdUnit bwd_unit_pair(const BwdArgs& a, int u, int gr
   w.kv_len = bwd_kv_len<kMod>(a, w.b);
   w.j = 2 * jp + rank;
   int lo0, hi0, lo1 = 0, hi1 = 0;
-  bwd_qblk_range<kMod, QB>(a, 2 * jp, w.kv_len, lo0, hi0);
-  if (2 * jp + 1 < a.n_ktiles) bwd_qblk_range<kMod, QB>(a, 2 * jp + 1, w.kv_len, lo1, hi1);
+  bwd_qblk_range<kMod, QB>(a, a.Sq, 2 * jp, w.kv_len, lo0, hi0);
+  if (2 * jp + 1 < a.n_ktiles) bwd_qblk_range<kMod, QB>(a, a.Sq, 2 * jp + 1, w.kv_len, lo1, hi1);
   int lo, hi;
   if (hi0 <= lo0) {
     lo = lo1, hi = hi1;

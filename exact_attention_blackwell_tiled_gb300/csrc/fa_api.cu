@@ -84,6 +84,8 @@ int check_mod(const ModArgs& m) {
 // The exact causal window keeps the causal schedules (longest units first).
 int is_causal(const ModArgs& m) { return (m.wl < 0 && m.wr == 0) ? 1 : 0; }
 
+}  // namespace
+
 int check_device() {
   int dev;
   DeviceInfo info;
@@ -99,7 +101,7 @@ int check_device() {
   return FA_OK;
 }
 
-}  // namespace
+void reset_launches() { t_launches = 0; }
 
 void note_launches(int n) { t_launches += n; }
 
@@ -138,10 +140,15 @@ bool current_device(int* dev, DeviceInfo* out) {
 }
 
 bool make_tmap_bsd(CUtensorMap* map, const void* base, int BH, int S, int D, int box_rows) {
+  return make_tmap_strided(map, base, BH, S, D, D, (long long)S * D, box_rows);
+}
+
+bool make_tmap_strided(CUtensorMap* map, const void* base, int H, int S, int D,
+                       long long row_stride, long long head_stride, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)BH};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)S * D * 2};
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)H};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)head_stride * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,

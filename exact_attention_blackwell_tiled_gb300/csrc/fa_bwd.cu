@@ -188,6 +188,79 @@ __global__ void __launch_bounds__(256) bwd_preprocess(const BwdArgs a) {
   }
 }
 
+// The same for a packed batch: a block takes (kv-tile item, q head) pairs of the
+// plan, whose 128 rows are also a tile of the sequence's queries.  Rows up to the
+// next multiple of 64 get LSE2 = +inf and Delta = 0.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int kLanesPerRow = D / 8;
+  constexpr int kRowsPerStep = 32 / kLanesPerRow;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane / kLanesPerRow, seg = lane % kLanesPerRow;
+  const int n_units = *a.n_items * a.Hq;
+  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+    const int item = u / a.Hq, h = u - item * a.Hq;
+    const VarItem it = load_item(a.items, item);
+    const int pad0 = a.items[item].pad0;
+    const int i0 = it.tile * kTile;
+    const int i1 = min(i0 + kTile, (it.len + kQB - 1) / kQB * kQB);
+    // kTile / 8 = 16 rows per warp, kPreUnroll steps of them in flight
+#pragma unroll 1
+    for (int s0 = 0; s0 < kTile / 8; s0 += kRowsPerStep * kPreUnroll) {
+      uint4 ov[kPreUnroll], gv[kPreUnroll];
+#pragma unroll
+      for (int x = 0; x < kPreUnroll; ++x) {
+        const int i = i0 + warp * (kTile / 8) + s0 + x * kRowsPerStep + sub;
+        ov[x] = gv[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < it.len && s0 + x * kRowsPerStep < kTile / 8) {
+          const size_t off = ((size_t)(it.row0 + i) * a.Hq + h) * D + seg * 8;
+          ov[x] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.o) + off);
+          gv[x] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.dO) + off);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kPreUnroll; ++x) {
+        const int i = i0 + warp * (kTile / 8) + s0 + x * kRowsPerStep + sub;
+        const uint32_t* ow = &ov[x].x;
+        const uint32_t* gw = &gv[x].x;
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 of = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ow[e]));
+          const float2 gf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e]));
+          acc = fmaf(of.x, gf.x, acc);
+          acc = fmaf(of.y, gf.y, acc);
+        }
+#pragma unroll
+        for (int sft = kLanesPerRow / 2; sft > 0; sft >>= 1)
+          acc += __shfl_xor_sync(0xffffffffu, acc, sft);
+        if (i < i1 && s0 + x * kRowsPerStep < kTile / 8) {
+          const bool real = i < it.len;
+          if (seg == 0) {
+            const size_t v = (size_t)h * a.T_pad + pad0 + i;
+            a.delta[v] = acc;
+            a.lse2[v] = real ? a.lse[(size_t)h * a.T + it.row0 + i] * 1.4426950408889634f : INFINITY;
+          }
+          if (!a.deterministic && real) {
+            float4* dqa = reinterpret_cast<float4*>(
+                a.dq_acc + ((size_t)h * a.T + it.row0 + i) * D + seg * 8);
+            dqa[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+            dqa[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      }
+    }
+  }
+  if (a.deterministic) {
+    const long long nsem = (long long)a.dq_groups * a.sem_group_stride;
+    for (long long s = (long long)blockIdx.x * blockDim.x + threadIdx.x; s < nsem;
+         s += (long long)gridDim.x * blockDim.x)
+      a.sem[s] = 0;
+  }
+}
+
 // ------------------------------------------------------------------ main kernel
 
 template <int D>
@@ -249,8 +322,11 @@ struct BwdSmem {
 };
 
 // kMod: a sliding window and / or the relative-position bias (a.alibi); the
-// plain kernel applies no mask or the causal one.
-template <int D, bool kMod>
+// plain kernel applies no mask or the causal one.  kVar: a packed batch, with
+// tensor maps a.maps[4 b + 0..3] (q, k, v, dO) that end at the sequence's last
+// row, so that rows past it arrive as zeros; the dQ accumulators hold no padding
+// rows, so a block's rows past the end are not added.
+template <int D, bool kMod, bool kVar>
 __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     bwd_main(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -306,7 +382,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == R::kTmaWarp && lane == 0) {
+  if (!kVar && warp == R::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -321,6 +397,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
+  const int n_units = kVar ? *a.n_items * a.Hkv : a.n_units;
   // The r-th unit of this CTA.  Static dealing: computed by every role alike.
   // Dynamic dealing: the TMA thread takes the next unit number from the global
   // counter and posts it in ring slot r % kURing (take_unit); the other roles
@@ -332,7 +409,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     const int s = r % L::kURing;
     if (!mbar_wait(bar(L::kBarUEmpty + s), ((r / L::kURing) & 1) ^ 1, abort_flag)) return -1;
     int u = atomicAdd(a.unit_counter, 1);
-    if (u >= a.n_units) u = -1;
+    if (u >= n_units) u = -1;
     uring[s] = u;
     mbar_arrive(bar(L::kBarUFull + s));
     return u;
@@ -347,12 +424,33 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     if (!warp_wide || lane == 0) mbar_arrive(bar(L::kBarUEmpty + s));
     return u;
   };
-  auto unit_of = [&](int u) { return bwd_unit<kMod, kQB>(a, u, group); };
+  auto unit_of = [&](int u) {
+    if constexpr (kVar) return bwd_unit_var<kMod, kQB>(a, u, group);
+    else return bwd_unit<kMod, kQB>(a, u, group);
+  };
+  // the q head of the tensor maps' head coordinate, and (bh, block iq)'s places
+  // in lse2 / delta, in the dQ accumulators and among the semaphores
+  auto head_of = [&](const BwdUnit& w, int gi) {
+    return (kVar ? 0 : w.b * a.Hq) + w.hk * group + gi;
+  };
+  auto vec_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
+    return kVar ? (size_t)bh * a.T_pad + w.pad0 + (size_t)iq * kQB
+                : (size_t)bh * a.Sq_pad + (size_t)iq * kQB;
+  };
+  auto acc_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
+    return (kVar ? (size_t)bh * a.T + w.row0 + (size_t)iq * kQB
+                 : (size_t)bh * a.Sq_pad + (size_t)iq * kQB) * D;
+  };
+  auto sem_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
+    return (size_t)bh * a.n_qblk + (kVar ? w.pad0 / kQB : 0) + iq;
+  };
 
   if (warp == R::kTmaWarp) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0, unit = 0;
+      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
+      const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v, *mdo = &tm_do;
       bool ok = true;
       // K_j and V_j of a unit, once every issuer is done with the previous ones
       auto load_kv = [&](const BwdUnit& w, uint32_t un) -> bool {
@@ -360,15 +458,25 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
         mbar_arrive_expect_tx(bar(L::kBarKVFull), 2 * L::kKVTileBytes);
 #pragma unroll
         for (int cb = 0; cb < L::kColBlocks; ++cb) {
-          tma_load_3d(sbase + L::kOffK + cb * L::kKVBlockBytes, &tm_k, bar(L::kBarKVFull),
+          tma_load_3d(sbase + L::kOffK + cb * L::kKVBlockBytes, mk, bar(L::kBarKVFull),
                       cb * 64, w.j * kTile, w.bhk);
-          tma_load_3d(sbase + L::kOffV + cb * L::kKVBlockBytes, &tm_v, bar(L::kBarKVFull),
+          tma_load_3d(sbase + L::kOffV + cb * L::kKVBlockBytes, mv, bar(L::kBarKVFull),
                       cb * 64, w.j * kTile, w.bhk);
         }
         return true;
       };
       for (int ri = 0, u = take_unit(0); ok && u >= 0; u = take_unit(++ri), ++unit) {
         const BwdUnit w = unit_of(u);
+        if constexpr (kVar) {
+          mq = a.maps + 4 * (size_t)w.b;
+          mk = mq + 1;
+          mv = mq + 2;
+          mdo = mq + 3;
+          if (w.b != last_b) {  // the plan kernel wrote these maps
+            for (int i = 0; i < 4; ++i) tmap_acquire(mq + i);
+            last_b = w.b;
+          }
+        }
         // The unit's first block's Q / dO go out before its K / V: its stage
         // frees up while the previous unit still holds K and V, so it has landed
         // by the time K and V can be replaced.  Later blocks follow K and V, which
@@ -380,7 +488,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
           }
           const int gi = t / w.n_blk;
           const int iq = w.lo + (t - gi * w.n_blk);
-          const int bh = w.b * a.Hq + w.hk * group + gi;
+          const int bh = head_of(w, gi);
           const uint32_t st = it % L::kStages;
           if (!mbar_wait(bar(L::kBarQEmpty + st), ((it / L::kStages) & 1) ^ 1, abort_flag)) {
             ok = false;
@@ -390,12 +498,12 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
           mbar_arrive_expect_tx(bar(L::kBarQFull + st), 2 * L::kQTileBytes + 2 * kQB * 4);
 #pragma unroll
           for (int cb = 0; cb < L::kColBlocks; ++cb) {
-            tma_load_3d(sdst + cb * L::kQBlockBytes, &tm_q, bar(L::kBarQFull + st), cb * 64,
+            tma_load_3d(sdst + cb * L::kQBlockBytes, mq, bar(L::kBarQFull + st), cb * 64,
                         iq * kQB, bh);
-            tma_load_3d(sdst + L::kQTileBytes + cb * L::kQBlockBytes, &tm_do,
+            tma_load_3d(sdst + L::kQTileBytes + cb * L::kQBlockBytes, mdo,
                         bar(L::kBarQFull + st), cb * 64, iq * kQB, bh);
           }
-          const size_t voff = (size_t)bh * a.Sq_pad + (size_t)iq * kQB;
+          const size_t voff = vec_off(w, bh, iq);
           bulk_load(sdst + 2 * L::kQTileBytes, a.lse2 + voff, kQB * 4, bar(L::kBarQFull + st));
           bulk_load(sdst + 2 * L::kQTileBytes + kQB * 4, a.delta + voff, kQB * 4,
                     bar(L::kBarQFull + st));
@@ -732,7 +840,9 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
       for (int t = 0; t < w.n_it; ++t, ++it) {
         const int gi = t / w.n_blk;
         const int iq = w.lo + (t - gi * w.n_blk);
-        const int bh = w.b * a.Hq + w.hk * group + gi;
+        const int bh = head_of(w, gi);
+        // query rows of the block that exist (kVar)
+        const int n_rows = kVar ? w.kv_len - iq * kQB : kQB;
         if (kSemWarp && a.deterministic && wq >= kAddWarps) {
           if (wq == kAddWarps) {
             // once drain warps 0-1 have added block it (their arrives release
@@ -745,7 +855,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
               } else {
                 mbar_arrive(bar(L::kBarDQAddedFree));
                 int* sem = a.sem + (size_t)(w.j % a.dq_groups) * a.sem_group_stride +
-                           (size_t)bh * a.n_qblk + iq;
+                           sem_off(w, bh, iq);
                 asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(sem) : "memory");
               }
             }
@@ -765,7 +875,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
         if (!a.deterministic) {
           // two 32-column halves, so that only 32 values are live at a time;
           // the columns are released once the second half is read
-          float* dst = a.dq_acc + ((size_t)bh * a.Sq_pad + (size_t)iq * kQB) * D + r;
+          float* dst = a.dq_acc + acc_off(w, bh, iq) + r;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t v[32];
@@ -777,6 +887,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
             if (r < D) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
+                if (kVar && hf * 32 + e >= n_rows) break;
                 asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(
                                  dst + (size_t)(hf * 32 + e) * D),
                              "f"(u2f(v[e]))
@@ -804,9 +915,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
                         w.j) / a.dq_groups
                      : (w.j - group_first(qblk_first_contributor<kQB>(win_left<kMod>(a), iq), g,
                                           a.dq_groups)) / a.dq_groups;
-          float* dst = a.dq_acc + (size_t)g * a.dq_group_stride +
-                       ((size_t)bh * a.Sq_pad + (size_t)iq * kQB) * D + r;
-          int* sem = a.sem + (size_t)g * a.sem_group_stride + (size_t)bh * a.n_qblk + iq;
+          float* dst = a.dq_acc + (size_t)g * a.dq_group_stride + acc_off(w, bh, iq) + r;
+          int* sem = a.sem + (size_t)g * a.sem_group_stride + sem_off(w, bh, iq);
           if (wq < kAddWarps && turn > 0) {
             // the semaphore counts the group's finished adding warps (with
             // the semaphore warp: the group's finished tiles)
@@ -834,10 +944,12 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
             if (good && r < D) {
               if (turn == 0) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) dst[(size_t)(hf * 32 + e) * D] = u2f(v[e]);
+                for (int e = 0; e < 32; ++e)
+                  if (!kVar || hf * 32 + e < n_rows) dst[(size_t)(hf * 32 + e) * D] = u2f(v[e]);
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
+                  if (!kVar || hf * 32 + e < n_rows)
                   asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(
                                    dst + (size_t)(hf * 32 + e) * D),
                                "f"(u2f(v[e]))
@@ -871,8 +983,12 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
       // transpose) so that lane 4k+i writes piece i of rows 4k..4k+3.
       const int grp = lane & ~3, pc = lane & 3;
       const int row0 = w.j * kTile + wq * 32 + grp;  // first key row of the lane group
-      __nv_bfloat16* dk_base = reinterpret_cast<__nv_bfloat16*>(a.dk) + (size_t)w.bhk * a.Sk * D;
-      __nv_bfloat16* dv_base = reinterpret_cast<__nv_bfloat16*>(a.dv) + (size_t)w.bhk * a.Sk * D;
+      // dK / dV rows: [B, Hkv, Sk, D], or [T, Hkv, D] in packed calls
+      const int Sk = kVar ? w.kv_len : a.Sk;
+      const size_t kv_off = kVar ? ((size_t)w.row0 * a.Hkv + w.hk) * D : (size_t)w.bhk * Sk * D;
+      const size_t kv_row = kVar ? (size_t)a.Hkv * D : (size_t)D;
+      __nv_bfloat16* dk_base = reinterpret_cast<__nv_bfloat16*>(a.dk) + kv_off;
+      __nv_bfloat16* dv_base = reinterpret_cast<__nv_bfloat16*>(a.dv) + kv_off;
       // 32 columns of dK, then of dV, per pass (the register budget of 768
       // threads holds one 32-column group at a time)
 #pragma unroll 1
@@ -907,8 +1023,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
         __nv_bfloat16* base = is_v ? dv_base : dk_base;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          if (row0 + m < a.Sk) {
-            const size_t off = (size_t)(row0 + m) * D + c * 32 + pc * 8;
+          if (row0 + m < Sk) {
+            const size_t off = (row0 + m) * kv_row + c * 32 + pc * 8;
             *reinterpret_cast<uint4*>(base + off) =
                 make_uint4(wk[4 * m], wk[4 * m + 1], wk[4 * m + 2], wk[4 * m + 3]);
           }
@@ -967,6 +1083,47 @@ __global__ void __launch_bounds__(256) bwd_dq_convert(const BwdArgs a) {
   }
 }
 
+// The same for a packed batch, over (kv-tile item, q head) pairs of the plan;
+// dQ is [T, Hq, D], and rows of no sequence are left as they are.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
+  grid_dep_wait();
+  constexpr int kPerRow = D / 8;
+  const int n_units = *a.n_items * a.Hq;
+  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+    const int item = u / a.Hq, h = u - item * a.Hq;
+    const VarItem it = load_item(a.items, item);
+    const int pad0 = a.items[item].pad0;
+    const int rows = min(kTile, it.len - it.tile * kTile);
+    for (int x = threadIdx.x; x < rows * kPerRow; x += blockDim.x) {
+      const int i = it.tile * kTile + x / kPerRow, c8 = x % kPerRow;
+      const float* base = a.dq_acc + ((size_t)h * a.T + it.row0 + i) * D + c8 * 8;
+      float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+      if (!a.deterministic) {
+        x0 = reinterpret_cast<const float4*>(base)[0];
+        x1 = reinterpret_cast<const float4*>(base)[1];
+      } else {
+        // in fixed order, the groups that some kv tile wrote for this block
+        const int* sem = a.sem + (size_t)h * a.n_qblk + (pad0 + i) / kQB;
+        for (int g = 0; g < a.dq_groups; ++g) {
+          if (sem[(size_t)g * a.sem_group_stride] == 0) continue;
+          const float4* src = reinterpret_cast<const float4*>(base + (size_t)g * a.dq_group_stride);
+          const float4 y0 = src[0], y1 = src[1];
+          x0.x += y0.x, x0.y += y0.y, x0.z += y0.z, x0.w += y0.w;
+          x1.x += y1.x, x1.y += y1.y, x1.z += y1.z, x1.w += y1.w;
+        }
+      }
+      uint4 w;
+      w.x = pack_bf16x2(x0.x * a.scale, x0.y * a.scale);
+      w.y = pack_bf16x2(x0.z * a.scale, x0.w * a.scale);
+      w.z = pack_bf16x2(x1.x * a.scale, x1.y * a.scale);
+      w.w = pack_bf16x2(x1.z * a.scale, x1.w * a.scale);
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.dq) +
+                                ((size_t)(it.row0 + i) * a.Hq + h) * D + c8 * 8) = w;
+    }
+  }
+}
+
 std::atomic<int> g_bwd_kernel{FA_BWD_KERNEL_AUTO};
 
 template <int D>
@@ -978,9 +1135,9 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(bwd_main<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(bwd_main<D, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kAllocBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(bwd_main<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(bwd_main<D, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kAllocBytes) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
@@ -1004,7 +1161,7 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
     // general kernel
     const bool mod =
         a.alibi || a.seqlens_k || !(a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal)));
-    const auto kernel = mod ? bwd_main<D, true> : bwd_main<D, false>;
+    const auto kernel = mod ? bwd_main<D, true, false> : bwd_main<D, false, false>;
     const int threads =
         (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
     record_timing(false, stream);
@@ -1076,6 +1233,65 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
 int launch_bwd(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream) {
   if (a.D == 128) return launch_bwd_d<128>(m, a, stream);
   if (a.D == 64) return launch_bwd_d<64>(m, a, stream);
+  return FA_ERR_UNSUPPORTED;
+}
+
+template <int D>
+static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
+                            cudaStream_t stream) {
+  using L = BwdSmem<D>;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
+  static bool attr_done[64] = {};
+  if (dev < 64 && !attr_done[dev]) {
+    if (cudaFuncSetAttribute(bwd_main<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::kAllocBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(bwd_main<D, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::kAllocBytes) != cudaSuccess)
+      return FA_ERR_CUDA;
+    attr_done[dev] = true;
+  }
+  const int sms = info.sm_count;
+  const long long q_units = (long long)max_items * a.Hq, kv_units = (long long)max_items * a.Hkv;
+  const int small_grid = (int)(q_units < 8LL * sms ? q_units : 8LL * sms);
+  const int grid = (int)(kv_units < sms ? kv_units : sms);
+  if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  // units come from the global counter in the plan's order (longest first, each
+  // sequence's kv tiles ascending, which is also the order of the deterministic
+  // mode's chain)
+  a.dyn = 1;
+  const bool mod = !(a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal)));
+  const auto kernel = mod ? bwd_main<D, true, true> : bwd_main<D, false, true>;
+  const int threads = (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
+  record_timing(false, stream);
+  if (a.deterministic) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = L::kAllocBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // every block resident: the chain waits
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, any, any, any, any, a) != cudaSuccess) return FA_ERR_CUDA;
+  } else if (launch_pdl(kernel, dim3(grid), dim3(threads), L::kAllocBytes, stream, any, any, any,
+                        any, a) != cudaSuccess) {
+    return FA_ERR_CUDA;
+  }
+  record_timing(true, stream);
+  if (launch_pdl(bwd_dq_convert_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(3);
+  return FA_OK;
+}
+
+int launch_bwd_var(const CUtensorMap& any, const BwdArgs& a, int max_items, cudaStream_t stream) {
+  if (a.D == 128) return launch_bwd_var_d<128>(any, a, max_items, stream);
+  if (a.D == 64) return launch_bwd_var_d<64>(any, a, max_items, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

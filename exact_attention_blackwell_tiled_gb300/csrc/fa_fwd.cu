@@ -80,7 +80,11 @@ struct FwdLayout {
 // kMod: 0 plain (no mask or the causal one), 1 a sliding window, 2 a window
 // and the relative-position bias (a.alibi) added to every score.  kSplit: a
 // unit covers one split of the kv tiles and writes fp32 parts for the merge.
-template <int D, int kMod, bool kSplit>
+// kVar: a packed batch.  Its tensor maps are a.maps[3 b + 0 / 1 / 2], one set
+// per sequence that ends at the sequence's last row, so that a tile's rows past
+// it arrive as zeros, never as another sequence's (or uninitialised) rows,
+// whose infinities or NaN would survive a weight of zero in GEMM 2.
+template <int D, int kMod, bool kSplit, bool kVar>
 __global__ void __launch_bounds__(320, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (!kVar && warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -132,7 +136,12 @@ __global__ void __launch_bounds__(320, 1)
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
+  const int n_units = kVar ? *a.n_items * a.Hq : a.n_units;
   constexpr bool kWin = kMod >= 1, kBias = kMod == 2;
+  // packed calls keep every exponential on MUFU: the cubic's 7.5e-5 would be
+  // the largest error of their LSE by two orders of magnitude, for the 1-2% of
+  // the time that it saves at D = 64
+  constexpr int kPoly = kVar ? 0 : L::kPolyPairs;
   // the window; plain calls carry only the causal flag
   const int wl = kWin ? a.wl : -1;
   const int wr = kWin ? a.wr : (a.causal ? 0 : -1);
@@ -140,6 +149,7 @@ __global__ void __launch_bounds__(320, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t kv_it = 0, q_it = 0;
+      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
       bool ok = true;
       auto load_kv = [&](const CUtensorMap* tm, int bhk, int j) -> bool {
         const uint32_t st = kv_it % L::kKVStages;
@@ -154,14 +164,26 @@ __global__ void __launch_bounds__(320, 1)
         ++kv_it;
         return true;
       };
-      for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
-        int bh, pair, split;
-        unit_coords(a, u, bh, pair, split);
-        const int b = bh / a.Hq, h = bh - b * a.Hq;
-        const int bhk = b * a.Hkv + h / group;
+      for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const int pair = w.pair;
+        const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<kSplit>(a, wl, wr, batch_kv_len<kWin>(a, b), pair, split, lo, hi, jlo, nmax);
+        pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), pair, w.split, lo, hi,
+                             jlo, nmax);
         if (nmax == 0) continue;
+        const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v;
+        if constexpr (kVar) {
+          mq = a.maps + 3 * (size_t)w.b;
+          mk = mq + 1;
+          mv = mq + 2;
+          if (w.b != last_b) {  // the plan kernel wrote these maps
+            tmap_acquire(mq);
+            tmap_acquire(mk);
+            tmap_acquire(mv);
+            last_b = w.b;
+          }
+        }
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
           ok = false;
@@ -173,11 +195,11 @@ __global__ void __launch_bounds__(320, 1)
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int cb = 0; cb < L::kColBlocks; ++cb)
-            tma_load_3d(qdst + t * L::kTileBytes + cb * L::kBlockBytes, &tm_q,
-                        bar(L::kBarQFull + qs), cb * 64, (2 * pair + t) * kTile, bh);
+            tma_load_3d(qdst + t * L::kTileBytes + cb * L::kBlockBytes, mq,
+                        bar(L::kBarQFull + qs), cb * 64, (2 * pair + t) * kTile, w.bh);
         ++q_it;
         for (int j = jlo; j < jlo + nmax; ++j) {
-          if (!load_kv(&tm_k, bhk, j) || !load_kv(&tm_v, bhk, j)) { ok = false; break; }
+          if (!load_kv(mk, bhk, j) || !load_kv(mv, bhk, j)) { ok = false; break; }
         }
       }
       // Let every issued copy land before the CTA can exit.
@@ -196,14 +218,13 @@ __global__ void __launch_bounds__(320, 1)
       uint32_t p_seen[2] = {0u, 0u};  // P-ready phases consumed, per tile
       uint32_t units_t[2] = {0u, 0u};  // units with work, per tile (O-free phases)
       bool ok = true;
-      for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
-        int bh, pair, split;
-        unit_coords(a, u, bh, pair, split);
+      for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+        const FwdUnit w = fwd_unit<kVar>(a, u);
         // kv tile j sits at position p = j - jlo of the pair's range; tile t
         // computes S for positions [plo[t], phi[t]) and O one position behind
         int plo[2], phi[2], jlo, nmax;
-        pair_kv_span<kSplit>(a, wl, wr, batch_kv_len<kWin>(a, bh / a.Hq), pair, split, plo, phi,
-                             jlo, nmax);
+        pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), w.pair, w.split, plo,
+                             phi, jlo, nmax);
         if (nmax == 0) continue;
         for (int t = 0; t < 2; ++t) {
           plo[t] -= jlo;
@@ -298,25 +319,30 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t col_s = t * kTile, col_o = L::kColO + t * D;
     uint32_t g = 0, nu = 0;  // S-full phases and units consumed by this group
     bool ok = true;
-    for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
-      int bh, pair, split;
-      unit_coords(a, u, bh, pair, split);
-      const int qt = 2 * pair + t;
-      const int kv_len = batch_kv_len<kWin>(a, bh / a.Hq);
+    for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+      const FwdUnit w = fwd_unit<kVar>(a, u);
+      const int bh = w.bh, split = w.split, Sq = w.Sq;
+      const int qt = 2 * w.pair + t;
+      const int kv_len = unit_kv_len<kWin, kVar>(a, w);
       int jlo, jhi;
-      split_kv_range<kSplit>(a, wl, wr, kv_len, qt, split, jlo, jhi);
+      split_kv_range<kSplit>(a, Sq, wl, wr, kv_len, qt, split, jlo, jhi);
       const int q_row = qt * kTile + r;
-      const size_t part_row = ((size_t)split * a.B * a.Hq + bh) * a.Sq + q_row;
+      const size_t part_row = ((size_t)split * a.B * a.Hq + bh) * Sq + q_row;
+      // O rows of the unit: element offset of row 0 and from row to row
+      const size_t o_off = kVar ? ((size_t)w.row0 * a.Hq + w.h) * D : (size_t)bh * Sq * D;
+      const size_t o_row = kVar ? (size_t)a.Hq * D : (size_t)D;
+      // its LSE values: [Hq, T] in packed calls
+      float* lse_u = a.lse + (kVar ? (size_t)w.h * a.T + w.row0 : (size_t)bh * Sq);
       if (jhi == jlo) {
         // no key (of this split) reaches the tile: an empty part, or with a
         // window or padding the whole tile sees no key: O = 0, LSE = -inf
-        if (kSplit && q_row < a.Sq) a.lse_part[part_row] = -INFINITY;
-        if (!kSplit && kWin && q_row < a.Sq) {
-          uint4* orow = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o) +
-                                                 ((size_t)bh * a.Sq + q_row) * D);
+        if (kSplit && q_row < Sq) a.lse_part[part_row] = -INFINITY;
+        if (!kSplit && kWin && q_row < Sq) {
+          uint4* orow = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o) + o_off +
+                                                 q_row * o_row);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) orow[i] = make_uint4(0u, 0u, 0u, 0u);
-          a.lse[(size_t)bh * a.Sq + q_row] = -INFINITY;
+          lse_u[q_row] = -INFINITY;
         }
         continue;
       }
@@ -423,7 +449,7 @@ __global__ void __launch_bounds__(320, 1)
                                  make_float2(bias0 + neg_m, bias0 + neg_m));
               const float2 tt = __ffma2_rn(make_float2(u2f(src[e]), u2f(src[e + 1])), c2, add);
               float p0, p1;
-              if ((i & 7) < L::kPolyPairs) {
+              if ((i & 7) < kPoly) {
                 const float2 pp = ex2_poly2(tt);
                 p0 = pp.x, p1 = pp.y;
               } else {
@@ -504,7 +530,7 @@ __global__ void __launch_bounds__(320, 1)
       if (!warp_wait(bar(L::kBarOFinal + t), nu & 1, abort_flag)) { ok = false; break; }
       ++nu;
       tc_fence_after();
-      const bool row_ok = q_row < a.Sq;
+      const bool row_ok = q_row < Sq;
       if (kSplit) {
         // fp32 part: O / l and the part's LSE; a row with no visible key in
         // this split (its running max still -inf) is an empty part, O = 0 and
@@ -540,7 +566,7 @@ __global__ void __launch_bounds__(320, 1)
             // v[16hf + 4m .. +3] is now piece 4hf + pc of row grp_row0 + m
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              if (grp_row0 + m < a.Sq)
+              if (grp_row0 + m < Sq)
                 *reinterpret_cast<uint4*>(pbase + (size_t)m * D + c * 32 + (4 * hf + pc) * 4) =
                     make_uint4(v[16 * hf + 4 * m], v[16 * hf + 4 * m + 1], v[16 * hf + 4 * m + 2],
                                v[16 * hf + 4 * m + 3]);
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(320, 1)
         // a group trade 16-byte pieces (a 4x4 transpose): lane 4k+i then writes
         // piece i of rows 4k..4k+3.  O is released after its last TMEM read.
         const int grp_row0 = qt * kTile + (r & ~3), pc = lane & 3;
-        __nv_bfloat16* obase = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)bh * a.Sq * D;
+        __nv_bfloat16* obase = reinterpret_cast<__nv_bfloat16*>(a.o) + o_off;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -587,18 +613,18 @@ __global__ void __launch_bounds__(320, 1)
           // w[4m..4m+3] is now piece pc of row grp_row0 + m
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            if (grp_row0 + m < a.Sq)
-              *reinterpret_cast<uint4*>(obase + (size_t)(grp_row0 + m) * D + c * 32 + pc * 8) =
+            if (grp_row0 + m < Sq)
+              *reinterpret_cast<uint4*>(obase + (grp_row0 + m) * o_row + c * 32 + pc * 8) =
                   make_uint4(w[4 * m], w[4 * m + 1], w[4 * m + 2], w[4 * m + 3]);
           }
         }
-        if (row_ok) a.lse[(size_t)bh * a.Sq + q_row] = row_lse;
+        if (row_ok) lse_u[q_row] = row_lse;
       } else {
         // D = 64: each thread stores its own row, and O is released after the
         // stores (both measured faster here than the D = 128 form, whose
         // shuffles cost the softmax-bound loop more than they save)
         __nv_bfloat16* orow =
-            reinterpret_cast<__nv_bfloat16*>(a.o) + ((size_t)bh * a.Sq + (row_ok ? q_row : 0)) * D;
+            reinterpret_cast<__nv_bfloat16*>(a.o) + o_off + (row_ok ? q_row : 0) * o_row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -615,7 +641,7 @@ __global__ void __launch_bounds__(320, 1)
               dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
         }
-        if (row_ok) a.lse[(size_t)bh * a.Sq + q_row] = row_lse;
+        if (row_ok) lse_u[q_row] = row_lse;
         tc_fence_before();
         mbar_arrive(bar(L::kBarOFree + t));
       }
@@ -641,9 +667,9 @@ static int launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
     const void* kernels[] = {
-        (const void*)fwd_kernel<D, 0, false>, (const void*)fwd_kernel<D, 1, false>,
-        (const void*)fwd_kernel<D, 2, false>, (const void*)fwd_kernel<D, 0, true>,
-        (const void*)fwd_kernel<D, 1, true>,  (const void*)fwd_kernel<D, 2, true>};
+        (const void*)fwd_kernel<D, 0, false, false>, (const void*)fwd_kernel<D, 1, false, false>,
+        (const void*)fwd_kernel<D, 2, false, false>, (const void*)fwd_kernel<D, 0, true, false>,
+        (const void*)fwd_kernel<D, 1, true, false>,  (const void*)fwd_kernel<D, 2, true, false>};
     for (const void* k : kernels)
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAllocBytes) !=
           cudaSuccess)
@@ -686,16 +712,62 @@ static int launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     return FA_OK;
   }
   using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, FwdArgs);
-  const KernelFn kernels[2][3] = {{fwd_kernel<D, 0, false>, fwd_kernel<D, 1, false>,
-                                   fwd_kernel<D, 2, false>},
-                                  {fwd_kernel<D, 0, true>, fwd_kernel<D, 1, true>,
-                                   fwd_kernel<D, 2, true>}};
+  const KernelFn kernels[2][3] = {{fwd_kernel<D, 0, false, false>, fwd_kernel<D, 1, false, false>,
+                                   fwd_kernel<D, 2, false, false>},
+                                  {fwd_kernel<D, 0, true, false>, fwd_kernel<D, 1, true, false>,
+                                   fwd_kernel<D, 2, true, false>}};
   if (launch_pdl(kernels[a.n_split > 1 ? 1 : 0][mode], dim3(grid), dim3(320), L::kAllocBytes,
                  stream, tq, tk, tv, a) != cudaSuccess)
     return FA_ERR_CUDA;
   record_timing(true, stream);
   note_launches(1);
   return FA_OK;
+}
+
+template <int D>
+static int launch_fwd_var_d(const CUtensorMap& any, FwdArgs a, int max_items, cudaStream_t stream) {
+  using L = FwdLayout<D>;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
+  static bool attr_done[64] = {};
+  if (dev < 64 && !attr_done[dev]) {
+    const void* kernels[] = {(const void*)fwd_kernel<D, 0, false, true>,
+                             (const void*)fwd_kernel<D, 1, false, true>};
+    for (const void* k : kernels)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAllocBytes) !=
+          cudaSuccess)
+        return FA_ERR_CUDA;
+    attr_done[dev] = true;
+  }
+  // the plan lists the longest items first; dealt in a snake as in the dense
+  // causal call
+  a.sched = 2;
+  const long long units = (long long)max_items * a.Hq;
+  const int grid = (int)(units < info.sm_count ? units : info.sm_count);
+  const bool plain = a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal));
+  const auto kernel = plain ? fwd_kernel<D, 0, false, true> : fwd_kernel<D, 1, false, true>;
+  record_timing(false, stream);
+  if (launch_pdl(kernel, dim3(grid), dim3(320), L::kAllocBytes, stream, any, any, any, a) !=
+      cudaSuccess)
+    return FA_ERR_CUDA;
+  record_timing(true, stream);
+  note_launches(1);
+  return FA_OK;
+}
+
+int launch_fwd_var(const CUtensorMap& any, const FwdArgs& a, int D, int max_items,
+                   cudaStream_t stream) {
+  if (D == 128) return launch_fwd_var_d<128>(any, a, max_items, stream);
+  if (D == 64) return launch_fwd_var_d<64>(any, a, max_items, stream);
+  return FA_ERR_UNSUPPORTED;
+}
+
+int* fwd_status_word() {
+  int* status = nullptr;
+  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&status), g_fwd_status) != cudaSuccess)
+    return nullptr;
+  return status;
 }
 
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -180,13 +180,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         ++it;
         return true;
       };
-      for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
+      for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
         int bh, pair, split;
         unit_coords(a, u, bh, pair, split);
         const int b = bh / a.Hq, h = bh - b * a.Hq;
         const int bhk = b * a.Hkv + h / group;
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<false>(a, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
+        pair_kv_span<false>(a, a.Sq, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
         if (nmax == 0) continue;
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
@@ -224,11 +224,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       uint32_t k_it = 0, q_it = 0;
       uint32_t gs = 0;  // score halves issued for this tile (all units)
       bool ok = true;
-      for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
+      for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
         int bh, pair, split;
         unit_coords(a, u, bh, pair, split);
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<false>(a, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
+        pair_kv_span<false>(a, a.Sq, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
         if (nmax == 0) continue;
         // both tiles start at kv tile jlo (no left window); this one reaches m
         // of the unit's nmax kv tiles
@@ -313,11 +313,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       uint32_t go = 0;     // P halves consumed for this tile (all units)
       uint32_t units = 0;  // units in which this tile had keys (O-free phases)
       bool ok = true;
-      for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
+      for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
         int bh, pair, split;
         unit_coords(a, u, bh, pair, split);
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<false>(a, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
+        pair_kv_span<false>(a, a.Sq, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
         if (nmax == 0) continue;
         const int m = hi[t] - lo[t], n = 2 * m;
         const uint32_t vbase = v_it;  // ring position of V_jlo
@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     bool ok = true;
     const float c = a.scale_log2;  // > 0 for this kernel
     const float2 c2 = make_float2(c, c);
-    for (int ri = 0, u = cta_unit(a, 0); ok && u >= 0; u = cta_unit(a, ++ri)) {
+    for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
       int bh, pair, split;
       unit_coords(a, u, bh, pair, split);
       const int qt = 2 * pair + t;
       int jlo, jhi;
-      split_kv_range<false>(a, -1, wr, a.Sk, qt, 0, jlo, jhi);
+      split_kv_range<false>(a, a.Sq, -1, wr, a.Sk, qt, 0, jlo, jhi);
       if (jhi == jlo) continue;  // a tile past the last query row
       const int q_row = qt * kTile + r;
       const int lim = wr >= 0 ? min(a.Sk, q_row + 1) : a.Sk;  // keys [0, lim) visible

@@ -31,6 +31,50 @@ bool current_device(int* dev, DeviceInfo* info);
 bool make_tmap_bsd(CUtensorMap* map, const void* base, int BH, int S, int D,
                    int box_rows = kTile);
 
+// The same for a tensor whose rows are row_stride and whose heads head_stride
+// elements apart (multiples of 8).
+bool make_tmap_strided(CUtensorMap* map, const void* base, int H, int S, int D,
+                       long long row_stride, long long head_stride, int box_rows);
+
+// FA_OK if the current device can run the kernels; makes its primary context
+// current on the calling thread.
+int check_device();
+void reset_launches();
+
+// One unit of a packed call's plan: a block of rows of one sequence.  Forward:
+// query rows 256 tile .. of the sequence (a pair of query tiles); backward: its
+// keys 128 tile ...  Units are (item, head) with the head running fastest.
+struct alignas(32) VarItem {
+  int row0;  // the sequence's first row in the packed tensors
+  int len;   // its rows
+  int tile;
+  int b;
+  int pad0;  // the sequence's first row in arrays that pad each one to 64 rows
+  int unused[3];
+};
+
+// Plan of a packed call: one warp per sequence edits the tensor maps (copies of
+// tmpl whose base is the sequence's first row and whose row count is its
+// length) and writes the sequence's items at their places in the order.
+struct PlanArgs {
+  CUtensorMap tmpl[4];
+  const void* base[4];
+  long long row_bytes[4];
+  int n_maps;
+  const int* cu;  // [B + 1] first rows
+  int B, T;
+  int item_rows;  // 256 (forward: pairs of query tiles) or 128 (backward: kv tiles)
+  int causal;
+  VarItem* items;
+  int max_items;
+  int* n_items;
+  CUtensorMap* maps;
+  int* status;   // gets FA_ERR_INVALID_ARG where cu is not ascending within [0, T]
+  int clear;     // 1: *status and *counter start at zero (backward)
+  int* counter;
+};
+int launch_plan(const PlanArgs& p, cudaStream_t stream);
+
 struct FwdArgs {
   void* o;
   float* lse;
@@ -58,10 +102,22 @@ struct FwdArgs {
   int split_tiles;
   float* o_part;    // [n_split, B * Hq, Sq, D]
   float* lse_part;  // [n_split, B * Hq, Sq], natural log, -inf: no visible key
+  // packed calls: the plan's items and their number, three tensor maps per
+  // sequence (q, k, v), and the rows of the packed tensors
+  const VarItem* items;
+  const int* n_items;
+  const CUtensorMap* maps;
+  int T;
 };
 
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                const FwdArgs& a, int D, cudaStream_t stream);
+
+// The same kernel over a packed batch: `any` fills the tensor map parameters,
+// which it does not read; at most max_items items.
+int launch_fwd_var(const CUtensorMap& any, const FwdArgs& a, int D, int max_items,
+                   cudaStream_t stream);
+int* fwd_status_word();  // on the current device; null if it cannot be found
 
 // The D = 64 forward with a ring of score buffers per query tile, for no mask or
 // the causal one, a positive scale and no split (mode 0 of the forward: no
@@ -126,6 +182,13 @@ struct BwdArgs {
   int dq_groups;
   size_t dq_group_stride;  // floats from one accumulator to the next
   int sem_group_stride;    // semaphores from one group to the next
+  // packed calls: the plan, four tensor maps per sequence (q, k, v, dO), the
+  // rows of the packed tensors, and the rows that lse2 and delta hold per head
+  // (every sequence padded to 64); the dQ accumulators are [Hq, T, D]
+  const VarItem* items;
+  const int* n_items;
+  const CUtensorMap* maps;
+  int T, T_pad;
   int qblk_rows;           // query rows per block of the main kernel (64 or 128):
                            // semaphore i of a head counts the writers of block i
 };
@@ -163,6 +226,9 @@ struct BwdMaps {
 };
 
 int launch_bwd(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream);
+// The same for a packed batch (at most max_items items); `any` as in
+// launch_fwd_var.
+int launch_bwd_var(const CUtensorMap& any, const BwdArgs& a, int max_items, cudaStream_t stream);
 
 // The CTA-pair main kernel (D = 128, atomic dQ, no score modification), and
 // the process-wide kernel choice fa_set_bwd_kernel sets.

@@ -1,0 +1,375 @@
+// fa_varlen.cu -- attention over packed sequences of different lengths: the plan
+// kernel and the entry points fa_fwd_varlen / fa_bwd_varlen.
+//
+// Sequence b holds rows cu[b] .. cu[b+1]-1 of tensors [T, H, D]; a query sees
+// keys of its own sequence only.  The attention kernels are the dense ones
+// (fa_fwd.cu, fa_bwd.cu) with another walk over the work:
+//   - The lengths are on the device, so a plan kernel lists the work there: one
+//     item per pair of query tiles (forward) or kv tile (backward) that exists,
+//     the longest first, as the dense causal calls deal theirs.  An item's place
+//     is counted in closed form (the items before it, over all sequences), so
+//     every item is written at once and no sort or scan runs.
+//   - A tile may reach past its sequence's last row.  Each sequence gets its own
+//     tensor maps, copies of the call's that start at its first row and end at
+//     its last, so the TMA unit fills the rows past it with zeros: the products
+//     never meet another sequence's rows or uninitialised memory.
+// The plan costs one launch of a warp per sequence and no pass over the data; it
+// overlaps the end of the kernel before it and the attention kernel's prologue.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kPlanWarps = 4;
+
+__device__ __forceinline__ int warp_add(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Items of sequence `other` that go before item `t` of the sequence `own` with
+// n_own blocks of item_rows rows; len_other / len_own in 64-row blocks.
+//   forward, causal: pair t attends to 2 t + 2 kv tiles: by t, descending;
+//   backward, causal: kv tile t is seen by blocks64 - 2 t query blocks;
+//   otherwise: the longest sequence first, its items in order.
+// Ties go to the lower sequence.  Within a sequence the backward's tiles ascend.
+__device__ __forceinline__ int items_before(int mode, int t, int n_own, int blk_own, int n_other,
+                                            int blk_other, bool lower) {
+  if (mode == 0) {  // forward, causal
+    const int more = max(0, n_other - 1 - t);
+    return more + (lower && n_other > t ? 1 : 0);
+  }
+  if (mode == 1) {  // backward, causal: blk_other - 2 t' > blk_own - 2 t
+    const int d = blk_other - (blk_own - 2 * t);  // 2 t' < d
+    const int more = d > 0 ? min(n_other, (d + 1) / 2) : 0;
+    const bool tie = d >= 0 && (d & 1) == 0 && d / 2 < n_other;
+    return more + (lower && tie ? 1 : 0);
+  }
+  return n_other > n_own || (n_other == n_own && lower) ? n_other : 0;
+}
+
+// One warp per sequence.  What bounds it is the latency of reading cu (twice:
+// once to check it, once per item to place it) and the call's launch; with B
+// sequences it reads B values per item, which L1 serves.
+__global__ void __launch_bounds__(kPlanWarps * 32)
+    plan_kernel(const __grid_constant__ PlanArgs p) {
+  __shared__ alignas(128) CUtensorMap slots[kPlanWarps][4];
+  grid_dep_wait();  // the caller's kernels may have written cu
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x * kPlanWarps + warp;
+  if (b >= p.B) return;
+  // every sequence ascending inside [0, T], or no work at all
+  int bad = 0, total = 0, pad0 = 0;
+  for (int i = lane; i < p.B; i += 32) {
+    const int lo = p.cu[i], hi = p.cu[i + 1];
+    if (lo < 0 || hi < lo || hi > p.T) {
+      bad = 1;
+    } else {
+      total += (hi - lo + p.item_rows - 1) / p.item_rows;
+      if (i < b) pad0 += (hi - lo + 63) / 64 * 64;
+    }
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  total = bad ? 0 : warp_add(total);
+  pad0 = warp_add(pad0);
+  if (b == 0 && lane == 0) {
+    *p.n_items = total;
+    if (p.clear) {
+      *p.status = bad ? (int)FA_ERR_INVALID_ARG : 0;
+      *p.counter = 0;
+    } else if (bad) {
+      atomicExch(p.status, (int)FA_ERR_INVALID_ARG);
+    }
+  }
+  if (bad) return;
+  const int row0 = p.cu[b], len = p.cu[b + 1] - row0;
+  if (len == 0) return;
+  for (int m = 0; m < p.n_maps; ++m) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(&p.tmpl[m]);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(&slots[warp][m]);
+    slot[lane] = src[lane];
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t s = smem_u32(slot);
+      const uint64_t addr =
+          reinterpret_cast<uint64_t>(p.base[m]) + (uint64_t)row0 * (uint64_t)p.row_bytes[m];
+      asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(s),
+                   "l"(addr)
+                   : "memory");
+      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(s),
+                   "r"(len)
+                   : "memory");
+    }
+    __syncwarp();
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned"
+        " [%0], [%1], 128;" ::"l"(p.maps + (size_t)b * p.n_maps + m),
+        "r"(smem_u32(slot))
+        : "memory");
+  }
+  const int n_own = (len + p.item_rows - 1) / p.item_rows, blk_own = (len + 63) / 64;
+  const int mode = p.causal ? (p.item_rows == 256 ? 0 : 1) : 2;
+  for (int t = 0; t < n_own; ++t) {
+    int before = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      if (i == b) continue;
+      const int n = p.cu[i + 1] - p.cu[i];
+      before += items_before(mode, t, n_own, blk_own, (n + p.item_rows - 1) / p.item_rows,
+                             (n + 63) / 64, i < b);
+    }
+    before = warp_add(before) + (mode == 0 ? n_own - 1 - t : t);
+    if (lane == 0 && before < p.max_items) {
+      int4* dst = reinterpret_cast<int4*>(p.items + before);
+      dst[0] = make_int4(row0, len, t, b);
+      dst[1] = make_int4(pad0, 0, 0, 0);
+    }
+  }
+}
+
+}  // namespace
+
+int launch_plan(const PlanArgs& p, cudaStream_t stream) {
+  const int grid = (p.B + kPlanWarps - 1) / kPlanWarps;
+  if (launch_pdl(plan_kernel, dim3(grid), dim3(kPlanWarps * 32), 0, stream, p) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
+
+namespace {
+
+constexpr size_t kHeader = 256;  // status word, item count (+64), unit counter (+128)
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+struct VarLayout {
+  int max_items, groups;
+  long long t_pad;
+  size_t off_items, off_maps, off_acc, off_delta, off_lse2, off_sem, total;
+};
+
+int check_var(int B, int T, int Hq, int Hkv, int D) {
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (T > (1 << 30) || B > (1 << 24)) return FA_ERR_INVALID_ARG;
+  // units (item, head) and the packed rows over all heads are counted in 32 bits
+  const long long t_pad = ((long long)T + 63) / 64 * 64 + 64LL * B;
+  if (t_pad * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+VarLayout var_layout(int B, int T, int Hq, int D, bool backward, bool deterministic) {
+  VarLayout L{};
+  const int rows = backward ? 128 : 256;
+  L.max_items = T / rows + B;
+  L.off_items = kHeader;
+  L.off_maps = up256(L.off_items + (size_t)L.max_items * sizeof(VarItem));
+  L.total = up256(L.off_maps + (size_t)B * (backward ? 4 : 3) * sizeof(CUtensorMap));
+  if (!backward) return L;
+  L.groups = dq_group_count(T, deterministic);
+  L.t_pad = ((long long)T + 63) / 64 * 64 + 64LL * B;
+  L.off_acc = L.total;
+  L.off_delta = up256(L.off_acc + (size_t)L.groups * Hq * T * D * sizeof(float));
+  L.off_lse2 = up256(L.off_delta + (size_t)Hq * L.t_pad * sizeof(float));
+  L.off_sem = up256(L.off_lse2 + (size_t)Hq * L.t_pad * sizeof(float));
+  L.total = L.off_sem;
+  if (deterministic)
+    L.total = up256(L.off_sem + (size_t)L.groups * Hq * (L.t_pad / 64) * sizeof(int));
+  return L;
+}
+
+// Rows and heads a tensor's elements are apart: null strides are contiguous.
+int tensor_strides(const fa_packed_stride* s, int H, int D, long long* row, long long* head) {
+  *row = s ? (long long)s->token : (long long)H * D;
+  *head = s ? (long long)s->head : (long long)D;
+  if (*row < D || *head < D || *row > (1LL << 36) || *head > (1LL << 36)) return FA_ERR_INVALID_ARG;
+  if ((*row & 7) || (*head & 7)) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+struct VarTensor {
+  const void* p;
+  const fa_packed_stride* s;
+  int H, box_rows;
+};
+
+// The plan's maps from the call's tensors (in the order of t).
+int plan_maps(const VarTensor* t, int n, int T, int D, PlanArgs* p) {
+  p->n_maps = n;
+  for (int i = 0; i < n; ++i) {
+    long long row, head;
+    const int rc = tensor_strides(t[i].s, t[i].H, D, &row, &head);
+    if (rc) return rc;
+    p->base[i] = t[i].p;
+    p->row_bytes[i] = row * 2;
+    if (!make_tmap_strided(&p->tmpl[i], t[i].p, t[i].H, T, D, row, head, t[i].box_rows))
+      return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+int check_strides(const VarTensor* t, int n, int D) {
+  for (int i = 0; i < n; ++i) {
+    long long row, head;
+    const int rc = tensor_strides(t[i].s, t[i].H, D, &row, &head);
+    if (rc) return rc;
+  }
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_varlen_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int backward,
+                                 int deterministic) {
+  if (check_var(B, T, Hq, Hkv, D) != FA_OK) return 0;
+  return var_layout(B, T, Hq, D, backward != 0, deterministic != 0).total;
+}
+
+int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                  const int* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
+                  const fa_packed_stride* q_stride, const fa_packed_stride* k_stride,
+                  const fa_packed_stride* v_stride, int window_left, int window_right, float scale,
+                  void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_var(B, T, Hq, Hkv, D);
+  if (rc) return rc;
+  if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  const VarTensor t[3] = {{q, q_stride, Hq, kTile}, {k, k_stride, Hkv, kTile}, {v, v_stride, Hkv, kTile}};
+  if ((rc = check_strides(t, 3, D))) return rc;
+  if (T == 0) return FA_OK;
+  if (!q || !k || !v || !o || !lse || !cu_seqlens) return FA_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
+      misaligned(lse, 4) || misaligned(cu_seqlens, 4))
+    return FA_ERR_MISALIGNED;
+  const VarLayout L = var_layout(B, T, Hq, D, false, false);
+  if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
+  if ((rc = check_device())) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PlanArgs p{};
+  if ((rc = plan_maps(t, 3, T, D, &p))) return rc;
+  FwdArgs a{};
+  a.wl = window_left < 0 ? -1 : window_left;
+  a.wr = window_right < 0 ? -1 : window_right;
+  a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
+  p.cu = cu_seqlens;
+  p.B = B;
+  p.T = T;
+  p.item_rows = 256;
+  p.causal = a.causal;
+  p.items = reinterpret_cast<VarItem*>(ws + L.off_items);
+  p.max_items = L.max_items;
+  p.n_items = reinterpret_cast<int*>(ws + 64);
+  p.maps = reinterpret_cast<CUtensorMap*>(ws + L.off_maps);
+  p.status = fwd_status_word();
+  p.counter = reinterpret_cast<int*>(ws + 128);
+  if (!p.status) return FA_ERR_CUDA;
+  a.o = o;
+  a.lse = lse;
+  a.status = p.status;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.n_split = 1;
+  a.items = p.items;
+  a.n_items = p.n_items;
+  a.maps = p.maps;
+  a.T = T;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = launch_plan(p, st))) return rc;
+  return launch_fwd_var(p.tmpl[0], a, D, L.max_items, st);
+}
+
+int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                  const float* lse, void* dq, void* dk, void* dv, const int* cu_seqlens, int B,
+                  int T, int Hq, int Hkv, int D, const fa_packed_stride* q_stride,
+                  const fa_packed_stride* k_stride, const fa_packed_stride* v_stride,
+                  int window_left, int window_right, float scale, void* workspace,
+                  size_t workspace_bytes, int deterministic, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_var(B, T, Hq, Hkv, D);
+  if (rc) return rc;
+  if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  const VarTensor t[4] = {{q, q_stride, Hq, 64}, {k, k_stride, Hkv, kTile},
+                          {v, v_stride, Hkv, kTile}, {dO, nullptr, Hq, 64}};
+  if ((rc = check_strides(t, 4, D))) return rc;
+  if (T == 0) return FA_OK;
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv || !cu_seqlens)
+    return FA_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
+      misaligned(dO, 16) || misaligned(dq, 16) || misaligned(dk, 16) || misaligned(dv, 16) ||
+      misaligned(lse, 4) || misaligned(cu_seqlens, 4))
+    return FA_ERR_MISALIGNED;
+  const VarLayout L = var_layout(B, T, Hq, D, true, deterministic != 0);
+  if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
+  if ((rc = check_device())) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PlanArgs p{};
+  if ((rc = plan_maps(t, 4, T, D, &p))) return rc;
+  BwdArgs a{};
+  a.wl = window_left < 0 ? -1 : window_left;
+  a.wr = window_right < 0 ? -1 : window_right;
+  a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
+  p.cu = cu_seqlens;
+  p.B = B;
+  p.T = T;
+  p.item_rows = 128;
+  p.causal = a.causal;
+  p.items = reinterpret_cast<VarItem*>(ws + L.off_items);
+  p.max_items = L.max_items;
+  p.n_items = reinterpret_cast<int*>(ws + 64);
+  p.maps = reinterpret_cast<CUtensorMap*>(ws + L.off_maps);
+  p.status = reinterpret_cast<int*>(ws);
+  p.clear = 1;
+  p.counter = reinterpret_cast<int*>(ws + 128);
+  a.o = o;
+  a.dO = dO;
+  a.lse = lse;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dq_acc = reinterpret_cast<float*>(ws + L.off_acc);
+  a.delta = reinterpret_cast<float*>(ws + L.off_delta);
+  a.lse2 = reinterpret_cast<float*>(ws + L.off_lse2);
+  a.sem = reinterpret_cast<int*>(ws + L.off_sem);
+  a.status = p.status;
+  a.unit_counter = p.counter;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.deterministic = deterministic ? 1 : 0;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.dq_groups = L.groups;
+  a.dq_group_stride = (size_t)Hq * T * D;
+  a.n_qblk = (int)(L.t_pad / 64);
+  a.sem_group_stride = Hq * a.n_qblk;
+  a.qblk_rows = 64;
+  a.items = p.items;
+  a.n_items = p.n_items;
+  a.maps = p.maps;
+  a.T = T;
+  a.T_pad = (int)L.t_pad;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = launch_plan(p, st))) return rc;
+  return launch_bwd_var(p.tmpl[0], a, L.max_items, st);
+}
+
+}  // extern "C"

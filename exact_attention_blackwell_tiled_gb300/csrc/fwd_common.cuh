@@ -5,12 +5,13 @@
 
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "var_common.cuh"
 
 namespace fa {
 
-// The r-th unit this CTA processes (-1 when it has no more).  Every role of
-// the CTA walks the same sequence.
-__device__ __forceinline__ int cta_unit(const FwdArgs& a, int r) {
+// The r-th of n_units units that this CTA processes (-1 when it has no more).
+// Every role of the CTA walks the same sequence.
+__device__ __forceinline__ int cta_unit(const FwdArgs& a, int n_units, int r) {
   int k;
   if (a.sched == 2) {
     // boustrophedon: each round of gridDim.x units alternates direction, so
@@ -19,7 +20,7 @@ __device__ __forceinline__ int cta_unit(const FwdArgs& a, int r) {
   } else {
     k = blockIdx.x + r * gridDim.x;
   }
-  return k < a.n_units ? k : -1;
+  return k < n_units ? k : -1;
 }
 
 // Unit u -> (flat batch*head index, tile pair p: query tiles 2p and 2p+1).
@@ -50,6 +51,40 @@ __device__ __forceinline__ void unit_coords(const FwdArgs& a, int u, int& bh, in
   pair = u - bh * np;
 }
 
+// A unit of work: query head bh (flat over the batch), the pair of query tiles
+// 2 * pair and 2 * pair + 1, its split of the kv tiles, and the sizes of its
+// sequence.  Packed calls (kVar): units are (item, head) with the head running
+// fastest, an item of the plan names a sequence (rows row0 .. row0 + Sq - 1 of
+// the packed tensors) and a pair of its query tiles, and bh is the head alone.
+struct FwdUnit {
+  int bh, pair, split;
+  int b, h;   // batch entry and query head
+  int Sq;     // query rows of the sequence
+  int row0;   // its first packed row (kVar)
+};
+
+template <bool kVar>
+__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
+  FwdUnit w;
+  w.row0 = 0;
+  if constexpr (kVar) {
+    const int item = u / a.Hq;
+    const VarItem it = load_item(a.items, item);
+    w.h = w.bh = u - item * a.Hq;
+    w.b = it.b;
+    w.pair = it.tile;
+    w.split = 0;
+    w.Sq = it.len;
+    w.row0 = it.row0;
+  } else {
+    unit_coords(a, u, w.bh, w.pair, w.split);
+    w.b = w.bh / a.Hq;
+    w.h = w.bh - w.b * a.Hq;
+    w.Sq = a.Sq;
+  }
+  return w;
+}
+
 // Keys of batch b that exist: seqlens_k[b] clamped to [0, Sk] (the key padding
 // mask); all Sk without lengths, and always in the plain kernel.
 template <bool kWin>
@@ -59,13 +94,20 @@ __device__ __forceinline__ int batch_kv_len(const FwdArgs& a, int b) {
   return n < 0 ? 0 : (n < a.Sk ? n : a.Sk);
 }
 
+// The same for a unit: a packed sequence has as many keys as queries.
+template <bool kWin, bool kVar>
+__device__ __forceinline__ int unit_kv_len(const FwdArgs& a, const FwdUnit& w) {
+  if constexpr (kVar) return w.Sq;
+  return batch_kv_len<kWin>(a, w.b);
+}
+
 // kv tiles [lo, hi) that query tile qt sees under the window (wl, wr) among the
 // first kv_len keys (empty when the tile lies past Sq or sees no key)
-__device__ __forceinline__ void tile_kv_range(const FwdArgs& a, int wl, int wr, int kv_len, int qt,
-                                              int& lo, int& hi) {
+__device__ __forceinline__ void tile_kv_range(int Sq, int wl, int wr, int kv_len, int qt, int& lo,
+                                              int& hi) {
   lo = hi = 0;
-  if (qt * kTile >= a.Sq) return;
-  const int last = min(a.Sq, (qt + 1) * kTile) - 1;  // last query row of the tile
+  if (qt * kTile >= Sq) return;
+  const int last = min(Sq, (qt + 1) * kTile) - 1;  // last query row of the tile
   const int lo_key = wl >= 0 ? max(0, qt * kTile - wl) : 0;
   const int hi_key = wr >= 0 ? min(kv_len, last + wr + 1) : kv_len;
   lo = lo_key / kTile;
@@ -74,9 +116,9 @@ __device__ __forceinline__ void tile_kv_range(const FwdArgs& a, int wl, int wr, 
 
 // A tile's range cut to the kv tiles of `split` (kSplit); may become empty.
 template <bool kSplit>
-__device__ __forceinline__ void split_kv_range(const FwdArgs& a, int wl, int wr, int kv_len, int qt,
-                                               int split, int& lo, int& hi) {
-  tile_kv_range(a, wl, wr, kv_len, qt, lo, hi);
+__device__ __forceinline__ void split_kv_range(const FwdArgs& a, int Sq, int wl, int wr, int kv_len,
+                                               int qt, int split, int& lo, int& hi) {
+  tile_kv_range(Sq, wl, wr, kv_len, qt, lo, hi);
   if (kSplit) {
     const int s0 = split * a.split_tiles;
     lo = max(lo, s0);
@@ -88,10 +130,11 @@ __device__ __forceinline__ void split_kv_range(const FwdArgs& a, int wl, int wr,
 // and their union [jlo, jlo + nmax).  An empty tile gets lo = hi = jlo; both
 // empty: nmax = 0 and the unit is skipped.
 template <bool kSplit>
-__device__ __forceinline__ void pair_kv_span(const FwdArgs& a, int wl, int wr, int kv_len, int pair,
-                                             int split, int lo[2], int hi[2], int& jlo, int& nmax) {
-  split_kv_range<kSplit>(a, wl, wr, kv_len, 2 * pair, split, lo[0], hi[0]);
-  split_kv_range<kSplit>(a, wl, wr, kv_len, 2 * pair + 1, split, lo[1], hi[1]);
+__device__ __forceinline__ void pair_kv_span(const FwdArgs& a, int Sq, int wl, int wr, int kv_len,
+                                             int pair, int split, int lo[2], int hi[2], int& jlo,
+                                             int& nmax) {
+  split_kv_range<kSplit>(a, Sq, wl, wr, kv_len, 2 * pair, split, lo[0], hi[0]);
+  split_kv_range<kSplit>(a, Sq, wl, wr, kv_len, 2 * pair + 1, split, lo[1], hi[1]);
   const bool e0 = hi[0] <= lo[0], e1 = hi[1] <= lo[1];
   if (e0 && e1) {
     jlo = lo[0];

@@ -248,6 +248,52 @@ int fa_fwd_split(const void* q, const void* k, const void* v, void* o, float* ls
 int fa_lse_merge(const float* o_parts, const float* lse_parts, int n_parts, void* o, float* lse,
                  int64_t rows, int D, fa_stream_t stream);
 
+/*
+ * Attention over packed sequences of different lengths (the pages have no
+ * counterpart: they fix one length per call; this is the same definition
+ * applied to every sequence by itself, for batches of whole prompts and packed
+ * training documents).  Sequence b holds rows cu_seqlens[b] .. cu_seqlens[b+1]-1
+ * of the packed tensors; its queries see its own keys only, under the window
+ * (window_left, window_right; negative: unbounded, so {-1, 0} is causal) counted
+ * inside the sequence.
+ *   q [T, Hq, D], k, v [T, Hkv, D] bf16, D elements contiguous, rows and heads
+ *     apart by *_stride (elements, multiples of 8, at least D; null: contiguous),
+ *     so slices of one fused projection serve;
+ *   o, dO, dq [T, Hq, D], dk, dv [T, Hkv, D] bf16, contiguous;  lse [Hq, T] fp32.
+ *   cu_seqlens: device array of B + 1 int32, ascending inside [0, T].  Sequences
+ *     may be empty.  It is read on the device: a value out of order writes no
+ *     output and records FA_ERR_INVALID_ARG, which fa_fwd_status (forward) or
+ *     fa_bwd_status(workspace) (backward) reports.
+ * Rows of no sequence (before the first, behind the last) are neither read into
+ * any result nor written.  T >= 0 (0 is a no-op), B >= 1, D in {64, 128}; the
+ * rows padded per sequence to 64, times Hq, stay below 2^31.  The bf16 tensors are 16-byte
+ * aligned, lse and cu_seqlens 4-byte aligned.
+ * workspace: fa_varlen_workspace_bytes(...) bytes of device memory, 256-byte
+ * aligned, uninitialised; it holds the work list and tensor maps of the call
+ * (and the backward's fp32 accumulators), so calls that may run at the same time
+ * need one each, captured ones among them.
+ * The backward's gradients sum over the heads of a group; deterministic != 0
+ * gives the same bits in every run, as in fa_bwd.
+ */
+typedef struct {
+  int64_t token; /* elements from one row (token) to the next */
+  int64_t head;  /* elements from one head to the next */
+} fa_packed_stride;
+
+size_t fa_varlen_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int backward,
+                                 int deterministic);
+int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                  const int* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
+                  const fa_packed_stride* q_stride, const fa_packed_stride* k_stride,
+                  const fa_packed_stride* v_stride, int window_left, int window_right, float scale,
+                  void* workspace, size_t workspace_bytes, fa_stream_t stream);
+int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                  const float* lse, void* dq, void* dk, void* dv, const int* cu_seqlens, int B,
+                  int T, int Hq, int Hkv, int D, const fa_packed_stride* q_stride,
+                  const fa_packed_stride* k_stride, const fa_packed_stride* v_stride,
+                  int window_left, int window_right, float scale, void* workspace,
+                  size_t workspace_bytes, int deterministic, fa_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fa_status_string(int status);
 
