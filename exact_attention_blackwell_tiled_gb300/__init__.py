@@ -31,7 +31,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_status", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bw
            "fa_bwd_noalloc", "fa_fwd_mod", "fa_bwd_mod", "fa_fwd_split_count",
            "fa_fwd_split_workspace_bytes", "fa_fwd_split", "fa_lse_merge", "fa_wait_test",
            "fa_bwd_noalloc_status", "fa_varlen_workspace_bytes", "fa_fwd_varlen",
-           "fa_bwd_varlen")
+           "fa_bwd_varlen", "fa_cache4_page_bytes", "fa_cache4_append", "fa_cache4_read",
+           "fa_cache4_attend_workspace_bytes", "fa_cache4_attend", "fa_cache4_evict",
+           "fa_cache4_status")
 
 
 class ScoreMod(ctypes.Structure):
@@ -109,6 +111,22 @@ def _bind(lib):
     lib.fa_fwd_varlen.restype = i
     lib.fa_bwd_varlen.argtypes = [vp] * 10 + [i, i, i, i, i, psp, psp, psp, i, i, f, vp, sz, i, vp]
     lib.fa_bwd_varlen.restype = i
+    lib.fa_cache4_page_bytes.argtypes = [i, i, i]
+    lib.fa_cache4_page_bytes.restype = sz
+    lib.fa_cache4_append.argtypes = [vp, i, i, vp, vp, psp, psp, i, i, i, i, vp, vp, vp, i, vp]
+    lib.fa_cache4_append.restype = i
+    lib.fa_cache4_read.argtypes = [vp, i, i, vp, vp, i, i, i, i, vp, vp, vp, i, vp]
+    lib.fa_cache4_read.restype = i
+    lib.fa_cache4_attend_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.fa_cache4_attend_workspace_bytes.restype = sz
+    lib.fa_cache4_attend.argtypes = [vp, i64, i64, vp, i, i, vp, vp, i, i, i, i, vp, vp, i, f, vp,
+                                     vp, i, vp, sz, vp]
+    lib.fa_cache4_attend.restype = i
+    lib.fa_cache4_evict.argtypes = [vp, i, i, vp, i, vp, vp, i, i, i, i, i, i, vp, i, vp, vp, vp,
+                                    vp]
+    lib.fa_cache4_evict.restype = i
+    lib.fa_cache4_status.argtypes = [vp]
+    lib.fa_cache4_status.restype = i
     return lib
 
 
@@ -563,3 +581,182 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     ``cu_seqlens`` int32 [B+1] (see fwd_varlen).  Tokens of no sequence get zeros
     in O and in every gradient.  Returns O [T,Hq,D] bf16."""
     return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic)
+
+
+def _cache4(cache, D):
+    """(pages, Hkv, page size) of a 4-bit cache tensor for head dimension D."""
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.uint8:
+        raise TypeError("cache must be a uint8 CUDA tensor")
+    if cache.dim() != 3 or not cache.is_contiguous() or D not in (64, 128):
+        raise ValueError("cache must be a contiguous [pages, Hkv, bytes] tensor of cache4_empty, "
+                         "with head dimension 64 or 128")
+    page, rest = divmod(cache.shape[2], D + D // 4)
+    if rest or page not in (16, 32, 64, 128):
+        raise ValueError(f"cache pages of {cache.shape[2]} bytes do not hold tokens of {D} elements")
+    return cache.shape[0], cache.shape[1], page
+
+
+def _page_table(t, B, device, name="page_table"):
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device
+            or t.dtype != torch.int32 or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous int32 tensor on the cache's device")
+    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [{B}, pages per sequence]")
+    return t.shape[1]
+
+
+def _weights(t, B, Hkv, device, name):
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device
+            or t.dtype != torch.float32 or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous fp32 tensor on the cache's device")
+    if t.dim() != 3 or tuple(t.shape[:2]) != (B, Hkv) or t.shape[2] < 1:
+        raise ValueError(f"{name} must be [{B}, {Hkv}, slots]")
+    return t.shape[2]
+
+
+def cache4_empty(num_pages: int, Hkv: int, D: int, page_size: int = 64, device="cuda"):
+    """A paged 4-bit key/value cache (include/fa.h, fa_cache4_page_bytes): uint8
+    [num_pages, Hkv, bytes of a page and head], zeroed.  page_size: 16, 32, 64 or
+    128 tokens.  The bytes are opaque; cache4_read returns the values."""
+    nbytes = int(lib().fa_cache4_page_bytes(Hkv, D, page_size))
+    if nbytes == 0:
+        raise FAError("fa_cache4_page_bytes", 2)
+    return torch.zeros((num_pages, Hkv, nbytes // Hkv), dtype=torch.uint8, device=device)
+
+
+def cache4_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                  cache_lens: torch.Tensor, cu_seqlens: torch.Tensor | None = None, stream=None):
+    """Quantises and stores new tokens (fa_cache4_append).
+
+    k, v [T,Hkv,D] bf16 CUDA, elements contiguous; ``page_table`` int32 [B,width];
+    ``cache_lens`` int32 [B]: tokens held before, which is where the new ones go;
+    ``cu_seqlens`` int32 [B+1] packs several per sequence, None means one each
+    (T == B).  cache_lens is left as it is: add the new tokens to it afterwards.
+    """
+    ks = _packed(k, "k")
+    T, Hkv, D = k.shape
+    vs = _packed(v, "v", Hkv, k)
+    pages, heads, page = _cache4(cache, D)
+    if heads != Hkv or cache.device != k.device:
+        raise ValueError("cache and k must have the same kv heads and device")
+    B = _int32(cache_lens, None, k.device, "cache_lens").numel()
+    width = _page_table(page_table, B, k.device)
+    if cu_seqlens is not None:
+        _int32(cu_seqlens, B + 1, k.device, "cu_seqlens")
+    with torch.cuda.device(k.device):
+        rc = lib().fa_cache4_append(_ptr(cache), pages, page, _ptr(k), _ptr(v), ctypes.byref(ks),
+                                    ctypes.byref(vs), B, T, Hkv, D,
+                                    None if cu_seqlens is None else _ptr(cu_seqlens),
+                                    _ptr(cache_lens), _ptr(page_table), width, _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_cache4_append", rc)
+
+
+def cache4_read(cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tensor | None,
+                count: torch.Tensor, S: int, D: int, k=None, v=None, stream=None):
+    """The values the cache holds (fa_cache4_read): slots first[b] .. first[b] +
+    count[b] - 1 of every sequence (``first`` None: from 0) as bf16 k, v
+    [B,Hkv,S,D], zero from count[b] on."""
+    pages, Hkv, page = _cache4(cache, D)
+    B = _int32(count, None, cache.device, "count").numel()
+    width = _page_table(page_table, B, cache.device)
+    if first is not None:
+        _int32(first, B, cache.device, "first")
+    with torch.cuda.device(cache.device):
+        k = _out(k, (B, Hkv, S, D), torch.bfloat16, cache.device, "k", stream)
+        v = _out(v, (B, Hkv, S, D), torch.bfloat16, cache.device, "v", stream)
+        rc = lib().fa_cache4_read(_ptr(cache), pages, page, _ptr(k), _ptr(v), B, Hkv, int(S), D,
+                                  None if first is None else _ptr(first), _ptr(count),
+                                  _ptr(page_table), width, _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_cache4_read", rc)
+    return k, v
+
+
+def cache4_attend_workspace_bytes(B, Hq, Hkv, D, weight_slots: int = 0) -> int:
+    return int(lib().fa_cache4_attend_workspace_bytes(B, Hq, Hkv, D, int(weight_slots)))
+
+
+def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                  cache_lens: torch.Tensor, scale: float | None = None,
+                  weights: torch.Tensor | None = None, weights_out: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """One query token per sequence attends to its cache (fa_cache4_attend).
+
+    q [B,Hq,D] bf16 CUDA, elements contiguous; ``cache_lens`` int32 [B].
+    ``weights`` fp32 [B,Hkv,slots] has the tokens' softmax weights, summed over each
+    kv head's query heads, added to it in place, or to a copy in ``weights_out``;
+    ``weights_out`` alone gets this step's.  Tokens that an append adds later start
+    at what the tensor holds there, so it begins as zeros.
+    Returns (o [B,Hq,D] bf16, lse [B,Hq] fp32); o = 0, lse = -inf without tokens.
+    """
+    qs = _packed(q, "q")
+    B, Hq, D = q.shape
+    pages, Hkv, page = _cache4(cache, D)
+    if cache.device != q.device:
+        raise ValueError("cache and q must be on one device")
+    _int32(cache_lens, B, q.device, "cache_lens")
+    width = _page_table(page_table, B, q.device)
+    slots = 0
+    if weights is not None:
+        slots = _weights(weights, B, Hkv, q.device, "weights")
+        weights_out = weights if weights_out is None else weights_out
+    if weights_out is not None:
+        if weights is not None and weights_out.shape != weights.shape:
+            raise ValueError("weights_out must have weights' shape")
+        slots = _weights(weights_out, B, Hkv, q.device, "weights_out")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with torch.cuda.device(q.device):
+        out = _out(out, (B, Hq, D), torch.bfloat16, q.device, "out", stream)
+        lse = _out(lse, (B, Hq), torch.float32, q.device, "lse", stream)
+        workspace = _workspace(workspace, cache4_attend_workspace_bytes(B, Hq, Hkv, D, slots),
+                               q.device, stream)
+        rc = lib().fa_cache4_attend(_ptr(q), qs.token, qs.head, _ptr(cache), pages, page, _ptr(out),
+                                    _ptr(lse), B, Hq, Hkv, D, _ptr(cache_lens), _ptr(page_table),
+                                    width, float(scale),
+                                    None if weights is None else _ptr(weights),
+                                    None if weights_out is None else _ptr(weights_out), slots,
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_cache4_attend", rc)
+    return out, lse
+
+
+def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torch.Tensor,
+                 weights: torch.Tensor, out_page_table: torch.Tensor, D: int, budget: int,
+                 recent: int = 0, src=None, weights_out=None, lens_out=None, stream=None):
+    """Keeps at most ``budget`` tokens per (sequence, kv head): the latest ``recent``
+    and the largest ``weights`` [B,Hkv,slots] of the others, copied in order to the
+    pages of ``out_page_table`` (fa_cache4_evict), which no table in use may name.
+
+    Returns (src int32 [B,Hkv,budget]: each kept token's old slot, -1 behind the
+    last; weights fp32 [B,Hkv,budget], 0 behind the last; lens int32 [B]).
+    """
+    pages, Hkv, page = _cache4(cache, D)
+    dev = cache.device
+    B = _int32(cache_lens, None, dev, "cache_lens").numel()
+    width = _page_table(page_table, B, dev)
+    out_width = _page_table(out_page_table, B, dev, "out_page_table")
+    cap = _weights(weights, B, Hkv, dev, "weights")
+    if budget < 1 or not 0 <= recent <= budget or out_width * page < budget:
+        raise ValueError("budget must be positive, at least recent and within out_page_table")
+    with torch.cuda.device(dev):
+        src = _out(src, (B, Hkv, budget), torch.int32, dev, "src", stream)
+        weights_out = _out(weights_out, (B, Hkv, budget), torch.float32, dev, "weights_out", stream)
+        lens_out = _out(lens_out, (B,), torch.int32, dev, "lens_out", stream)
+        rc = lib().fa_cache4_evict(_ptr(cache), pages, page, _ptr(weights), cap, _ptr(cache_lens),
+                                   _ptr(page_table), width, B, Hkv, D, int(budget), int(recent),
+                                   _ptr(out_page_table), out_width, _ptr(src), _ptr(weights_out),
+                                   _ptr(lens_out), _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_cache4_evict", rc)
+    return src, weights_out, lens_out
+
+
+def cache4_status(stream=None) -> int:
+    """Synchronise and return (then clear) what the cache calls recorded: a page id
+    or length out of range (1), a device-side wait that ran out (6)."""
+    return int(lib().fa_cache4_status(_stream(stream)))

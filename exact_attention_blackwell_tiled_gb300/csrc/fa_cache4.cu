@@ -1,0 +1,610 @@
+// fa_cache4.cu -- filling, reading back and thinning out the paged 4-bit cache
+// (cache4.cuh has its layout); fa_cache4_attend.cu attends to it.
+//
+// append: per group of 32 elements x, in fp32 with every operation rounded to
+//   nearest as written, so that the codes are those of the formula:
+//     mn = min x,  scale = bf16((max x - mn) / 15),
+//     code = clamp(rint((x - mn) / scale), 0, 15), 0 where scale is 0.
+//   mn is an element and so exact in bf16; the codes are taken with the rounded
+//   scale, so its rounding (2^-9) moves the top code's value, not the others'
+//   choice.  Bound by memory: it reads 4 D bytes of a token's key and value and
+//   writes 5/4 D.  Half a warp holds one vector (16 bytes a lane at D = 128), so
+//   minimum and maximum take two shuffles each and a warp stores a token's key
+//   and value together.
+// read: value = min + scale * code in one fp32 FMA, rounded once to bf16.  Reads
+//   5/4 D bytes of a token, writes 4 D.
+// evict: two kernels.  The first ranks one (sequence, kv head) per block: the K
+//   largest weights are found digit by digit (four passes of 8 bits over the
+//   weights' bit patterns, which order like the values), and a last pass in
+//   index order counts what is kept, ties from the lowest index up, and writes
+//   each kept key's old place and weight.  The second copies the kept keys' codes
+//   to the new pages in order: 16 slots per warp, in 16-byte pieces.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "cache4.cuh"
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+__device__ int g_cache4_status = 0;
+
+namespace {
+
+// ------------------------------------------------------------------ append
+
+struct AppendArgs {
+  uint8_t* cache;
+  const __nv_bfloat16 *k, *v;
+  long long k_token, k_head, v_token, v_head;
+  const int* cu;    // [B + 1], or null: one token per sequence
+  const int* lens;  // [B] tokens held before
+  C4Table table;
+  int B, T, Hkv;
+};
+
+constexpr int kAppendWarps = 8, kAppendItems = 4;  // (token, head) pairs per warp
+
+// Sequence that holds packed token i, or -1: cu ascends, so halving finds it.
+__device__ int find_sequence(const int* cu, int B, int i) {
+  int lo = 0, hi = B;  // cu[lo] <= i < cu[hi]
+  if (i < cu[0] || i >= cu[B]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
+  using L = C4<D>;
+  constexpr int kE = D / 16;  // elements per lane: 16 lanes hold a vector
+  constexpr int kLanesPerGroup = 32 / kE;
+  __shared__ long long s_block[kAppendWarps * kAppendItems];  // byte offset of the block, or -1
+  __shared__ int s_slot[kAppendWarps * kAppendItems];
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long total = (long long)a.T * a.Hkv;
+  const long long base = (long long)blockIdx.x * (kAppendWarps * kAppendItems);
+  if (threadIdx.x < kAppendWarps * kAppendItems) {
+    const long long item = base + threadIdx.x;
+    long long off = -1;
+    int slot = 0;
+    if (item < total) {
+      const int tok = (int)(item / a.Hkv), h = (int)(item - (long long)tok * a.Hkv);
+      const int b = a.cu ? find_sequence(a.cu, a.B, tok) : tok;
+      if (b >= 0) {
+        const long long s = (long long)a.lens[b] + (a.cu ? tok - a.cu[b] : 0);
+        int page = -1;
+        if (s >= 0 && s < (long long)a.table.width * a.table.blocks_per_page * kC4Block)
+          page = c4_page(a.table, b, (int)(s / kC4Block));
+        if (page < 0) {
+          c4_flag(a.table);
+        } else {
+          slot = (int)(s % kC4Block);
+          const int blk = (int)(s / kC4Block) % a.table.blocks_per_page;
+          off = (((long long)page * a.Hkv + h) * a.table.blocks_per_page + blk) * L::kBytes;
+        }
+      }
+    }
+    s_block[threadIdx.x] = off;
+    s_slot[threadIdx.x] = slot;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool is_v = lane >= 16;
+  const int l = lane & 15;
+  const int g = l / kLanesPerGroup, part = l % kLanesPerGroup;
+  uint32_t x[kAppendItems][kE / 2];
+#pragma unroll
+  for (int n = 0; n < kAppendItems; ++n) {
+    const long long item = base + warp * kAppendItems + n;
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) x[n][e] = 0u;
+    if (s_block[warp * kAppendItems + n] >= 0) {
+      const int tok = (int)(item / a.Hkv), h = (int)(item - (long long)tok * a.Hkv);
+      const __nv_bfloat16* src = (is_v ? a.v + tok * a.v_token + h * a.v_head
+                                       : a.k + tok * a.k_token + h * a.k_head) + l * kE;
+      if constexpr (kE == 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
+        x[n][0] = w.x, x[n][1] = w.y, x[n][2] = w.z, x[n][3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(src);
+        x[n][0] = w.x, x[n][1] = w.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kAppendItems; ++n) {
+    const long long off = s_block[warp * kAppendItems + n];
+    const int slot = s_slot[warp * kAppendItems + n];
+    float f[kE], mn = INFINITY, mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      f[e] = (e & 1) ? __uint_as_float(x[n][e / 2] & 0xffff0000u) : __uint_as_float(x[n][e / 2] << 16);
+      mn = fminf(mn, f[e]);
+      mx = fmaxf(mx, f[e]);
+    }
+#pragma unroll
+    for (int s = 1; s < kLanesPerGroup; s <<= 1) {
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    }
+    const __nv_bfloat16 sc16 = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
+    const float sc = __bfloat162float(sc16);
+    uint32_t codes = 0;
+    if (sc > 0.f) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const float c = rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc));
+        codes |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * e);
+      }
+    }
+    if (off < 0) continue;
+    uint8_t* blk = a.cache + off;
+    if (!is_v) {
+      // elements 32 g + kE part ..: word (t, g), t = 8-element piece of the group
+      const int t = part * kE / 8;
+      uint8_t* w = blk + slot * L::kRow + (t * L::kGroups + g) * 4;
+      if constexpr (kE == 8) *reinterpret_cast<uint32_t*>(w) = codes;
+      else *reinterpret_cast<uint16_t*>(w + (part & 1) * 2) = (uint16_t)codes;
+    } else {
+      const int i = part * kE / 4;
+      *reinterpret_cast<uint16_t*>(blk + L::v_half(slot, i, g)) = (uint16_t)codes;
+      if constexpr (kE == 8)
+        *reinterpret_cast<uint16_t*>(blk + L::v_half(slot, i + 1, g)) = (uint16_t)(codes >> 16);
+    }
+    if (part == 0) {
+      const uint32_t par = (uint32_t)__bfloat16_as_ushort(sc16) | (__float_as_uint(mn) & 0xffff0000u);
+      *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kOffVPar : L::kOffKPar) + slot * L::kPar +
+                                   g * 4) = par;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ read
+
+struct ReadArgs {
+  const uint8_t* cache;
+  __nv_bfloat16 *k, *v;  // [B, Hkv, S, D]
+  const int* first;      // [B] or null (0)
+  const int* count;      // [B]
+  C4Table table;
+  int B, Hkv, S;
+};
+
+// A warp takes one slot of one head: lanes 0..15 its key, 16..31 its value.
+template <int D>
+__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
+  using L = C4<D>;
+  constexpr int kE = D / 16, kLanesPerGroup = 32 / kE;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const bool is_v = lane >= 16;
+  const int l = lane & 15, g = l / kLanesPerGroup, part = l % kLanesPerGroup;
+  const long long total = (long long)a.B * a.Hkv * a.S;
+  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+  for (long long x = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); x < total;
+       x += warps) {
+    const long long bh = x / a.S;
+    const int s = (int)(x - bh * a.S), b = (int)(bh / a.Hkv), h = (int)(bh - (long long)b * a.Hkv);
+    uint32_t out[kE / 2];
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) out[e] = 0u;
+    if (s < a.count[b]) {
+      const long long at = (long long)(a.first ? a.first[b] : 0) + s;
+      int page = -1;
+      if (at >= 0 && at < (long long)a.table.width * a.table.blocks_per_page * kC4Block)
+        page = c4_page(a.table, b, (int)(at / kC4Block));
+      if (page < 0) {
+        if (lane == 0) c4_flag(a.table);
+      } else {
+        const int slot = (int)(at % kC4Block), blk = (int)(at / kC4Block) % a.table.blocks_per_page;
+        const uint8_t* p =
+            a.cache + (((long long)page * a.Hkv + h) * a.table.blocks_per_page + blk) * L::kBytes;
+        uint32_t codes;
+        if (!is_v) {
+          const uint8_t* w = p + slot * L::kRow + ((part * kE / 8) * L::kGroups + g) * 4;
+          if constexpr (kE == 8) codes = *reinterpret_cast<const uint32_t*>(w);
+          else codes = *reinterpret_cast<const uint16_t*>(w + (part & 1) * 2);
+        } else {
+          const int i = part * kE / 4;
+          codes = *reinterpret_cast<const uint16_t*>(p + L::v_half(slot, i, g));
+          if constexpr (kE == 8)
+            codes |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + L::v_half(slot, i + 1, g)) << 16;
+        }
+        const uint32_t par = *reinterpret_cast<const uint32_t*>(
+            p + (is_v ? L::kOffVPar : L::kOffKPar) + slot * L::kPar + g * 4);
+        const float sc = c4_scale(par), mn = c4_min(par);
+#pragma unroll
+        for (int e = 0; e < kE / 2; ++e)
+          out[e] = pack_bf16x2(__fmaf_rn(sc, (float)((codes >> (8 * e)) & 15u), mn),
+                               __fmaf_rn(sc, (float)((codes >> (8 * e + 4)) & 15u), mn));
+      }
+    }
+    __nv_bfloat16* dst = (is_v ? a.v : a.k) + x * D + l * kE;
+    if constexpr (kE == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  }
+}
+
+// ------------------------------------------------------------------ evict
+
+struct EvictArgs {
+  uint8_t* cache;
+  const float* weights;  // [B, Hkv, cap]
+  float* weights_out;    // [B, Hkv, budget]
+  int* src;              // [B, Hkv, budget]
+  const int* lens;       // [B]
+  int* lens_out;         // [B]
+  C4Table in, out;
+  int B, Hkv, cap, budget, recent;
+};
+
+constexpr int kRankThreads = 1024;
+
+// Bit pattern that orders like the value (negative values reversed; -0 as +0).
+__device__ __forceinline__ uint32_t order_key(float w) {
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Sum over the block of one value per thread below this thread, and the total.
+__device__ __forceinline__ int block_prefix(int x, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();  // s_warp may still be read from the call before
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int y = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    s_warp[lane] = y;
+  }
+  __syncthreads();
+  *total = s_warp[31];
+  return inc - x + (warp ? s_warp[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictArgs a) {
+  __shared__ int s_hist[256];
+  __shared__ int s_warp[32];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int bh = blockIdx.x, b = bh / a.Hkv;
+  const int cap = min(a.cap, (int)min((long long)a.in.width * a.in.blocks_per_page * kC4Block,
+                                      (long long)0x7fffffff));
+  int n = a.lens[b];
+  if (n < 0 || n > cap) {
+    if (threadIdx.x == 0) c4_flag(a.in);
+    n = n < 0 ? 0 : cap;
+  }
+  const float* w = a.weights + (size_t)bh * a.cap;
+  float* w_out = a.weights_out + (size_t)bh * a.budget;
+  int* src = a.src + (size_t)bh * a.budget;
+  const int kept = min(n, a.budget);
+  if (bh - b * a.Hkv == 0 && threadIdx.x == 0) a.lens_out[b] = kept;
+  for (int i = kept + threadIdx.x; i < a.budget; i += kRankThreads) {
+    src[i] = -1;
+    w_out[i] = 0.f;
+  }
+  if (n <= a.budget) {
+    for (int i = threadIdx.x; i < n; i += kRankThreads) {
+      src[i] = i;
+      w_out[i] = w[i];
+    }
+    return;
+  }
+  const int early = n - a.recent;        // candidates; the rest are kept
+  const int want = a.budget - a.recent;  // of them, the largest (0 <= want < early)
+  // the want-th largest key, a digit of 8 bits at a time from the top
+  uint32_t prefix = 0;
+  int need = want;  // still to find among the keys that start with prefix
+  for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
+    if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < early; i += kRankThreads) {
+      const uint32_t key = order_key(w[i]);
+      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&s_hist[(key >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // lane l sums digits 255 - 8 l - 0..7, highest first
+      int part = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part += s_hist[255 - 8 * threadIdx.x - e];
+      int inc = part;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (threadIdx.x >= o) inc += y;
+      }
+      int above = inc - part;  // keys with a higher digit than this lane's
+      if (above < need && need <= inc) {
+        for (int e = 0; e < 8; ++e) {
+          const int d = 255 - 8 * threadIdx.x - e, c = s_hist[d];
+          if (above + c >= need) {
+            s_prefix = prefix | ((uint32_t)d << shift);
+            s_need = need - above;
+            break;
+          }
+          above += c;
+        }
+      }
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    need = s_need;
+    __syncthreads();
+  }
+  // in index order: keys above the threshold, the first `need` at it, the latest
+  int done = 0, ties = 0;
+  for (int i0 = 0; i0 < n; i0 += kRankThreads) {
+    const int i = i0 + threadIdx.x;
+    float wi = 0.f;
+    bool keep = false, tie = false;
+    if (i < n) {
+      wi = w[i];
+      if (i >= early) {
+        keep = true;
+      } else if (want > 0) {
+        const uint32_t key = order_key(wi);
+        keep = key > prefix;
+        tie = key == prefix;
+      }
+    }
+    // ties counted in the high half (at most 1024 of each per step)
+    int total;
+    const int before = block_prefix((tie ? 0x10000 : 0) | (keep ? 1 : 0), s_warp, &total);
+    const int ties_before = ties + (before >> 16);
+    const int kept_ties = min(ties_before, need) - min(ties, need);  // in this step, before i
+    if (tie) keep = ties_before < need;
+    const int at = done + (before & 0xffff) + kept_ties;
+    if (keep && at < a.budget) {
+      src[at] = i;
+      w_out[at] = wi;
+    }
+    const int ties_after = ties + (total >> 16);
+    done += (total & 0xffff) + (min(ties_after, need) - min(ties, need));
+    ties = ties_after;
+  }
+}
+
+// One warp per block of 16 kept slots of a (sequence, kv head).
+template <int D>
+__global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
+  using L = C4<D>;
+  constexpr int kPiece = D / 8;               // 16 or 8 bytes
+  constexpr int kPieces = 10 * kC4Block;      // per block: 4 + 1 of K, 4 + 1 of V per slot
+  using Piece = typename std::conditional<D == 128, uint4, uint2>::type;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int blocks = (a.budget + kC4Block - 1) / kC4Block;
+  const long long x = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (x >= (long long)a.B * a.Hkv * blocks) return;
+  const int bh = (int)(x / blocks), blk = (int)(x - (long long)bh * blocks);
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+  const int slots = min(kC4Block, a.lens_out[b] - blk * kC4Block);
+  if (slots <= 0) return;
+  // lane s: the byte offset of slot s's source block and its slot there
+  long long from = -1;
+  int from_slot = 0;
+  if (lane < slots) {
+    const int i = a.src[(size_t)bh * a.budget + blk * kC4Block + lane];
+    const int page = i >= 0 ? c4_page(a.in, b, i / kC4Block) : -1;
+    if (page >= 0) {
+      from = (((long long)page * a.Hkv + h) * a.in.blocks_per_page +
+              (i / kC4Block) % a.in.blocks_per_page) * L::kBytes;
+      from_slot = i % kC4Block;
+    } else {
+      c4_flag(a.in);
+    }
+  }
+  const int page = c4_page(a.out, b, blk);
+  if (page < 0) {
+    if (lane == 0) c4_flag(a.out);
+    return;
+  }
+  uint8_t* dst = a.cache + (((long long)page * a.Hkv + h) * a.out.blocks_per_page +
+                            blk % a.out.blocks_per_page) * L::kBytes;
+  // piece p of slot s: 0..3 K codes, 4 K parameters, 5..8 V codes, 9 V parameters
+  auto offset = [](int s, int p) {
+    if (p < 4) return s * L::kRow + p * kPiece;
+    if (p == 4) return L::kOffKPar + s * L::kPar;
+    if (p < 9)
+      return D == 128 ? L::kOffV + s * L::kRow + ((p - 5) ^ ((s & 4) >> 1)) * kPiece
+                      : L::kOffV + (s ^ ((s >> 2) & 1)) * L::kRow + (p - 5) * kPiece;
+    return L::kOffVPar + s * L::kPar;
+  };
+  Piece val[kPieces / 32];
+#pragma unroll
+  for (int n = 0; n < kPieces / 32; ++n) {
+    const int e = n * 32 + lane, s = e / 10, p = e - 10 * s;
+    const long long f = __shfl_sync(0xffffffffu, from, s);
+    const int fs = __shfl_sync(0xffffffffu, from_slot, s);
+    if (f >= 0) val[n] = *reinterpret_cast<const Piece*>(a.cache + f + offset(fs, p));
+  }
+#pragma unroll
+  for (int n = 0; n < kPieces / 32; ++n) {
+    const int e = n * 32 + lane, s = e / 10, p = e - 10 * s;
+    const long long f = __shfl_sync(0xffffffffu, from, s);
+    if (f >= 0) *reinterpret_cast<Piece*>(dst + offset(s, p)) = val[n];
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace
+
+int* cache4_status_word() {
+  int* p = nullptr;
+  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_cache4_status) != cudaSuccess)
+    return nullptr;
+  return p;
+}
+
+// Shape rules of every cache call.
+int check_cache4(int num_pages, int Hkv, int D, int page_size, int B, int width) {
+  if (num_pages < 1 || Hkv < 1 || B < 1 || width < 1) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return FA_ERR_UNSUPPORTED;
+  // a sequence's slots, and the rows over all sequences and heads, are counted in 32 bits
+  if ((long long)width * page_size > (1LL << 30) || (long long)B * Hkv > (1LL << 30))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+namespace {
+
+C4Table make_table(const int* pages, int width, int num_pages, int page_size, int* status) {
+  return C4Table{pages, width, num_pages, page_size / kC4Block, status};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_cache4_page_bytes(int Hkv, int D, int page_size) {
+  if (check_cache4(1, Hkv, D, page_size, 1, 1) != FA_OK) return 0;
+  return (size_t)Hkv * (page_size / kC4Block) * c4_block_bytes(D);
+}
+
+int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, const void* v,
+                     const fa_packed_stride* k_stride, const fa_packed_stride* v_stride, int B,
+                     int T, int Hkv, int D, const int* cu_seqlens, const int* cache_lens,
+                     const int* page_table, int table_width, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_cache4(num_pages, Hkv, D, page_size, B, table_width);
+  if (rc) return rc;
+  if (T < 0 || (!cu_seqlens && T != B) || (long long)T * Hkv > (1LL << 34)) return FA_ERR_INVALID_ARG;
+  const fa_packed_stride plain = {(int64_t)Hkv * D, D};
+  const fa_packed_stride ks = k_stride ? *k_stride : plain, vs = v_stride ? *v_stride : plain;
+  for (int64_t s : {ks.token, ks.head, vs.token, vs.head}) {
+    if (s < 0) return FA_ERR_INVALID_ARG;
+    if (s & 7) return FA_ERR_MISALIGNED;
+  }
+  if (T == 0) return FA_OK;
+  if (!cache || !k || !v || !cache_lens || !page_table) return FA_ERR_INVALID_ARG;
+  if (misaligned(cache, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(cu_seqlens, 4) ||
+      misaligned(cache_lens, 4) || misaligned(page_table, 4))
+    return FA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  int* status = cache4_status_word();
+  if (!status) return FA_ERR_CUDA;
+  AppendArgs a{static_cast<uint8_t*>(cache), static_cast<const __nv_bfloat16*>(k),
+               static_cast<const __nv_bfloat16*>(v), ks.token, ks.head, vs.token, vs.head,
+               cu_seqlens, cache_lens,
+               make_table(page_table, table_width, num_pages, page_size, status), B, T, Hkv};
+  const long long per = kAppendWarps * kAppendItems;
+  const long long grid = ((long long)T * Hkv + per - 1) / per;
+  const auto kernel = D == 128 ? append_kernel<128> : append_kernel<64>;
+  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kAppendWarps * 32), 0,
+                 static_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
+
+int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, void* v, int B, int Hkv,
+                   int S, int D, const int* first, const int* count, const int* page_table,
+                   int table_width, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_cache4(num_pages, Hkv, D, page_size, B, table_width);
+  if (rc) return rc;
+  if (S < 0) return FA_ERR_INVALID_ARG;
+  if (S == 0) return FA_OK;
+  if (!cache || !k || !v || !count || !page_table) return FA_ERR_INVALID_ARG;
+  if (misaligned(cache, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(first, 4) ||
+      misaligned(count, 4) || misaligned(page_table, 4))
+    return FA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
+  int* status = cache4_status_word();
+  if (!status) return FA_ERR_CUDA;
+  ReadArgs a{static_cast<const uint8_t*>(cache), static_cast<__nv_bfloat16*>(k),
+             static_cast<__nv_bfloat16*>(v), first, count,
+             make_table(page_table, table_width, num_pages, page_size, status), B, Hkv, S};
+  const long long blocks = ((long long)B * Hkv * S + 7) / 8;
+  const int grid = (int)(blocks < 32LL * info.sm_count ? blocks : 32LL * info.sm_count);
+  const auto kernel = D == 128 ? read_kernel<128> : read_kernel<64>;
+  if (launch_pdl(kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), a) !=
+      cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
+
+int fa_cache4_evict(void* cache, int num_pages, int page_size, const float* weights, int cap,
+                    const int* cache_lens, const int* page_table, int table_width, int B, int Hkv,
+                    int D, int budget, int recent, const int* out_page_table, int out_table_width,
+                    int* src, float* weights_out, int* lens_out, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_cache4(num_pages, Hkv, D, page_size, B, table_width);
+  if (rc) return rc;
+  if (out_table_width < 1 || cap < 1 || budget < 1 || recent < 0 || recent > budget ||
+      (long long)out_table_width * page_size < budget)
+    return FA_ERR_INVALID_ARG;
+  if (!cache || !weights || !cache_lens || !page_table || !out_page_table || !src || !weights_out ||
+      !lens_out)
+    return FA_ERR_INVALID_ARG;
+  if (misaligned(cache, 16) || misaligned(weights, 4) || misaligned(cache_lens, 4) ||
+      misaligned(page_table, 4) || misaligned(out_page_table, 4) || misaligned(src, 4) ||
+      misaligned(weights_out, 4) || misaligned(lens_out, 4))
+    return FA_ERR_MISALIGNED;
+  const long long blocks = (long long)B * Hkv * ((budget + kC4Block - 1) / kC4Block);
+  if ((blocks + 7) / 8 > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if ((rc = check_device())) return rc;
+  int* status = cache4_status_word();
+  if (!status) return FA_ERR_CUDA;
+  EvictArgs a{static_cast<uint8_t*>(cache), weights, weights_out, src, cache_lens, lens_out,
+              make_table(page_table, table_width, num_pages, page_size, status),
+              make_table(out_page_table, out_table_width, num_pages, page_size, status),
+              B, Hkv, cap, budget, recent};
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (launch_pdl(rank_kernel, dim3(B * Hkv), dim3(kRankThreads), 0, st, a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  const auto kernel = D == 128 ? move_kernel<128> : move_kernel<64>;
+  if (launch_pdl(kernel, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, st, a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(2);
+  return FA_OK;
+}
+
+int fa_cache4_status(fa_stream_t stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_cache4_status, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
+  if (v != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_cache4_status, &zero, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return v;
+}
+
+}  // extern "C"

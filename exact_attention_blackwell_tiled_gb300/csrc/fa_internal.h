@@ -253,6 +253,11 @@ int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
                          const CUtensorMap& tdo, const BwdArgs& a, bool mod, int grid,
                          cudaStream_t stream);
 
+// The 4-bit cache: the status word its kernels record bad tables and lengths in
+// (null if it cannot be found), and the shape rules of its calls.
+int* cache4_status_word();
+int check_cache4(int num_pages, int Hkv, int D, int page_size, int B, int width);
+
 void note_launches(int n);
 
 // Launch with programmatic stream serialisation: the kernel may be scheduled

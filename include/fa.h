@@ -294,6 +294,95 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
                   int window_left, int window_right, float scale, void* workspace,
                   size_t workspace_bytes, int deterministic, fa_stream_t stream);
 
+/*
+ * A paged key/value cache held in 4 bits, the attention of single query tokens to
+ * it, and its thinning out by accumulated attention weight (the pages have no
+ * counterpart; the method they describe serves the prompt, these calls what
+ * follows it).  A head vector of D elements is held as D/32 groups of 32 codes:
+ *   mn = min(x), scale = bf16((max(x) - mn) / 15),
+ *   code = clamp(rint((x - mn) / scale), 0, 15) (0 where scale is 0),
+ *   value = mn + scale * code                       (fp32 arithmetic, finite x)
+ * cache: num_pages pages of fa_cache4_page_bytes(Hkv, D, page_size) bytes, 16-byte
+ * aligned; page_size (tokens) is 16, 32, 64 or 128.  page_table: device int32
+ * [B, table_width]; slot s of sequence b lies in page page_table[b][s / page_size].
+ * Pages may be shared by sequences that only read them.  A page id outside
+ * [0, num_pages), or a length or slot outside the table, is recorded: its token is
+ * not stored, read as zero, or left out of the attention, nothing out of bounds is
+ * touched, and fa_cache4_status returns FA_ERR_INVALID_ARG.
+ * cache_lens: device int32 [B], the tokens each sequence holds (0 allowed).
+ * Lengths and tables are read on the device, so captured calls replay on new ones.
+ * B * Hkv, and a sequence's slots, are at most 2^30; D in {64, 128}.
+ */
+size_t fa_cache4_page_bytes(int Hkv, int D, int page_size); /* 0 on bad sizes */
+
+/*
+ * Stores T new tokens' k, v [T, Hkv, D] bf16 (rows and heads apart by *_stride,
+ * multiples of 8 elements; null: contiguous).  Token i of sequence b is packed row
+ * cu_seqlens[b] + i and goes to slot cache_lens[b] + i; a null cu_seqlens means one
+ * token per sequence (T == B).  cu_seqlens ascends; rows of no sequence are not
+ * stored.  cache_lens is not changed: the caller adds the new tokens to it.
+ */
+int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, const void* v,
+                     const fa_packed_stride* k_stride, const fa_packed_stride* v_stride, int B,
+                     int T, int Hkv, int D, const int* cu_seqlens, const int* cache_lens,
+                     const int* page_table, int table_width, fa_stream_t stream);
+
+/*
+ * The stored values of slots first[b] .. first[b] + count[b] - 1 of every sequence
+ * (first null: from 0), as k, v [B, Hkv, S, D] bf16 (contiguous, 16-byte aligned,
+ * rounded to nearest from the fp32 value); rows from count[b] on are zero.
+ */
+int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, void* v, int B, int Hkv,
+                   int S, int D, const int* first, const int* count, const int* page_table,
+                   int table_width, fa_stream_t stream);
+
+/*
+ * One query token per sequence attends to its cache_lens[b] stored tokens:
+ *   q bf16, element [b][h][d] at b * q_batch_stride + h * q_head_stride + d
+ *   (strides multiples of 8);  o [B, Hq, D] bf16;  lse [B, Hq] fp32, natural log.
+ * A sequence without tokens gets o = 0 and lse = -inf.  Hq / Hkv is at most 128.
+ * weights_out (null: none) [B, Hkv, weight_slots] fp32: for every stored token j
+ *   weights_out[b][hk][j] = weights_in[b][hk][j] + sum of its softmax weights over
+ *   the query heads of hk  (weights_in null: 0; it may be weights_out itself);
+ * elements from cache_lens[b] on are neither read nor written; cache_lens is then
+ * at most weight_slots.  The result does not depend on the order in which blocks
+ * run.  workspace: fa_cache4_attend_workspace_bytes(..., weight_slots or 0) bytes on
+ * the current device, 256-byte aligned, uninitialised; calls that may run at the
+ * same time, captured ones among them, need one each.
+ */
+size_t fa_cache4_attend_workspace_bytes(int B, int Hq, int Hkv, int D, int weight_slots);
+int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_stride, const void* cache,
+                     int num_pages, int page_size, void* o, float* lse, int B, int Hq, int Hkv,
+                     int D, const int* cache_lens, const int* page_table, int table_width,
+                     float scale, const float* weights_in, float* weights_out, int weight_slots,
+                     void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * Keeps at most `budget` tokens of every (sequence, kv head): the latest `recent`
+ * ones and, of the others, those with the largest weights [B, Hkv, cap] (ties: the
+ * lowest slot first; weights are not NaN).  The kept tokens' codes are copied
+ * unchanged, in slot order, to slots 0, 1, ... of the pages of out_page_table
+ * [B, out_table_width], which must be other pages than any table in use names; the
+ * old pages are only read, so sequences that share them lose nothing.  A sequence
+ * with at most `budget` tokens keeps all.
+ *   src [B, Hkv, budget] int32: the old slot of each kept token, -1 behind the last;
+ *   weights_out [B, Hkv, budget] fp32: their weights, 0 behind the last;
+ *   lens_out [B] int32: min(cache_lens[b], budget).
+ * 0 <= recent <= budget, budget >= 1 and at most the slots of out_page_table.
+ */
+int fa_cache4_evict(void* cache, int num_pages, int page_size, const float* weights, int cap,
+                    const int* cache_lens, const int* page_table, int table_width, int B, int Hkv,
+                    int D, int budget, int recent, const int* out_page_table, int out_table_width,
+                    int* src, float* weights_out, int* lens_out, fa_stream_t stream);
+
+/*
+ * Synchronises `stream`, returns and clears what the cache calls on this device
+ * recorded since the previous call: FA_OK, FA_ERR_INVALID_ARG (a page id or length
+ * out of range), FA_ERR_TIMEOUT (a device-side wait); FA_ERR_CUDA if the
+ * synchronisation fails.
+ */
+int fa_cache4_status(fa_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fa_status_string(int status);
 
