@@ -9,6 +9,7 @@ contiguous bf16 CUDA tensor, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -412,56 +413,83 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
                             seqlens_k)
 
 
-def _packed(t, name, heads=None, like=None):
-    """Checks a packed [T, H, D] bf16 CUDA tensor and returns its PackedStride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [T, H, D] with contiguous elements")
-    if like is not None and (t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]
-                             or t.device != like.device):
-        raise ValueError(f"{name} must have q's tokens, head dimension and device")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} must have {heads} heads")
-    # the stride of a dimension of one element is arbitrary: give the kernel a valid one
+# The calls below serve single tokens, where the host's time is most of a call's, so
+# they ask torch for as little as the checks need: device indices instead of device
+# objects and guards, raw stream handles, sizes looked up once per shape.
+
+def _raw_stream(stream, index):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere(index):
+    """Whether device `index` is not the current one (the call is then repeated under
+    a guard)."""
+    return torch._C._cuda_getDevice() != index
+
+
+def _packed(t, name, index=None, shape=None):
+    """Checks a packed [T, H, D] bf16 CUDA tensor (of `shape` on device `index`) and
+    returns its PackedStride by reference, or None where it is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head dimension]")
+    if shape is not None and (t.shape != shape or t.get_device() != index):
+        raise ValueError(f"{name} must be {tuple(shape)} on the same device")
+    if t.is_contiguous():
+        return None
     T, H, D = t.shape
+    if D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous elements")
+    # the stride of a dimension of one element is arbitrary: give the kernel a valid one
     head = t.stride(1) if H > 1 else D
-    token = t.stride(0) if T > 1 else max(H * D, head)
-    return PackedStride(token, head)
+    return ctypes.byref(PackedStride(t.stride(0) if T > 1 else max(H * D, head), head))
 
 
-def _out(t, shape, dtype, device, name, stream):
-    """A checked output of the caller, or a new one that `stream` may write."""
-    if t is not None:
-        if (not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape)
-                or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {tuple(shape)}")
-        return t
+def _packed_kv(q, k, v):
+    """Checks packed q, k, v together; returns their strides."""
+    qs = _packed(q, "q")
+    ks = _packed(k, "k")
+    T, _, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D or k.get_device() != q.get_device():
+        raise ValueError("k must have q's tokens, head dimension and device")
+    return qs, ks, _packed(v, "v", k.get_device(), k.shape)
+
+
+def _given(t, shape, dtype, index, name):
+    """Checks a contiguous tensor of the caller."""
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype
+            or t.get_device() != index or t.shape != torch.Size(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on the inputs' "
+                         "device")
+    return t
+
+
+def _new(shape, dtype, device, stream):
+    """A new tensor that `stream` may write."""
     t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:  # keep its memory until that stream has passed
         t.record_stream(stream)
     return t
 
 
-def _workspace(t, nbytes, device, stream):
-    """The caller's workspace, or a new one of nbytes that `stream` may use."""
-    if t is not None:
-        if not t.is_cuda or t.device != device or not t.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-        return t
-    return _out(None, (max(nbytes, 1),), torch.uint8, device, "workspace", stream)
+def _workspace(t, nbytes, like, stream):
+    """(tensor, bytes) of the caller's workspace, or of a new one that `stream` may use."""
+    if t is None:
+        t = _new(nbytes or 1, torch.uint8, like.device, stream)
+    elif not t.is_cuda or t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return t, t.numel() * t.element_size()
 
 
-def _int32(t, n, device, name):
-    """Checks an int32 CUDA vector of n elements (n None: any number above one)."""
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device
-            or t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != 1):
+def _int32(t, n, index, name):
+    """Checks an int32 CUDA vector of n elements (n None: any number); returns n."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.int32
+            or t.dim() != 1 or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous int32 vector on the inputs' device")
-    if n is not None and t.numel() != n:
+    if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} must have {n} elements")
-    return t
+    return t.shape[0]
 
 
 def _var_window(causal, window):
@@ -472,6 +500,7 @@ def _var_window(causal, window):
     return int(window[0]), int(window[1])
 
 
+@functools.lru_cache(maxsize=4096)
 def varlen_workspace_bytes(B, T, Hq, Hkv, D, backward=False, deterministic=False) -> int:
     return int(lib().fa_varlen_workspace_bytes(B, T, Hq, Hkv, D, int(bool(backward)),
                                                int(bool(deterministic))))
@@ -490,23 +519,29 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: to
     Returns (o [T,Hq,D] bf16, lse [Hq,T] fp32); tokens of no sequence are not
     written.  fwd_status() reports a cu_seqlens that does not ascend in [0, T].
     """
-    qs = _packed(q, "q")
+    qs, ks, vs = _packed_kv(q, k, v)
+    index = q.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return fwd_varlen(q, k, v, cu_seqlens, causal, scale, window, out, lse, workspace,
+                              stream)
     T, Hq, D = q.shape
-    ks = _packed(k, "k", None, q)
     Hkv = k.shape[1]
-    vs = _packed(v, "v", Hkv, q)
     wl, wr = _var_window(causal, window)
-    B = _int32(cu_seqlens, None, q.device, "cu_seqlens").numel() - 1
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with torch.cuda.device(q.device):
-        out = _out(out, (T, Hq, D), torch.bfloat16, q.device, "out", stream)
-        lse = _out(lse, (Hq, T), torch.float32, q.device, "lse", stream)
-        workspace = _workspace(workspace, varlen_workspace_bytes(B, T, Hq, Hkv, D), q.device, stream)
-        rc = lib().fa_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
-                                 B, T, Hq, Hkv, D, ctypes.byref(qs), ctypes.byref(ks),
-                                 ctypes.byref(vs), wl, wr, float(scale), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    B = _int32(cu_seqlens, None, index, "cu_seqlens") - 1
+    if out is None:
+        out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
+    else:
+        _given(out, (T, Hq, D), torch.bfloat16, index, "out")
+    if lse is None:
+        lse = _new((Hq, T), torch.float32, q.device, stream)
+    else:
+        _given(lse, (Hq, T), torch.float32, index, "lse")
+    ws, nbytes = _workspace(workspace, varlen_workspace_bytes(B, T, Hq, Hkv, D), q, stream)
+    rc = lib().fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                             lse.data_ptr(), cu_seqlens.data_ptr(), B, T, Hq, Hkv, D, qs, ks, vs,
+                             wl, wr, 1.0 / math.sqrt(D) if scale is None else scale,
+                             ws.data_ptr(), nbytes, _raw_stream(stream, index))
     if rc != FA_OK:
         raise FAError("fa_fwd_varlen", rc)
     return out, lse
@@ -519,32 +554,31 @@ def bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal: bool = False, scale: flo
     [T,Hkv,D]) bf16, contiguous; tokens of no sequence are not written.  o, do
     and lse are contiguous; the other arguments as in fwd_varlen, and as given
     to it."""
-    qs = _packed(q, "q")
+    qs, ks, vs = _packed_kv(q, k, v)
+    index = q.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal, scale, window,
+                              deterministic, workspace, dq, dk, dv, stream)
     T, Hq, D = q.shape
-    ks = _packed(k, "k", None, q)
     Hkv = k.shape[1]
-    vs = _packed(v, "v", Hkv, q)
-    for t, n in ((o, "o"), (do, "do")):
-        _packed(t, n, Hq, q)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    _out(lse, (Hq, T), torch.float32, q.device, "lse", None)
+    bf = torch.bfloat16
+    _given(o, q.shape, bf, index, "o")
+    _given(do, q.shape, bf, index, "do")
+    _given(lse, (Hq, T), torch.float32, index, "lse")
     wl, wr = _var_window(causal, window)
-    B = _int32(cu_seqlens, None, q.device, "cu_seqlens").numel() - 1
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with torch.cuda.device(q.device):
-        need = varlen_workspace_bytes(B, T, Hq, Hkv, D, True, deterministic)
-        workspace = _workspace(workspace, need, q.device, stream)
-        dq = _out(dq, q.shape, torch.bfloat16, q.device, "dq", stream)
-        dk = _out(dk, k.shape, torch.bfloat16, q.device, "dk", stream)
-        dv = _out(dv, v.shape, torch.bfloat16, q.device, "dv", stream)
-        rc = lib().fa_bwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
-                                 _ptr(dk), _ptr(dv), _ptr(cu_seqlens), B, T, Hq, Hkv, D,
-                                 ctypes.byref(qs), ctypes.byref(ks), ctypes.byref(vs), wl, wr,
-                                 float(scale), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(),
-                                 int(bool(deterministic)), _stream(stream))
+    B = _int32(cu_seqlens, None, index, "cu_seqlens") - 1
+    ws, nbytes = _workspace(workspace,
+                            varlen_workspace_bytes(B, T, Hq, Hkv, D, True, bool(deterministic)),
+                            q, stream)
+    dq = _new(q.shape, bf, q.device, stream) if dq is None else _given(dq, q.shape, bf, index, "dq")
+    dk = _new(k.shape, bf, q.device, stream) if dk is None else _given(dk, k.shape, bf, index, "dk")
+    dv = _new(k.shape, bf, q.device, stream) if dv is None else _given(dv, k.shape, bf, index, "dv")
+    rc = lib().fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                             lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                             cu_seqlens.data_ptr(), B, T, Hq, Hkv, D, qs, ks, vs, wl, wr,
+                             1.0 / math.sqrt(D) if scale is None else scale, ws.data_ptr(), nbytes,
+                             int(bool(deterministic)), _raw_stream(stream, index))
     if rc != FA_OK:
         raise FAError("fa_bwd_varlen", rc)
     return dq, dk, dv
@@ -590,26 +624,27 @@ def _cache4(cache, D):
     if cache.dim() != 3 or not cache.is_contiguous() or D not in (64, 128):
         raise ValueError("cache must be a contiguous [pages, Hkv, bytes] tensor of cache4_empty, "
                          "with head dimension 64 or 128")
-    page, rest = divmod(cache.shape[2], D + D // 4)
+    pages, Hkv, nbytes = cache.shape
+    page, rest = divmod(nbytes, D + D // 4)
     if rest or page not in (16, 32, 64, 128):
-        raise ValueError(f"cache pages of {cache.shape[2]} bytes do not hold tokens of {D} elements")
-    return cache.shape[0], cache.shape[1], page
+        raise ValueError(f"cache pages of {nbytes} bytes do not hold tokens of {D} elements")
+    return pages, Hkv, page
 
 
-def _page_table(t, B, device, name="page_table"):
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device
-            or t.dtype != torch.int32 or not t.is_contiguous()):
+def _page_table(t, B, index, name="page_table"):
+    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.int32
+            or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous int32 tensor on the cache's device")
     if t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1:
         raise ValueError(f"{name} must be [{B}, pages per sequence]")
     return t.shape[1]
 
 
-def _weights(t, B, Hkv, device, name):
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device
-            or t.dtype != torch.float32 or not t.is_contiguous()):
+def _weights(t, B, Hkv, index, name):
+    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.float32
+            or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous fp32 tensor on the cache's device")
-    if t.dim() != 3 or tuple(t.shape[:2]) != (B, Hkv) or t.shape[2] < 1:
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != Hkv or t.shape[2] < 1:
         raise ValueError(f"{name} must be [{B}, {Hkv}, slots]")
     return t.shape[2]
 
@@ -634,20 +669,24 @@ def cache4_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_ta
     (T == B).  cache_lens is left as it is: add the new tokens to it afterwards.
     """
     ks = _packed(k, "k")
+    index = k.get_device()
+    vs = _packed(v, "v", index, k.shape)
     T, Hkv, D = k.shape
-    vs = _packed(v, "v", Hkv, k)
     pages, heads, page = _cache4(cache, D)
-    if heads != Hkv or cache.device != k.device:
+    if heads != Hkv or cache.get_device() != index:
         raise ValueError("cache and k must have the same kv heads and device")
-    B = _int32(cache_lens, None, k.device, "cache_lens").numel()
-    width = _page_table(page_table, B, k.device)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return cache4_append(cache, k, v, page_table, cache_lens, cu_seqlens, stream)
+    B = _int32(cache_lens, None, index, "cache_lens")
+    width = _page_table(page_table, B, index)
+    cu = None
     if cu_seqlens is not None:
-        _int32(cu_seqlens, B + 1, k.device, "cu_seqlens")
-    with torch.cuda.device(k.device):
-        rc = lib().fa_cache4_append(_ptr(cache), pages, page, _ptr(k), _ptr(v), ctypes.byref(ks),
-                                    ctypes.byref(vs), B, T, Hkv, D,
-                                    None if cu_seqlens is None else _ptr(cu_seqlens),
-                                    _ptr(cache_lens), _ptr(page_table), width, _stream(stream))
+        _int32(cu_seqlens, B + 1, index, "cu_seqlens")
+        cu = cu_seqlens.data_ptr()
+    rc = lib().fa_cache4_append(cache.data_ptr(), pages, page, k.data_ptr(), v.data_ptr(), ks, vs, B,
+                                T, Hkv, D, cu, cache_lens.data_ptr(), page_table.data_ptr(), width,
+                                _raw_stream(stream, index))
     if rc != FA_OK:
         raise FAError("fa_cache4_append", rc)
 
@@ -658,23 +697,36 @@ def cache4_read(cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tens
     count[b] - 1 of every sequence (``first`` None: from 0) as bf16 k, v
     [B,Hkv,S,D], zero from count[b] on."""
     pages, Hkv, page = _cache4(cache, D)
-    B = _int32(count, None, cache.device, "count").numel()
-    width = _page_table(page_table, B, cache.device)
+    index = cache.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return cache4_read(cache, page_table, first, count, S, D, k, v, stream)
+    B = _int32(count, None, index, "count")
+    width = _page_table(page_table, B, index)
+    at = None
     if first is not None:
-        _int32(first, B, cache.device, "first")
-    with torch.cuda.device(cache.device):
-        k = _out(k, (B, Hkv, S, D), torch.bfloat16, cache.device, "k", stream)
-        v = _out(v, (B, Hkv, S, D), torch.bfloat16, cache.device, "v", stream)
-        rc = lib().fa_cache4_read(_ptr(cache), pages, page, _ptr(k), _ptr(v), B, Hkv, int(S), D,
-                                  None if first is None else _ptr(first), _ptr(count),
-                                  _ptr(page_table), width, _stream(stream))
+        _int32(first, B, index, "first")
+        at = first.data_ptr()
+    shape, bf = (B, Hkv, S, D), torch.bfloat16
+    k = _new(shape, bf, cache.device, stream) if k is None else _given(k, shape, bf, index, "k")
+    v = _new(shape, bf, cache.device, stream) if v is None else _given(v, shape, bf, index, "v")
+    rc = lib().fa_cache4_read(cache.data_ptr(), pages, page, k.data_ptr(), v.data_ptr(), B, Hkv, S, D,
+                              at, count.data_ptr(), page_table.data_ptr(), width,
+                              _raw_stream(stream, index))
     if rc != FA_OK:
         raise FAError("fa_cache4_read", rc)
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
+def _attend_bytes(index, B, Hq, Hkv, D, weight_slots):
+    return int(lib().fa_cache4_attend_workspace_bytes(B, Hq, Hkv, D, weight_slots))
+
+
 def cache4_attend_workspace_bytes(B, Hq, Hkv, D, weight_slots: int = 0) -> int:
-    return int(lib().fa_cache4_attend_workspace_bytes(B, Hq, Hkv, D, int(weight_slots)))
+    """Workspace bytes of cache4_attend on the current device; weight_slots: the last
+    dimension of its weights, 0 without."""
+    return _attend_bytes(torch._C._cuda_getDevice(), B, Hq, Hkv, D, int(weight_slots))
 
 
 def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
@@ -691,35 +743,41 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     at what the tensor holds there, so it begins as zeros.
     Returns (o [B,Hq,D] bf16, lse [B,Hq] fp32); o = 0, lse = -inf without tokens.
     """
-    qs = _packed(q, "q")
+    _packed(q, "q")
+    index = q.get_device()
     B, Hq, D = q.shape
     pages, Hkv, page = _cache4(cache, D)
-    if cache.device != q.device:
+    if cache.get_device() != index:
         raise ValueError("cache and q must be on one device")
-    _int32(cache_lens, B, q.device, "cache_lens")
-    width = _page_table(page_table, B, q.device)
-    slots = 0
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return cache4_attend(q, cache, page_table, cache_lens, scale, weights, weights_out, out,
+                                 lse, workspace, stream)
+    _int32(cache_lens, B, index, "cache_lens")
+    width = _page_table(page_table, B, index)
+    slots, w_in, w_out = 0, None, None
     if weights is not None:
-        slots = _weights(weights, B, Hkv, q.device, "weights")
-        weights_out = weights if weights_out is None else weights_out
+        slots = _weights(weights, B, Hkv, index, "weights")
+        w_in = w_out = weights.data_ptr()
     if weights_out is not None:
-        if weights is not None and weights_out.shape != weights.shape:
+        n = _weights(weights_out, B, Hkv, index, "weights_out")
+        if weights is not None and n != slots:
             raise ValueError("weights_out must have weights' shape")
-        slots = _weights(weights_out, B, Hkv, q.device, "weights_out")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with torch.cuda.device(q.device):
-        out = _out(out, (B, Hq, D), torch.bfloat16, q.device, "out", stream)
-        lse = _out(lse, (B, Hq), torch.float32, q.device, "lse", stream)
-        workspace = _workspace(workspace, cache4_attend_workspace_bytes(B, Hq, Hkv, D, slots),
-                               q.device, stream)
-        rc = lib().fa_cache4_attend(_ptr(q), qs.token, qs.head, _ptr(cache), pages, page, _ptr(out),
-                                    _ptr(lse), B, Hq, Hkv, D, _ptr(cache_lens), _ptr(page_table),
-                                    width, float(scale),
-                                    None if weights is None else _ptr(weights),
-                                    None if weights_out is None else _ptr(weights_out), slots,
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream(stream))
+        slots, w_out = n, weights_out.data_ptr()
+    if out is None:
+        out = _new((B, Hq, D), torch.bfloat16, q.device, stream)
+    else:
+        _given(out, (B, Hq, D), torch.bfloat16, index, "out")
+    if lse is None:
+        lse = _new((B, Hq), torch.float32, q.device, stream)
+    else:
+        _given(lse, (B, Hq), torch.float32, index, "lse")
+    ws, nbytes = _workspace(workspace, _attend_bytes(index, B, Hq, Hkv, D, slots), q, stream)
+    rc = lib().fa_cache4_attend(q.data_ptr(), q.stride(0), q.stride(1), cache.data_ptr(), pages, page,
+                                out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D,
+                                cache_lens.data_ptr(), page_table.data_ptr(), width,
+                                1.0 / math.sqrt(D) if scale is None else scale, w_in, w_out, slots,
+                                ws.data_ptr(), nbytes, _raw_stream(stream, index))
     if rc != FA_OK:
         raise FAError("fa_cache4_attend", rc)
     return out, lse
@@ -736,21 +794,35 @@ def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torc
     last; weights fp32 [B,Hkv,budget], 0 behind the last; lens int32 [B]).
     """
     pages, Hkv, page = _cache4(cache, D)
-    dev = cache.device
-    B = _int32(cache_lens, None, dev, "cache_lens").numel()
-    width = _page_table(page_table, B, dev)
-    out_width = _page_table(out_page_table, B, dev, "out_page_table")
-    cap = _weights(weights, B, Hkv, dev, "weights")
+    index = cache.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return cache4_evict(cache, page_table, cache_lens, weights, out_page_table, D, budget,
+                                recent, src, weights_out, lens_out, stream)
+    B = _int32(cache_lens, None, index, "cache_lens")
+    width = _page_table(page_table, B, index)
+    out_width = _page_table(out_page_table, B, index, "out_page_table")
+    cap = _weights(weights, B, Hkv, index, "weights")
     if budget < 1 or not 0 <= recent <= budget or out_width * page < budget:
         raise ValueError("budget must be positive, at least recent and within out_page_table")
-    with torch.cuda.device(dev):
-        src = _out(src, (B, Hkv, budget), torch.int32, dev, "src", stream)
-        weights_out = _out(weights_out, (B, Hkv, budget), torch.float32, dev, "weights_out", stream)
-        lens_out = _out(lens_out, (B,), torch.int32, dev, "lens_out", stream)
-        rc = lib().fa_cache4_evict(_ptr(cache), pages, page, _ptr(weights), cap, _ptr(cache_lens),
-                                   _ptr(page_table), width, B, Hkv, D, int(budget), int(recent),
-                                   _ptr(out_page_table), out_width, _ptr(src), _ptr(weights_out),
-                                   _ptr(lens_out), _stream(stream))
+    shape = (B, Hkv, budget)
+    if src is None:
+        src = _new(shape, torch.int32, cache.device, stream)
+    else:
+        _given(src, shape, torch.int32, index, "src")
+    if weights_out is None:
+        weights_out = _new(shape, torch.float32, cache.device, stream)
+    else:
+        _given(weights_out, shape, torch.float32, index, "weights_out")
+    if lens_out is None:
+        lens_out = _new((B,), torch.int32, cache.device, stream)
+    else:
+        _given(lens_out, (B,), torch.int32, index, "lens_out")
+    rc = lib().fa_cache4_evict(cache.data_ptr(), pages, page, weights.data_ptr(), cap,
+                               cache_lens.data_ptr(), page_table.data_ptr(), width, B, Hkv, D,
+                               budget, recent, out_page_table.data_ptr(), out_width, src.data_ptr(),
+                               weights_out.data_ptr(), lens_out.data_ptr(),
+                               _raw_stream(stream, index))
     if rc != FA_OK:
         raise FAError("fa_cache4_evict", rc)
     return src, weights_out, lens_out

@@ -241,13 +241,16 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u, int group) 
   return w;
 }
 
-// Unit u of a packed call: (item, kv head), the head running fastest.
+// Unit u of a packed call with n_items items: groups of head_group kv heads in
+// turn; in a group (item, kv head), the head running fastest.
 template <bool kMod, int QB>
-__device__ __forceinline__ BwdUnit bwd_unit_var(const BwdArgs& a, int u, int group) {
+__device__ __forceinline__ BwdUnit bwd_unit_var(const BwdArgs& a, int u, int group, int n_items) {
   BwdUnit w;
-  const int item = u / a.Hkv;
+  const int G = a.head_group, g = u / (G * n_items), h0 = g * G, gg = min(G, a.Hkv - h0);
+  const int r = u - g * G * n_items;
+  const int item = r / gg;
   const VarItem it = load_item(a.items, item);
-  w.hk = w.bhk = u - item * a.Hkv;
+  w.hk = w.bhk = h0 + (r - item * gg);
   w.b = it.b;
   w.j = it.tile;
   w.kv_len = it.len;

@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
-  const int n_units = kVar ? *a.n_items * a.Hkv : a.n_units;
+  const int n_items = kVar ? *a.n_items : 0;
+  const int n_units = kVar ? n_items * a.Hkv : a.n_units;
   // The r-th unit of this CTA.  Static dealing: computed by every role alike.
   // Dynamic dealing: the TMA thread takes the next unit number from the global
   // counter and posts it in ring slot r % kURing (take_unit); the other roles
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     return u;
   };
   auto unit_of = [&](int u) {
-    if constexpr (kVar) return bwd_unit_var<kMod, kQB>(a, u, group);
+    if constexpr (kVar) return bwd_unit_var<kMod, kQB>(a, u, group, n_items);
     else return bwd_unit<kMod, kQB>(a, u, group);
   };
   // the q head of the tensor maps' head coordinate, and (bh, block iq)'s places

@@ -10,7 +10,8 @@
 //   choice.  Bound by memory: it reads 4 D bytes of a token's key and value and
 //   writes 5/4 D.  Half a warp holds one vector (16 bytes a lane at D = 128), so
 //   minimum and maximum take two shuffles each and a warp stores a token's key
-//   and value together.
+//   and value together; a warp takes four (token, head) pairs, whose loads it
+//   issues before it looks for the places they go to.
 // read: value = min + scale * code in one fp32 FMA, rounded once to bf16.  Reads
 //   5/4 D bytes of a token, writes 4 D.
 // evict: two kernels.  The first ranks one (sequence, kv head) per block: the K
@@ -44,18 +45,35 @@ struct AppendArgs {
   int B, T, Hkv;
 };
 
-constexpr int kAppendWarps = 8, kAppendItems = 4;  // (token, head) pairs per warp
+constexpr int kAppendWarps = 4, kAppendItems = 4;  // (token, head) pairs per warp
 
-// Sequence that holds packed token i, or -1: cu ascends, so halving finds it.
+// Sequence that holds packed token i, or -1, by a whole warp: each step splits the
+// range that cu bounds in 32.
 __device__ int find_sequence(const int* cu, int B, int i) {
-  int lo = 0, hi = B;  // cu[lo] <= i < cu[hi]
-  if (i < cu[0] || i >= cu[B]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= i) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // the sequence is among lo .. lo + n - 1, if there is one
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int at = lo + lane * step;  // first sequence of the lane's piece
+    const unsigned m = __ballot_sync(0xffffffffu, at < lo + n && cu[at] <= i);
+    const int pieces = 32 - __clz(m | 1);  // cu ascends: the last piece that begins at or before i
+    n = min(step, lo + n - (lo + (pieces - 1) * step));
+    lo += (pieces - 1) * step;
   }
-  return lo;
+  return cu[lo] <= i && i < cu[lo + 1] ? lo : -1;
+}
+
+// Code of d = x - mn for scale sc: rint(d / sc), ties to even.  A product with the
+// reciprocal gives the code or one beside it; the remainder d - code sc, exact in
+// one FMA since code * sc has 13 bits and lies within sc of d, tells which.
+__device__ __forceinline__ uint32_t quantise_one(float d, float sc, float rcp, float half) {
+  const float m = __fmaf_rn(d, rcp, 12582912.f);  // 1.5 * 2^23 + code
+  const float e = __fmaf_rn(-__fsub_rn(m, 12582912.f), sc, d);
+  int c = __float_as_int(m) & 31;
+  // an odd code gives way at a remainder of exactly half a step
+  const float limit = __int_as_float(__float_as_int(half) - (c & 1));
+  if (fabsf(e) > limit) c += e > 0.f ? 1 : -1;
+  return (uint32_t)min(c, 15);
 }
 
 template <int D>
@@ -63,49 +81,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   using L = C4<D>;
   constexpr int kE = D / 16;  // elements per lane: 16 lanes hold a vector
   constexpr int kLanesPerGroup = 32 / kE;
-  __shared__ long long s_block[kAppendWarps * kAppendItems];  // byte offset of the block, or -1
-  __shared__ int s_slot[kAppendWarps * kAppendItems];
-  grid_dep_wait();
-  grid_dep_launch();
-  const long long total = (long long)a.T * a.Hkv;
-  const long long base = (long long)blockIdx.x * (kAppendWarps * kAppendItems);
-  if (threadIdx.x < kAppendWarps * kAppendItems) {
-    const long long item = base + threadIdx.x;
-    long long off = -1;
-    int slot = 0;
-    if (item < total) {
-      const int tok = (int)(item / a.Hkv), h = (int)(item - (long long)tok * a.Hkv);
-      const int b = a.cu ? find_sequence(a.cu, a.B, tok) : tok;
-      if (b >= 0) {
-        const long long s = (long long)a.lens[b] + (a.cu ? tok - a.cu[b] : 0);
-        int page = -1;
-        if (s >= 0 && s < (long long)a.table.width * a.table.blocks_per_page * kC4Block)
-          page = c4_page(a.table, b, (int)(s / kC4Block));
-        if (page < 0) {
-          c4_flag(a.table);
-        } else {
-          slot = (int)(s % kC4Block);
-          const int blk = (int)(s / kC4Block) % a.table.blocks_per_page;
-          off = (((long long)page * a.Hkv + h) * a.table.blocks_per_page + blk) * L::kBytes;
-        }
-      }
-    }
-    s_block[threadIdx.x] = off;
-    s_slot[threadIdx.x] = slot;
-  }
-  __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool is_v = lane >= 16;
   const int l = lane & 15;
   const int g = l / kLanesPerGroup, part = l % kLanesPerGroup;
+  const long long total = (long long)a.T * a.Hkv;
+  const long long item0 = ((long long)blockIdx.x * kAppendWarps + warp) * kAppendItems;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (item0 >= total) return;
+  // the vectors first: where they go is found while they are on their way
+  const int tok0 = (int)(item0 / a.Hkv), h0 = (int)(item0 - (long long)tok0 * a.Hkv);
   uint32_t x[kAppendItems][kE / 2];
 #pragma unroll
   for (int n = 0; n < kAppendItems; ++n) {
-    const long long item = base + warp * kAppendItems + n;
 #pragma unroll
     for (int e = 0; e < kE / 2; ++e) x[n][e] = 0u;
-    if (s_block[warp * kAppendItems + n] >= 0) {
-      const int tok = (int)(item / a.Hkv), h = (int)(item - (long long)tok * a.Hkv);
+    if (item0 + n < total) {
+      const int tok = tok0 + (h0 + n) / a.Hkv, h = (h0 + n) % a.Hkv;
       const __nv_bfloat16* src = (is_v ? a.v + tok * a.v_token + h * a.v_head
                                        : a.k + tok * a.k_token + h * a.k_head) + l * kE;
       if constexpr (kE == 8) {
@@ -117,10 +110,40 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
       }
     }
   }
+  // lane n: the byte offset of item n's block, or -1, and its slot there
+  long long off_n = -1;
+  int slot_n = 0;
+  {
+    const int first = a.cu ? find_sequence(a.cu, a.B, tok0) : tok0;
+    if (lane < kAppendItems && item0 + lane < total) {
+      const int tok = tok0 + (h0 + lane) / a.Hkv, h = (h0 + lane) % a.Hkv;
+      int b = a.cu ? first : tok;
+      if (a.cu) {
+        // later items may belong to later sequences
+        if (b < 0 && tok > tok0) b = 0;
+        while (b >= 0 && b < a.B && tok >= a.cu[b + 1]) ++b;
+        if (b >= a.B || (b >= 0 && tok < a.cu[b])) b = -1;
+      }
+      if (b >= 0) {
+        const long long s = (long long)a.lens[b] + (a.cu ? tok - a.cu[b] : 0);
+        int page = -1;
+        if (s >= 0 && s < (long long)a.table.width * a.table.blocks_per_page * kC4Block)
+          page = c4_page(a.table, b, (int)(s / kC4Block));
+        if (page < 0) {
+          c4_flag(a.table);
+        } else {
+          slot_n = (int)(s % kC4Block);
+          const int blk = (int)(s / kC4Block) & (a.table.blocks_per_page - 1);
+          off_n = (((long long)page * a.Hkv + h) * a.table.blocks_per_page + blk) * L::kBytes;
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int n = 0; n < kAppendItems; ++n) {
-    const long long off = s_block[warp * kAppendItems + n];
-    const int slot = s_slot[warp * kAppendItems + n];
+    const long long off = __shfl_sync(0xffffffffu, off_n, n);
+    const int slot = __shfl_sync(0xffffffffu, slot_n, n);
+    if (off < 0) continue;
     float f[kE], mn = INFINITY, mx = -INFINITY;
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
@@ -136,14 +159,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
     const __nv_bfloat16 sc16 = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
     const float sc = __bfloat162float(sc16);
     uint32_t codes = 0;
-    if (sc > 0.f) {
+    if (sc >= 1.17549435e-38f) {
+      const float rcp = __fdiv_rn(1.0f, sc), half = 0.5f * sc;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const float c = rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc));
-        codes |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * e);
-      }
+      for (int e = 0; e < kE; ++e)
+        codes |= quantise_one(__fsub_rn(f[e], mn), sc, rcp, half) << (4 * e);
+    } else if (sc > 0.f) {  // no reciprocal in range
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        codes |= (uint32_t)fminf(rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc)), 15.f) << (4 * e);
     }
-    if (off < 0) continue;
     uint8_t* blk = a.cache + off;
     if (!is_v) {
       // elements 32 g + kE part ..: word (t, g), t = 8-element piece of the group
@@ -174,61 +199,84 @@ struct ReadArgs {
   const int* count;      // [B]
   C4Table table;
   int B, Hkv, S;
+  int blocks;  // cache blocks that S slots can lie in
 };
 
-// A warp takes one slot of one head: lanes 0..15 its key, 16..31 its value.
+// Two fields of w (low byte of w >> s) as their values, rounded to bf16.
+__device__ __forceinline__ uint32_t two_values(uint32_t w, int s, float sc, float mn) {
+  return pack_bf16x2(__fmaf_rn(sc, (float)((w >> s) & 15u), mn),
+                     __fmaf_rn(sc, (float)((w >> (s + 4)) & 15u), mn));
+}
+
+// One warp per cache block of 16 slots of a head, four lanes per key or value: a
+// lane loads its quarter of the codes and the parameters in one piece each and
+// stores 8 elements of every group, so eight loads are in flight per lane before
+// the first store.
 template <int D>
-__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(128) read_kernel(const ReadArgs a) {
   using L = C4<D>;
-  constexpr int kE = D / 16, kLanesPerGroup = 32 / kE;
+  constexpr int kG = L::kGroups;
+  const int lane = threadIdx.x & 31;
+  const long long x = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const bool is_v = lane >= 16;
-  const int l = lane & 15, g = l / kLanesPerGroup, part = l % kLanesPerGroup;
-  const long long total = (long long)a.B * a.Hkv * a.S;
-  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
-  for (long long x = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); x < total;
-       x += warps) {
-    const long long bh = x / a.S;
-    const int s = (int)(x - bh * a.S), b = (int)(bh / a.Hkv), h = (int)(bh - (long long)b * a.Hkv);
-    uint32_t out[kE / 2];
+  if (x >= (long long)a.B * a.Hkv * a.blocks) return;
+  const int bh = (int)(x / a.blocks), j = (int)(x - (long long)bh * a.blocks);
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+  const int from = a.first ? a.first[b] : 0, count = min(a.count[b], a.S);
+  const int first = max(from, 0);  // a negative one is out of range: rows of zeros
+  const int blk = first / kC4Block + j;
+  // output row of slot s of the block; rows outside [0, S) are not this warp's
+  const long long row0 = (long long)blk * kC4Block - first;
+  if (row0 >= a.S) return;
+  int page = -1;
+  if (row0 < count) {
+    page = from >= 0 ? c4_page(a.table, b, blk) : -1;
+    if (page < 0 && lane == 0) c4_flag(a.table);
+  }
+  const uint8_t* src = a.cache + (((long long)page * a.Hkv + h) * a.table.blocks_per_page +
+                                  (blk & (a.table.blocks_per_page - 1))) * L::kBytes;
+  const int t = lane & 3;
+  uint32_t w[4][kG], par[4][kG];  // K of slots lane / 4 and + 8, V of the same
 #pragma unroll
-    for (int e = 0; e < kE / 2; ++e) out[e] = 0u;
-    if (s < a.count[b]) {
-      const long long at = (long long)(a.first ? a.first[b] : 0) + s;
-      int page = -1;
-      if (at >= 0 && at < (long long)a.table.width * a.table.blocks_per_page * kC4Block)
-        page = c4_page(a.table, b, (int)(at / kC4Block));
-      if (page < 0) {
-        if (lane == 0) c4_flag(a.table);
-      } else {
-        const int slot = (int)(at % kC4Block), blk = (int)(at / kC4Block) % a.table.blocks_per_page;
-        const uint8_t* p =
-            a.cache + (((long long)page * a.Hkv + h) * a.table.blocks_per_page + blk) * L::kBytes;
-        uint32_t codes;
-        if (!is_v) {
-          const uint8_t* w = p + slot * L::kRow + ((part * kE / 8) * L::kGroups + g) * 4;
-          if constexpr (kE == 8) codes = *reinterpret_cast<const uint32_t*>(w);
-          else codes = *reinterpret_cast<const uint16_t*>(w + (part & 1) * 2);
-        } else {
-          const int i = part * kE / 4;
-          codes = *reinterpret_cast<const uint16_t*>(p + L::v_half(slot, i, g));
-          if constexpr (kE == 8)
-            codes |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + L::v_half(slot, i + 1, g)) << 16;
-        }
-        const uint32_t par = *reinterpret_cast<const uint32_t*>(
-            p + (is_v ? L::kOffVPar : L::kOffKPar) + slot * L::kPar + g * 4);
-        const float sc = c4_scale(par), mn = c4_min(par);
+  for (int n = 0; n < 4; ++n) {
+    const int s = (lane >> 2) + 8 * (n & 1);
 #pragma unroll
-        for (int e = 0; e < kE / 2; ++e)
-          out[e] = pack_bf16x2(__fmaf_rn(sc, (float)((codes >> (8 * e)) & 15u), mn),
-                               __fmaf_rn(sc, (float)((codes >> (8 * e + 4)) & 15u), mn));
-      }
+    for (int g = 0; g < kG; ++g) w[n][g] = par[n][g] = 0u;
+    if (page < 0 || row0 + s < 0 || row0 + s >= count) continue;
+    // words t * kG ..: K's lane piece; V's chunks 2 t and 2 t + 1
+    const uint8_t* c = src + (n < 2 ? s * L::kRow + t * 4 * kG : L::v_half(s, 2 * t, 0));
+    const uint8_t* q = src + (n < 2 ? L::kOffKPar : L::kOffVPar) + s * L::kPar;
+    if constexpr (kG == 4) {
+      const uint4 y = *reinterpret_cast<const uint4*>(c), z = *reinterpret_cast<const uint4*>(q);
+      w[n][0] = y.x, w[n][1] = y.y, w[n][2] = y.z, w[n][3] = y.w;
+      par[n][0] = z.x, par[n][1] = z.y, par[n][2] = z.z, par[n][3] = z.w;
+    } else {
+      const uint2 y = *reinterpret_cast<const uint2*>(c), z = *reinterpret_cast<const uint2*>(q);
+      w[n][0] = y.x, w[n][1] = y.y;
+      par[n][0] = z.x, par[n][1] = z.y;
     }
-    __nv_bfloat16* dst = (is_v ? a.v : a.k) + x * D + l * kE;
-    if constexpr (kE == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const long long row = row0 + (lane >> 2) + 8 * (n & 1);
+    if (row < 0 || row >= a.S) continue;
+    __nv_bfloat16* dst = (n < 2 ? a.k : a.v) + ((long long)bh * a.S + row) * D + 8 * t;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      // elements 32 g + 8 t + 0..7: K's word g; V's half g of two chunks
+      uint32_t codes = w[n][g];
+      if (n >= 2) {
+        if constexpr (kG == 4)
+          codes = __byte_perm(w[n][g / 2], w[n][2 + g / 2], (g & 1) ? 0x7632 : 0x5410);
+        else
+          codes = __byte_perm(w[n][0], w[n][1], (g & 1) ? 0x7632 : 0x5410);
+      }
+      const float sc = c4_scale(par[n][g]), mn = c4_min(par[n][g]);
+      *reinterpret_cast<uint4*>(dst + 32 * g) =
+          make_uint4(two_values(codes, 0, sc, mn), two_values(codes, 8, sc, mn),
+                     two_values(codes, 16, sc, mn), two_values(codes, 24, sc, mn));
+    }
   }
 }
 
@@ -456,9 +504,16 @@ bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>
 }  // namespace
 
 int* cache4_status_word() {
-  int* p = nullptr;
+  // looked up once per device: the lookup takes longer than the rest of a call
+  static std::atomic<int*> known[64] = {};
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return nullptr;
+  int* p = known[dev].load(std::memory_order_acquire);
+  if (p) return p;
   if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_cache4_status) != cudaSuccess)
     return nullptr;
+  known[dev].store(p, std::memory_order_release);
   return p;
 }
 
@@ -521,6 +576,7 @@ int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, c
                make_table(page_table, table_width, num_pages, page_size, status), B, T, Hkv};
   const long long per = kAppendWarps * kAppendItems;
   const long long grid = ((long long)T * Hkv + per - 1) / per;
+  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   const auto kernel = D == 128 ? append_kernel<128> : append_kernel<64>;
   if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kAppendWarps * 32), 0,
                  static_cast<cudaStream_t>(stream), a) != cudaSuccess)
@@ -542,18 +598,18 @@ int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, voi
       misaligned(count, 4) || misaligned(page_table, 4))
     return FA_ERR_MISALIGNED;
   if ((rc = check_device())) return rc;
-  int dev;
-  DeviceInfo info;
-  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   int* status = cache4_status_word();
   if (!status) return FA_ERR_CUDA;
+  // S slots from any first one
+  const int blocks = (int)(((long long)S + (first ? kC4Block - 1 : 0) + kC4Block - 1) / kC4Block);
+  const long long grid = ((long long)B * Hkv * blocks + 3) / 4;
+  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   ReadArgs a{static_cast<const uint8_t*>(cache), static_cast<__nv_bfloat16*>(k),
              static_cast<__nv_bfloat16*>(v), first, count,
-             make_table(page_table, table_width, num_pages, page_size, status), B, Hkv, S};
-  const long long blocks = ((long long)B * Hkv * S + 7) / 8;
-  const int grid = (int)(blocks < 32LL * info.sm_count ? blocks : 32LL * info.sm_count);
+             make_table(page_table, table_width, num_pages, page_size, status), B, Hkv, S,
+             blocks};
   const auto kernel = D == 128 ? read_kernel<128> : read_kernel<64>;
-  if (launch_pdl(kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), a) !=
+  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(128), 0, static_cast<cudaStream_t>(stream), a) !=
       cudaSuccess)
     return FA_ERR_CUDA;
   note_launches(1);

@@ -764,10 +764,17 @@ int launch_fwd_var(const CUtensorMap& any, const FwdArgs& a, int D, int max_item
 }
 
 int* fwd_status_word() {
-  int* status = nullptr;
-  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&status), g_fwd_status) != cudaSuccess)
+  // looked up once per device
+  static std::atomic<int*> known[64] = {};
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return nullptr;
+  int* p = known[dev].load(std::memory_order_acquire);
+  if (p) return p;
+  if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_fwd_status) != cudaSuccess)
     return nullptr;
-  return status;
+  known[dev].store(p, std::memory_order_release);
+  return p;
 }
 
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -185,6 +185,8 @@ def test_append_and_read(gpu, D, page):
     cu = _cu(lens)
     k, v = _kv(cu[-1] + 5, Hkv, D, page)
     k[2], v[3] = 1.5, 0.0                              # groups of one value
+    k[5:20] = (torch.arange(15 * Hkv * D).view(15, Hkv, D) * 7 % 31).bfloat16() / 4  # ties
+    v[5:20] = (torch.arange(15 * Hkv * D).view(15, Hkv, D) * 11 % 48).bfloat16()
     k[4] = torch.linspace(-1e30, 1e30, D).bfloat16()   # wide and tiny ranges
     v[4] = (torch.linspace(0, 1, D) * 1e-38).bfloat16()
     table, n = _table([x + 1 for x in lens], page)

@@ -84,7 +84,7 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         fa._var_window(True, (-1, 0))
     with pytest.raises(TypeError):
-        fa._int32(cu, None, torch.device("cuda"), "cu_seqlens")
+        fa._int32(cu, None, 0, "cu_seqlens")
 
 
 def test_reference_gradient():
