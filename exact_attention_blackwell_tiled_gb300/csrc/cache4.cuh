@@ -56,13 +56,21 @@ struct C4Table {
   const int* pages;  // [B, width]
   int width;
   int num_pages;
-  int blocks_per_page;
+  int shift;  // log2 of the blocks per page
   int* status;
+  __host__ __device__ int blocks_per_page() const { return 1 << shift; }
+  __host__ __device__ int in_page(int blk) const { return blk & ((1 << shift) - 1); }
 };
+
+inline int c4_shift(int page_size) {
+  int s = 0;
+  while ((kC4Block << s) < page_size) ++s;
+  return s;
+}
 
 // The page of block blk of sequence b, or -1.
 __device__ __forceinline__ int c4_page(const C4Table& t, int b, int blk) {
-  const int e = blk / t.blocks_per_page;
+  const int e = blk >> t.shift;
   if (e >= t.width) return -1;
   const int p = __ldg(t.pages + (size_t)b * t.width + e);
   return p >= 0 && p < t.num_pages ? p : -1;

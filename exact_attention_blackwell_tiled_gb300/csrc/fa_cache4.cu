@@ -127,14 +127,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
       if (b >= 0) {
         const long long s = (long long)a.lens[b] + (a.cu ? tok - a.cu[b] : 0);
         int page = -1;
-        if (s >= 0 && s < (long long)a.table.width * a.table.blocks_per_page * kC4Block)
+        if (s >= 0 && s < (long long)a.table.width * a.table.blocks_per_page() * kC4Block)
           page = c4_page(a.table, b, (int)(s / kC4Block));
         if (page < 0) {
           c4_flag(a.table);
         } else {
           slot_n = (int)(s % kC4Block);
-          const int blk = (int)(s / kC4Block) & (a.table.blocks_per_page - 1);
-          off_n = (((long long)page * a.Hkv + h) * a.table.blocks_per_page + blk) * L::kBytes;
+          const int blk = a.table.in_page((int)(s / kC4Block));
+          off_n = (((long long)page * a.Hkv + h) * a.table.blocks_per_page() + blk) * L::kBytes;
         }
       }
     }
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(128) read_kernel(const ReadArgs a) {
     page = from >= 0 ? c4_page(a.table, b, blk) : -1;
     if (page < 0 && lane == 0) c4_flag(a.table);
   }
-  const uint8_t* src = a.cache + (((long long)page * a.Hkv + h) * a.table.blocks_per_page +
-                                  (blk & (a.table.blocks_per_page - 1))) * L::kBytes;
+  const uint8_t* src = a.cache + (((long long)page * a.Hkv + h) * a.table.blocks_per_page() +
+                                  a.table.in_page(blk)) * L::kBytes;
   const int t = lane & 3;
   uint32_t w[4][kG], par[4][kG];  // K of slots lane / 4 and + 8, V of the same
 #pragma unroll
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int bh = blockIdx.x, b = bh / a.Hkv;
-  const int cap = min(a.cap, (int)min((long long)a.in.width * a.in.blocks_per_page * kC4Block,
+  const int cap = min(a.cap, (int)min((long long)a.in.width * a.in.blocks_per_page() * kC4Block,
                                       (long long)0x7fffffff));
   int n = a.lens[b];
   if (n < 0 || n > cap) {
@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
     const int i = a.src[(size_t)bh * a.budget + blk * kC4Block + lane];
     const int page = i >= 0 ? c4_page(a.in, b, i / kC4Block) : -1;
     if (page >= 0) {
-      from = (((long long)page * a.Hkv + h) * a.in.blocks_per_page +
-              (i / kC4Block) % a.in.blocks_per_page) * L::kBytes;
+      from = (((long long)page * a.Hkv + h) * a.in.blocks_per_page() +
+              a.in.in_page(i / kC4Block)) * L::kBytes;
       from_slot = i % kC4Block;
     } else {
       c4_flag(a.in);
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
     if (lane == 0) c4_flag(a.out);
     return;
   }
-  uint8_t* dst = a.cache + (((long long)page * a.Hkv + h) * a.out.blocks_per_page +
-                            blk % a.out.blocks_per_page) * L::kBytes;
+  uint8_t* dst = a.cache + (((long long)page * a.Hkv + h) * a.out.blocks_per_page() +
+                            a.out.in_page(blk)) * L::kBytes;
   // piece p of slot s: 0..3 K codes, 4 K parameters, 5..8 V codes, 9 V parameters
   auto offset = [](int s, int p) {
     if (p < 4) return s * L::kRow + p * kPiece;
@@ -536,7 +536,7 @@ using namespace fa;
 namespace {
 
 C4Table make_table(const int* pages, int width, int num_pages, int page_size, int* status) {
-  return C4Table{pages, width, num_pages, page_size / kC4Block, status};
+  return C4Table{pages, width, num_pages, c4_shift(page_size), status};
 }
 
 }  // namespace

@@ -45,7 +45,6 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;      // per block; they share nothing but the launch
-constexpr int kJoinThreads = 256;
 constexpr int kWeightKeys = 1024;  // keys of a (sequence, kv head) per step of the weight pass
 
 struct AttendArgs {
@@ -74,14 +73,13 @@ struct AttendArgs {
 // cost more than the work split off.
 constexpr int kMinBlocks = 4;
 
-// A warp's ring of blocks in shared memory, filled kFill at a time: 10 KB, so that
-// 16 warps keep up to 160 KB on their way to an SM (the bytes that cover the
-// memory's latency at its full rate are about 45 KB).
+// A warp's ring in shared memory: two stages of blocks, 10 KB, so that 16 warps
+// keep up to 160 KB on their way to an SM (the bytes that cover the memory's
+// latency at its full rate are about 45 KB).
 template <int D>
 struct Ring {
-  static constexpr int kCount = D == 128 ? 4 : 8;
-  static constexpr int kFill = kCount / 2;
-  static constexpr int kBytes = kCount * C4<D>::kBytes;
+  static constexpr int kBlocks = D == 128 ? 2 : 4;  // of a stage
+  static constexpr int kBytes = kBlocks * C4<D>::kBytes;
 };
 
 __device__ __forceinline__ int seq_len(const AttendArgs& a, int b) {
@@ -93,40 +91,56 @@ __device__ __forceinline__ int seq_blocks(const AttendArgs& a, int b) {
   return (seq_len(a, b) + kC4Block - 1) / kC4Block;
 }
 
-// Blocks of the whole list, by a whole warp: rows (b, kv head, tile) in order,
-// row by row.
-__device__ long long list_blocks(const AttendArgs& a) {
-  long long n = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) n += seq_blocks(a, b);
+// Prefix sums of the sequences' blocks by a whole warp: lane l holds sequences
+// l * per .. and the blocks before them, so that one round of loads serves both
+// the total and the search for a position.
+struct List {
+  int per;           // sequences per lane
+  long long before;  // blocks of the sequences of lower lanes
+  long long own;     // blocks of this lane's
+  long long total;
+};
+
+__device__ __forceinline__ List read_list(const AttendArgs& a) {
+  const int lane = threadIdx.x & 31;
+  List s;
+  s.per = (a.B + 31) >> 5;
+  s.own = 0;
+  const int b0 = lane * s.per, b1 = min(a.B, b0 + s.per);
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) s.own += seq_blocks(a, b);
+  long long inc = s.own;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n * a.Hkv * a.tiles;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  s.before = inc - s.own;
+  s.total = __shfl_sync(0xffffffffu, inc, 31);
+  return s;
 }
 
-// The sequence whose entries hold position x, and its first position; a sequence
-// has `unit(b)` x mult entries.  By a whole warp; x lies inside the list.
-template <typename Unit>
-__device__ int locate(const AttendArgs& a, long long x, int mult, Unit unit, long long* base) {
+// The sequence that holds block x of the list (x < total), and its first block.
+__device__ __forceinline__ int locate(const AttendArgs& a, const List& s, long long x,
+                                      long long* base) {
   const int lane = threadIdx.x & 31;
-  long long before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long n = b0 + lane < a.B ? (long long)unit(b0 + lane) * mult : 0;
-    long long inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, x < before + inc);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      *base = before + __shfl_sync(0xffffffffu, inc - n, l);
-      return b0 + l;
-    }
-    before += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  *base = before;
-  return a.B;
+  const unsigned hit = __ballot_sync(0xffffffffu, x >= s.before && x < s.before + s.own);
+  const int l = __ffs(hit) - 1;
+  long long at = s.before;
+  int b = lane * s.per;
+  if (lane == l)
+    for (int n; x >= at + (n = seq_blocks(a, b)); ++b) at += n;
+  *base = __shfl_sync(0xffffffffu, at, l);
+  return __shfl_sync(0xffffffffu, b, l);
+}
+
+// Blocks before sequence b.
+__device__ __forceinline__ long long list_before(const AttendArgs& a, const List& s, int b) {
+  const int l = b / s.per;
+  long long at = s.before;
+  if ((threadIdx.x & 31) == l)
+    for (int x = l * s.per; x < b; ++x) at += seq_blocks(a, x);
+  return __shfl_sync(0xffffffffu, at, l);
 }
 
 // Shares: warp w of W takes list positions w N / W .. (w + 1) N / W - 1.
@@ -137,37 +151,6 @@ __device__ __forceinline__ int share_count(const AttendArgs& a, long long N) {
 __device__ __forceinline__ long long share_begin(long long N, int W, int w) { return w * N / W; }
 __device__ __forceinline__ int share_of(long long N, int W, long long x) {
   return (int)(((x + 1) * W - 1) / N);
-}
-
-// A place in the warp's share: row (b, hk, tile) = (b, row / tiles, row % tiles),
-// next block blk of it, and where the share or the row ends.
-struct Cursor {
-  int b, row, blk, end, nb;
-  long long left;  // blocks of the share from blk on
-};
-
-__device__ __forceinline__ void cursor_row(Cursor& c) {
-  const long long e = c.blk + c.left;
-  c.end = (int)(e < c.nb ? e : c.nb);
-}
-
-// Past n blocks; at a row's end on to the next row that has blocks.
-__device__ __forceinline__ void cursor_advance(const AttendArgs& a, Cursor& c, int n) {
-  c.blk += n;
-  c.left -= n;
-  if (c.left <= 0 || c.blk < c.end) return;
-  c.blk = 0;
-  if (++c.row == a.Hkv * a.tiles) {
-    c.row = 0;
-    do {
-      ++c.b;
-    } while (c.b < a.B && (c.nb = seq_blocks(a, c.b)) == 0);
-    if (c.b >= a.B) {  // not reached: the share ends inside the list
-      c.left = 0;
-      return;
-    }
-  }
-  cursor_row(c);
 }
 
 // ------------------------------------------------------------------ fragments
@@ -277,85 +260,73 @@ __device__ __forceinline__ void write_lse(const AttendArgs& a, size_t row, float
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(const AttendArgs a) {
   using L = C4<D>;
   using R = Ring<D>;
   constexpr int kG = L::kGroups;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ alignas(8) uint64_t s_bar[kWarps][R::kCount];
+  __shared__ alignas(8) uint64_t s_bar[kWarps][2];
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, t = lane & 3;
-  const uint8_t* ring = smem + warp * R::kBytes;
+  const uint8_t* ring = smem + warp * 2 * R::kBytes;
   const uint32_t bars = smem_u32(&s_bar[warp][0]);
   if (threadIdx.x == 0) s_abort = 0;
-  if (lane < R::kCount) mbar_init(bars + 8 * lane, 1);
+  if (lane < 2) mbar_init(bars + 8 * lane, 1);
   fence_mbarrier_init();
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
-  const long long N = list_blocks(a);
+  // rows (b, kv head, tile) in order: a sequence has rows_per rows of its blocks
+  const int rows_per = a.Hkv * a.tiles;
+  const List list = read_list(a);
+  const long long N = list.total * rows_per;
   if (N == 0) return;
   const int W = share_count(a, N);
   const int w = blockIdx.x + warp * gridDim.x;  // neighbouring shares on different SMs
   if (w >= W) return;
-  const long long begin = share_begin(N, W, w), end = share_begin(N, W, w + 1);
-
-  Cursor head;  // of the copies; the products follow behind it
-  {
-    long long base;
-    head.b = locate(a, begin, a.Hkv * a.tiles, [&](int b) { return seq_blocks(a, b); }, &base);
-    head.nb = seq_blocks(a, head.b);
-    const long long r = begin - base;
-    head.row = (int)(r / head.nb);
-    head.blk = (int)(r - (long long)head.row * head.nb);
-    head.left = end - begin;
-    cursor_row(head);
-  }
-  Cursor cur = head;
-  int win_b = -1, win = 0, win_page = -1;  // page of block win + lane of sequence win_b
-  uint32_t issued = 0, n = 0;              // blocks copied (or on their way) and consumed
-  uint32_t have_bits = 0;                  // bit (block number & 31): its page was in range
-  const int page_mask = a.table.blocks_per_page - 1;
-  // Copies the next blocks of the head's row, at most kFill: a lane each.
-  auto fill = [&]() {
-    if (head.left <= 0) return;
-    const int count = min(R::kFill, head.end - head.blk);
-    if (head.b != win_b || head.blk < win || head.blk + count > win + 32) {
-      win_b = head.b;
-      win = head.blk;
-      win_page = win + lane < head.nb ? c4_page(a.table, win_b, win + lane) : -1;
-    }
-    const int page = __shfl_sync(0xffffffffu, win_page, (head.blk + lane - win) & 31);
-    const uint32_t good = __ballot_sync(0xffffffffu, lane < count && page >= 0);
-    if (lane < count) {
-      const int s = (issued + lane) % R::kCount;
-      const uint32_t bar = bars + 8 * s;
-      mbar_arrive_expect_tx(bar, page >= 0 ? L::kBytes : 0);
-      if (page >= 0)
-        copy_block(smem_u32(ring) + s * L::kBytes,
-                   a.cache + (((long long)page * a.Hkv + head.row / a.tiles) *
-                                  a.table.blocks_per_page + ((head.blk + lane) & page_mask)) * L::kBytes,
-                   L::kBytes, bar);
-      else
-        c4_flag(a.table);
-    }
-    const uint32_t mask = (1u << count) - 1;
-    have_bits = (have_bits & ~__funnelshift_l(mask, mask, issued & 31)) |
-                __funnelshift_l(good, good, issued & 31);
-    issued += count;
-    cursor_advance(a, head, count);
-  };
-  for (int s = 0; s < R::kCount / R::kFill; ++s) fill();
+  const long long begin = share_begin(N, W, w);
+  int left = (int)(share_begin(N, W, w + 1) - begin);  // blocks of the share still to do
+  long long base;
+  int row_b = locate(a, list, begin / rows_per, &base);
+  int len = seq_len(a, row_b), nb = (len + kC4Block - 1) / kC4Block;
+  // where in the sequence's rows the share begins
+  int row = (int)((begin - base * rows_per) / nb);
+  int blk0 = (int)(begin - base * rows_per - (long long)row * nb);
 
   const int slot_i = i ^ ((i >> 1) & 1);  // slot of product row i; row i + 8 is slot_i + 8
   // this lane's value slots: product rows 2 t and 2 t + 1 (and those + 8)
   const int va = (2 * t) ^ (t & 1), vb = (2 * t + 1) ^ (t & 1);
-  while (cur.left > 0) {
+  uint32_t stages = 0;  // consumed so far
+  while (left > 0) {
+    const int blk1 = min(nb, blk0 + left);
+    const int hk = row / a.tiles, tile = row - hk * a.tiles;
+    // ---- copies: lane x takes block x of a stage; its page is looked up a stage ahead
+    const uint8_t* head_base = a.cache + (size_t)hk * a.table.blocks_per_page() * L::kBytes;
+    const size_t page_bytes = (size_t)a.Hkv * a.table.blocks_per_page() * L::kBytes;
+    int next = blk0 + lane;  // block of the lane's next copy
+    auto look_up = [&]() { return lane < R::kBlocks && next < blk1 ? c4_page(a.table, row_b, next) : 0; };
+    int page = look_up();
+    uint32_t bad = 0;  // bit kBlocks * stage + x: that block's page is out of range
+    auto fill = [&](int st, int first) {  // blocks first .. of the row into stage st
+      if (first >= blk1) return;
+      const bool mine = lane < R::kBlocks && next < blk1;
+      const uint32_t miss = __ballot_sync(0xffffffffu, mine && page < 0);
+      const int count = min(R::kBlocks, blk1 - first) - __popc(miss);
+      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * st, count * L::kBytes);
+      if (mine && page >= 0)
+        copy_block(smem_u32(ring) + st * R::kBytes + lane * L::kBytes,
+                   head_base + page * page_bytes +
+                       a.table.in_page(next) * L::kBytes,
+                   L::kBytes, bars + 8 * st);
+      bad = (bad & ~(((1u << R::kBlocks) - 1) << (st * R::kBlocks))) | (miss << (st * R::kBlocks));
+      if (miss && lane == 0) c4_flag(a.table);
+      next += R::kBlocks;
+      page = look_up();
+    };
+    fill(stages & 1, blk0);
+    fill((stages & 1) ^ 1, blk0 + R::kBlocks);
     // ---- a row: its queries
-    const int row_b = cur.b, hk = cur.row / a.tiles, tile = cur.row - hk * a.tiles;
-    const int blk0 = cur.blk, blk1 = cur.end, nb = cur.nb;
-    const int len = seq_len(a, row_b);
     const int heads = min(8 * NT, a.group - tile * 8 * NT);  // real query columns
     uint32_t qf[kG][NT][4];  // B fragments: steps 2 g (0, 1) and 2 g + 1 (2, 3)
     uint32_t qp[NT][3];      // B fragments of the parameter product
@@ -423,39 +394,46 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) attend_kernel(co
     if (a.scores)
       score = a.scores + (((size_t)row_b * a.Hkv + hk) * a.cap + blk0 * kC4Block + slot_i) * a.group +
               tile * 8 * NT + 2 * t;
-    // ---- its blocks
+    // ---- its blocks, two at a time: their chains of dependent steps interleave
 #pragma unroll 1
-    for (int at = blk0; at < blk1; ++at) {
-      const bool ok = mbar_wait(bars + 8 * (n % R::kCount), (n / R::kCount) & 1, &s_abort);
-      if (!__all_sync(0xffffffffu, ok)) {
-        // give up, once the copies under way have landed (or that wait runs out too)
-        if (lane == 0) {
-          atomicExch(a.table.status, (int)FA_ERR_TIMEOUT);
-          for (uint32_t f = n; f < issued; ++f) {
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(bars + 8 * (f % R::kCount), (f / R::kCount) & 1))
-              if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    for (int at = blk0; at < blk1; at += 2) {
+      const int x = (at - blk0) & (R::kBlocks - 1), st = stages & 1;
+      if (x == 0) {
+        const bool ok = mbar_wait(bars + 8 * st, (stages >> 1) & 1, &s_abort);
+        if (!__all_sync(0xffffffffu, ok)) {
+          // give up, once the copies under way have landed (or that wait runs out too)
+          if (lane == 0) {
+            atomicExch(a.table.status, (int)FA_ERR_TIMEOUT);
+            for (uint32_t f = stages; f < stages + (at + R::kBlocks < blk1 ? 2 : 1); ++f) {
+              const uint64_t t0 = global_timer_ns();
+              while (!mbar_try_wait(bars + 8 * (f & 1), (f >> 1) & 1))
+                if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+            }
           }
+          __syncwarp();
+          return;
         }
-        __syncwarp();
-        return;
       }
-      const uint8_t* blk = ring + (n % R::kCount) * L::kBytes;
-      // scores of 16 keys: [0, 1] row i, [2, 3] row i + 8
-      float sc[NT][4];
-      {
+      // the second block may lie behind the row's last: what its place in the ring
+      // holds then counts for nothing, like a slot behind the last key
+      const uint8_t* blk = ring + st * R::kBytes + x * L::kBytes;
+      // scores of 2 x 16 keys: [0, 1] row i, [2, 3] row i + 8
+      float sc[2][NT][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
         uint32_t k0[kG], k1[kG], p0[kG], p1[kG];
-        const uint8_t* par = blk + L::kOffKPar + slot_i * L::kPar;
-        lds(k0, blk + slot_i * L::kRow + t * 4 * kG);
-        lds(k1, blk + (slot_i + 8) * L::kRow + t * 4 * kG);
+        const uint8_t* kb = blk + y * L::kBytes;
+        const uint8_t* par = kb + L::kOffKPar + slot_i * L::kPar;
+        lds(k0, kb + slot_i * L::kRow + t * 4 * kG);
+        lds(k1, kb + (slot_i + 8) * L::kRow + t * 4 * kG);
         lds(p0, par);
         lds(p1, par + 8 * L::kPar);
         const uint32_t w0 = *reinterpret_cast<const uint32_t*>(par + (t & (kG - 1)) * 4);
         const uint32_t w1 = *reinterpret_cast<const uint32_t*>(par + 8 * L::kPar + (t & (kG - 1)) * 4);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma16816_first(sc[nt], w0, w1, w0, w1, qp[nt][0], qp[nt][1]);
-          if constexpr (D == 128) mma1688(sc[nt], w0, w1, qp[nt][2]);
+          mma16816_first(sc[y][nt], w0, w1, w0, w1, qp[nt][0], qp[nt][1]);
+          if constexpr (D == 128) mma1688(sc[y][nt], w0, w1, qp[nt][2]);
         }
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
@@ -469,62 +447,76 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) attend_kernel(co
             float d[4];
             mma16816_first(d, a00, a10, a01, a11, qf[g][nt][0], qf[g][nt][1]);
             mma16816(d, a02, a12, a03, a13, qf[g][nt][2], qf[g][nt][3]);
-            sc[nt][0] = fmaf(c0, d[0], sc[nt][0]);
-            sc[nt][1] = fmaf(c0, d[1], sc[nt][1]);
-            sc[nt][2] = fmaf(c1, d[2], sc[nt][2]);
-            sc[nt][3] = fmaf(c1, d[3], sc[nt][3]);
+            sc[y][nt][0] = fmaf(c0, d[0], sc[y][nt][0]);
+            sc[y][nt][1] = fmaf(c0, d[1], sc[y][nt][1]);
+            sc[y][nt][2] = fmaf(c1, d[2], sc[y][nt][2]);
+            sc[y][nt][3] = fmaf(c1, d[3], sc[y][nt][3]);
           }
         }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] *= a.scale_log2;
-      // a block with slots behind the last key, or whose page is out of range
-      const int left = len - at * kC4Block - slot_i;  // row i has a key iff left > 0
-      const bool have = (have_bits >> (n & 31)) & 1;
-      const bool full = have && (at + 1) * kC4Block <= len;
-      const bool live0 = have && left > 0, live1 = have && left > 8;
-      if (!full) {
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] = (e < 2 ? live0 : live1) ? sc[nt][e] : -INFINITY;
+          for (int e = 0; e < 4; ++e) sc[y][nt][e] *= a.scale_log2;
+      // slots behind the last key, and blocks whose page is out of range
+      const uint32_t miss = (bad >> (st * R::kBlocks + x)) & 3u;
+      const int ends = min(len, blk1 * kC4Block) - at * kC4Block;  // the share's keys from here on
+      const bool full = miss == 0 && ends >= 2 * kC4Block;
+      bool live[2][2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          live[y][z] = !((miss >> y) & 1) && y * kC4Block + slot_i + 8 * z < ends;
+      if (!full) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc[y][nt][e] = live[y][e >> 1] ? sc[y][nt][e] : -INFINITY;
       }
       bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         // a stale maximum stands until a score passes it by 8 (weights up to 2^8)
-        grow |= fmaxf(sc[nt][0], sc[nt][2]) > r.m[nt][0] + 8.f;
-        grow |= fmaxf(sc[nt][1], sc[nt][3]) > r.m[nt][1] + 8.f;
+        grow |= fmaxf(fmaxf(sc[0][nt][0], sc[0][nt][2]), fmaxf(sc[1][nt][0], sc[1][nt][2])) >
+                r.m[nt][0] + 8.f;
+        grow |= fmaxf(fmaxf(sc[0][nt][1], sc[0][nt][3]), fmaxf(sc[1][nt][1], sc[1][nt][3])) >
+                r.m[nt][1] + 8.f;
       }
       if (a.scores) {
-        float* next = score + 8 * a.group;
+        const int mine = ends - slot_i;  // keys of the share from row i on
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int col = nt * 8 + 2 * t;
-          if ((a.group & 1) == 0) {
-            if (col < heads) {
-              if (left > 0) *reinterpret_cast<float2*>(score + nt * 8) = make_float2(sc[nt][0], sc[nt][1]);
-              if (left > 8) *reinterpret_cast<float2*>(next + nt * 8) = make_float2(sc[nt][2], sc[nt][3]);
-            }
-          } else {
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if (col + c < heads) {
-                if (left > 0) score[nt * 8 + c] = sc[nt][c];
-                if (left > 8) next[nt * 8 + c] = sc[nt][2 + c];
+          for (int z = 0; z < 2; ++z) {
+            if (mine <= y * kC4Block + 8 * z) continue;
+            float* dst = score + (y * kC4Block + 8 * z) * a.group;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int col = nt * 8 + 2 * t;
+              if ((a.group & 1) == 0) {
+                if (col < heads)
+                  *reinterpret_cast<float2*>(dst + nt * 8) =
+                      make_float2(sc[y][nt][2 * z], sc[y][nt][2 * z + 1]);
+              } else {
+                if (col < heads) dst[nt * 8] = sc[y][nt][2 * z];
+                if (col + 1 < heads) dst[nt * 8 + 1] = sc[y][nt][2 * z + 1];
               }
+            }
           }
-        }
-        score += 16 * a.group;
+        score += 2 * kC4Block * a.group;
       }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(sc[nt][c], sc[nt][2 + c]);
+            float mx = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             if (mx > r.m[nt][c]) {
@@ -545,58 +537,65 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) attend_kernel(co
       for (int nt = 0; nt < NT; ++nt) {
         const float n0 = r.m[nt][0] == -INFINITY ? 0.f : r.m[nt][0];
         const float n1 = r.m[nt][1] == -INFINITY ? 0.f : r.m[nt][1];
-        sc[nt][0] = ex2_mufu(sc[nt][0] - n0);
-        sc[nt][1] = ex2_mufu(sc[nt][1] - n1);
-        sc[nt][2] = ex2_mufu(sc[nt][2] - n0);
-        sc[nt][3] = ex2_mufu(sc[nt][3] - n1);
-        r.l[nt][0] += sc[nt][0] + sc[nt][2];
-        r.l[nt][1] += sc[nt][1] + sc[nt][3];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          sc[y][nt][0] = ex2_mufu(sc[y][nt][0] - n0);
+          sc[y][nt][1] = ex2_mufu(sc[y][nt][1] - n1);
+          sc[y][nt][2] = ex2_mufu(sc[y][nt][2] - n0);
+          sc[y][nt][3] = ex2_mufu(sc[y][nt][3] - n1);
+          r.l[nt][0] += sc[y][nt][0] + sc[y][nt][2];
+          r.l[nt][1] += sc[y][nt][1] + sc[y][nt][3];
+        }
       }
-      uint32_t v[4][(kG + 1) / 2], p0[kG], p1[kG];
-      lds(v[0], blk + L::v_half(va, i, 0));
-      lds(v[1], blk + L::v_half(vb, i, 0));
-      lds(v[2], blk + L::v_half(va + 8, i, 0));
-      lds(v[3], blk + L::v_half(vb + 8, i, 0));
-      lds(p0, blk + L::kOffVPar + slot_i * L::kPar);
-      lds(p1, blk + L::kOffVPar + (slot_i + 8) * L::kPar);
-      if (!full) {
-        // a slot without a key holds anything: its parameters count as zero
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint8_t* vb_ = blk + y * L::kBytes;
+        uint32_t v[4][(kG + 1) / 2], p0[kG], p1[kG];
+        lds(v[0], vb_ + L::v_half(va, i, 0));
+        lds(v[1], vb_ + L::v_half(vb, i, 0));
+        lds(v[2], vb_ + L::v_half(va + 8, i, 0));
+        lds(v[3], vb_ + L::v_half(vb + 8, i, 0));
+        lds(p0, vb_ + L::kOffVPar + slot_i * L::kPar);
+        lds(p1, vb_ + L::kOffVPar + (slot_i + 8) * L::kPar);
+        if (!full) {
+          // a slot without a key holds anything: its parameters count as zero
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            p0[g] = live[y][0] ? p0[g] : 0u;
+            p1[g] = live[y][1] ? p1[g] : 0u;
+          }
+        }
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          p0[g] = live0 ? p0[g] : 0u;
-          p1[g] = live1 ? p1[g] : 0u;
+          const float c0 = c4_scale(p0[g]), m0 = fmaf(8.f, c0, c4_min(p0[g]));
+          const float c1 = c4_scale(p1[g]), m1 = fmaf(8.f, c1, c4_min(p1[g]));
+          uint32_t b0[NT], b1[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float(&p)[4] = sc[y][nt];
+            r.mid[g][nt][0] = fmaf(p[0], m0, fmaf(p[2], m1, r.mid[g][nt][0]));
+            r.mid[g][nt][1] = fmaf(p[1], m0, fmaf(p[3], m1, r.mid[g][nt][1]));
+            b0[nt] = transpose8x8(pack_bf16x2(p[0] * c0, p[1] * c0));
+            b1[nt] = transpose8x8(pack_bf16x2(p[2] * c1, p[3] * c1));
+          }
+          constexpr uint32_t kLow = 0x5410, kHigh = 0x7632;
+          const uint32_t y0 = __byte_perm(v[0][g / 2], v[1][g / 2], (g & 1) ? kHigh : kLow);
+          const uint32_t y1 = __byte_perm(v[2][g / 2], v[3][g / 2], (g & 1) ? kHigh : kLow);
+          const uint32_t e0 = minus8<0>(y0), e1 = minus8<1>(y0), e2 = minus8<2>(y0), e3 = minus8<3>(y0);
+          const uint32_t f0 = minus8<0>(y1), f1 = minus8<1>(y1), f2 = minus8<2>(y1), f3 = minus8<3>(y1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(r.acc[2 * g][nt], e0, e1, f0, f1, b0[nt], b1[nt]);
+            mma16816(r.acc[2 * g + 1][nt], e2, e3, f2, f3, b0[nt], b1[nt]);
+          }
         }
       }
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        const float c0 = c4_scale(p0[g]), m0 = fmaf(8.f, c0, c4_min(p0[g]));
-        const float c1 = c4_scale(p1[g]), m1 = fmaf(8.f, c1, c4_min(p1[g]));
-        uint32_t b0[NT], b1[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          r.mid[g][nt][0] = fmaf(sc[nt][0], m0, fmaf(sc[nt][2], m1, r.mid[g][nt][0]));
-          r.mid[g][nt][1] = fmaf(sc[nt][1], m0, fmaf(sc[nt][3], m1, r.mid[g][nt][1]));
-          b0[nt] = transpose8x8(pack_bf16x2(sc[nt][0] * c0, sc[nt][1] * c0));
-          b1[nt] = transpose8x8(pack_bf16x2(sc[nt][2] * c1, sc[nt][3] * c1));
-        }
-        constexpr uint32_t kLow = 0x5410, kHigh = 0x7632;
-        const uint32_t y0 = __byte_perm(v[0][g / 2], v[1][g / 2], (g & 1) ? kHigh : kLow);
-        const uint32_t y1 = __byte_perm(v[2][g / 2], v[3][g / 2], (g & 1) ? kHigh : kLow);
-        const uint32_t e0 = minus8<0>(y0), e1 = minus8<1>(y0), e2 = minus8<2>(y0), e3 = minus8<3>(y0);
-        const uint32_t f0 = minus8<0>(y1), f1 = minus8<1>(y1), f2 = minus8<2>(y1), f3 = minus8<3>(y1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(r.acc[2 * g][nt], e0, e1, f0, f1, b0[nt], b1[nt]);
-          mma16816(r.acc[2 * g + 1][nt], e2, e3, f2, f3, b0[nt], b1[nt]);
-        }
-      }
-      ++n;
-      if (issued - n <= R::kCount - R::kFill) {
-        __syncwarp();  // every lane has read the blocks whose places are filled again
-        fill();
+      if (x == R::kBlocks - 2 || at + 2 >= blk1) {
+        __syncwarp();  // every lane has read the stage that is filled again
+        fill(st, at + 2 + R::kBlocks);
+        ++stages;
       }
     }
-    cursor_advance(a, cur, blk1 - blk0);
     // ---- the row's result, or this share's part of it
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -642,6 +641,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) attend_kernel(co
             a.part_ml[part + col] = make_float2(m, l);
         }
       }
+    // ---- on to the next row of the share
+    left -= blk1 - blk0;
+    blk0 = 0;
+    if (left > 0 && ++row == rows_per) {
+      row = 0;
+      do {
+        len = seq_len(a, ++row_b);  // the share ends inside the list
+      } while (len == 0);
+      nb = (len + kC4Block - 1) / kC4Block;
+    }
   }
 }
 
@@ -653,14 +662,13 @@ struct RowSpan {
   int nb;
 };
 
-__device__ RowSpan row_span(const AttendArgs& a, long long N, int b, int row) {
+__device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int b, int row) {
+  const List list = read_list(a);
   RowSpan s{0, 0, seq_blocks(a, b)};
+  const long long before = list_before(a, list, b);
   if (s.nb == 0) return s;
-  long long before = 0;
-  for (int x = threadIdx.x & 31; x < b; x += 32) before += seq_blocks(a, x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const long long first = before * a.Hkv * a.tiles + (long long)row * s.nb;
+  const int rows_per = a.Hkv * a.tiles;
+  const long long N = list.total * rows_per, first = before * rows_per + (long long)row * s.nb;
   const int W = share_count(a, N);
   s.w0 = share_of(N, W, first);
   s.w1 = share_of(N, W, first + s.nb - 1);
@@ -696,24 +704,25 @@ __device__ float2 join_ml(const AttendArgs& a, const RowSpan& s, int col) {
 }
 
 // One block per (sequence, query head) whose row was cut by shares, or is empty.
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs a) {
-  constexpr int kV = D / 32, kW = kJoinThreads / 32;
+// kW warps: two where there are rows enough to fill the GPU (64 sequences of 32 heads:
+// one wave of blocks), eight where few rows were cut into many parts.
+template <int D, int NT, int kW>
+__global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
+  constexpr int kV = D / 32;
   __shared__ float s_o[kW][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The lengths were complete before the attention kernel let this one start, so
   // they are read, and the row's parts found, while it still runs.
-  const long long N = list_blocks(a);
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
   const int hk = hq / a.group, in_group = hq - hk * a.group;
   const int tile = in_group / (8 * NT), col = in_group - tile * 8 * NT;
-  const RowSpan s = row_span(a, N, b, hk * a.tiles + tile);
+  const RowSpan s = row_span(a, b, hk * a.tiles + tile);
   grid_dep_wait();
   grid_dep_launch();
   if (hq == 0 && threadIdx.x == 0 && a.lens[b] != seq_len(a, b)) c4_flag(a.table);
   __nv_bfloat16* o = a.o + (size_t)blockIdx.x * D;
   if (s.nb == 0) {  // an empty sequence
-    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(o)[threadIdx.x] = 0u;
+    for (int x = threadIdx.x; x < D / 2; x += kW * 32) reinterpret_cast<uint32_t*>(o)[x] = 0u;
     if (threadIdx.x == 0) write_lse(a, blockIdx.x, 0.f, 0.f);
     return;
   }
@@ -722,7 +731,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs a) 
   float acc[kV];
 #pragma unroll
   for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int w = s.w0 + warp; w <= s.w1; w += kW) {
     const size_t p = part_index<NT>(s, w, col);
     const float2 x = a.part_ml[p];
@@ -742,7 +751,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs a) 
 #pragma unroll
   for (int e = 0; e < kV; ++e) s_o[warp][lane * kV + e] = acc[e];
   __syncthreads();
-  if (threadIdx.x < D / 2) {
+  if (threadIdx.x < D / 2) {  // at most 64 threads
     const float inv = ml.y > 0.f ? 1.0f / ml.y : 0.f;
     float x0 = 0.f, x1 = 0.f;
 #pragma unroll
@@ -808,7 +817,7 @@ int tile_count(int group, int* nt) {
 }
 
 // Shares: every warp that is resident at once.
-int share_limit(int sms, int nt) { return sms * (nt == 1 ? 4 : 2) * kWarps; }
+int share_limit(int sms, int nt) { return sms * (nt == 1 ? 3 : 2) * kWarps; }
 
 struct AttendLayout {
   size_t off_ml, off_lse2, off_scores, total;
@@ -828,7 +837,7 @@ AttendLayout attend_layout(int B, int Hq, int Hkv, int D, int cap, int sms) {
 
 template <int D, int NT>
 int launch_attend(const AttendArgs& a, cudaStream_t stream) {
-  constexpr int kSmem = kWarps * Ring<D>::kBytes;
+  constexpr int kSmem = kWarps * 2 * Ring<D>::kBytes;
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
@@ -844,8 +853,9 @@ int launch_attend(const AttendArgs& a, cudaStream_t stream) {
                  a) != cudaSuccess)
     return FA_ERR_CUDA;
   record_timing(true, stream);
-  if (launch_pdl(join_kernel<D, NT>, dim3(a.B * a.Hq), dim3(kJoinThreads), 0, stream, a) !=
-      cudaSuccess)
+  const int rows = a.B * a.Hq;
+  const auto join = rows >= 1024 ? join_kernel<D, NT, 2> : join_kernel<D, NT, 8>;
+  if (launch_pdl(join, dim3(rows), dim3(rows >= 1024 ? 64 : 256), 0, stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
   int launches = 2;
   if (a.scores) {
@@ -916,7 +926,7 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   a.lens = cache_lens;
-  a.table = C4Table{page_table, table_width, num_pages, page_size / kC4Block, status};
+  a.table = C4Table{page_table, table_width, num_pages, c4_shift(page_size), status};
   a.B = B;
   a.Hq = Hq;
   a.Hkv = Hkv;
