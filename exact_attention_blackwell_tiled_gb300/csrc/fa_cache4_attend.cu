@@ -4,17 +4,20 @@
 //   s_j = scale q . k_j,  k_j = m_j + c_j z_j  per group of 32 elements (minimum m,
 //   scale c, codes z), so  q . k_j = sum_g c_jg (q_g . z_jg) + m_jg sum(q_g):
 // the codes, small integers, go to the matrix instruction exactly, as does the
-// bf16 query, and the scales are applied to its fp32 result.  Codes become bf16
-// numbers by placing their bits in the mantissa of 16.0 or 128.0 (one and-or,
-// and a shift for three of four); with z' = z + off the score is
-//   sum_g c_jg (q_g . z'_jg) + sum_g [c_jg, m_jg] . [-sum(off q_g), sum(q_g)]
-// whose second part is one more small product: a lane's stored parameter word is
-// its A fragment as it stands, and the sums, split into three bf16 parts each (24
-// bits), are the B fragments, made once per row.  For the values
+// bf16 query, and the scales are applied to its fp32 result.  A 4-bit code masked
+// out of its word in place is already a bf16 number: z in bits 0..3 of a half is
+// z 2^-133 and in bits 4..7 16 z 2^-133 (subnormal, or of the smallest exponent,
+// where bf16 is linear), which the matrix unit multiplies exactly.  So two codes
+// cost one mask, and every other pair a shift; 2^64 times the query (2^60 where
+// the code has the factor 16), and exponentials 2^64 times too large, bring the
+// products back into fp32's normal range.  The second sum, over the minima, is one
+// more small product: a lane's stored parameter word is its A fragment as it
+// stands, and sum(q_g), split into three bf16 parts (24 bits), the B fragment, made
+// once per row.  For the values
 //   O = sum_j p_j (m_j + 8 c_j) + sum_j (p_j c_j) (z_j - 8)
 // the first sum stays in fp32 and p_j c_j is rounded to bf16 for the second, the
-// only rounding before O's own.  (z - 8, not z' with a correction at the end:
-// over a long cache the offset's accumulation error would outgrow O.)
+// only rounding before O's own.  (z - 8, not z: the rounding then counts for the
+// value's distance from the middle of its group only.)
 //
 // Bound by memory: a key and its value are 5/2 D bytes of codes and parameters,
 // read once for all query heads of the kv head (up to 8 NT of them, the columns of
@@ -28,9 +31,8 @@
 // registers.  So sequences of any lengths load the SMs evenly with no barrier
 // between warps.  A row that lies inside one share is finished there; a row cut
 // by shares leaves parts (fp32 O, maximum, sum), at most two per warp, which a
-// second kernel joins; it also writes the rows of empty sequences.  A third, when
-// weights are asked for, turns the stored scores into them, now that the sums are
-// known.
+// second kernel joins; it also writes the rows of empty sequences and, when weights
+// are asked for, turns the stored scores into them, now that the sums are known.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -63,7 +65,7 @@ struct AttendArgs {
   float* part_o;    // [n_warps, 2, 8 NT, D]
   float2* part_ml;  // [n_warps, 2, 8 NT]: maximum (log2 units) and sum
   float* scores;    // [B, Hkv, cap, group] in log2 units, or null
-  float* lse2;      // [B, Hq] log2 of the sums, for the weights
+  float* lse2;      // [B, Hq] log2 of the sums of the rows that no share cut, or unused
   const float* w_in;
   float* w_out;  // [B, Hkv, w_stride]
   int w_stride;
@@ -73,11 +75,13 @@ struct AttendArgs {
 // cost more than the work split off.
 constexpr int kMinBlocks = 4;
 
-// A warp's ring in shared memory: two stages of blocks, 10 KB, so that 16 warps
-// keep up to 160 KB on their way to an SM (the bytes that cover the memory's
-// latency at its full rate are about 45 KB).
+// A warp's ring in shared memory: two stages of 5 KB, so that an SM's 12 warps have
+// 60 to 120 KB on their way (the bytes that cover the memory's latency at its full
+// rate are about 45 KB); a third stage measured the same or 3% slower, four blocks of
+// 4 warps per SM (128 registers a thread) 6% slower.
 template <int D>
 struct Ring {
+  static constexpr int kStages = 2;
   static constexpr int kBlocks = D == 128 ? 2 : 4;  // of a stage
   static constexpr int kBytes = kBlocks * C4<D>::kBytes;
 };
@@ -187,23 +191,30 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// 4-bit field R of the low and of the high half of w as bf16 numbers field + kOff<R>.
+// 4-bit field R (0..3) of the low and of the high half of w as bf16 numbers: times
+// 2^-133 for the even fields, 16 * 2^-133 for the odd ones.
 template <int R>
-constexpr float kOff = R == 0 ? 128.f : 16.f;
-template <int R>
-__device__ __forceinline__ uint32_t offset_code(uint32_t w) {
-  if constexpr (R == 0) return (w & 0x000f000fu) | 0x43004300u;
-  else return ((w >> (4 * R - 3)) & 0x00780078u) | 0x41804180u;
+__device__ __forceinline__ uint32_t code(uint32_t w) {
+  return (R < 2 ? w : w >> 8) & ((R & 1) ? 0x00f000f0u : 0x000f000fu);
 }
 
-// ... as field - 8 (exact).
+// ... the field minus 8 (exact).
 template <int R>
 __device__ __forceinline__ uint32_t minus8(uint32_t w) {
-  const uint32_t x = offset_code<R>(w);
-  const __nv_bfloat16 k = __ushort_as_bfloat16(R == 0 ? 0x4308 : 0x41C0);  // 136, 24
-  const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __nv_bfloat162(k, k));
+  const uint32_t x = code<R>(w), k = (R & 1) ? 0x00800080u : 0x00080008u;
+  const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&k));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
+
+// Two bf16 numbers times a power of two.
+__device__ __forceinline__ uint32_t times(uint32_t w, float f) {
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(f));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+constexpr float kTop = 64.f;         // exponentials are 2^(s - m + kTop)
+constexpr float kScoreUp = 0x1p69f;  // products of queries and codes carry 2^(64 - 133)
 
 // x as three bf16 parts (their sum is x to 24 bits).
 __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&p)[3]) {
@@ -248,8 +259,10 @@ template <int D, int NT>
 struct RowState {
   static constexpr int kG = D / 32;
   float acc[2 * kG][NT][4];  // O^T: tile 2 g + x, rows i and i + 8 are elements 32 g + 4 i + 2 x, + 1
-  float mid[kG][NT][2];      // this lane's sum of p (m + 8 c)
+  // (times 2^-69, 2^-65 for the odd elements)
+  float mid[kG][NT][2];      // this lane's sum of p (m + 8 c), times 2^64
   float m[NT][2], l[NT][2];  // maximum (log2 units; the same in the lanes of one t), lane's sum
+                             // times 2^64
 };
 
 // A row's log-sum-exp from its maximum and sum.
@@ -265,14 +278,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
   using R = Ring<D>;
   constexpr int kG = L::kGroups;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ alignas(8) uint64_t s_bar[kWarps][2];
+  __shared__ alignas(8) uint64_t s_bar[kWarps][R::kStages];
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, t = lane & 3;
-  const uint8_t* ring = smem + warp * 2 * R::kBytes;
+  const uint8_t* ring = smem + warp * R::kStages * R::kBytes;
   const uint32_t bars = smem_u32(&s_bar[warp][0]);
   if (threadIdx.x == 0) s_abort = 0;
-  if (lane < 2) mbar_init(bars + 8 * lane, 1);
+  if (lane < R::kStages) mbar_init(bars + 8 * lane, 1);
   fence_mbarrier_init();
   __syncthreads();
   grid_dep_wait();
@@ -294,10 +307,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
   int row = (int)((begin - base * rows_per) / nb);
   int blk0 = (int)(begin - base * rows_per - (long long)row * nb);
 
+  const float score_up = a.scale_log2 * kScoreUp;
   const int slot_i = i ^ ((i >> 1) & 1);  // slot of product row i; row i + 8 is slot_i + 8
   // this lane's value slots: product rows 2 t and 2 t + 1 (and those + 8)
   const int va = (2 * t) ^ (t & 1), vb = (2 * t + 1) ^ (t & 1);
-  uint32_t stages = 0;  // consumed so far
+  int st = 0;          // the stage consumed next, and its barrier's phase
+  uint32_t phase = 0;
   while (left > 0) {
     const int blk1 = min(nb, blk0 + left);
     const int hk = row / a.tiles, tile = row - hk * a.tiles;
@@ -324,8 +339,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
       next += R::kBlocks;
       page = look_up();
     };
-    fill(stages & 1, blk0);
-    fill((stages & 1) ^ 1, blk0 + R::kBlocks);
+#pragma unroll
+    for (int f = 0; f < R::kStages; ++f)
+      fill(st + f < R::kStages ? st + f : st + f - R::kStages, blk0 + f * R::kBlocks);
     // ---- a row: its queries
     const int heads = min(8 * NT, a.group - tile * 8 * NT);  // real query columns
     uint32_t qf[kG][NT][4];  // B fragments: steps 2 g (0, 1) and 2 g + 1 (2, 3)
@@ -335,48 +351,34 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
       const int col = nt * 8 + i;
       const __nv_bfloat16* src =
           a.q + row_b * a.q_batch + (long long)(hk * a.group + tile * 8 * NT + col) * a.q_head + 8 * t;
-      float sum_t = 0.f, off_t = 0.f;  // of this lane's group in the parameter product
+      float sum_t = 0.f;  // of this lane's group in the parameter product
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (col < heads) x = *reinterpret_cast<const uint4*>(src + 32 * g);
         // elements 0..7 in pairs x.x = (0,1) .. x.w = (6,7)
-        qf[g][nt][0] = __byte_perm(x.x, x.z, 0x5410);  // (0, 4): fields 0
-        qf[g][nt][1] = __byte_perm(x.x, x.z, 0x7632);  // (1, 5): fields 1
-        qf[g][nt][2] = __byte_perm(x.y, x.w, 0x5410);  // (2, 6): fields 2
-        qf[g][nt][3] = __byte_perm(x.y, x.w, 0x7632);  // (3, 7): fields 3
-        float sum = 0.f, first = 0.f;
+        qf[g][nt][0] = times(__byte_perm(x.x, x.z, 0x5410), 0x1p64f);  // (0, 4): fields 0
+        qf[g][nt][1] = times(__byte_perm(x.x, x.z, 0x7632), 0x1p60f);  // (1, 5): fields 1
+        qf[g][nt][2] = times(__byte_perm(x.y, x.w, 0x5410), 0x1p64f);  // (2, 6): fields 2
+        qf[g][nt][3] = times(__byte_perm(x.y, x.w, 0x7632), 0x1p60f);  // (3, 7): fields 3
+        float sum = 0.f;
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float lo = __uint_as_float(xs[e] << 16), hi = __uint_as_float(xs[e] & 0xffff0000u);
-          if ((e & 1) == 0) first += lo;  // elements 0 and 4
-          sum += lo + hi;
-        }
+        for (int e = 0; e < 4; ++e)
+          sum += __uint_as_float(xs[e] << 16) + __uint_as_float(xs[e] & 0xffff0000u);
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          first += __shfl_xor_sync(0xffffffffu, first, o);
-        }
-        if (g == (t & (kG - 1))) {
-          sum_t = sum;
-          off_t = kOff<1> * sum + (kOff<0> - kOff<1>) * first;
-        }
+        for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (g == (t & (kG - 1))) sum_t = sum;
       }
-      __nv_bfloat16 sp[3], op[3];
-      split3(sum_t, sp);
-      split3(-off_t, op);
-      // k index 2 t is the scale, 2 t + 1 the minimum, of group t (D = 128), with
-      // parts 0 and 1, then 2; at D = 64 lanes t >= 2 take part 2 of group t - 2
-      if constexpr (D == 128) {
-        qp[nt][0] = pair16(op[0], sp[0]);
-        qp[nt][1] = pair16(op[1], sp[1]);
-        qp[nt][2] = pair16(op[2], sp[2]);
-      } else {
-        qp[nt][0] = t < 2 ? pair16(op[0], sp[0]) : pair16(op[2], sp[2]);
-        qp[nt][1] = t < 2 ? pair16(op[1], sp[1]) : 0u;
-        qp[nt][2] = 0u;
-      }
+      __nv_bfloat16 part[3];
+      split3(sum_t * (1.f / kScoreUp), part);
+      // k index 2 t is the scale (times zero), 2 t + 1 the minimum, of group t
+      // (D = 128), with parts 0 and 1, then 2; at D = 64 lanes t >= 2 take part 2 of
+      // group t - 2
+      const __nv_bfloat16 zero = __ushort_as_bfloat16(0);
+      qp[nt][0] = pair16(zero, D == 128 || t < 2 ? part[0] : part[2]);
+      qp[nt][1] = pair16(zero, D == 128 || t < 2 ? part[1] : zero);
+      qp[nt][2] = pair16(zero, part[2]);
     }
     RowState<D, NT> r;
 #pragma unroll
@@ -397,16 +399,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
     // ---- its blocks, two at a time: their chains of dependent steps interleave
 #pragma unroll 1
     for (int at = blk0; at < blk1; at += 2) {
-      const int x = (at - blk0) & (R::kBlocks - 1), st = stages & 1;
+      const int x = (at - blk0) & (R::kBlocks - 1);
       if (x == 0) {
-        const bool ok = mbar_wait(bars + 8 * st, (stages >> 1) & 1, &s_abort);
+        const bool ok = mbar_wait(bars + 8 * st, phase, &s_abort);
         if (!__all_sync(0xffffffffu, ok)) {
           // give up, once the copies under way have landed (or that wait runs out too)
           if (lane == 0) {
             atomicExch(a.table.status, (int)FA_ERR_TIMEOUT);
-            for (uint32_t f = stages; f < stages + (at + R::kBlocks < blk1 ? 2 : 1); ++f) {
+            for (int f = 0; f < R::kStages && at + f * R::kBlocks < blk1; ++f) {
+              const int y = st + f < R::kStages ? st + f : st + f - R::kStages;
               const uint64_t t0 = global_timer_ns();
-              while (!mbar_try_wait(bars + 8 * (f & 1), (f >> 1) & 1))
+              while (!mbar_try_wait(bars + 8 * y, phase ^ (y < st ? 1u : 0u)))
                 if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
             }
           }
@@ -437,10 +440,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
         }
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          const uint32_t a00 = offset_code<0>(k0[g]), a01 = offset_code<1>(k0[g]),
-                         a02 = offset_code<2>(k0[g]), a03 = offset_code<3>(k0[g]);
-          const uint32_t a10 = offset_code<0>(k1[g]), a11 = offset_code<1>(k1[g]),
-                         a12 = offset_code<2>(k1[g]), a13 = offset_code<3>(k1[g]);
+          const uint32_t a00 = code<0>(k0[g]), a01 = code<1>(k0[g]),
+                         a02 = code<2>(k0[g]), a03 = code<3>(k0[g]);
+          const uint32_t a10 = code<0>(k1[g]), a11 = code<1>(k1[g]),
+                         a12 = code<2>(k1[g]), a13 = code<3>(k1[g]);
           const float c0 = c4_scale(p0[g]), c1 = c4_scale(p1[g]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[y][nt][e] *= a.scale_log2;
+          for (int e = 0; e < 4; ++e) sc[y][nt][e] *= score_up;
       // slots behind the last key, and blocks whose page is out of range
       const uint32_t miss = (bad >> (st * R::kBlocks + x)) & 3u;
       const int ends = min(len, blk1 * kC4Block) - at * kC4Block;  // the share's keys from here on
@@ -471,6 +474,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
         for (int z = 0; z < 2; ++z)
           live[y][z] = !((miss >> y) & 1) && y * kC4Block + slot_i + 8 * z < ends;
       if (!full) {
+        asm volatile("" ::: "memory");  // a branch, not selects in every iteration
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -535,8 +539,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float n0 = r.m[nt][0] == -INFINITY ? 0.f : r.m[nt][0];
-        const float n1 = r.m[nt][1] == -INFINITY ? 0.f : r.m[nt][1];
+        const float n0 = r.m[nt][0] == -INFINITY ? 0.f : r.m[nt][0] - kTop;
+        const float n1 = r.m[nt][1] == -INFINITY ? 0.f : r.m[nt][1] - kTop;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           sc[y][nt][0] = ex2_mufu(sc[y][nt][0] - n0);
@@ -559,6 +563,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
         lds(p1, vb_ + L::kOffVPar + (slot_i + 8) * L::kPar);
         if (!full) {
           // a slot without a key holds anything: its parameters count as zero
+          asm volatile("" ::: "memory");
 #pragma unroll
           for (int g = 0; g < kG; ++g) {
             p0[g] = live[y][0] ? p0[g] : 0u;
@@ -592,8 +597,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
       }
       if (x == R::kBlocks - 2 || at + 2 >= blk1) {
         __syncwarp();  // every lane has read the stage that is filled again
-        fill(st, at + 2 + R::kBlocks);
-        ++stages;
+        fill(st, at - x + R::kStages * R::kBlocks);
+        if (++st == R::kStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
     }
     // ---- the row's result, or this share's part of it
@@ -617,16 +625,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
       for (int c = 0; c < 2; ++c) {
         const int col = nt * 8 + 2 * t + c;
         if (col >= heads) continue;
-        const float l = r.l[nt][c], m = r.m[nt][c];
+        const float l = r.l[nt][c] * 0x1p-64f, m = r.m[nt][c];
         const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
         const size_t out = (size_t)row_b * a.Hq + hk * a.group + tile * 8 * NT + col;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          const float mid = r.mid[g][nt][c];
-          const float x0 = (r.acc[2 * g][nt][c] + mid) * inv;
-          const float x1 = (r.acc[2 * g][nt][2 + c] + mid) * inv;
-          const float x2 = (r.acc[2 * g + 1][nt][c] + mid) * inv;
-          const float x3 = (r.acc[2 * g + 1][nt][2 + c] + mid) * inv;
+          const float mid = r.mid[g][nt][c] * 0x1p-64f;
+          const float x0 = fmaf(r.acc[2 * g][nt][c], 0x1p69f, mid) * inv;
+          const float x1 = fmaf(r.acc[2 * g][nt][2 + c], 0x1p65f, mid) * inv;
+          const float x2 = fmaf(r.acc[2 * g + 1][nt][c], 0x1p69f, mid) * inv;
+          const float x3 = fmaf(r.acc[2 * g + 1][nt][2 + c], 0x1p65f, mid) * inv;
           if (whole)
             *reinterpret_cast<uint2*>(a.o + out * D + 32 * g + 4 * i) =
                 make_uint2(pack_bf16x2(x0, x1), pack_bf16x2(x2, x3));
@@ -704,8 +712,80 @@ __device__ float2 join_ml(const AttendArgs& a, const RowSpan& s, int col) {
 }
 
 // One block per (sequence, query head) whose row was cut by shares, or is empty.
-// kW warps: two where there are rows enough to fill the GPU (64 sequences of 32 heads:
-// one wave of blocks), eight where few rows were cut into many parts.
+// w_out = w_in + sum over the group of 2^(score - log2 sum), for kWeightKeys keys of
+// a (sequence, kv head).  The scores are on their way while the sums of rows that
+// shares cut are joined, a warp per query head.
+template <int NT, int kW>
+__device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_lse2) {
+  constexpr int kPer = kWeightKeys / (kW * 32);
+  const int steps = (a.cap + kWeightKeys - 1) / kWeightKeys;
+  const int bh = unit / steps, j0 = (unit - bh * steps) * kWeightKeys + threadIdx.x;
+  const int b = bh / a.Hkv, hk = bh - b * a.Hkv, len = seq_len(a, b);
+  if ((unit - bh * steps) * kWeightKeys >= len) {
+    grid_dep_wait();
+    grid_dep_launch();
+    return;
+  }
+  float w[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int j = j0 + x * kW * 32;
+    w[x] = a.w_in && j < len ? a.w_in[(size_t)bh * a.w_stride + j] : 0.f;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  const float* src = a.scores + (size_t)bh * a.cap * a.group;
+  const bool four = (a.group & 3) == 0;
+  float4 s[kPer];  // the first four (or one) of each key
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int j = j0 + x * kW * 32;
+    s[x] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (j >= len) continue;
+    if (four) s[x] = *reinterpret_cast<const float4*>(src + (size_t)j * a.group);
+    else s[x].x = src[(size_t)j * a.group];
+  }
+  const int warp = threadIdx.x >> 5;
+  for (int h = warp; h < a.group; h += kW) {
+    const int tile = h / (8 * NT), col = h - tile * 8 * NT;
+    const RowSpan sp = row_span(a, b, hk * a.tiles + tile);
+    float z;
+    if (sp.w0 == sp.w1) {
+      z = a.lse2[(size_t)b * a.Hq + hk * a.group + h];
+    } else {
+      const float2 ml = join_ml<NT>(a, sp, col);
+      z = ml.y > 0.f ? ml.x + __log2f(ml.y) : -INFINITY;
+    }
+    if ((threadIdx.x & 31) == 0) s_lse2[h] = z;
+  }
+  __syncthreads();
+  const bool empty = s_lse2[0] == -INFINITY;  // every page out of range
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int j = j0 + x * kW * 32;
+    if (j >= len) break;
+    float sum = 0.f;
+    if (four) {
+      float4 y = s[x];
+      for (int h = 0;;) {
+        sum += (ex2_mufu(y.x - s_lse2[h]) + ex2_mufu(y.y - s_lse2[h + 1])) +
+               (ex2_mufu(y.z - s_lse2[h + 2]) + ex2_mufu(y.w - s_lse2[h + 3]));
+        if ((h += 4) >= a.group) break;
+        y = *reinterpret_cast<const float4*>(src + (size_t)j * a.group + h);
+      }
+    } else {
+      sum = ex2_mufu(s[x].x - s_lse2[0]);
+      for (int h = 1; h < a.group; ++h) sum += ex2_mufu(src[(size_t)j * a.group + h] - s_lse2[h]);
+    }
+    a.w_out[(size_t)bh * a.w_stride + j] = w[x] + (empty ? 0.f : sum);
+  }
+}
+
+// The first B * Hq blocks: one (sequence, query head) each, whose row was cut by
+// shares or is empty.  The others, where weights are asked for: a unit of weights
+// each.  kW warps: four where there are rows enough to fill the GPU, eight where few
+// rows were cut into many parts; with weights or without, so that O has the same
+// bits.
 template <int D, int NT, int kW>
 __global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
   constexpr int kV = D / 32;
@@ -713,6 +793,11 @@ __global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The lengths were complete before the attention kernel let this one start, so
   // they are read, and the row's parts found, while it still runs.
+  if ((int)blockIdx.x >= a.B * a.Hq) {
+    __shared__ float s_lse2[128];
+    weigh<NT, kW>(a, blockIdx.x - a.B * a.Hq, s_lse2);
+    return;
+  }
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
   const int hk = hq / a.group, in_group = hq - hk * a.group;
   const int tile = in_group / (8 * NT), col = in_group - tile * 8 * NT;
@@ -723,7 +808,7 @@ __global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
   __nv_bfloat16* o = a.o + (size_t)blockIdx.x * D;
   if (s.nb == 0) {  // an empty sequence
     for (int x = threadIdx.x; x < D / 2; x += kW * 32) reinterpret_cast<uint32_t*>(o)[x] = 0u;
-    if (threadIdx.x == 0) write_lse(a, blockIdx.x, 0.f, 0.f);
+    if (threadIdx.x == 0) a.lse[blockIdx.x] = -INFINITY;
     return;
   }
   if (s.w0 == s.w1) return;
@@ -761,51 +846,8 @@ __global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
     }
     reinterpret_cast<uint32_t*>(o)[threadIdx.x] = pack_bf16x2(x0 * inv, x1 * inv);
   }
-  if (threadIdx.x == 0) write_lse(a, blockIdx.x, ml.x, ml.y);
-}
-
-// w_out = w_in + sum over the group of 2^(score - log2 sum), for kWeightKeys keys of
-// a (sequence, kv head) per block.
-__global__ void __launch_bounds__(256) weight_kernel(const AttendArgs a) {
-  __shared__ float s_lse2[128];
-  const int b = blockIdx.z, hk = blockIdx.y, len = seq_len(a, b);
-  const int j0 = blockIdx.x * kWeightKeys;
-  constexpr int kPer = kWeightKeys / 256;
-  const size_t row = (size_t)b * a.Hkv + hk;
-  float w[kPer];
-  if (j0 < len && a.w_in) {
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int j = j0 + x * 256 + threadIdx.x;
-      w[x] = j < len ? a.w_in[row * a.w_stride + j] : 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) w[x] = 0.f;
-  }
-  grid_dep_wait();
-  grid_dep_launch();
-  if (j0 >= len) return;
-  if (threadIdx.x < a.group) s_lse2[threadIdx.x] = a.lse2[(size_t)b * a.Hq + hk * a.group + threadIdx.x];
-  __syncthreads();
-  const bool empty = s_lse2[0] == -INFINITY;  // every page out of range
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) {
-    const int j = j0 + x * 256 + threadIdx.x;
-    if (j >= len) break;
-    const float* src = a.scores + (row * a.cap + j) * a.group;
-    float sum = 0.f;
-    if ((a.group & 3) == 0) {
-      for (int h = 0; h < a.group; h += 4) {
-        const float4 s = *reinterpret_cast<const float4*>(src + h);
-        sum += (ex2_mufu(s.x - s_lse2[h]) + ex2_mufu(s.y - s_lse2[h + 1])) +
-               (ex2_mufu(s.z - s_lse2[h + 2]) + ex2_mufu(s.w - s_lse2[h + 3]));
-      }
-    } else {
-      for (int h = 0; h < a.group; ++h) sum += ex2_mufu(src[h] - s_lse2[h]);
-    }
-    a.w_out[row * a.w_stride + j] = w[x] + (empty ? 0.f : sum);
-  }
+  if (threadIdx.x == 0)
+    a.lse[blockIdx.x] = ml.y > 0.f ? (ml.x + __log2f(ml.y)) * 0.69314718055994531f : -INFINITY;
 }
 
 bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -837,7 +879,7 @@ AttendLayout attend_layout(int B, int Hq, int Hkv, int D, int cap, int sms) {
 
 template <int D, int NT>
 int launch_attend(const AttendArgs& a, cudaStream_t stream) {
-  constexpr int kSmem = kWarps * 2 * Ring<D>::kBytes;
+  constexpr int kSmem = kWarps * Ring<D>::kStages * Ring<D>::kBytes;
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
@@ -854,16 +896,13 @@ int launch_attend(const AttendArgs& a, cudaStream_t stream) {
     return FA_ERR_CUDA;
   record_timing(true, stream);
   const int rows = a.B * a.Hq;
-  const auto join = rows >= 1024 ? join_kernel<D, NT, 2> : join_kernel<D, NT, 8>;
-  if (launch_pdl(join, dim3(rows), dim3(rows >= 1024 ? 64 : 256), 0, stream, a) != cudaSuccess)
+  long long blocks = rows;
+  if (a.scores) blocks += (long long)a.B * a.Hkv * ((a.cap + kWeightKeys - 1) / kWeightKeys);
+  const int warps = rows >= 1024 ? 4 : 8;
+  const auto join = warps == 4 ? join_kernel<D, NT, 4> : join_kernel<D, NT, 8>;
+  if (launch_pdl(join, dim3((unsigned)blocks), dim3(warps * 32), 0, stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
-  int launches = 2;
-  if (a.scores) {
-    const dim3 grid((a.cap + kWeightKeys - 1) / kWeightKeys, a.Hkv, a.B);
-    if (launch_pdl(weight_kernel, grid, dim3(256), 0, stream, a) != cudaSuccess) return FA_ERR_CUDA;
-    ++launches;
-  }
-  note_launches(launches);
+  note_launches(2);
   return FA_OK;
 }
 
@@ -896,7 +935,8 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   if (Hq < 1 || Hq % Hkv != 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
   if ((long long)B * Hq > (1LL << 30)) return FA_ERR_INVALID_ARG;
-  if (weights_out && (B > 65535 || Hkv > 65535)) return FA_ERR_UNSUPPORTED;  // its launch grid
+  if (weights_out && (long long)B * Hkv * (weight_slots / kWeightKeys + 1) > (1LL << 30))
+    return FA_ERR_INVALID_ARG;
   if (q_batch_stride < 0 || q_head_stride < 0) return FA_ERR_INVALID_ARG;
   if ((q_batch_stride & 7) || (q_head_stride & 7)) return FA_ERR_MISALIGNED;
   if (!q || !cache || !o || !lse || !cache_lens || !page_table) return FA_ERR_INVALID_ARG;
