@@ -183,6 +183,7 @@ struct BwdUnit {
   // packed calls: the sequence's first row, and its first row where each one
   // is padded to 64; its queries and keys are kv_len, bhk is the kv head
   int row0, pad0;
+  int gi0;  // the unit's q head of the group where the heads are split, else 0
 };
 
 // The r-th unit this CTA processes under static dealing (-1 when it has no
@@ -241,16 +242,21 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u, int group) 
   return w;
 }
 
-// Unit u of a packed call with n_items items: groups of head_group kv heads in
-// turn; in a group (item, kv head), the head running fastest.
+// Unit u of a packed call with n_items items: groups of head_group heads in turn
+// (kv heads, or q heads where they are split); in a group (item, head), the head
+// running fastest.
 template <bool kMod, int QB>
 __device__ __forceinline__ BwdUnit bwd_unit_var(const BwdArgs& a, int u, int group, int n_items) {
   BwdUnit w;
-  const int G = a.head_group, g = u / (G * n_items), h0 = g * G, gg = min(G, a.Hkv - h0);
+  const bool split = a.dk_part != nullptr;
+  const int G = a.head_group, g = u / (G * n_items), h0 = g * G;
+  const int gg = min(G, (split ? a.Hq : a.Hkv) - h0);
   const int r = u - g * G * n_items;
   const int item = r / gg;
   const VarItem it = load_item(a.items, item);
-  w.hk = w.bhk = h0 + (r - item * gg);
+  const int h = h0 + (r - item * gg);
+  w.hk = w.bhk = split ? h / group : h;
+  w.gi0 = split ? h - w.hk * group : 0;
   w.b = it.b;
   w.j = it.tile;
   w.kv_len = it.len;
@@ -259,7 +265,7 @@ __device__ __forceinline__ BwdUnit bwd_unit_var(const BwdArgs& a, int u, int gro
   int hi;
   bwd_qblk_range<kMod, QB>(a, it.len, w.j, it.len, w.lo, hi);
   w.n_blk = hi - w.lo;
-  w.n_it = group * w.n_blk;
+  w.n_it = split ? w.n_blk : group * w.n_blk;
   return w;
 }
 

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
   const int n_items = kVar ? *a.n_items : 0;
-  const int n_units = kVar ? n_items * a.Hkv : a.n_units;
+  const int n_units = kVar ? n_items * (a.dk_part ? a.Hq : a.Hkv) : a.n_units;
   // The r-th unit of this CTA.  Static dealing: computed by every role alike.
   // Dynamic dealing: the TMA thread takes the next unit number from the global
   // counter and posts it in ring slot r % kURing (take_unit); the other roles
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
   // the q head of the tensor maps' head coordinate, and (bh, block iq)'s places
   // in lse2 / delta, in the dQ accumulators and among the semaphores
   auto head_of = [&](const BwdUnit& w, int gi) {
-    return (kVar ? 0 : w.b * a.Hq) + w.hk * group + gi;
+    return (kVar ? w.gi0 : w.b * a.Hq) + w.hk * group + gi;
   };
   auto vec_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
     return kVar ? (size_t)bh * a.T_pad + w.pad0 + (size_t)iq * kQB
@@ -1021,6 +1021,31 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
           mbar_arrive(bar(L::kBarDKVEmpty));
         }
         const float sc = is_v ? 1.f : a.scale;
+        if (kVar && a.dk_part) {
+          // this q head's fp32 part; the lanes trade 16-byte pieces as below
+          float* base = (is_v ? a.dv_part : a.dk_part) +
+                        ((size_t)(w.hk * group + w.gi0) * a.T + w.row0) * D;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t y[16];
+#pragma unroll
+            for (int wd = 0; wd < 4; ++wd) {
+              uint32_t x[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                x[m] = __float_as_uint(u2f(vk[16 * hf + 4 * m + wd]) * sc);
+              xpose4(x, lane);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) y[4 * m + wd] = x[m];
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              if (row0 + m < Sk)
+                *reinterpret_cast<uint4*>(base + (size_t)(row0 + m) * D + c * 32 + (4 * hf + pc) * 4) =
+                    make_uint4(y[4 * m], y[4 * m + 1], y[4 * m + 2], y[4 * m + 3]);
+          }
+          continue;
+        }
         uint32_t wk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) wk[e] = pack_bf16x2(u2f(vk[2 * e]) * sc, u2f(vk[2 * e + 1]) * sc);
@@ -1132,6 +1157,33 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
       w.w = pack_bf16x2(x1.z * a.scale, x1.w * a.scale);
       *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.dq) +
                                 ((size_t)(it.row0 + i) * a.Hq + h) * D + c8 * 8) = w;
+    }
+  }
+  if (!a.dk_part) return;
+  // the q heads' parts of dK and dV, summed in head order
+  const int group = a.Hq / a.Hkv, n_kv = *a.n_items * a.Hkv;
+  for (int u = blockIdx.x; u < 2 * n_kv; u += gridDim.x) {
+    const bool is_v = u >= n_kv;
+    const int x0 = is_v ? u - n_kv : u;
+    const int item = x0 / a.Hkv, hk = x0 - item * a.Hkv;
+    const VarItem it = load_item(a.items, item);
+    const int rows = min(kTile, it.len - it.tile * kTile);
+    const float* part = is_v ? a.dv_part : a.dk_part;
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(is_v ? a.dv : a.dk);
+    for (int x = threadIdx.x; x < rows * kPerRow; x += blockDim.x) {
+      const int i = it.row0 + it.tile * kTile + x / kPerRow, c8 = x % kPerRow;
+      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f), y1 = y0;
+#pragma unroll 4
+      for (int g = 0; g < group; ++g) {
+        const float4* src = reinterpret_cast<const float4*>(
+            part + ((size_t)(hk * group + g) * a.T + i) * D + c8 * 8);
+        const float4 z0 = src[0], z1 = src[1];
+        y0.x += z0.x, y0.y += z0.y, y0.z += z0.z, y0.w += z0.w;
+        y1.x += z1.x, y1.y += z1.y, y1.z += z1.z, y1.w += z1.w;
+      }
+      *reinterpret_cast<uint4*>(out + ((size_t)i * a.Hkv + hk) * D + c8 * 8) =
+          make_uint4(pack_bf16x2(y0.x, y0.y), pack_bf16x2(y0.z, y0.w), pack_bf16x2(y1.x, y1.y),
+                     pack_bf16x2(y1.z, y1.w));
     }
   }
 }
@@ -1267,7 +1319,8 @@ static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
   const int sms = info.sm_count;
   const long long q_units = (long long)max_items * a.Hq, kv_units = (long long)max_items * a.Hkv;
   const int small_grid = (int)(q_units < 8LL * sms ? q_units : 8LL * sms);
-  const int grid = (int)(kv_units < sms ? kv_units : sms);
+  const long long units = a.dk_part ? q_units : kv_units;
+  const int grid = (int)(units < sms ? units : sms);
   if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
   // units come from the global counter in the plan's order (longest first, each

@@ -189,6 +189,11 @@ struct BwdArgs {
   const int* n_items;
   const CUtensorMap* maps;
   int T, T_pad;
+  // packed calls with few units: each q head of a group is a unit of its own and
+  // leaves fp32 parts of dK and dV [Hq, T, D], which the last kernel sums in head
+  // order; null otherwise (a unit then loops over the group)
+  float* dk_part;
+  float* dv_part;
   int qblk_rows;           // query rows per block of the main kernel (64 or 128):
                            // semaphore i of a head counts the writers of block i
 };

@@ -177,8 +177,14 @@ bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>
 struct VarLayout {
   int max_items, groups;
   long long t_pad;
-  size_t off_items, off_maps, off_acc, off_delta, off_lse2, off_sem, total;
+  bool split;  // q heads are units of their own (BwdArgs::dk_part)
+  size_t off_items, off_maps, off_acc, off_delta, off_lse2, off_sem, off_dk, off_dv, total;
 };
+
+// Up to this many (kv tile, kv head) units a grouped backward splits its q heads:
+// with u units a causal sequence's longest one is 304 / u of an SM's even share of
+// 152, so below two to four units per SM the longest unit sets the time.
+constexpr long long kSplitUnits = 608;
 
 int check_var(int B, int T, int Hq, int Hkv, int D) {
   if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
@@ -190,7 +196,7 @@ int check_var(int B, int T, int Hq, int Hkv, int D) {
   return FA_OK;
 }
 
-VarLayout var_layout(int B, int T, int Hq, int D, bool backward, bool deterministic) {
+VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool deterministic) {
   VarLayout L{};
   const int rows = backward ? 128 : 256;
   L.max_items = T / rows + B;
@@ -207,6 +213,12 @@ VarLayout var_layout(int B, int T, int Hq, int D, bool backward, bool determinis
   L.total = L.off_sem;
   if (deterministic)
     L.total = up256(L.off_sem + (size_t)L.groups * Hq * (L.t_pad / 64) * sizeof(int));
+  L.split = Hq > Hkv && (long long)L.max_items * Hkv <= kSplitUnits;
+  if (L.split) {
+    L.off_dk = L.total;
+    L.off_dv = up256(L.off_dk + (size_t)Hq * T * D * sizeof(float));
+    L.total = up256(L.off_dv + (size_t)Hq * T * D * sizeof(float));
+  }
   return L;
 }
 
@@ -259,7 +271,7 @@ extern "C" {
 size_t fa_varlen_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int backward,
                                  int deterministic) {
   if (check_var(B, T, Hq, Hkv, D) != FA_OK) return 0;
-  return var_layout(B, T, Hq, D, backward != 0, deterministic != 0).total;
+  return var_layout(B, T, Hq, Hkv, D, backward != 0, deterministic != 0).total;
 }
 
 int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -278,7 +290,7 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
       misaligned(lse, 4) || misaligned(cu_seqlens, 4))
     return FA_ERR_MISALIGNED;
-  const VarLayout L = var_layout(B, T, Hq, D, false, false);
+  const VarLayout L = var_layout(B, T, Hq, Hkv, D, false, false);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -337,7 +349,7 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
       misaligned(dO, 16) || misaligned(dq, 16) || misaligned(dk, 16) || misaligned(dv, 16) ||
       misaligned(lse, 4) || misaligned(cu_seqlens, 4))
     return FA_ERR_MISALIGNED;
-  const VarLayout L = var_layout(B, T, Hq, D, true, deterministic != 0);
+  const VarLayout L = var_layout(B, T, Hq, Hkv, D, true, deterministic != 0);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -369,6 +381,10 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   a.delta = reinterpret_cast<float*>(ws + L.off_delta);
   a.lse2 = reinterpret_cast<float*>(ws + L.off_lse2);
   a.sem = reinterpret_cast<int*>(ws + L.off_sem);
+  if (L.split) {
+    a.dk_part = reinterpret_cast<float*>(ws + L.off_dk);
+    a.dv_part = reinterpret_cast<float*>(ws + L.off_dv);
+  }
   a.status = p.status;
   a.unit_counter = p.counter;
   a.B = B;
@@ -385,12 +401,11 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   a.qblk_rows = 64;
   {
     // kv heads dealt together, so that their q, dO, dQ accumulators and K / V stay
-    // in L2, as in the dense call: measured at 16384 tokens and 16 heads of 128
-    // elements, the main kernel runs 1,077 us over all heads at once
+    // in L2, as in the dense call
     const double per_kv_head =
         (double)(Hq / Hkv) * T * D * (4.0 + 4.0 * L.groups) + (double)T * D * 4.0;
     const int hg = (int)(kBwdGroupBytes / per_kv_head < Hkv ? kBwdGroupBytes / per_kv_head : Hkv);
-    a.head_group = hg < 1 ? 1 : hg;
+    a.head_group = (hg < 1 ? 1 : hg) * (L.split ? Hq / Hkv : 1);
   }
   a.items = p.items;
   a.n_items = p.n_items;

@@ -73,7 +73,12 @@ def test_workspace_bytes(L):
     one = L.fa_varlen_workspace_bytes(4, 1000, 8, 2, 128, 1, 0)
     det = L.fa_varlen_workspace_bytes(4, 1000, 8, 2, 128, 1, 1)
     acc = 8 * 1000 * 128 * 4
-    assert acc < one < 1.1 * acc and 4 * acc < det < 4.1 * acc
+    # ... and, few units of grouped heads, a part of dK and of dV per query head
+    assert 3 * acc < one < 3.1 * acc and 6 * acc < det < 6.1 * acc
+    same = L.fa_varlen_workspace_bytes(4, 1000, 8, 8, 128, 1, 0)
+    assert acc < same < 1.1 * acc
+    many = L.fa_varlen_workspace_bytes(4, 100000, 8, 4, 128, 1, 0)
+    assert 100 * acc < many < 110 * acc
 
 
 def test_binding_refusals():
