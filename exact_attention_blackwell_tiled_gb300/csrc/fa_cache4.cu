@@ -15,10 +15,10 @@
 // read: value = min + scale * code in one fp32 FMA, rounded once to bf16.  Reads
 //   5/4 D bytes of a token, writes 4 D.
 // evict: two kernels.  The first ranks one (sequence, kv head) per block: the K
-//   largest weights are found digit by digit (four passes of 8 bits over the
-//   weights' bit patterns, which order like the values), and a last pass in
-//   index order counts what is kept, ties from the lowest index up, and writes
-//   each kept key's old place and weight.  The second copies the kept keys' codes
+//   largest weights are found digit by digit (three passes of 11, 11 and 10 bits
+//   over the weights' bit patterns, which order like the values; up to 16384 of
+//   them stay in registers), and a last pass in index order counts what is kept,
+//   ties from the lowest index up, and writes each kept key's old place and weight.  The second copies the kept keys' codes
 //   to the new pages in order: 16 slots per warp, in 16-byte pieces.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -63,17 +63,63 @@ __device__ int find_sequence(const int* cu, int B, int i) {
   return cu[lo] <= i && i < cu[lo + 1] ? lo : -1;
 }
 
-// Code of d = x - mn for scale sc: rint(d / sc), ties to even.  A product with the
-// reciprocal gives the code or one beside it; the remainder d - code sc, exact in
-// one FMA since code * sc has 13 bits and lies within sc of d, tells which.
-__device__ __forceinline__ uint32_t quantise_one(float d, float sc, float rcp, float half) {
-  const float m = __fmaf_rn(d, rcp, 12582912.f);  // 1.5 * 2^23 + code
-  const float e = __fmaf_rn(-__fsub_rn(m, 12582912.f), sc, d);
-  int c = __float_as_int(m) & 31;
-  // an odd code gives way at a remainder of exactly half a step
-  const float limit = __int_as_float(__float_as_int(half) - (c & 1));
-  if (fabsf(e) > limit) c += e > 0.f ? 1 : -1;
-  return (uint32_t)min(c, 15);
+// RN(a / b) from y near 1 / b: the quotient of the product is off by an ulp or two,
+// its remainder is exact in one FMA, and the correction leaves an error far below
+// half an ulp before the last rounding (Markstein's division step).  For a code's
+// quotient that is enough for the sides of a tie, d = (code + 1/2) sc: a tie comes
+// out exactly, and the nearest other d, an ulp away, lies more than half an ulp of
+// the quotient off it, since code + 1/2 has 5 bits and sc 8.
+__device__ __forceinline__ float divide(float a, float b, float y) {
+  const float q = __fmul_rn(a, y);
+  return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+}
+
+__device__ __forceinline__ float reciprocal_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Scale and codes of a lane's E elements f of a group whose minimum is mn and
+// maximum mx; the codes come packed, element e in bits 4 e.
+template <int E>
+__device__ __forceinline__ uint32_t quantise(const float (&f)[E], float mn, float mx, uint32_t* scale) {
+  const float range = __fsub_rn(mx, mn);
+  // far from the ends of fp32's range the divisions are the short ones above
+  const bool plain = range >= 0x1p-80f && range <= 0x1p80f;
+  const __nv_bfloat16 sc16 =
+      __float2bfloat16_rn(plain ? divide(range, 15.f, 0x1.111112p-4f) : __fdiv_rn(range, 15.f));
+  *scale = __bfloat16_as_ushort(sc16);
+  const float sc = __bfloat162float(sc16);
+  uint32_t codes = 0;
+  if (plain) {
+    const float y = reciprocal_approx(sc);
+    // adding 1.5 * 2^23 rounds to the nearest integer, ties to even, and leaves it in
+    // the low bits; the codes are at most 15 (the scale is at most 2^-9 too small),
+    // so the words add up without touching each other but for a constant
+    uint32_t sum = 0, magic = 0;
+#pragma unroll
+    for (int e = E - 1; e >= 0; --e) {
+      const float m = __fadd_rn(divide(__fsub_rn(f[e], mn), sc, y), 12582912.f);
+      sum = sum * 16u + __float_as_uint(m);
+      magic = magic * 16u + 0x4B400000u;
+    }
+    codes = sum - magic;
+  } else if (sc > 0.f) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      codes |= (uint32_t)fminf(rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc)), 15.f) << (4 * e);
+  }
+  return codes;
+}
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 y = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
 
 template <int D>
@@ -85,22 +131,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   const bool is_v = lane >= 16;
   const int l = lane & 15;
   const int g = l / kLanesPerGroup, part = l % kLanesPerGroup;
-  const long long total = (long long)a.T * a.Hkv;
-  const long long item0 = ((long long)blockIdx.x * kAppendWarps + warp) * kAppendItems;
+  const uint32_t total = (uint32_t)a.T * a.Hkv;  // below 2^31
+  const uint32_t item0 = (blockIdx.x * kAppendWarps + warp) * kAppendItems;
   grid_dep_wait();
   grid_dep_launch();
   if (item0 >= total) return;
   // the vectors first: where they go is found while they are on their way
-  const int tok0 = (int)(item0 / a.Hkv), h0 = (int)(item0 - (long long)tok0 * a.Hkv);
+  const int tok0 = (int)(item0 / (uint32_t)a.Hkv), h0 = (int)(item0 - (uint32_t)tok0 * a.Hkv);
+  const long long token = is_v ? a.v_token : a.k_token, head = is_v ? a.v_head : a.k_head;
+  const __nv_bfloat16* src = (is_v ? a.v : a.k) + tok0 * token + h0 * head + l * kE;
   uint32_t x[kAppendItems][kE / 2];
+  // this lane's own item (lanes below kAppendItems), found on the way
+  int tok_n = tok0, h_n = h0;
 #pragma unroll
-  for (int n = 0; n < kAppendItems; ++n) {
+  for (int n = 0, h = h0, tok = tok0; n < kAppendItems; ++n) {
 #pragma unroll
     for (int e = 0; e < kE / 2; ++e) x[n][e] = 0u;
+    if (lane == n) tok_n = tok, h_n = h;
     if (item0 + n < total) {
-      const int tok = tok0 + (h0 + n) / a.Hkv, h = (h0 + n) % a.Hkv;
-      const __nv_bfloat16* src = (is_v ? a.v + tok * a.v_token + h * a.v_head
-                                       : a.k + tok * a.k_token + h * a.k_head) + l * kE;
       if constexpr (kE == 8) {
         const uint4 w = *reinterpret_cast<const uint4*>(src);
         x[n][0] = w.x, x[n][1] = w.y, x[n][2] = w.z, x[n][3] = w.w;
@@ -109,6 +157,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
         x[n][0] = w.x, x[n][1] = w.y;
       }
     }
+    src += head;
+    if (++h == a.Hkv) {
+      h = 0;
+      ++tok;
+      src += token - a.Hkv * head;
+    }
   }
   // lane n: the byte offset of item n's block, or -1, and its slot there
   long long off_n = -1;
@@ -116,7 +170,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   {
     const int first = a.cu ? find_sequence(a.cu, a.B, tok0) : tok0;
     if (lane < kAppendItems && item0 + lane < total) {
-      const int tok = tok0 + (h0 + lane) / a.Hkv, h = (h0 + lane) % a.Hkv;
+      const int tok = tok_n, h = h_n;
       int b = a.cu ? first : tok;
       if (a.cu) {
         // later items may belong to later sequences
@@ -144,31 +198,27 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
     const long long off = __shfl_sync(0xffffffffu, off_n, n);
     const int slot = __shfl_sync(0xffffffffu, slot_n, n);
     if (off < 0) continue;
-    float f[kE], mn = INFINITY, mx = -INFINITY;
+    // minimum and maximum two elements at a time, over the group's lanes, then of
+    // the two
+    uint32_t lo = x[n][0], hi = x[n][0];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      f[e] = (e & 1) ? __uint_as_float(x[n][e / 2] & 0xffff0000u) : __uint_as_float(x[n][e / 2] << 16);
-      mn = fminf(mn, f[e]);
-      mx = fmaxf(mx, f[e]);
+    for (int e = 1; e < kE / 2; ++e) {
+      lo = min2(lo, x[n][e]);
+      hi = max2(hi, x[n][e]);
     }
 #pragma unroll
     for (int s = 1; s < kLanesPerGroup; s <<= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+      lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+      hi = max2(hi, __shfl_xor_sync(0xffffffffu, hi, s));
     }
-    const __nv_bfloat16 sc16 = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
-    const float sc = __bfloat162float(sc16);
-    uint32_t codes = 0;
-    if (sc >= 1.17549435e-38f) {
-      const float rcp = __fdiv_rn(1.0f, sc), half = 0.5f * sc;
+    const float mn = fminf(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
+    const float mx = fmaxf(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    float f[kE];
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        codes |= quantise_one(__fsub_rn(f[e], mn), sc, rcp, half) << (4 * e);
-    } else if (sc > 0.f) {  // no reciprocal in range
-#pragma unroll
-      for (int e = 0; e < kE; ++e)
-        codes |= (uint32_t)fminf(rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc)), 15.f) << (4 * e);
-    }
+    for (int e = 0; e < kE; ++e)
+      f[e] = (e & 1) ? __uint_as_float(x[n][e / 2] & 0xffff0000u) : __uint_as_float(x[n][e / 2] << 16);
+    uint32_t scale;
+    const uint32_t codes = quantise<kE>(f, mn, mx, &scale);
     uint8_t* blk = a.cache + off;
     if (!is_v) {
       // elements 32 g + kE part ..: word (t, g), t = 8-element piece of the group
@@ -183,7 +233,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
         *reinterpret_cast<uint16_t*>(blk + L::v_half(slot, i + 1, g)) = (uint16_t)(codes >> 16);
     }
     if (part == 0) {
-      const uint32_t par = (uint32_t)__bfloat16_as_ushort(sc16) | (__float_as_uint(mn) & 0xffff0000u);
+      const uint32_t par = scale | (__float_as_uint(mn) & 0xffff0000u);
       *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kOffVPar : L::kOffKPar) + slot * L::kPar +
                                    g * 4) = par;
     }
@@ -202,10 +252,19 @@ struct ReadArgs {
   int blocks;  // cache blocks that S slots can lie in
 };
 
-// Two fields of w (low byte of w >> s) as their values, rounded to bf16.
-__device__ __forceinline__ uint32_t two_values(uint32_t w, int s, float sc, float mn) {
-  return pack_bf16x2(__fmaf_rn(sc, (float)((w >> s) & 15u), mn),
-                     __fmaf_rn(sc, (float)((w >> (s + 4)) & 15u), mn));
+// The values of w's eight 4-bit fields, rounded to bf16.  A field masked into the
+// mantissa of 2^23 is a number field * 2^k more; what the FMA sees is exact.
+__device__ __forceinline__ uint4 eight_values(uint32_t w, float sc, float mn) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int k = e < 5 ? 4 * e : 4 * (e - 5);  // fields 5..7 after a shift by 20
+    const uint32_t x = ((e < 5 ? w : w >> 20) & (15u << k)) | 0x4B000000u;
+    const float c = __fsub_rn(__uint_as_float(x), 8388608.f);           // field * 2^k
+    v[e] = __fmaf_rn(sc * __uint_as_float((127u - k) << 23), c, mn);  // sc 2^-k is exact
+  }
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 
 // One warp per cache block of 16 slots of a head, four lanes per key or value: a
@@ -217,11 +276,11 @@ __global__ void __launch_bounds__(128) read_kernel(const ReadArgs a) {
   using L = C4<D>;
   constexpr int kG = L::kGroups;
   const int lane = threadIdx.x & 31;
-  const long long x = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const uint32_t x = blockIdx.x * 4 + (threadIdx.x >> 5);  // below 2^31
   grid_dep_wait();
   grid_dep_launch();
-  if (x >= (long long)a.B * a.Hkv * a.blocks) return;
-  const int bh = (int)(x / a.blocks), j = (int)(x - (long long)bh * a.blocks);
+  if (x >= (uint32_t)a.B * a.Hkv * a.blocks) return;
+  const int bh = (int)(x / (uint32_t)a.blocks), j = (int)(x - (uint32_t)bh * a.blocks);
   const int b = bh / a.Hkv, h = bh - b * a.Hkv;
   const int from = a.first ? a.first[b] : 0, count = min(a.count[b], a.S);
   const int first = max(from, 0);  // a negative one is out of range: rows of zeros
@@ -273,9 +332,7 @@ __global__ void __launch_bounds__(128) read_kernel(const ReadArgs a) {
           codes = __byte_perm(w[n][0], w[n][1], (g & 1) ? 0x7632 : 0x5410);
       }
       const float sc = c4_scale(par[n][g]), mn = c4_min(par[n][g]);
-      *reinterpret_cast<uint4*>(dst + 32 * g) =
-          make_uint4(two_values(codes, 0, sc, mn), two_values(codes, 8, sc, mn),
-                     two_values(codes, 16, sc, mn), two_values(codes, 24, sc, mn));
+      *reinterpret_cast<uint4*>(dst + 32 * g) = eight_values(codes, sc, mn);
     }
   }
 }
@@ -327,8 +384,10 @@ __device__ __forceinline__ int block_prefix(int x, int* s_warp, int* total) {
   return inc - x + (warp ? s_warp[warp - 1] : 0);
 }
 
+constexpr int kRankKeys = 16;  // weights a thread keeps in registers
+
 __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictArgs a) {
-  __shared__ int s_hist[256];
+  __shared__ int s_hist[2048];
   __shared__ int s_warp[32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -360,76 +419,99 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictArgs a) {
   }
   const int early = n - a.recent;        // candidates; the rest are kept
   const int want = a.budget - a.recent;  // of them, the largest (0 <= want < early)
-  // the want-th largest key, a digit of 8 bits at a time from the top
+  // Thread t has weights t * per .. t * per + per - 1, in registers where they fit.
+  const int per = (n + kRankThreads - 1) / kRankThreads;
+  const bool cached = per <= kRankKeys;
+  const int i0 = threadIdx.x * per;
+  uint32_t key[kRankKeys];
+  if (cached) {
+#pragma unroll
+    for (int x = 0; x < kRankKeys; ++x)
+      if (x < per) key[x] = i0 + x < n ? order_key(w[i0 + x]) : 0u;
+  }
+  // the want-th largest key, a digit of 11, 11 and 10 bits at a time from the top
   uint32_t prefix = 0;
   int need = want;  // still to find among the keys that start with prefix
-  for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-    if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
+  for (int pass = 0; pass < 3 && want > 0; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
+    s_hist[threadIdx.x] = s_hist[threadIdx.x + 1024] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < early; i += kRankThreads) {
-      const uint32_t key = order_key(w[i]);
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&s_hist[(key >> shift) & 255], 1);
+    auto visit = [&](int i, uint32_t k) {
+      const bool on = i < early && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) ==
+                                                     (prefix >> (pass == 1 ? 21 : 10)));
+      if (on) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+    };
+    if (cached) {
+#pragma unroll
+      for (int x = 0; x < kRankKeys; ++x)
+        if (x < per) visit(i0 + x, key[x]);
+    } else {
+      for (int i = threadIdx.x; i < per * kRankThreads; i += kRankThreads)
+        visit(i, i < n ? order_key(w[i]) : 0u);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-      // lane l sums digits 255 - 8 l - 0..7, highest first
-      int part = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) part += s_hist[255 - 8 * threadIdx.x - e];
-      int inc = part;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (threadIdx.x >= o) inc += y;
-      }
-      int above = inc - part;  // keys with a higher digit than this lane's
-      if (above < need && need <= inc) {
-        for (int e = 0; e < 8; ++e) {
-          const int d = 255 - 8 * threadIdx.x - e, c = s_hist[d];
-          if (above + c >= need) {
-            s_prefix = prefix | ((uint32_t)d << shift);
-            s_need = need - above;
-            break;
-          }
-          above += c;
-        }
-      }
+    // thread t has bins bins - 1 - 2 t and the one below, from the highest digit down
+    const int top = bins - 1 - 2 * (int)threadIdx.x;
+    const int c0 = top > 0 ? s_hist[top] : 0, c1 = top > 0 ? s_hist[top - 1] : 0;
+    int total;
+    const int above = block_prefix(c0 + c1, s_warp, &total);
+    if (above < need && need <= above + c0 + c1) {
+      const bool first = need <= above + c0;
+      s_prefix = prefix | ((uint32_t)(first ? top : top - 1) << shift);
+      s_need = need - above - (first ? 0 : c0);
     }
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
-    __syncthreads();
   }
-  // in index order: keys above the threshold, the first `need` at it, the latest
-  int done = 0, ties = 0;
-  for (int i0 = 0; i0 < n; i0 += kRankThreads) {
-    const int i = i0 + threadIdx.x;
-    float wi = 0.f;
-    bool keep = false, tie = false;
-    if (i < n) {
-      wi = w[i];
-      if (i >= early) {
-        keep = true;
-      } else if (want > 0) {
-        const uint32_t key = order_key(wi);
-        keep = key > prefix;
-        tie = key == prefix;
-      }
+  // In index order: keys above the threshold, the first `need` at it, the latest.
+  // A thread counts what it keeps for certain and its ties, in one prefix sum over
+  // the block; then it knows how many ties before it were taken.
+  auto verdict = [&](int i, uint32_t k, bool* tie) {
+    *tie = i < early && want > 0 && k == prefix;
+    return i < n && (i >= early || (want > 0 && k > prefix));
+  };
+  auto put = [&](int at, int i, uint32_t k) {
+    if (at >= a.budget) return;
+    src[at] = i;
+    w_out[at] = __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+  };
+  if (cached) {
+    int sure = 0, ties = 0;
+#pragma unroll
+    for (int x = 0; x < kRankKeys; ++x) {
+      if (x >= per) continue;
+      bool tie;
+      sure += verdict(i0 + x, key[x], &tie) ? 1 : 0;
+      ties += tie ? 1 : 0;
     }
-    // ties counted in the high half (at most 1024 of each per step)
+    int total;
+    const int before = block_prefix((ties << 16) | sure, s_warp, &total);  // at most 16384 each
+    int ties_before = before >> 16, at = (before & 0xffff) + min(ties_before, need);
+#pragma unroll
+    for (int x = 0; x < kRankKeys; ++x) {
+      if (x >= per) continue;
+      bool tie;
+      bool keep = verdict(i0 + x, key[x], &tie);
+      if (tie) keep = ties_before++ < need;
+      if (keep) put(at++, i0 + x, key[x]);
+    }
+    return;
+  }
+  int done = 0, ties = 0;
+  for (int c = 0; c < n; c += kRankThreads) {
+    const int i = c + threadIdx.x;
+    const uint32_t k = i < n ? order_key(w[i]) : 0u;
+    bool tie;
+    bool keep = verdict(i, k, &tie);
     int total;
     const int before = block_prefix((tie ? 0x10000 : 0) | (keep ? 1 : 0), s_warp, &total);
     const int ties_before = ties + (before >> 16);
-    const int kept_ties = min(ties_before, need) - min(ties, need);  // in this step, before i
+    const int at = done + (before & 0xffff) + min(ties_before, need) - min(ties, need);
     if (tie) keep = ties_before < need;
-    const int at = done + (before & 0xffff) + kept_ties;
-    if (keep && at < a.budget) {
-      src[at] = i;
-      w_out[at] = wi;
-    }
+    if (keep) put(at, i, k);
     const int ties_after = ties + (total >> 16);
-    done += (total & 0xffff) + (min(ties_after, need) - min(ties, need));
+    done += (total & 0xffff) + min(ties_after, need) - min(ties, need);
     ties = ties_after;
   }
 }
@@ -445,9 +527,9 @@ __global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int blocks = (a.budget + kC4Block - 1) / kC4Block;
-  const long long x = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (x >= (long long)a.B * a.Hkv * blocks) return;
-  const int bh = (int)(x / blocks), blk = (int)(x - (long long)bh * blocks);
+  const uint32_t x = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);  // below 2^31
+  if (x >= (uint32_t)a.B * a.Hkv * blocks) return;
+  const int bh = (int)(x / (uint32_t)blocks), blk = (int)(x - (uint32_t)bh * blocks);
   const int b = bh / a.Hkv, h = bh - b * a.Hkv;
   const int slots = min(kC4Block, a.lens_out[b] - blk * kC4Block);
   if (slots <= 0) return;
@@ -555,7 +637,7 @@ int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, c
   reset_launches();
   int rc = check_cache4(num_pages, Hkv, D, page_size, B, table_width);
   if (rc) return rc;
-  if (T < 0 || (!cu_seqlens && T != B) || (long long)T * Hkv > (1LL << 34)) return FA_ERR_INVALID_ARG;
+  if (T < 0 || (!cu_seqlens && T != B) || (long long)T * Hkv >= (1LL << 31) - 64) return FA_ERR_INVALID_ARG;
   const fa_packed_stride plain = {(int64_t)Hkv * D, D};
   const fa_packed_stride ks = k_stride ? *k_stride : plain, vs = v_stride ? *v_stride : plain;
   for (int64_t s : {ks.token, ks.head, vs.token, vs.head}) {
@@ -576,7 +658,6 @@ int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, c
                make_table(page_table, table_width, num_pages, page_size, status), B, T, Hkv};
   const long long per = kAppendWarps * kAppendItems;
   const long long grid = ((long long)T * Hkv + per - 1) / per;
-  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   const auto kernel = D == 128 ? append_kernel<128> : append_kernel<64>;
   if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kAppendWarps * 32), 0,
                  static_cast<cudaStream_t>(stream), a) != cudaSuccess)
@@ -603,7 +684,7 @@ int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, voi
   // S slots from any first one
   const int blocks = (int)(((long long)S + (first ? kC4Block - 1 : 0) + kC4Block - 1) / kC4Block);
   const long long grid = ((long long)B * Hkv * blocks + 3) / 4;
-  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (grid >= (1LL << 29)) return FA_ERR_INVALID_ARG;
   ReadArgs a{static_cast<const uint8_t*>(cache), static_cast<__nv_bfloat16*>(k),
              static_cast<__nv_bfloat16*>(v), first, count,
              make_table(page_table, table_width, num_pages, page_size, status), B, Hkv, S,
@@ -634,7 +715,7 @@ int fa_cache4_evict(void* cache, int num_pages, int page_size, const float* weig
       misaligned(weights_out, 4) || misaligned(lens_out, 4))
     return FA_ERR_MISALIGNED;
   const long long blocks = (long long)B * Hkv * ((budget + kC4Block - 1) / kC4Block);
-  if ((blocks + 7) / 8 > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (blocks >= (1LL << 31) - 64) return FA_ERR_INVALID_ARG;
   if ((rc = check_device())) return rc;
   int* status = cache4_status_word();
   if (!status) return FA_ERR_CUDA;
