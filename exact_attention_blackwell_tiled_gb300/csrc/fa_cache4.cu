@@ -8,10 +8,8 @@
 //   mn is an element and so exact in bf16; the codes are taken with the rounded
 //   scale, so its rounding (2^-9) moves the top code's value, not the others'
 //   choice.  Bound by memory: it reads 4 D bytes of a token's key and value and
-//   writes 5/4 D.  Half a warp holds one vector (16 bytes a lane at D = 128), so
-//   minimum and maximum take two shuffles each and a warp stores a token's key
-//   and value together; a warp takes four (token, head) pairs, whose loads it
-//   issues before it looks for the places they go to.
+//   writes 5/4 D.  A warp takes eight (token, head) pairs, whose loads it issues
+//   before it looks for the places they go to.
 // read: value = min + scale * code in one fp32 FMA, rounded once to bf16.  Reads
 //   5/4 D bytes of a token, writes 4 D.
 // evict: two kernels.  The first ranks one (sequence, kv head) per block: the K
@@ -45,7 +43,7 @@ struct AppendArgs {
   int B, T, Hkv;
 };
 
-constexpr int kAppendWarps = 4, kAppendItems = 4;  // (token, head) pairs per warp
+constexpr int kAppendWarps = 4, kAppendItems = 8;  // (token, head) pairs per warp
 
 // Sequence that holds packed token i, or -1, by a whole warp: each step splits the
 // range that cu bounds in 32.
@@ -80,10 +78,10 @@ __device__ __forceinline__ float reciprocal_approx(float x) {
   return y;
 }
 
-// Scale and codes of a lane's E elements f of a group whose minimum is mn and
-// maximum mx; the codes come packed, element e in bits 4 e.
-template <int E>
-__device__ __forceinline__ uint32_t quantise(const float (&f)[E], float mn, float mx, uint32_t* scale) {
+// Scale and codes of a lane's 16 elements f of a group whose minimum is mn and
+// maximum mx; the codes come packed, element e in bits 4 (e % 8) of word e / 8.
+__device__ __forceinline__ void quantise(const float (&f)[16], float mn, float mx, uint32_t* scale,
+                                         uint32_t (&codes)[2]) {
   const float range = __fsub_rn(mx, mn);
   // far from the ends of fp32's range the divisions are the short ones above
   const bool plain = range >= 0x1p-80f && range <= 0x1p80f;
@@ -91,26 +89,28 @@ __device__ __forceinline__ uint32_t quantise(const float (&f)[E], float mn, floa
       __float2bfloat16_rn(plain ? divide(range, 15.f, 0x1.111112p-4f) : __fdiv_rn(range, 15.f));
   *scale = __bfloat16_as_ushort(sc16);
   const float sc = __bfloat162float(sc16);
-  uint32_t codes = 0;
+  codes[0] = codes[1] = 0;
   if (plain) {
     const float y = reciprocal_approx(sc);
     // adding 1.5 * 2^23 rounds to the nearest integer, ties to even, and leaves it in
     // the low bits; the codes are at most 15 (the scale is at most 2^-9 too small),
     // so the words add up without touching each other but for a constant
-    uint32_t sum = 0, magic = 0;
 #pragma unroll
-    for (int e = E - 1; e >= 0; --e) {
-      const float m = __fadd_rn(divide(__fsub_rn(f[e], mn), sc, y), 12582912.f);
-      sum = sum * 16u + __float_as_uint(m);
-      magic = magic * 16u + 0x4B400000u;
+    for (int z = 0; z < 2; ++z) {
+      uint32_t sum = 0, magic = 0;
+#pragma unroll
+      for (int e = 7; e >= 0; --e) {
+        const float m = __fadd_rn(divide(__fsub_rn(f[8 * z + e], mn), sc, y), 12582912.f);
+        sum = sum * 16u + __float_as_uint(m);
+        magic = magic * 16u + 0x4B400000u;
+      }
+      codes[z] = sum - magic;
     }
-    codes = sum - magic;
   } else if (sc > 0.f) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      codes |= (uint32_t)fminf(rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc)), 15.f) << (4 * e);
+    for (int e = 0; e < 16; ++e)
+      codes[e / 8] |= (uint32_t)fminf(rintf(__fdiv_rn(__fsub_rn(f[e], mn), sc)), 15.f) << (4 * (e % 8));
   }
-  return codes;
 }
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
@@ -122,55 +122,48 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// A lane takes 16 elements, half a group, so that 32 elements share one scale, one
+// shuffle each for minimum and maximum, and four stores; D / 16 lanes hold a vector,
+// and the lanes of a warp 1024 / D vectors at a time: the key and the value of
+// 512 / D (token, head) items.
 template <int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
   using L = C4<D>;
-  constexpr int kE = D / 16;  // elements per lane: 16 lanes hold a vector
-  constexpr int kLanesPerGroup = 32 / kE;
+  constexpr int kLanes = D / 16;          // of a vector
+  constexpr int kAtOnce = 16 / kLanes;    // items: 2 or 4
+  constexpr int kSteps = kAppendItems / kAtOnce;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool is_v = lane >= 16;
-  const int l = lane & 15;
-  const int g = l / kLanesPerGroup, part = l % kLanesPerGroup;
+  const int vec = lane / kLanes, l = lane % kLanes;
+  const bool is_v = vec & 1;
+  const int mine = vec >> 1;  // the lane's item of a step
+  const int g = l >> 1, half = l & 1;
   const uint32_t total = (uint32_t)a.T * a.Hkv;  // below 2^31
   const uint32_t item0 = (blockIdx.x * kAppendWarps + warp) * kAppendItems;
   grid_dep_wait();
   grid_dep_launch();
   if (item0 >= total) return;
   // the vectors first: where they go is found while they are on their way
-  const int tok0 = (int)(item0 / (uint32_t)a.Hkv), h0 = (int)(item0 - (uint32_t)tok0 * a.Hkv);
-  const long long token = is_v ? a.v_token : a.k_token, head = is_v ? a.v_head : a.k_head;
-  const __nv_bfloat16* src = (is_v ? a.v : a.k) + tok0 * token + h0 * head + l * kE;
-  uint32_t x[kAppendItems][kE / 2];
-  // this lane's own item (lanes below kAppendItems), found on the way
-  int tok_n = tok0, h_n = h0;
+  uint4 x[kSteps][2];
 #pragma unroll
-  for (int n = 0, h = h0, tok = tok0; n < kAppendItems; ++n) {
-#pragma unroll
-    for (int e = 0; e < kE / 2; ++e) x[n][e] = 0u;
-    if (lane == n) tok_n = tok, h_n = h;
-    if (item0 + n < total) {
-      if constexpr (kE == 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src);
-        x[n][0] = w.x, x[n][1] = w.y, x[n][2] = w.z, x[n][3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(src);
-        x[n][0] = w.x, x[n][1] = w.y;
-      }
-    }
-    src += head;
-    if (++h == a.Hkv) {
-      h = 0;
-      ++tok;
-      src += token - a.Hkv * head;
-    }
+  for (int n = 0; n < kSteps; ++n) {
+    const uint32_t item = item0 + n * kAtOnce + mine;
+    x[n][0] = x[n][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (item >= total) continue;
+    const uint32_t tok = item / (uint32_t)a.Hkv, h = item - tok * a.Hkv;
+    const __nv_bfloat16* src = (is_v ? a.v + tok * a.v_token + h * a.v_head
+                                     : a.k + tok * a.k_token + h * a.k_head) + l * 16;
+    x[n][0] = reinterpret_cast<const uint4*>(src)[0];
+    x[n][1] = reinterpret_cast<const uint4*>(src)[1];
   }
   // lane n: the byte offset of item n's block, or -1, and its slot there
   long long off_n = -1;
   int slot_n = 0;
   {
+    const int tok0 = (int)(item0 / (uint32_t)a.Hkv);
     const int first = a.cu ? find_sequence(a.cu, a.B, tok0) : tok0;
-    if (lane < kAppendItems && item0 + lane < total) {
-      const int tok = tok_n, h = h_n;
+    const uint32_t item = item0 + lane;
+    if (lane < kAppendItems && item < total) {
+      const int tok = (int)(item / (uint32_t)a.Hkv), h = (int)(item - (uint32_t)tok * a.Hkv);
       int b = a.cu ? first : tok;
       if (a.cu) {
         // later items may belong to later sequences
@@ -194,45 +187,46 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
     }
   }
 #pragma unroll
-  for (int n = 0; n < kAppendItems; ++n) {
-    const long long off = __shfl_sync(0xffffffffu, off_n, n);
-    const int slot = __shfl_sync(0xffffffffu, slot_n, n);
+  for (int n = 0; n < kSteps; ++n) {
+    const long long off = __shfl_sync(0xffffffffu, off_n, n * kAtOnce + mine);
+    const int slot = __shfl_sync(0xffffffffu, slot_n, n * kAtOnce + mine);
+    const uint32_t w[8] = {x[n][0].x, x[n][0].y, x[n][0].z, x[n][0].w,
+                           x[n][1].x, x[n][1].y, x[n][1].z, x[n][1].w};
+    // minimum and maximum two elements at a time, over the group's two lanes, then
+    // of the two
+    uint32_t lo = w[0], hi = w[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+      lo = min2(lo, w[e]);
+      hi = max2(hi, w[e]);
+    }
+    lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    hi = max2(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     if (off < 0) continue;
-    // minimum and maximum two elements at a time, over the group's lanes, then of
-    // the two
-    uint32_t lo = x[n][0], hi = x[n][0];
-#pragma unroll
-    for (int e = 1; e < kE / 2; ++e) {
-      lo = min2(lo, x[n][e]);
-      hi = max2(hi, x[n][e]);
-    }
-#pragma unroll
-    for (int s = 1; s < kLanesPerGroup; s <<= 1) {
-      lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-      hi = max2(hi, __shfl_xor_sync(0xffffffffu, hi, s));
-    }
     const float mn = fminf(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
     const float mx = fmaxf(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
-    float f[kE];
+    float f[16];
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
-      f[e] = (e & 1) ? __uint_as_float(x[n][e / 2] & 0xffff0000u) : __uint_as_float(x[n][e / 2] << 16);
-    uint32_t scale;
-    const uint32_t codes = quantise<kE>(f, mn, mx, &scale);
+    for (int e = 0; e < 16; ++e)
+      f[e] = (e & 1) ? __uint_as_float(w[e / 2] & 0xffff0000u) : __uint_as_float(w[e / 2] << 16);
+    uint32_t scale, codes[2];
+    quantise(f, mn, mx, &scale, codes);
     uint8_t* blk = a.cache + off;
     if (!is_v) {
-      // elements 32 g + kE part ..: word (t, g), t = 8-element piece of the group
-      const int t = part * kE / 8;
-      uint8_t* w = blk + slot * L::kRow + (t * L::kGroups + g) * 4;
-      if constexpr (kE == 8) *reinterpret_cast<uint32_t*>(w) = codes;
-      else *reinterpret_cast<uint16_t*>(w + (part & 1) * 2) = (uint16_t)codes;
+      // elements 32 g + 16 half ..: words t = 2 half and 2 half + 1 of group g
+      uint8_t* p = blk + slot * L::kRow + (2 * half * L::kGroups + g) * 4;
+      *reinterpret_cast<uint32_t*>(p) = codes[0];
+      *reinterpret_cast<uint32_t*>(p + L::kGroups * 4) = codes[1];
     } else {
-      const int i = part * kE / 4;
-      *reinterpret_cast<uint16_t*>(blk + L::v_half(slot, i, g)) = (uint16_t)codes;
-      if constexpr (kE == 8)
-        *reinterpret_cast<uint16_t*>(blk + L::v_half(slot, i + 1, g)) = (uint16_t)(codes >> 16);
+      // half g of chunks i = 4 half .. 4 half + 3
+      uint8_t* p = blk + L::v_half(slot, 4 * half, g);
+      constexpr int kChunk = D / 16;
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)codes[0];
+      *reinterpret_cast<uint16_t*>(p + kChunk) = (uint16_t)(codes[0] >> 16);
+      *reinterpret_cast<uint16_t*>(p + 2 * kChunk) = (uint16_t)codes[1];
+      *reinterpret_cast<uint16_t*>(p + 3 * kChunk) = (uint16_t)(codes[1] >> 16);
     }
-    if (part == 0) {
+    if (half == 0) {
       const uint32_t par = scale | (__float_as_uint(mn) & 0xffff0000u);
       *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kOffVPar : L::kOffKPar) + slot * L::kPar +
                                    g * 4) = par;
