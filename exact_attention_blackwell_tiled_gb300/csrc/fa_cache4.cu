@@ -399,7 +399,6 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const EvictArgs a) {
   float* w_out = a.weights_out + (size_t)bh * a.budget;
   int* src = a.src + (size_t)bh * a.budget;
   const int kept = min(n, a.budget);
-  if (bh - b * a.Hkv == 0 && threadIdx.x == 0) a.lens_out[b] = kept;
   for (int i = kept + threadIdx.x; i < a.budget; i += kRankThreads) {
     src[i] = -1;
     w_out[i] = 0.f;
@@ -525,7 +524,11 @@ __global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
   if (x >= (uint32_t)a.B * a.Hkv * blocks) return;
   const int bh = (int)(x / (uint32_t)blocks), blk = (int)(x - (uint32_t)bh * blocks);
   const int b = bh / a.Hkv, h = bh - b * a.Hkv;
-  const int slots = min(kC4Block, a.lens_out[b] - blk * kC4Block);
+  // lens_out may be lens itself: what is kept of what was kept is the same
+  const long long in_slots = (long long)a.in.width * a.in.blocks_per_page() * kC4Block;
+  const int kept = max(0, min(min(a.lens[b], a.budget), (int)min((long long)a.cap, in_slots)));
+  if (h == 0 && blk == 0 && lane == 0) a.lens_out[b] = kept;
+  const int slots = min(kC4Block, kept - blk * kC4Block);
   if (slots <= 0) return;
   // lane s: the byte offset of slot s's source block and its slot there
   long long from = -1;

@@ -937,6 +937,10 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   if ((long long)B * Hq > (1LL << 30)) return FA_ERR_INVALID_ARG;
   if (weights_out && (long long)B * Hkv * (weight_slots / kWeightKeys + 1) > (1LL << 30))
     return FA_ERR_INVALID_ARG;
+  const int slots = table_width * page_size;
+  // the list of blocks over all rows, and a warp's share of it, are counted in 64 and
+  // 32 bits
+  if ((long long)B * Hq * (slots / kC4Block + 1LL) >= (1LL << 40)) return FA_ERR_INVALID_ARG;
   if (q_batch_stride < 0 || q_head_stride < 0) return FA_ERR_INVALID_ARG;
   if ((q_batch_stride & 7) || (q_head_stride & 7)) return FA_ERR_MISALIGNED;
   if (!q || !cache || !o || !lse || !cache_lens || !page_table) return FA_ERR_INVALID_ARG;
@@ -950,7 +954,6 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
-  const int slots = table_width * page_size;
   AttendArgs a{};
   a.cap = weights_out ? (weight_slots < slots ? weight_slots : slots) : slots;
   const AttendLayout L = attend_layout(B, Hq, Hkv, D, weights_out ? a.cap : 0, info.sm_count);

@@ -189,7 +189,7 @@ constexpr long long kSplitUnits = 608;
 int check_var(int B, int T, int Hq, int Hkv, int D) {
   if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-  if (T > (1 << 30) || B > (1 << 24)) return FA_ERR_INVALID_ARG;
+  if (T > (1 << 30) || B > (1 << 18)) return FA_ERR_INVALID_ARG;  // the plan takes B^2 steps
   // units (item, head) and the packed rows over all heads are counted in 32 bits
   const long long t_pad = ((long long)T + 63) / 64 * 64 + 64LL * B;
   if (t_pad * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;

@@ -112,8 +112,9 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
 
 /*
  * Synchronises `stream`, returns FA_OK or FA_ERR_TIMEOUT if any forward launch on
- * this device since the previous call recorded a timed-out wait, and clears the
- * record.  FA_ERR_CUDA if the synchronisation itself fails.
+ * this device since the previous call recorded a timed-out wait (FA_ERR_INVALID_ARG
+ * if fa_fwd_varlen found its boundaries out of order), and clears the record.
+ * FA_ERR_CUDA if the synchronisation itself fails.
  */
 int fa_fwd_status(fa_stream_t stream);
 
@@ -265,7 +266,7 @@ int fa_lse_merge(const float* o_parts, const float* lse_parts, int n_parts, void
  *     output and records FA_ERR_INVALID_ARG, which fa_fwd_status (forward) or
  *     fa_bwd_status(workspace) (backward) reports.
  * Rows of no sequence (before the first, behind the last) are neither read into
- * any result nor written.  T >= 0 (0 is a no-op), B >= 1, D in {64, 128}; the
+ * any result nor written.  T >= 0 (0 is a no-op), 1 <= B <= 2^18, D in {64, 128}; the
  * rows padded per sequence to 64, times Hq, stay below 2^31.  The bf16 tensors are 16-byte
  * aligned, lse and cu_seqlens 4-byte aligned.
  * workspace: fa_varlen_workspace_bytes(...) bytes of device memory, 256-byte
@@ -310,8 +311,11 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
  * not stored, read as zero, or left out of the attention, nothing out of bounds is
  * touched, and fa_cache4_status returns FA_ERR_INVALID_ARG.
  * cache_lens: device int32 [B], the tokens each sequence holds (0 allowed).
- * Lengths and tables are read on the device, so captured calls replay on new ones.
- * B * Hkv, and a sequence's slots, are at most 2^30; D in {64, 128}.
+ * Lengths and tables are read on the device, so captured calls replay on new ones
+ * (the first call of each kind on a device looks up symbols and sets attributes: make
+ * it before a capture).  B * Hkv, and a sequence's slots, are at most 2^30, the tokens
+ * times heads of an append and the 16-slot blocks of a read or eviction below 2^31;
+ * D in {64, 128}.
  */
 size_t fa_cache4_page_bytes(int Hkv, int D, int page_size); /* 0 on bad sizes */
 
@@ -367,7 +371,7 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
  * with at most `budget` tokens keeps all.
  *   src [B, Hkv, budget] int32: the old slot of each kept token, -1 behind the last;
  *   weights_out [B, Hkv, budget] fp32: their weights, 0 behind the last;
- *   lens_out [B] int32: min(cache_lens[b], budget).
+ *   lens_out [B] int32: min(cache_lens[b], budget); it may be cache_lens itself.
  * 0 <= recent <= budget, budget >= 1 and at most the slots of out_page_table.
  */
 int fa_cache4_evict(void* cache, int num_pages, int page_size, const float* weights, int cap,

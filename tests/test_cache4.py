@@ -68,8 +68,8 @@ def test_read_refusals(L):
 def test_attend_refusals(L):
     def call(q=P, qb=512, qh=128, o=P, B=2, Hq=4, Hkv=2, D=128, page=64, lens=P, scale=0.1,
              w_in=None, w_out=None, slots=0, ws=P, wsb=1 << 40):
-        return L.fa_cache4_attend(q, qb, qh, P, 4, page, o, P, B, Hq, Hkv, D, lens, P, 2, scale,
-                                  w_in, w_out, slots, ws, wsb, None)
+        return L.fa_cache4_attend(q, qb, qh, P, 4, page, o, P, B, Hq, Hkv, D, lens, P,
+                                  2 if B < 9 else 1 << 20, scale, w_in, w_out, slots, ws, wsb, None)
     assert call(q=None) == 1
     assert call(o=None) == 1
     assert call(Hq=3) == 1
@@ -84,6 +84,7 @@ def test_attend_refusals(L):
     assert call(w_out=P2, slots=4) == 3
     assert call(ws=None) == 4
     assert call(ws=P4) == 4
+    assert call(B=1 << 20, Hq=1 << 10, Hkv=1 << 10, page=128) == 1  # a list past 2^40 blocks
 
 
 def test_evict_refusals(L):
@@ -282,9 +283,9 @@ def test_attend_repeats_to_the_bit_and_takes_strides(gpu):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lens,budget,recent", [
     ([50, 7, 300], 40, 10), ([33], 32, 0), ([100, 64, 65], 64, 64), ([2500, 1, 0], 999, 17),
-    ([40], 1, 0), ([40], 1, 1), ([5000], 17, 5)])
+    ([40], 1, 0), ([40], 1, 1), ([5000], 17, 5), ([17000, 16384], 4099, 100)])
 def test_evict(gpu, D, lens, budget, recent):
-    Hkv, page = 2, 16
+    Hkv, page = 2, (16 if max(lens) < 6000 else 128)
     cache, table, n, cu, k, v = _filled(lens, Hkv, D, page)
     gen = torch.Generator().manual_seed(budget)
     slots = max(lens) + 3
@@ -310,6 +311,10 @@ def test_evict(gpu, D, lens, budget, recent):
             assert bool((w_out[b, h, len(want):] == 0).all())
             for a, c in zip(old, new):
                 assert torch.equal(c[b, h, : len(want)], a[b, h, want])
+    # the lengths updated in place
+    src2, w2, n2 = fa.cache4_evict(big, table, n, w.cuda(), extra, D, budget, recent, lens_out=n)
+    assert n2 is n and n.tolist() == kept
+    assert torch.equal(src2, src) and torch.equal(w2, w_out)
 
 
 @pytest.mark.gpu

@@ -49,6 +49,7 @@ def test_forward_refusals(L):
     assert _fwd(L, wsb=L.fa_varlen_workspace_bytes(2, 8, 2, 2, 64, 0, 0) - 1) == 4
     assert _fwd(L, T=0, q=None, cu=None, ws=None) == 0
     assert _fwd(L, T=1 << 30, Hq=2) == 1  # rows over all heads pass 32 bits
+    assert _fwd(L, B=(1 << 18) + 1) == 1  # more sequences than a plan is made for
 
 
 def test_backward_refusals(L):
@@ -329,10 +330,12 @@ def test_captured_and_on_another_stream(gpu):
 
 
 @pytest.mark.gpu
-def test_many_sequences_and_grouped_heads(gpu):
-    """More sequences than SMs, one kv head for eight query heads, sampled."""
+@pytest.mark.parametrize("count", [400, 4500])
+def test_many_sequences_and_grouped_heads(gpu, count):
+    """More sequences than SMs, or than the plan keeps lengths of, one kv head for
+    eight query heads, sampled."""
     gen = torch.Generator().manual_seed(8)
-    lens = torch.randint(0, 40, (400,), generator=gen).tolist() + [1500]
+    lens = torch.randint(0, 40 if count < 1000 else 5, (count,), generator=gen).tolist() + [1500]
     cu = _cu(lens)
     q, k, v, do = _inputs(cu[-1], 8, 1, 128, 12)
     cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
