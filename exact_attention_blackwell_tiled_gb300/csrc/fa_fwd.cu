@@ -139,8 +139,7 @@ __global__ void __launch_bounds__(320, 1)
   const int n_units = kVar ? *a.n_items * a.Hq : a.n_units;
   constexpr bool kWin = kMod >= 1, kBias = kMod == 2;
   // packed calls keep every exponential on MUFU: the cubic's 7.5e-5 would be
-  // the largest error of their LSE by two orders of magnitude, for the 1-2% of
-  // the time that it saves at D = 64
+  // the largest error of their LSE by two orders of magnitude
   constexpr int kPoly = kVar ? 0 : L::kPolyPairs;
   // the window; plain calls carry only the causal flag
   const int wl = kWin ? a.wl : -1;
@@ -748,7 +747,10 @@ static int launch_fwd_var_d(const CUtensorMap& any, FwdArgs a, int max_items, cu
   const bool plain = a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal));
   const auto kernel = plain ? fwd_kernel<D, 0, false, true> : fwd_kernel<D, 1, false, true>;
   record_timing(false, stream);
-  if (launch_pdl(kernel, dim3(grid), dim3(320), L::kAllocBytes, stream, any, any, any, a) !=
+  // D = 64 without a window: the ring of score buffers, as in the dense call
+  if (fwd_ring64_eligible(a, D, plain ? 0 : 1)) {
+    if (launch_fwd_ring64(any, any, any, a, grid, stream) != FA_OK) return FA_ERR_CUDA;
+  } else if (launch_pdl(kernel, dim3(grid), dim3(320), L::kAllocBytes, stream, any, any, any, a) !=
       cudaSuccess)
     return FA_ERR_CUDA;
   record_timing(true, stream);

@@ -99,6 +99,9 @@ static_assert(RingLayout::kRing * 64 + RingLayout::D <= (int)RingLayout::kColsPe
 
 constexpr int kRingThreads = 416;  // 8 softmax warps, the producer, four issuers
 
+// kVar: a packed batch, as in fwd_kernel (tensor maps per sequence, every
+// exponential on MUFU).
+template <bool kVar>
 __global__ void __launch_bounds__(kRingThreads, 1)
     fwd_ring64_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (!kVar && warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -158,6 +161,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
   const int wr = a.causal ? 0 : -1;
+  const int n_units = kVar ? *a.n_items * a.Hq : a.n_units;
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
@@ -166,6 +170,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     // half K tiles, ahead of GEMM 2).
     if (lane == 0) {
       uint32_t k_it = 0, v_it = 0, q_it = 0;
+      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
+      const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v;
       bool ok = true;
       auto load = [&](bool is_v, int bhk, int j) -> bool {
         uint32_t& it = is_v ? v_it : k_it;
@@ -176,18 +182,28 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         if (!mbar_wait(empty, ((it / n) & 1) ^ 1, abort_flag)) return false;
         mbar_arrive_expect_tx(full, L::kTileBytes);
         tma_load_3d(sbase + (is_v ? L::kOffV : L::kOffK) + st * L::kTileBytes,
-                    is_v ? &tm_v : &tm_k, full, 0, j * kTile, bhk);
+                    is_v ? mv : mk, full, 0, j * kTile, bhk);
         ++it;
         return true;
       };
-      for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
-        int bh, pair, split;
-        unit_coords(a, u, bh, pair, split);
-        const int b = bh / a.Hq, h = bh - b * a.Hq;
-        const int bhk = b * a.Hkv + h / group;
+      for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<false>(a, a.Sq, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
+        pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
+                            nmax);
         if (nmax == 0) continue;
+        if constexpr (kVar) {
+          mq = a.maps + 3 * (size_t)w.b;
+          mk = mq + 1;
+          mv = mq + 2;
+          if (w.b != last_b) {  // the plan kernel wrote these maps
+            tmap_acquire(mq);
+            tmap_acquire(mk);
+            tmap_acquire(mv);
+            last_b = w.b;
+          }
+        }
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
           ok = false;
@@ -197,8 +213,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         const uint32_t qdst = sbase + L::kOffQ + qs * 2 * L::kTileBytes;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          tma_load_3d(qdst + t * L::kTileBytes, &tm_q, bar(L::kBarQFull + qs), 0,
-                      (2 * pair + t) * kTile, bh);
+          tma_load_3d(qdst + t * L::kTileBytes, mq, bar(L::kBarQFull + qs), 0,
+                      (2 * w.pair + t) * kTile, w.bh);
         ++q_it;
         ok = load(false, bhk, jlo) && (nmax < 2 || load(false, bhk, jlo + 1));
         for (int i = 0; ok && i < nmax; ++i)
@@ -224,11 +240,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       uint32_t k_it = 0, q_it = 0;
       uint32_t gs = 0;  // score halves issued for this tile (all units)
       bool ok = true;
-      for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
-        int bh, pair, split;
-        unit_coords(a, u, bh, pair, split);
+      for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+        const FwdUnit w = fwd_unit<kVar>(a, u);
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<false>(a, a.Sq, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
+        pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
+                            nmax);
         if (nmax == 0) continue;
         // both tiles start at kv tile jlo (no left window); this one reaches m
         // of the unit's nmax kv tiles
@@ -313,11 +329,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       uint32_t go = 0;     // P halves consumed for this tile (all units)
       uint32_t units = 0;  // units in which this tile had keys (O-free phases)
       bool ok = true;
-      for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
-        int bh, pair, split;
-        unit_coords(a, u, bh, pair, split);
+      for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+        const FwdUnit w = fwd_unit<kVar>(a, u);
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<false>(a, a.Sq, -1, wr, a.Sk, pair, 0, lo, hi, jlo, nmax);
+        pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
+                            nmax);
         if (nmax == 0) continue;
         const int m = hi[t] - lo[t], n = 2 * m;
         const uint32_t vbase = v_it;  // ring position of V_jlo
@@ -363,15 +379,14 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     bool ok = true;
     const float c = a.scale_log2;  // > 0 for this kernel
     const float2 c2 = make_float2(c, c);
-    for (int ri = 0, u = cta_unit(a, a.n_units, 0); ok && u >= 0; u = cta_unit(a, a.n_units, ++ri)) {
-      int bh, pair, split;
-      unit_coords(a, u, bh, pair, split);
-      const int qt = 2 * pair + t;
+    for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
+      const FwdUnit w = fwd_unit<kVar>(a, u);
+      const int qt = 2 * w.pair + t, Sq = w.Sq, kv_len = unit_kv_len<false, kVar>(a, w);
       int jlo, jhi;
-      split_kv_range<false>(a, a.Sq, -1, wr, a.Sk, qt, 0, jlo, jhi);
+      split_kv_range<false>(a, Sq, -1, wr, kv_len, qt, 0, jlo, jhi);
       if (jhi == jlo) continue;  // a tile past the last query row
       const int q_row = qt * kTile + r;
-      const int lim = wr >= 0 ? min(a.Sk, q_row + 1) : a.Sk;  // keys [0, lim) visible
+      const int lim = wr >= 0 ? min(kv_len, q_row + 1) : kv_len;  // keys [0, lim) visible
       const int n = 2 * (jhi - jlo);
       float m_run = -INFINITY, l_run = 0.f;
       for (int k = 0; k < n; ++k) {
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         for (int i = 0; i < 32; ++i) {
           const float2 tt = __ffma2_rn(make_float2(u2f(v[2 * i]), u2f(v[2 * i + 1])), c2, nm2);
           float p0, p1;
-          if ((i & 7) < L::kPolyPairs) {
+          if ((i & 7) < (kVar ? 0 : L::kPolyPairs)) {
             const float2 pp = ex2_poly2(tt);
             p0 = pp.x, p1 = pp.y;
           } else {
@@ -464,28 +479,30 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         break;
       }
       tc_fence_after();
-      const bool row_ok = q_row < a.Sq;
+      const bool row_ok = q_row < Sq;
       const float inv_l = 1.0f / l_run;
+      const size_t o_off = kVar ? ((size_t)w.row0 * a.Hq + w.h) * D : (size_t)w.bh * Sq * D;
+      const size_t o_row = kVar ? (size_t)a.Hq * D : (size_t)D;
       __nv_bfloat16* orow =
-          reinterpret_cast<__nv_bfloat16*>(a.o) + ((size_t)bh * a.Sq + (row_ok ? q_row : 0)) * D;
+          reinterpret_cast<__nv_bfloat16*>(a.o) + o_off + (row_ok ? q_row : 0) * o_row;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
         __syncwarp();  // reconverge after the per-row store before the warp-wide load
         tmem_ld32(t_row + L::kColO + cc * 32, o);
-        uint32_t w[16];
+        uint32_t y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = pack_bf16x2(u2f(o[2 * i]) * inv_l, u2f(o[2 * i + 1]) * inv_l);
+          y[i] = pack_bf16x2(u2f(o[2 * i]) * inv_l, u2f(o[2 * i + 1]) * inv_l);
         if (row_ok) {
           uint4* dst = reinterpret_cast<uint4*>(orow + cc * 32);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            dst[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
       }
       if (row_ok)
-        a.lse[(size_t)bh * a.Sq + q_row] = (m_run + __log2f(l_run)) * 0.69314718055994531f;
+        a.lse[(kVar ? (size_t)w.h * a.T + w.row0 : (size_t)w.bh * Sq) + q_row] = (m_run + __log2f(l_run)) * 0.69314718055994531f;
       tc_fence_before();
       mbar_arrive(bar(L::kBarOFree + t));
     }
@@ -514,13 +531,17 @@ int launch_fwd_ring64(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(fwd_ring64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::kAllocBytes) != cudaSuccess)
-      return FA_ERR_CUDA;
+    const void* kernels[] = {(const void*)fwd_ring64_kernel<false>,
+                             (const void*)fwd_ring64_kernel<true>};
+    for (const void* k : kernels)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAllocBytes) !=
+          cudaSuccess)
+        return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  if (launch_pdl(fwd_ring64_kernel, dim3(grid), dim3(kRingThreads), L::kAllocBytes, stream, tq,
-                 tk, tv, a) != cudaSuccess)
+  const auto kernel = a.items ? fwd_ring64_kernel<true> : fwd_ring64_kernel<false>;
+  if (launch_pdl(kernel, dim3(grid), dim3(kRingThreads), L::kAllocBytes, stream, tq, tk, tv, a) !=
+      cudaSuccess)
     return FA_ERR_CUDA;
   return FA_OK;
 }
