@@ -181,7 +181,7 @@ struct BwdUnit {
   int bhk, j, b, hk, lo, n_blk, n_it;
   int kv_len;  // keys of batch b
   // packed calls: the sequence's first row, and its first row where each one
-  // is padded to 64; its queries and keys are kv_len, bhk is the kv head
+  // is padded to a query block; its queries and keys are kv_len, bhk is the kv head
   int row0, pad0;
   int gi0;  // the unit's q head of the group where the heads are split, else 0
 };
@@ -267,6 +267,68 @@ __device__ __forceinline__ BwdUnit bwd_unit_var(const BwdArgs& a, int u, int gro
   w.n_blk = hi - w.lo;
   w.n_it = split ? w.n_blk : group * w.n_blk;
   return w;
+}
+
+// The number of units, and unit u, of a call that may be a packed one (n_items: its
+// items).
+template <bool kVar>
+__device__ __forceinline__ int bwd_unit_count(const BwdArgs& a, int n_items) {
+  return kVar ? n_items * (a.dk_part ? a.Hq : a.Hkv) : a.n_units;
+}
+template <bool kMod, bool kVar, int QB>
+__device__ __forceinline__ BwdUnit bwd_any_unit(const BwdArgs& a, int u, int group, int n_items) {
+  if constexpr (kVar) return bwd_unit_var<kMod, QB>(a, u, group, n_items);
+  else return bwd_unit<kMod, QB>(a, u, group);
+}
+
+// The q head of the tensor maps' head coordinate (flat over the batch in dense
+// calls), and the places of its query block iq in lse2 / delta, in a dQ accumulator
+// and among a group's semaphores.
+template <bool kVar>
+__device__ __forceinline__ int bwd_head(const BwdArgs& a, const BwdUnit& w, int group, int gi) {
+  return (kVar ? w.gi0 : w.b * a.Hq) + w.hk * group + gi;
+}
+template <bool kVar, int QB>
+__device__ __forceinline__ size_t bwd_vec_off(const BwdArgs& a, const BwdUnit& w, int bh, int iq) {
+  return kVar ? (size_t)bh * a.T_pad + w.pad0 + (size_t)iq * QB
+              : (size_t)bh * a.Sq_pad + (size_t)iq * QB;
+}
+template <bool kVar, int QB, int D>
+__device__ __forceinline__ size_t bwd_acc_off(const BwdArgs& a, const BwdUnit& w, int bh, int iq) {
+  return (kVar ? (size_t)bh * a.T + w.row0 + (size_t)iq * QB
+               : (size_t)bh * a.Sq_pad + (size_t)iq * QB) * D;
+}
+template <bool kVar, int QB>
+__device__ __forceinline__ size_t bwd_sem_off(const BwdArgs& a, const BwdUnit& w, int bh, int iq) {
+  return (size_t)bh * a.n_qblk + (kVar ? w.pad0 / QB : 0) + iq;
+}
+
+// 32 columns (32 c ..) of dK or dV for the unit's q head as an fp32 part, times sc: the
+// lanes of a group of four, which hold rows row0 .. row0 + 3, trade 16-byte pieces.
+__device__ __forceinline__ void bwd_store_part(const BwdArgs& a, const BwdUnit& w, int group,
+                                               bool is_v, int c, int D, const uint32_t (&vk)[32],
+                                               float sc, int row0, int Sk, int lane) {
+  const int pc = lane & 3;
+  float* base =
+      (is_v ? a.dv_part : a.dk_part) + ((size_t)(w.hk * group + w.gi0) * a.T + w.row0) * D;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t y[16];
+#pragma unroll
+    for (int wd = 0; wd < 4; ++wd) {
+      uint32_t x[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) x[m] = __float_as_uint(u2f(vk[16 * hf + 4 * m + wd]) * sc);
+      xpose4(x, lane);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[4 * m + wd] = x[m];
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      if (row0 + m < Sk)
+        *reinterpret_cast<uint4*>(base + (size_t)(row0 + m) * D + c * 32 + (4 * hf + pc) * 4) =
+            make_uint4(y[4 * m], y[4 * m + 1], y[4 * m + 2], y[4 * m + 3]);
+  }
 }
 
 // Pair unit u of a cluster of two CTAs: (batch, kv head, kv tiles 2p and 2p+1);

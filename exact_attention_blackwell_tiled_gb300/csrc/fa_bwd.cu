@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess(const BwdArgs a) {
 
 // The same for a packed batch: a block takes (kv-tile item, q head) pairs of the
 // plan, whose 128 rows are also a tile of the sequence's queries.  Rows up to the
-// next multiple of 64 get LSE2 = +inf and Delta = 0.
+// next multiple of the main kernel's block get LSE2 = +inf and Delta = 0.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a) {
   grid_dep_wait();
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a) {
     const VarItem it = load_item(a.items, item);
     const int pad0 = a.items[item].pad0;
     const int i0 = it.tile * kTile;
-    const int i1 = min(i0 + kTile, (it.len + kQB - 1) / kQB * kQB);
+    const int i1 = min(i0 + kTile, (it.len + a.qblk_rows - 1) / a.qblk_rows * a.qblk_rows);
     // kTile / 8 = 16 rows per warp, kPreUnroll steps of them in flight
 #pragma unroll 1
     for (int s0 = 0; s0 < kTile / 8; s0 += kRowsPerStep * kPreUnroll) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
   const int n_items = kVar ? *a.n_items : 0;
-  const int n_units = kVar ? n_items * (a.dk_part ? a.Hq : a.Hkv) : a.n_units;
+  const int n_units = bwd_unit_count<kVar>(a, n_items);
   // The r-th unit of this CTA.  Static dealing: computed by every role alike.
   // Dynamic dealing: the TMA thread takes the next unit number from the global
   // counter and posts it in ring slot r % kURing (take_unit); the other roles
@@ -425,26 +425,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     if (!warp_wide || lane == 0) mbar_arrive(bar(L::kBarUEmpty + s));
     return u;
   };
-  auto unit_of = [&](int u) {
-    if constexpr (kVar) return bwd_unit_var<kMod, kQB>(a, u, group, n_items);
-    else return bwd_unit<kMod, kQB>(a, u, group);
-  };
-  // the q head of the tensor maps' head coordinate, and (bh, block iq)'s places
-  // in lse2 / delta, in the dQ accumulators and among the semaphores
-  auto head_of = [&](const BwdUnit& w, int gi) {
-    return (kVar ? w.gi0 : w.b * a.Hq) + w.hk * group + gi;
-  };
-  auto vec_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
-    return kVar ? (size_t)bh * a.T_pad + w.pad0 + (size_t)iq * kQB
-                : (size_t)bh * a.Sq_pad + (size_t)iq * kQB;
-  };
-  auto acc_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
-    return (kVar ? (size_t)bh * a.T + w.row0 + (size_t)iq * kQB
-                 : (size_t)bh * a.Sq_pad + (size_t)iq * kQB) * D;
-  };
-  auto sem_off = [&](const BwdUnit& w, int bh, int iq) -> size_t {
-    return (size_t)bh * a.n_qblk + (kVar ? w.pad0 / kQB : 0) + iq;
-  };
+  auto unit_of = [&](int u) { return bwd_any_unit<kMod, kVar, kQB>(a, u, group, n_items); };
+  auto head_of = [&](const BwdUnit& w, int gi) { return bwd_head<kVar>(a, w, group, gi); };
 
   if (warp == R::kTmaWarp) {
     // ------------------------------------------------------------ TMA producer
@@ -504,7 +486,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
             tma_load_3d(sdst + L::kQTileBytes + cb * L::kQBlockBytes, mdo,
                         bar(L::kBarQFull + st), cb * 64, iq * kQB, bh);
           }
-          const size_t voff = vec_off(w, bh, iq);
+          const size_t voff = bwd_vec_off<kVar, kQB>(a, w, bh, iq);
           bulk_load(sdst + 2 * L::kQTileBytes, a.lse2 + voff, kQB * 4, bar(L::kBarQFull + st));
           bulk_load(sdst + 2 * L::kQTileBytes + kQB * 4, a.delta + voff, kQB * 4,
                     bar(L::kBarQFull + st));
@@ -856,7 +838,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
               } else {
                 mbar_arrive(bar(L::kBarDQAddedFree));
                 int* sem = a.sem + (size_t)(w.j % a.dq_groups) * a.sem_group_stride +
-                           sem_off(w, bh, iq);
+                           bwd_sem_off<kVar, kQB>(a, w, bh, iq);
                 asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(sem) : "memory");
               }
             }
@@ -876,7 +858,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
         if (!a.deterministic) {
           // two 32-column halves, so that only 32 values are live at a time;
           // the columns are released once the second half is read
-          float* dst = a.dq_acc + acc_off(w, bh, iq) + r;
+          float* dst = a.dq_acc + bwd_acc_off<kVar, kQB, D>(a, w, bh, iq) + r;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t v[32];
@@ -927,8 +909,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
                         w.j) / a.dq_groups
                      : (w.j - group_first(qblk_first_contributor<kQB>(win_left<kMod>(a), iq), g,
                                           a.dq_groups)) / a.dq_groups;
-          float* dst = a.dq_acc + (size_t)g * a.dq_group_stride + acc_off(w, bh, iq) + r;
-          int* sem = a.sem + (size_t)g * a.sem_group_stride + sem_off(w, bh, iq);
+          float* dst = a.dq_acc + (size_t)g * a.dq_group_stride + bwd_acc_off<kVar, kQB, D>(a, w, bh, iq) + r;
+          int* sem = a.sem + (size_t)g * a.sem_group_stride + bwd_sem_off<kVar, kQB>(a, w, bh, iq);
           if (wq < kAddWarps && turn > 0) {
             // the semaphore counts the group's finished adding warps (with
             // the semaphore warp: the group's finished tiles)
@@ -1022,28 +1004,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
         }
         const float sc = is_v ? 1.f : a.scale;
         if (kVar && a.dk_part) {
-          // this q head's fp32 part; the lanes trade 16-byte pieces as below
-          float* base = (is_v ? a.dv_part : a.dk_part) +
-                        ((size_t)(w.hk * group + w.gi0) * a.T + w.row0) * D;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t y[16];
-#pragma unroll
-            for (int wd = 0; wd < 4; ++wd) {
-              uint32_t x[4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-                x[m] = __float_as_uint(u2f(vk[16 * hf + 4 * m + wd]) * sc);
-              xpose4(x, lane);
-#pragma unroll
-              for (int m = 0; m < 4; ++m) y[4 * m + wd] = x[m];
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              if (row0 + m < Sk)
-                *reinterpret_cast<uint4*>(base + (size_t)(row0 + m) * D + c * 32 + (4 * hf + pc) * 4) =
-                    make_uint4(y[4 * m], y[4 * m + 1], y[4 * m + 2], y[4 * m + 3]);
-          }
+          bwd_store_part(a, w, group, is_v, c, D, vk, sc, row0, Sk, lane);
           continue;
         }
         uint32_t wk[16];
@@ -1141,7 +1102,7 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
         x1 = reinterpret_cast<const float4*>(base)[1];
       } else {
         // in fixed order, the groups that some kv tile wrote for this block
-        const int* sem = a.sem + (size_t)h * a.n_qblk + (pad0 + i) / kQB;
+        const int* sem = a.sem + (size_t)h * a.n_qblk + (pad0 + i) / a.qblk_rows;
         for (int g = 0; g < a.dq_groups; ++g) {
           if (sem[(size_t)g * a.sem_group_stride] == 0) continue;
           const float4* src = reinterpret_cast<const float4*>(base + (size_t)g * a.dq_group_stride);
@@ -1331,7 +1292,10 @@ static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
   const auto kernel = mod ? bwd_main<D, true, true> : bwd_main<D, false, true>;
   const int threads = (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
   record_timing(false, stream);
-  if (a.deterministic) {
+  if (a.qblk_rows == 128) {
+    const int rc = launch_bwd_main_q128(any, any, any, any, a, mod, grid, stream);
+    if (rc != FA_OK) return rc;
+  } else if (a.deterministic) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);

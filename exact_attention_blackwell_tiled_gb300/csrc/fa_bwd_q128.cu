@@ -133,7 +133,8 @@ static_assert(Q128Layout::kBytes <= kQ128MaxSmem, "q128 backward layout exceeds 
 
 }  // namespace
 
-template <bool kMod>
+// kVar: a packed batch, as in bwd_main.
+template <bool kMod, bool kVar>
 __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     bwd_main_q128(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v,
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == L::kTmaWarp && lane == 0) {
+  if (!kVar && warp == L::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -207,6 +208,8 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
+  const int n_items = kVar ? *a.n_items : 0;
+  const int n_units = bwd_unit_count<kVar>(a, n_items);
   // The r-th unit of this CTA: static dealing computes it in every role;
   // dynamic dealing has the TMA thread take the next number from the global
   // counter and post it in ring slot r % kURing, where the other roles read it.
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     const int s = r % L::kURing;
     if (!mbar_wait(bar(L::kBarUEmpty + s), ((r / L::kURing) & 1) ^ 1, abort_flag)) return -1;
     int u = atomicAdd(a.unit_counter, 1);
-    if (u >= a.n_units) u = -1;
+    if (u >= n_units) u = -1;
     uring[s] = u;
     mbar_arrive(bar(L::kBarUFull + s));
     return u;
@@ -251,21 +254,33 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0, unit = 0;
+      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
+      const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v, *mdo = &tm_do;
       bool ok = true;
       auto load_kv = [&](const BwdUnit& w, uint32_t un) -> bool {
         if (!mbar_wait(bar(L::kBarKVEmpty), (un & 1) ^ 1, abort_flag)) return false;
         mbar_arrive_expect_tx(bar(L::kBarKVFull), 2 * L::kTileBytes);
 #pragma unroll
         for (int cb = 0; cb < 2; ++cb) {
-          tma_load_3d(sbase + L::kOffK + cb * L::kBlockBytes, &tm_k, bar(L::kBarKVFull), cb * 64,
+          tma_load_3d(sbase + L::kOffK + cb * L::kBlockBytes, mk, bar(L::kBarKVFull), cb * 64,
                       w.j * kTile, w.bhk);
-          tma_load_3d(sbase + L::kOffV + cb * L::kBlockBytes, &tm_v, bar(L::kBarKVFull), cb * 64,
+          tma_load_3d(sbase + L::kOffV + cb * L::kBlockBytes, mv, bar(L::kBarKVFull), cb * 64,
                       w.j * kTile, w.bhk);
         }
         return true;
       };
       for (int ri = 0, u = take_unit(0); ok && u >= 0; u = take_unit(++ri), ++unit) {
-        const BwdUnit w = bwd_unit<kMod, kQB2>(a, u, group);
+        const BwdUnit w = bwd_any_unit<kMod, kVar, kQB2>(a, u, group, n_items);
+        if constexpr (kVar) {
+          mq = a.maps + 4 * (size_t)w.b;
+          mk = mq + 1;
+          mv = mq + 2;
+          mdo = mq + 3;
+          if (w.b != last_b) {  // the plan kernel wrote these maps
+            for (int i = 0; i < 4; ++i) tmap_acquire(mq + i);
+            last_b = w.b;
+          }
+        }
         // the unit's first block's Q / dO go out before its K / V: that stage
         // frees while the previous unit still holds K and V
         const int early = w.n_it < 1 ? w.n_it : 1;
@@ -275,7 +290,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           }
           const int gi = t / w.n_blk;
           const int iq = w.lo + (t - gi * w.n_blk);
-          const int bh = w.b * a.Hq + w.hk * group + gi;
+          const int bh = bwd_head<kVar>(a, w, group, gi);
           const uint32_t st = it % L::kStages;
           if (!mbar_wait(bar(L::kBarQEmpty + st), ((it / L::kStages) & 1) ^ 1, abort_flag)) {
             ok = false;
@@ -285,12 +300,12 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           mbar_arrive_expect_tx(bar(L::kBarQFull + st), 2 * L::kTileBytes + 2 * L::kVecBytes);
 #pragma unroll
           for (int cb = 0; cb < 2; ++cb) {
-            tma_load_3d(sdst + cb * L::kBlockBytes, &tm_q, bar(L::kBarQFull + st), cb * 64,
+            tma_load_3d(sdst + cb * L::kBlockBytes, mq, bar(L::kBarQFull + st), cb * 64,
                         iq * kQB2, bh);
-            tma_load_3d(sdst + L::kTileBytes + cb * L::kBlockBytes, &tm_do,
+            tma_load_3d(sdst + L::kTileBytes + cb * L::kBlockBytes, mdo,
                         bar(L::kBarQFull + st), cb * 64, iq * kQB2, bh);
           }
-          const size_t voff = (size_t)bh * a.Sq_pad + (size_t)iq * kQB2;
+          const size_t voff = bwd_vec_off<kVar, kQB2>(a, w, bh, iq);
           bulk_load(sdst + 2 * L::kTileBytes, a.lse2 + voff, L::kVecBytes,
                       bar(L::kBarQFull + st));
           bulk_load(sdst + 2 * L::kTileBytes + L::kVecBytes, a.delta + voff, L::kVecBytes,
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
       uint32_t it = 0, unit = 0;
       bool ok = true;
       for (int ri = 0, u = read_unit(0, false); ok && u >= 0; u = read_unit(++ri, false), ++unit) {
-        const BwdUnit w = bwd_unit<kMod, kQB2>(a, u, group);
+        const BwdUnit w = bwd_any_unit<kMod, kVar, kQB2>(a, u, group, n_items);
         if (!mbar_wait(bar(L::kBarKVFull), unit & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (!grad) {
@@ -446,18 +461,18 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int ri = 0, u = read_unit(0, false); ok && u >= 0; u = read_unit(++ri, false)) {
-        const BwdUnit w = bwd_unit<kMod, kQB2>(a, u, group);
+        const BwdUnit w = bwd_any_unit<kMod, kVar, kQB2>(a, u, group, n_items);
         const int g = w.j % a.dq_groups;
         for (int t = 0; t < w.n_it; ++t, ++it) {
           const int gi = t / w.n_blk;
           const int iq = w.lo + (t - gi * w.n_blk);
-          const int bh = w.b * a.Hq + w.hk * group + gi;
+          const int bh = bwd_head<kVar>(a, w, group, gi);
           if (!mbar_wait(bar(L::kBarDQAdded), it & 1, abort_flag)) {
             ok = false;
             break;
           }
           mbar_arrive(bar(L::kBarDQAddedFree));
-          int* sem = a.sem + (size_t)g * a.sem_group_stride + (size_t)bh * a.n_qblk + iq;
+          int* sem = a.sem + (size_t)g * a.sem_group_stride + bwd_sem_off<kVar, kQB2>(a, w, bh, iq);
           asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(sem) : "memory");
         }
       }
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int ri = 0, u = read_unit(0, true); ok && u >= 0; u = read_unit(++ri, true)) {
-      const BwdUnit w = bwd_unit<kMod, kQB2>(a, u, group);
+      const BwdUnit w = bwd_any_unit<kMod, kVar, kQB2>(a, u, group, n_items);
       const int kv = w.j * kTile + r;
       const bool row_dead = kv >= w.kv_len;
       for (int t = 0; t < w.n_it; ++t, ++it) {
@@ -616,11 +631,11 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
       return true;
     };
     for (int ri = 0, u = read_unit(0, true); ok && u >= 0; u = read_unit(++ri, true), ++unit) {
-      const BwdUnit w = bwd_unit<kMod, kQB2>(a, u, group);
+      const BwdUnit w = bwd_any_unit<kMod, kVar, kQB2>(a, u, group, n_items);
       for (int t = 0; t < w.n_it; ++t, ++it) {
         const int gi = t / w.n_blk;
         const int iq = w.lo + (t - gi * w.n_blk);
-        const int bh = w.b * a.Hq + w.hk * group + gi;
+        const int bh = bwd_head<kVar>(a, w, group, gi);
         ok = warp_wait_b(bar(L::kBarDQFull), it & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -648,7 +663,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
                         w.j) / a.dq_groups
                      : (w.j - group_first(qblk_first_contributor<kQB2>(win_left<kMod>(a), iq), g,
                                           a.dq_groups)) / a.dq_groups;
-          sem = a.sem + (size_t)g * a.sem_group_stride + (size_t)bh * a.n_qblk + iq;
+          sem = a.sem + (size_t)g * a.sem_group_stride + bwd_sem_off<kVar, kQB2>(a, w, bh, iq);
           if (good && turn > 0) {
             // the semaphore counts the group's tiles whose adds are done
             if (lane == 0) {
@@ -665,18 +680,27 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
             __syncwarp();
           }
         }
-        float* dst = a.dq_acc + (size_t)g * a.dq_group_stride +
-                     ((size_t)bh * a.Sq_pad + (size_t)iq * kQB2) * D + r;
+        float* dst = a.dq_acc + (size_t)g * a.dq_group_stride + bwd_acc_off<kVar, kQB2, D>(a, w, bh, iq) + r;
+        // query rows of the block that exist (kVar)
+        const int n_rows = kVar ? w.kv_len - iq * kQB2 : kQB2;
         if (good) {
           if (a.deterministic && turn == 0) {
 #pragma unroll
-            for (int e = 0; e < kQB2; ++e) dst[(size_t)e * D] = u2f(v[e]);
-          } else {
+            for (int e = 0; e < kQB2; ++e)
+              if (!kVar || e < n_rows) dst[(size_t)e * D] = u2f(v[e]);
+          } else if (!kVar || n_rows >= kQB2) {
 #pragma unroll
             for (int e = 0; e < kQB2; ++e)
               asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst + (size_t)e * D),
                            "f"(u2f(v[e]))
                            : "memory");
+          } else {
+#pragma unroll
+            for (int e = 0; e < kQB2; ++e)
+              if (e < n_rows)
+                asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst + (size_t)e * D),
+                             "f"(u2f(v[e]))
+                             : "memory");
           }
         }
         if (a.deterministic && good) handoff_due = true;
@@ -696,8 +720,12 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
       // transpose) so that lane 4k+i writes piece i of rows 4k..4k+3.
       const int grp = lane & ~3, pc = lane & 3;
       const int row0 = w.j * kTile + wq * 32 + grp;  // first key row of the lane group
-      __nv_bfloat16* dk_base = reinterpret_cast<__nv_bfloat16*>(a.dk) + (size_t)w.bhk * a.Sk * D;
-      __nv_bfloat16* dv_base = reinterpret_cast<__nv_bfloat16*>(a.dv) + (size_t)w.bhk * a.Sk * D;
+      // dK / dV rows: [B, Hkv, Sk, D], or [T, Hkv, D] in packed calls
+      const int Sk = kVar ? w.kv_len : a.Sk;
+      const size_t kv_off = kVar ? ((size_t)w.row0 * a.Hkv + w.hk) * D : (size_t)w.bhk * Sk * D;
+      const size_t kv_row = kVar ? (size_t)a.Hkv * D : (size_t)D;
+      __nv_bfloat16* dk_base = reinterpret_cast<__nv_bfloat16*>(a.dk) + kv_off;
+      __nv_bfloat16* dv_base = reinterpret_cast<__nv_bfloat16*>(a.dv) + kv_off;
 #pragma unroll 1
       for (int pass = 0; pass < 2 * (D / 32); ++pass) {
         const int c = pass >> 1;
@@ -716,6 +744,10 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           mbar_arrive(bar(L::kBarDKVEmpty));
         }
         const float sc = is_v ? 1.f : a.scale;
+        if (kVar && a.dk_part) {
+          bwd_store_part(a, w, group, is_v, c, D, vk, sc, row0, Sk, lane);
+          continue;
+        }
         uint32_t wk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) wk[e] = pack_bf16x2(u2f(vk[2 * e]) * sc, u2f(vk[2 * e + 1]) * sc);
@@ -730,8 +762,8 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
         __nv_bfloat16* base = is_v ? dv_base : dk_base;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          if (row0 + m < a.Sk) {
-            const size_t off = (size_t)(row0 + m) * D + c * 32 + pc * 8;
+          if (row0 + m < Sk) {
+            const size_t off = (row0 + m) * kv_row + c * 32 + pc * 8;
             *reinterpret_cast<uint4*>(base + off) =
                 make_uint4(wk[4 * m], wk[4 * m + 1], wk[4 * m + 2], wk[4 * m + 3]);
           }
@@ -761,23 +793,27 @@ int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   if (smem < Q128Layout::kBytes) return FA_ERR_UNSUPPORTED;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(bwd_main_q128<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess ||
-        cudaFuncSetAttribute(bwd_main_q128<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
-      return FA_ERR_CUDA;
+    const void* kernels[] = {
+        (const void*)bwd_main_q128<false, false>, (const void*)bwd_main_q128<true, false>,
+        (const void*)bwd_main_q128<false, true>, (const void*)bwd_main_q128<true, true>};
+    for (const void* k : kernels)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  const auto kernel = mod ? bwd_main_q128<true> : bwd_main_q128<false>;
+  const bool var = a.items != nullptr;
+  const auto kernel = var ? (mod ? bwd_main_q128<true, true> : bwd_main_q128<false, true>)
+                          : (mod ? bwd_main_q128<true, false> : bwd_main_q128<false, false>);
+  const int which = (mod ? 1 : 0) + (var ? 2 : 0);
   // the setmaxnreg split assumes exactly kRegsLaunch registers per thread at
   // launch: a different count could leave the drain warpgroup's request
   // unserved, so such a build is refused
-  static bool regs_ok[2] = {false, false};
-  if (!regs_ok[mod ? 1 : 0]) {
+  static bool regs_ok[4] = {};
+  if (!regs_ok[which]) {
     cudaFuncAttributes fattr;
     if (cudaFuncGetAttributes(&fattr, kernel) != cudaSuccess) return FA_ERR_CUDA;
     if (fattr.numRegs != Q128Layout::kRegsLaunch) return FA_ERR_UNSUPPORTED;
-    regs_ok[mod ? 1 : 0] = true;
+    regs_ok[which] = true;
   }
   cudaError_t e;
   if (a.deterministic) {

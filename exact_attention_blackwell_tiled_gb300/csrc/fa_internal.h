@@ -49,7 +49,7 @@ struct alignas(32) VarItem {
   int len;   // its rows
   int tile;
   int b;
-  int pad0;  // the sequence's first row in arrays that pad each one to 64 rows
+  int pad0;  // the sequence's first row in arrays that pad each one to a query block
   int unused[3];
 };
 
@@ -65,6 +65,7 @@ struct PlanArgs {
   int B, T;
   int item_rows;  // 256 (forward: pairs of query tiles) or 128 (backward: kv tiles)
   int causal;
+  int pad;  // VarItem::pad0 counts sequences padded to this many rows (a power of two)
   VarItem* items;
   int max_items;
   int* n_items;
@@ -184,7 +185,7 @@ struct BwdArgs {
   int sem_group_stride;    // semaphores from one group to the next
   // packed calls: the plan, four tensor maps per sequence (q, k, v, dO), the
   // rows of the packed tensors, and the rows that lse2 and delta hold per head
-  // (every sequence padded to 64); the dQ accumulators are [Hq, T, D]
+  // (every sequence padded to qblk_rows); the dQ accumulators are [Hq, T, D]
   const VarItem* items;
   const int* n_items;
   const CUtensorMap* maps;

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
         : "memory");
   auto len_of = [&](int i) { return i < kPlanCache ? s_len[i] : p.cu[i + 1] - p.cu[i]; };
   int pad0 = 0;
-  for (int i = lane; i < b; i += 32) pad0 += (len_of(i) + 63) & ~63;
+  for (int i = lane; i < b; i += 32) pad0 += (len_of(i) + p.pad - 1) & -p.pad;
   pad0 = warp_add(pad0);
   const int n_own = (len + p.item_rows - 1) >> shift, blk_own = (len + 63) >> 6;
   const int mode = p.causal ? (p.item_rows == 256 ? 0 : 1) : 2;
@@ -176,6 +176,7 @@ bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>
 
 struct VarLayout {
   int max_items, groups;
+  int pad;  // rows of the backward's query blocks
   long long t_pad;
   bool split;  // q heads are units of their own (BwdArgs::dk_part)
   size_t off_items, off_maps, off_acc, off_delta, off_lse2, off_sem, off_dk, off_dv, total;
@@ -191,7 +192,7 @@ int check_var(int B, int T, int Hq, int Hkv, int D) {
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (T > (1 << 30) || B > (1 << 18)) return FA_ERR_INVALID_ARG;  // the plan takes B^2 steps
   // units (item, head) and the packed rows over all heads are counted in 32 bits
-  const long long t_pad = ((long long)T + 63) / 64 * 64 + 64LL * B;
+  const long long t_pad = ((long long)T + 127) / 128 * 128 + 128LL * B;
   if (t_pad * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
@@ -207,14 +208,15 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
   // as many accumulators as a dense call of twice the mean length would take
   const long long twice = 2LL * T / B + 1;
   L.groups = dq_group_count((int)(twice < T ? twice : T), deterministic);
-  L.t_pad = ((long long)T + 63) / 64 * 64 + 64LL * B;
+  L.pad = bwd_qblk_rows(D, deterministic);
+  L.t_pad = ((long long)T + L.pad - 1) / L.pad * L.pad + (long long)L.pad * B;
   L.off_acc = L.total;
   L.off_delta = up256(L.off_acc + (size_t)L.groups * Hq * T * D * sizeof(float));
   L.off_lse2 = up256(L.off_delta + (size_t)Hq * L.t_pad * sizeof(float));
   L.off_sem = up256(L.off_lse2 + (size_t)Hq * L.t_pad * sizeof(float));
   L.total = L.off_sem;
   if (deterministic)
-    L.total = up256(L.off_sem + (size_t)L.groups * Hq * (L.t_pad / 64) * sizeof(int));
+    L.total = up256(L.off_sem + (size_t)L.groups * Hq * (L.t_pad / L.pad) * sizeof(int));
   L.split = Hq > Hkv && (long long)L.max_items * Hkv <= kSplitUnits;
   if (L.split) {
     L.off_dk = L.total;
@@ -306,6 +308,7 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   p.B = B;
   p.T = T;
   p.item_rows = 256;
+  p.pad = 64;
   p.causal = a.causal;
   p.items = reinterpret_cast<VarItem*>(ws + L.off_items);
   p.max_items = L.max_items;
@@ -341,8 +344,9 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   int rc = check_var(B, T, Hq, Hkv, D);
   if (rc) return rc;
   if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
-  const VarTensor t[4] = {{q, q_stride, Hq, 64}, {k, k_stride, Hkv, kTile},
-                          {v, v_stride, Hkv, kTile}, {dO, nullptr, Hq, 64}};
+  const int qrows = bwd_qblk_rows(D, deterministic);
+  const VarTensor t[4] = {{q, q_stride, Hq, qrows}, {k, k_stride, Hkv, kTile},
+                          {v, v_stride, Hkv, kTile}, {dO, nullptr, Hq, qrows}};
   if ((rc = check_strides(t, 4, D))) return rc;
   if (T == 0) return FA_OK;
   if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv || !cu_seqlens)
@@ -372,6 +376,7 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   p.maps = reinterpret_cast<CUtensorMap*>(ws + L.off_maps);
   p.status = reinterpret_cast<int*>(ws);
   p.clear = 1;
+  p.pad = L.pad;
   p.counter = reinterpret_cast<int*>(ws + 128);
   a.o = o;
   a.dO = dO;
@@ -398,9 +403,9 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   a.scale_log2 = scale * 1.4426950408889634f;
   a.dq_groups = L.groups;
   a.dq_group_stride = (size_t)Hq * T * D;
-  a.n_qblk = (int)(L.t_pad / 64);
+  a.n_qblk = (int)(L.t_pad / L.pad);
   a.sem_group_stride = Hq * a.n_qblk;
-  a.qblk_rows = 64;
+  a.qblk_rows = L.pad;
   {
     // kv heads dealt together, so that their q, dO, dQ accumulators and K / V stay
     // in L2, as in the dense call; in the deterministic mode all of them, since tiles

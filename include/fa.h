@@ -267,7 +267,7 @@ int fa_lse_merge(const float* o_parts, const float* lse_parts, int n_parts, void
  *     fa_bwd_status(workspace) (backward) reports.
  * Rows of no sequence (before the first, behind the last) are neither read into
  * any result nor written.  T >= 0 (0 is a no-op), 1 <= B <= 2^18, D in {64, 128}; the
- * rows padded per sequence to 64, times Hq, stay below 2^31.  The bf16 tensors are 16-byte
+ * rows padded per sequence to 128, times Hq, stay below 2^31.  The bf16 tensors are 16-byte
  * aligned, lse and cu_seqlens 4-byte aligned.
  * workspace: fa_varlen_workspace_bytes(...) bytes of device memory, 256-byte
  * aligned, uninitialised; it holds the work list and tensor maps of the call
