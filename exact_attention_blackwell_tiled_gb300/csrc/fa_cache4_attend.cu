@@ -33,6 +33,8 @@
 // by shares leaves parts (fp32 O, maximum, sum), at most two per warp, which a
 // second kernel joins; it also writes the rows of empty sequences and, when weights
 // are asked for, turns the stored scores into them, now that the sums are known.
+// Short caches in few rows, where that second launch is most of the time, take a
+// block per row instead and join in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,6 +49,15 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;      // per block; they share nothing but the launch
+// One block per row (kOwn): caches of up to 64 blocks of 16 slots, so that a warp has
+// at most 8, and at most two rows per SM, except where two blocks of it fit an SM
+// (D = 64, 8 columns).  Measured, us of a step without / with weights, one block per
+// row against shares, 32 query and 8 kv heads:
+//   D = 128, 1 x 300 tokens 5.1 / 6.5 against 9.4 / 10.5;  38 x 300: 10.3 / 13.6
+//   against 15.7 / 16.6;  38 x 1000: 16.0 / 22.4 against 20.0 / 22.1;  64 x 300 (more
+//   than two rows per SM): 19.5 / 25.3 against 19.6 / 22.5;
+//   D = 64, 400 x 300: 48.6 / 71.7 against 68.4 / 87.3.
+constexpr int kOwnWarps = 8, kOwnBlocks = 64, kOwnRowsPerSm = 2;
 constexpr int kWeightKeys = 1024;  // keys of a (sequence, kv head) per step of the weight pass
 
 struct AttendArgs {
@@ -272,13 +283,18 @@ __device__ __forceinline__ void write_lse(const AttendArgs& a, size_t row, float
   if (a.scores) a.lse2[row] = z;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(const AttendArgs a) {
+// kOwn: short caches and few rows.  A block of 8 warps takes one row, its warps equal
+// parts of it, and joins them in shared memory, weights included: one launch.
+// Otherwise every warp takes a share of the list.
+template <int D, int NT, bool kOwn>
+__global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : (NT == 1 ? 3 : 2))
+    attend_kernel(const AttendArgs a) {
   using L = C4<D>;
   using R = Ring<D>;
-  constexpr int kG = L::kGroups;
+  constexpr int kG = L::kGroups, kW = kOwn ? kOwnWarps : kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ alignas(8) uint64_t s_bar[kWarps][R::kStages];
+  __shared__ alignas(8) uint64_t s_bar[kW][R::kStages];
+  __shared__ float2 s_ml[kOwn ? kW : 1][8 * NT];  // maximum and sum of a warp's part
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, t = lane & 3;
@@ -292,20 +308,35 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
   grid_dep_launch();
   // rows (b, kv head, tile) in order: a sequence has rows_per rows of its blocks
   const int rows_per = a.Hkv * a.tiles;
-  const List list = read_list(a);
-  const long long N = list.total * rows_per;
-  if (N == 0) return;
-  const int W = share_count(a, N);
-  const int w = blockIdx.x + warp * gridDim.x;  // neighbouring shares on different SMs
-  if (w >= W) return;
-  const long long begin = share_begin(N, W, w);
-  int left = (int)(share_begin(N, W, w + 1) - begin);  // blocks of the share still to do
-  long long base;
-  int row_b = locate(a, list, begin / rows_per, &base);
-  int len = seq_len(a, row_b), nb = (len + kC4Block - 1) / kC4Block;
-  // where in the sequence's rows the share begins
-  int row = (int)((begin - base * rows_per) / nb);
-  int blk0 = (int)(begin - base * rows_per - (long long)row * nb);
+  int row_b, row, len, nb, blk0, left;  // left: blocks still to do
+  int w = 0;
+  if constexpr (kOwn) {
+    row_b = blockIdx.x / rows_per;
+    row = blockIdx.x - row_b * rows_per;
+    len = seq_len(a, row_b);
+    nb = (len + kC4Block - 1) / kC4Block;
+    const int per = (nb + 2 * kW - 1) / (2 * kW) * 2;  // pairs of blocks
+    blk0 = min(nb, warp * per);
+    left = min(per, nb - blk0);
+    if (lane < 8 * NT) s_ml[warp][lane] = make_float2(-INFINITY, 0.f);
+    if (row == 0 && threadIdx.x == 0 && a.lens[row_b] != len) c4_flag(a.table);
+  } else {
+    const List list = read_list(a);
+    const long long N = list.total * rows_per;
+    if (N == 0) return;
+    const int W = share_count(a, N);
+    w = blockIdx.x + warp * gridDim.x;  // neighbouring shares on different SMs
+    if (w >= W) return;
+    const long long begin = share_begin(N, W, w);
+    left = (int)(share_begin(N, W, w + 1) - begin);
+    long long base;
+    row_b = locate(a, list, begin / rows_per, &base);
+    len = seq_len(a, row_b);
+    nb = (len + kC4Block - 1) / kC4Block;
+    // where in the sequence's rows the share begins
+    row = (int)((begin - base * rows_per) / nb);
+    blk0 = (int)(begin - base * rows_per - (long long)row * nb);
+  }
 
   const float score_up = a.scale_log2 * kScoreUp;
   const int slot_i = i ^ ((i >> 1) & 1);  // slot of product row i; row i + 8 is slot_i + 8
@@ -414,7 +445,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
             }
           }
           __syncwarp();
-          return;
+          if constexpr (!kOwn) return;
+          left = 0;  // (the other warps of the block are not left waiting)
+          break;
         }
       }
       // the second block may lie behind the row's last: what its place in the ring
@@ -617,8 +650,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
             r.mid[g][nt][c] += __shfl_xor_sync(0xffffffffu, r.mid[g][nt][c], o);
         }
       }
-    const bool whole = blk0 == 0 && blk1 == nb;
+    const bool whole = !kOwn && blk0 == 0 && blk1 == nb;
     const size_t part = ((size_t)w * 2 + (blk0 == 0 ? 1 : 0)) * (8 * NT);
+    float* mine = kOwn ? reinterpret_cast<float*>(smem + warp * R::kStages * R::kBytes)
+                       : a.part_o + part * D;  // the warp's own ring, which it has read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -639,17 +674,19 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
             *reinterpret_cast<uint2*>(a.o + out * D + 32 * g + 4 * i) =
                 make_uint2(pack_bf16x2(x0, x1), pack_bf16x2(x2, x3));
           else
-            *reinterpret_cast<float4*>(a.part_o + (part + col) * D + 32 * g + 4 * i) =
-                make_float4(x0, x1, x2, x3);
+            *reinterpret_cast<float4*>(mine + col * D + 32 * g + 4 * i) = make_float4(x0, x1, x2, x3);
         }
         if (i == 0) {
           if (whole)
             write_lse(a, out, m, l);
+          else if (kOwn)
+            s_ml[warp][col] = make_float2(m, l);
           else
             a.part_ml[part + col] = make_float2(m, l);
         }
       }
     // ---- on to the next row of the share
+    if (kOwn) break;
     left -= blk1 - blk0;
     blk0 = 0;
     if (left > 0 && ++row == rows_per) {
@@ -658,6 +695,50 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) attend_kernel(co
         len = seq_len(a, ++row_b);  // the share ends inside the list
       } while (len == 0);
       nb = (len + kC4Block - 1) / kC4Block;
+    }
+  }
+  if constexpr (kOwn) {
+    // ---- the row from its warps' parts (a warp without blocks has sum 0)
+    __syncthreads();
+    const int hk = row / a.tiles, tile = row - hk * a.tiles;
+    const int heads = min(8 * NT, a.group - tile * 8 * NT);
+    const size_t out0 = (size_t)row_b * a.Hq + hk * a.group + tile * 8 * NT;
+    for (int x = threadIdx.x; x < heads * (D / 4); x += kW * 32) {
+      const int col = x / (D / 4), d = (x - col * (D / 4)) * 4;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int y = 0; y < kW; ++y) m = fmaxf(m, s_ml[y][col].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < kW; ++y) {
+        const float2 ml = s_ml[y][col];
+        if (!(ml.y > 0.f)) continue;
+        const float f = ex2_mufu(ml.x - m);
+        const float4 v = *reinterpret_cast<const float4*>(smem + y * R::kStages * R::kBytes +
+                                                          (col * D + d) * 4);
+        l = fmaf(f, ml.y, l);
+        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+      }
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      *reinterpret_cast<uint2*>(a.o + (out0 + col) * D + d) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (d == 0) write_lse(a, out0 + col, m, l);
+    }
+    if (a.scores) {
+      // the weights of the row's keys: the scores and sums are the block's own
+      __syncthreads();
+      const size_t bh = (size_t)row_b * a.Hkv + hk;
+      for (int j = threadIdx.x; j < len; j += kW * 32) {
+        const float* src = a.scores + (bh * a.cap + j) * a.group;
+        float sum = 0.f;
+        for (int h = 0; h < a.group; ++h) {
+          const float z = a.lse2[out0 + h];
+          sum += z == -INFINITY ? 0.f : ex2_mufu(src[h] - z);
+        }
+        const size_t at = bh * a.w_stride + j;
+        a.w_out[at] = a.w_in ? a.w_in[at] + sum : sum;
+      }
     }
   }
 }
@@ -878,21 +959,36 @@ AttendLayout attend_layout(int B, int Hq, int Hkv, int D, int cap, int sms) {
 }
 
 template <int D, int NT>
-int launch_attend(const AttendArgs& a, cudaStream_t stream) {
+int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) {
   constexpr int kSmem = kWarps * Ring<D>::kStages * Ring<D>::kBytes;
+  constexpr int kOwnSmem = kOwnWarps * Ring<D>::kStages * Ring<D>::kBytes;
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (!attr_done[dev]) {
-    if (cudaFuncSetAttribute(attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(attend_kernel<D, NT, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(attend_kernel<D, NT, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
+  // One launch with a block per row, by the table's slots: the lengths are on the device
+  const long long own_rows = (long long)a.B * a.Hkv;
+  if (slots <= kOwnBlocks * kC4Block && a.tiles == 1 &&
+      ((D == 64 && NT == 1) || own_rows <= (long long)kOwnRowsPerSm * sms)) {
+    record_timing(false, stream);
+    if (launch_pdl(attend_kernel<D, NT, true>, dim3((unsigned)own_rows), dim3(kOwnWarps * 32),
+                   kOwnSmem, stream, a) != cudaSuccess)
+      return FA_ERR_CUDA;
+    record_timing(true, stream);
+    note_launches(1);
+    return FA_OK;
+  }
   record_timing(false, stream);
-  if (launch_pdl(attend_kernel<D, NT>, dim3(a.n_warps / kWarps), dim3(kWarps * 32), kSmem, stream,
-                 a) != cudaSuccess)
+  if (launch_pdl(attend_kernel<D, NT, false>, dim3(a.n_warps / kWarps), dim3(kWarps * 32), kSmem,
+                 stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
   record_timing(true, stream);
   const int rows = a.B * a.Hq;
@@ -986,10 +1082,10 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   a.w_stride = weight_slots;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (D == 128)
-    return nt == 1 ? launch_attend<128, 1>(a, st)
-                   : launch_attend<128, 2>(a, st);
-  return nt == 1 ? launch_attend<64, 1>(a, st)
-                 : launch_attend<64, 2>(a, st);
+    return nt == 1 ? launch_attend<128, 1>(a, slots, info.sm_count, st)
+                   : launch_attend<128, 2>(a, slots, info.sm_count, st);
+  return nt == 1 ? launch_attend<64, 1>(a, slots, info.sm_count, st)
+                 : launch_attend<64, 2>(a, slots, info.sm_count, st);
 }
 
 }  // extern "C"

@@ -221,7 +221,8 @@ def test_append_and_read(gpu, D, page):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lens,page,Hkv,group", [
     ([1], 16, 1, 1), ([0, 5, 16, 17], 16, 2, 4), ([300, 31], 32, 2, 5), ([1000, 0, 64], 64, 3, 8),
-    ([2049, 777], 128, 1, 12), ([129] * 40, 16, 4, 2), ([4000], 64, 1, 40)])
+    ([2049, 777], 128, 1, 12), ([129] * 40, 16, 4, 2), ([4000], 64, 1, 40), ([900, 0, 33], 16, 2, 16),
+    ([250] * 100, 32, 4, 1)])
 def test_attend(gpu, D, lens, page, Hkv, group):
     cache, table, n, cu, k, v = _filled(lens, Hkv, D, page, fill=255)
     q = torch.randn(len(lens), Hkv * group, D, generator=torch.Generator().manual_seed(1)).to(
@@ -230,7 +231,7 @@ def test_attend(gpu, D, lens, page, Hkv, group):
     w0 = torch.rand(len(lens), Hkv, slots, generator=torch.Generator().manual_seed(2))
     wd = w0.cuda()
     o, lse = fa.cache4_attend(q.cuda(), cache, table, n)
-    assert fa.last_launch_count() == 2
+    assert fa.last_launch_count() in (1, 2)
     o2, lse2 = fa.cache4_attend(q.cuda(), cache, table, n, weights=wd)
     assert fa.cache4_status() == fa.FA_OK
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
