@@ -19,10 +19,15 @@
 // only rounding before O's own.  (z - 8, not z: the rounding then counts for the
 // value's distance from the middle of its group only.)
 //
-// Bound by memory: a key and its value are 5/2 D bytes of codes and parameters,
-// read once for all query heads of the kv head (up to 8 NT of them, the columns of
-// the products); the arithmetic to unpack them is about 20 warp instructions per
-// key, 0.7 of what the SM can issue in the time the bytes take.
+// A key and its value are 5/4 D bytes of codes and parameters, read once for all
+// query heads of the kv head (up to 8 NT of them, the columns of the products), and
+// cost about 24 warp instructions to unpack, multiply and weigh at D = 128.
+// Measured with 64 sequences of 512 to 8192 tokens, 32 query and 8 kv heads of 128
+// (265 MB): 60 us, 4.4 TB/s, the SMs issuing in 57% of the cycles; the copies alone
+// take 50 us.  So memory and issue bound it together: with 12 warps per SM (registers)
+// a warp's chains of dependent steps are not wholly covered by the others.  Storing
+// the scores for the weights adds 7 us, the second kernel 5 to 9 (17 with weights,
+// cold).
 //
 // Every warp works by itself: the 16-slot blocks of all (sequence, kv head) rows
 // lie in one list, and each warp takes an equal contiguous share of it, streams it
@@ -30,8 +35,9 @@
 // an mbarrier per stage) and keeps maximum, sum and O of the row at hand in
 // registers.  So sequences of any lengths load the SMs evenly with no barrier
 // between warps.  A row that lies inside one share is finished there; a row cut
-// by shares leaves parts (fp32 O, maximum, sum), at most two per warp, which a
-// second kernel joins; it also writes the rows of empty sequences and, when weights
+// by shares leaves parts (fp32 O, maximum, sum), at most two per warp, and the
+// numbers of its first and last share, by which a second kernel finds and joins them
+// (finding them from the lengths again took 8 us more); it also writes the rows of empty sequences and, when weights
 // are asked for, turns the stored scores into them, now that the sums are known.
 // Short caches in few rows, where that second launch is most of the time, take a
 // block per row instead and join in shared memory.
@@ -58,7 +64,7 @@ constexpr int kWarps = 4;      // per block; they share nothing but the launch
 //   than two rows per SM): 19.5 / 25.3 against 19.6 / 22.5;
 //   D = 64, 400 x 300: 48.6 / 71.7 against 68.4 / 87.3.
 constexpr int kOwnWarps = 8, kOwnBlocks = 64, kOwnRowsPerSm = 2;
-constexpr int kWeightKeys = 1024;  // keys of a (sequence, kv head) per step of the weight pass
+constexpr int kWeightKeys = 1024;  // keys of a (sequence, kv head) per unit of the weight pass
 
 struct AttendArgs {
   const __nv_bfloat16* q;
@@ -75,6 +81,7 @@ struct AttendArgs {
   int n_warps;
   float* part_o;    // [n_warps, 2, 8 NT, D]
   float2* part_ml;  // [n_warps, 2, 8 NT]: maximum (log2 units) and sum
+  int* span;        // [B Hkv tiles, 2]: first and last share of a row that is not empty
   float* scores;    // [B, Hkv, cap, group] in log2 units, or null
   float* lse2;      // [B, Hq] log2 of the sums of the rows that no share cut, or unused
   const float* w_in;
@@ -149,24 +156,12 @@ __device__ __forceinline__ int locate(const AttendArgs& a, const List& s, long l
   return __shfl_sync(0xffffffffu, b, l);
 }
 
-// Blocks before sequence b.
-__device__ __forceinline__ long long list_before(const AttendArgs& a, const List& s, int b) {
-  const int l = b / s.per;
-  long long at = s.before;
-  if ((threadIdx.x & 31) == l)
-    for (int x = l * s.per; x < b; ++x) at += seq_blocks(a, x);
-  return __shfl_sync(0xffffffffu, at, l);
-}
-
 // Shares: warp w of W takes list positions w N / W .. (w + 1) N / W - 1.
 __device__ __forceinline__ int share_count(const AttendArgs& a, long long N) {
   const long long most = (N + kMinBlocks - 1) / kMinBlocks;
   return (int)(most < a.n_warps ? most : a.n_warps);
 }
 __device__ __forceinline__ long long share_begin(long long N, int W, int w) { return w * N / W; }
-__device__ __forceinline__ int share_of(long long N, int W, long long x) {
-  return (int)(((x + 1) * W - 1) / N);
-}
 
 // ------------------------------------------------------------------ fragments
 
@@ -651,6 +646,11 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : (
         }
       }
     const bool whole = !kOwn && blk0 == 0 && blk1 == nb;
+    if (!kOwn && lane == 0) {
+      int* span = a.span + 2 * ((size_t)row_b * rows_per + row);
+      if (blk0 == 0) span[0] = w;
+      if (blk1 == nb) span[1] = w;
+    }
     const size_t part = ((size_t)w * 2 + (blk0 == 0 ? 1 : 0)) * (8 * NT);
     float* mine = kOwn ? reinterpret_cast<float*>(smem + warp * R::kStages * R::kBytes)
                        : a.part_o + part * D;  // the warp's own ring, which it has read
@@ -745,23 +745,16 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : (
 
 // ------------------------------------------------------------------ join and weights
 
-// Where row (b, hk, tile)'s blocks lie in the list, and the shares that hold them.
+// The shares that hold a row's blocks; w0 == w1: the row was finished by that one.
 struct RowSpan {
-  int w0, w1;  // first and last share; w0 == w1: the row was finished by it
-  int nb;
+  int w0, w1;
 };
 
 __device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int b, int row) {
-  const List list = read_list(a);
-  RowSpan s{0, 0, seq_blocks(a, b)};
-  const long long before = list_before(a, list, b);
-  if (s.nb == 0) return s;
-  const int rows_per = a.Hkv * a.tiles;
-  const long long N = list.total * rows_per, first = before * rows_per + (long long)row * s.nb;
-  const int W = share_count(a, N);
-  s.w0 = share_of(N, W, first);
-  s.w1 = share_of(N, W, first + s.nb - 1);
-  return s;
+  const int2 s = *reinterpret_cast<const int2*>(a.span + 2 * ((size_t)b * a.Hkv * a.tiles + row));
+  // (a share that gave up wrote nothing)
+  const int w0 = min(max(s.x, 0), a.n_warps - 1);
+  return {w0, min(max(s.y, w0), a.n_warps - 1)};
 }
 
 // Index of column col of the part that share w of the row holds.
@@ -792,42 +785,31 @@ __device__ float2 join_ml(const AttendArgs& a, const RowSpan& s, int col) {
   return make_float2(mx, l);
 }
 
-// One block per (sequence, query head) whose row was cut by shares, or is empty.
 // w_out = w_in + sum over the group of 2^(score - log2 sum), for kWeightKeys keys of
 // a (sequence, kv head).  The scores are on their way while the sums of rows that
 // shares cut are joined, a warp per query head.
 template <int NT, int kW>
 __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_lse2) {
   constexpr int kPer = kWeightKeys / (kW * 32);
-  const int steps = (a.cap + kWeightKeys - 1) / kWeightKeys;
-  const int bh = unit / steps, j0 = (unit - bh * steps) * kWeightKeys + threadIdx.x;
-  const int b = bh / a.Hkv, hk = bh - b * a.Hkv, len = seq_len(a, b);
-  if ((unit - bh * steps) * kWeightKeys >= len) {
-    grid_dep_wait();
-    grid_dep_launch();
-    return;
-  }
+  const int units = (a.cap + kWeightKeys - 1) / kWeightKeys;
+  const int bh = unit / units, first = (unit - bh * units) * kWeightKeys;
+  const int b = bh / a.Hkv, hk = bh - b * a.Hkv, len = seq_len(a, b), j0 = first + threadIdx.x;
+  if (first >= len) return;
+  const float* src = a.scores + ((size_t)bh * a.cap + j0) * a.group;
+  const size_t step = (size_t)kW * 32 * a.group, at = (size_t)bh * a.w_stride + j0;
+  const bool four = (a.group & 3) == 0;
+  float4 s[kPer];  // the first four (or one) of each key
   float w[kPer];
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
-    const int j = j0 + x * kW * 32;
-    w[x] = a.w_in && j < len ? a.w_in[(size_t)bh * a.w_stride + j] : 0.f;
-  }
-  grid_dep_wait();
-  grid_dep_launch();
-  const float* src = a.scores + (size_t)bh * a.cap * a.group;
-  const bool four = (a.group & 3) == 0;
-  float4 s[kPer];  // the first four (or one) of each key
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) {
-    const int j = j0 + x * kW * 32;
     s[x] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (j >= len) continue;
-    if (four) s[x] = *reinterpret_cast<const float4*>(src + (size_t)j * a.group);
-    else s[x].x = src[(size_t)j * a.group];
+    w[x] = 0.f;
+    if (j0 + x * kW * 32 >= len) continue;
+    if (four) s[x] = *reinterpret_cast<const float4*>(src + x * step);
+    else s[x].x = src[x * step];
+    if (a.w_in) w[x] = a.w_in[at + x * kW * 32];
   }
-  const int warp = threadIdx.x >> 5;
-  for (int h = warp; h < a.group; h += kW) {
+  for (int h = threadIdx.x >> 5; h < a.group; h += kW) {
     const int tile = h / (8 * NT), col = h - tile * 8 * NT;
     const RowSpan sp = row_span(a, b, hk * a.tiles + tile);
     float z;
@@ -843,8 +825,7 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_ls
   const bool empty = s_lse2[0] == -INFINITY;  // every page out of range
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
-    const int j = j0 + x * kW * 32;
-    if (j >= len) break;
+    if (j0 + x * kW * 32 >= len) break;
     float sum = 0.f;
     if (four) {
       float4 y = s[x];
@@ -852,44 +833,45 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_ls
         sum += (ex2_mufu(y.x - s_lse2[h]) + ex2_mufu(y.y - s_lse2[h + 1])) +
                (ex2_mufu(y.z - s_lse2[h + 2]) + ex2_mufu(y.w - s_lse2[h + 3]));
         if ((h += 4) >= a.group) break;
-        y = *reinterpret_cast<const float4*>(src + (size_t)j * a.group + h);
+        y = *reinterpret_cast<const float4*>(src + x * step + h);
       }
     } else {
       sum = ex2_mufu(s[x].x - s_lse2[0]);
-      for (int h = 1; h < a.group; ++h) sum += ex2_mufu(src[(size_t)j * a.group + h] - s_lse2[h]);
+      for (int h = 1; h < a.group; ++h) sum += ex2_mufu(src[x * step + h] - s_lse2[h]);
     }
-    a.w_out[(size_t)bh * a.w_stride + j] = w[x] + (empty ? 0.f : sum);
+    a.w_out[at + x * kW * 32] = w[x] + (empty ? 0.f : sum);
   }
 }
 
-// The first B * Hq blocks: one (sequence, query head) each, whose row was cut by
-// shares or is empty.  The others, where weights are asked for: a unit of weights
-// each.  kW warps: four where there are rows enough to fill the GPU, eight where few
-// rows were cut into many parts; with weights or without, so that O has the same
-// bits.
+// The first blocks: a unit of weights each, where weights are asked for.  The others:
+// one (sequence, query head) each, whose row was cut by shares or is empty.  kW
+// warps: four where there are rows enough to fill the GPU, eight where few rows were
+// cut into many parts; with weights or without, so that O has the same bits.  A block
+// is a chain of dependent loads, so what counts is how many are resident: 32 warps
+// per SM with 64 registers a thread, for 20 with 95 (1 us less).
 template <int D, int NT, int kW>
-__global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kW * 32, 32 / kW) join_kernel(const AttendArgs a, int units) {
   constexpr int kV = D / 32;
   __shared__ float s_o[kW][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The lengths were complete before the attention kernel let this one start, so
-  // they are read, and the row's parts found, while it still runs.
-  if ((int)blockIdx.x >= a.B * a.Hq) {
-    __shared__ float s_lse2[128];
-    weigh<NT, kW>(a, blockIdx.x - a.B * a.Hq, s_lse2);
-    return;
-  }
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
-  const int hk = hq / a.group, in_group = hq - hk * a.group;
-  const int tile = in_group / (8 * NT), col = in_group - tile * 8 * NT;
-  const RowSpan s = row_span(a, b, hk * a.tiles + tile);
   grid_dep_wait();
   grid_dep_launch();
-  if (hq == 0 && threadIdx.x == 0 && a.lens[b] != seq_len(a, b)) c4_flag(a.table);
-  __nv_bfloat16* o = a.o + (size_t)blockIdx.x * D;
-  if (s.nb == 0) {  // an empty sequence
+  if ((int)blockIdx.x < units) {
+    __shared__ float s_lse2[128];
+    weigh<NT, kW>(a, blockIdx.x, s_lse2);
+    return;
+  }
+  const int out = blockIdx.x - units;  // (sequence, query head)
+  const int b = out / a.Hq, hq = out - b * a.Hq;
+  const int hk = hq / a.group, in_group = hq - hk * a.group;
+  const int tile = in_group / (8 * NT), col = in_group - tile * 8 * NT;
+  const int len = seq_len(a, b);
+  const RowSpan s = row_span(a, b, hk * a.tiles + tile);
+  if (hq == 0 && threadIdx.x == 0 && a.lens[b] != len) c4_flag(a.table);
+  __nv_bfloat16* o = a.o + (size_t)out * D;
+  if (len == 0) {  // an empty sequence
     for (int x = threadIdx.x; x < D / 2; x += kW * 32) reinterpret_cast<uint32_t*>(o)[x] = 0u;
-    if (threadIdx.x == 0) a.lse[blockIdx.x] = -INFINITY;
+    if (threadIdx.x == 0) a.lse[out] = -INFINITY;
     return;
   }
   if (s.w0 == s.w1) return;
@@ -928,7 +910,7 @@ __global__ void __launch_bounds__(kW * 32) join_kernel(const AttendArgs a) {
     reinterpret_cast<uint32_t*>(o)[threadIdx.x] = pack_bf16x2(x0 * inv, x1 * inv);
   }
   if (threadIdx.x == 0)
-    a.lse[blockIdx.x] = ml.y > 0.f ? (ml.x + __log2f(ml.y)) * 0.69314718055994531f : -INFINITY;
+    a.lse[out] = ml.y > 0.f ? (ml.x + __log2f(ml.y)) * 0.69314718055994531f : -INFINITY;
 }
 
 bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -943,16 +925,17 @@ int tile_count(int group, int* nt) {
 int share_limit(int sms, int nt) { return sms * (nt == 1 ? 3 : 2) * kWarps; }
 
 struct AttendLayout {
-  size_t off_ml, off_lse2, off_scores, total;
+  size_t off_ml, off_span, off_lse2, off_scores, total;
 };
 
 AttendLayout attend_layout(int B, int Hq, int Hkv, int D, int cap, int sms) {
   int nt;
-  tile_count(Hq / Hkv, &nt);
+  const int tiles = tile_count(Hq / Hkv, &nt);
   const size_t rows = (size_t)share_limit(sms, nt) * 2 * 8 * nt;
   AttendLayout L;
   L.off_ml = rows * D * sizeof(float);
-  L.off_lse2 = (L.off_ml + rows * sizeof(float2) + 255) & ~(size_t)255;
+  L.off_span = L.off_ml + rows * sizeof(float2);
+  L.off_lse2 = (L.off_span + (size_t)B * Hkv * tiles * 2 * sizeof(int) + 255) & ~(size_t)255;
   L.off_scores = (L.off_lse2 + (cap > 0 ? (size_t)B * Hq * sizeof(float) : 0) + 255) & ~(size_t)255;
   L.total = L.off_scores + (size_t)B * Hq * cap * sizeof(float);
   return L;
@@ -992,11 +975,10 @@ int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) 
     return FA_ERR_CUDA;
   record_timing(true, stream);
   const int rows = a.B * a.Hq;
-  long long blocks = rows;
-  if (a.scores) blocks += (long long)a.B * a.Hkv * ((a.cap + kWeightKeys - 1) / kWeightKeys);
+  const int units = a.scores ? a.B * a.Hkv * ((a.cap + kWeightKeys - 1) / kWeightKeys) : 0;
   const int warps = rows >= 1024 ? 4 : 8;
   const auto join = warps == 4 ? join_kernel<D, NT, 4> : join_kernel<D, NT, 8>;
-  if (launch_pdl(join, dim3((unsigned)blocks), dim3(warps * 32), 0, stream, a) != cudaSuccess)
+  if (launch_pdl(join, dim3((unsigned)units + (unsigned)rows), dim3(warps * 32), 0, stream, a, units) != cudaSuccess)
     return FA_ERR_CUDA;
   note_launches(2);
   return FA_OK;
@@ -1075,6 +1057,7 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   a.n_warps = share_limit(info.sm_count, nt);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
+  a.span = reinterpret_cast<int*>(ws + L.off_span);
   a.lse2 = reinterpret_cast<float*>(ws + L.off_lse2);
   a.scores = weights_out ? reinterpret_cast<float*>(ws + L.off_scores) : nullptr;
   a.w_in = weights_in;
