@@ -248,12 +248,17 @@ __device__ __forceinline__ void lds(uint32_t (&r)[N], const uint8_t* p) {
   }
 }
 
+// The codes pass through L2 as lines to be evicted first: they are read once in a
+// call, while the scores and parts are read again by the second kernel (77.3 us
+// against 74.0 for the 64 sequences above with weights).
 __device__ __forceinline__ void copy_block(uint32_t dst, const void* src, uint32_t bytes,
                                            uint32_t bar) {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
 }
 
