@@ -1081,43 +1081,66 @@ __global__ void __launch_bounds__(256) bwd_dq_convert(const BwdArgs a) {
   }
 }
 
+__device__ __forceinline__ void add_eight(float4 (&x)[2], const float4* src) {
+  const float4 y0 = src[0], y1 = src[1];
+  x[0].x += y0.x, x[0].y += y0.y, x[0].z += y0.z, x[0].w += y0.w;
+  x[1].x += y1.x, x[1].y += y1.y, x[1].z += y1.z, x[1].w += y1.w;
+}
+
+__device__ __forceinline__ uint4 eight_bf16(const float4 (&x)[2], float scale) {
+  return make_uint4(pack_bf16x2(x[0].x * scale, x[0].y * scale),
+                    pack_bf16x2(x[0].z * scale, x[0].w * scale),
+                    pack_bf16x2(x[1].x * scale, x[1].y * scale),
+                    pack_bf16x2(x[1].z * scale, x[1].w * scale));
+}
+
 // The same for a packed batch, over (kv-tile item, q head) pairs of the plan;
-// dQ is [T, Hq, D], and rows of no sequence are left as they are.
+// dQ is [T, Hq, D], and rows of no sequence are left as they are.  A thread has
+// four pieces of a tile in flight: 28.3 us for 16384 rows of 16 heads of 128 (201 MB,
+// 7.1 TB/s, part of it from L2), 32.5 us with one piece.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
   grid_dep_wait();
-  constexpr int kPerRow = D / 8;
+  constexpr int kPerRow = D / 8, kRows = 256 / kPerRow;  // rows of a block's pass
+  constexpr int kPieces = 4;
+  const int row = threadIdx.x / kPerRow, c8 = threadIdx.x % kPerRow;
   const int n_units = *a.n_items * a.Hq;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int item = u / a.Hq, h = u - item * a.Hq;
     const VarItem it = load_item(a.items, item);
     const int pad0 = a.items[item].pad0;
     const int rows = min(kTile, it.len - it.tile * kTile);
-    for (int x = threadIdx.x; x < rows * kPerRow; x += blockDim.x) {
-      const int i = it.tile * kTile + x / kPerRow, c8 = x % kPerRow;
-      const float* base = a.dq_acc + ((size_t)h * a.T + it.row0 + i) * D + c8 * 8;
-      float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-      if (!a.deterministic) {
-        x0 = reinterpret_cast<const float4*>(base)[0];
-        x1 = reinterpret_cast<const float4*>(base)[1];
-      } else {
-        // in fixed order, the groups that some kv tile wrote for this block
-        const int* sem = a.sem + (size_t)h * a.n_qblk + (pad0 + i) / a.qblk_rows;
-        for (int g = 0; g < a.dq_groups; ++g) {
-          if (sem[(size_t)g * a.sem_group_stride] == 0) continue;
-          const float4* src = reinterpret_cast<const float4*>(base + (size_t)g * a.dq_group_stride);
-          const float4 y0 = src[0], y1 = src[1];
-          x0.x += y0.x, x0.y += y0.y, x0.z += y0.z, x0.w += y0.w;
-          x1.x += y1.x, x1.y += y1.y, x1.z += y1.z, x1.w += y1.w;
+#pragma unroll 1
+    for (int r0 = row; r0 < rows; r0 += kPieces * kRows) {
+      const int i0 = it.tile * kTile + r0;
+      const float* base = a.dq_acc + ((size_t)h * a.T + it.row0 + i0) * D + c8 * 8;
+      float4 x[kPieces][2];
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) x[e][0] = x[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      // (deterministic: in fixed order, the groups that some kv tile wrote for this
+      // block; otherwise the one accumulator, cleared before the main kernel)
+#pragma unroll 2
+      for (int g = 0; g < (a.deterministic ? a.dq_groups : 1); ++g) {
+        bool on[kPieces];
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+          on[e] = r0 + e * kRows < rows;
+          if (a.deterministic && on[e])
+            on[e] = a.sem[(size_t)h * a.n_qblk + (size_t)g * a.sem_group_stride +
+                          (pad0 + i0 + e * kRows) / a.qblk_rows] != 0;
         }
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e)
+          if (on[e])
+            add_eight(x[e], reinterpret_cast<const float4*>(base + (size_t)g * a.dq_group_stride +
+                                                            (size_t)e * kRows * D));
       }
-      uint4 w;
-      w.x = pack_bf16x2(x0.x * a.scale, x0.y * a.scale);
-      w.y = pack_bf16x2(x0.z * a.scale, x0.w * a.scale);
-      w.z = pack_bf16x2(x1.x * a.scale, x1.y * a.scale);
-      w.w = pack_bf16x2(x1.z * a.scale, x1.w * a.scale);
-      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.dq) +
-                                ((size_t)(it.row0 + i) * a.Hq + h) * D + c8 * 8) = w;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.dq) +
+                           ((size_t)(it.row0 + i0) * a.Hq + h) * D + c8 * 8;
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e)
+        if (r0 + e * kRows < rows)
+          *reinterpret_cast<uint4*>(out + (size_t)e * kRows * a.Hq * D) = eight_bf16(x[e], a.scale);
     }
   }
   if (!a.dk_part) return;
@@ -1129,22 +1152,25 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
     const int item = x0 / a.Hkv, hk = x0 - item * a.Hkv;
     const VarItem it = load_item(a.items, item);
     const int rows = min(kTile, it.len - it.tile * kTile);
-    const float* part = is_v ? a.dv_part : a.dk_part;
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(is_v ? a.dv : a.dk);
-    for (int x = threadIdx.x; x < rows * kPerRow; x += blockDim.x) {
-      const int i = it.row0 + it.tile * kTile + x / kPerRow, c8 = x % kPerRow;
-      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f), y1 = y0;
-#pragma unroll 4
-      for (int g = 0; g < group; ++g) {
-        const float4* src = reinterpret_cast<const float4*>(
-            part + ((size_t)(hk * group + g) * a.T + i) * D + c8 * 8);
-        const float4 z0 = src[0], z1 = src[1];
-        y0.x += z0.x, y0.y += z0.y, y0.z += z0.z, y0.w += z0.w;
-        y1.x += z1.x, y1.y += z1.y, y1.z += z1.z, y1.w += z1.w;
-      }
-      *reinterpret_cast<uint4*>(out + ((size_t)i * a.Hkv + hk) * D + c8 * 8) =
-          make_uint4(pack_bf16x2(y0.x, y0.y), pack_bf16x2(y0.z, y0.w), pack_bf16x2(y1.x, y1.y),
-                     pack_bf16x2(y1.z, y1.w));
+#pragma unroll 1
+    for (int r0 = row; r0 < rows; r0 += kPieces * kRows) {
+      const size_t i0 = it.row0 + it.tile * kTile + r0;
+      const float* base = (is_v ? a.dv_part : a.dk_part) + ((size_t)hk * group * a.T + i0) * D + c8 * 8;
+      float4 x[kPieces][2];
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) x[e][0] = x[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int g = 0; g < group; ++g)
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e)
+          if (r0 + e * kRows < rows)
+            add_eight(x[e], reinterpret_cast<const float4*>(base + ((size_t)g * a.T + e * kRows) * D));
+      __nv_bfloat16* out =
+          reinterpret_cast<__nv_bfloat16*>(is_v ? a.dv : a.dk) + (i0 * a.Hkv + hk) * D + c8 * 8;
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e)
+        if (r0 + e * kRows < rows)
+          *reinterpret_cast<uint4*>(out + (size_t)e * kRows * a.Hkv * D) = eight_bf16(x[e], 1.f);
     }
   }
 }
