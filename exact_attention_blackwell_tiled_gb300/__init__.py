@@ -773,7 +773,9 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     else:
         _given(lse, (B, Hq), torch.float32, index, "lse")
     ws, nbytes = _workspace(workspace, _attend_bytes(index, B, Hq, Hkv, D, slots), q, stream)
-    rc = lib().fa_cache4_attend(q.data_ptr(), q.stride(0), q.stride(1), cache.data_ptr(), pages, page,
+    # the stride of a dimension of one element is arbitrary
+    rc = lib().fa_cache4_attend(q.data_ptr(), q.stride(0) if B > 1 else 0,
+                                q.stride(1) if Hq > 1 else 0, cache.data_ptr(), pages, page,
                                 out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D,
                                 cache_lens.data_ptr(), page_table.data_ptr(), width,
                                 1.0 / math.sqrt(D) if scale is None else scale, w_in, w_out, slots,

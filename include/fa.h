@@ -344,7 +344,10 @@ int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, voi
  * One query token per sequence attends to its cache_lens[b] stored tokens:
  *   q bf16, element [b][h][d] at b * q_batch_stride + h * q_head_stride + d
  *   (strides multiples of 8);  o [B, Hq, D] bf16;  lse [B, Hq] fp32, natural log.
- * A sequence without tokens gets o = 0 and lse = -inf.  Hq / Hkv is at most 128.
+ * A sequence without tokens gets o = 0 and lse = -inf.  Hq / Hkv is at most 128,
+ * B * Hq at most 2^30, B * Hq * table slots / 16 below 2^40 and, with weights,
+ * B * Hkv * weight_slots / 1024 below 2^30.  |q| and the stored values stay below 2^32:
+ * the products are taken on scaled operands, which larger ones may overflow.
  * weights_out (null: none) [B, Hkv, weight_slots] fp32: for every stored token j
  *   weights_out[b][hk][j] = weights_in[b][hk][j] + sum of its softmax weights over
  *   the query heads of hk  (weights_in null: 0; it may be weights_out itself);
@@ -366,8 +369,8 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
  * ones and, of the others, those with the largest weights [B, Hkv, cap] (ties: the
  * lowest slot first; weights are not NaN).  The kept tokens' codes are copied
  * unchanged, in slot order, to slots 0, 1, ... of the pages of out_page_table
- * [B, out_table_width], which must be other pages than any table in use names; the
- * old pages are only read, so sequences that share them lose nothing.  A sequence
+ * [B, out_table_width], which must be other pages than any table in use names, each
+ * named once; the old pages are only read, so sequences that share them lose nothing.  A sequence
  * with at most `budget` tokens keeps all.
  *   src [B, Hkv, budget] int32: the old slot of each kept token, -1 behind the last;
  *   weights_out [B, Hkv, budget] fp32: their weights, 0 behind the last;

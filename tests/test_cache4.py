@@ -267,6 +267,55 @@ def test_attend_scales_and_late_maxima(gpu, scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shift", [29, -20])
+def test_attend_is_the_same_at_other_magnitudes(gpu, D, shift):
+    """Powers of two on q, k and v change no code and no rounding: the scores are
+    the same, and O is O times the power, to the bit."""
+    up, Hkv = 2.0 ** shift, 2
+    cache, table, lens, cu, k, v = _filled([130, 1501, 0, 17], Hkv, D, 32)
+    q = torch.randn(4, 6, D, device="cuda").to(torch.bfloat16)
+    w = torch.zeros(2, 4, Hkv, 1501, device="cuda")
+    o, lse = fa.cache4_attend(q, cache, table, lens, weights=w[0])
+    fa.cache4_append(cache, (k / up).cuda(), (v * up).cuda(), table, torch.zeros_like(lens), _i32(cu))
+    o2, lse2 = fa.cache4_attend(q * up, cache, table, lens, weights=w[1])
+    assert torch.equal(o * up, o2) and torch.equal(lse, lse2) and torch.equal(w[0], w[1])
+    assert fa.cache4_status() == fa.FA_OK
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once(gpu):
+    D, Hkv = 128, 2
+    sets = []
+    for n in (300, 2000, 700):  # one block per row, shares, both
+        cache, table, lens, *_ = _filled([n, 3 * n], Hkv, D, 64, seed=n)
+        q = torch.randn(2, 8, D, device="cuda").to(torch.bfloat16)
+        sets.append((q, cache, table, lens))
+    want = [fa.cache4_attend(*x) for x in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for st in streams:
+            got.append([fa.cache4_attend(*x, stream=st) for x in sets])
+    torch.cuda.synchronize()
+    for run in got:
+        for (o, lse), (o2, lse2) in zip(want, run):
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
+def test_attend_one_row_of_any_stride(gpu):
+    """The stride of a dimension of one element means nothing."""
+    D = 64
+    cache, table, lens, *_ = _filled([40], 1, D, 16)
+    q = torch.randn(2 * D, device="cuda").to(torch.bfloat16)
+    a = fa.cache4_attend(q[:D].view(1, 1, D), cache, table, lens)
+    b = fa.cache4_attend(q.as_strided((1, 1, D), (3, 5, 1)), cache, table, lens)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
 def test_attend_repeats_to_the_bit_and_takes_strides(gpu):
     D, Hkv, group = 64, 2, 3
     cache, table, n, *_ = _filled([500, 1200, 3], Hkv, D, 32)
