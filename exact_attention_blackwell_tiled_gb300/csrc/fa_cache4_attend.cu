@@ -37,8 +37,9 @@
 // between warps.  A row that lies inside one share is finished there; a row cut
 // by shares leaves parts (fp32 O, maximum, sum), at most two per warp, and the
 // numbers of its first and last share, by which a second kernel finds and joins them
-// (finding them from the lengths again took 8 us more); it also writes the rows of empty sequences and, when weights
-// are asked for, turns the stored scores into them, now that the sums are known.
+// (finding them from the lengths again took 8 us more); it also writes the rows of
+// empty sequences and, when weights are asked for, turns the stored scores into them,
+// now that the sums are known.
 // Short caches in few rows, where that second launch is most of the time, take a
 // block per row instead and join in shared memory.
 #include <cuda_bf16.h>
