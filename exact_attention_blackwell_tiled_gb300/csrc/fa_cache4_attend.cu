@@ -57,14 +57,18 @@ namespace {
 
 constexpr int kWarps = 4;      // per block; they share nothing but the launch
 // One block per row (kOwn): caches of up to 64 blocks of 16 slots, so that a warp has
-// at most 8, and at most two rows per SM, except where two blocks of it fit an SM
+// at most 8, and at most two rows per SM, eight where two blocks of it fit an SM
 // (D = 64, 8 columns).  Measured, us of a step without / with weights, one block per
 // row against shares, 32 query and 8 kv heads:
-//   D = 128, 1 x 300 tokens 5.1 / 6.5 against 9.4 / 10.5;  38 x 300: 10.3 / 13.6
-//   against 15.7 / 16.6;  38 x 1000: 16.0 / 22.4 against 20.0 / 22.1;  64 x 300 (more
-//   than two rows per SM): 19.5 / 25.3 against 19.6 / 22.5;
-//   D = 64, 400 x 300: 48.6 / 71.7 against 68.4 / 87.3.
-constexpr int kOwnWarps = 8, kOwnBlocks = 64, kOwnRowsPerSm = 2;
+//   D = 128, 1 x 300 tokens 5.1 / 6.6 against 10.0 / 10.6;  38 x 300 (two rows per
+//   SM): 10.5 / 13.8 against 13.7 / 16.0;  38 x 1000: 16.5 / 22.7 against 18.3 / 22.1;
+//   64 x 300: 19.5 / 25.3 against 17.5 / 19.1;
+//   D = 64, 38 x 300: 5.1 / 6.8 against 11.7 / 13.8;  152 x 300 (eight rows per SM):
+//   18.3 / 25.0 against 21.4 / 25.1;  152 x 1000: 34.7 / 47.4 against 37.8 / 46.6;
+//   228 x 300: 27.4 / 37.7 against 23.1 / 28.4.
+constexpr int kOwnWarps = 8, kOwnBlocks = 64;
+template <int D, int NT>
+constexpr int kOwnRowsPerSm = D == 64 && NT == 1 ? 8 : 2;
 constexpr int kWeightKeys = 1024;  // keys of a (sequence, kv head) per unit of the weight pass
 
 struct AttendArgs {
@@ -966,7 +970,7 @@ int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) 
   // One launch with a block per row, by the table's slots: the lengths are on the device
   const long long own_rows = (long long)a.B * a.Hkv;
   if (slots <= kOwnBlocks * kC4Block && a.tiles == 1 &&
-      ((D == 64 && NT == 1) || own_rows <= (long long)kOwnRowsPerSm * sms)) {
+      own_rows <= (long long)kOwnRowsPerSm<D, NT> * sms) {
     record_timing(false, stream);
     if (launch_pdl(attend_kernel<D, NT, true>, dim3((unsigned)own_rows), dim3(kOwnWarps * 32),
                    kOwnSmem, stream, a) != cudaSuccess)
