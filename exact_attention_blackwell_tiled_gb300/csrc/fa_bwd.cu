@@ -299,12 +299,14 @@ struct BwdSmem {
   static constexpr int kBarSFree = kBarDKVEmpty + 1;   // 2: S^T buffer read by dV and dK
   static constexpr int kBarDrain = kBarSFree + 2;      // 3: one per issuer
   // deterministic mode at D = 64: drain warps 0-1 hand each block they have
-  // added to lane 0 of drain warp 2, which raises the block's semaphore
+  // added to lane 0 of drain warp 2, which raises the block's semaphore, and get
+  // each block's turn from lane 0 of drain warp 3, which waits for it
   static constexpr int kBarDQAdded = kBarDrain + 3;       // (D = 64 only)
   static constexpr int kBarDQAddedFree = kBarDQAdded + 1;
+  static constexpr int kBarSemOk = kBarDQAddedFree + 1;  // 2
   // dynamic dealing: a ring of unit numbers taken by the TMA thread
   static constexpr int kURing = 8;
-  static constexpr int kBarUFull = kBarDrain + 3 + (D < 128 ? 2 : 0);  // kURing
+  static constexpr int kBarUFull = kBarDrain + 3 + (D < 128 ? 4 : 0);  // kURing
   static constexpr int kBarUEmpty = kBarUFull + kURing;  // kURing
   static constexpr int kNumBars = kBarUEmpty + kURing;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM slot, abort flag
@@ -321,17 +323,24 @@ struct BwdSmem {
   }
 };
 
+__device__ __forceinline__ void red_add(float* p, float x) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory");
+}
+
 // kMod: a sliding window and / or the relative-position bias (a.alibi); the
 // plain kernel applies no mask or the causal one.  kVar: a packed batch, with
 // tensor maps a.maps[4 b + 0..3] (q, k, v, dO) that end at the sequence's last
 // row, so that rows past it arrive as zeros; the dQ accumulators hold no padding
-// rows, so a block's rows past the end are not added.
-template <int D, bool kMod, bool kVar>
+// rows, so a block's rows past the end are not added.  kDet: the deterministic mode
+// (D = 64; at D = 128 it is the 128-row kernel's); a kernel of its own, since the
+// atomic mode's adds lost 13% of its rate to code that it does not run.
+template <int D, bool kMod, bool kVar, bool kDet>
 __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     bwd_main(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
              const BwdArgs a) {
   using L = BwdSmem<D>;
+  static_assert(!kDet || D == 64, "D = 128 deterministic calls run the 128-row kernel");
   using R = BwdRoles<kMod || D == 64>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -362,10 +371,11 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     mbar_init(bar(L::kBarDQFull), 1);
     // the drain threads that read dQ^T: all 128, but in the deterministic mode
     // at D = 64 only drain warps 0-1, which hold its head-dim rows
-    mbar_init(bar(L::kBarDQEmpty), (D < 128 && a.deterministic) ? D : 128);
-    if (D < 128) {
+    mbar_init(bar(L::kBarDQEmpty), kDet ? D : 128);
+    if (kDet) {
       mbar_init(bar(L::kBarDQAdded), D);
-      mbar_init(bar(L::kBarDQAddedFree), 1);
+      mbar_init(bar(L::kBarDQAddedFree), 2);
+      for (int s = 0; s < 2; ++s) mbar_init(bar(L::kBarSemOk + s), 1);
     }
     mbar_init(bar(L::kBarDKVFull), 1);
     mbar_init(bar(L::kBarDKVEmpty), 128);
@@ -508,12 +518,10 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
       constexpr uint32_t kLboKT = (D == 128) ? (uint32_t)L::kKVBlockBytes : 0u;
       constexpr uint32_t kHi = sdesc_hi(1024);
       const int role = warp - R::kScoreWarp;  // 0: S^T, 1: dP^T, 2: gradients
-      // who issues dQ^T: the gradient thread after dK, or at D = 64 the dP^T
-      // thread, behind dP^T of the next block (measured: D = 64 atomic +5 to
-      // +7%, its deterministic mode 0 to -3%, D = 128 -12%).  A compile-time
-      // choice: testing the mode at run time in the issuing loops cost the
-      // atomic mode 2-3%.
-      constexpr bool dq_on_dp = (D == 64);
+      // who issues dQ^T: the gradient thread after dK, or in D = 64's atomic mode
+      // the dP^T thread, behind dP^T of the next block (measured: D = 64 atomic +5
+      // to +7%, deterministic -4% causal, -12% not, D = 128 -12%).
+      constexpr bool dq_on_dp = D == 64 && !kDet;
       uint32_t it = 0, unit = 0;
       bool ok = true;
       for (int ri = 0, u = read_unit(0, false); ok && u >= 0; u = read_unit(++ri, false), ++unit) {
@@ -802,14 +810,16 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     uint32_t it = 0, unit = 0;
     bool ok = true;
     constexpr int kAddWarps = D / 32;  // warps whose lanes hold real head-dim rows
-    // D = 64: the other two drain warps read no dQ^T; in the deterministic
-    // mode lane 0 of the first of them raises the semaphores (below)
-    constexpr bool kSemWarp = kAddWarps < 4;
-    // Deterministic mode with the semaphore warp: block it - 1's adds are
-    // handed over only once block it's dQ^T is complete (or the unit's dK/dV
-    // are), so that the arrive, which orders this thread's adds before it (a
-    // release at CTA scope), does not hold the drain while they are on their
-    // way to L2.  The free barrier keeps the arrives one phase per block.
+    // Deterministic mode (D = 64): drain warps 0-1 hold the head-dim rows and add;
+    // the other two read no dQ^T.  Lane 0 of warp 2 raises the semaphores, lane 0 of
+    // warp 3 waits for them, a block ahead (measured at B2 H16 S8192, causal / not:
+    // 441 / 386 TFLOP/s with the adding warps waiting for themselves, 537 / 444 so;
+    // with dQ^T issued behind dK, 560 / 515).
+    // Block it - 1's adds are handed over only once block it's dQ^T is complete (or
+    // the unit's dK/dV are), so that the arrive, which orders this thread's adds
+    // before it (a release at CTA scope), does not hold the drain while they are on
+    // their way to L2.  The free barrier keeps the arrives one phase per block.
+    const bool helper = kDet && wq >= kAddWarps;
     bool handoff_due = false;
     auto hand_off = [&]() -> bool {
       if (!handoff_due) return true;
@@ -818,105 +828,46 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
       mbar_arrive(bar(L::kBarDQAdded));
       return true;
     };
+    // Deterministic mode: kv tile j adds into accumulator j % G after the group's
+    // tiles before it in the dealing order, the first of them storing instead of
+    // adding: from the block's first contributor up (ascending order), or from its
+    // last contributor down (each head's tiles dealt highest first; causal tiles
+    // then reach a block in chain order, tile j starting at block 2j).  The tiles
+    // before this one:
+    auto turn_of = [&](const BwdUnit& w, int iq) -> int {
+      const int g = w.j % a.dq_groups;
+      return a.desc ? (group_last(qblk_last_contributor<kMod, kQB>(a, iq, w.kv_len), g, a.dq_groups) -
+                       w.j) / a.dq_groups
+                    : (w.j - group_first(qblk_first_contributor<kQB>(win_left<kMod>(a), iq), g,
+                                         a.dq_groups)) / a.dq_groups;
+    };
     for (int ri = 0, u = read_unit(0, true); ok && u >= 0; u = read_unit(++ri, true), ++unit) {
       const BwdUnit w = unit_of(u);
-      for (int t = 0; t < w.n_it; ++t, ++it) {
-        const int gi = t / w.n_blk;
-        const int iq = w.lo + (t - gi * w.n_blk);
-        const int bh = head_of(w, gi);
-        // query rows of the block that exist (kVar)
-        const int n_rows = kVar ? w.kv_len - iq * kQB : kQB;
-        if (kSemWarp && a.deterministic && wq >= kAddWarps) {
-          if (wq == kAddWarps) {
-            // once drain warps 0-1 have added block it (their arrives release
-            // at CTA scope what each thread added, this wait acquires it), one
-            // add with release order at GPU scope moves its semaphore
-            int good = 1;
-            if (lane == 0) {
-              if (!mbar_wait(bar(L::kBarDQAdded), it & 1, abort_flag)) {
-                good = 0;
-              } else {
-                mbar_arrive(bar(L::kBarDQAddedFree));
-                int* sem = a.sem + (size_t)(w.j % a.dq_groups) * a.sem_group_stride +
-                           bwd_sem_off<kVar, kQB>(a, w, bh, iq);
-                asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(sem) : "memory");
-              }
+      if constexpr (kDet) {
+        for (int t = 0; helper && t < w.n_it; ++t, ++it) {
+          const int gi = t / w.n_blk;
+          const int iq = w.lo + (t - gi * w.n_blk);
+          int* sem = a.sem + (size_t)(w.j % a.dq_groups) * a.sem_group_stride +
+                     bwd_sem_off<kVar, kQB>(a, w, head_of(w, gi), iq);
+          int good = 1;
+          if (lane == 0 && wq == kAddWarps) {
+            // once drain warps 0-1 have added block it (their arrives release at CTA
+            // scope what each thread added, this wait acquires it), one add with
+            // release order at GPU scope moves its semaphore
+            if (mbar_wait(bar(L::kBarDQAdded), it & 1, abort_flag)) {
+              mbar_arrive(bar(L::kBarDQAddedFree));
+              asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(sem) : "memory");
+            } else {
+              good = 0;
             }
-            ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-            if (!ok) break;
-          }
-          continue;
-        }
-        ok = warp_wait_b(bar(L::kBarDQFull), it & 1, abort_flag);
-        if (ok && kSemWarp && a.deterministic) ok = hand_off();
-        if (!ok) break;
-        tc_fence_after();
-        // Row r of dQ^T (head-dim index r, 64 queries) goes straight from TMEM
-        // to the fp32 accumulator: for each query the 32 lanes of a warp add
-        // 32 consecutive floats, one 128-byte line per instruction.
-        int good = 1;
-        if (!a.deterministic) {
-          // two 32-column halves, so that only 32 values are live at a time;
-          // the columns are released once the second half is read
-          float* dst = a.dq_acc + bwd_acc_off<kVar, kQB, D>(a, w, bh, iq) + r;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t v[32];
-            tmem_ld32(t_row + L::kColDQ + hf * 32, v);
-            if (hf == 1) {
-              tc_fence_before();
-              mbar_arrive(bar(L::kBarDQEmpty));
-            }
-            if (r < D) {
-              // all 64 rows in a branch of their own: a test before every add
-              // would undo the adds' spacing
-              if (!kVar || n_rows >= kQB) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(
-                                   dst + (size_t)(hf * 32 + e) * D),
-                               "f"(u2f(v[e]))
-                               : "memory");
-                  // D = 128: a pause after every eight adds spreads a block's
-                  // adds over its period; issued in one burst, they hold up the
-                  // shared-memory and barrier operations of the softmax warps
-                  // on the same SM sub-partitions (measured: +2.2% at B2 H16
-                  // S8192 causal, +2.5% at B4 H16 S2048; at D = 64, whose blocks
-                  // are shorter, the drain then falls behind: -11%)
-                  if (D == 128 && (e & 7) == 7) __nanosleep(16);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (hf * 32 + e < n_rows)
-                    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(
-                                     dst + (size_t)(hf * 32 + e) * D),
-                                 "f"(u2f(v[e]))
-                                 : "memory");
-              }
-            }
-          }
-        } else {
-          // deterministic mode: kv tile j adds into accumulator g = j % G after
-          // the group's tiles before it in the dealing order, the first of
-          // them storing instead of adding: from the block's first contributor
-          // up (ascending order), or from its last contributor down (each
-          // head's tiles dealt highest first; causal tiles then reach a block
-          // in chain order, tile j starting at block 2j)
-          const int g = w.j % a.dq_groups;
-          const int turn =
-              a.desc ? (group_last(qblk_last_contributor<kMod, kQB>(a, iq, w.kv_len), g, a.dq_groups) -
-                        w.j) / a.dq_groups
-                     : (w.j - group_first(qblk_first_contributor<kQB>(win_left<kMod>(a), iq), g,
-                                          a.dq_groups)) / a.dq_groups;
-          float* dst = a.dq_acc + (size_t)g * a.dq_group_stride + bwd_acc_off<kVar, kQB, D>(a, w, bh, iq) + r;
-          int* sem = a.sem + (size_t)g * a.sem_group_stride + bwd_sem_off<kVar, kQB>(a, w, bh, iq);
-          if (wq < kAddWarps && turn > 0) {
-            // the semaphore counts the group's finished adding warps (with
-            // the semaphore warp: the group's finished tiles)
-            if (lane == 0) {
+          } else if (lane == 0) {
+            // the semaphore counts the group's finished tiles; what the acquire saw
+            // goes to the drain with the arrive.  Behind the drain's block it - 1 the
+            // two barriers, one per parity of it, cannot lap the drain.
+            const int turn = turn_of(w, iq);
+            if (turn > 0) {
               const uint64_t t0 = global_timer_ns();
-              while (ld_acquire(sem) < turn * (kSemWarp ? 1 : kAddWarps)) {
+              while (ld_acquire(sem) < turn) {
                 if (*abort_flag || global_timer_ns() - t0 > kWaitTimeoutNs) {
                   *abort_flag = 1;
                   good = 0;
@@ -924,52 +875,94 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
                 }
               }
             }
-            good = __shfl_sync(0xffffffffu, good, 0);
-            __syncwarp();
-          }
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t v[32];
-            tmem_ld32(t_row + L::kColDQ + hf * 32, v);
-            if (hf == 1) {
-              tc_fence_before();
-              mbar_arrive(bar(L::kBarDQEmpty));
-            }
-            if (good && r < D) {
-              if (turn == 0) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!kVar || hf * 32 + e < n_rows) dst[(size_t)(hf * 32 + e) * D] = u2f(v[e]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!kVar || hf * 32 + e < n_rows)
-                  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(
-                                   dst + (size_t)(hf * 32 + e) * D),
-                               "f"(u2f(v[e]))
-                               : "memory");
+            if (good) {
+              mbar_arrive(bar(L::kBarSemOk + (it & 1)));
+              if (it > 0) {
+                if (mbar_wait(bar(L::kBarDQAdded), (it - 1) & 1, abort_flag))
+                  mbar_arrive(bar(L::kBarDQAddedFree));
+                else
+                  good = 0;
               }
             }
           }
-          if (wq < kAddWarps && good) {
-            if (kSemWarp) {
-              handoff_due = true;
+          ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+          if (!ok) break;
+        }
+      }
+      for (int t = 0; t < (helper ? 0 : w.n_it); ++t, ++it) {
+        const int gi = t / w.n_blk;
+        const int iq = w.lo + (t - gi * w.n_blk);
+        const int bh = head_of(w, gi);
+        // query rows of the block that exist (kVar)
+        const int n_rows = kVar ? w.kv_len - iq * kQB : kQB;
+        ok = warp_wait_b(bar(L::kBarDQFull), it & 1, abort_flag);
+        if (ok && kDet) ok = hand_off();
+        if (!ok) break;
+        tc_fence_after();
+        // Row r of dQ^T (head-dim index r, 64 queries) goes straight from TMEM
+        // to the fp32 accumulator: for each query the 32 lanes of a warp add
+        // 32 consecutive floats, one 128-byte line per instruction.
+        float* dst = a.dq_acc + bwd_acc_off<kVar, kQB, D>(a, w, bh, iq) + r;
+        bool first = false;  // this tile stores (deterministic mode)
+        if (kDet) {
+          dst += (size_t)(w.j % a.dq_groups) * a.dq_group_stride;
+          first = turn_of(w, iq) == 0;
+          if (!first) ok = warp_wait_b(bar(L::kBarSemOk + (it & 1)), (it >> 1) & 1, abort_flag);
+          if (!ok) break;
+        }
+        // two 32-column halves, so that only 32 values are live at a time; the
+        // columns are released once the second half is read.  Packed calls at
+        // D = 64 keep the loop: unrolled, 16384 tokens in 3 sequences of 16 heads
+        // took 870 us, not 787 (deterministic 1,066, not 1,000), but dense calls
+        // are 1-2% faster unrolled.
+        constexpr int kUnroll = kVar && D == 64 ? 1 : 2;
+#pragma unroll kUnroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t v[32];
+          tmem_ld32(t_row + L::kColDQ + hf * 32, v);
+          if (hf == 1) {
+            tc_fence_before();
+            mbar_arrive(bar(L::kBarDQEmpty));
+          }
+          if (r < D) {
+            // all 64 rows in a branch of their own: a test before every add
+            // would undo the adds' spacing (packed, D = 64, deterministic: 1,410
+            // -> 1,066 us for the tokens above)
+            if (!kVar || n_rows >= kQB) {
+              if (kDet && first) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) dst[(size_t)(hf * 32 + e) * D] = u2f(v[e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  red_add(dst + (size_t)(hf * 32 + e) * D, u2f(v[e]));
+                  // D = 128: a pause after every eight adds spreads a block's
+                  // adds over its period; issued in one burst, they hold up the
+                  // shared-memory and barrier operations of the softmax warps
+                  // on the same SM sub-partitions (measured: +2.2% at B2 H16
+                  // S8192 causal, +2.5% at B4 H16 S2048; at D = 64, whose blocks
+                  // are shorter, the drain then falls behind: -11%); none after
+                  // the last (+0.4% at S2048)
+                  if (D == 128 && (e & 7) == 7 && !(hf == 1 && e == 31)) __nanosleep(16);
+                }
+              }
+            } else if (kDet && first) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (hf * 32 + e < n_rows) dst[(size_t)(hf * 32 + e) * D] = u2f(v[e]);
             } else {
-              // the warp barrier orders every lane's adds before lane 0's
-              // release, which makes them visible before the count moves
-              __syncwarp();
-              if (lane == 0)
-                asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(sem) : "memory");
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (hf * 32 + e < n_rows) red_add(dst + (size_t)(hf * 32 + e) * D, u2f(v[e]));
             }
           }
         }
-        ok = good != 0;
-        if (!ok) break;
+        handoff_due = kDet;
       }
       if (!ok) break;
       // ---- dK, dV epilogue for key row kv
       ok = warp_wait_b(bar(L::kBarDKVFull), unit & 1, abort_flag);
-      if (kSemWarp && wq < kAddWarps && !hand_off()) ok = false;  // the unit's last block
+      if (kDet && !helper && !hand_off()) ok = false;  // the unit's last block
       if (!ok) break;
       tc_fence_after();
       // Each thread holds one key row; to store whole 64-byte row pieces per
@@ -1179,6 +1172,7 @@ std::atomic<int> g_bwd_kernel{FA_BWD_KERNEL_AUTO};
 
 template <int D>
 static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream) {
+  constexpr bool kDet = D == 64;  // bwd_main has a deterministic mode
   const CUtensorMap &tq = m.q, &tk = m.k, &tv = m.v, &tdo = m.dO;
   using L = BwdSmem<D>;
   int dev;
@@ -1186,10 +1180,12 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(bwd_main<D, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::kAllocBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(bwd_main<D, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::kAllocBytes) != cudaSuccess)
+    const auto set = [](auto kernel) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  L::kAllocBytes) == cudaSuccess;
+    };
+    if (!set(bwd_main<D, false, false, false>) || !set(bwd_main<D, true, false, false>) ||
+        !set(bwd_main<D, false, false, kDet>) || !set(bwd_main<D, true, false, kDet>))
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
@@ -1212,7 +1208,9 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
     // general kernel
     const bool mod =
         a.alibi || a.seqlens_k || !(a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal)));
-    const auto kernel = mod ? bwd_main<D, true, false> : bwd_main<D, false, false>;
+    const auto kernel = kDet && a.deterministic
+                            ? (mod ? bwd_main<D, true, false, kDet> : bwd_main<D, false, false, kDet>)
+                            : (mod ? bwd_main<D, true, false, false> : bwd_main<D, false, false, false>);
     const int threads =
         (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
     record_timing(false, stream);
@@ -1290,16 +1288,19 @@ int launch_bwd(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream) {
 template <int D>
 static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
                             cudaStream_t stream) {
+  constexpr bool kDet = D == 64;
   using L = BwdSmem<D>;
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    if (cudaFuncSetAttribute(bwd_main<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::kAllocBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(bwd_main<D, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::kAllocBytes) != cudaSuccess)
+    const auto set = [](auto kernel) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  L::kAllocBytes) == cudaSuccess;
+    };
+    if (!set(bwd_main<D, false, true, false>) || !set(bwd_main<D, true, true, false>) ||
+        !set(bwd_main<D, false, true, kDet>) || !set(bwd_main<D, true, true, kDet>))
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
@@ -1315,7 +1316,9 @@ static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
   // mode's chain)
   a.dyn = 1;
   const bool mod = !(a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal)));
-  const auto kernel = mod ? bwd_main<D, true, true> : bwd_main<D, false, true>;
+  const auto kernel = kDet && a.deterministic
+                          ? (mod ? bwd_main<D, true, true, kDet> : bwd_main<D, false, true, kDet>)
+                          : (mod ? bwd_main<D, true, true, false> : bwd_main<D, false, true, false>);
   const int threads = (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
   record_timing(false, stream);
   if (a.qblk_rows == 128) {
