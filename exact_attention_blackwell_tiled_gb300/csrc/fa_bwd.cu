@@ -40,12 +40,14 @@
 //                 lanes) and query columns c*(w/4).. of the block, c = 4*64/n
 //                 (32 or 16), so each SM sub-partition runs n/4 of them and
 //                 their latencies hide behind each other's work;
-//   warps n..n+3  dQ drain (one head-dim row per thread) and the dK/dV epilogue;
+//   warps n..n+3  dQ drain (one head-dim row per thread) and the dK/dV epilogue; at
+//                 D = 64, where warps n+2 and n+3 have no row, they raise and wait
+//                 for the semaphores of the deterministic mode;
 //   warp n+4      TMA producer: K_j, V_j per unit; Q_i, dO_i, LSE2_i, Delta_i
 //                 per block into a 3-stage ring;
 //   warp n+5      TMEM owner; one thread issues S^T;
-//   warp n+6      one thread issues dP^T (and, at D = 64, dQ^T of the previous
-//                 block behind it);
+//   warp n+6      one thread issues dP^T (and, in D = 64's atomic mode, dQ^T of the
+//                 previous block behind it);
 //   warp n+7      one thread issues dV, dK and dQ^T (dV and dK where warp n+6
 //                 issues dQ^T).
 // TMEM columns: S^T double buffer [0,64) [64,128); P^T and dS^T (bf16 pairs)
@@ -190,7 +192,10 @@ __global__ void __launch_bounds__(256) bwd_preprocess(const BwdArgs a) {
 
 // The same for a packed batch: a block takes (kv-tile item, q head) pairs of the
 // plan, whose 128 rows are also a tile of the sequence's queries.  Rows up to the
-// next multiple of the main kernel's block get LSE2 = +inf and Delta = 0.
+// next multiple of the main kernel's block get LSE2 = +inf and Delta = 0.  Delta is
+// taken, in fp32, from the O that the forward returned, which is rounded to bf16: for
+// rows with few keys that moves dS about as much as its own rounding to bf16 for the
+// products does (2^-9 of it each).
 template <int D>
 __global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a) {
   grid_dep_wait();
@@ -936,14 +941,17 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   red_add(dst + (size_t)(hf * 32 + e) * D, u2f(v[e]));
-                  // D = 128: a pause after every eight adds spreads a block's
-                  // adds over its period; issued in one burst, they hold up the
-                  // shared-memory and barrier operations of the softmax warps
-                  // on the same SM sub-partitions (measured: +2.2% at B2 H16
-                  // S8192 causal, +2.5% at B4 H16 S2048; at D = 64, whose blocks
-                  // are shorter, the drain then falls behind: -11%); none after
-                  // the last (+0.4% at S2048)
-                  if (D == 128 && (e & 7) == 7 && !(hf == 1 && e == 31)) __nanosleep(16);
+                  // D = 128: pauses spread a block's adds over its period; issued in one
+                  // burst, they hold up the shared-memory and barrier operations
+                  // of the softmax warps on the same SM sub-partitions.  One after
+                  // the 8th and the 16th add of each half, in packed calls the 24th
+                  // too (measured, main kernel, B2 H16 S8192 causal / B4 H16 S2048
+                  // / packed 16384 tokens in 3 sequences of 16 heads, us: none
+                  // 1,067 / 329 / 863; after every eight 1,090 / 336 / 836; these
+                  // 1,043 / 324 / 831, with the 24th's choice the other way round
+                  // 1,060 / 328 / 842).  D = 64, whose blocks are shorter, falls
+                  // behind with any pause (-11%)
+                  if (D == 128 && (e & 7) == 7 && e < (kVar ? 31 : 23)) __nanosleep(24);
                 }
               }
             } else if (kDet && first) {

@@ -411,7 +411,8 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
     // kv heads dealt together, so that their q, dO, dQ accumulators and K / V stay
     // in L2, as in the dense call; in the deterministic mode all of them, since tiles
     // of one head that run side by side wait for each other (16384 tokens in 3
-    // sequences, 16 heads of 64: 1,961 -> 1,670 us)
+    // sequences, 16 heads of 64: 1,961 -> 1,670 us, before the waits were taken off
+    // the adding warps, which made it 1,000)
     const double per_kv_head = (double)(Hq / Hkv) * T * D * (4.0 + 4.0) + (double)T * D * 4.0;
     const double fit = kBwdGroupBytes / per_kv_head;
     const int hg = deterministic || fit >= Hkv ? Hkv : (fit < 1.0 ? 1 : (int)fit);
