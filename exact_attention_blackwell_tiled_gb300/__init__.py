@@ -2,14 +2,14 @@
 
 Every computation runs in the library's CUDA kernels; this module only checks
 tensor properties, allocates outputs with torch and passes raw pointers plus the
-current CUDA stream through the C ABI declared in ``include/fa.h``.  There is no
+current CUDA stream through the C ABI declared in ``include/fa.h`` (the packed and
+cache calls do so in a compiled module, csrc/binding.cpp).  There is no
 CPU or eager fallback: if the library is missing or a tensor is not a
 contiguous bf16 CUDA tensor, the call raises.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -413,83 +413,20 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
                             seqlens_k)
 
 
-# The calls below serve single tokens, where the host's time is most of a call's, so
-# they ask torch for as little as the checks need: device indices instead of device
-# objects and guards, raw stream handles, sizes looked up once per shape.
+# The calls below also serve single tokens, where the host's time is most of a
+# call's, so their checks and allocations are compiled (csrc/binding.cpp).
 
-def _raw_stream(stream, index):
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+_COMPILED = None
 
 
-def _elsewhere(index):
-    """Whether device `index` is not the current one (the call is then repeated under
-    a guard)."""
-    return torch._C._cuda_getDevice() != index
-
-
-def _packed(t, name, index=None, shape=None):
-    """Checks a packed [T, H, D] bf16 CUDA tensor (of `shape` on device `index`) and
-    returns its PackedStride by reference, or None where it is contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head dimension]")
-    if shape is not None and (t.shape != shape or t.get_device() != index):
-        raise ValueError(f"{name} must be {tuple(shape)} on the same device")
-    if t.is_contiguous():
-        return None
-    T, H, D = t.shape
-    if D > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name} must have contiguous elements")
-    # the stride of a dimension of one element is arbitrary: give the kernel a valid one
-    head = t.stride(1) if H > 1 else D
-    return ctypes.byref(PackedStride(t.stride(0) if T > 1 else max(H * D, head), head))
-
-
-def _packed_kv(q, k, v):
-    """Checks packed q, k, v together; returns their strides."""
-    qs = _packed(q, "q")
-    ks = _packed(k, "k")
-    T, _, D = q.shape
-    if k.shape[0] != T or k.shape[2] != D or k.get_device() != q.get_device():
-        raise ValueError("k must have q's tokens, head dimension and device")
-    return qs, ks, _packed(v, "v", k.get_device(), k.shape)
-
-
-def _given(t, shape, dtype, index, name):
-    """Checks a contiguous tensor of the caller."""
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype
-            or t.get_device() != index or t.shape != torch.Size(shape) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on the inputs' "
-                         "device")
-    return t
-
-
-def _new(shape, dtype, device, stream):
-    """A new tensor that `stream` may write."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:  # keep its memory until that stream has passed
-        t.record_stream(stream)
-    return t
-
-
-def _workspace(t, nbytes, like, stream):
-    """(tensor, bytes) of the caller's workspace, or of a new one that `stream` may use."""
-    if t is None:
-        t = _new(nbytes or 1, torch.uint8, like.device, stream)
-    elif not t.is_cuda or t.get_device() != like.get_device() or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return t, t.numel() * t.element_size()
-
-
-def _int32(t, n, index, name):
-    """Checks an int32 CUDA vector of n elements (n None: any number); returns n."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.int32
-            or t.dim() != 1 or not t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous int32 vector on the inputs' device")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} elements")
-    return t.shape[0]
+def _compiled():
+    global _COMPILED
+    if _COMPILED is None:
+        lib()  # raises if the library has not been built
+        from . import _binding
+        _binding.set_error(FAError)
+        _COMPILED = _binding
+    return _COMPILED
 
 
 def _var_window(causal, window):
@@ -500,7 +437,6 @@ def _var_window(causal, window):
     return int(window[0]), int(window[1])
 
 
-@functools.lru_cache(maxsize=4096)
 def varlen_workspace_bytes(B, T, Hq, Hkv, D, backward=False, deterministic=False) -> int:
     return int(lib().fa_varlen_workspace_bytes(B, T, Hq, Hkv, D, int(bool(backward)),
                                                int(bool(deterministic))))
@@ -519,32 +455,8 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: to
     Returns (o [T,Hq,D] bf16, lse [Hq,T] fp32); tokens of no sequence are not
     written.  fwd_status() reports a cu_seqlens that does not ascend in [0, T].
     """
-    qs, ks, vs = _packed_kv(q, k, v)
-    index = q.get_device()
-    if _elsewhere(index):
-        with torch.cuda.device(index):
-            return fwd_varlen(q, k, v, cu_seqlens, causal, scale, window, out, lse, workspace,
-                              stream)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
     wl, wr = _var_window(causal, window)
-    B = _int32(cu_seqlens, None, index, "cu_seqlens") - 1
-    if out is None:
-        out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
-    else:
-        _given(out, (T, Hq, D), torch.bfloat16, index, "out")
-    if lse is None:
-        lse = _new((Hq, T), torch.float32, q.device, stream)
-    else:
-        _given(lse, (Hq, T), torch.float32, index, "lse")
-    ws, nbytes = _workspace(workspace, varlen_workspace_bytes(B, T, Hq, Hkv, D), q, stream)
-    rc = lib().fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                             lse.data_ptr(), cu_seqlens.data_ptr(), B, T, Hq, Hkv, D, qs, ks, vs,
-                             wl, wr, 1.0 / math.sqrt(D) if scale is None else scale,
-                             ws.data_ptr(), nbytes, _raw_stream(stream, index))
-    if rc != FA_OK:
-        raise FAError("fa_fwd_varlen", rc)
-    return out, lse
+    return _compiled().fwd_varlen(q, k, v, cu_seqlens, wl, wr, scale, out, lse, workspace, stream)
 
 
 def bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal: bool = False, scale: float | None = None,
@@ -554,34 +466,9 @@ def bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal: bool = False, scale: flo
     [T,Hkv,D]) bf16, contiguous; tokens of no sequence are not written.  o, do
     and lse are contiguous; the other arguments as in fwd_varlen, and as given
     to it."""
-    qs, ks, vs = _packed_kv(q, k, v)
-    index = q.get_device()
-    if _elsewhere(index):
-        with torch.cuda.device(index):
-            return bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal, scale, window,
-                              deterministic, workspace, dq, dk, dv, stream)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    bf = torch.bfloat16
-    _given(o, q.shape, bf, index, "o")
-    _given(do, q.shape, bf, index, "do")
-    _given(lse, (Hq, T), torch.float32, index, "lse")
     wl, wr = _var_window(causal, window)
-    B = _int32(cu_seqlens, None, index, "cu_seqlens") - 1
-    ws, nbytes = _workspace(workspace,
-                            varlen_workspace_bytes(B, T, Hq, Hkv, D, True, bool(deterministic)),
-                            q, stream)
-    dq = _new(q.shape, bf, q.device, stream) if dq is None else _given(dq, q.shape, bf, index, "dq")
-    dk = _new(k.shape, bf, q.device, stream) if dk is None else _given(dk, k.shape, bf, index, "dk")
-    dv = _new(k.shape, bf, q.device, stream) if dv is None else _given(dv, k.shape, bf, index, "dv")
-    rc = lib().fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                             lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                             cu_seqlens.data_ptr(), B, T, Hq, Hkv, D, qs, ks, vs, wl, wr,
-                             1.0 / math.sqrt(D) if scale is None else scale, ws.data_ptr(), nbytes,
-                             int(bool(deterministic)), _raw_stream(stream, index))
-    if rc != FA_OK:
-        raise FAError("fa_bwd_varlen", rc)
-    return dq, dk, dv
+    return _compiled().bwd_varlen(q, k, v, o, do, lse, cu_seqlens, wl, wr, scale, deterministic,
+                                  workspace, dq, dk, dv, stream)
 
 
 class _AttentionVarlen(torch.autograd.Function):
@@ -617,38 +504,6 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic)
 
 
-def _cache4(cache, D):
-    """(pages, Hkv, page size) of a 4-bit cache tensor for head dimension D."""
-    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.uint8:
-        raise TypeError("cache must be a uint8 CUDA tensor")
-    if cache.dim() != 3 or not cache.is_contiguous() or D not in (64, 128):
-        raise ValueError("cache must be a contiguous [pages, Hkv, bytes] tensor of cache4_empty, "
-                         "with head dimension 64 or 128")
-    pages, Hkv, nbytes = cache.shape
-    page, rest = divmod(nbytes, D + D // 4)
-    if rest or page not in (16, 32, 64, 128):
-        raise ValueError(f"cache pages of {nbytes} bytes do not hold tokens of {D} elements")
-    return pages, Hkv, page
-
-
-def _page_table(t, B, index, name="page_table"):
-    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.int32
-            or not t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous int32 tensor on the cache's device")
-    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [{B}, pages per sequence]")
-    return t.shape[1]
-
-
-def _weights(t, B, Hkv, index, name):
-    if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != torch.float32
-            or not t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous fp32 tensor on the cache's device")
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != Hkv or t.shape[2] < 1:
-        raise ValueError(f"{name} must be [{B}, {Hkv}, slots]")
-    return t.shape[2]
-
-
 def cache4_empty(num_pages: int, Hkv: int, D: int, page_size: int = 64, device="cuda"):
     """A paged 4-bit key/value cache (include/fa.h, fa_cache4_page_bytes): uint8
     [num_pages, Hkv, bytes of a page and head], zeroed.  page_size: 16, 32, 64 or
@@ -668,27 +523,7 @@ def cache4_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_ta
     ``cu_seqlens`` int32 [B+1] packs several per sequence, None means one each
     (T == B).  cache_lens is left as it is: add the new tokens to it afterwards.
     """
-    ks = _packed(k, "k")
-    index = k.get_device()
-    vs = _packed(v, "v", index, k.shape)
-    T, Hkv, D = k.shape
-    pages, heads, page = _cache4(cache, D)
-    if heads != Hkv or cache.get_device() != index:
-        raise ValueError("cache and k must have the same kv heads and device")
-    if _elsewhere(index):
-        with torch.cuda.device(index):
-            return cache4_append(cache, k, v, page_table, cache_lens, cu_seqlens, stream)
-    B = _int32(cache_lens, None, index, "cache_lens")
-    width = _page_table(page_table, B, index)
-    cu = None
-    if cu_seqlens is not None:
-        _int32(cu_seqlens, B + 1, index, "cu_seqlens")
-        cu = cu_seqlens.data_ptr()
-    rc = lib().fa_cache4_append(cache.data_ptr(), pages, page, k.data_ptr(), v.data_ptr(), ks, vs, B,
-                                T, Hkv, D, cu, cache_lens.data_ptr(), page_table.data_ptr(), width,
-                                _raw_stream(stream, index))
-    if rc != FA_OK:
-        raise FAError("fa_cache4_append", rc)
+    _compiled().cache4_append(cache, k, v, page_table, cache_lens, cu_seqlens, stream)
 
 
 def cache4_read(cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tensor | None,
@@ -696,37 +531,13 @@ def cache4_read(cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tens
     """The values the cache holds (fa_cache4_read): slots first[b] .. first[b] +
     count[b] - 1 of every sequence (``first`` None: from 0) as bf16 k, v
     [B,Hkv,S,D], zero from count[b] on."""
-    pages, Hkv, page = _cache4(cache, D)
-    index = cache.get_device()
-    if _elsewhere(index):
-        with torch.cuda.device(index):
-            return cache4_read(cache, page_table, first, count, S, D, k, v, stream)
-    B = _int32(count, None, index, "count")
-    width = _page_table(page_table, B, index)
-    at = None
-    if first is not None:
-        _int32(first, B, index, "first")
-        at = first.data_ptr()
-    shape, bf = (B, Hkv, S, D), torch.bfloat16
-    k = _new(shape, bf, cache.device, stream) if k is None else _given(k, shape, bf, index, "k")
-    v = _new(shape, bf, cache.device, stream) if v is None else _given(v, shape, bf, index, "v")
-    rc = lib().fa_cache4_read(cache.data_ptr(), pages, page, k.data_ptr(), v.data_ptr(), B, Hkv, S, D,
-                              at, count.data_ptr(), page_table.data_ptr(), width,
-                              _raw_stream(stream, index))
-    if rc != FA_OK:
-        raise FAError("fa_cache4_read", rc)
-    return k, v
-
-
-@functools.lru_cache(maxsize=4096)
-def _attend_bytes(index, B, Hq, Hkv, D, weight_slots):
-    return int(lib().fa_cache4_attend_workspace_bytes(B, Hq, Hkv, D, weight_slots))
+    return _compiled().cache4_read(cache, page_table, first, count, S, D, k, v, stream)
 
 
 def cache4_attend_workspace_bytes(B, Hq, Hkv, D, weight_slots: int = 0) -> int:
     """Workspace bytes of cache4_attend on the current device; weight_slots: the last
     dimension of its weights, 0 without."""
-    return _attend_bytes(torch._C._cuda_getDevice(), B, Hq, Hkv, D, int(weight_slots))
+    return int(lib().fa_cache4_attend_workspace_bytes(B, Hq, Hkv, D, int(weight_slots)))
 
 
 def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
@@ -743,46 +554,8 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     at what the tensor holds there, so it begins as zeros.
     Returns (o [B,Hq,D] bf16, lse [B,Hq] fp32); o = 0, lse = -inf without tokens.
     """
-    _packed(q, "q")
-    index = q.get_device()
-    B, Hq, D = q.shape
-    pages, Hkv, page = _cache4(cache, D)
-    if cache.get_device() != index:
-        raise ValueError("cache and q must be on one device")
-    if _elsewhere(index):
-        with torch.cuda.device(index):
-            return cache4_attend(q, cache, page_table, cache_lens, scale, weights, weights_out, out,
-                                 lse, workspace, stream)
-    _int32(cache_lens, B, index, "cache_lens")
-    width = _page_table(page_table, B, index)
-    slots, w_in, w_out = 0, None, None
-    if weights is not None:
-        slots = _weights(weights, B, Hkv, index, "weights")
-        w_in = w_out = weights.data_ptr()
-    if weights_out is not None:
-        n = _weights(weights_out, B, Hkv, index, "weights_out")
-        if weights is not None and n != slots:
-            raise ValueError("weights_out must have weights' shape")
-        slots, w_out = n, weights_out.data_ptr()
-    if out is None:
-        out = _new((B, Hq, D), torch.bfloat16, q.device, stream)
-    else:
-        _given(out, (B, Hq, D), torch.bfloat16, index, "out")
-    if lse is None:
-        lse = _new((B, Hq), torch.float32, q.device, stream)
-    else:
-        _given(lse, (B, Hq), torch.float32, index, "lse")
-    ws, nbytes = _workspace(workspace, _attend_bytes(index, B, Hq, Hkv, D, slots), q, stream)
-    # the stride of a dimension of one element is arbitrary
-    rc = lib().fa_cache4_attend(q.data_ptr(), q.stride(0) if B > 1 else 0,
-                                q.stride(1) if Hq > 1 else 0, cache.data_ptr(), pages, page,
-                                out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D,
-                                cache_lens.data_ptr(), page_table.data_ptr(), width,
-                                1.0 / math.sqrt(D) if scale is None else scale, w_in, w_out, slots,
-                                ws.data_ptr(), nbytes, _raw_stream(stream, index))
-    if rc != FA_OK:
-        raise FAError("fa_cache4_attend", rc)
-    return out, lse
+    return _compiled().cache4_attend(q, cache, page_table, cache_lens, scale, weights, weights_out,
+                                     out, lse, workspace, stream)
 
 
 def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torch.Tensor,
@@ -795,39 +568,8 @@ def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torc
     Returns (src int32 [B,Hkv,budget]: each kept token's old slot, -1 behind the
     last; weights fp32 [B,Hkv,budget], 0 behind the last; lens int32 [B]).
     """
-    pages, Hkv, page = _cache4(cache, D)
-    index = cache.get_device()
-    if _elsewhere(index):
-        with torch.cuda.device(index):
-            return cache4_evict(cache, page_table, cache_lens, weights, out_page_table, D, budget,
-                                recent, src, weights_out, lens_out, stream)
-    B = _int32(cache_lens, None, index, "cache_lens")
-    width = _page_table(page_table, B, index)
-    out_width = _page_table(out_page_table, B, index, "out_page_table")
-    cap = _weights(weights, B, Hkv, index, "weights")
-    if budget < 1 or not 0 <= recent <= budget or out_width * page < budget:
-        raise ValueError("budget must be positive, at least recent and within out_page_table")
-    shape = (B, Hkv, budget)
-    if src is None:
-        src = _new(shape, torch.int32, cache.device, stream)
-    else:
-        _given(src, shape, torch.int32, index, "src")
-    if weights_out is None:
-        weights_out = _new(shape, torch.float32, cache.device, stream)
-    else:
-        _given(weights_out, shape, torch.float32, index, "weights_out")
-    if lens_out is None:
-        lens_out = _new((B,), torch.int32, cache.device, stream)
-    else:
-        _given(lens_out, (B,), torch.int32, index, "lens_out")
-    rc = lib().fa_cache4_evict(cache.data_ptr(), pages, page, weights.data_ptr(), cap,
-                               cache_lens.data_ptr(), page_table.data_ptr(), width, B, Hkv, D,
-                               budget, recent, out_page_table.data_ptr(), out_width, src.data_ptr(),
-                               weights_out.data_ptr(), lens_out.data_ptr(),
-                               _raw_stream(stream, index))
-    if rc != FA_OK:
-        raise FAError("fa_cache4_evict", rc)
-    return src, weights_out, lens_out
+    return _compiled().cache4_evict(cache, page_table, cache_lens, weights, out_page_table, D, budget,
+                                    recent, src, weights_out, lens_out, stream)
 
 
 def cache4_status(stream=None) -> int:

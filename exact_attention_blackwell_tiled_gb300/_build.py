@@ -1,12 +1,14 @@
 """Build libfa.so in-tree with nvcc for sm_103a (one -gencode, sources compiled in
-parallel, no cmake)."""
+parallel, no cmake), and the compiled part of the Python binding with g++."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,6 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libfa.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_ring.cu", "fa_bwd.cu", "fa_bwd_q128.cu", "fa_bwd_pair.cu", "fa_merge.cu", "fa_noalloc.cu",
            "fa_varlen.cu", "fa_cache4.cu", "fa_cache4_attend.cu"]
 HEADERS = ["fa_internal.h", "ptx.cuh", "exp2.cuh", "bwd_common.cuh", "fwd_common.cuh",
@@ -29,17 +33,49 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _newer(path: str, deps: list[str]) -> bool:
+    """Whether `path` is missing or one of `deps` is newer."""
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "fa.h")]
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
+
+
+def _build_binding() -> None:
+    """csrc/binding.cpp against this machine's torch (found, not imported) and libfa.so."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found")
+    inc = [INCLUDE, os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{d}" for d in inc], BINDING_SOURCE,
+          "-o", tmp, f"-L{PKG}", "-l:libfa.so", "-Wl,-rpath,$ORIGIN",
+          "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+         "g++ for binding.cpp")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = ()) -> str:
-    if not force and not _stale():
-        return LIB_PATH
+    header = os.path.join(INCLUDE, "fa.h")
+    if force or _newer(LIB_PATH, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [header]):
+        _build_library(verbose, extra)
+    if force or _newer(BINDING_PATH, [BINDING_SOURCE, header]):
+        _build_binding()
+    return LIB_PATH
+
+
+def _build_library(verbose: bool, extra: tuple[str, ...]) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
 
@@ -48,10 +84,7 @@ def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = (
         cmd = [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
+        return obj, _run(cmd, f"nvcc for {src}")
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
@@ -59,12 +92,8 @@ def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = (
         for _, log in results:
             sys.stderr.write(log)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]], "link")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -104,7 +104,7 @@ def test_evict_refusals(L):
 def test_binding_refusals():
     c = torch.zeros(2, 1, 16 * 80, dtype=torch.uint8)
     with pytest.raises(TypeError):
-        fa._cache4(c, 64)                  # host memory
+        fa.cache4_read(c, None, None, None, 1, 64)                  # host memory
     with pytest.raises(TypeError):
         fa.cache4_append(c, torch.zeros(1, 1, 64, dtype=torch.bfloat16), None, None, None)
 
@@ -280,6 +280,69 @@ def test_attend_is_the_same_at_other_magnitudes(gpu, D, shift):
     fa.cache4_append(cache, (k / up).cuda(), (v * up).cuda(), table, torch.zeros_like(lens), _i32(cu))
     o2, lse2 = fa.cache4_attend(q * up, cache, table, lens, weights=w[1])
     assert torch.equal(o * up, o2) and torch.equal(lse, lse2) and torch.equal(w[0], w[1])
+    assert fa.cache4_status() == fa.FA_OK
+
+
+@pytest.mark.gpu
+def test_binding_refusals_of_device_tensors(gpu):
+    D, Hkv = 64, 2
+    cache, table, lens, *_ = _filled([40, 7], Hkv, D, 16)
+    q = torch.randn(2, 4, D, device="cuda").to(torch.bfloat16)
+    k = torch.randn(2, Hkv, D, device="cuda").to(torch.bfloat16)
+    w = torch.zeros(2, Hkv, 48, device="cuda")
+    out = table + table.numel()
+    good = dict(q=q, cache=cache, page_table=table, cache_lens=lens, weights=w)
+    fa.cache4_attend(**good)
+
+    def attend(error, **kw):
+        with pytest.raises(error):
+            fa.cache4_attend(**{**good, **kw})
+
+    attend(TypeError, q=q.float())
+    attend(TypeError, q=q.cpu())
+    attend(ValueError, q=q[0])
+    attend(ValueError, q=q.transpose(1, 2).contiguous().transpose(1, 2))
+    attend(TypeError, cache=cache.cpu())
+    attend(TypeError, cache=cache.view(torch.int8))
+    attend(ValueError, cache=cache[:, :, :-1])
+    attend(ValueError, cache=cache[:, :, :-80].contiguous())
+    attend(TypeError, page_table=table.long())
+    attend(TypeError, page_table=table.cpu())
+    attend(ValueError, page_table=table[:1])
+    attend(TypeError, cache_lens=lens.long())
+    attend(TypeError, cache_lens=[40, 7])
+    attend(ValueError, cache_lens=lens[:1])
+    attend(TypeError, weights=w.double())
+    attend(ValueError, weights=w[:, :1].contiguous())
+    attend(ValueError, weights_out=torch.zeros(2, Hkv, 47, device="cuda"))
+    attend(ValueError, out=torch.empty(2, 4, D, device="cuda"))
+    attend(ValueError, lse=torch.empty(4, 2, device="cuda"))
+    attend(ValueError, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    attend(fa.FAError, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    attend(fa.FAError, scale=math.inf)
+    attend(TypeError, scale="1")
+    attend(fa.FAError, q=q[:, :3])  # three query heads to two kv heads
+    with pytest.raises(ValueError):
+        fa.cache4_append(cache, k, k[:, :1], table, lens)
+    with pytest.raises(ValueError):
+        fa.cache4_append(cache, k[:, :1], k[:, :1], table, lens)
+    with pytest.raises(fa.FAError):  # one token per sequence without boundaries
+        fa.cache4_append(cache, k[:1], k[:1], table, lens)
+    with pytest.raises(ValueError):
+        fa.cache4_append(cache, k, k, table, lens, _i32([0, 2]))
+    with pytest.raises(fa.FAError):
+        fa.cache4_read(cache, table, None, lens, -1, D)
+    with pytest.raises(ValueError):
+        fa.cache4_read(cache, table, lens[:1], lens, 8, D)
+    with pytest.raises(ValueError):
+        fa.cache4_read(cache, table, None, lens, 8, 96)
+    for budget, recent in ((0, 0), (8, 9), (8, -1), (table.shape[1] * 16 + 1, 0)):
+        with pytest.raises(ValueError):
+            fa.cache4_evict(cache, table, lens, w, out, D, budget, recent)
+    with pytest.raises(TypeError):
+        fa.cache4_evict(cache, table, lens, w, out, D, 8.0)
+    with pytest.raises(OverflowError):
+        fa.cache4_evict(cache, table, lens, w, out, D, 1 << 40)
     assert fa.cache4_status() == fa.FA_OK
 
 

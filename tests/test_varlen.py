@@ -90,7 +90,7 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         fa._var_window(True, (-1, 0))
     with pytest.raises(TypeError):
-        fa._int32(cu, None, 0, "cu_seqlens")
+        fa.fwd_varlen(4, x, x, cu)
 
 
 def test_reference_gradient():
@@ -256,6 +256,37 @@ def test_autograd(gpu):
     for x, n in zip(leaves, ("dq", "dk", "dv")):
         assert_within(x.grad, ref[n], ref[n + "_tol"], n)
         assert bool((x.grad[cu[-1]:] == 0).all())
+
+
+@pytest.mark.gpu
+def test_binding_refusals_of_device_tensors(gpu):
+    q, k, v, do = (x.cuda() for x in _inputs(6, 4, 2, 64, 3))
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    o, lse = fa.fwd_varlen(q, k, v, cu)
+
+    def refuses(error, fn, *a, **kw):
+        with pytest.raises(error):
+            fn(*a, **kw)
+
+    refuses(TypeError, fa.fwd_varlen, q.half(), k, v, cu)
+    refuses(TypeError, fa.fwd_varlen, q, k.cpu(), v, cu)
+    refuses(ValueError, fa.fwd_varlen, q[None], k, v, cu)
+    refuses(ValueError, fa.fwd_varlen, q, k[:5], v[:5], cu)
+    refuses(ValueError, fa.fwd_varlen, q, k, v[:, :1], cu)
+    refuses(TypeError, fa.fwd_varlen, q, k, v, cu.long())
+    refuses(TypeError, fa.fwd_varlen, q, k, v, cu.cpu())
+    refuses(fa.FAError, fa.fwd_varlen, q, k, v, cu[:1])  # no sequence
+    refuses(fa.FAError, fa.fwd_varlen, q[:, :3], k, v, cu)
+    refuses(fa.FAError, fa.fwd_varlen, q[:, :1].expand(6, 4, 64), k, v, cu)  # heads 0 apart
+    refuses(ValueError, fa.fwd_varlen, q, k, v, cu, out=torch.empty_like(q)[:5])
+    refuses(ValueError, fa.fwd_varlen, q, k, v, cu, lse=lse.T.contiguous())
+    refuses(ValueError, fa.fwd_varlen, q, k, v, cu, causal=True, window=(-1, 0))
+    refuses(ValueError, fa.bwd_varlen, q, k, v, o[:5], do, lse, cu)
+    refuses(ValueError, fa.bwd_varlen, q, k, v, o, do.float(), lse, cu)
+    refuses(ValueError, fa.bwd_varlen, q, k, v, o, do, lse, cu, dk=torch.empty_like(q))
+    refuses(fa.FAError, fa.bwd_varlen, q, k, v, o, do, lse, cu,
+            workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert fa.fwd_status() == fa.FA_OK
 
 
 @pytest.mark.gpu
