@@ -43,6 +43,23 @@ void check(const char* function, int code) {
   throw Raised{};
 }
 
+// One call of the C ABI, other Python threads running meanwhile (a launch can wait for
+// room in its queue).
+struct Unlocked {
+  PyThreadState* threads = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(threads); }
+};
+
+template <typename F>
+void call(const char* function, F f) {
+  int code;
+  {
+    const Unlocked unlocked;
+    code = f();
+  }
+  check(function, code);
+}
+
 // ------------------------------------------------------------------ arguments
 
 int to_int(PyObject* o) {
@@ -262,11 +279,12 @@ PyObject* fwd_varlen(PyObject* const* a) {
   const at::Tensor lse = output(a[8], {x.Hq, x.T}, at::kFloat, x.device, "lse", a[10]);
   const size_t need = a[9] == Py_None ? fa_varlen_workspace_bytes(B, x.T, x.Hq, x.Hkv, x.D, 0, 0) : 0;
   const at::Tensor ws = workspace(a[9], need, x.device, a[10]);
-  check("fa_fwd_varlen",
-        fa_fwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
-                      static_cast<float*>(lse.data_ptr()), cu, B, x.T, x.Hq, x.Hkv, x.D,
-                      x.q.stride(), x.k.stride(), x.v.stride(), wl, wr, scale, ws.data_ptr(),
-                      ws.nbytes(), place.stream));
+  call("fa_fwd_varlen", [&] {
+    return fa_fwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
+                         static_cast<float*>(lse.data_ptr()), cu, B, x.T, x.Hq, x.Hkv, x.D,
+                         x.q.stride(), x.k.stride(), x.v.stride(), wl, wr, scale, ws.data_ptr(),
+                         ws.nbytes(), place.stream);
+  });
   return tuple(o, lse);
 }
 
@@ -290,12 +308,13 @@ PyObject* bwd_varlen(PyObject* const* a) {
   const at::Tensor dq = output(a[12], q_shape, at::kBFloat16, x.device, "dq", stream);
   const at::Tensor dk = output(a[13], k_shape, at::kBFloat16, x.device, "dk", stream);
   const at::Tensor dv = output(a[14], k_shape, at::kBFloat16, x.device, "dv", stream);
-  check("fa_bwd_varlen",
-        fa_bwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
-                      dO.data_ptr(), static_cast<const float*>(lse.data_ptr()), dq.data_ptr(),
-                      dk.data_ptr(), dv.data_ptr(), cu, B, x.T, x.Hq, x.Hkv, x.D, x.q.stride(),
-                      x.k.stride(), x.v.stride(), wl, wr, scale, ws.data_ptr(), ws.nbytes(), det,
-                      place.stream));
+  call("fa_bwd_varlen", [&] {
+    return fa_bwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
+                         dO.data_ptr(), static_cast<const float*>(lse.data_ptr()), dq.data_ptr(),
+                         dk.data_ptr(), dv.data_ptr(), cu, B, x.T, x.Hq, x.Hkv, x.D, x.q.stride(),
+                         x.k.stride(), x.v.stride(), wl, wr, scale, ws.data_ptr(), ws.nbytes(),
+                         det, place.stream);
+  });
   return tuple(dq, dk, dv);
 }
 
@@ -313,9 +332,10 @@ PyObject* cache4_append(PyObject* const* a) {
   int width;
   const int* table = page_table(a[3], B, device, &width);
   const int* cu = a[5] == Py_None ? nullptr : int32s(a[5], B + 1, device, "cu_seqlens");
-  check("fa_cache4_append",
-        fa_cache4_append(c.p, c.pages, c.page, k.t->data_ptr(), v.t->data_ptr(), k.stride(), v.stride(),
-                         (int)B, T, Hkv, D, cu, lens, table, width, place.stream));
+  call("fa_cache4_append", [&] {
+    return fa_cache4_append(c.p, c.pages, c.page, k.t->data_ptr(), v.t->data_ptr(), k.stride(),
+                            v.stride(), (int)B, T, Hkv, D, cu, lens, table, width, place.stream);
+  });
   Py_RETURN_NONE;
 }
 
@@ -332,8 +352,10 @@ PyObject* cache4_read(PyObject* const* a) {
   if (S < 0) check("fa_cache4_read", 1);
   const at::Tensor k = output(a[6], {B, c.Hkv, S, D}, at::kBFloat16, c.device, "k", a[8]);
   const at::Tensor v = output(a[7], {B, c.Hkv, S, D}, at::kBFloat16, c.device, "v", a[8]);
-  check("fa_cache4_read", fa_cache4_read(c.p, c.pages, c.page, k.data_ptr(), v.data_ptr(), (int)B, c.Hkv,
-                                         S, D, first, count, table, width, place.stream));
+  call("fa_cache4_read", [&] {
+    return fa_cache4_read(c.p, c.pages, c.page, k.data_ptr(), v.data_ptr(), (int)B, c.Hkv, S, D,
+                          first, count, table, width, place.stream);
+  });
   return tuple(k, v);
 }
 
@@ -364,11 +386,13 @@ PyObject* cache4_attend(PyObject* const* a) {
       a[9] == Py_None ? fa_cache4_attend_workspace_bytes(B, Hq, c.Hkv, D, slots) : 0;
   const at::Tensor ws = workspace(a[9], need, device, stream);
   // the stride of a dimension of one element is arbitrary
-  check("fa_cache4_attend",
-        fa_cache4_attend(q.t->data_ptr(), B > 1 ? q.t->stride(0) : 0, Hq > 1 ? q.t->stride(1) : 0, c.p,
-                         c.pages, c.page, o.data_ptr(), static_cast<float*>(lse.data_ptr()), B, Hq,
-                         c.Hkv, D, lens, table, width, scale, w_in, w_out, slots, ws.data_ptr(),
-                         ws.nbytes(), place.stream));
+  call("fa_cache4_attend", [&] {
+    return fa_cache4_attend(q.t->data_ptr(), B > 1 ? q.t->stride(0) : 0,
+                            Hq > 1 ? q.t->stride(1) : 0, c.p, c.pages, c.page, o.data_ptr(),
+                            static_cast<float*>(lse.data_ptr()), B, Hq, c.Hkv, D, lens, table,
+                            width, scale, w_in, w_out, slots, ws.data_ptr(), ws.nbytes(),
+                            place.stream);
+  });
   return tuple(o, lse);
 }
 
@@ -390,11 +414,12 @@ PyObject* cache4_evict(PyObject* const* a) {
   const at::Tensor src = output(a[8], {B, c.Hkv, budget}, at::kInt, c.device, "src", stream);
   const at::Tensor w_out = output(a[9], {B, c.Hkv, budget}, at::kFloat, c.device, "weights_out", stream);
   const at::Tensor lens_out = output(a[10], {B}, at::kInt, c.device, "lens_out", stream);
-  check("fa_cache4_evict",
-        fa_cache4_evict(c.p, c.pages, c.page, w, cap, lens, table, width, (int)B, c.Hkv, D, budget,
-                        recent, out_table, out_width, static_cast<int*>(src.data_ptr()),
-                        static_cast<float*>(w_out.data_ptr()), static_cast<int*>(lens_out.data_ptr()),
-                        place.stream));
+  call("fa_cache4_evict", [&] {
+    return fa_cache4_evict(c.p, c.pages, c.page, w, cap, lens, table, width, (int)B, c.Hkv, D,
+                           budget, recent, out_table, out_width, static_cast<int*>(src.data_ptr()),
+                           static_cast<float*>(w_out.data_ptr()),
+                           static_cast<int*>(lens_out.data_ptr()), place.stream);
+  });
   return tuple(src, w_out, lens_out);
 }
 
