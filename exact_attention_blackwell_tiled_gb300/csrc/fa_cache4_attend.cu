@@ -64,8 +64,8 @@ constexpr int kWarps = 4;      // per block; they share nothing but the launch
 //   SM): 10.5 / 13.8 against 13.7 / 16.0;  38 x 1000: 16.5 / 22.7 against 18.3 / 22.1;
 //   64 x 300: 19.5 / 25.3 against 17.5 / 19.1;
 //   D = 64, 38 x 300: 5.1 / 6.8 against 11.7 / 13.8;  152 x 300 (eight rows per SM):
-//   18.3 / 25.0 against 21.4 / 25.1;  152 x 1000: 34.7 / 47.4 against 37.8 / 46.6;
-//   228 x 300: 27.4 / 37.7 against 23.1 / 28.4.
+//   18.3 / 25.0 against 20.1 / 23.4;  152 x 1000: 34.7 / 47.4 against 35.8 / 43.4;
+//   228 x 300: 27.4 / 37.7 against 29.1 / 34.2;  400 x 300: 49.0 / 65.7 against 42.1 / 51.7.
 constexpr int kOwnWarps = 8, kOwnBlocks = 64;
 template <int D, int NT>
 constexpr int kOwnRowsPerSm = D == 64 && NT == 1 ? 8 : 2;
@@ -98,10 +98,16 @@ struct AttendArgs {
 // cost more than the work split off.
 constexpr int kMinBlocks = 4;
 
+// Resident blocks of attend_kernel with shares, by the registers a row takes (D = 64,
+// 8 columns: four of 126 registers, 2 x 32768 tokens of 16 heads 27.2 us; three 28.3,
+// five of 96 30.4.  D = 128: four, of 128 registers, measured 6% slower than three).
+__host__ __device__ constexpr int blocks_per_sm(int D, int nt) {
+  return nt == 2 ? 2 : (D == 64 ? 4 : 3);
+}
+
 // A warp's ring in shared memory: two stages of 5 KB, so that an SM's 12 warps have
 // 60 to 120 KB on their way (the bytes that cover the memory's latency at its full
-// rate are about 45 KB); a third stage measured the same or 3% slower, four blocks of
-// 4 warps per SM (128 registers a thread) 6% slower.
+// rate are about 45 KB); a third stage measured the same or 3% slower.
 template <int D>
 struct Ring {
   static constexpr int kStages = 2;
@@ -292,7 +298,7 @@ __device__ __forceinline__ void write_lse(const AttendArgs& a, size_t row, float
 // parts of it, and joins them in shared memory, weights included: one launch.
 // Otherwise every warp takes a share of the list.
 template <int D, int NT, bool kOwn>
-__global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : (NT == 1 ? 3 : 2))
+__global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : blocks_per_sm(D, NT))
     attend_kernel(const AttendArgs a) {
   using L = C4<D>;
   using R = Ring<D>;
@@ -932,7 +938,7 @@ int tile_count(int group, int* nt) {
 }
 
 // Shares: every warp that is resident at once.
-int share_limit(int sms, int nt) { return sms * (nt == 1 ? 3 : 2) * kWarps; }
+int share_limit(int sms, int D, int nt) { return sms * blocks_per_sm(D, nt) * kWarps; }
 
 struct AttendLayout {
   size_t off_ml, off_span, off_lse2, off_scores, total;
@@ -941,7 +947,7 @@ struct AttendLayout {
 AttendLayout attend_layout(int B, int Hq, int Hkv, int D, int cap, int sms) {
   int nt;
   const int tiles = tile_count(Hq / Hkv, &nt);
-  const size_t rows = (size_t)share_limit(sms, nt) * 2 * 8 * nt;
+  const size_t rows = (size_t)share_limit(sms, D, nt) * 2 * 8 * nt;
   AttendLayout L;
   L.off_ml = rows * D * sizeof(float);
   L.off_span = L.off_ml + rows * sizeof(float2);
@@ -1064,7 +1070,7 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   a.group = Hq / Hkv;
   a.tiles = tile_count(a.group, &nt);
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.n_warps = share_limit(info.sm_count, nt);
+  a.n_warps = share_limit(info.sm_count, D, nt);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   a.span = reinterpret_cast<int*>(ws + L.off_span);
