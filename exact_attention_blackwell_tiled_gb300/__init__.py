@@ -500,7 +500,9 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
                      deterministic: bool = False) -> torch.Tensor:
     """attention() over packed sequences: q [T,Hq,D], k/v [T,Hkv,D] bf16 CUDA,
     ``cu_seqlens`` int32 [B+1] (see fwd_varlen).  Tokens of no sequence get zeros
-    in O and in every gradient.  Returns O [T,Hq,D] bf16."""
+    in O and in every gradient.  A training step can be captured into a CUDA graph
+    after a step on a side stream; no other graph of the same leaves may be alive
+    then.  Returns O [T,Hq,D] bf16."""
     return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic)
 
 

@@ -259,6 +259,39 @@ def test_autograd(gpu):
 
 
 @pytest.mark.gpu
+def test_captured_training_step(gpu):
+    """Forward and backward captured into one graph, replayed on new values and
+    boundaries.  (No eager graph of the leaves lives at the capture.)"""
+    cu = [0, 70, 70, 300]
+    q, k, v, do = (x.cuda() for x in _inputs(cu[-1], 4, 2, 64, 31))
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+
+    def step(leaves):
+        o = fa.attention_varlen(*leaves, cud, causal=True, deterministic=True)
+        grads = torch.autograd.grad(o, leaves, do)
+        return [o.detach(), *grads]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(leaves)
+    for shift, cut in ((1, [0, 70, 70, 300]), (7, [0, 256, 257, 299])):
+        with torch.no_grad():
+            for x, y in zip(leaves, (q, k, v)):
+                x.copy_(y.roll(shift, 0))
+        cud.copy_(torch.tensor(cut, dtype=torch.int32))
+        g.replay()
+        want = step([x.detach().clone().requires_grad_() for x in leaves])
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_binding_refusals_of_device_tensors(gpu):
     q, k, v, do = (x.cuda() for x in _inputs(6, 4, 2, 64, 3))
     cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
