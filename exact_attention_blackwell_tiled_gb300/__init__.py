@@ -414,7 +414,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
 
 
 # The calls below also serve single tokens, where the host's time is most of a
-# call's, so their checks and allocations are compiled (csrc/binding.cpp).
+# call's, so their checks and allocations are compiled (csrc/binding.cpp).  With
+# ``stream`` a call runs there and what it allocates is that stream's; the caller
+# orders it behind the arguments' last writers, and the results' readers behind it.
 
 _COMPILED = None
 

@@ -136,28 +136,49 @@ const at::Tensor& given(PyObject* o, at::IntArrayRef shape, at::ScalarType dtype
   return *t;
 }
 
-// The same, or for None a new one that the stream may write.
-at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType dtype, int device,
-                  const char* name, PyObject* stream) {
-  if (o == Py_None) {
-    at::Tensor t = at::empty(shape, at::TensorOptions().dtype(dtype).device(c10::Device(at::kCUDA, device)));
-    if (stream != Py_None) {  // keep its memory until that stream has passed
-      PyObject* w = THPVariable_Wrap(t);
-      PyObject* r = w ? PyObject_CallMethod(w, "record_stream", "O", stream) : nullptr;
-      Py_XDECREF(w);
-      if (!r) throw Raised{};
-      Py_DECREF(r);
-    }
-    return t;
+// The device and the stream of a call made current: memory that the call allocates
+// comes from the pool of the stream that writes it, so nothing queued elsewhere still
+// uses it, and what the call drops (a workspace) goes back there behind its kernels.
+struct Place {
+  int device;
+  c10::cuda::OptionalCUDAGuard on_device;
+  c10::cuda::CUDAStream caller;  // the current stream of the device before the call
+  c10::cuda::OptionalCUDAStreamGuard on_stream;
+  fa_stream_t stream;
+  Place(int d, PyObject* s) : device(d), caller(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)d)) {
+    if (c10::cuda::current_device() != d) on_device.set_index((c10::DeviceIndex)d);
+    stream = caller.stream();
+    if (s == Py_None) return;
+    PyObject* h = PyObject_GetAttrString(s, "cuda_stream");
+    if (!h) throw Raised{};
+    stream = reinterpret_cast<fa_stream_t>(PyLong_AsUnsignedLongLong(h));
+    Py_DECREF(h);
+    if (PyErr_Occurred()) throw Raised{};
+    if (stream != caller.stream())
+      on_stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream),
+                                                              (c10::DeviceIndex)d));
   }
-  return given(o, shape, dtype, device, name);
+  bool elsewhere() const { return stream != static_cast<fa_stream_t>(caller.stream()); }
+};
+
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const Place& place) {
+  return at::empty(shape, at::TensorOptions().dtype(dtype).device(c10::Device(at::kCUDA, place.device)));
 }
 
-at::Tensor workspace(PyObject* o, size_t bytes, int device, PyObject* stream) {
-  if (o == Py_None)
-    return output(o, {(int64_t)(bytes ? bytes : 1)}, at::kByte, device, "workspace", stream);
+// The same, or for None a new one, whose memory stays until the caller's stream, where
+// it is used next, has passed.
+at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType dtype, const Place& place,
+                  const char* name) {
+  if (o != Py_None) return given(o, shape, dtype, place.device, name);
+  at::Tensor t = fresh(shape, dtype, place);
+  if (place.elsewhere()) t.record_stream(place.caller.unwrap());
+  return t;
+}
+
+at::Tensor workspace(PyObject* o, size_t bytes, const Place& place) {
+  if (o == Py_None) return fresh({(int64_t)(bytes ? bytes : 1)}, at::kByte, place);
   const at::Tensor* t = tensor(o);
-  if (!t || !t->is_cuda() || t->get_device() != device || !t->is_contiguous())
+  if (!t || !t->is_cuda() || t->get_device() != place.device || !t->is_contiguous())
     value_error("workspace must be a contiguous tensor on the inputs' device");
   return *t;
 }
@@ -215,24 +236,6 @@ float* weights(PyObject* o, int64_t B, int Hkv, int device, int* slots, const ch
   return static_cast<float*>(t->data_ptr());
 }
 
-// The device made current for a call, and the call's stream.
-struct Place {
-  c10::cuda::OptionalCUDAGuard guard;
-  fa_stream_t stream;
-  Place(int device, PyObject* s) {
-    if (c10::cuda::current_device() != device) guard.set_index((c10::DeviceIndex)device);
-    if (s == Py_None) {
-      stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-      return;
-    }
-    PyObject* h = PyObject_GetAttrString(s, "cuda_stream");
-    if (!h) throw Raised{};
-    stream = reinterpret_cast<fa_stream_t>(PyLong_AsUnsignedLongLong(h));
-    Py_DECREF(h);
-    if (PyErr_Occurred()) throw Raised{};
-  }
-};
-
 template <typename... T>
 PyObject* tuple(const T&... t) {
   PyObject* r = PyTuple_New(sizeof...(t));
@@ -275,10 +278,10 @@ PyObject* fwd_varlen(PyObject* const* a) {
   const int* cu = int32s(a[3], -1, x.device, "cu_seqlens", &n);
   const int B = (int)n - 1, wl = to_int(a[4]), wr = to_int(a[5]);
   const float scale = to_scale(a[6], x.D);
-  const at::Tensor o = output(a[7], {x.T, x.Hq, x.D}, at::kBFloat16, x.device, "out", a[10]);
-  const at::Tensor lse = output(a[8], {x.Hq, x.T}, at::kFloat, x.device, "lse", a[10]);
+  const at::Tensor o = output(a[7], {x.T, x.Hq, x.D}, at::kBFloat16, place, "out");
+  const at::Tensor lse = output(a[8], {x.Hq, x.T}, at::kFloat, place, "lse");
   const size_t need = a[9] == Py_None ? fa_varlen_workspace_bytes(B, x.T, x.Hq, x.Hkv, x.D, 0, 0) : 0;
-  const at::Tensor ws = workspace(a[9], need, x.device, a[10]);
+  const at::Tensor ws = workspace(a[9], need, place);
   call("fa_fwd_varlen", [&] {
     return fa_fwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
                          static_cast<float*>(lse.data_ptr()), cu, B, x.T, x.Hq, x.Hkv, x.D,
@@ -304,10 +307,10 @@ PyObject* bwd_varlen(PyObject* const* a) {
   const float scale = to_scale(a[9], x.D);
   const int det = to_bool(a[10]) ? 1 : 0;
   const size_t need = a[11] == Py_None ? fa_varlen_workspace_bytes(B, x.T, x.Hq, x.Hkv, x.D, 1, det) : 0;
-  const at::Tensor ws = workspace(a[11], need, x.device, stream);
-  const at::Tensor dq = output(a[12], q_shape, at::kBFloat16, x.device, "dq", stream);
-  const at::Tensor dk = output(a[13], k_shape, at::kBFloat16, x.device, "dk", stream);
-  const at::Tensor dv = output(a[14], k_shape, at::kBFloat16, x.device, "dv", stream);
+  const at::Tensor ws = workspace(a[11], need, place);
+  const at::Tensor dq = output(a[12], q_shape, at::kBFloat16, place, "dq");
+  const at::Tensor dk = output(a[13], k_shape, at::kBFloat16, place, "dk");
+  const at::Tensor dv = output(a[14], k_shape, at::kBFloat16, place, "dv");
   call("fa_bwd_varlen", [&] {
     return fa_bwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
                          dO.data_ptr(), static_cast<const float*>(lse.data_ptr()), dq.data_ptr(),
@@ -350,8 +353,8 @@ PyObject* cache4_read(PyObject* const* a) {
   const int* table = page_table(a[1], B, c.device, &width);
   const int* first = a[2] == Py_None ? nullptr : int32s(a[2], B, c.device, "first");
   if (S < 0) check("fa_cache4_read", 1);
-  const at::Tensor k = output(a[6], {B, c.Hkv, S, D}, at::kBFloat16, c.device, "k", a[8]);
-  const at::Tensor v = output(a[7], {B, c.Hkv, S, D}, at::kBFloat16, c.device, "v", a[8]);
+  const at::Tensor k = output(a[6], {B, c.Hkv, S, D}, at::kBFloat16, place, "k");
+  const at::Tensor v = output(a[7], {B, c.Hkv, S, D}, at::kBFloat16, place, "v");
   call("fa_cache4_read", [&] {
     return fa_cache4_read(c.p, c.pages, c.page, k.data_ptr(), v.data_ptr(), (int)B, c.Hkv, S, D,
                           first, count, table, width, place.stream);
@@ -380,11 +383,11 @@ PyObject* cache4_attend(PyObject* const* a) {
     if (w_in && n != slots) value_error("weights_out must have weights' shape");
     slots = n;
   }
-  const at::Tensor o = output(a[7], {B, Hq, D}, at::kBFloat16, device, "out", stream);
-  const at::Tensor lse = output(a[8], {B, Hq}, at::kFloat, device, "lse", stream);
+  const at::Tensor o = output(a[7], {B, Hq, D}, at::kBFloat16, place, "out");
+  const at::Tensor lse = output(a[8], {B, Hq}, at::kFloat, place, "lse");
   const size_t need =
       a[9] == Py_None ? fa_cache4_attend_workspace_bytes(B, Hq, c.Hkv, D, slots) : 0;
-  const at::Tensor ws = workspace(a[9], need, device, stream);
+  const at::Tensor ws = workspace(a[9], need, place);
   // the stride of a dimension of one element is arbitrary
   call("fa_cache4_attend", [&] {
     return fa_cache4_attend(q.t->data_ptr(), B > 1 ? q.t->stride(0) : 0,
@@ -411,9 +414,9 @@ PyObject* cache4_evict(PyObject* const* a) {
   const float* w = weights(a[3], B, c.Hkv, c.device, &cap, "weights");
   if (budget < 1 || recent < 0 || recent > budget || (int64_t)out_width * c.page < budget)
     value_error("budget must be positive, at least recent and within out_page_table");
-  const at::Tensor src = output(a[8], {B, c.Hkv, budget}, at::kInt, c.device, "src", stream);
-  const at::Tensor w_out = output(a[9], {B, c.Hkv, budget}, at::kFloat, c.device, "weights_out", stream);
-  const at::Tensor lens_out = output(a[10], {B}, at::kInt, c.device, "lens_out", stream);
+  const at::Tensor src = output(a[8], {B, c.Hkv, budget}, at::kInt, place, "src");
+  const at::Tensor w_out = output(a[9], {B, c.Hkv, budget}, at::kFloat, place, "weights_out");
+  const at::Tensor lens_out = output(a[10], {B}, at::kInt, place, "lens_out");
   call("fa_cache4_evict", [&] {
     return fa_cache4_evict(c.p, c.pages, c.page, w, cap, lens, table, width, (int)B, c.Hkv, D,
                            budget, recent, out_table, out_width, static_cast<int*>(src.data_ptr()),
