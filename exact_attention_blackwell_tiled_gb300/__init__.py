@@ -174,6 +174,21 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream=None, returned=True):
+    """New memory for a call on ``stream``: from that stream's pool, where nothing
+    queued elsewhere still uses it.  What is returned stays until the caller's
+    current stream, where it is used next, has passed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _check(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -210,16 +225,17 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq, Sq), torch.float32, q.device, stream)
     mod = _score_mod(causal, window, alibi_slopes, Hq, seqlens_k, B)
     if n_splits is not None:
         if mod is None and causal:
             mod = ScoreMod(-1, 0, None, None)
         ws_bytes = fwd_split_workspace_bytes(B, Hq, Sq, Sk, D, n_splits)
         if split_workspace is None:
-            split_workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
+            split_workspace = _new((max(ws_bytes, 1),), torch.uint8, q.device, stream,
+                                   returned=False)
         rc = lib().fa_fwd_split(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq,
                                 Sk, D, None if mod is None else ctypes.byref(mod), float(scale),
                                 int(n_splits), _ptr(split_workspace),
@@ -263,9 +279,9 @@ def lse_merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, out: torch.Tensor 
     n, D = o_parts.shape[0], o_parts.shape[-1]
     rows = lse_parts[0].numel() if n > 0 else 0
     if out is None:
-        out = torch.empty(o_parts.shape[1:], dtype=torch.bfloat16, device=o_parts.device)
+        out = _new(o_parts.shape[1:], torch.bfloat16, o_parts.device, stream)
     if lse is None:
-        lse = torch.empty(lse_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
+        lse = _new(lse_parts.shape[1:], torch.float32, o_parts.device, stream)
     rc = lib().fa_lse_merge(_ptr(o_parts), _ptr(lse_parts), int(n), _ptr(out), _ptr(lse),
                             int(rows), int(D), _stream(stream))
     if rc != FA_OK:
@@ -294,10 +310,9 @@ def bwd(q, k, v, o, do, lse, causal: bool = False, scale: float | None = None,
         scale = 1.0 / math.sqrt(D)
     need = bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, deterministic)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+        workspace = _new((need,), torch.uint8, q.device, stream, returned=False)
+    dq, dk, dv = (_new(x.shape, x.dtype, x.device, stream) if g is None else g
+                  for x, g in ((q, dq), (k, dk), (v, dv)))
     mod = _score_mod(causal, window, alibi_slopes, Hq, seqlens_k, B)
     if mod is None:
         rc = lib().fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
@@ -328,7 +343,7 @@ def exp2_test(x: torch.Tensor, which: int, stream=None) -> torch.Tensor:
     packed two-lane polynomial path (which=2)."""
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise TypeError("x must be a contiguous fp32 CUDA tensor")
-    y = torch.empty_like(x)
+    y = _new(x.shape, x.dtype, x.device, stream)
     rc = lib().fa_exp2_test(_ptr(x), _ptr(y), x.numel(), int(which), _stream(stream))
     if rc != FA_OK:
         raise FAError("fa_exp2_test", rc)
@@ -338,13 +353,16 @@ def exp2_test(x: torch.Tensor, which: int, stream=None) -> torch.Tensor:
 def wait_test(which: int, flag: torch.Tensor | None = None, stream=None) -> int:
     """Run one of the kernels' bounded waits (fa_wait_test); returns the status it
     wrote: FA_OK or FA_ERR_TIMEOUT (6).  flag: an int32 CUDA scalar for which=0."""
-    status = torch.full((1,), -1, dtype=torch.int32, device=flag.device if flag is not None
-                        else torch.device("cuda", torch.cuda.current_device()))
+    device = flag.device if flag is not None else torch.device("cuda", torch.cuda.current_device())
+    status = _new((1,), torch.int32, device, stream)
+    with torch.cuda.stream(stream):  # (None: the current one)
+        status.fill_(-1)
     rc = lib().fa_wait_test(None if flag is None else _ptr(flag), int(which), _ptr(status),
                             _stream(stream))
     if rc != FA_OK:
         raise FAError("fa_wait_test", rc)
-    return int(status.item())
+    with torch.cuda.stream(stream):
+        return int(status.item())
 
 
 def last_launch_count() -> int:

@@ -100,6 +100,57 @@ def test_cache_calls_allocate_on_their_stream():
     assert fa.cache4_status() == fa.FA_OK
 
 
+def _dense():
+    gen = torch.Generator().manual_seed(9)
+    return [torch.randn(2, h, 700, D, generator=gen).to(torch.bfloat16).cuda()
+            for h in (HQ, HKV, HKV, HQ)]
+
+
+def test_dense_calls_allocate_on_their_stream():
+    q, k, v, do = _dense()
+    o, lse = fa.fwd(q, k, v, causal=True)
+    _check_pool(lambda s, **kw: fa.fwd(q, k, v, causal=True, stream=s, **kw), names=("out", "lse"),
+                workspace=False)
+    _check_pool(lambda s, **kw: fa.fwd(q, k, v, n_splits=3, stream=s, **kw), names=("out", "lse"),
+                workspace=True)
+    _check_pool(lambda s, **kw: fa.bwd(q, k, v, o, do, lse, causal=True, deterministic=True,
+                                       stream=s, **kw),
+                names=("dq", "dk", "dv"), workspace=True)
+    parts = torch.randn(3, 500, D, device="cuda"), torch.randn(3, 500, device="cuda")
+    _check_pool(lambda s, **kw: fa.lse_merge(*parts, stream=s, **kw), names=("out", "lse"),
+                workspace=False)
+    x = torch.linspace(-3, 3, 1000, device="cuda")
+    _check_pool(lambda s: (fa.exp2_test(x, 0, stream=s),), names=(), workspace=True)
+
+
+def test_dense_calls_in_turn_on_two_streams():
+    q, k, v, do = _dense()
+    o, lse = fa.fwd(q, k, v, causal=True)
+
+    def calls(stream):
+        return (*fa.fwd(q, k, v, causal=True, stream=stream), *fa.fwd(q, k, v, n_splits=3, stream=stream),
+                *fa.bwd(q, k, v, o, do, lse, causal=True, deterministic=True, stream=stream))
+
+    want = calls(None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(10):
+        got += [calls(None), calls(side)]
+    torch.cuda.synchronize()
+    for run in got:
+        for a, b in zip(want, run):
+            assert torch.equal(a, b)
+
+
+def test_wait_test_on_another_stream():
+    """The status is set, written and read on the stream of the call."""
+    side = torch.cuda.Stream()
+    flag = torch.ones(1, dtype=torch.int32, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    assert fa.wait_test(0, flag, stream=side) == fa.FA_OK
+
+
 def test_calls_in_turn_on_two_streams():
     """No synchronisation between a call on the current stream and the next on another:
     each call frees its workspace as soon as it is launched."""
