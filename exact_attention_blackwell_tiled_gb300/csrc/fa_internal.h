@@ -36,6 +36,10 @@ bool make_tmap_bsd(CUtensorMap* map, const void* base, int BH, int S, int D,
 bool make_tmap_strided(CUtensorMap* map, const void* base, int H, int S, int D,
                        long long row_stride, long long head_stride, int box_rows);
 
+// A side of a window over rows that are at most n - 1 apart: negative is unbounded,
+// and the kernels add it to indices in 32 bits, so larger ones are cut to n.
+inline int window_side(int w, int n) { return w < 0 ? -1 : (w < n ? w : n); }
+
 // FA_OK if the current device can run the kernels; makes its primary context
 // current on the calling thread.
 int check_device();

@@ -303,8 +303,8 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   PlanArgs p{};
   if ((rc = plan_maps(t, 3, T, D, &p))) return rc;
   FwdArgs a{};
-  a.wl = window_left < 0 ? -1 : window_left;
-  a.wr = window_right < 0 ? -1 : window_right;
+  a.wl = window_side(window_left, T);
+  a.wr = window_side(window_right, T);
   a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
   p.cu = cu_seqlens;
   p.B = B;
@@ -364,8 +364,8 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   PlanArgs p{};
   if ((rc = plan_maps(t, 4, T, D, &p))) return rc;
   BwdArgs a{};
-  a.wl = window_left < 0 ? -1 : window_left;
-  a.wr = window_right < 0 ? -1 : window_right;
+  a.wl = window_side(window_left, T);
+  a.wr = window_side(window_right, T);
   a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
   p.cu = cu_seqlens;
   p.B = B;
