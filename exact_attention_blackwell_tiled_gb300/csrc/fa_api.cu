@@ -67,10 +67,11 @@ struct ModArgs {
 
 ModArgs plain_mod(int causal) { return ModArgs{-1, causal ? 0 : -1, nullptr, nullptr}; }
 
-ModArgs read_mod(const fa_score_mod* m) {
+// (a query is at most Sq - 1 rows behind a key, a key at most Sk - 1 behind a query)
+ModArgs read_mod(const fa_score_mod* m, int Sq, int Sk) {
   if (!m) return plain_mod(0);
-  return ModArgs{m->window_left < 0 ? -1 : m->window_left,
-                 m->window_right < 0 ? -1 : m->window_right, m->alibi_slopes, m->seqlens_k};
+  return ModArgs{window_side(m->window_left, Sq), window_side(m->window_right, Sk),
+                 m->alibi_slopes, m->seqlens_k};
 }
 
 // The device arrays a modification reads are 4-byte aligned.  (A row that sees
@@ -340,7 +341,7 @@ int fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int
 int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                int Hkv, int Sq, int Sk, int D, const fa_score_mod* mod, float scale,
                fa_stream_t stream) {
-  return fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, read_mod(mod), scale, stream);
+  return fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, read_mod(mod, Sq, Sk), scale, stream);
 }
 
 int fa_fwd_status(fa_stream_t stream) { return fwd_status_take(static_cast<cudaStream_t>(stream)); }
@@ -363,7 +364,7 @@ int fa_fwd_split(const void* q, const void* k, const void* v, void* o, float* ls
                  int n_splits, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   t_launches = 0;
   if (n_splits < 0) return FA_ERR_INVALID_ARG;
-  const ModArgs m = read_mod(mod);
+  const ModArgs m = read_mod(mod, Sq, Sk);
   CUtensorMap tq, tk, tv;
   FwdArgs a;
   bool nothing;
@@ -534,7 +535,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
                const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq,
                int Sk, int D, const fa_score_mod* mod, float scale, void* workspace,
                size_t workspace_bytes, int deterministic, fa_stream_t stream) {
-  return bwd_impl(q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, read_mod(mod), scale,
+  return bwd_impl(q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, read_mod(mod, Sq, Sk), scale,
                   workspace, workspace_bytes, deterministic, stream);
 }
 
