@@ -150,7 +150,9 @@ def _score_mod(causal, window, alibi_slopes, Hq, seqlens_k=None, B=None):
                 or seqlens_k.numel() != B or not seqlens_k.is_contiguous()):
             raise TypeError("seqlens_k must be a contiguous int32 CUDA tensor of B key counts")
         lens = seqlens_k.data_ptr()
-    return ScoreMod(int(wl), int(wr), ptr, lens)
+    # (a ctypes int would wrap; distances stay below 2^31)
+    wl, wr = (max(-1, min(int(w), 2 ** 31 - 1)) for w in (wl, wr))
+    return ScoreMod(wl, wr, ptr, lens)
 
 
 def lib():
