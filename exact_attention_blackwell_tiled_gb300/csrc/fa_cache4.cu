@@ -585,13 +585,13 @@ __global__ void __launch_bounds__(256) move_kernel(const EvictArgs a) {
     const int e = n * 32 + lane, s = e / 10, p = e - 10 * s;
     const long long f = __shfl_sync(0xffffffffu, from, s);
     const int fs = __shfl_sync(0xffffffffu, from_slot, s);
+    val[n] = Piece{};  // a token whose old page is out of range: zeros, as read gives it
     if (f >= 0) val[n] = *reinterpret_cast<const Piece*>(a.cache + f + offset(fs, p));
   }
 #pragma unroll
   for (int n = 0; n < kPieces / 32; ++n) {
     const int e = n * 32 + lane, s = e / 10, p = e - 10 * s;
-    const long long f = __shfl_sync(0xffffffffu, from, s);
-    if (f >= 0) *reinterpret_cast<Piece*>(dst + offset(s, p)) = val[n];
+    if (s < slots) *reinterpret_cast<Piece*>(dst + offset(s, p)) = val[n];
   }
 }
 

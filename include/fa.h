@@ -371,7 +371,8 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
  * unchanged, in slot order, to slots 0, 1, ... of the pages of out_page_table
  * [B, out_table_width], which must be other pages than any table in use names, each
  * named once; the old pages are only read, so sequences that share them lose nothing.  A sequence
- * with at most `budget` tokens keeps all.
+ * with at most `budget` tokens keeps all.  A kept token whose old page is out of range is recorded
+ * and becomes one of zeros, as fa_cache4_read gives it.
  *   src [B, Hkv, budget] int32: the old slot of each kept token, -1 behind the last;
  *   weights_out [B, Hkv, budget] fp32: their weights, 0 behind the last;
  *   lens_out [B] int32: min(cache_lens[b], budget); it may be cache_lens itself.

@@ -1,0 +1,68 @@
+"""The 4-bit cache at the edges of its tables: pages out of range, idle sequences."""
+import pytest
+import torch
+
+import __graft_entry__
+import exact_attention_blackwell_tiled_gb300 as fa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    __graft_entry__.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _filled(lens, Hkv, D, page, pages, seed=3):
+    """A pool of `pages` pages of other bytes with the sequences in the first ones."""
+    gen = torch.Generator().manual_seed(seed)
+    T, width = sum(lens), max(-(-n // page) for n in lens)
+    k, v = (torch.randn(T, Hkv, D, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    cache = fa.cache4_empty(pages, Hkv, D, page)
+    cache.fill_(0x5a)
+    table = torch.arange(len(lens) * width, dtype=torch.int32, device="cuda").view(len(lens), width)
+    cu = torch.tensor([0, *lens]).cumsum(0).to(torch.int32).cuda()
+    fa.cache4_append(cache, k, v, table, _i32([0] * len(lens)), cu)
+    return cache, table
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("budget", [24, 100])  # fewer than the tokens, or all of them
+def test_evict_of_a_token_whose_page_is_out_of_range(D, budget):
+    """It is reported and becomes a token of zeros; nothing of the new page's old bytes is
+    left in a live slot, and nothing behind the last slot is written."""
+    lens, page, Hkv, recent = [40, 33], 16, 2, 8
+    cache, table = _filled(lens, Hkv, D, page, 30)
+    n = _i32(lens)
+    bad = table.clone()
+    bad[0, 1], bad[1, 2] = 30, -1
+    w = torch.rand(2, Hkv, 40, generator=torch.Generator().manual_seed(budget)).cuda()
+    width = -(-budget // page)
+    fresh = (16 + torch.arange(2 * width, dtype=torch.int32, device="cuda")).view(2, width)
+    before = cache.clone()
+    src, _, kept = fa.cache4_evict(cache, bad, n, w, fresh, D, budget, recent)
+    assert fa.cache4_status() == 1
+    assert kept.tolist() == [min(x, budget) for x in lens]
+    old = fa.cache4_read(before, bad, None, n, 40, D)  # zeros where the page is out of range
+    assert fa.cache4_status() == 1
+    new = fa.cache4_read(cache, fresh, None, kept, budget, D)
+    assert fa.cache4_status() == fa.FA_OK
+    for b in range(2):
+        m = int(kept[b])
+        for h in range(Hkv):
+            at = src[b, h, :m].long()
+            assert bool((at // page == (1 if b == 0 else 2)).any())  # (some of them are kept)
+            for x, y in zip(old, new):
+                assert torch.equal(y[b, h, :m], x[b, h, at])
+    # slots behind the last kept one: as they were
+    full = _i32([width * page] * 2)
+    was, now = (fa.cache4_read(c, fresh, None, full, width * page, D) for c in (before, cache))
+    for b in range(2):
+        for x, y in zip(was, now):
+            assert torch.equal(x[b, :, int(kept[b]):], y[b, :, int(kept[b]):])
