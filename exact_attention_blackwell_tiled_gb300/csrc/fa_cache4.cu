@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(128) read_kernel(const ReadArgs a) {
   const long long row0 = (long long)blk * kC4Block - first;
   if (row0 >= a.S) return;
   int page = -1;
-  if (row0 < count) {
+  if (max(row0, 0LL) < count) {  // (the first block begins before `first`)
     page = from >= 0 ? c4_page(a.table, b, blk) : -1;
     if (page < 0 && lane == 0) c4_flag(a.table);
   }

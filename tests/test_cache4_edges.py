@@ -66,3 +66,24 @@ def test_evict_of_a_token_whose_page_is_out_of_range(D, budget):
     for b in range(2):
         for x, y in zip(was, now):
             assert torch.equal(x[b, :, int(kept[b]):], y[b, :, int(kept[b]):])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_read_looks_only_at_pages_with_rows(D):
+    """No row of a sequence asked for: its pages, released, are not looked at, wherever
+    `first` lies in a block; rows asked for of the last page alone do not report the others."""
+    cache, table = _filled([40, 33], 2, D, 16, 6)
+    gone = table.clone()
+    gone[0] = -1
+    k, v = fa.cache4_read(cache, gone, _i32([37, 20]), _i32([0, 9]), 20, D)
+    assert fa.cache4_status() == fa.FA_OK
+    whole = fa.cache4_read(cache, table, None, _i32([40, 33]), 40, D)
+    for x, y in zip((k, v), whole):
+        assert bool((x[0] == 0).all()) and bool((x[1, :, 9:] == 0).all())
+        assert torch.equal(x[1, :, :9], y[1, :, 20:29])
+    gone[0, 2] = table[0, 2]
+    k, v = fa.cache4_read(cache, gone, _i32([35, 0]), _i32([5, 0]), 20, D)
+    assert fa.cache4_status() == fa.FA_OK
+    assert torch.equal(k[0, :, :5], whole[0][0, :, 35:]) and torch.equal(v[0, :, :5], whole[1][0, :, 35:])
+    fa.cache4_read(cache, gone, _i32([31, 0]), _i32([5, 0]), 20, D)
+    assert fa.cache4_status() == 1  # slot 31 lies on a page that is gone
