@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(128) read_kernel(const ReadArgs a) {
   // output row of slot s of the block; rows outside [0, S) are not this warp's
   const long long row0 = (long long)blk * kC4Block - first;
   if (row0 >= a.S) return;
+  if (count < 0 && j == 0 && lane == 0) c4_flag(a.table);
   int page = -1;
   if (max(row0, 0LL) < count) {  // (the first block begins before `first`)
     page = from >= 0 ? c4_page(a.table, b, blk) : -1;

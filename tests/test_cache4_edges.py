@@ -87,3 +87,13 @@ def test_read_looks_only_at_pages_with_rows(D):
     assert torch.equal(k[0, :, :5], whole[0][0, :, 35:]) and torch.equal(v[0, :, :5], whole[1][0, :, 35:])
     fa.cache4_read(cache, gone, _i32([31, 0]), _i32([5, 0]), 20, D)
     assert fa.cache4_status() == 1  # slot 31 lies on a page that is gone
+
+
+@pytest.mark.parametrize("first", [None, 3])
+def test_read_reports_a_negative_count(first):
+    """A length out of range, as the other calls report it; the rows are zeros."""
+    cache, table = _filled([40, 33], 2, 64, 16, 6)
+    at = None if first is None else _i32([first] * 2)
+    k, v = fa.cache4_read(cache, table, at, _i32([8, -2]), 8, 64)
+    assert fa.cache4_status() == 1
+    assert bool((k[1] == 0).all()) and bool((v[1] == 0).all()) and bool((k[0] != 0).any())
