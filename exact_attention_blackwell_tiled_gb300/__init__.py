@@ -575,7 +575,9 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     ``weights`` fp32 [B,Hkv,slots] has the tokens' softmax weights, summed over each
     kv head's query heads, added to it in place, or to a copy in ``weights_out``;
     ``weights_out`` alone gets this step's.  Tokens that an append adds later start
-    at what the tensor holds there, so it begins as zeros.
+    at what the tensor holds there, so it begins as zeros.  ``slots`` is at least
+    every length: tokens behind it are left out of all results and cache4_status()
+    reports them.
     Returns (o [B,Hq,D] bf16, lse [B,Hq] fp32); o = 0, lse = -inf without tokens.
     """
     return _compiled().cache4_attend(q, cache, page_table, cache_lens, scale, weights, weights_out,
@@ -591,6 +593,8 @@ def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torc
 
     Returns (src int32 [B,Hkv,budget]: each kept token's old slot, -1 behind the
     last; weights fp32 [B,Hkv,budget], 0 behind the last; lens int32 [B]).
+    For the next steps' cache4_attend copy the weights into a tensor with slots for
+    the tokens to come, zeros there.
     """
     return _compiled().cache4_evict(cache, page_table, cache_lens, weights, out_page_table, D, budget,
                                     recent, src, weights_out, lens_out, stream)
