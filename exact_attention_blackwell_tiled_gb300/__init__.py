@@ -14,6 +14,7 @@ import math
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfa.so")
@@ -507,6 +508,7 @@ class _AttentionVarlen(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
         causal, scale, window, deterministic = ctx.args
@@ -524,7 +526,8 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     ``cu_seqlens`` int32 [B+1] (see fwd_varlen).  Tokens of no sequence get zeros
     in O and in every gradient.  A training step can be captured into a CUDA graph
     after a step on a side stream; no other graph of the same leaves may be alive
-    then.  Returns O [T,Hq,D] bf16."""
+    then.  The gradients cannot be differentiated again (RuntimeError).  Returns O
+    [T,Hq,D] bf16."""
     return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic)
 
 
