@@ -411,6 +411,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse = ctx.saved_tensors
         causal, scale, window, alibi_slopes, deterministic, seqlens_k = ctx.args
@@ -427,8 +428,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
 
     q [B,Hq,Sq,D], k/v [B,Hkv,Sk,D] bf16 CUDA; ``causal``, ``window``,
     ``alibi_slopes`` and ``seqlens_k`` as in fwd; ``deterministic`` selects the
-    backward mode.  O.backward() runs fa_bwd (the slopes get no gradient).
-    Returns O bf16.
+    backward mode.  O.backward() runs fa_bwd (the slopes get no gradient, and the
+    gradients cannot be differentiated again: RuntimeError).  Returns O bf16.
     """
     return _Attention.apply(q, k, v, causal, scale, window, alibi_slopes, deterministic,
                             seqlens_k)

@@ -31,3 +31,8 @@ def test_attention_varlen():
     cu = torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda")
     _refuses(lambda q, k, v: fa.attention_varlen(q, k, v, cu, causal=True), (70, 4, 64), (70, 2, 64),
              (70, 2, 64))
+
+
+def test_attention():
+    _refuses(lambda q, k, v: fa.attention(q, k, v, causal=True), (1, 4, 70, 64), (1, 2, 70, 64),
+             (1, 2, 70, 64))
