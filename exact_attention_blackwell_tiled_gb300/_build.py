@@ -17,6 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libfa.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_KEY_PATH = os.path.join(BUILD_DIR, "_binding.key")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_ring.cu", "fa_bwd.cu", "fa_bwd_q128.cu", "fa_bwd_pair.cu", "fa_merge.cu", "fa_noalloc.cu",
            "fa_varlen.cu", "fa_cache4.cu", "fa_cache4_attend.cu"]
@@ -48,9 +49,27 @@ def _run(cmd: list[str], what: str) -> str:
     return r.stderr
 
 
+def _torch_dir() -> str:
+    """torch's folder (found, not imported)."""
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _binding_key() -> str:
+    """What _binding.so is linked to besides libfa.so: this Python and this torch's C++."""
+    with open(os.path.join(_torch_dir(), "version.py"), encoding="utf-8") as f:
+        return "\n".join((sysconfig.get_config_var("SOABI") or sys.version, _torch_dir(), f.read()))
+
+
+def _binding_stale(header: str) -> bool:
+    if _newer(BINDING_PATH, [BINDING_SOURCE, header]) or not os.path.exists(BINDING_KEY_PATH):
+        return True
+    with open(BINDING_KEY_PATH, encoding="utf-8") as f:
+        return f.read() != _binding_key()
+
+
 def _build_binding() -> None:
-    """csrc/binding.cpp against this machine's torch (found, not imported) and libfa.so."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """csrc/binding.cpp against this machine's torch and libfa.so."""
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
@@ -64,13 +83,17 @@ def _build_binding() -> None:
           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
          "g++ for binding.cpp")
     os.replace(tmp, BINDING_PATH)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(BINDING_KEY_PATH + f".tmp{os.getpid()}", "w", encoding="utf-8") as f:
+        f.write(_binding_key())
+    os.replace(f.name, BINDING_KEY_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = ()) -> str:
     header = os.path.join(INCLUDE, "fa.h")
     if force or _newer(LIB_PATH, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [header]):
         _build_library(verbose, extra)
-    if force or _newer(BINDING_PATH, [BINDING_SOURCE, header]):
+    if force or _binding_stale(header):
         _build_binding()
     return LIB_PATH
 
