@@ -333,17 +333,17 @@ __device__ __forceinline__ void red_add(float* p, float x) {
 }
 
 // kMod: a sliding window and / or the relative-position bias (a.alibi); the
-// plain kernel applies no mask or the causal one.  kVar: a packed batch, with
-// tensor maps a.maps[4 b + 0..3] (q, k, v, dO) that end at the sequence's last
-// row, so that rows past it arrive as zeros; the dQ accumulators hold no padding
-// rows, so a block's rows past the end are not added.  kDet: the deterministic mode
+// plain kernel applies no mask or the causal one.  kVar: a packed batch, with tensor
+// maps over the rows of all sequences; rows past a sequence's last one are loaded as
+// zeros (load_rows); the dQ accumulators hold no padding rows, so a block's rows past
+// the end are not added.  kDet: the deterministic mode
 // (D = 64; at D = 128 it is the 128-row kernel's); a kernel of its own, since the
 // atomic mode's adds lost 13% of its rate to code that it does not run.
 template <int D, bool kMod, bool kVar, bool kDet>
 __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     bwd_main(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-             const BwdArgs a) {
+             const BwdArgs a, const __grid_constant__ Tails<kVar, 4> tails) {
   using L = BwdSmem<D>;
   static_assert(!kDet || D == 64, "D = 128 deterministic calls run the 128-row kernel");
   using R = BwdRoles<kMod || D == 64>;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (!kVar && warp == R::kTmaWarp && lane == 0) {
+  if (warp == R::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -447,34 +447,30 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0, unit = 0;
-      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
-      const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v, *mdo = &tm_do;
       bool ok = true;
       // K_j and V_j of a unit, once every issuer is done with the previous ones
       auto load_kv = [&](const BwdUnit& w, uint32_t un) -> bool {
         if (!mbar_wait(bar(L::kBarKVEmpty), (un & 1) ^ 1, abort_flag)) return false;
         mbar_arrive_expect_tx(bar(L::kBarKVFull), 2 * L::kKVTileBytes);
+        if constexpr (kVar) {
+          const int row = w.row0 + w.j * kTile, valid = w.kv_len - w.j * kTile;
+          load_rows<kTile, L::kColBlocks>(sbase + L::kOffK, L::kKVBlockBytes, &tm_k, tails.of[1],
+                                          bar(L::kBarKVFull), row, valid, a.T, w.bhk);
+          load_rows<kTile, L::kColBlocks>(sbase + L::kOffV, L::kKVBlockBytes, &tm_v, tails.of[2],
+                                          bar(L::kBarKVFull), row, valid, a.T, w.bhk);
+        } else {
 #pragma unroll
-        for (int cb = 0; cb < L::kColBlocks; ++cb) {
-          tma_load_3d(sbase + L::kOffK + cb * L::kKVBlockBytes, mk, bar(L::kBarKVFull),
-                      cb * 64, w.j * kTile, w.bhk);
-          tma_load_3d(sbase + L::kOffV + cb * L::kKVBlockBytes, mv, bar(L::kBarKVFull),
-                      cb * 64, w.j * kTile, w.bhk);
+          for (int cb = 0; cb < L::kColBlocks; ++cb) {
+            tma_load_3d(sbase + L::kOffK + cb * L::kKVBlockBytes, &tm_k, bar(L::kBarKVFull),
+                        cb * 64, w.j * kTile, w.bhk);
+            tma_load_3d(sbase + L::kOffV + cb * L::kKVBlockBytes, &tm_v, bar(L::kBarKVFull),
+                        cb * 64, w.j * kTile, w.bhk);
+          }
         }
         return true;
       };
       for (int ri = 0, u = take_unit(0); ok && u >= 0; u = take_unit(++ri), ++unit) {
         const BwdUnit w = unit_of(u);
-        if constexpr (kVar) {
-          mq = a.maps + 4 * (size_t)w.b;
-          mk = mq + 1;
-          mv = mq + 2;
-          mdo = mq + 3;
-          if (w.b != last_b) {  // the plan kernel wrote these maps
-            for (int i = 0; i < 4; ++i) tmap_acquire(mq + i);
-            last_b = w.b;
-          }
-        }
         // The unit's first block's Q / dO go out before its K / V: its stage
         // frees up while the previous unit still holds K and V, so it has landed
         // by the time K and V can be replaced.  Later blocks follow K and V, which
@@ -494,12 +490,20 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
           }
           const uint32_t sdst = sbase + stage_off(it);
           mbar_arrive_expect_tx(bar(L::kBarQFull + st), 2 * L::kQTileBytes + 2 * kQB * 4);
+          if constexpr (kVar) {
+            const int row = w.row0 + iq * kQB, valid = w.kv_len - iq * kQB;
+            load_rows<kQB, L::kColBlocks>(sdst, L::kQBlockBytes, &tm_q, tails.of[0],
+                                          bar(L::kBarQFull + st), row, valid, a.T, bh);
+            load_rows<kQB, L::kColBlocks>(sdst + L::kQTileBytes, L::kQBlockBytes, &tm_do, tails.of[3],
+                                          bar(L::kBarQFull + st), row, valid, a.T, bh);
+          } else {
 #pragma unroll
-          for (int cb = 0; cb < L::kColBlocks; ++cb) {
-            tma_load_3d(sdst + cb * L::kQBlockBytes, mq, bar(L::kBarQFull + st), cb * 64,
-                        iq * kQB, bh);
-            tma_load_3d(sdst + L::kQTileBytes + cb * L::kQBlockBytes, mdo,
-                        bar(L::kBarQFull + st), cb * 64, iq * kQB, bh);
+            for (int cb = 0; cb < L::kColBlocks; ++cb) {
+              tma_load_3d(sdst + cb * L::kQBlockBytes, &tm_q, bar(L::kBarQFull + st), cb * 64,
+                          iq * kQB, bh);
+              tma_load_3d(sdst + L::kQTileBytes + cb * L::kQBlockBytes, &tm_do,
+                          bar(L::kBarQFull + st), cb * 64, iq * kQB, bh);
+            }
           }
           const size_t voff = bwd_vec_off<kVar, kQB>(a, w, bh, iq);
           bulk_load(sdst + 2 * L::kQTileBytes, a.lse2 + voff, kQB * 4, bar(L::kBarQFull + st));
@@ -1257,7 +1261,7 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
       attr[0].val.cooperative = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, tdo, am) != cudaSuccess)
+      if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, tdo, am, Tails<false, 4>{}) != cudaSuccess)
         return FA_ERR_CUDA;
     } else {
       // dynamic dealing at D = 128 with the snake (measured against the static
@@ -1266,7 +1270,7 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
       BwdArgs am = a;
       am.dyn = (D == 128) ? a.snake : 0;
       if (launch_pdl(kernel, dim3(grid), dim3(threads), L::kAllocBytes, stream, tq, tk, tv,
-                     tdo, am) != cudaSuccess)
+                     tdo, am, Tails<false, 4>{}) != cudaSuccess)
         return FA_ERR_CUDA;
     }
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
@@ -1294,8 +1298,7 @@ int launch_bwd(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream) {
 }
 
 template <int D>
-static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
-                            cudaStream_t stream) {
+static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaStream_t stream) {
   constexpr bool kDet = D == 64;
   using L = BwdSmem<D>;
   int dev;
@@ -1330,7 +1333,7 @@ static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
   const int threads = (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
   record_timing(false, stream);
   if (a.qblk_rows == 128) {
-    const int rc = launch_bwd_main_q128(any, any, any, any, a, mod, grid, stream);
+    const int rc = launch_bwd_main_q128_var(m, a, mod, grid, stream);
     if (rc != FA_OK) return rc;
   } else if (a.deterministic) {
     cudaLaunchConfig_t cfg = {};
@@ -1343,9 +1346,10 @@ static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, any, any, any, any, a) != cudaSuccess) return FA_ERR_CUDA;
-  } else if (launch_pdl(kernel, dim3(grid), dim3(threads), L::kAllocBytes, stream, any, any, any,
-                        any, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, m.v, m.dO, a, m.tails) != cudaSuccess)
+      return FA_ERR_CUDA;
+  } else if (launch_pdl(kernel, dim3(grid), dim3(threads), L::kAllocBytes, stream, m.q, m.k, m.v,
+                        m.dO, a, m.tails) != cudaSuccess) {
     return FA_ERR_CUDA;
   }
   record_timing(true, stream);
@@ -1355,9 +1359,9 @@ static int launch_bwd_var_d(const CUtensorMap& any, BwdArgs a, int max_items,
   return FA_OK;
 }
 
-int launch_bwd_var(const CUtensorMap& any, const BwdArgs& a, int max_items, cudaStream_t stream) {
-  if (a.D == 128) return launch_bwd_var_d<128>(any, a, max_items, stream);
-  if (a.D == 64) return launch_bwd_var_d<64>(any, a, max_items, stream);
+int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, int max_items, cudaStream_t stream) {
+  if (a.D == 128) return launch_bwd_var_d<128>(m, a, max_items, stream);
+  if (a.D == 64) return launch_bwd_var_d<64>(m, a, max_items, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

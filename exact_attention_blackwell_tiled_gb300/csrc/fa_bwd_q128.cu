@@ -138,7 +138,8 @@ template <bool kMod, bool kVar>
 __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     bwd_main_q128(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_do, const BwdArgs a, int smem_bytes) {
+                  const __grid_constant__ CUtensorMap tm_do, const BwdArgs a, int smem_bytes,
+                  const __grid_constant__ Tails<kVar, 4> tails) {
   using L = Q128Layout;
   constexpr int D = L::D;
   extern __shared__ uint8_t smem_raw[];
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (!kVar && warp == L::kTmaWarp && lane == 0) {
+  if (warp == L::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -254,33 +255,29 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0, unit = 0;
-      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
-      const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v, *mdo = &tm_do;
       bool ok = true;
       auto load_kv = [&](const BwdUnit& w, uint32_t un) -> bool {
         if (!mbar_wait(bar(L::kBarKVEmpty), (un & 1) ^ 1, abort_flag)) return false;
         mbar_arrive_expect_tx(bar(L::kBarKVFull), 2 * L::kTileBytes);
+        if constexpr (kVar) {
+          const int row = w.row0 + w.j * kTile, valid = w.kv_len - w.j * kTile;
+          load_rows<kTile, 2>(sbase + L::kOffK, L::kBlockBytes, &tm_k, tails.of[1],
+                              bar(L::kBarKVFull), row, valid, a.T, w.bhk);
+          load_rows<kTile, 2>(sbase + L::kOffV, L::kBlockBytes, &tm_v, tails.of[2],
+                              bar(L::kBarKVFull), row, valid, a.T, w.bhk);
+        } else {
 #pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-          tma_load_3d(sbase + L::kOffK + cb * L::kBlockBytes, mk, bar(L::kBarKVFull), cb * 64,
-                      w.j * kTile, w.bhk);
-          tma_load_3d(sbase + L::kOffV + cb * L::kBlockBytes, mv, bar(L::kBarKVFull), cb * 64,
-                      w.j * kTile, w.bhk);
+          for (int cb = 0; cb < 2; ++cb) {
+            tma_load_3d(sbase + L::kOffK + cb * L::kBlockBytes, &tm_k, bar(L::kBarKVFull), cb * 64,
+                        w.j * kTile, w.bhk);
+            tma_load_3d(sbase + L::kOffV + cb * L::kBlockBytes, &tm_v, bar(L::kBarKVFull), cb * 64,
+                        w.j * kTile, w.bhk);
+          }
         }
         return true;
       };
       for (int ri = 0, u = take_unit(0); ok && u >= 0; u = take_unit(++ri), ++unit) {
         const BwdUnit w = bwd_any_unit<kMod, kVar, kQB2>(a, u, group, n_items);
-        if constexpr (kVar) {
-          mq = a.maps + 4 * (size_t)w.b;
-          mk = mq + 1;
-          mv = mq + 2;
-          mdo = mq + 3;
-          if (w.b != last_b) {  // the plan kernel wrote these maps
-            for (int i = 0; i < 4; ++i) tmap_acquire(mq + i);
-            last_b = w.b;
-          }
-        }
         // the unit's first block's Q / dO go out before its K / V: that stage
         // frees while the previous unit still holds K and V
         const int early = w.n_it < 1 ? w.n_it : 1;
@@ -298,12 +295,20 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           }
           const uint32_t sdst = sbase + stage_off(it);
           mbar_arrive_expect_tx(bar(L::kBarQFull + st), 2 * L::kTileBytes + 2 * L::kVecBytes);
+          if constexpr (kVar) {
+            const int row = w.row0 + iq * kQB2, valid = w.kv_len - iq * kQB2;
+            load_rows<kQB2, 2>(sdst, L::kBlockBytes, &tm_q, tails.of[0], bar(L::kBarQFull + st), row,
+                               valid, a.T, bh);
+            load_rows<kQB2, 2>(sdst + L::kTileBytes, L::kBlockBytes, &tm_do, tails.of[3],
+                               bar(L::kBarQFull + st), row, valid, a.T, bh);
+          } else {
 #pragma unroll
-          for (int cb = 0; cb < 2; ++cb) {
-            tma_load_3d(sdst + cb * L::kBlockBytes, mq, bar(L::kBarQFull + st), cb * 64,
-                        iq * kQB2, bh);
-            tma_load_3d(sdst + L::kTileBytes + cb * L::kBlockBytes, mdo,
-                        bar(L::kBarQFull + st), cb * 64, iq * kQB2, bh);
+            for (int cb = 0; cb < 2; ++cb) {
+              tma_load_3d(sdst + cb * L::kBlockBytes, &tm_q, bar(L::kBarQFull + st), cb * 64,
+                          iq * kQB2, bh);
+              tma_load_3d(sdst + L::kTileBytes + cb * L::kBlockBytes, &tm_do,
+                          bar(L::kBarQFull + st), cb * 64, iq * kQB2, bh);
+            }
           }
           const size_t voff = bwd_vec_off<kVar, kQB2>(a, w, bh, iq);
           bulk_load(sdst + 2 * L::kTileBytes, a.lse2 + voff, L::kVecBytes,
@@ -783,9 +788,10 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
 
 // Launches the main kernel of the 128-row-block backward (D = 128).  The
 // preprocess and convert kernels are the same as for the 64-row kernel.
-int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                         const CUtensorMap& tdo, const BwdArgs& a, bool mod, int grid,
-                         cudaStream_t stream) {
+template <bool kVar>
+static int launch_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const CUtensorMap& tdo, const Tails<kVar, 4>& tails, const BwdArgs& a,
+                       bool mod, int grid, cudaStream_t stream) {
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
@@ -793,27 +799,23 @@ int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   if (smem < Q128Layout::kBytes) return FA_ERR_UNSUPPORTED;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    const void* kernels[] = {
-        (const void*)bwd_main_q128<false, false>, (const void*)bwd_main_q128<true, false>,
-        (const void*)bwd_main_q128<false, true>, (const void*)bwd_main_q128<true, true>};
-    for (const void* k : kernels)
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return FA_ERR_CUDA;
+    if (cudaFuncSetAttribute(bwd_main_q128<false, kVar>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess ||
+        cudaFuncSetAttribute(bwd_main_q128<true, kVar>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+      return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  const bool var = a.items != nullptr;
-  const auto kernel = var ? (mod ? bwd_main_q128<true, true> : bwd_main_q128<false, true>)
-                          : (mod ? bwd_main_q128<true, false> : bwd_main_q128<false, false>);
-  const int which = (mod ? 1 : 0) + (var ? 2 : 0);
+  const auto kernel = mod ? bwd_main_q128<true, kVar> : bwd_main_q128<false, kVar>;
   // the setmaxnreg split assumes exactly kRegsLaunch registers per thread at
   // launch: a different count could leave the drain warpgroup's request
   // unserved, so such a build is refused
-  static bool regs_ok[4] = {};
-  if (!regs_ok[which]) {
+  static bool regs_ok[2] = {false, false};
+  if (!regs_ok[mod ? 1 : 0]) {
     cudaFuncAttributes fattr;
     if (cudaFuncGetAttributes(&fattr, kernel) != cudaSuccess) return FA_ERR_CUDA;
     if (fattr.numRegs != Q128Layout::kRegsLaunch) return FA_ERR_UNSUPPORTED;
-    regs_ok[which] = true;
+    regs_ok[mod ? 1 : 0] = true;
   }
   cudaError_t e;
   if (a.deterministic) {
@@ -827,13 +829,24 @@ int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, tdo, a, smem);
+    e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, tdo, a, smem, tails);
   } else {
     e = launch_pdl(kernel, dim3(grid), dim3(Q128Layout::kThreads), (size_t)smem, stream, tq, tk,
-                   tv, tdo, a, smem);
+                   tv, tdo, a, smem, tails);
   }
   if (e != cudaSuccess) return FA_ERR_CUDA;
   return FA_OK;
+}
+
+int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const CUtensorMap& tdo, const BwdArgs& a, bool mod, int grid,
+                         cudaStream_t stream) {
+  return launch_q128<false>(tq, tk, tv, tdo, {}, a, mod, grid, stream);
+}
+
+int launch_bwd_main_q128_var(const BwdVarMaps& m, const BwdArgs& a, bool mod, int grid,
+                             cudaStream_t stream) {
+  return launch_q128<true>(m.q, m.k, m.v, m.dO, m.tails, a, mod, grid, stream);
 }
 
 }  // namespace fa

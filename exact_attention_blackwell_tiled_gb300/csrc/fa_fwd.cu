@@ -80,14 +80,15 @@ struct FwdLayout {
 // kMod: 0 plain (no mask or the causal one), 1 a sliding window, 2 a window
 // and the relative-position bias (a.alibi) added to every score.  kSplit: a
 // unit covers one split of the kv tiles and writes fp32 parts for the merge.
-// kVar: a packed batch.  Its tensor maps are a.maps[3 b + 0 / 1 / 2], one set
-// per sequence that ends at the sequence's last row, so that a tile's rows past
-// it arrive as zeros, never as another sequence's (or uninitialised) rows,
-// whose infinities or NaN would survive a weight of zero in GEMM 2.
+// kVar: a packed batch.  Its tensor maps go over the rows of all sequences.  Rows of
+// Q and K past the sequence's last one (another sequence's, or uninitialised) only
+// reach scores that are masked or rows that are not stored; rows of V have to be zeros
+// there, since infinities or NaN would survive a weight of zero in GEMM 2 (load_rows).
 template <int D, int kMod, bool kSplit, bool kVar>
 __global__ void __launch_bounds__(320, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
+               const __grid_constant__ CUtensorMap tm_v, const FwdArgs a,
+               const __grid_constant__ Tails<kVar, 1> tails) {
   using L = FwdLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (!kVar && warp == 8 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -148,18 +149,22 @@ __global__ void __launch_bounds__(320, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t kv_it = 0, q_it = 0;
-      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
       bool ok = true;
-      auto load_kv = [&](const CUtensorMap* tm, int bhk, int j) -> bool {
+      // kv tile j of K or V, its first row `row` of head bhk; `valid` rows exist (kVar)
+      auto load_kv = [&](const CUtensorMap* tm, int bhk, int row, int valid) -> bool {
         const uint32_t st = kv_it % L::kKVStages;
         if (!mbar_wait(bar(L::kBarKVEmpty + st), ((kv_it / L::kKVStages) & 1) ^ 1, abort_flag))
           return false;
         mbar_arrive_expect_tx(bar(L::kBarKVFull + st), L::kTileBytes);
         const uint32_t dst = sbase + L::kOffKV + st * L::kTileBytes;
+        if constexpr (kVar) {
+          load_rows<kTile, L::kColBlocks>(dst, L::kBlockBytes, tm, tails.of[0],
+                                          bar(L::kBarKVFull + st), row, valid, a.T, bhk);
+        } else {
 #pragma unroll
-        for (int cb = 0; cb < L::kColBlocks; ++cb)
-          tma_load_3d(dst + cb * L::kBlockBytes, tm, bar(L::kBarKVFull + st), cb * 64, j * kTile,
-                      bhk);
+          for (int cb = 0; cb < L::kColBlocks; ++cb)
+            tma_load_3d(dst + cb * L::kBlockBytes, tm, bar(L::kBarKVFull + st), cb * 64, row, bhk);
+        }
         ++kv_it;
         return true;
       };
@@ -171,18 +176,6 @@ __global__ void __launch_bounds__(320, 1)
         pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), pair, w.split, lo, hi,
                              jlo, nmax);
         if (nmax == 0) continue;
-        const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v;
-        if constexpr (kVar) {
-          mq = a.maps + 3 * (size_t)w.b;
-          mk = mq + 1;
-          mv = mq + 2;
-          if (w.b != last_b) {  // the plan kernel wrote these maps
-            tmap_acquire(mq);
-            tmap_acquire(mk);
-            tmap_acquire(mv);
-            last_b = w.b;
-          }
-        }
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
           ok = false;
@@ -191,14 +184,21 @@ __global__ void __launch_bounds__(320, 1)
         mbar_arrive_expect_tx(bar(L::kBarQFull + qs), 2 * L::kTileBytes);
         const uint32_t qdst = sbase + L::kOffQ + qs * 2 * L::kTileBytes;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
+          // (a packed tile that the sequence does not reach: zeros)
+          const int q0 = (2 * pair + t) * kTile, row = !kVar ? q0 : (q0 < w.Sq ? w.row0 + q0 : a.T);
 #pragma unroll
           for (int cb = 0; cb < L::kColBlocks; ++cb)
-            tma_load_3d(qdst + t * L::kTileBytes + cb * L::kBlockBytes, mq,
-                        bar(L::kBarQFull + qs), cb * 64, (2 * pair + t) * kTile, w.bh);
+            tma_load_3d(qdst + t * L::kTileBytes + cb * L::kBlockBytes, &tm_q,
+                        bar(L::kBarQFull + qs), cb * 64, row, w.bh);
+        }
         ++q_it;
         for (int j = jlo; j < jlo + nmax; ++j) {
-          if (!load_kv(mk, bhk, j) || !load_kv(mv, bhk, j)) { ok = false; break; }
+          const int row = w.row0 + j * kTile;
+          if (!load_kv(&tm_k, bhk, row, kTile) || !load_kv(&tm_v, bhk, row, w.Sq - j * kTile)) {
+            ok = false;
+            break;
+          }
         }
       }
       // Let every issued copy land before the CTA can exit.
@@ -710,13 +710,13 @@ static int launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     note_launches(1);
     return FA_OK;
   }
-  using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, FwdArgs);
+  using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, FwdArgs, Tails<false, 1>);
   const KernelFn kernels[2][3] = {{fwd_kernel<D, 0, false, false>, fwd_kernel<D, 1, false, false>,
                                    fwd_kernel<D, 2, false, false>},
                                   {fwd_kernel<D, 0, true, false>, fwd_kernel<D, 1, true, false>,
                                    fwd_kernel<D, 2, true, false>}};
   if (launch_pdl(kernels[a.n_split > 1 ? 1 : 0][mode], dim3(grid), dim3(320), L::kAllocBytes,
-                 stream, tq, tk, tv, a) != cudaSuccess)
+                 stream, tq, tk, tv, a, Tails<false, 1>{}) != cudaSuccess)
     return FA_ERR_CUDA;
   record_timing(true, stream);
   note_launches(1);
@@ -724,7 +724,9 @@ static int launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 }
 
 template <int D>
-static int launch_fwd_var_d(const CUtensorMap& any, FwdArgs a, int max_items, cudaStream_t stream) {
+static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const TailMaps& v_tails, FwdArgs a, int max_items,
+                            cudaStream_t stream) {
   using L = FwdLayout<D>;
   int dev;
   DeviceInfo info;
@@ -749,19 +751,21 @@ static int launch_fwd_var_d(const CUtensorMap& any, FwdArgs a, int max_items, cu
   record_timing(false, stream);
   // D = 64 without a window: the ring of score buffers, as in the dense call
   if (fwd_ring64_eligible(a, D, plain ? 0 : 1)) {
-    if (launch_fwd_ring64(any, any, any, a, grid, stream) != FA_OK) return FA_ERR_CUDA;
-  } else if (launch_pdl(kernel, dim3(grid), dim3(320), L::kAllocBytes, stream, any, any, any, a) !=
-      cudaSuccess)
+    if (launch_fwd_ring64_var(tq, tk, tv, v_tails, a, grid, stream) != FA_OK) return FA_ERR_CUDA;
+  } else if (launch_pdl(kernel, dim3(grid), dim3(320), L::kAllocBytes, stream, tq, tk, tv, a,
+                        Tails<true, 1>{{v_tails}}) != cudaSuccess) {
     return FA_ERR_CUDA;
+  }
   record_timing(true, stream);
   note_launches(1);
   return FA_OK;
 }
 
-int launch_fwd_var(const CUtensorMap& any, const FwdArgs& a, int D, int max_items,
+int launch_fwd_var(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const TailMaps& v_tails, const FwdArgs& a, int D, int max_items,
                    cudaStream_t stream) {
-  if (D == 128) return launch_fwd_var_d<128>(any, a, max_items, stream);
-  if (D == 64) return launch_fwd_var_d<64>(any, a, max_items, stream);
+  if (D == 128) return launch_fwd_var_d<128>(tq, tk, tv, v_tails, a, max_items, stream);
+  if (D == 64) return launch_fwd_var_d<64>(tq, tk, tv, v_tails, a, max_items, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

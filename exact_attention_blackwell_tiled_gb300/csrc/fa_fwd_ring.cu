@@ -99,13 +99,14 @@ static_assert(RingLayout::kRing * 64 + RingLayout::D <= (int)RingLayout::kColsPe
 
 constexpr int kRingThreads = 416;  // 8 softmax warps, the producer, four issuers
 
-// kVar: a packed batch, as in fwd_kernel (tensor maps per sequence, every
-// exponential on MUFU).
+// kVar: a packed batch, as in fwd_kernel (V tiles by load_rows, every exponential on
+// MUFU).
 template <bool kVar>
 __global__ void __launch_bounds__(kRingThreads, 1)
     fwd_ring64_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
+                      const __grid_constant__ CUtensorMap tm_v, const FwdArgs a,
+                      const __grid_constant__ Tails<kVar, 1> tails) {
   using L = RingLayout;
   constexpr int D = L::D;
   extern __shared__ uint8_t smem_raw[];
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
-  if (!kVar && warp == 8 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -170,9 +171,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     // half K tiles, ahead of GEMM 2).
     if (lane == 0) {
       uint32_t k_it = 0, v_it = 0, q_it = 0;
-      int last_b = -1;  // the sequence whose maps were acquired last (kVar)
-      const CUtensorMap *mq = &tm_q, *mk = &tm_k, *mv = &tm_v;
       bool ok = true;
+      int row0 = 0, kv_len = 0;  // of the unit's sequence (kVar)
       auto load = [&](bool is_v, int bhk, int j) -> bool {
         uint32_t& it = is_v ? v_it : k_it;
         const int n = is_v ? L::kVStages : L::kKStages;
@@ -181,8 +181,14 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         const uint32_t empty = bar((is_v ? L::kBarVEmpty : L::kBarKEmpty) + st);
         if (!mbar_wait(empty, ((it / n) & 1) ^ 1, abort_flag)) return false;
         mbar_arrive_expect_tx(full, L::kTileBytes);
-        tma_load_3d(sbase + (is_v ? L::kOffV : L::kOffK) + st * L::kTileBytes,
-                    is_v ? mv : mk, full, 0, j * kTile, bhk);
+        const uint32_t dst = sbase + (is_v ? L::kOffV : L::kOffK) + st * L::kTileBytes;
+        if (kVar && is_v) {
+          if constexpr (kVar)
+            load_rows<kTile, 1>(dst, 0, &tm_v, tails.of[0], full, row0 + j * kTile,
+                                kv_len - j * kTile, a.T, bhk);
+        } else {
+          tma_load_3d(dst, is_v ? &tm_v : &tm_k, full, 0, row0 + j * kTile, bhk);
+        }
         ++it;
         return true;
       };
@@ -193,16 +199,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
                             nmax);
         if (nmax == 0) continue;
-        if constexpr (kVar) {
-          mq = a.maps + 3 * (size_t)w.b;
-          mk = mq + 1;
-          mv = mq + 2;
-          if (w.b != last_b) {  // the plan kernel wrote these maps
-            tmap_acquire(mq);
-            tmap_acquire(mk);
-            tmap_acquire(mv);
-            last_b = w.b;
-          }
+        if (kVar) {
+          row0 = w.row0;
+          kv_len = w.Sq;
         }
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
@@ -212,9 +211,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         mbar_arrive_expect_tx(bar(L::kBarQFull + qs), 2 * L::kTileBytes);
         const uint32_t qdst = sbase + L::kOffQ + qs * 2 * L::kTileBytes;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          tma_load_3d(qdst + t * L::kTileBytes, mq, bar(L::kBarQFull + qs), 0,
-                      (2 * w.pair + t) * kTile, w.bh);
+        for (int t = 0; t < 2; ++t) {
+          // (a packed tile that the sequence does not reach: zeros)
+          const int q0 = (2 * w.pair + t) * kTile;
+          tma_load_3d(qdst + t * L::kTileBytes, &tm_q, bar(L::kBarQFull + qs), 0,
+                      !kVar ? q0 : (q0 < w.Sq ? row0 + q0 : a.T), w.bh);
+        }
         ++q_it;
         ok = load(false, bhk, jlo) && (nmax < 2 || load(false, bhk, jlo + 1));
         for (int i = 0; ok && i < nmax; ++i)
@@ -523,27 +525,36 @@ bool fwd_ring64_eligible(const FwdArgs& a, int D, int mode) {
   return D == 64 && mode == 0 && a.n_split <= 1 && a.scale_log2 > 0.f;
 }
 
-int launch_fwd_ring64(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                      const FwdArgs& a, int grid, cudaStream_t stream) {
+template <bool kVar>
+static int launch_ring(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const FwdArgs& a, const Tails<kVar, 1>& tails, int grid,
+                       cudaStream_t stream) {
   using L = RingLayout;
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    const void* kernels[] = {(const void*)fwd_ring64_kernel<false>,
-                             (const void*)fwd_ring64_kernel<true>};
-    for (const void* k : kernels)
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAllocBytes) !=
-          cudaSuccess)
-        return FA_ERR_CUDA;
+    if (cudaFuncSetAttribute(fwd_ring64_kernel<kVar>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::kAllocBytes) != cudaSuccess)
+      return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  const auto kernel = a.items ? fwd_ring64_kernel<true> : fwd_ring64_kernel<false>;
-  if (launch_pdl(kernel, dim3(grid), dim3(kRingThreads), L::kAllocBytes, stream, tq, tk, tv, a) !=
-      cudaSuccess)
+  if (launch_pdl(fwd_ring64_kernel<kVar>, dim3(grid), dim3(kRingThreads), L::kAllocBytes, stream, tq,
+                 tk, tv, a, tails) != cudaSuccess)
     return FA_ERR_CUDA;
   return FA_OK;
+}
+
+int launch_fwd_ring64(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                      const FwdArgs& a, int grid, cudaStream_t stream) {
+  return launch_ring<false>(tq, tk, tv, a, {}, grid, stream);
+}
+
+int launch_fwd_ring64_var(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const TailMaps& v_tails, const FwdArgs& a, int grid,
+                          cudaStream_t stream) {
+  return launch_ring<true>(tq, tk, tv, a, Tails<true, 1>{{v_tails}}, grid, stream);
 }
 
 }  // namespace fa

@@ -57,14 +57,23 @@ struct alignas(32) VarItem {
   int unused[3];
 };
 
-// Plan of a packed call: one warp per sequence edits the tensor maps (copies of
-// tmpl whose base is the sequence's first row and whose row count is its
-// length) and writes the sequence's items at their places in the order.
+// Tensor maps over a packed tensor [T, H, D] in boxes of 64, 16, 4 and 1 rows (by 64
+// columns): the pieces of a tile that ends with its sequence.
+constexpr int kTailBoxes = 4;
+struct TailMaps {
+  CUtensorMap box[kTailBoxes];
+};
+// The kernel parameter that carries them, for N tensors; nothing in dense calls.
+template <bool kVar, int N>
+struct Tails {
+  TailMaps of[N];
+};
+template <int N>
+struct Tails<false, N> {};
+
+// Plan of a packed call: one warp per sequence writes the sequence's items at their
+// places in the order.
 struct PlanArgs {
-  CUtensorMap tmpl[4];
-  const void* base[4];
-  long long row_bytes[4];
-  int n_maps;
   const int* cu;  // [B + 1] first rows
   int B, T;
   int item_rows;  // 256 (forward: pairs of query tiles) or 128 (backward: kv tiles)
@@ -73,7 +82,6 @@ struct PlanArgs {
   VarItem* items;
   int max_items;
   int* n_items;
-  CUtensorMap* maps;
   int* status;   // gets FA_ERR_INVALID_ARG where cu is not ascending within [0, T]
   int clear;     // 1: *status and *counter start at zero (backward)
   int* counter;
@@ -107,20 +115,20 @@ struct FwdArgs {
   int split_tiles;
   float* o_part;    // [n_split, B * Hq, Sq, D]
   float* lse_part;  // [n_split, B * Hq, Sq], natural log, -inf: no visible key
-  // packed calls: the plan's items and their number, three tensor maps per
-  // sequence (q, k, v), and the rows of the packed tensors
+  // packed calls: the plan's items and their number, and the rows of the packed
+  // tensors
   const VarItem* items;
   const int* n_items;
-  const CUtensorMap* maps;
   int T;
 };
 
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                const FwdArgs& a, int D, cudaStream_t stream);
 
-// The same kernel over a packed batch: `any` fills the tensor map parameters,
-// which it does not read; at most max_items items.
-int launch_fwd_var(const CUtensorMap& any, const FwdArgs& a, int D, int max_items,
+// The same kernel over a packed batch (maps over all its rows) of at most max_items
+// items; v_tails: v's smaller boxes.
+int launch_fwd_var(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const TailMaps& v_tails, const FwdArgs& a, int D, int max_items,
                    cudaStream_t stream);
 int* fwd_status_word();  // on the current device; null if it cannot be found
 
@@ -131,6 +139,9 @@ int* fwd_status_word();  // on the current device; null if it cannot be found
 bool fwd_ring64_eligible(const FwdArgs& a, int D, int mode);
 int launch_fwd_ring64(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const FwdArgs& a, int grid, cudaStream_t stream);
+// ... over a packed batch
+int launch_fwd_ring64_var(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const TailMaps& v_tails, const FwdArgs& a, int grid, cudaStream_t stream);
 
 
 // Log-sum-exp merge of n attention parts over disjoint key sets.
@@ -187,12 +198,11 @@ struct BwdArgs {
   int dq_groups;
   size_t dq_group_stride;  // floats from one accumulator to the next
   int sem_group_stride;    // semaphores from one group to the next
-  // packed calls: the plan, four tensor maps per sequence (q, k, v, dO), the
-  // rows of the packed tensors, and the rows that lse2 and delta hold per head
-  // (every sequence padded to qblk_rows); the dQ accumulators are [Hq, T, D]
+  // packed calls: the plan, the rows of the packed tensors, and the rows that lse2
+  // and delta hold per head (every sequence padded to qblk_rows); the dQ
+  // accumulators are [Hq, T, D]
   const VarItem* items;
   const int* n_items;
-  const CUtensorMap* maps;
   int T, T_pad;
   // packed calls with few units: each q head of a group is a unit of its own and
   // leaves fp32 parts of dK and dV [Hq, T, D], which the last kernel sums in head
@@ -236,9 +246,13 @@ struct BwdMaps {
 };
 
 int launch_bwd(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream);
-// The same for a packed batch (at most max_items items); `any` as in
-// launch_fwd_var.
-int launch_bwd_var(const CUtensorMap& any, const BwdArgs& a, int max_items, cudaStream_t stream);
+// The same for a packed batch of at most max_items items (maps over all its rows, q
+// and dO in boxes of a.qblk_rows rows).
+struct BwdVarMaps {
+  CUtensorMap q, k, v, dO;
+  Tails<true, 4> tails;  // of q, k, v and dO
+};
+int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, int max_items, cudaStream_t stream);
 
 // The CTA-pair main kernel (D = 128, atomic dQ, no score modification), and
 // the process-wide kernel choice fa_set_bwd_kernel sets.
@@ -262,6 +276,9 @@ inline int bwd_qblk_rows(int D, int deterministic) {
 int launch_bwd_main_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const BwdArgs& a, bool mod, int grid,
                          cudaStream_t stream);
+// ... over a packed batch
+int launch_bwd_main_q128_var(const BwdVarMaps& m, const BwdArgs& a, bool mod, int grid,
+                             cudaStream_t stream);
 
 // The 4-bit cache: the status word its kernels record bad tables and lengths in
 // (null if it cannot be found), and the shape rules of its calls.

@@ -9,10 +9,9 @@
 //     the longest first, as the dense causal calls deal theirs.  An item's place
 //     is counted in closed form (the items before it, over all sequences), so
 //     every item is written at once and no sort or scan runs.
-//   - A tile may reach past its sequence's last row.  Each sequence gets its own
-//     tensor maps, copies of the call's that start at its first row and end at
-//     its last, so the TMA unit fills the rows past it with zeros: the products
-//     never meet another sequence's rows or uninitialised memory.
+//   - A tile may reach past its sequence's last row: it is loaded in pieces, zeros
+//     behind the sequence's rows, by maps over the rows of all sequences (load_rows,
+//     var_common.cuh).
 // The plan costs one launch of a warp per sequence and no pass over the data; it
 // overlaps the end of the kernel before it and the attention kernel's prologue.
 #include <cuda.h>
@@ -61,20 +60,13 @@ __device__ __forceinline__ int items_before(int mode, int t, int n_own, int blk_
 // One warp per sequence.  Bound by the latency of reading cu once and by the
 // counting: B steps for every 32 items of a sequence (lanes are items), or B / 32
 // for every item where a sequence has few (lanes are the other sequences).  With
-// the lengths in shared memory 16384 tokens in 3 to 6 sequences take 5 us between
-// the kernels around it (7 to 9 us cold and alone), against 14-25 us when each item
-// read them again.
-__global__ void __launch_bounds__(kPlanWarps * 32)
-    plan_kernel(const __grid_constant__ PlanArgs p) {
-  __shared__ alignas(128) CUtensorMap slots[kPlanWarps][4];
+// the lengths in shared memory 16384 tokens in 3 sequences take 3.6 us, 437 in short
+// ones 3.7 (cold and alone), against 14-25 us when each item read them again.
+__global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const PlanArgs p) {
   __shared__ int s_len[kPlanCache], s_row0[kPlanWarps];
   __shared__ int s_total;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s_total = 0;
-  // (before the wait: the kernel's own arguments; 0.9 us of a short call's 9.3)
-  for (int m = 0; m < p.n_maps; ++m)
-    reinterpret_cast<uint32_t*>(&slots[warp][m])[lane] =
-        reinterpret_cast<const uint32_t*>(&p.tmpl[m])[lane];
   __syncthreads();
   grid_dep_wait();  // the caller's kernels may have written cu
   grid_dep_launch();
@@ -107,24 +99,6 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
   auto len_of = [&](int i) { return i < kPlanCache ? s_len[i] : p.cu[i + 1] - p.cu[i]; };
   const int row0 = s_row0[warp], len = len_of(b);
   if (len == 0) return;
-  if (lane < p.n_maps) {
-    const uint32_t s = smem_u32(&slots[warp][lane]);
-    const uint64_t addr =
-        reinterpret_cast<uint64_t>(p.base[lane]) + (uint64_t)row0 * (uint64_t)p.row_bytes[lane];
-    asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(s),
-                 "l"(addr)
-                 : "memory");
-    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(s),
-                 "r"(len)
-                 : "memory");
-  }
-  __syncwarp();
-  for (int m = 0; m < p.n_maps; ++m)
-    asm volatile(
-        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned"
-        " [%0], [%1], 128;" ::"l"(p.maps + (size_t)b * p.n_maps + m),
-        "r"(smem_u32(&slots[warp][m]))
-        : "memory");
   int pad0 = 0;
   for (int i = lane; i < b; i += 32) pad0 += (len_of(i) + p.pad - 1) & -p.pad;
   pad0 = warp_add(pad0);
@@ -181,7 +155,7 @@ struct VarLayout {
   int pad;  // rows of the backward's query blocks
   long long t_pad;
   bool split;  // q heads are units of their own (BwdArgs::dk_part)
-  size_t off_items, off_maps, off_acc, off_delta, off_lse2, off_sem, off_dk, off_dv, total;
+  size_t off_items, off_acc, off_delta, off_lse2, off_sem, off_dk, off_dv, total;
 };
 
 // Up to this many (kv tile, kv head) units a grouped backward splits its q heads:
@@ -204,8 +178,10 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
   const int rows = backward ? 128 : 256;
   L.max_items = T / rows + B;
   L.off_items = kHeader;
-  L.off_maps = up256(L.off_items + (size_t)L.max_items * sizeof(VarItem));
-  L.total = up256(L.off_maps + (size_t)B * (backward ? 4 : 3) * sizeof(CUtensorMap));
+  // (a workspace has room for a tensor map per sequence and tensor behind the items,
+  // which nothing uses: its size is part of the interface)
+  const size_t maps = (size_t)B * (backward ? 4 : 3) * sizeof(CUtensorMap);
+  L.total = up256(up256(L.off_items + (size_t)L.max_items * sizeof(VarItem)) + maps);
   if (!backward) return L;
   // as many accumulators as a dense call of twice the mean length would take
   const long long twice = 2LL * T / B + 1;
@@ -243,19 +219,18 @@ struct VarTensor {
   int H, box_rows;
 };
 
-// The plan's maps from the call's tensors (in the order of t).
-int plan_maps(const VarTensor* t, int n, int T, int D, PlanArgs* p) {
-  p->n_maps = n;
-  for (int i = 0; i < n; ++i) {
-    long long row, head;
-    const int rc = tensor_strides(t[i].s, t[i].H, D, &row, &head);
-    if (rc) return rc;
-    p->base[i] = t[i].p;
-    p->row_bytes[i] = row * 2;
-    if (!make_tmap_strided(&p->tmpl[i], t[i].p, t[i].H, T, D, row, head, t[i].box_rows))
-      return FA_ERR_CUDA;
-  }
-  return FA_OK;
+// A tensor's map over all its rows, in boxes of t.box_rows.
+bool full_map(const VarTensor& t, int T, int D, CUtensorMap* map) {
+  long long row, head;
+  return tensor_strides(t.s, t.H, D, &row, &head) == FA_OK &&
+         make_tmap_strided(map, t.p, t.H, T, D, row, head, t.box_rows);
+}
+
+// ... and in the pieces' boxes.
+bool tail_maps(const VarTensor& t, int T, int D, TailMaps* maps) {
+  for (int i = 0; i < kTailBoxes; ++i)
+    if (!full_map({t.p, t.s, t.H, 64 >> (2 * i)}, T, D, &maps->box[i])) return false;
+  return true;
 }
 
 int check_strides(const VarTensor* t, int n, int D) {
@@ -300,8 +275,12 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  CUtensorMap maps[3];
+  TailMaps v_tails;
+  for (int i = 0; i < 3; ++i)
+    if (!full_map(t[i], T, D, &maps[i])) return FA_ERR_CUDA;
+  if (!tail_maps(t[2], T, D, &v_tails)) return FA_ERR_CUDA;
   PlanArgs p{};
-  if ((rc = plan_maps(t, 3, T, D, &p))) return rc;
   FwdArgs a{};
   a.wl = window_side(window_left, T);
   a.wr = window_side(window_right, T);
@@ -315,7 +294,6 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   p.items = reinterpret_cast<VarItem*>(ws + L.off_items);
   p.max_items = L.max_items;
   p.n_items = reinterpret_cast<int*>(ws + 64);
-  p.maps = reinterpret_cast<CUtensorMap*>(ws + L.off_maps);
   p.status = fwd_status_word();
   p.counter = reinterpret_cast<int*>(ws + 128);
   if (!p.status) return FA_ERR_CUDA;
@@ -329,11 +307,10 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   a.n_split = 1;
   a.items = p.items;
   a.n_items = p.n_items;
-  a.maps = p.maps;
   a.T = T;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((rc = launch_plan(p, st))) return rc;
-  return launch_fwd_var(p.tmpl[0], a, D, L.max_items, st);
+  return launch_fwd_var(maps[0], maps[1], maps[2], v_tails, a, D, L.max_items, st);
 }
 
 int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const void* dO,
@@ -361,8 +338,11 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  BwdVarMaps m;
+  CUtensorMap* const maps[4] = {&m.q, &m.k, &m.v, &m.dO};
+  for (int i = 0; i < 4; ++i)
+    if (!full_map(t[i], T, D, maps[i]) || !tail_maps(t[i], T, D, &m.tails.of[i])) return FA_ERR_CUDA;
   PlanArgs p{};
-  if ((rc = plan_maps(t, 4, T, D, &p))) return rc;
   BwdArgs a{};
   a.wl = window_side(window_left, T);
   a.wr = window_side(window_right, T);
@@ -375,7 +355,6 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   p.items = reinterpret_cast<VarItem*>(ws + L.off_items);
   p.max_items = L.max_items;
   p.n_items = reinterpret_cast<int*>(ws + 64);
-  p.maps = reinterpret_cast<CUtensorMap*>(ws + L.off_maps);
   p.status = reinterpret_cast<int*>(ws);
   p.clear = 1;
   p.pad = L.pad;
@@ -433,12 +412,11 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   }
   a.items = p.items;
   a.n_items = p.n_items;
-  a.maps = p.maps;
   a.T = T;
   a.T_pad = (int)L.t_pad;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((rc = launch_plan(p, st))) return rc;
-  return launch_bwd_var(p.tmpl[0], a, L.max_items, st);
+  return launch_bwd_var(m, a, L.max_items, st);
 }
 
 }  // extern "C"

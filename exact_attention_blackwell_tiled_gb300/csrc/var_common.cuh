@@ -4,6 +4,7 @@
 #pragma once
 
 #include "fa_internal.h"
+#include "ptx.cuh"
 
 namespace fa {
 
@@ -18,13 +19,45 @@ __device__ __forceinline__ VarItem load_item(const VarItem* items, int i) {
   return it;
 }
 
-// Orders this thread's later reads of a tensor map (by the TMA unit) after the
-// plan kernel's write of it, which the grid dependency has already made visible
-// to ordinary loads.
-__device__ __forceinline__ void tmap_acquire(const CUtensorMap* m) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
-                   reinterpret_cast<uint64_t>(m))
-               : "memory");
+// Rows row .. row + valid - 1 of head `head` of a packed tensor into a tile of kRows
+// rows (128 bytes each, kColBlocks blocks of 64 columns), zeros behind them: one box
+// where the tile is full, pieces of 64, 16, 4 and 1 rows where the sequence ends in
+// it, at most 11 with those of rows T .., which do not exist and arrive as zeros.  So
+// the products never meet another sequence's rows.  (The swizzle goes by the address
+// in shared memory, so a piece lies as the full box would have put its rows.)
+//
+// Maps of each sequence by itself, written by the plan kernel, would need no pieces;
+// but then the TMA unit reads descriptors that another kernel has just written, and a
+// run of calls whose tensors lay all over the address space ended in an illegal access,
+// with every other address shown in bounds.  These maps are made on the host.
+template <int kRows, int kColBlocks>
+__device__ __forceinline__ void load_rows(uint32_t dst, uint32_t block_bytes, const CUtensorMap* full,
+                                          const TailMaps& tails, uint32_t bar, int row, int valid,
+                                          int T, int head) {
+  if (valid >= kRows) {
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb)
+      tma_load_3d(dst + cb * block_bytes, full, bar, cb * 64, row, head);
+    return;
+  }
+  int at = 0, from = row, n = valid;
+#pragma unroll 1
+  for (int zeros = 0; zeros < 2; ++zeros) {
+#pragma unroll 1
+    for (int x = 0; x < kTailBoxes; ++x) {
+      const int rows = 64 >> (2 * x);
+#pragma unroll 1
+      for (; n >= rows; n -= rows) {
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb)
+          tma_load_3d(dst + cb * block_bytes + at * 128, &tails.box[x], bar, cb * 64, from, head);
+        at += rows;
+        if (!zeros) from += rows;
+      }
+    }
+    from = T;
+    n = kRows - at;
+  }
 }
 
 }  // namespace fa

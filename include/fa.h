@@ -270,9 +270,9 @@ int fa_lse_merge(const float* o_parts, const float* lse_parts, int n_parts, void
  * rows padded per sequence to 128, times Hq, stay below 2^31.  The bf16 tensors are 16-byte
  * aligned, lse and cu_seqlens 4-byte aligned.
  * workspace: fa_varlen_workspace_bytes(...) bytes of device memory, 256-byte
- * aligned, uninitialised; it holds the work list and tensor maps of the call
- * (and the backward's fp32 accumulators), so calls that may run at the same time
- * need one each, captured ones among them.
+ * aligned, uninitialised; it holds the work list of the call (and the backward's fp32
+ * accumulators), so calls that may run at the same time need one each, captured ones
+ * among them.
  * The backward's gradients sum over the heads of a group; deterministic != 0
  * gives the same bits in every run, as in fa_bwd.
  */
