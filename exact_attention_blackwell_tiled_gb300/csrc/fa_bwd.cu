@@ -397,6 +397,9 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (kVar) {
+    if (warp == R::kTmaWarp) prefetch_tails(tails, lane);
+  }
   if (warp == R::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);

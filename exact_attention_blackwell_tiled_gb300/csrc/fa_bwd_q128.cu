@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (kVar) {
+    if (warp == L::kTmaWarp) prefetch_tails(tails, lane);
+  }
   if (warp == L::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);

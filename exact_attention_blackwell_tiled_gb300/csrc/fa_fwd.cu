@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (kVar) {
+    if (warp == 8) prefetch_tails(tails, lane);
+  }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);

@@ -19,6 +19,12 @@ __device__ __forceinline__ VarItem load_item(const VarItem* items, int i) {
   return it;
 }
 
+// The pieces' maps of N tensors on their way before the first use, a lane each.
+template <int N>
+__device__ __forceinline__ void prefetch_tails(const Tails<true, N>& tails, int lane) {
+  if (lane < N * kTailBoxes) tma_prefetch_desc(&tails.of[lane / kTailBoxes].box[lane % kTailBoxes]);
+}
+
 // Rows row .. row + valid - 1 of head `head` of a packed tensor into a tile of kRows
 // rows (128 bytes each, kColBlocks blocks of 64 columns), zeros behind them: one box
 // where the tile is full, pieces of 64, 16, 4 and 1 rows where the sequence ends in
