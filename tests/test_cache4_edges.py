@@ -97,3 +97,33 @@ def test_read_reports_a_negative_count(first):
     k, v = fa.cache4_read(cache, table, at, _i32([8, -2]), 8, 64)
     assert fa.cache4_status() == 1
     assert bool((k[1] == 0).all()) and bool((v[1] == 0).all()) and bool((k[0] != 0).any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_past_32_bit_offsets(D):
+    """A pool of more than 2^32 bytes: the first and the last pages, and the eviction from
+    the one end to the other."""
+    Hkv, page, lens = 4, 128, [300, 140]
+    per_page = fa.cache4_empty(1, Hkv, D, page).numel()
+    pages = (1 << 32) // per_page + 40
+    gen = torch.Generator().manual_seed(D)
+    k, v = (torch.randn(440, Hkv, D, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(2, 2 * Hkv, D, generator=gen).to(torch.bfloat16).cuda()
+    n, cu = _i32(lens), _i32([0, 300, 440])
+    low = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)
+    high = pages - 6 + low
+    cache = fa.cache4_empty(pages, Hkv, D, page)
+    got = []
+    for table in (low, high):
+        fa.cache4_append(cache, k, v, table, _i32([0, 0]), cu)
+        w = torch.zeros(2, Hkv, 300, device="cuda")
+        out = fa.cache4_attend(q, cache, table, n, weights=w)
+        got.append((*out, w, *fa.cache4_read(cache, table, None, n, 300, D)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool((got[0][3] != 0).any())
+    src, _, kept = fa.cache4_evict(cache, high, n, got[0][2], low + 6, D, 100, 10)
+    new = fa.cache4_read(cache, low + 6, None, kept, 100, D)
+    for x, y in zip(got[0][3:], new):
+        assert torch.equal(y, x.gather(2, src.long()[..., None].expand(-1, -1, -1, D)))
+    assert fa.cache4_status() == fa.FA_OK

@@ -44,3 +44,40 @@ def test_sequences_past_the_kept_lengths(D, causal):
             again = fa.bwd_varlen(qd, kd, vd, o, dod, lse, cud, causal=causal, deterministic=True)
             for a, b in zip(grads, again):
                 assert torch.equal(a, b)
+
+
+def test_tensors_past_32_bit_offsets():
+    """More than 2^31 elements of q, o and their gradients: the last sequences against the
+    reference on their rows alone."""
+    Hq, Hkv, D, n, tail = 128, 2, 128, 128, [77, 300]
+    lens = [n] * 1050 + tail
+    cu = torch.tensor([0, *lens]).cumsum(0)
+    T = int(cu[-1])
+    assert T * Hq * D > 2 ** 31
+    torch.manual_seed(5)
+    q, do = (torch.randn(T, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.randn(T, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cud = cu.to(torch.int32).cuda()
+    o, lse = fa.fwd_varlen(q, k, v, cud, causal=True)
+    lo = T - sum(tail)
+    heads = [0, 1, 63, 64, 127]  # of both kv heads
+    rows = [x[lo:].cpu() for x in (q, k, v, do)]
+    bounds = [(0, tail[0]), (tail[0], sum(tail))]
+
+    def check(got, name, ref):
+        assert_within(got, ref[name], ref[name + "_tol"], name)
+
+    refs = []
+    for h in heads:
+        g = h // (Hq // Hkv)
+        r = packed(rows[0][:, h:h + 1], rows[1][:, g:g + 1], rows[2][:, g:g + 1], bounds,
+                   do=rows[3][:, h:h + 1])
+        refs.append(r)
+        check(o[lo:, h:h + 1], "o", r)
+        check(lse[h:h + 1, lo:], "lse", r)
+    for det in (False, True):
+        dq, dk, dv = fa.bwd_varlen(q, k, v, o, do, lse, cud, causal=True, deterministic=det)
+        for h, r in zip(heads, refs):
+            check(dq[lo:, h:h + 1], "dq", r)
+        del dq, dk, dv
+    assert fa.fwd_status() == fa.FA_OK
