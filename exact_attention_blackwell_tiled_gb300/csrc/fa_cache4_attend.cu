@@ -66,6 +66,10 @@ constexpr int kWarps = 4;      // per block; they share nothing but the launch
 //   D = 64, 38 x 300: 5.1 / 6.8 against 11.7 / 13.8;  152 x 300 (eight rows per SM):
 //   18.3 / 25.0 against 20.1 / 23.4;  152 x 1000: 34.7 / 47.4 against 35.8 / 43.4;
 //   228 x 300: 27.4 / 37.7 against 29.1 / 34.2;  400 x 300: 49.0 / 65.7 against 42.1 / 51.7.
+// The rule goes by the step without weights: with them it loses 2 to 9% at the most
+// rows it takes.  It sees the table's width, not the lengths (which are on the device):
+// short caches in a table of more than 1024 slots take shares.  Other groups than four
+// query heads were not measured.
 constexpr int kOwnWarps = 8, kOwnBlocks = 64;
 template <int D, int NT>
 constexpr int kOwnRowsPerSm = D == 64 && NT == 1 ? 8 : 2;

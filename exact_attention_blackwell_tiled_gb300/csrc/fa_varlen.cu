@@ -160,7 +160,8 @@ struct VarLayout {
 
 // Up to this many (kv tile, kv head) units a grouped backward splits its q heads:
 // with u units a causal sequence's longest one is 304 / u of an SM's even share of
-// 152, so below two to four units per SM the longest unit sets the time.
+// 152, so below two to four units per SM the longest unit sets the time.  (The parts take
+// 8 T Hq D bytes, at most 80 MB times the group at D = 128: T Hkv is below 77,824.)
 constexpr long long kSplitUnits = 608;
 
 int check_var(int B, int T, int Hq, int Hkv, int D) {
@@ -183,7 +184,8 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
   const size_t maps = (size_t)B * (backward ? 4 : 3) * sizeof(CUtensorMap);
   L.total = up256(up256(L.off_items + (size_t)L.max_items * sizeof(VarItem)) + maps);
   if (!backward) return L;
-  // as many accumulators as a dense call of twice the mean length would take
+  // as many accumulators as a dense call of twice the mean length would take (at most;
+  // the causal mask and D = 128 use fewer, see fa_bwd_varlen)
   const long long twice = 2LL * T / B + 1;
   L.groups = dq_group_count((int)(twice < T ? twice : T), deterministic);
   L.pad = bwd_qblk_rows(D, deterministic);
@@ -385,7 +387,8 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   if (deterministic) {
     // Accumulators, at most: causal tiles of all heads, dealt together, reach a block
     // one after the other by themselves, so that more of them only cost the convert
-    // its reads.  Measured, us of the whole backward, 1 / 2 / 4 accumulators: causal
+    // its reads.  Read off two shapes, one choice for both.  Measured, us of the whole
+    // backward, 1 / 2 / 4 accumulators: causal
     // 16 x 1024 tokens of 16 heads of 128 379 / 399 / 425, of 64 275 / 291 / 309; 5 x
     // 820 tokens, 16 / 4 heads, of 128 139 / 140 / 149, of 64 99 / 95 / 97; without a
     // mask of 128 555 / 545 / 567 and 186 / 181 / 187, of 64 493 / 474 / 439 and 148 /

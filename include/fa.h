@@ -347,7 +347,9 @@ int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, voi
  * A sequence without tokens gets o = 0 and lse = -inf.  Hq / Hkv is at most 128,
  * B * Hq at most 2^30, B * Hq * table slots / 16 below 2^40 and, with weights,
  * B * Hkv * weight_slots / 1024 below 2^30.  |q| and the stored values stay below 2^32:
- * the products are taken on scaled operands, which larger ones may overflow.
+ * the products are taken on scaled operands, which larger ones may overflow.  At the
+ * lower end, query elements under 2^-57, and products of a weight (relative to the row's
+ * largest) and a group's scale under 2^-57, lose bits to fp32's smallest normal number.
  * weights_out (null: none) [B, Hkv, weight_slots] fp32: for every stored token j
  *   weights_out[b][hk][j] = weights_in[b][hk][j] + sum of its softmax weights over
  *   the query heads of hk  (weights_in null: 0; it may be weights_out itself);
