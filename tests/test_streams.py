@@ -176,3 +176,45 @@ def test_calls_in_turn_on_two_streams():
     for run in got:
         for a, b in zip(want, run):
             assert torch.equal(a, b)
+
+
+def test_threads_with_streams_of_their_own():
+    """Four threads, each on a stream of its own, some of them by stream=."""
+    import threading
+
+    q, k, v, do, cu = _packed()
+    cache, table, n, q1 = _cache()
+    o, lse = fa.fwd_varlen(q, k, v, cu, causal=True)
+
+    def calls(stream=None):
+        grads = fa.bwd_varlen(q, k, v, o, do, lse, cu, causal=True, deterministic=True, stream=stream)
+        return (*fa.fwd_varlen(q, k, v, cu, causal=True, stream=stream), *grads,
+                *fa.cache4_attend(q1, cache, table, n, stream=stream),
+                *fa.cache4_read(cache, table, None, n, 1200, D, stream=stream))
+
+    want = calls()
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(i):
+        try:
+            side = torch.cuda.Stream()
+            for _ in range(15):
+                if i % 2:
+                    got = calls(side)
+                else:
+                    with torch.cuda.stream(side):
+                        got = calls()
+                side.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(want, got)):
+                    failed.append((i, "different"))
+        except Exception as e:  # reported by the main thread
+            failed.append((i, repr(e)))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    assert fa.fwd_status() == fa.FA_OK and fa.cache4_status() == fa.FA_OK
