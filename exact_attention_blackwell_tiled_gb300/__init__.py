@@ -33,7 +33,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_status", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bw
            "fa_bwd_noalloc", "fa_fwd_mod", "fa_bwd_mod", "fa_fwd_split_count",
            "fa_fwd_split_workspace_bytes", "fa_fwd_split", "fa_lse_merge", "fa_wait_test",
            "fa_bwd_noalloc_status", "fa_varlen_workspace_bytes", "fa_fwd_varlen",
-           "fa_bwd_varlen", "fa_cache4_page_bytes", "fa_cache4_append", "fa_cache4_read",
+           "fa_bwd_varlen", "fa_varlen_sink_workspace_bytes", "fa_fwd_varlen_sink",
+           "fa_bwd_varlen_sink", "fa_cache4_page_bytes", "fa_cache4_append", "fa_cache4_read",
            "fa_cache4_attend_workspace_bytes", "fa_cache4_attend", "fa_cache4_evict",
            "fa_cache4_status")
 
@@ -113,6 +114,14 @@ def _bind(lib):
     lib.fa_fwd_varlen.restype = i
     lib.fa_bwd_varlen.argtypes = [vp] * 10 + [i, i, i, i, i, psp, psp, psp, i, i, f, vp, sz, i, vp]
     lib.fa_bwd_varlen.restype = i
+    lib.fa_varlen_sink_workspace_bytes.argtypes = [i] * 9
+    lib.fa_varlen_sink_workspace_bytes.restype = sz
+    lib.fa_fwd_varlen_sink.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, psp, psp, psp, i, i,
+                                       i, f, vp, sz, vp]
+    lib.fa_fwd_varlen_sink.restype = i
+    lib.fa_bwd_varlen_sink.argtypes = [vp] * 10 + [i, i, i, i, i, psp, psp, psp, i, i, i, f, vp,
+                                                   sz, i, vp]
+    lib.fa_bwd_varlen_sink.restype = i
     lib.fa_cache4_page_bytes.argtypes = [i, i, i]
     lib.fa_cache4_page_bytes.restype = sz
     lib.fa_cache4_append.argtypes = [vp, i, i, vp, vp, psp, psp, i, i, i, i, vp, vp, vp, i, vp]
@@ -461,75 +470,84 @@ def _var_window(causal, window):
     return int(window[0]), int(window[1])
 
 
-def varlen_workspace_bytes(B, T, Hq, Hkv, D, backward=False, deterministic=False) -> int:
-    return int(lib().fa_varlen_workspace_bytes(B, T, Hq, Hkv, D, int(bool(backward)),
-                                               int(bool(deterministic))))
+def varlen_workspace_bytes(B, T, Hq, Hkv, D, backward=False, deterministic=False, window=None,
+                           sinks: int = 0) -> int:
+    """Workspace bytes of fwd_varlen or bwd_varlen; a backward with ``sinks`` takes more, by
+    its ``window``."""
+    wl = _var_window(False, window)[0]
+    # (a ctypes int would wrap; lengths stay below 2^31)
+    return int(lib().fa_varlen_sink_workspace_bytes(
+        B, T, Hq, Hkv, D, int(bool(backward)), int(bool(deterministic)),
+        max(-1, min(wl, 2 ** 31 - 1)), int(sinks)))
 
 
 def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                causal: bool = False, scale: float | None = None, window=None,
                out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-               workspace: torch.Tensor | None = None, stream=None):
-    """Forward attention over packed sequences (fa_fwd_varlen).
+               workspace: torch.Tensor | None = None, stream=None, sinks: int = 0):
+    """Forward attention over packed sequences (fa_fwd_varlen, fa_fwd_varlen_sink).
 
     q [T,Hq,D], k/v [T,Hkv,D] bf16 CUDA, elements contiguous, tokens and heads at
     any stride that is a multiple of 8 (slices of a fused projection);
     ``cu_seqlens`` int32 [B+1]: sequence b is tokens cu_seqlens[b] ..
-    cu_seqlens[b+1]-1.  ``causal`` / ``window`` as in fwd, inside each sequence.
+    cu_seqlens[b+1]-1.  ``causal`` / ``window`` as in fwd, inside each sequence;
+    the first ``sinks`` tokens (at most 128) stay visible behind the window's left side.
     Returns (o [T,Hq,D] bf16, lse [Hq,T] fp32); tokens of no sequence are not
     written.  fwd_status() reports a cu_seqlens that does not ascend in [0, T].
     """
     wl, wr = _var_window(causal, window)
-    return _compiled().fwd_varlen(q, k, v, cu_seqlens, wl, wr, scale, out, lse, workspace, stream)
+    return _compiled().fwd_varlen(q, k, v, cu_seqlens, wl, wr, scale, out, lse, workspace, stream,
+                                  sinks)
 
 
 def bwd_varlen(q, k, v, o, do, lse, cu_seqlens, causal: bool = False, scale: float | None = None,
                window=None, deterministic: bool = False, workspace: torch.Tensor | None = None,
-               dq=None, dk=None, dv=None, stream=None):
-    """Backward of fwd_varlen (fa_bwd_varlen).  Returns (dq [T,Hq,D], dk, dv
+               dq=None, dk=None, dv=None, stream=None, sinks: int = 0):
+    """Backward of fwd_varlen (fa_bwd_varlen, fa_bwd_varlen_sink).  Returns (dq [T,Hq,D], dk, dv
     [T,Hkv,D]) bf16, contiguous; tokens of no sequence are not written.  o, do
     and lse are contiguous; the other arguments as in fwd_varlen, and as given
     to it."""
     wl, wr = _var_window(causal, window)
     return _compiled().bwd_varlen(q, k, v, o, do, lse, cu_seqlens, wl, wr, scale, deterministic,
-                                  workspace, dq, dk, dv, stream)
+                                  workspace, dq, dk, dv, stream, sinks)
 
 
 class _AttentionVarlen(torch.autograd.Function):
     """fwd_varlen in forward (saving O and LSE), bwd_varlen in backward."""
 
     @staticmethod
-    def forward(ctx, q, k, v, cu_seqlens, causal, scale, window, deterministic):
+    def forward(ctx, q, k, v, cu_seqlens, causal, scale, window, deterministic, sinks):
         # tokens of no sequence: zeros, so that neither O nor a gradient holds
         # uninitialised memory
         o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-        _, lse = fwd_varlen(q, k, v, cu_seqlens, causal=causal, scale=scale, window=window, out=o)
+        _, lse = fwd_varlen(q, k, v, cu_seqlens, causal=causal, scale=scale, window=window, out=o,
+                            sinks=sinks)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
-        ctx.args = (causal, scale, window, deterministic)
+        ctx.args = (causal, scale, window, deterministic, sinks)
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
-        causal, scale, window, deterministic = ctx.args
+        causal, scale, window, deterministic, sinks = ctx.args
         grads = [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
         bwd_varlen(q, k, v, o, do.contiguous(), lse, cu_seqlens, causal=causal, scale=scale,
                    window=window, deterministic=deterministic, dq=grads[0], dk=grads[1],
-                   dv=grads[2])
-        return (*grads, None, None, None, None, None)
+                   dv=grads[2], sinks=sinks)
+        return (*grads, None, None, None, None, None, None)
 
 
 def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                      causal: bool = False, scale: float | None = None, window=None,
-                     deterministic: bool = False) -> torch.Tensor:
+                     deterministic: bool = False, sinks: int = 0) -> torch.Tensor:
     """attention() over packed sequences: q [T,Hq,D], k/v [T,Hkv,D] bf16 CUDA,
-    ``cu_seqlens`` int32 [B+1] (see fwd_varlen).  Tokens of no sequence get zeros
+    ``cu_seqlens`` int32 [B+1], ``sinks`` (see fwd_varlen).  Tokens of no sequence get zeros
     in O and in every gradient.  A training step can be captured into a CUDA graph
     after a step on a side stream; no other graph of the same leaves may be alive
     then.  The gradients cannot be differentiated again (RuntimeError).  Returns O
     [T,Hq,D] bf16."""
-    return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic)
+    return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic, sinks)
 
 
 def cache4_empty(num_pages: int, Hkv: int, D: int, page_size: int = 64, device="cuda"):

@@ -270,10 +270,11 @@ PackedInputs packed_inputs(PyObject* const* a) {
   return {q, k, v, (int)q.size(0), (int)q.size(1), (int)k.size(1), (int)q.size(2), q.device()};
 }
 
-// q, k, v, cu_seqlens, window left, right, scale, out, lse, workspace, stream
+// q, k, v, cu_seqlens, window left, right, scale, out, lse, workspace, stream, sinks
 PyObject* fwd_varlen(PyObject* const* a) {
   const PackedInputs x = packed_inputs(a);
   const Place place(x.device, a[10]);
+  const int sinks = to_int(a[11]);
   int64_t n;
   const int* cu = int32s(a[3], -1, x.device, "cu_seqlens", &n);
   const int B = (int)n - 1, wl = to_int(a[4]), wr = to_int(a[5]);
@@ -282,17 +283,17 @@ PyObject* fwd_varlen(PyObject* const* a) {
   const at::Tensor lse = output(a[8], {x.Hq, x.T}, at::kFloat, place, "lse");
   const size_t need = a[9] == Py_None ? fa_varlen_workspace_bytes(B, x.T, x.Hq, x.Hkv, x.D, 0, 0) : 0;
   const at::Tensor ws = workspace(a[9], need, place);
-  call("fa_fwd_varlen", [&] {
-    return fa_fwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
+  call(sinks ? "fa_fwd_varlen_sink" : "fa_fwd_varlen", [&] {
+    return fa_fwd_varlen_sink(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
                          static_cast<float*>(lse.data_ptr()), cu, B, x.T, x.Hq, x.Hkv, x.D,
-                         x.q.stride(), x.k.stride(), x.v.stride(), wl, wr, scale, ws.data_ptr(),
-                         ws.nbytes(), place.stream);
+                         x.q.stride(), x.k.stride(), x.v.stride(), wl, wr, sinks, scale,
+                         ws.data_ptr(), ws.nbytes(), place.stream);
   });
   return tuple(o, lse);
 }
 
 // q, k, v, o, do, lse, cu_seqlens, window left, right, scale, deterministic,
-// workspace, dq, dk, dv, stream
+// workspace, dq, dk, dv, stream, sinks
 PyObject* bwd_varlen(PyObject* const* a) {
   const PackedInputs x = packed_inputs(a);
   PyObject* const stream = a[15];
@@ -306,17 +307,20 @@ PyObject* bwd_varlen(PyObject* const* a) {
   const int B = (int)n - 1, wl = to_int(a[7]), wr = to_int(a[8]);
   const float scale = to_scale(a[9], x.D);
   const int det = to_bool(a[10]) ? 1 : 0;
-  const size_t need = a[11] == Py_None ? fa_varlen_workspace_bytes(B, x.T, x.Hq, x.Hkv, x.D, 1, det) : 0;
+  const int sinks = to_int(a[16]);
+  const size_t need = a[11] == Py_None ? fa_varlen_sink_workspace_bytes(B, x.T, x.Hq, x.Hkv, x.D, 1, det,
+                                                                        wl, sinks)
+                                       : 0;
   const at::Tensor ws = workspace(a[11], need, place);
   const at::Tensor dq = output(a[12], q_shape, at::kBFloat16, place, "dq");
   const at::Tensor dk = output(a[13], k_shape, at::kBFloat16, place, "dk");
   const at::Tensor dv = output(a[14], k_shape, at::kBFloat16, place, "dv");
-  call("fa_bwd_varlen", [&] {
-    return fa_bwd_varlen(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
+  call(sinks ? "fa_bwd_varlen_sink" : "fa_bwd_varlen", [&] {
+    return fa_bwd_varlen_sink(x.q.t->data_ptr(), x.k.t->data_ptr(), x.v.t->data_ptr(), o.data_ptr(),
                          dO.data_ptr(), static_cast<const float*>(lse.data_ptr()), dq.data_ptr(),
                          dk.data_ptr(), dv.data_ptr(), cu, B, x.T, x.Hq, x.Hkv, x.D, x.q.stride(),
-                         x.k.stride(), x.v.stride(), wl, wr, scale, ws.data_ptr(), ws.nbytes(),
-                         det, place.stream);
+                         x.k.stride(), x.v.stride(), wl, wr, sinks, scale, ws.data_ptr(),
+                         ws.nbytes(), det, place.stream);
   });
   return tuple(dq, dk, dv);
 }
@@ -453,8 +457,8 @@ PyMethodDef method(const char* name) {
           nullptr};
 }
 
-PyMethodDef g_methods[] = {method<fwd_varlen, 11>("fwd_varlen"),
-                           method<bwd_varlen, 16>("bwd_varlen"),
+PyMethodDef g_methods[] = {method<fwd_varlen, 12>("fwd_varlen"),
+                           method<bwd_varlen, 17>("bwd_varlen"),
                            method<cache4_append, 7>("cache4_append"),
                            method<cache4_read, 9>("cache4_read"),
                            method<cache4_attend, 11>("cache4_attend"),

@@ -303,14 +303,44 @@ __device__ __forceinline__ size_t bwd_sem_off(const BwdArgs& a, const BwdUnit& w
   return (size_t)bh * a.n_qblk + (kVar ? w.pad0 / QB : 0) + iq;
 }
 
-// 32 columns (32 c ..) of dK or dV for the unit's q head as an fp32 part, times sc: the
-// lanes of a group of four, which hold rows row0 .. row0 + 3, trade 16-byte pieces.
-__device__ __forceinline__ void bwd_store_part(const BwdArgs& a, const BwdUnit& w, int group,
-                                               bool is_v, int c, int D, const uint32_t (&vk)[32],
-                                               float sc, int row0, int Sk, int lane) {
+// Whether a packed sequence has a query that sees a sink behind its window, and whether
+// tile `tile` of its queries has one.
+__device__ __forceinline__ bool sink_sequence(const BwdArgs& a, int len) {
+  return a.sinks > 0 && len > a.wl + 1;
+}
+__device__ __forceinline__ bool sink_tile(const BwdArgs& a, int len, int tile) {
+  return a.sinks > 0 && min(len, (tile + 1) * kTile) > a.wl + 1;
+}
+// The first such tile.
+__device__ __forceinline__ int sink_first_tile(const BwdArgs& a) { return (a.wl + 1) / kTile; }
+
+// The first of the min(sinks, len) rows in sink_dk and its like (one head) of a run of
+// query tiles that begins at `tile`, in the sequence whose first row is row0.  Rows of
+// different tiles and sequences do not meet: with windows of at least `sinks` keys a
+// sequence of ceil(len / 128) tiles, which is longer than wl + 1, has that many slots of
+// `sinks` rows (row0 / 128 grows by floor(len / 128) at least to the next one,
+// row0 / (wl + 2) by one); with shorter ones its last slot has len rows of its own.
+__device__ __forceinline__ size_t sink_slot(const BwdArgs& a, int row0, int tile) {
+  return a.wl + 2 >= a.sinks
+             ? (size_t)(row0 / kTile + row0 / (a.wl + 2) + tile) * a.sinks
+             : (size_t)(row0 / kTile + tile) * a.sinks + row0;
+}
+
+// The list positions (head, item) of the sinks' kernel, head by head, are dealt in equal
+// contiguous shares.
+__device__ __forceinline__ int sink_shares(const BwdArgs& a, long long total) {
+  return total < a.sink_grid ? (int)total : a.sink_grid;
+}
+__device__ __forceinline__ long long sink_share(long long total, int shares, int k) {
+  return k * total / shares;
+}
+
+// 32 columns (32 c ..) of rows row0 .. row0 + 3, held by the lanes of a group of four, as
+// fp32 at base (row 0's first element), times sc, up to row `rows`: the lanes trade
+// 16-byte pieces.
+__device__ __forceinline__ void store_rows_f32(float* base, int c, int D, const uint32_t (&vk)[32],
+                                               float sc, int row0, int rows, int lane) {
   const int pc = lane & 3;
-  float* base =
-      (is_v ? a.dv_part : a.dk_part) + ((size_t)(w.hk * group + w.gi0) * a.T + w.row0) * D;
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     uint32_t y[16];
@@ -325,10 +355,27 @@ __device__ __forceinline__ void bwd_store_part(const BwdArgs& a, const BwdUnit& 
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m)
-      if (row0 + m < Sk)
+      if (row0 + m < rows)
         *reinterpret_cast<uint4*>(base + (size_t)(row0 + m) * D + c * 32 + (4 * hf + pc) * 4) =
             make_uint4(y[4 * m], y[4 * m + 1], y[4 * m + 2], y[4 * m + 3]);
   }
+}
+
+// Such columns of dK or dV for the unit's q head as an fp32 part.
+__device__ __forceinline__ void bwd_store_part(const BwdArgs& a, const BwdUnit& w, int group,
+                                               bool is_v, int c, int D, const uint32_t (&vk)[32],
+                                               float sc, int row0, int Sk, int lane) {
+  store_rows_f32((is_v ? a.dv_part : a.dk_part) + ((size_t)(w.hk * group + w.gi0) * a.T + w.row0) * D,
+                 c, D, vk, sc, row0, Sk, lane);
+}
+
+// ... of the sinks, for the sum with the sinks' kernel's parts.
+__device__ __forceinline__ void bwd_store_sinks(const BwdArgs& a, const BwdUnit& w, bool is_v, int c,
+                                                int D, const uint32_t (&vk)[32], float sc, int row0,
+                                                int lane) {
+  store_rows_f32((is_v ? a.sink_dv0 : a.sink_dk0) +
+                     ((size_t)w.hk * a.sink_rows + sink_slot(a, w.row0, 0)) * D,
+                 c, D, vk, sc, row0, min(a.sinks, w.kv_len), lane);
 }
 
 // Pair unit u of a cluster of two CTAs: (batch, kv head, kv tiles 2p and 2p+1);

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a) {
             a.delta[v] = acc;
             a.lse2[v] = real ? a.lse[(size_t)h * a.T + it.row0 + i] * 1.4426950408889634f : INFINITY;
           }
-          if (!a.deterministic && real) {
+          if (!a.deterministic && real && !sink_tile(a, it.len, it.tile)) {
             float4* dqa = reinterpret_cast<float4*>(
                 a.dq_acc + ((size_t)h * a.T + it.row0 + i) * D + seg * 8);
             dqa[0] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1015,6 +1015,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
           bwd_store_part(a, w, group, is_v, c, D, vk, sc, row0, Sk, lane);
           continue;
         }
+        if (kVar && kMod && w.j == 0 && wq * 32 < a.sinks && sink_sequence(a, w.kv_len))
+          bwd_store_sinks(a, w, is_v, c, D, vk, sc, row0, lane);
         uint32_t wk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) wk[e] = pack_bf16x2(u2f(vk[2 * e]) * sc, u2f(vk[2 * e + 1]) * sc);
@@ -1102,17 +1104,87 @@ __device__ __forceinline__ uint4 eight_bf16(const float4 (&x)[2], float scale) {
                     pack_bf16x2(x[1].z * scale, x[1].w * scale));
 }
 
+// dK and dV of the sinks, tile 0 of a sequence with queries that see them behind their
+// window: what the main kernel left for the window, by q head or summed, and the parts of
+// the sinks' kernel, one per share that holds tiles of a q head of the group.  Part p goes
+// to thread group p % groups, and the groups' sums are added in order, so that repeated
+// runs give the same bits.
+template <int D>
+__device__ void sum_sinks(const BwdArgs& a, int n_items, int item, const VarItem& it, int hk,
+                          bool is_v, float4 (*s_sum)[2]) {
+  constexpr int kPerRow = D / 8, kSlots = 256 / kPerRow;
+  const int group = a.Hq / a.Hkv, rows = min(a.sinks, it.len);
+  int at_once = 1;  // rows
+  while (at_once < rows && at_once < kSlots) at_once *= 2;
+  const int groups = kSlots / at_once;
+  const int c8 = threadIdx.x % kPerRow, slot = threadIdx.x / kPerRow;
+  const int my_row = slot % at_once, my_group = slot / at_once;
+  const long long total = (long long)n_items * a.Hq;
+  const int shares = sink_shares(a, total);
+  const int first = sink_first_tile(a), last = (it.len - 1) / kTile;
+  // the shares of the group's q heads, one after the other
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int r = r0 + my_row;
+    float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    int part = 0;
+    for (int g = 0; g < group; ++g) {
+      const int h = hk * group + g;
+      const float* parts = (is_v ? a.sink_dv : a.sink_dk) + (size_t)h * a.sink_rows * D;
+      const long long x0 = (long long)h * n_items + item;  // the sequence's tile 0
+      int k = (int)((x0 + first) * shares / total);  // the share that holds it
+      while (sink_share(total, shares, k + 1) <= x0 + first) ++k;
+      while (sink_share(total, shares, k) > x0 + first) --k;
+      int tile = first;
+      do {
+        if (part++ % groups == my_group && r < rows)
+          add_eight(x, reinterpret_cast<const float4*>(parts + (sink_slot(a, it.row0, tile) + r) * D +
+                                                       c8 * 8));
+        tile = (int)(sink_share(total, shares, ++k) - x0);
+      } while (tile <= last);
+    }
+    __syncthreads();
+    s_sum[threadIdx.x][0] = x[0];
+    s_sum[threadIdx.x][1] = x[1];
+    __syncthreads();
+    if (my_group == 0 && r < rows) {
+      for (int g = 1; g < groups; ++g) add_eight(x, s_sum[threadIdx.x + g * at_once * kPerRow]);
+      if (a.dk_part) {
+        const float* base = (is_v ? a.dv_part : a.dk_part) +
+                            ((size_t)hk * group * a.T + it.row0 + r) * D + c8 * 8;
+        for (int g = 0; g < group; ++g)
+          add_eight(x, reinterpret_cast<const float4*>(base + (size_t)g * a.T * D));
+      } else {
+        add_eight(x, reinterpret_cast<const float4*>(
+                         (is_v ? a.sink_dv0 : a.sink_dk0) +
+                         ((size_t)hk * a.sink_rows + sink_slot(a, it.row0, 0) + r) * D + c8 * 8));
+      }
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(is_v ? a.dv : a.dk) +
+                                ((size_t)(it.row0 + r) * a.Hkv + hk) * D + c8 * 8) = eight_bf16(x, 1.f);
+    }
+  }
+}
+
 // The same for a packed batch, over (kv-tile item, q head) pairs of the plan;
 // dQ is [T, Hq, D], and rows of no sequence are left as they are.  A thread has
 // four pieces of a tile in flight: 28.3 us for 16384 rows of 16 heads of 128 (201 MB,
 // 7.1 TB/s, part of it from L2), 32.5 us with one piece.
-template <int D>
+template <int D, bool kSink>
 __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
   grid_dep_wait();
   constexpr int kPerRow = D / 8, kRows = 256 / kPerRow;  // rows of a block's pass
   constexpr int kPieces = 4;
   const int row = threadIdx.x / kPerRow, c8 = threadIdx.x % kPerRow;
   const int n_units = *a.n_items * a.Hq;
+  if constexpr (kSink) {
+    __shared__ float4 s_sum[256][2];
+    const int n = *a.n_items * a.Hkv;
+    for (int u = blockIdx.x; u < 2 * n; u += gridDim.x) {
+      const int x = u < n ? u : u - n, item = x / a.Hkv;
+      const VarItem it = load_item(a.items, item);
+      if (it.tile == 0 && sink_sequence(a, it.len))
+        sum_sinks<D>(a, *a.n_items, item, it, x - item * a.Hkv, u >= n, s_sum);
+    }
+  }
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int item = u / a.Hq, h = u - item * a.Hq;
     const VarItem it = load_item(a.items, item);
@@ -1125,6 +1197,13 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
       float4 x[kPieces][2];
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) x[e][0] = x[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.dq_sink && sink_tile(a, it.len, it.tile)) {
+        const float* sinks = a.dq_sink + ((size_t)h * a.T + it.row0 + i0) * D + c8 * 8;
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e)
+          if (r0 + e * kRows < rows)
+            add_eight(x[e], reinterpret_cast<const float4*>(sinks + (size_t)e * kRows * D));
+      }
       // (deterministic: in fixed order, the groups that some kv tile wrote for this
       // block; otherwise the one accumulator, cleared before the main kernel)
 #pragma unroll 2
@@ -1175,9 +1254,10 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
             add_eight(x[e], reinterpret_cast<const float4*>(base + ((size_t)g * a.T + e * kRows) * D));
       __nv_bfloat16* out =
           reinterpret_cast<__nv_bfloat16*>(is_v ? a.dv : a.dk) + (i0 * a.Hkv + hk) * D + c8 * 8;
+      const int first = it.tile == 0 && sink_sequence(a, it.len) ? a.sinks : 0;  // (sum_sinks)
 #pragma unroll
       for (int e = 0; e < kPieces; ++e)
-        if (r0 + e * kRows < rows)
+        if (r0 + e * kRows < rows && r0 + e * kRows >= first)
           *reinterpret_cast<uint4*>(out + (size_t)e * kRows * a.Hkv * D) = eight_bf16(x[e], 1.f);
     }
   }
@@ -1325,6 +1405,12 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaS
   const int grid = (int)(units < sms ? units : sms);
   if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
+  if (a.sinks) {
+    const long long shares = q_units < sms ? q_units : sms;
+    a.sink_grid = (int)shares;
+    const int rc = launch_bwd_sink(m, a, stream);
+    if (rc != FA_OK) return rc;
+  }
   // units come from the global counter in the plan's order (longest first, each
   // sequence's kv tiles ascending, which is also the order of the deterministic
   // mode's chain)
@@ -1356,9 +1442,10 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaS
     return FA_ERR_CUDA;
   }
   record_timing(true, stream);
-  if (launch_pdl(bwd_dq_convert_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
+  const auto convert = a.sinks ? bwd_dq_convert_var<D, true> : bwd_dq_convert_var<D, false>;
+  if (launch_pdl(convert, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
-  note_launches(3);
+  note_launches(a.sinks ? 4 : 3);
   return FA_OK;
 }
 

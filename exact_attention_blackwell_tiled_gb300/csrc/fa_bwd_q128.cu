@@ -756,6 +756,8 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           bwd_store_part(a, w, group, is_v, c, D, vk, sc, row0, Sk, lane);
           continue;
         }
+        if (kVar && kMod && w.j == 0 && wq * 32 < a.sinks && sink_sequence(a, w.kv_len))
+          bwd_store_sinks(a, w, is_v, c, D, vk, sc, row0, lane);
         uint32_t wk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) wk[e] = pack_bf16x2(u2f(vk[2 * e]) * sc, u2f(vk[2 * e + 1]) * sc);

@@ -78,7 +78,8 @@ struct FwdLayout {
 };
 
 // kMod: 0 plain (no mask or the causal one), 1 a sliding window, 2 a window
-// and the relative-position bias (a.alibi) added to every score.  kSplit: a
+// and the relative-position bias (a.alibi) added to every score, 3 (packed) a window
+// with sinks: kv tile 0 first, then the window's tiles, what lies between left out.  kSplit: a
 // unit covers one split of the kv tiles and writes fp32 parts for the merge.
 // kVar: a packed batch.  Its tensor maps go over the rows of all sequences.  Rows of
 // Q and K past the sequence's last one (another sequence's, or uninitialised) only
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
   const int n_units = kVar ? *a.n_items * a.Hq : a.n_units;
-  constexpr bool kWin = kMod >= 1, kBias = kMod == 2;
+  constexpr bool kWin = kMod >= 1, kBias = kMod == 2, kSink = kMod == 3;
+  static_assert(!kSink || kVar, "sinks: packed calls");
   // packed calls keep every exponential on MUFU: the cubic's 7.5e-5 would be
   // the largest error of their LSE by two orders of magnitude
   constexpr int kPoly = kVar ? 0 : L::kPolyPairs;
@@ -176,8 +178,15 @@ __global__ void __launch_bounds__(320, 1)
         const int pair = w.pair;
         const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
-        pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), pair, w.split, lo, hi,
-                             jlo, nmax);
+        SinkSpan span;
+        if constexpr (kSink) {
+          span = sink_kv_span(w.Sq, wl, wr, pair);
+          jlo = 0;
+          nmax = span.n;
+        } else {
+          pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), pair, w.split, lo, hi,
+                               jlo, nmax);
+        }
         if (nmax == 0) continue;
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
@@ -196,7 +205,8 @@ __global__ void __launch_bounds__(320, 1)
                         bar(L::kBarQFull + qs), cb * 64, row, w.bh);
         }
         ++q_it;
-        for (int j = jlo; j < jlo + nmax; ++j) {
+        for (int p = jlo; p < jlo + nmax; ++p) {
+          const int j = kSink ? span.tile(p) : p;
           const int row = w.row0 + j * kTile;
           if (!load_kv(&tm_k, bhk, row, kTile) || !load_kv(&tm_v, bhk, row, w.Sq - j * kTile)) {
             ok = false;
@@ -224,14 +234,28 @@ __global__ void __launch_bounds__(320, 1)
         const FwdUnit w = fwd_unit<kVar>(a, u);
         // kv tile j sits at position p = j - jlo of the pair's range; tile t
         // computes S for positions [plo[t], phi[t]) and O one position behind
+        // (sinks: position 0 and the window's, SinkSpan)
         int plo[2], phi[2], jlo, nmax;
-        pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), w.pair, w.split, plo,
-                             phi, jlo, nmax);
+        SinkSpan span;
+        if constexpr (kSink) {
+          span = sink_kv_span(w.Sq, wl, wr, w.pair);
+          nmax = span.n;
+          for (int t = 0; t < 2; ++t) {
+            plo[t] = 0;  // the first position
+            phi[t] = span.phi[t];
+          }
+        } else {
+          pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), w.pair, w.split, plo,
+                               phi, jlo, nmax);
+        }
         if (nmax == 0) continue;
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2 && !kSink; ++t) {
           plo[t] -= jlo;
           phi[t] -= jlo;
         }
+        auto active = [&](int t, int p) {
+          return kSink ? span.active(t, p) : p >= plo[t] && p < phi[t];
+        };
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQFull + qs), (q_it / L::kQStages) & 1, abort_flag)) {
           ok = false;
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(320, 1)
           const uint32_t k_base = sbase + L::kOffKV + k_st * L::kTileBytes;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (j >= plo[t] + 1 && j <= phi[t]) {
+            if (kSink ? j >= 1 && active(t, j - 1) : j >= plo[t] + 1 && j <= phi[t]) {
               // GEMM 2: O_t += P_t(j-1) V_{j-1}
               if (!mbar_wait(bar(L::kBarPFull + t), p_seen[t] & 1, abort_flag)) {
                 ok = false;
@@ -281,7 +305,7 @@ __global__ void __launch_bounds__(320, 1)
                           (j > plo[t] + 1 || kk > 0) ? 1u : 0u);
               if (j == phi[t]) umma_commit(bar(L::kBarOFinal + t));
             }
-            if (j >= plo[t] && j < phi[t]) {
+            if (active(t, j)) {
               // GEMM 1: S_t = Q_t K_j^T
               const uint32_t q_lo = sdesc_lo(q_base + t * L::kTileBytes, 16);
               const uint32_t k_lo = sdesc_lo(k_base, 16);
@@ -327,7 +351,14 @@ __global__ void __launch_bounds__(320, 1)
       const int qt = 2 * w.pair + t;
       const int kv_len = unit_kv_len<kWin, kVar>(a, w);
       int jlo, jhi;
-      split_kv_range<kSplit>(a, Sq, wl, wr, kv_len, qt, split, jlo, jhi);
+      SinkSpan span;
+      if constexpr (kSink) {
+        span = sink_kv_span(Sq, wl, wr, w.pair);
+        jlo = 0;  // positions
+        jhi = span.phi[t];
+      } else {
+        split_kv_range<kSplit>(a, Sq, wl, wr, kv_len, qt, split, jlo, jhi);
+      }
       const int q_row = qt * kTile + r;
       const size_t part_row = ((size_t)split * a.B * a.Hq + bh) * Sq + q_row;
       // O rows of the unit: element offset of row 0 and from row to row
@@ -339,7 +370,7 @@ __global__ void __launch_bounds__(320, 1)
         // no key (of this split) reaches the tile: an empty part, or with a
         // window or padding the whole tile sees no key: O = 0, LSE = -inf
         if (kSplit && q_row < Sq) a.lse_part[part_row] = -INFINITY;
-        if (!kSplit && kWin && q_row < Sq) {
+        if (!kSplit && kWin && !kSink && q_row < Sq) {
           uint4* orow = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o) + o_off +
                                                  q_row * o_row);
 #pragma unroll
@@ -351,14 +382,18 @@ __global__ void __launch_bounds__(320, 1)
       // keys [lo_row, lim) are visible to this row
       const int lim = wr >= 0 ? min(kv_len, q_row + wr + 1) : kv_len;
       const int lo_row = wl >= 0 ? max(0, q_row - wl) : 0;
-      auto hidden = [&](int key) { return key >= lim || (kWin && key < lo_row); };
+      const int sinks = kSink ? a.sinks : 0;
+      auto hidden = [&](int key) {
+        return key >= lim || (kWin && key < lo_row && !(kSink && key < sinks));
+      };
       // relative-position bias in log2 units: slope * log2(e) per key offset,
       // and the same per unit of raw score (slope2 / c) for the max pass
       const float slope2 = kBias ? a.alibi[bh % a.Hq] * 1.4426950408889634f : 0.f;
       const float kslope = kBias ? slope2 / a.scale_log2 : 0.f;
       const bool kslope_ok = kBias && a.scale_log2 > 0.f && fabsf(kslope) < 1e30f;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = jlo; j < jhi; ++j) {
+      for (int p = jlo; p < jhi; p = kSink ? max(p + 1, span.plo[t]) : p + 1) {
+        const int j = kSink ? span.tile(p) : p;
         if (!warp_wait(bar(L::kBarSFull + t), g & 1, abort_flag)) { ok = false; break; }
         ++g;
         tc_fence_after();
@@ -372,7 +407,7 @@ __global__ void __launch_bounds__(320, 1)
         // Conditional rescale: keep a stale running max unless the new max
         // exceeds it by more than 8 (P then stays <= 2^8).
         auto update_max = [&](float tmax) {
-          if (j == jlo) {
+          if (p == jlo) {
             m_run = tmax;
           } else if (tmax > m_run + 8.0f) {
             alpha = ex2_mufu(m_run - tmax);
@@ -737,7 +772,8 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
     const void* kernels[] = {(const void*)fwd_kernel<D, 0, false, true>,
-                             (const void*)fwd_kernel<D, 1, false, true>};
+                             (const void*)fwd_kernel<D, 1, false, true>,
+                             (const void*)fwd_kernel<D, 3, false, true>};
     for (const void* k : kernels)
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAllocBytes) !=
           cudaSuccess)
@@ -750,7 +786,8 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
   const long long units = (long long)max_items * a.Hq;
   const int grid = (int)(units < info.sm_count ? units : info.sm_count);
   const bool plain = a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal));
-  const auto kernel = plain ? fwd_kernel<D, 0, false, true> : fwd_kernel<D, 1, false, true>;
+  const auto kernel = plain ? fwd_kernel<D, 0, false, true>
+                     : a.sinks ? fwd_kernel<D, 3, false, true> : fwd_kernel<D, 1, false, true>;
   record_timing(false, stream);
   // D = 64 without a window: the ring of score buffers, as in the dense call
   if (fwd_ring64_eligible(a, D, plain ? 0 : 1)) {

@@ -120,6 +120,9 @@ struct FwdArgs {
   const VarItem* items;
   const int* n_items;
   int T;
+  // packed calls with a window: the keys j < sinks of a sequence stay visible behind
+  // it (at most kTile, so tile 0 holds them)
+  int sinks;
 };
 
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -209,6 +212,19 @@ struct BwdArgs {
   // order; null otherwise (a unit then loops over the group)
   float* dk_part;
   float* dv_part;
+  // packed calls with a window: the keys j < sinks of a sequence stay visible behind it
+  // (at most kTile).  Pairs of a query and a sink behind its window are a kernel of
+  // their own (fa_bwd_sink.cu), which leaves parts of dK and dV [Hq, sink_rows, D] (one
+  // per run of query tiles, at sink_slot) and its share of dQ, in the accumulator or, in
+  // the deterministic mode, in dq_sink [Hq, T, D].  The main kernel leaves the sinks'
+  // dK and dV over the window in fp32 too, [Hkv, sink_rows, D], unless dk_part holds
+  // them; the last kernel sums.
+  int sinks;
+  long long sink_rows;
+  int sink_grid;           // blocks of that kernel
+  float *sink_dk, *sink_dv;
+  float *sink_dk0, *sink_dv0;
+  float* dq_sink;
   int qblk_rows;           // query rows per block of the main kernel (64 or 128):
                            // semaphore i of a head counts the writers of block i
 };
@@ -253,6 +269,16 @@ struct BwdVarMaps {
   Tails<true, 4> tails;  // of q, k, v and dO
 };
 int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, int max_items, cudaStream_t stream);
+
+// The pairs of queries and sinks behind the window (a.sinks > 0), before the main kernel.
+int launch_bwd_sink(const BwdVarMaps& m, const BwdArgs& a, cudaStream_t stream);
+
+// Rows of sink_dk and its like, per head, for T packed rows (sink_slot's largest and
+// the rows behind it).
+inline long long sink_row_count(int T, int wl, int sinks) {
+  return wl + 2LL >= sinks ? (T / kTile + T / (wl + 2LL) + 2) * sinks
+                           : (T / kTile + 2LL) * sinks + T;
+}
 
 // The CTA-pair main kernel (D = 128, atomic dQ, no score modification), and
 // the process-wide kernel choice fa_set_bwd_kernel sets.

@@ -155,6 +155,8 @@ struct VarLayout {
   int pad;  // rows of the backward's query blocks
   long long t_pad;
   bool split;  // q heads are units of their own (BwdArgs::dk_part)
+  long long sink_rows;  // BwdArgs::sink_rows
+  size_t off_sink[4], off_dq_sink;
   size_t off_items, off_acc, off_delta, off_lse2, off_sem, off_dk, off_dv, total;
 };
 
@@ -174,7 +176,11 @@ int check_var(int B, int T, int Hq, int Hkv, int D) {
   return FA_OK;
 }
 
-VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool deterministic) {
+// The sinks of a call that count: none where no window hides a key from any query.
+int window_sinks(int sinks, int wl, int T) { return wl >= 0 && wl < T - 1 ? sinks : 0; }
+
+VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool deterministic,
+                     int wl, int sinks) {
   VarLayout L{};
   const int rows = backward ? 128 : 256;
   L.max_items = T / rows + B;
@@ -202,6 +208,16 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
     L.off_dk = L.total;
     L.off_dv = up256(L.off_dk + (size_t)Hq * T * D * sizeof(float));
     L.total = up256(L.off_dv + (size_t)Hq * T * D * sizeof(float));
+  }
+  if (sinks > 0) {
+    L.sink_rows = sink_row_count(T, wl, sinks);
+    for (int i = 0; i < 4; ++i) {  // dK, dV of the sinks' kernel; of the main kernel
+      L.off_sink[i] = L.total;
+      const int heads = i < 2 ? Hq : (L.split ? 0 : Hkv);
+      L.total = up256(L.total + (size_t)heads * L.sink_rows * D * sizeof(float));
+    }
+    L.off_dq_sink = L.total;
+    if (deterministic) L.total = up256(L.total + (size_t)Hq * T * D * sizeof(float));
   }
   return L;
 }
@@ -235,6 +251,11 @@ bool tail_maps(const VarTensor& t, int T, int D, TailMaps* maps) {
   return true;
 }
 
+int check_sinks(int sinks) {
+  if (sinks < 0) return FA_ERR_INVALID_ARG;
+  return sinks > kTile ? FA_ERR_UNSUPPORTED : FA_OK;  // the kernels keep them in one tile
+}
+
 int check_strides(const VarTensor* t, int n, int D) {
   for (int i = 0; i < n; ++i) {
     long long row, head;
@@ -254,7 +275,15 @@ extern "C" {
 size_t fa_varlen_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int backward,
                                  int deterministic) {
   if (check_var(B, T, Hq, Hkv, D) != FA_OK) return 0;
-  return var_layout(B, T, Hq, Hkv, D, backward != 0, deterministic != 0).total;
+  return var_layout(B, T, Hq, Hkv, D, backward != 0, deterministic != 0, -1, 0).total;
+}
+
+size_t fa_varlen_sink_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int backward,
+                                      int deterministic, int window_left, int sinks) {
+  if (check_var(B, T, Hq, Hkv, D) != FA_OK || sinks < 0 || sinks > kTile) return 0;
+  const int wl = window_side(window_left, T);
+  return var_layout(B, T, Hq, Hkv, D, backward != 0, deterministic != 0, wl,
+                    window_sinks(sinks, wl, T)).total;
 }
 
 int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -262,9 +291,21 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
                   const fa_packed_stride* q_stride, const fa_packed_stride* k_stride,
                   const fa_packed_stride* v_stride, int window_left, int window_right, float scale,
                   void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  return fa_fwd_varlen_sink(q, k, v, o, lse, cu_seqlens, B, T, Hq, Hkv, D, q_stride, k_stride,
+                            v_stride, window_left, window_right, 0, scale, workspace,
+                            workspace_bytes, stream);
+}
+
+int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, float* lse,
+                       const int* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
+                       const fa_packed_stride* q_stride, const fa_packed_stride* k_stride,
+                       const fa_packed_stride* v_stride, int window_left, int window_right,
+                       int sinks, float scale, void* workspace, size_t workspace_bytes,
+                       fa_stream_t stream) {
   reset_launches();
   int rc = check_var(B, T, Hq, Hkv, D);
   if (rc) return rc;
+  if ((rc = check_sinks(sinks))) return rc;
   if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   const VarTensor t[3] = {{q, q_stride, Hq, kTile}, {k, k_stride, Hkv, kTile}, {v, v_stride, Hkv, kTile}};
   if ((rc = check_strides(t, 3, D))) return rc;
@@ -273,7 +314,7 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
       misaligned(lse, 4) || misaligned(cu_seqlens, 4))
     return FA_ERR_MISALIGNED;
-  const VarLayout L = var_layout(B, T, Hq, Hkv, D, false, false);
+  const VarLayout L = var_layout(B, T, Hq, Hkv, D, false, false, -1, 0);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -287,6 +328,7 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
   a.wl = window_side(window_left, T);
   a.wr = window_side(window_right, T);
   a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
+  a.sinks = window_sinks(sinks, a.wl, T);
   p.cu = cu_seqlens;
   p.B = B;
   p.T = T;
@@ -321,9 +363,21 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
                   const fa_packed_stride* k_stride, const fa_packed_stride* v_stride,
                   int window_left, int window_right, float scale, void* workspace,
                   size_t workspace_bytes, int deterministic, fa_stream_t stream) {
+  return fa_bwd_varlen_sink(q, k, v, o, dO, lse, dq, dk, dv, cu_seqlens, B, T, Hq, Hkv, D,
+                            q_stride, k_stride, v_stride, window_left, window_right, 0, scale,
+                            workspace, workspace_bytes, deterministic, stream);
+}
+
+int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                       const float* lse, void* dq, void* dk, void* dv, const int* cu_seqlens, int B,
+                       int T, int Hq, int Hkv, int D, const fa_packed_stride* q_stride,
+                       const fa_packed_stride* k_stride, const fa_packed_stride* v_stride,
+                       int window_left, int window_right, int sinks, float scale, void* workspace,
+                       size_t workspace_bytes, int deterministic, fa_stream_t stream) {
   reset_launches();
   int rc = check_var(B, T, Hq, Hkv, D);
   if (rc) return rc;
+  if ((rc = check_sinks(sinks))) return rc;
   if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   const int qrows = bwd_qblk_rows(D, deterministic);
   const VarTensor t[4] = {{q, q_stride, Hq, qrows}, {k, k_stride, Hkv, kTile},
@@ -336,7 +390,8 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
       misaligned(dO, 16) || misaligned(dq, 16) || misaligned(dk, 16) || misaligned(dv, 16) ||
       misaligned(lse, 4) || misaligned(cu_seqlens, 4))
     return FA_ERR_MISALIGNED;
-  const VarLayout L = var_layout(B, T, Hq, Hkv, D, true, deterministic != 0);
+  const int wl = window_side(window_left, T), seen = window_sinks(sinks, wl, T);
+  const VarLayout L = var_layout(B, T, Hq, Hkv, D, true, deterministic != 0, wl, seen);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -346,7 +401,7 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
     if (!full_map(t[i], T, D, maps[i]) || !tail_maps(t[i], T, D, &m.tails.of[i])) return FA_ERR_CUDA;
   PlanArgs p{};
   BwdArgs a{};
-  a.wl = window_side(window_left, T);
+  a.wl = wl;
   a.wr = window_side(window_right, T);
   a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
   p.cu = cu_seqlens;
@@ -374,6 +429,15 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
   if (L.split) {
     a.dk_part = reinterpret_cast<float*>(ws + L.off_dk);
     a.dv_part = reinterpret_cast<float*>(ws + L.off_dv);
+  }
+  if (seen > 0) {
+    a.sinks = seen;
+    a.sink_rows = L.sink_rows;
+    a.sink_dk = reinterpret_cast<float*>(ws + L.off_sink[0]);
+    a.sink_dv = reinterpret_cast<float*>(ws + L.off_sink[1]);
+    a.sink_dk0 = reinterpret_cast<float*>(ws + L.off_sink[2]);
+    a.sink_dv0 = reinterpret_cast<float*>(ws + L.off_sink[3]);
+    if (deterministic) a.dq_sink = reinterpret_cast<float*>(ws + L.off_dq_sink);
   }
   a.status = p.status;
   a.unit_counter = p.counter;

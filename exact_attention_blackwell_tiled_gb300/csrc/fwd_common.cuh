@@ -148,6 +148,36 @@ __device__ __forceinline__ void pair_kv_span(const FwdArgs& a, int Sq, int wl, i
   if (e1) lo[1] = hi[1] = jlo;
 }
 
+// The same with sinks: kv tile 0 comes first for every query tile with rows.  Position
+// p of the unit is tile 0 where p == 0, else jlo + p - first, so that the tiles between
+// the sinks and the window are left out; plo[t] .. phi[t] are the positions of tile t's
+// window.  Returns false where the unit has no rows (never: the plan lists none).
+struct SinkSpan {
+  int plo[2], phi[2];  // phi 0: no rows
+  int jlo, first, n;
+  __device__ __forceinline__ int tile(int p) const { return p == 0 ? 0 : jlo + p - first; }
+  __device__ __forceinline__ bool active(int t, int p) const {
+    return p == 0 ? phi[t] > 0 : p >= plo[t] && p < phi[t];
+  }
+};
+__device__ __forceinline__ SinkSpan sink_kv_span(int Sq, int wl, int wr, int pair) {
+  SinkSpan s;
+  int lo[2], hi[2];
+  tile_kv_range(Sq, wl, wr, Sq, 2 * pair, lo[0], hi[0]);
+  tile_kv_range(Sq, wl, wr, Sq, 2 * pair + 1, lo[1], hi[1]);
+  s.jlo = lo[0];
+  s.first = s.jlo > 0 ? 1 : 0;
+  s.n = s.first;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const bool rows = hi[t] > lo[t];
+    s.plo[t] = rows ? lo[t] - s.jlo + s.first : 0;
+    s.phi[t] = rows ? hi[t] - s.jlo + s.first : 0;
+    s.n = max(s.n, s.phi[t]);
+  }
+  return s;
+}
+
 // Bounded wait done by every lane of a warp; the outcome is made warp-uniform so
 // the warp-collective tcgen05.ld/st that follow are never reached by part of it.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {

@@ -296,6 +296,31 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
                   size_t workspace_bytes, int deterministic, fa_stream_t stream);
 
 /*
+ * The packed calls under a window that the first keys of a sequence stay visible behind
+ * (sinks): key j is seen by query i of its sequence iff
+ *   j <= i + window_right (any j where it is negative) and
+ *   (window_left < 0 or j >= i - window_left or j < sinks).
+ * 0 <= sinks <= 128 (more: FA_ERR_UNSUPPORTED); 0 is fa_fwd_varlen / fa_bwd_varlen.  Same
+ * tensors, sizes, pointer rules, roundings and errors as those calls.  The forward's
+ * workspace is fa_varlen_workspace_bytes(..., 0, 0) bytes, the backward's
+ * fa_varlen_sink_workspace_bytes(..., 1, deterministic, window_left, sinks).
+ */
+size_t fa_varlen_sink_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int backward,
+                                      int deterministic, int window_left, int sinks);
+int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, float* lse,
+                       const int* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
+                       const fa_packed_stride* q_stride, const fa_packed_stride* k_stride,
+                       const fa_packed_stride* v_stride, int window_left, int window_right,
+                       int sinks, float scale, void* workspace, size_t workspace_bytes,
+                       fa_stream_t stream);
+int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                       const float* lse, void* dq, void* dk, void* dv, const int* cu_seqlens, int B,
+                       int T, int Hq, int Hkv, int D, const fa_packed_stride* q_stride,
+                       const fa_packed_stride* k_stride, const fa_packed_stride* v_stride,
+                       int window_left, int window_right, int sinks, float scale, void* workspace,
+                       size_t workspace_bytes, int deterministic, fa_stream_t stream);
+
+/*
  * A paged key/value cache held in 4 bits, the attention of single query tokens to
  * it, and its thinning out by accumulated attention weight (the pages have no
  * counterpart; the method they describe serves the prompt, these calls what

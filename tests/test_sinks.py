@@ -1,0 +1,288 @@
+"""Packed attention under a window with sinks (fa_fwd_varlen_sink, fa_bwd_varlen_sink)
+against the plain 64-bit form."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import __graft_entry__
+import exact_attention_blackwell_tiled_gb300 as fa
+from packed_reference import assert_within
+from sink_reference import packed_sinks, sink_mask
+
+P256 = ctypes.c_void_p(256 * 1024)
+P16 = ctypes.c_void_p(256 * 1024 + 16)
+
+
+# ------------------------------------------------------------------ without a GPU
+
+@pytest.fixture(scope="module")
+def L():
+    __graft_entry__.build()
+    return fa.lib()
+
+
+def test_refusals(L):
+    def fwd(sinks, T=8, ws=P256, need=1 << 20):
+        return L.fa_fwd_varlen_sink(P16, P16, P16, P16, P16, P16, 2, T, 2, 2, 64, None, None, None,
+                                    4, 0, sinks, 0.1, ws, need, None)
+
+    def bwd(sinks, T=8, need=None):
+        need = L.fa_varlen_sink_workspace_bytes(2, 8, 2, 2, 64, 1, 0, 4, 4) if need is None else need
+        return L.fa_bwd_varlen_sink(P16, P16, P16, P16, P16, P16, P16, P16, P16, P16, 2, T, 2, 2, 64,
+                                    None, None, None, 4, 0, sinks, 0.1, P256, need, 0, None)
+    assert fwd(-1) == 1 and bwd(-1) == 1
+    assert fwd(129) == 2 and bwd(129) == 2
+    assert fwd(4, T=0) == 0 and bwd(4, T=0) == 0
+    assert fwd(4, ws=None) == 4
+    plain = L.fa_varlen_workspace_bytes(2, 8, 2, 2, 64, 1, 0)
+    assert bwd(4, need=plain) == 4
+    assert L.fa_varlen_sink_workspace_bytes(2, 8, 2, 2, 64, 1, 0, 4, 129) == 0
+    assert L.fa_varlen_sink_workspace_bytes(2, 8, 2, 2, 64, 1, 0, 4, -1) == 0
+    # without sinks, or with a window that hides nothing, it is the plain call's
+    for wl, sinks in ((4, 0), (-1, 4), (7, 4), (1 << 30, 4)):
+        assert L.fa_varlen_sink_workspace_bytes(2, 8, 2, 2, 64, 1, 1, wl, sinks) == \
+            L.fa_varlen_workspace_bytes(2, 8, 2, 2, 64, 1, 1)
+
+
+def test_workspace_grows_with_what_it_holds(L):
+    """Parts take rows for runs of queries, not rows per token: 16384 tokens of 16 heads of
+    128 under 1024 with 4 sinks cost far below one accumulator more."""
+    plain = L.fa_varlen_workspace_bytes(4, 16384, 16, 16, 128, 1, 0)
+    more = L.fa_varlen_sink_workspace_bytes(4, 16384, 16, 16, 128, 1, 0, 1023, 4)
+    assert 0 < more - plain < 16384 * 16 * 128 * 4 // 4
+    # the narrowest window with the most sinks stays within a few of them
+    worst = L.fa_varlen_sink_workspace_bytes(4, 16384, 16, 16, 128, 1, 0, 0, 128)
+    assert worst - plain < 10 * 16384 * 16 * 128 * 4
+
+
+def _slot(wl, sinks, row0, tile):
+    return ((row0 // 128 + row0 // (wl + 2) + tile) * sinks if wl + 2 >= sinks
+            else (row0 // 128 + tile) * sinks + row0)
+
+
+@pytest.mark.parametrize("wl,sinks", [(0, 1), (0, 128), (1, 4), (2, 4), (3, 4), (63, 64), (61, 64),
+                                      (100, 4), (127, 128), (126, 128), (500, 16)])
+def test_parts_do_not_meet(L, wl, sinks):
+    """The rows of the sinks' parts, per head, by their closed form: no two tiles of long
+    sequences share one, and all lie inside the workspace's count."""
+    import random
+    rng = random.Random(wl * 1000 + sinks)
+    for _ in range(60):
+        used, row0 = set(), rng.randrange(0, 5)
+        for _ in range(rng.randrange(1, 60)):
+            n = rng.choice([0, 1, 2, wl + 1, wl + 2, wl + 3, 127, 128, 129, 300, 1000])
+            if n > wl + 1:
+                for tile in range(-(-n // 128)):
+                    first = _slot(wl, sinks, row0, tile)
+                    rows = range(first, first + min(sinks, n))
+                    assert used.isdisjoint(rows)
+                    used.update(rows)
+            row0 += n
+        T = row0
+        bound = ((T // 128 + T // (wl + 2) + 2) * sinks if wl + 2 >= sinks
+                 else (T // 128 + 2) * sinks + T)
+        assert not used or max(used) < bound
+
+
+def test_reference_gradients_by_differences():
+    gen = torch.Generator().manual_seed(3)
+    n, D, window, sinks = 7, 4, (2, 0), 2
+    x = [torch.randn(n, 1, D, generator=gen, dtype=torch.float64) for _ in range(4)]
+    q, k, v, do = x
+    r = packed_sinks(q, k, v, [(0, n)], window, sinks, scale=0.7, do=do)
+    mask = sink_mask(n, window, sinks)
+    assert mask[6].tolist() == [True, True, False, False, True, True, True]
+
+    def loss(q, k, v):
+        s = (q[:, 0] @ k[:, 0].T * 0.7).masked_fill(~mask, -math.inf)
+        return float(((torch.softmax(s, 1) @ v[:, 0]) * do[:, 0]).sum())
+    for name, t in (("dq", 0), ("dk", 1), ("dv", 2)):
+        for at in ((0, 0, 1), (3, 0, 0), (6, 0, 3)):
+            args = [y.clone() for y in (q, k, v)]
+            eps = 1e-6
+            args[t][at] += eps
+            up = loss(*args)
+            args[t][at] -= 2 * eps
+            diff = (up - loss(*args)) / (2 * eps)
+            assert abs(diff - float(r[name][at])) < 1e-7
+
+
+# ------------------------------------------------------------------ on the GPU
+
+def _inputs(T, Hq, Hkv, D, seed, spread=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return [(torch.randn(T, h, D, generator=gen) * spread).to(torch.bfloat16)
+            for h in (Hq, Hkv, Hkv, Hq)]
+
+
+def _bounds(lens, first=0):
+    out, at = [], first
+    for n in lens:
+        out.append((at, at + n))
+        at += n
+    return out
+
+
+def _cu(bounds):
+    return torch.tensor([bounds[0][0]] + [hi for _, hi in bounds], dtype=torch.int32, device="cuda")
+
+
+CASES = [
+    # lengths, Hq, Hkv, D, window, sinks
+    ([1, 0, 2, 130, 5], 2, 2, 64, (0, 0), 1),
+    ([1, 0, 2, 130, 5], 2, 1, 128, (1, 0), 4),
+    ([300], 2, 2, 128, (63, 0), 4),
+    ([700, 129, 128, 127], 2, 2, 64, (100, 0), 16),
+    ([513, 900], 4, 2, 128, (200, 0), 7),
+    ([513, 900], 4, 2, 64, (200, 0), 33),
+    ([640, 257], 2, 1, 128, (130, 3), 128),       # the widest sinks, a right side
+    ([640, 257], 2, 1, 64, (130, -1), 65),        # no right side
+    ([400, 90], 3, 3, 128, (10, 0), 64),          # more sinks than the window holds
+    ([400, 90], 3, 3, 64, (2, 0), 100),
+    ([1200], 8, 1, 128, (127, 0), 4),
+    ([1200, 1200], 1, 1, 64, (255, 0), 17),
+    ([40] * 30 + [500], 4, 4, 64, (37, 0), 3),
+    ([40] * 30 + [500], 4, 4, 128, (38, 0), 3),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Hq,Hkv,D,window,sinks", CASES)
+def test_forward_and_backward(lens, Hq, Hkv, D, window, sinks):
+    __graft_entry__.build()
+    bounds = _bounds(lens)
+    T = bounds[-1][1]
+    q, k, v, do = _inputs(T, Hq, Hkv, D, 17 + T)
+    r = packed_sinks(q, k, v, bounds, window, sinks, do=do)
+    cu = _cu(bounds)
+    d = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.fwd_varlen(*d[:3], cu, window=window, sinks=sinks)
+    assert fa.fwd_status() == fa.FA_OK
+    assert_within(o, r["o"], r["o_tol"], "o")
+    assert_within(lse, r["lse"], r["lse_tol"], "lse")
+    for det in (False, True):
+        ws = torch.full((fa.varlen_workspace_bytes(len(lens), T, Hq, Hkv, D, True, det, window=window,
+                                                   sinks=sinks),), 0xff, dtype=torch.uint8, device="cuda")
+        g = fa.bwd_varlen(*d[:3], o, d[3], lse, cu, window=window, sinks=sinks, deterministic=det,
+                          workspace=ws)
+        assert fa.bwd_status(ws) == fa.FA_OK
+        for name, x in zip(("dq", "dk", "dv"), g):
+            assert_within(x, r[name], r[name + "_tol"], f"{name}, deterministic={det}")
+        if det:
+            for _ in range(3):
+                again = fa.bwd_varlen(*d[:3], o, d[3], lse, cu, window=window, sinks=sinks,
+                                      deterministic=True)
+                assert all(torch.equal(x, y) for x, y in zip(g, again))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("det", [False, True])
+def test_large_scores_and_strides(D, det):
+    """Slices of a fused projection, scores far apart, a negative scale too; tokens in front
+    of the first and behind the last sequence stay as they were and may be NaN."""
+    __graft_entry__.build()
+    Hq, Hkv, window, sinks = 4, 2, (70, 0), 5
+    bounds = _bounds([333, 0, 150], first=9)
+    T = bounds[-1][1] + 11
+    gen = torch.Generator().manual_seed(5)
+    fused = (torch.randn(T, Hq + 2 * Hkv, D, generator=gen) * 3).to(torch.bfloat16)
+    do = torch.randn(T, Hq, D, generator=gen).to(torch.bfloat16)
+    for rows in (slice(0, 9), slice(T - 11, T)):
+        fused[rows] = math.nan
+    dev = fused.cuda()
+    parts = dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:]
+    cu = _cu(bounds)
+    for scale in (None, -0.05):
+        r = packed_sinks(*(x.cpu() for x in parts), bounds, window, sinks, scale=scale, do=do)
+        o = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((Hq, T), 7.0, device="cuda")
+        fa.fwd_varlen(*parts, cu, window=window, sinks=sinks, scale=scale, out=o, lse=lse)
+        assert_within(o, r["o"], r["o_tol"], "o")
+        assert_within(lse, r["lse"], r["lse_tol"], "lse")
+        grads = [torch.full((T, h, D), 7.0, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv)]
+        fa.bwd_varlen(*parts, o, do.cuda(), lse, cu, window=window, sinks=sinks, scale=scale,
+                      deterministic=det, dq=grads[0], dk=grads[1], dv=grads[2])
+        for name, x in zip(("dq", "dk", "dv"), grads):
+            assert_within(x, r[name], r[name + "_tol"], name)
+        for x in (o, *grads):
+            assert bool((x[:9] == 7).all()) and bool((x[-11:] == 7).all())
+
+
+@pytest.mark.gpu
+def test_a_window_that_hides_nothing_is_the_plain_call():
+    __graft_entry__.build()
+    q, k, v, do = (x.cuda() for x in _inputs(500, 4, 2, 128, 1))
+    cu = _cu(_bounds([200, 300]))
+    for window in ((499, 0), (-1, 0), (2 ** 31 - 1, 0)):
+        a = fa.fwd_varlen(q, k, v, cu, window=window, sinks=4)
+        b = fa.fwd_varlen(q, k, v, cu, window=window)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        ga, gb = (fa.bwd_varlen(q, k, v, *b[:1], do, b[1], cu, window=window, deterministic=True,
+                                sinks=s) for s in (4, 0))
+        assert all(torch.equal(x, y) for x, y in zip(ga, gb))
+
+
+@pytest.mark.gpu
+def test_autograd_and_capture():
+    """attention_varlen's gradients are the calls'; a captured step replays on new lengths."""
+    __graft_entry__.build()
+    window, sinks, T, Hq, Hkv, D = (50, 0), 4, 600, 4, 2, 64
+    x = _inputs(T, Hq, Hkv, D, 2)
+    q, k, v = (t.cuda().requires_grad_() for t in x[:3])
+    do = x[3].cuda()
+    cu = _cu(_bounds([250, 350]))
+    o = fa.attention_varlen(q, k, v, cu, window=window, sinks=sinks, deterministic=True)
+    o.backward(do)
+    oo, lse = fa.fwd_varlen(q.detach(), k.detach(), v.detach(), cu, window=window, sinks=sinks)
+    g = fa.bwd_varlen(q.detach(), k.detach(), v.detach(), oo, do, lse, cu, window=window,
+                      sinks=sinks, deterministic=True)
+    assert torch.equal(o, oo)
+    assert all(torch.equal(a.grad, b) for a, b in zip((q, k, v), g))
+
+    d = [t.cuda() for t in x[:3]]
+
+    def step():
+        oo, lse = fa.fwd_varlen(*d, cu, window=window, sinks=sinks)
+        return (oo, *fa.bwd_varlen(*d, oo, do, lse, cu, window=window, sinks=sinks, deterministic=True))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for lens in ([250, 350], [1, 599], [600, 0]):
+        cu.copy_(_cu(_bounds(lens)))
+        d[0].copy_(torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(lens[0])))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.gpu
+def test_two_streams():
+    __graft_entry__.build()
+    window, sinks = (300, 0), 20
+    sets = [[t.cuda() for t in _inputs(2000, 4, 2, 128, s)] for s in (1, 2)]
+    cu = _cu(_bounds([1500, 500]))
+
+    def step(q, k, v, do):
+        o, lse = fa.fwd_varlen(q, k, v, cu, window=window, sinks=sinks)
+        return (o, *fa.bwd_varlen(q, k, v, o, do, lse, cu, window=window, sinks=sinks, deterministic=True))
+    want = [step(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[] for _ in sets]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(*sets[i]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for g in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, g))
