@@ -77,6 +77,20 @@ struct FwdLayout {
   static constexpr int kPolyPairs = (D == 64) ? 1 : 0;
 };
 
+// At most this many sinks in front of the window take a step of so many columns: GEMM 1
+// with N, GEMM 2 with K of 32, a quarter of the softmax.
+constexpr int kFewSinks = 32;
+
+// Bit i: key k0 + i is visible, in [lo, lim) or below sinks (and lim).
+__device__ __forceinline__ uint32_t seen_bits(int k0, int lo, int lim, int sinks) {
+  auto below = [&](int n) {  // bits of the keys from n on
+    uint32_t m;
+    asm("shl.b32 %0, %1, %2;" : "=r"(m) : "r"(0xffffffffu), "r"(max(n - k0, 0)));
+    return m;
+  };
+  return ~below(lim) & (below(lo) | ~below(sinks));
+}
+
 // kMod: 0 plain (no mask or the causal one), 1 a sliding window, 2 a window
 // and the relative-position bias (a.alibi) added to every score, 3 (packed) a window
 // with sinks: kv tile 0 first, then the window's tiles, what lies between left out.  kSplit: a
@@ -226,6 +240,7 @@ __global__ void __launch_bounds__(320, 1)
       constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile, false, false);
       constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D, false, true);
       constexpr uint32_t kHi = sdesc_hi(1024);  // SBO 1024 B, version 1, 128B swizzle
+      constexpr uint32_t kIdescFew = idesc_bf16_f32(kTile, kFewSinks, false, false);
       uint32_t kv_it = 0, q_it = 0;
       uint32_t p_seen[2] = {0u, 0u};  // P-ready phases consumed, per tile
       uint32_t units_t[2] = {0u, 0u};  // units with work, per tile (O-free phases)
@@ -256,6 +271,7 @@ __global__ void __launch_bounds__(320, 1)
         auto active = [&](int t, int p) {
           return kSink ? span.active(t, p) : p >= plo[t] && p < phi[t];
         };
+        const bool few = kSink && span.first && a.sinks <= kFewSinks && a.scale_log2 > 0.f;
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQFull + qs), (q_it / L::kQStages) & 1, abort_flag)) {
           ok = false;
@@ -299,10 +315,12 @@ __global__ void __launch_bounds__(320, 1)
               tc_fence_after();
               const uint32_t v_lo = sdesc_lo(v_base, L::kBlockBytes);
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
+              for (int kk = 0; kk < kTile / 16; ++kk) {
+                if (kSink && few && j == 1 && kk == kFewSinks / 16) break;
                 umma_ts_w(tmem + L::kColO + t * D, tmem + t * kTile + kk * 8,
                           v_lo + ((kk * 16 * 128) >> 4), kHi, kIdescO,
                           (j > plo[t] + 1 || kk > 0) ? 1u : 0u);
+              }
               if (j == phi[t]) umma_commit(bar(L::kBarOFinal + t));
             }
             if (active(t, j)) {
@@ -312,10 +330,11 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * L::kBlockBytes + (kk & 3) * 32) >> 4;
+                const uint32_t idesc = kSink && few && j == 0 ? kIdescFew : kIdescS;
                 if (kk == 0)
-                  umma_ss_w<0>(tmem + t * kTile, q_lo + off, kHi, k_lo + off, kHi, kIdescS);
+                  umma_ss_w<0>(tmem + t * kTile, q_lo + off, kHi, k_lo + off, kHi, idesc);
                 else
-                  umma_ss_w<1>(tmem + t * kTile, q_lo + off, kHi, k_lo + off, kHi, kIdescS);
+                  umma_ss_w<1>(tmem + t * kTile, q_lo + off, kHi, k_lo + off, kHi, idesc);
               }
               umma_commit(bar(L::kBarSFull + t));
             }
@@ -398,6 +417,34 @@ __global__ void __launch_bounds__(320, 1)
         ++g;
         tc_fence_after();
         const int kv0 = j * kTile;
+        if constexpr (kSink) {
+          if (p == 0 && span.first && sinks <= kFewSinks && a.scale_log2 > 0.f) {
+            // the sinks in front of the window: only their columns were computed
+            uint32_t v[kFewSinks], pk[kFewSinks / 2];
+            tmem_ld32(t_row + col_s, v);
+            const uint32_t seen = seen_bits(0, lo_row, lim, sinks);
+            float mraw = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kFewSinks; ++i) {
+              if (!(seen >> i & 1)) v[i] = __float_as_uint(-INFINITY);
+              mraw = fmaxf(mraw, u2f(v[i]));
+            }
+            m_run = mraw == -INFINITY ? mraw : mraw * a.scale_log2;
+            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+            for (int i = 0; i < kFewSinks / 2; ++i) {
+              const float p0 = ex2_mufu(fmaf(u2f(v[2 * i]), a.scale_log2, neg_m));
+              const float p1 = ex2_mufu(fmaf(u2f(v[2 * i + 1]), a.scale_log2, neg_m));
+              l_run += p0 + p1;
+              pk[i] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(t_row + col_s, pk);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            mbar_arrive(bar(L::kBarPFull + t));
+            continue;
+          }
+        }
         const bool masked_tile = kv0 + kTile > lim || (kWin && kv0 < lo_row);
         const float bias0 = slope2 * (float)(kv0 - q_row);  // bias of the tile's first key
         const float c = a.scale_log2;
@@ -417,17 +464,27 @@ __global__ void __launch_bounds__(320, 1)
         };
         if (c > 0.f) {
           // Common case.  Pass 1: the whole score row in one TMEM round trip,
-          // reduced to its max (masked columns skipped).  The plain kernel keeps
-          // the row in registers for pass 2; the score-modified kernels, which
-          // carry more live state, reload it.
+          // reduced to its max (masked columns skipped).  The plain kernel and the one
+          // with sinks keep the row in registers for pass 2; the other score-modified
+          // kernels, which carry more live state, reload it.
           float mraw = -INFINITY;
           uint32_t v[kTile];
           {
             tmem_ld128(t_row + col_s, v);
             if (masked_tile) {
+              if constexpr (kSink) {
 #pragma unroll
-              for (int i = 0; i < kTile; ++i)
-                if (hidden(kv0 + i)) v[i] = __float_as_uint(-INFINITY);
+                for (int h = 0; h < 4; ++h) {
+                  const uint32_t seen = seen_bits(kv0 + 32 * h, lo_row, lim, sinks);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!(seen >> i & 1)) v[32 * h + i] = __float_as_uint(-INFINITY);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < kTile; ++i)
+                  if (hidden(kv0 + i)) v[i] = __float_as_uint(-INFINITY);
+              }
             }
             if (kBias && kslope_ok) {
               // the bias varies along the row: with c > 0 the max of
@@ -457,7 +514,7 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t w0[32], w1[32], pk[32];
-            if constexpr (kMod == 0) {
+            if constexpr (kMod == 0 || kSink) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 w0[i] = v[h * 64 + i];
