@@ -36,7 +36,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_status", "fa_bwd_workspace_bytes", "fa_bwd", "fa_bw
            "fa_bwd_varlen", "fa_varlen_sink_workspace_bytes", "fa_fwd_varlen_sink",
            "fa_bwd_varlen_sink", "fa_cache4_page_bytes", "fa_cache4_append", "fa_cache4_read",
            "fa_cache4_attend_workspace_bytes", "fa_cache4_attend", "fa_cache4_evict",
-           "fa_cache4_status")
+           "fa_cache4_status", "fa_cache4_attend_sink", "fa_cache4_append_slots",
+           "fa_page_update", "fa_norm_rope_fwd", "fa_norm_rope_bwd",
+           "fa_norm_rope_workspace_bytes", "fa_rope_table")
 
 
 class ScoreMod(ctypes.Structure):
@@ -133,6 +135,23 @@ def _bind(lib):
     lib.fa_cache4_attend.argtypes = [vp, i64, i64, vp, i, i, vp, vp, i, i, i, i, vp, vp, i, f, vp,
                                      vp, i, vp, sz, vp]
     lib.fa_cache4_attend.restype = i
+    lib.fa_cache4_attend_sink.argtypes = [vp, i64, i64, vp, i, i, vp, vp, i, i, i, i, vp, vp, i, i,
+                                          i, f, vp, vp, i, vp, sz, vp]
+    lib.fa_cache4_attend_sink.restype = i
+    lib.fa_cache4_append_slots.argtypes = [vp, i, i, vp, vp, psp, psp, i, i, i, vp, vp]
+    lib.fa_cache4_append_slots.restype = i
+    lib.fa_page_update.argtypes = [vp, i, vp, vp, i, vp, vp, i, i, i, i, i, vp, vp, vp, vp]
+    lib.fa_page_update.restype = i
+    lib.fa_norm_rope_fwd.argtypes = [vp] * 6 + [i, vp, vp, vp, i, i, i, i, i, i, i, f, psp, psp, psp,
+                                                psp, i, vp]
+    lib.fa_norm_rope_fwd.restype = i
+    lib.fa_norm_rope_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_norm_rope_workspace_bytes.restype = sz
+    lib.fa_norm_rope_bwd.argtypes = [vp] * 10 + [i, vp, vp, vp, i, i, i, i, i, i, i, f, psp, psp,
+                                                 psp, psp, psp, psp, i, vp, sz, vp]
+    lib.fa_norm_rope_bwd.restype = i
+    lib.fa_rope_table.argtypes = [vp, vp, i64, i, ctypes.c_double, vp]
+    lib.fa_rope_table.restype = i
     lib.fa_cache4_evict.argtypes = [vp, i, i, vp, i, vp, vp, i, i, i, i, i, i, vp, i, vp, vp, vp,
                                     vp]
     lib.fa_cache4_evict.restype = i
@@ -550,6 +569,87 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     return _AttentionVarlen.apply(q, k, v, cu_seqlens, causal, scale, window, deterministic, sinks)
 
 
+def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda", stream=None):
+    """cos and sin fp32 [positions, rot/2] of the angles p base^(-2i/rot), taken in 64 bits
+    (fa_rope_table)."""
+    device = torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.device(device):
+        cos, sin = (_new((max(positions, 0), max(rot, 0) // 2), torch.float32, device, stream)
+                    for _ in range(2))
+        rc = lib().fa_rope_table(_ptr(cos), _ptr(sin), int(positions), int(rot), float(base),
+                                 _stream(stream))
+    if rc != FA_OK:
+        raise FAError("fa_rope_table", rc)
+    return cos, sin
+
+
+def norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                  cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6,
+                  interleaved: bool = False, q_out=None, k_out=None, zero_skipped: bool = False,
+                  stream=None):
+    """RMS norms of query and key heads and their rotation by position (fa_norm_rope_fwd).
+
+    q [T,Hq,D], k [T,Hkv,D] bf16 CUDA, elements contiguous, tokens and heads at any stride
+    that is a multiple of 8 (slices of a fused projection); weights [D], fp32 or bf16;
+    ``cos``, ``sin`` fp32 [P,rot/2] (rope_table): the first ``rot`` elements of a head are
+    rotated, in pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``; ``positions``
+    int32 [T].  A token with a negative position is of no sequence: its rows are not
+    written, or become zeros with ``zero_skipped``.  fwd_status() reports positions from P on,
+    which count as such.  ``q_out``, ``k_out``: like q and k, of any such strides, also q
+    and k themselves.  Returns (q_out, k_out) bf16.
+    """
+    return _compiled().norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, float(eps),
+                                     interleaved, q_out, k_out, zero_skipped, stream)
+
+
+def norm_rope_workspace_bytes(T, Hq, Hkv, D) -> int:
+    """Workspace bytes of norm_rope_bwd on the current device."""
+    return int(lib().fa_norm_rope_workspace_bytes(T, Hq, Hkv, D))
+
+
+def norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps: float = 1e-6,
+                  interleaved: bool = False, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                  workspace: torch.Tensor | None = None, zero_skipped: bool = False, stream=None):
+    """Backward of norm_rope_fwd (fa_norm_rope_bwd), whose arguments it takes as given there.
+    Returns (dq, dk bf16, dq_weight, dk_weight fp32 [D]); the same bits in every run."""
+    return _compiled().norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out,
+                                     float(eps), interleaved, dq, dk, dq_weight, dk_weight,
+                                     workspace, zero_skipped, stream)
+
+
+class _NormRope(torch.autograd.Function):
+    """norm_rope_fwd in forward, norm_rope_bwd in backward; nothing else runs."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.args = (eps, interleaved)
+        return norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, eps=eps,
+                             interleaved=interleaved, zero_skipped=True)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        eps, interleaved = ctx.args
+        dq, dk, dqw, dkw = norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions,
+                                         dq_out.contiguous(), dk_out.contiguous(), eps=eps,
+                                         interleaved=interleaved, zero_skipped=True)
+        return dq, dk, dqw.to(q_weight.dtype), dkw.to(k_weight.dtype), None, None, None, None, None
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+              cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6,
+              interleaved: bool = False):
+    """norm_rope_fwd as a differentiable op: gradients for q, k and the weights (those in the
+    weights' type).  Tokens with a negative position get zeros in the results and in every
+    gradient.  The gradients cannot be differentiated again (RuntimeError).  Returns (q, k)
+    bf16, contiguous."""
+    return _NormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+
 def cache4_empty(num_pages: int, Hkv: int, D: int, page_size: int = 64, device="cuda"):
     """A paged 4-bit key/value cache (include/fa.h, fa_cache4_page_bytes): uint8
     [num_pages, Hkv, bytes of a page and head], zeroed.  page_size: 16, 32, 64 or
@@ -572,6 +672,40 @@ def cache4_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, page_ta
     _compiled().cache4_append(cache, k, v, page_table, cache_lens, cu_seqlens, stream)
 
 
+def cache4_append_slots(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                        stream=None):
+    """Quantises and stores new tokens by slot (fa_cache4_append_slots): row i of k, v
+    [T,Hkv,D] goes to slot ``slots[i]`` (int64 [T], as page_update returns them), a negative
+    one nowhere."""
+    _compiled().cache4_append_slots(cache, k, v, slots, stream)
+
+
+def page_pool(num_pages: int, device="cuda"):
+    """A pool of free pages 0 .. num_pages - 1 for page_update: (free_pages int32
+    [num_pages], a stack, and free_count int32 [1])."""
+    return (torch.arange(num_pages, dtype=torch.int32, device=device),
+            torch.full((1,), num_pages, dtype=torch.int32, device=device))
+
+
+def page_update(page_table: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                lens: torch.Tensor, new_lens: torch.Tensor, page_size: int, T: int,
+                window_left: int | None = None, sinks: int = 0, cu_seqlens=None, positions=None,
+                slots=None, stream=None):
+    """Page tables for the lengths to come (fa_page_update), in place.
+
+    ``page_table`` int32 [B,width]; ``free_pages``, ``free_count``: the pool (page_pool);
+    ``lens``, ``new_lens`` int32 [B]: tokens held and to be held.  Entries past the new
+    length, and those that a window of ``window_left`` tokens with ``sinks`` hides from the
+    last token's query on, give their pages back; entries for new tokens take pages.
+    Returns (cu_seqlens int32 [B+1], positions int32 [T], slots int64 [T]) of the new
+    tokens, packed in order; ``T`` is the rows they have, and rows past the last get -1.
+    cache4_status() reports a pool or T that was too small, and lengths past the table.
+    """
+    return _compiled().page_update(page_table, free_pages, free_count, lens, new_lens, page_size, T,
+                                   -1 if window_left is None else window_left, sinks, cu_seqlens,
+                                   positions, slots, stream)
+
+
 def cache4_read(cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tensor | None,
                 count: torch.Tensor, S: int, D: int, k=None, v=None, stream=None):
     """The values the cache holds (fa_cache4_read): slots first[b] .. first[b] +
@@ -590,8 +724,10 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
                   cache_lens: torch.Tensor, scale: float | None = None,
                   weights: torch.Tensor | None = None, weights_out: torch.Tensor | None = None,
                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                  workspace: torch.Tensor | None = None, stream=None):
-    """One query token per sequence attends to its cache (fa_cache4_attend).
+                  workspace: torch.Tensor | None = None, stream=None,
+                  window_left: int | None = None, sinks: int = 0):
+    """One query token per sequence attends to its cache (fa_cache4_attend,
+    fa_cache4_attend_sink).
 
     q [B,Hq,D] bf16 CUDA, elements contiguous; ``cache_lens`` int32 [B].
     ``weights`` fp32 [B,Hkv,slots] has the tokens' softmax weights, summed over each
@@ -600,10 +736,13 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     at what the tensor holds there, so it begins as zeros.  ``slots`` is at least
     every length: tokens behind it are left out of all results and cache4_status()
     reports them.
+    ``window_left``: the query, which is the last token's, sees the ``window_left`` tokens
+    before it and the first ``sinks``; the pages of the others are not looked up.
     Returns (o [B,Hq,D] bf16, lse [B,Hq] fp32); o = 0, lse = -inf without tokens.
     """
+    wl = -1 if window_left is None else max(-1, min(int(window_left), 2 ** 31 - 1))
     return _compiled().cache4_attend(q, cache, page_table, cache_lens, scale, weights, weights_out,
-                                     out, lse, workspace, stream)
+                                     out, lse, workspace, stream, wl, sinks)
 
 
 def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torch.Tensor,

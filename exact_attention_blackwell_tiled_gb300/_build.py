@@ -20,7 +20,7 @@ BINDING_PATH = os.path.join(PKG, "_binding.so")
 BINDING_KEY_PATH = os.path.join(BUILD_DIR, "_binding.key")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_ring.cu", "fa_bwd.cu", "fa_bwd_q128.cu", "fa_bwd_pair.cu", "fa_bwd_sink.cu", "fa_merge.cu", "fa_noalloc.cu",
-           "fa_varlen.cu", "fa_cache4.cu", "fa_cache4_attend.cu"]
+           "fa_varlen.cu", "fa_cache4.cu", "fa_cache4_attend.cu", "fa_norm_rope.cu", "fa_pages.cu"]
 HEADERS = ["fa_internal.h", "ptx.cuh", "exp2.cuh", "bwd_common.cuh", "fwd_common.cuh",
            "var_common.cuh", "cache4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -346,6 +346,141 @@ PyObject* cache4_append(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// cache, k, v, slots, stream
+PyObject* cache4_append_slots(PyObject* const* a) {
+  const Packed k = packed(a[1], "k"), v = packed(a[2], "v", &k);
+  const int T = (int)k.size(0), Hkv = (int)k.size(1), D = (int)k.size(2), device = k.device();
+  const Cache c = cache4(a[0], D);
+  if (c.Hkv != Hkv || c.device != device) value_error("cache and k must have the same kv heads and device");
+  const Place place(device, a[4]);
+  const at::Tensor& slots = given(a[3], {T}, at::kLong, device, "slots");
+  call("fa_cache4_append_slots", [&] {
+    return fa_cache4_append_slots(c.p, c.pages, c.page, k.t->data_ptr(), v.t->data_ptr(), k.stride(),
+                                  v.stride(), T, Hkv, D, static_cast<const int64_t*>(slots.data_ptr()),
+                                  place.stream);
+  });
+  Py_RETURN_NONE;
+}
+
+// page_table, free_pages, free_count, lens, new_lens, page_size, T, window_left, sinks,
+// cu_seqlens, positions, slots, stream
+PyObject* page_update(PyObject* const* a) {
+  const at::Tensor* t = tensor(a[0]);
+  if (!t || !t->is_cuda()) type_error("page_table must be an int32 CUDA tensor");
+  const int device = t->get_device();
+  const Place place(device, a[12]);
+  int64_t B, pages;
+  const int* lens = int32s(a[3], -1, device, "lens", &B);
+  const int* new_lens = int32s(a[4], B, device, "new_lens");
+  int width;
+  int* table = const_cast<int*>(page_table(a[0], B, device, &width));
+  int* stack = const_cast<int*>(int32s(a[1], -1, device, "free_pages", &pages));
+  int* count = const_cast<int*>(int32s(a[2], 1, device, "free_count"));
+  const int page = to_int(a[5]), T = to_int(a[6]), wl = to_int(a[7]), sinks = to_int(a[8]);
+  if (T < 0) check("fa_page_update", 1);
+  const at::Tensor cu = output(a[9], {B + 1}, at::kInt, place, "cu_seqlens");
+  const at::Tensor pos = output(a[10], {T}, at::kInt, place, "positions");
+  const at::Tensor slots = output(a[11], {T}, at::kLong, place, "slots");
+  call("fa_page_update", [&] {
+    return fa_page_update(table, width, stack, count, (int)pages, lens, new_lens, (int)B, page, wl, sinks,
+                          T, static_cast<int*>(cu.data_ptr()), static_cast<int*>(pos.data_ptr()),
+                          static_cast<int64_t*>(slots.data_ptr()), place.stream);
+  });
+  return tuple(cu, pos, slots);
+}
+
+// ------------------------------------------------------------------ norms and rotation
+
+struct NormRope {
+  Packed q, k;
+  const at::Tensor *qw, *kw;
+  const float *cos, *sin;
+  const int* pos;
+  int T, Hq, Hkv, D, rows, rot, device, bf16;
+};
+
+// q, k, q_weight, k_weight, cos, sin, positions
+NormRope norm_rope_inputs(PyObject* const* a) {
+  const Packed q = packed(a[0], "q"), k = packed(a[1], "k");
+  if (k.size(0) != q.size(0) || k.size(2) != q.size(2) || k.device() != q.device())
+    value_error("k must have q's tokens, head dimension and device");
+  const int T = (int)q.size(0), D = (int)q.size(2), device = q.device();
+  const at::Tensor* w[2];
+  for (int i = 0; i < 2; ++i) {
+    const char* name = i ? "k_weight" : "q_weight";
+    w[i] = tensor(a[2 + i]);
+    if (!w[i] || !w[i]->is_cuda() || (w[i]->scalar_type() != at::kFloat && w[i]->scalar_type() != at::kBFloat16))
+      type_error(std::string(name) + " must be a fp32 or bfloat16 CUDA tensor");
+    if (w[i]->dim() != 1 || w[i]->size(0) != D || !w[i]->is_contiguous() || w[i]->get_device() != device)
+      value_error(std::string(name) + " must be contiguous, of q's head dimension, on its device");
+  }
+  if (w[0]->scalar_type() != w[1]->scalar_type()) value_error("q_weight and k_weight must have one type");
+  const at::Tensor* t = tensor(a[4]);
+  if (!t || t->dim() != 2 || t->size(0) > INT_MAX || t->size(1) > INT_MAX / 2)
+    type_error("cos must be a tensor [positions, rotated pairs]");
+  const int rows = (int)t->size(0), rot = 2 * (int)t->size(1);
+  const at::Tensor& cos = given(a[4], t->sizes(), at::kFloat, device, "cos");
+  const at::Tensor& sin = given(a[5], t->sizes(), at::kFloat, device, "sin");
+  return {q, k, w[0], w[1], static_cast<const float*>(cos.data_ptr()), static_cast<const float*>(sin.data_ptr()),
+          int32s(a[6], T, device, "positions"), T, (int)q.size(1), (int)k.size(1), D, rows, rot, device,
+          w[0]->scalar_type() == at::kBFloat16 ? 1 : 0};
+}
+
+// A result like `like`: the caller's, of any strides, or a new contiguous one.
+struct PackedOut {
+  at::Tensor t;
+  fa_packed_stride s;
+  bool plain;
+  const fa_packed_stride* stride() const { return plain ? nullptr : &s; }
+};
+PackedOut packed_output(PyObject* o, const Packed& like, const Place& place, const char* name) {
+  if (o == Py_None)
+    return {output(o, like.t->sizes(), at::kBFloat16, place, name), {0, 0}, true};
+  const Packed p = packed(o, name, &like);
+  return {*p.t, p.s, p.plain};
+}
+
+// q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out,
+// zero_skipped, stream
+PyObject* norm_rope_fwd(PyObject* const* a) {
+  const NormRope x = norm_rope_inputs(a);
+  const Place place(x.device, a[12]);
+  const float eps = to_scale(a[7], x.D);
+  const int interleaved = to_bool(a[8]), zero = to_bool(a[11]);
+  const PackedOut q = packed_output(a[9], x.q, place, "q_out"), k = packed_output(a[10], x.k, place, "k_out");
+  call("fa_norm_rope_fwd", [&] {
+    return fa_norm_rope_fwd(x.q.t->data_ptr(), x.k.t->data_ptr(), q.t.data_ptr(), k.t.data_ptr(),
+                            x.qw->data_ptr(), x.kw->data_ptr(), x.bf16, x.cos, x.sin, x.pos, x.T, x.Hq,
+                            x.Hkv, x.D, x.rows, x.rot, interleaved, eps, x.q.stride(), x.k.stride(),
+                            q.stride(), k.stride(), zero, place.stream);
+  });
+  return tuple(q.t, k.t);
+}
+
+// q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps, interleaved, dq, dk,
+// dq_weight, dk_weight, workspace, zero_skipped, stream
+PyObject* norm_rope_bwd(PyObject* const* a) {
+  const NormRope x = norm_rope_inputs(a);
+  const Packed gq = packed(a[7], "dq_out", &x.q), gk = packed(a[8], "dk_out", &x.k);
+  const Place place(x.device, a[17]);
+  const float eps = to_scale(a[9], x.D);
+  const int interleaved = to_bool(a[10]), zero = to_bool(a[16]);
+  const PackedOut q = packed_output(a[11], x.q, place, "dq"), k = packed_output(a[12], x.k, place, "dk");
+  const at::Tensor qw = output(a[13], {x.D}, at::kFloat, place, "dq_weight");
+  const at::Tensor kw = output(a[14], {x.D}, at::kFloat, place, "dk_weight");
+  const size_t need = a[15] == Py_None ? fa_norm_rope_workspace_bytes(x.T, x.Hq, x.Hkv, x.D) : 0;
+  const at::Tensor ws = workspace(a[15], need, place);
+  call("fa_norm_rope_bwd", [&] {
+    return fa_norm_rope_bwd(x.q.t->data_ptr(), x.k.t->data_ptr(), gq.t->data_ptr(), gk.t->data_ptr(),
+                            q.t.data_ptr(), k.t.data_ptr(), static_cast<float*>(qw.data_ptr()),
+                            static_cast<float*>(kw.data_ptr()), x.qw->data_ptr(), x.kw->data_ptr(), x.bf16,
+                            x.cos, x.sin, x.pos, x.T, x.Hq, x.Hkv, x.D, x.rows, x.rot, interleaved, eps,
+                            x.q.stride(), x.k.stride(), gq.stride(), gk.stride(), q.stride(), k.stride(),
+                            zero, ws.data_ptr(), ws.nbytes(), place.stream);
+  });
+  return tuple(q.t, k.t, qw, kw);
+}
+
 // cache, page_table, first, count, S, D, k, v, stream
 PyObject* cache4_read(PyObject* const* a) {
   const int S = to_int(a[4]), D = to_int(a[5]);
@@ -367,7 +502,7 @@ PyObject* cache4_read(PyObject* const* a) {
 }
 
 // q, cache, page_table, cache_lens, scale, weights, weights_out, out, lse, workspace,
-// stream
+// stream, window_left, sinks
 PyObject* cache4_attend(PyObject* const* a) {
   const Packed q = packed(a[0], "q");
   const int B = (int)q.size(0), Hq = (int)q.size(1), D = (int)q.size(2), device = q.device();
@@ -379,6 +514,7 @@ PyObject* cache4_attend(PyObject* const* a) {
   int width, slots = 0;
   const int* table = page_table(a[2], B, device, &width);
   const float scale = to_scale(a[4], D);
+  const int wl = to_int(a[11]), sinks = to_int(a[12]);
   float *w_in = nullptr, *w_out = nullptr;
   if (a[5] != Py_None) w_in = w_out = weights(a[5], B, c.Hkv, device, &slots, "weights");
   if (a[6] != Py_None) {
@@ -393,11 +529,11 @@ PyObject* cache4_attend(PyObject* const* a) {
       a[9] == Py_None ? fa_cache4_attend_workspace_bytes(B, Hq, c.Hkv, D, slots) : 0;
   const at::Tensor ws = workspace(a[9], need, place);
   // the stride of a dimension of one element is arbitrary
-  call("fa_cache4_attend", [&] {
-    return fa_cache4_attend(q.t->data_ptr(), B > 1 ? q.t->stride(0) : 0,
+  call(wl < 0 ? "fa_cache4_attend" : "fa_cache4_attend_sink", [&] {
+    return fa_cache4_attend_sink(q.t->data_ptr(), B > 1 ? q.t->stride(0) : 0,
                             Hq > 1 ? q.t->stride(1) : 0, c.p, c.pages, c.page, o.data_ptr(),
                             static_cast<float*>(lse.data_ptr()), B, Hq, c.Hkv, D, lens, table,
-                            width, scale, w_in, w_out, slots, ws.data_ptr(), ws.nbytes(),
+                            width, wl, sinks, scale, w_in, w_out, slots, ws.data_ptr(), ws.nbytes(),
                             place.stream);
   });
   return tuple(o, lse);
@@ -461,7 +597,11 @@ PyMethodDef g_methods[] = {method<fwd_varlen, 12>("fwd_varlen"),
                            method<bwd_varlen, 17>("bwd_varlen"),
                            method<cache4_append, 7>("cache4_append"),
                            method<cache4_read, 9>("cache4_read"),
-                           method<cache4_attend, 11>("cache4_attend"),
+                           method<cache4_append_slots, 5>("cache4_append_slots"),
+                           method<page_update, 13>("page_update"),
+                           method<norm_rope_fwd, 13>("norm_rope_fwd"),
+                           method<norm_rope_bwd, 18>("norm_rope_bwd"),
+                           method<cache4_attend, 13>("cache4_attend"),
                            method<cache4_evict, 12>("cache4_evict"),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

@@ -27,6 +27,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
+
 #include "cache4.cuh"
 #include "fa_internal.h"
 #include "ptx.cuh"
@@ -45,6 +47,7 @@ struct AppendArgs {
   long long k_token, k_head, v_token, v_head;
   const int* cu;    // [B + 1], or null: one token per sequence
   const int* lens;  // [B] tokens held before
+  const long long* slots;  // [T] (kSlots) where the tokens go, instead: -1 for nowhere
   C4Table table;
   int B, T, Hkv;
 };
@@ -136,8 +139,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // A lane takes 16 elements, half a group, so that 32 elements share one scale, one
 // shuffle each for minimum and maximum, and four stores; D / 16 lanes hold a vector,
 // and the lanes of a warp 1024 / D vectors at a time: the key and the value of
-// 512 / D (token, head) items.
-template <int D>
+// 512 / D (token, head) items.  kSlots: the tokens' slots are given.
+template <int D, bool kSlots>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
   using L = C4<D>;
   constexpr int kLanes = D / 16;          // of a vector
@@ -177,14 +180,23 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   long long off_n = -1;
   int slot_n = 0;
   {
-    const int first = a.cu ? find_sequence(a.cu, a.B, (int)tok0) : (int)tok0;
+    const int first = !kSlots && a.cu ? find_sequence(a.cu, a.B, (int)tok0) : (int)tok0;
     const uint32_t item = item0 + lane;
     if (lane < kAppendItems && item < total) {
       int tok = (int)tok0;
       uint32_t h = h0 + lane;
       for (; h >= heads; h -= heads) ++tok;
-      int b = a.cu ? first : tok;
-      if (a.cu) {
+      int b = kSlots ? -1 : a.cu ? first : tok;
+      if constexpr (kSlots) {
+        const long long s = a.slots[tok], page = s >> (a.table.shift + 4);
+        if (s >= 0 && page < a.table.num_pages) {
+          slot_n = (int)(s % kC4Block);
+          const int blk = a.table.in_page((int)((s / kC4Block) & INT_MAX));
+          off_n = ((page * a.Hkv + h) * a.table.blocks_per_page() + blk) * L::kBytes;
+        } else if (s >= 0) {
+          c4_flag(a.table);
+        }
+      } else if (a.cu) {
         // later items may belong to later sequences
         if (b < 0 && tok > (int)tok0) b = 0;
         while (b >= 0 && b < a.B && tok >= a.cu[b + 1]) ++b;
@@ -638,6 +650,16 @@ C4Table make_table(const int* pages, int width, int num_pages, int page_size, in
   return C4Table{pages, width, num_pages, c4_shift(page_size), status};
 }
 
+int launch_append(void (*kernel)(AppendArgs), const AppendArgs& a, fa_stream_t stream) {
+  const long long per = kAppendWarps * kAppendItems;
+  const long long grid = ((long long)a.T * a.Hkv + per - 1) / per;
+  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kAppendWarps * 32), 0,
+                 static_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -671,16 +693,36 @@ int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, c
   if (!status) return FA_ERR_CUDA;
   AppendArgs a{static_cast<uint8_t*>(cache), static_cast<const __nv_bfloat16*>(k),
                static_cast<const __nv_bfloat16*>(v), ks.token, ks.head, vs.token, vs.head,
-               cu_seqlens, cache_lens,
+               cu_seqlens, cache_lens, nullptr,
                make_table(page_table, table_width, num_pages, page_size, status), B, T, Hkv};
-  const long long per = kAppendWarps * kAppendItems;
-  const long long grid = ((long long)T * Hkv + per - 1) / per;
-  const auto kernel = D == 128 ? append_kernel<128> : append_kernel<64>;
-  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(kAppendWarps * 32), 0,
-                 static_cast<cudaStream_t>(stream), a) != cudaSuccess)
-    return FA_ERR_CUDA;
-  note_launches(1);
-  return FA_OK;
+  return launch_append(D == 128 ? append_kernel<128, false> : append_kernel<64, false>, a, stream);
+}
+
+int fa_cache4_append_slots(void* cache, int num_pages, int page_size, const void* k, const void* v,
+                           const fa_packed_stride* k_stride, const fa_packed_stride* v_stride, int T,
+                           int Hkv, int D, const int64_t* slots, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_cache4(num_pages, Hkv, D, page_size, 1, 1);
+  if (rc) return rc;
+  if (T < 0 || (long long)T * Hkv >= (1LL << 31) - 64) return FA_ERR_INVALID_ARG;
+  const fa_packed_stride plain = {(int64_t)Hkv * D, D};
+  const fa_packed_stride ks = k_stride ? *k_stride : plain, vs = v_stride ? *v_stride : plain;
+  for (int64_t s : {ks.token, ks.head, vs.token, vs.head}) {
+    if (s < 0) return FA_ERR_INVALID_ARG;
+    if (s & 7) return FA_ERR_MISALIGNED;
+  }
+  if (T == 0) return FA_OK;
+  if (!cache || !k || !v || !slots) return FA_ERR_INVALID_ARG;
+  if (misaligned(cache, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 8))
+    return FA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  int* status = cache4_status_word();
+  if (!status) return FA_ERR_CUDA;
+  AppendArgs a{static_cast<uint8_t*>(cache), static_cast<const __nv_bfloat16*>(k),
+               static_cast<const __nv_bfloat16*>(v), ks.token, ks.head, vs.token, vs.head,
+               nullptr, nullptr, reinterpret_cast<const long long*>(slots),
+               make_table(nullptr, 0, num_pages, page_size, status), 1, T, Hkv};
+  return launch_append(D == 128 ? append_kernel<128, true> : append_kernel<64, true>, a, stream);
 }
 
 int fa_cache4_read(const void* cache, int num_pages, int page_size, void* k, void* v, int B, int Hkv,

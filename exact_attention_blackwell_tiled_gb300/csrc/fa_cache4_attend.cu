@@ -96,6 +96,7 @@ struct AttendArgs {
   const float* w_in;
   float* w_out;  // [B, Hkv, w_stride]
   int w_stride;
+  int wl, sinks;  // the window (kWin): the last wl + 1 tokens and the first `sinks`
 };
 
 // Fewest 16-slot blocks worth a warp of its own: with fewer, the parts to join
@@ -124,8 +125,40 @@ __device__ __forceinline__ int seq_len(const AttendArgs& a, int b) {
   return n < 0 ? 0 : (n < a.cap ? n : a.cap);
 }
 
+// The blocks that a sequence's query sees, numbered 0 .. nb - 1: the first `front` ones,
+// which hold sinks, and those from block front + gap on.  Without a window: all.
+template <bool kWin>
+struct View {
+  int len, nb;
+  int lo, front, gap, sinks;  // (kWin) keys from lo on and below `sinks` are visible
+  __device__ __forceinline__ int block(int i) const { return !kWin || i < front ? i : i + gap; }
+  __device__ __forceinline__ bool key(int j) const { return j < len && (!kWin || j >= lo || j < sinks); }
+  // whether all keys of block `blk` are visible
+  __device__ __forceinline__ bool whole(int blk) const {
+    const int j = blk * kC4Block;
+    return j + kC4Block <= len && (!kWin || j >= lo || j + kC4Block <= sinks);
+  }
+};
+template <bool kWin>
+__device__ __forceinline__ View<kWin> seq_view(const AttendArgs& a, int b) {
+  View<kWin> v;
+  v.len = seq_len(a, b);
+  const int all = (v.len + kC4Block - 1) / kC4Block;
+  v.nb = all;
+  if constexpr (kWin) {
+    v.sinks = a.sinks;
+    v.lo = max(0, v.len - 1 - a.wl);
+    const int first = v.lo / kC4Block;
+    v.front = min((a.sinks + kC4Block - 1) / kC4Block, first);
+    v.gap = first - v.front;
+    v.nb = all - v.gap;
+  }
+  return v;
+}
+
+template <bool kWin>
 __device__ __forceinline__ int seq_blocks(const AttendArgs& a, int b) {
-  return (seq_len(a, b) + kC4Block - 1) / kC4Block;
+  return seq_view<kWin>(a, b).nb;
 }
 
 // Prefix sums of the sequences' blocks by a whole warp: lane l holds sequences
@@ -138,6 +171,7 @@ struct List {
   long long total;
 };
 
+template <bool kWin>
 __device__ __forceinline__ List read_list(const AttendArgs& a) {
   const int lane = threadIdx.x & 31;
   List s;
@@ -145,7 +179,7 @@ __device__ __forceinline__ List read_list(const AttendArgs& a) {
   s.own = 0;
   const int b0 = lane * s.per, b1 = min(a.B, b0 + s.per);
 #pragma unroll 4
-  for (int b = b0; b < b1; ++b) s.own += seq_blocks(a, b);
+  for (int b = b0; b < b1; ++b) s.own += seq_blocks<kWin>(a, b);
   long long inc = s.own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -158,6 +192,7 @@ __device__ __forceinline__ List read_list(const AttendArgs& a) {
 }
 
 // The sequence that holds block x of the list (x < total), and its first block.
+template <bool kWin>
 __device__ __forceinline__ int locate(const AttendArgs& a, const List& s, long long x,
                                       long long* base) {
   const int lane = threadIdx.x & 31;
@@ -166,7 +201,7 @@ __device__ __forceinline__ int locate(const AttendArgs& a, const List& s, long l
   long long at = s.before;
   int b = lane * s.per;
   if (lane == l)
-    for (int n; x >= at + (n = seq_blocks(a, b)); ++b) at += n;
+    for (int n; x >= at + (n = seq_blocks<kWin>(a, b)); ++b) at += n;
   *base = __shfl_sync(0xffffffffu, at, l);
   return __shfl_sync(0xffffffffu, b, l);
 }
@@ -300,8 +335,9 @@ __device__ __forceinline__ void write_lse(const AttendArgs& a, size_t row, float
 
 // kOwn: short caches and few rows.  A block of 8 warps takes one row, its warps equal
 // parts of it, and joins them in shared memory, weights included: one launch.
-// Otherwise every warp takes a share of the list.
-template <int D, int NT, bool kOwn>
+// Otherwise every warp takes a share of the list.  kWin: a window with sinks; blocks count
+// as View numbers them, and only those are looked up and read.
+template <int D, int NT, bool kOwn, bool kWin>
 __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : blocks_per_sm(D, NT))
     attend_kernel(const AttendArgs a) {
   using L = C4<D>;
@@ -323,20 +359,21 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
   grid_dep_launch();
   // rows (b, kv head, tile) in order: a sequence has rows_per rows of its blocks
   const int rows_per = a.Hkv * a.tiles;
-  int row_b, row, len, nb, blk0, left;  // left: blocks still to do
+  int row_b, row, blk0, left;  // left: blocks still to do
+  View<kWin> view;
   int w = 0;
   if constexpr (kOwn) {
     row_b = blockIdx.x / rows_per;
     row = blockIdx.x - row_b * rows_per;
-    len = seq_len(a, row_b);
-    nb = (len + kC4Block - 1) / kC4Block;
+    view = seq_view<kWin>(a, row_b);
+    const int nb = view.nb;
     const int per = (nb + 2 * kW - 1) / (2 * kW) * 2;  // pairs of blocks
     blk0 = min(nb, warp * per);
     left = min(per, nb - blk0);
     if (lane < 8 * NT) s_ml[warp][lane] = make_float2(-INFINITY, 0.f);
-    if (row == 0 && threadIdx.x == 0 && a.lens[row_b] != len) c4_flag(a.table);
+    if (row == 0 && threadIdx.x == 0 && a.lens[row_b] != view.len) c4_flag(a.table);
   } else {
-    const List list = read_list(a);
+    const List list = read_list<kWin>(a);
     const long long N = list.total * rows_per;
     if (N == 0) return;
     const int W = share_count(a, N);
@@ -345,12 +382,11 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
     const long long begin = share_begin(N, W, w);
     left = (int)(share_begin(N, W, w + 1) - begin);
     long long base;
-    row_b = locate(a, list, begin / rows_per, &base);
-    len = seq_len(a, row_b);
-    nb = (len + kC4Block - 1) / kC4Block;
+    row_b = locate<kWin>(a, list, begin / rows_per, &base);
+    view = seq_view<kWin>(a, row_b);
     // where in the sequence's rows the share begins
-    row = (int)((begin - base * rows_per) / nb);
-    blk0 = (int)(begin - base * rows_per - (long long)row * nb);
+    row = (int)((begin - base * rows_per) / view.nb);
+    blk0 = (int)(begin - base * rows_per - (long long)row * view.nb);
   }
 
   const float score_up = a.scale_log2 * kScoreUp;
@@ -360,13 +396,14 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
   int st = 0;          // the stage consumed next, and its barrier's phase
   uint32_t phase = 0;
   while (left > 0) {
+    const int nb = view.nb, len = view.len;
     const int blk1 = min(nb, blk0 + left);
     const int hk = row / a.tiles, tile = row - hk * a.tiles;
     // ---- copies: lane x takes block x of a stage; its page is looked up a stage ahead
     const uint8_t* head_base = a.cache + (size_t)hk * a.table.blocks_per_page() * L::kBytes;
     const size_t page_bytes = (size_t)a.Hkv * a.table.blocks_per_page() * L::kBytes;
     int next = blk0 + lane;  // block of the lane's next copy
-    auto look_up = [&]() { return lane < R::kBlocks && next < blk1 ? c4_page(a.table, row_b, next) : 0; };
+    auto look_up = [&]() { return lane < R::kBlocks && next < blk1 ? c4_page(a.table, row_b, view.block(next)) : 0; };
     int page = look_up();
     uint32_t bad = 0;  // bit kBlocks * stage + x: that block's page is out of range
     auto fill = [&](int st, int first) {  // blocks first .. of the row into stage st
@@ -378,7 +415,7 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
       if (mine && page >= 0)
         copy_block(smem_u32(ring) + st * R::kBytes + lane * L::kBytes,
                    head_base + page * page_bytes +
-                       a.table.in_page(next) * L::kBytes,
+                       a.table.in_page(view.block(next)) * L::kBytes,
                    L::kBytes, bars + 8 * st);
       bad = (bad & ~(((1u << R::kBlocks) - 1) << (st * R::kBlocks))) | (miss << (st * R::kBlocks));
       if (miss && lane == 0) c4_flag(a.table);
@@ -440,7 +477,8 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
     }
     float* score = nullptr;  // of this lane's first column and row i's key
     if (a.scores)
-      score = a.scores + (((size_t)row_b * a.Hkv + hk) * a.cap + blk0 * kC4Block + slot_i) * a.group +
+      score = a.scores +
+              (((size_t)row_b * a.Hkv + hk) * a.cap + (kWin ? 0 : blk0) * kC4Block + slot_i) * a.group +
               tile * 8 * NT + 2 * t;
     // ---- its blocks, two at a time: their chains of dependent steps interleave
 #pragma unroll 1
@@ -514,13 +552,26 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
       // slots behind the last key, and blocks whose page is out of range
       const uint32_t miss = (bad >> (st * R::kBlocks + x)) & 3u;
       const int ends = min(len, blk1 * kC4Block) - at * kC4Block;  // the share's keys from here on
-      const bool full = miss == 0 && ends >= 2 * kC4Block;
+      int key0[2] = {0, 0};  // (kWin) the blocks' first keys
+      bool full;
       bool live[2][2];
+      if constexpr (kWin) {
+        key0[0] = view.block(at) * kC4Block;
+        key0[1] = view.block(at + 1) * kC4Block;
+        full = miss == 0 && at + 1 < blk1 && view.whole(key0[0] / kC4Block) && view.whole(key0[1] / kC4Block);
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int z = 0; z < 2; ++z)
-          live[y][z] = !((miss >> y) & 1) && y * kC4Block + slot_i + 8 * z < ends;
+          for (int z = 0; z < 2; ++z)
+            live[y][z] = !((miss >> y) & 1) && at + y < blk1 && view.key(key0[y] + slot_i + 8 * z);
+      } else {
+        full = miss == 0 && ends >= 2 * kC4Block;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            live[y][z] = !((miss >> y) & 1) && y * kC4Block + slot_i + 8 * z < ends;
+      }
       if (!full) {
         asm volatile("" ::: "memory");  // a branch, not selects in every iteration
 #pragma unroll
@@ -546,8 +597,12 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            if (mine <= y * kC4Block + 8 * z) continue;
-            float* dst = score + (y * kC4Block + 8 * z) * a.group;
+            if constexpr (kWin) {
+              if (at + y >= blk1 || key0[y] + slot_i + 8 * z >= len) continue;
+            } else {
+              if (mine <= y * kC4Block + 8 * z) continue;
+            }
+            float* dst = score + ((kWin ? (size_t)key0[y] : (size_t)(y * kC4Block)) + 8 * z) * a.group;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const int col = nt * 8 + 2 * t;
@@ -561,7 +616,7 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
               }
             }
           }
-        score += 2 * kC4Block * a.group;
+        if (!kWin) score += 2 * kC4Block * a.group;
       }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -712,9 +767,8 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
     if (left > 0 && ++row == rows_per) {
       row = 0;
       do {
-        len = seq_len(a, ++row_b);  // the share ends inside the list
-      } while (len == 0);
-      nb = (len + kC4Block - 1) / kC4Block;
+        view = seq_view<kWin>(a, ++row_b);  // the share ends inside the list
+      } while (view.len == 0);
     }
   }
   if constexpr (kOwn) {
@@ -749,10 +803,11 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
       // the weights of the row's keys: the scores and sums are the block's own
       __syncthreads();
       const size_t bh = (size_t)row_b * a.Hkv + hk;
-      for (int j = threadIdx.x; j < len; j += kW * 32) {
+      for (int j = threadIdx.x; j < view.len; j += kW * 32) {
         const float* src = a.scores + (bh * a.cap + j) * a.group;
         float sum = 0.f;
-        for (int h = 0; h < a.group; ++h) {
+        const int heads_seen = view.key(j) ? a.group : 0;
+        for (int h = 0; h < heads_seen; ++h) {
           const float z = a.lse2[out0 + h];
           sum += z == -INFINITY ? 0.f : ex2_mufu(src[h] - z);
         }
@@ -807,13 +862,16 @@ __device__ float2 join_ml(const AttendArgs& a, const RowSpan& s, int col) {
 
 // w_out = w_in + sum over the group of 2^(score - log2 sum), for kWeightKeys keys of
 // a (sequence, kv head).  The scores are on their way while the sums of rows that
-// shares cut are joined, a warp per query head.
-template <int NT, int kW>
+// shares cut are joined, a warp per query head.  Keys out of sight (kWin) have no score and
+// add nothing.
+template <int NT, int kW, bool kWin>
 __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_lse2) {
   constexpr int kPer = kWeightKeys / (kW * 32);
   const int units = (a.cap + kWeightKeys - 1) / kWeightKeys;
   const int bh = unit / units, first = (unit - bh * units) * kWeightKeys;
-  const int b = bh / a.Hkv, hk = bh - b * a.Hkv, len = seq_len(a, b), j0 = first + threadIdx.x;
+  const int b = bh / a.Hkv, hk = bh - b * a.Hkv, j0 = first + threadIdx.x;
+  const View<kWin> view = seq_view<kWin>(a, b);
+  const int len = view.len;
   if (first >= len) return;
   const float* src = a.scores + ((size_t)bh * a.cap + j0) * a.group;
   const size_t step = (size_t)kW * 32 * a.group, at = (size_t)bh * a.w_stride + j0;
@@ -825,9 +883,10 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_ls
     s[x] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     w[x] = 0.f;
     if (j0 + x * kW * 32 >= len) continue;
+    if (a.w_in) w[x] = a.w_in[at + x * kW * 32];
+    if (kWin && !view.key(j0 + x * kW * 32)) continue;
     if (four) s[x] = *reinterpret_cast<const float4*>(src + x * step);
     else s[x].x = src[x * step];
-    if (a.w_in) w[x] = a.w_in[at + x * kW * 32];
   }
   for (int h = threadIdx.x >> 5; h < a.group; h += kW) {
     const int tile = h / (8 * NT), col = h - tile * 8 * NT;
@@ -847,7 +906,9 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_ls
   for (int x = 0; x < kPer; ++x) {
     if (j0 + x * kW * 32 >= len) break;
     float sum = 0.f;
-    if (four) {
+    if (kWin && !view.key(j0 + x * kW * 32)) {
+      // (nothing)
+    } else if (four) {
       float4 y = s[x];
       for (int h = 0;;) {
         sum += (ex2_mufu(y.x - s_lse2[h]) + ex2_mufu(y.y - s_lse2[h + 1])) +
@@ -869,7 +930,7 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_ls
 // cut into many parts; with weights or without, so that O has the same bits.  A block
 // is a chain of dependent loads, so what counts is how many are resident: 32 warps
 // per SM with 64 registers a thread, for 20 with 95 (1 us less).
-template <int D, int NT, int kW>
+template <int D, int NT, int kW, bool kWin>
 __global__ void __launch_bounds__(kW * 32, 32 / kW) join_kernel(const AttendArgs a, int units) {
   constexpr int kV = D / 32;
   __shared__ float s_o[kW][D];
@@ -878,7 +939,7 @@ __global__ void __launch_bounds__(kW * 32, 32 / kW) join_kernel(const AttendArgs
   grid_dep_launch();
   if ((int)blockIdx.x < units) {
     __shared__ float s_lse2[128];
-    weigh<NT, kW>(a, blockIdx.x, s_lse2);
+    weigh<NT, kW, kWin>(a, blockIdx.x, s_lse2);
     return;
   }
   const int out = blockIdx.x - units;  // (sequence, query head)
@@ -961,7 +1022,8 @@ AttendLayout attend_layout(int B, int Hq, int Hkv, int D, int cap, int sms) {
   return L;
 }
 
-template <int D, int NT>
+// slots: those that a sequence's query can see, by the table and the window
+template <int D, int NT, bool kWin>
 int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) {
   constexpr int kSmem = kWarps * Ring<D>::kStages * Ring<D>::kBytes;
   constexpr int kOwnSmem = kOwnWarps * Ring<D>::kStages * Ring<D>::kBytes;
@@ -970,9 +1032,9 @@ int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) 
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (!attr_done[dev]) {
-    if (cudaFuncSetAttribute(attend_kernel<D, NT, false>,
+    if (cudaFuncSetAttribute(attend_kernel<D, NT, false, kWin>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(attend_kernel<D, NT, true>,
+        cudaFuncSetAttribute(attend_kernel<D, NT, true, kWin>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
@@ -982,7 +1044,7 @@ int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) 
   if (slots <= kOwnBlocks * kC4Block && a.tiles == 1 &&
       own_rows <= (long long)kOwnRowsPerSm<D, NT> * sms) {
     record_timing(false, stream);
-    if (launch_pdl(attend_kernel<D, NT, true>, dim3((unsigned)own_rows), dim3(kOwnWarps * 32),
+    if (launch_pdl(attend_kernel<D, NT, true, kWin>, dim3((unsigned)own_rows), dim3(kOwnWarps * 32),
                    kOwnSmem, stream, a) != cudaSuccess)
       return FA_ERR_CUDA;
     record_timing(true, stream);
@@ -990,14 +1052,14 @@ int launch_attend(const AttendArgs& a, int slots, int sms, cudaStream_t stream) 
     return FA_OK;
   }
   record_timing(false, stream);
-  if (launch_pdl(attend_kernel<D, NT, false>, dim3(a.n_warps / kWarps), dim3(kWarps * 32), kSmem,
+  if (launch_pdl(attend_kernel<D, NT, false, kWin>, dim3(a.n_warps / kWarps), dim3(kWarps * 32), kSmem,
                  stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
   record_timing(true, stream);
   const int rows = a.B * a.Hq;
   const int units = a.scores ? a.B * a.Hkv * ((a.cap + kWeightKeys - 1) / kWeightKeys) : 0;
   const int warps = rows >= 1024 ? 4 : 8;
-  const auto join = warps == 4 ? join_kernel<D, NT, 4> : join_kernel<D, NT, 8>;
+  const auto join = warps == 4 ? join_kernel<D, NT, 4, kWin> : join_kernel<D, NT, 8, kWin>;
   if (launch_pdl(join, dim3((unsigned)units + (unsigned)rows), dim3(warps * 32), 0, stream, a, units) != cudaSuccess)
     return FA_ERR_CUDA;
   note_launches(2);
@@ -1027,10 +1089,21 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
                      int D, const int* cache_lens, const int* page_table, int table_width,
                      float scale, const float* weights_in, float* weights_out, int weight_slots,
                      void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  return fa_cache4_attend_sink(q, q_batch_stride, q_head_stride, cache, num_pages, page_size, o, lse, B,
+                               Hq, Hkv, D, cache_lens, page_table, table_width, -1, 0, scale, weights_in,
+                               weights_out, weight_slots, workspace, workspace_bytes, stream);
+}
+
+int fa_cache4_attend_sink(const void* q, int64_t q_batch_stride, int64_t q_head_stride,
+                          const void* cache, int num_pages, int page_size, void* o, float* lse, int B,
+                          int Hq, int Hkv, int D, const int* cache_lens, const int* page_table,
+                          int table_width, int window_left, int sinks, float scale,
+                          const float* weights_in, float* weights_out, int weight_slots,
+                          void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   reset_launches();
   int rc = check_cache4(num_pages, Hkv, D, page_size, B, table_width);
   if (rc) return rc;
-  if (Hq < 1 || Hq % Hkv != 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (Hq < 1 || Hq % Hkv != 0 || !std::isfinite(scale) || sinks < 0) return FA_ERR_INVALID_ARG;
   if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
   if ((long long)B * Hq > (1LL << 30)) return FA_ERR_INVALID_ARG;
   if (weights_out && (long long)B * Hkv * (weight_slots / kWeightKeys + 1) > (1LL << 30))
@@ -1084,11 +1157,25 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
   a.w_out = weights_out;
   a.w_stride = weight_slots;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // a window that hides a key of some length the table allows
+  if (window_left >= 0 && window_left < slots - 1 && sinks < slots - 1 - window_left) {
+    a.wl = window_left;
+    a.sinks = sinks;
+    // wl + 1 keys lie in at most (wl + 15) / 16 + 1 blocks
+    const long long seen =
+        ((sinks + kC4Block - 1LL) / kC4Block + (window_left + kC4Block - 1LL) / kC4Block + 1) * kC4Block;
+    const int most = (int)(seen < slots ? seen : slots);
+    if (D == 128)
+      return nt == 1 ? launch_attend<128, 1, true>(a, most, info.sm_count, st)
+                     : launch_attend<128, 2, true>(a, most, info.sm_count, st);
+    return nt == 1 ? launch_attend<64, 1, true>(a, most, info.sm_count, st)
+                   : launch_attend<64, 2, true>(a, most, info.sm_count, st);
+  }
   if (D == 128)
-    return nt == 1 ? launch_attend<128, 1>(a, slots, info.sm_count, st)
-                   : launch_attend<128, 2>(a, slots, info.sm_count, st);
-  return nt == 1 ? launch_attend<64, 1>(a, slots, info.sm_count, st)
-                 : launch_attend<64, 2>(a, slots, info.sm_count, st);
+    return nt == 1 ? launch_attend<128, 1, false>(a, slots, info.sm_count, st)
+                   : launch_attend<128, 2, false>(a, slots, info.sm_count, st);
+  return nt == 1 ? launch_attend<64, 1, false>(a, slots, info.sm_count, st)
+                 : launch_attend<64, 2, false>(a, slots, info.sm_count, st);
 }
 
 }  // extern "C"

@@ -113,7 +113,8 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
 /*
  * Synchronises `stream`, returns FA_OK or FA_ERR_TIMEOUT if any forward launch on
  * this device since the previous call recorded a timed-out wait (FA_ERR_INVALID_ARG
- * if fa_fwd_varlen found its boundaries out of order), and clears the record.
+ * if fa_fwd_varlen found its boundaries out of order, or fa_norm_rope_* a position past
+ * its tables), and clears the record.
  * FA_ERR_CUDA if the synchronisation itself fails.
  */
 int fa_fwd_status(fa_stream_t stream);
@@ -357,6 +358,47 @@ int fa_cache4_append(void* cache, int num_pages, int page_size, const void* k, c
                      const int* page_table, int table_width, fa_stream_t stream);
 
 /*
+ * fa_cache4_append by slots: token i (row i of k and v) goes to slot slots[i] of the whole
+ * cache, page * page_size + its place there (device int64 [T], as fa_page_update gives them);
+ * a negative one is not stored, one past the last page is recorded and not stored.  Tokens
+ * that are stored have slots of their own.
+ */
+int fa_cache4_append_slots(void* cache, int num_pages, int page_size, const void* k, const void* v,
+                           const fa_packed_stride* k_stride, const fa_packed_stride* v_stride, int T,
+                           int Hkv, int D, const int64_t* slots, fa_stream_t stream);
+
+/*
+ * Page tables for the lengths that the sequences are about to have.  lens, new_lens: device
+ * int32 [B], the tokens held and to be held (0 for a sequence that has not begun, or has
+ * ended); free_pages: a stack of page ids, device int32 [num_pages], its lowest free_count[0]
+ * (device int32 [1]) filled.  With n0 = ceil(lens / page_size), n1 = ceil(new_lens /
+ * page_size), an entry e of a sequence's table is hidden where window_left >= 0,
+ * (e + 1) page_size <= new_lens - 1 - window_left and e page_size >= sinks: no query from
+ * the last token on sees its tokens.
+ *   - entries e < n0 that hold a page (of [0, num_pages)) and are hidden, or e >= n1, give
+ *     it back: it goes on top of the stack, in the order of (sequence, entry); they become -1;
+ *   - entries n0 <= e < n1 that are not hidden then take pages from the top, in that order,
+ *     -1 where the stack is empty, which is recorded;
+ *   - the other entries stay as they are.  free_count is what the stack then holds, and
+ *     its elements above keep what the call wrote there.
+ * The new tokens (lens .. new_lens - 1) of all sequences, packed in order, have rows
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]), positions int32 [T], counted in
+ * their sequence, and slots int64 [T], page * page_size + position % page_size, or -1 where
+ * their entry has no page.  T is the rows there are: tokens past it are recorded and left
+ * out, rows past the tokens get -1 in both.  lens is not changed: the caller copies new_lens
+ * there once the tokens are stored.  A length outside [0, table_width * page_size] or a
+ * free_count outside [0, num_pages] is cut and recorded; fa_cache4_status returns
+ * FA_ERR_INVALID_ARG for all of these.
+ * page_size 16, 32, 64 or 128; 1 <= B <= 65536; B * table_width below 2^30, num_pages at most
+ * 2^30; int32 arrays 4-byte, slots 8-byte aligned.  One launch, no workspace; calls on
+ * the same tables or stack follow one another.
+ */
+int fa_page_update(int* page_table, int table_width, int* free_pages, int* free_count,
+                   int num_pages, const int* lens, const int* new_lens, int B, int page_size,
+                   int window_left, int sinks, int T, int* cu_seqlens, int* positions,
+                   int64_t* slots, fa_stream_t stream);
+
+/*
  * The stored values of slots first[b] .. first[b] + count[b] - 1 of every sequence
  * (first null: from 0), as k, v [B, Hkv, S, D] bf16 (contiguous, 16-byte aligned,
  * rounded to nearest from the fp32 value); rows from count[b] on are zero.
@@ -392,6 +434,20 @@ int fa_cache4_attend(const void* q, int64_t q_batch_stride, int64_t q_head_strid
                      void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * fa_cache4_attend under a window with sinks: of a sequence of n tokens its query (the
+ * last token's) sees slots j >= n - 1 - window_left and j < sinks (window_left negative:
+ * all; sinks >= 0).  Pages that hold none of these are not looked up, so their entries in
+ * the table may hold anything.  weights_out of the others: weights_in's, or 0 where that
+ * is null.  Everything else as in fa_cache4_attend, the workspace too.
+ */
+int fa_cache4_attend_sink(const void* q, int64_t q_batch_stride, int64_t q_head_stride,
+                          const void* cache, int num_pages, int page_size, void* o, float* lse, int B,
+                          int Hq, int Hkv, int D, const int* cache_lens, const int* page_table,
+                          int table_width, int window_left, int sinks, float scale,
+                          const float* weights_in, float* weights_out, int weight_slots,
+                          void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * Keeps at most `budget` tokens of every (sequence, kv head): the latest `recent`
  * ones and, of the others, those with the largest weights [B, Hkv, cap] (ties: the
  * lowest slot first; weights are not NaN).  The kept tokens' codes are copied
@@ -417,6 +473,60 @@ int fa_cache4_evict(void* cache, int num_pages, int page_size, const float* weig
  * synchronisation fails.
  */
 int fa_cache4_status(fa_stream_t stream);
+
+/*
+ * RMS norms of every query and key head and their rotation by position, in one pass, before
+ * attention (the pages begin behind it).  Per row x of D elements, weights w [D]:
+ *   r = 1 / sqrt(mean_d x_d^2 + eps),  n_d = x_d r w_d, and of the first `rot` elements the
+ *   pairs (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) where interleaved != 0, i < rot / 2:
+ *   y_a = n_a cos[p][i] - n_b sin[p][i],  y_b = n_b cos[p][i] + n_a sin[p][i];  y_d = n_d beyond
+ * in fp32, rounded once to bf16.
+ *   q [T, Hq, D], k [T, Hkv, D] bf16, rows and heads apart by *_stride (multiples of 8
+ *     elements; null: contiguous), and q_out, k_out likewise (at least D apart); q_out may be
+ *     q itself and k_out k, with the same strides;
+ *   q_weight, k_weight [D], fp32, or bf16 where weight_bf16 != 0;
+ *   cos, sin [table_rows, rot / 2] fp32, as fa_rope_table fills them, or scaled ones;
+ *   positions: device int32 [T].  A negative one marks a token of no sequence, whose rows are
+ *     not written (zero_skipped != 0: become zeros); one from table_rows on counts as such
+ *     and is recorded: fa_fwd_status returns FA_ERR_INVALID_ARG.
+ * T >= 0; D in {64, 128}; rot a multiple of 16 up to D; eps >= 0 (a row of zeros with eps 0
+ * is NaN); Hq, Hkv at most 2^20 and T (Hq / 8 + Hkv / 8 + 2) below 2^31.  Tensors 16-byte
+ * aligned, positions 4-byte.
+ */
+int fa_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                     const void* k_weight, int weight_bf16, const float* cos, const float* sin,
+                     const int* positions, int T, int Hq, int Hkv, int D, int table_rows, int rot,
+                     int interleaved, float eps, const fa_packed_stride* q_stride,
+                     const fa_packed_stride* k_stride, const fa_packed_stride* q_out_stride,
+                     const fa_packed_stride* k_out_stride, int zero_skipped, fa_stream_t stream);
+
+/*
+ * Its backward pass, from the inputs of the forward call and the gradients dq_out, dk_out of
+ * its results: dq, dk bf16 (strides as q_out's; they may be slices of one gradient, or
+ * dq_out and dk_out themselves) and the weights' gradients dq_weight, dk_weight [D] fp32,
+ * summed over all rows in a fixed order: repeated runs give the same bits.  Rows of no
+ * sequence add nothing and are treated as in the forward call.  With T == 0 the weights'
+ * gradients are zero.
+ * workspace: fa_norm_rope_workspace_bytes(...) bytes on the current device, 16-byte aligned,
+ * uninitialised; calls that may run at the same time need one each.
+ */
+size_t fa_norm_rope_workspace_bytes(int T, int Hq, int Hkv, int D);
+int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq,
+                     void* dk, float* dq_weight, float* dk_weight, const void* q_weight,
+                     const void* k_weight, int weight_bf16, const float* cos, const float* sin,
+                     const int* positions, int T, int Hq, int Hkv, int D, int table_rows, int rot,
+                     int interleaved, float eps, const fa_packed_stride* q_stride,
+                     const fa_packed_stride* k_stride, const fa_packed_stride* dq_out_stride,
+                     const fa_packed_stride* dk_out_stride, const fa_packed_stride* dq_stride,
+                     const fa_packed_stride* dk_stride, int zero_skipped, void* workspace,
+                     size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * cos and sin [positions, rot / 2] of p base^(-2 i / rot), the angles taken in fp64 and the
+ * results rounded to fp32.  positions >= 1; rot a multiple of 16 up to 128; base > 0.
+ */
+int fa_rope_table(float* cos, float* sin, int64_t positions, int rot, double base,
+                  fa_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char* fa_status_string(int status);
