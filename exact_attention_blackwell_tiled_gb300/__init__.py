@@ -489,15 +489,18 @@ def _var_window(causal, window):
     return int(window[0]), int(window[1])
 
 
+def _left(window_left):
+    """A window's left side for the C ABI: -1 for none; a C int would not hold the largest."""
+    return -1 if window_left is None else max(-1, min(int(window_left), 2 ** 31 - 1))
+
+
 def varlen_workspace_bytes(B, T, Hq, Hkv, D, backward=False, deterministic=False, window=None,
                            sinks: int = 0) -> int:
     """Workspace bytes of fwd_varlen or bwd_varlen; a backward with ``sinks`` takes more, by
     its ``window``."""
-    wl = _var_window(False, window)[0]
-    # (a ctypes int would wrap; lengths stay below 2^31)
     return int(lib().fa_varlen_sink_workspace_bytes(
         B, T, Hq, Hkv, D, int(bool(backward)), int(bool(deterministic)),
-        max(-1, min(wl, 2 ** 31 - 1)), int(sinks)))
+        _left(_var_window(False, window)[0]), int(sinks)))
 
 
 def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -702,8 +705,7 @@ def page_update(page_table: torch.Tensor, free_pages: torch.Tensor, free_count: 
     cache4_status() reports a pool or T that was too small, and lengths past the table.
     """
     return _compiled().page_update(page_table, free_pages, free_count, lens, new_lens, page_size, T,
-                                   -1 if window_left is None else window_left, sinks, cu_seqlens,
-                                   positions, slots, stream)
+                                   _left(window_left), sinks, cu_seqlens, positions, slots, stream)
 
 
 def cache4_read(cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tensor | None,
@@ -740,9 +742,8 @@ def cache4_attend(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     before it and the first ``sinks``; the pages of the others are not looked up.
     Returns (o [B,Hq,D] bf16, lse [B,Hq] fp32); o = 0, lse = -inf without tokens.
     """
-    wl = -1 if window_left is None else max(-1, min(int(window_left), 2 ** 31 - 1))
     return _compiled().cache4_attend(q, cache, page_table, cache_lens, scale, weights, weights_out,
-                                     out, lse, workspace, stream, wl, sinks)
+                                     out, lse, workspace, stream, _left(window_left), sinks)
 
 
 def cache4_evict(cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torch.Tensor,

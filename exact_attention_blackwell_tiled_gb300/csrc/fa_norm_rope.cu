@@ -1,0 +1,566 @@
+// fa_norm_rope.cu -- RMS norms of every query and key head and the rotation of both by
+// position, in one pass, and its backward pass.
+//
+//   r = 1 / sqrt(mean_d x_d^2 + eps),  n_d = x_d r w_d,
+//   pairs (a, b) of the first `rot` elements at position p, angle index i:
+//     y_a = n_a cos_pi - n_b sin_pi,  y_b = n_b cos_pi + n_a sin_pi,  else y_d = n_d
+//   backward, g the rotation of dy by the negative angle, h = g w:
+//     dw_d = sum over rows g_d x_d r,   dx = r (h - x r^2 mean_d(h x))
+// in fp32 throughout; y and dx are rounded once, to bf16.
+//
+// Memory bounds it: 4 D bytes per head forward, 6 D backward, against some 12 and 30
+// operations an element.  A lane holds 16 elements of a row, so that a pair's two lie in
+// one lane: halves paired (a, a + rot / 2): 8 elements of each half, two 16-byte pieces;
+// neighbours paired: 16 in a row.  A row is then D / 16 lanes, a warp holds 8 or 4 rows, and
+// takes 8 heads of one token, so that cosines, sines and weights are loaded once for
+// them.  dw: sums per lane over all rows that it meets, then over the lanes and warps of
+// a block in shared memory; a second kernel adds the blocks', always in the same order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kHeads = 8;       // heads of a token that a warp takes at a time
+constexpr int kGradBlocks = 2;  // of the backward kernel per SM
+
+struct Rows {
+  const __nv_bfloat16* x;
+  long long token, head;  // elements apart
+};
+struct RowsOut {
+  __nv_bfloat16* x;
+  long long token, head;
+};
+
+struct NormRopeArgs {
+  Rows in[2], dy[2];  // q, k; the gradients of the results
+  RowsOut out[2];     // the results, or the inputs' gradients
+  const void* w[2];
+  int w_bf16;
+  const float *cos, *sin;  // [P, rot / 2]
+  const int* pos;          // [T]
+  int T, H[2], P, rot;
+  int zero;  // rows of no sequence get zeros
+  float eps;
+  int* status;
+  float* part;    // [blocks, 2, D] sums of dw
+  float* dw[2];   // [D]
+  int blocks;
+};
+
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
+  uint4 x;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(p));
+  return x;
+}
+
+// Eight bf16 numbers as pairs of fp32.
+__device__ __forceinline__ void widen(const uint4& x, float2 (&f)[4]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 narrow(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+}
+
+// What a lane holds of a row: elements a0 .. a0 + 7 and b0 .. b0 + 7.
+template <int D, bool kPairs>
+struct Lane {
+  static constexpr int kPerRow = D / 16;       // lanes
+  static constexpr int kRows = 32 / kPerRow;   // rows of a warp
+  static constexpr int kSteps = kHeads / kRows < 1 ? 1 : kHeads / kRows;
+  int l, sub, a0, b0;
+  bool turns;  // the lane's elements are rotated
+  __device__ __forceinline__ Lane(int rot) {
+    const int lane = threadIdx.x & 31;
+    l = lane % kPerRow;
+    sub = lane / kPerRow;
+    turns = 16 * l < rot;
+    a0 = kPairs || !turns ? 16 * l : 8 * l;
+    b0 = kPairs || !turns ? 16 * l + 8 : 8 * l + rot / 2;
+  }
+};
+
+// 8 numbers at p, fp32 or bf16.
+__device__ __forceinline__ void load_weights(const void* w, int bf16, int at, float2 (&f)[4]) {
+  if (bf16) {
+    widen(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + at), f);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+    const float4 x = p[0], y = p[1];
+    f[0] = make_float2(x.x, x.y), f[1] = make_float2(x.z, x.w);
+    f[2] = make_float2(y.x, y.y), f[3] = make_float2(y.z, y.w);
+  }
+}
+
+// The lane's cosines and sines at position p: of its 8 pairs.
+template <int D, bool kPairs>
+__device__ __forceinline__ void load_angles(const NormRopeArgs& a, const Lane<D, kPairs>& L, int p,
+                                            float2 (&c)[4], float2 (&s)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] = make_float2(1.f, 1.f), s[e] = make_float2(0.f, 0.f);
+  if (!L.turns) return;
+  const size_t at = (size_t)p * (a.rot / 2) + 8 * L.l;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float4 x = *reinterpret_cast<const float4*>(a.cos + at + 4 * y);
+    const float4 z = *reinterpret_cast<const float4*>(a.sin + at + 4 * y);
+    c[2 * y] = make_float2(x.x, x.y), c[2 * y + 1] = make_float2(x.z, x.w);
+    s[2 * y] = make_float2(z.x, z.y), s[2 * y + 1] = make_float2(z.z, z.w);
+  }
+}
+
+// Rotates the lane's 8 pairs by the angle (kBack: its negative).  Halves: (a, b) element by
+// element.  Neighbours: pair e of a's four uses angle e, of b's 4 + e.
+template <bool kPairs, bool kBack>
+__device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const float2 (&c)[4],
+                                     const float2 (&s)[4]) {
+  if constexpr (kPairs) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float ca = (e & 1) ? c[e / 2].y : c[e / 2].x, sa = (e & 1) ? s[e / 2].y : s[e / 2].x;
+      const float cb = (e & 1) ? c[2 + e / 2].y : c[2 + e / 2].x;
+      const float sb = (e & 1) ? s[2 + e / 2].y : s[2 + e / 2].x;
+      const float2 x = a[e], y = b[e];
+      const float ta = kBack ? -sa : sa, tb = kBack ? -sb : sb;
+      a[e] = make_float2(fmaf(x.x, ca, -x.y * ta), fmaf(x.y, ca, x.x * ta));
+      b[e] = make_float2(fmaf(y.x, cb, -y.y * tb), fmaf(y.y, cb, y.x * tb));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = kBack ? make_float2(-s[e].x, -s[e].y) : s[e];
+      const float2 n = make_float2(-t.x, -t.y);
+      const float2 x = a[e], y = b[e];
+      a[e] = __ffma2_rn(x, c[e], __fmul2_rn(y, n));
+      b[e] = __ffma2_rn(y, c[e], __fmul2_rn(x, t));
+    }
+  }
+}
+
+// Token of a unit's rows: -1 where it is of no sequence, or its position has no angles.
+__device__ __forceinline__ int position(const NormRopeArgs& a, int token) {
+  const int p = __ldg(a.pos + token);
+  if (p >= a.P && (threadIdx.x & 31) == 0) atomicExch(a.status, (int)FA_ERR_INVALID_ARG);
+  return p < a.P ? p : -1;
+}
+
+template <int D, bool kPairs>
+__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeArgs a) {
+  using L = Lane<D, kPairs>;
+  const L lane(a.rot);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int units_q = (a.H[0] + kHeads - 1) / kHeads;
+  const int per_token = units_q + (a.H[1] + kHeads - 1) / kHeads;
+  const long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int token = (int)(u / per_token), part = (int)(u - (long long)token * per_token);
+  if (token >= a.T) return;
+  const int kind = part >= units_q ? 1 : 0;
+  const int h0 = (kind ? part - units_q : part) * kHeads;
+  const Rows& in = a.in[kind];
+  const RowsOut& out = a.out[kind];
+  uint4 xa[L::kSteps], xb[L::kSteps];
+#pragma unroll
+  for (int n = 0; n < L::kSteps; ++n) {
+    const int h = h0 + n * L::kRows + lane.sub;
+    xa[n] = xb[n] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < a.H[kind]) {
+      const __nv_bfloat16* row = in.x + token * in.token + h * in.head;
+      xa[n] = load16(row + lane.a0);
+      xb[n] = load16(row + lane.b0);
+    }
+  }
+  const int p = position(a, token);
+  if (p < 0 && !a.zero) return;
+  float2 c[4], s[4], wa[4], wb[4];
+  load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
+  load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
+  load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
+#pragma unroll
+  for (int n = 0; n < L::kSteps; ++n) {
+    const int h = h0 + n * L::kRows + lane.sub;
+    float2 fa_[4], fb[4], sum = make_float2(0.f, 0.f);
+    widen(xa[n], fa_);
+    widen(xb[n], fb);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum = __ffma2_rn(fa_[e], fa_[e], sum);
+      sum = __ffma2_rn(fb[e], fb[e], sum);
+    }
+    float ss = sum.x + sum.y;
+#pragma unroll
+    for (int o = L::kPerRow / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+    const float2 r2 = make_float2(r, r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      fa_[e] = __fmul2_rn(__fmul2_rn(fa_[e], r2), wa[e]);
+      fb[e] = __fmul2_rn(__fmul2_rn(fb[e], r2), wb[e]);
+    }
+    if (lane.turns) turn<kPairs, false>(fa_, fb, c, s);
+    if (h < a.H[kind]) {
+      __nv_bfloat16* row = out.x + token * out.token + h * out.head;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(row + lane.a0) = p < 0 ? zero : narrow(fa_);
+      *reinterpret_cast<uint4*>(row + lane.b0) = p < 0 ? zero : narrow(fb);
+    }
+  }
+}
+
+// A persistent grid: its warps walk q's units, then k's, and sum dw as they go.
+template <int D, bool kPairs>
+__global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
+  using L = Lane<D, kPairs>;
+  __shared__ float s_dw[kWarps][D];
+  const L lane(a.rot);
+  const int warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const Rows &in = a.in[kind], &dy = a.dy[kind];
+    const RowsOut& out = a.out[kind];
+    const int H = a.H[kind], per_token = (H + kHeads - 1) / kHeads;
+    const long long units = (long long)a.T * per_token;
+    float2 wa[4], wb[4], da[4], db[4];
+    load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
+    load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (long long u = (long long)warp * gridDim.x + blockIdx.x; u < units; u += (long long)kWarps * gridDim.x) {
+      const int token = (int)(u / per_token), h0 = (int)(u - (long long)token * per_token) * kHeads;
+      uint4 xa[L::kSteps], xb[L::kSteps], ga[L::kSteps], gb[L::kSteps];
+#pragma unroll
+      for (int n = 0; n < L::kSteps; ++n) {
+        const int h = h0 + n * L::kRows + lane.sub;
+        xa[n] = xb[n] = ga[n] = gb[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < H) {
+          const __nv_bfloat16* row = in.x + token * in.token + h * in.head;
+          const __nv_bfloat16* grad = dy.x + token * dy.token + h * dy.head;
+          xa[n] = load16(row + lane.a0);
+          xb[n] = load16(row + lane.b0);
+          ga[n] = load16(grad + lane.a0);
+          gb[n] = load16(grad + lane.b0);
+        }
+      }
+      const int p = position(a, token);
+      if (p < 0 && !a.zero) continue;
+      float2 c[4], s[4];
+      load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
+#pragma unroll
+      for (int n = 0; n < L::kSteps; ++n) {
+        const int h = h0 + n * L::kRows + lane.sub;
+        float2 fa_[4], fb[4], ha[4], hb[4];
+        widen(xa[n], fa_);
+        widen(xb[n], fb);
+        widen(ga[n], ha);
+        widen(gb[n], hb);
+        if (lane.turns) turn<kPairs, true>(ha, hb, c, s);
+        // sums of x^2 and of h x, h = g w
+        float2 sx = make_float2(0.f, 0.f), sh = make_float2(0.f, 0.f);
+        float2 ta[4], tb[4];  // g x
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sx = __ffma2_rn(fa_[e], fa_[e], sx);
+          sx = __ffma2_rn(fb[e], fb[e], sx);
+          ta[e] = __fmul2_rn(ha[e], fa_[e]);
+          tb[e] = __fmul2_rn(hb[e], fb[e]);
+          sh = __ffma2_rn(ta[e], wa[e], sh);
+          sh = __ffma2_rn(tb[e], wb[e], sh);
+        }
+        float ss = sx.x + sx.y, hx = sh.x + sh.y;
+#pragma unroll
+        for (int o = L::kPerRow / 2; o > 0; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          hx += __shfl_xor_sync(0xffffffffu, hx, o);
+        }
+        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        if (p < 0 || h >= H) {
+          if (h < H) {
+            __nv_bfloat16* row = out.x + token * out.token + h * out.head;
+            *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          continue;
+        }
+        const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
+        const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          da[e] = __ffma2_rn(ta[e], r2, da[e]);
+          db[e] = __ffma2_rn(tb[e], r2, db[e]);
+          ha[e] = __ffma2_rn(__fmul2_rn(ha[e], wa[e]), r2, __fmul2_rn(fa_[e], m2));
+          hb[e] = __ffma2_rn(__fmul2_rn(hb[e], wb[e]), r2, __fmul2_rn(fb[e], m2));
+        }
+        __nv_bfloat16* row = out.x + token * out.token + h * out.head;
+        *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ha);
+        *reinterpret_cast<uint4*>(row + lane.b0) = narrow(hb);
+      }
+    }
+    // the warp's sums over its rows, then the block's over its warps
+#pragma unroll
+    for (int o = L::kPerRow; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        da[e].x += __shfl_xor_sync(0xffffffffu, da[e].x, o);
+        da[e].y += __shfl_xor_sync(0xffffffffu, da[e].y, o);
+        db[e].x += __shfl_xor_sync(0xffffffffu, db[e].x, o);
+        db[e].y += __shfl_xor_sync(0xffffffffu, db[e].y, o);
+      }
+    __syncthreads();
+    if (lane.sub == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2*>(&s_dw[warp][lane.a0 + 2 * e]) = da[e];
+        *reinterpret_cast<float2*>(&s_dw[warp][lane.b0 + 2 * e]) = db[e];
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s_dw[w][threadIdx.x];
+      a.part[((size_t)blockIdx.x * 2 + kind) * D + threadIdx.x] = sum;
+    }
+  }
+}
+
+// dw from the blocks' sums: 32 of the 2 D columns a block, 32 warps over the rows.
+template <int D>
+__global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const NormRopeArgs a) {
+  __shared__ float s_sum[32][33];
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int b = warp; b < a.blocks; b += 32) sum += a.part[(size_t)b * 2 * D + col];
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  // column `warp` of the block's, its 32 partial sums a lane each
+  float x = s_sum[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0) {
+    const int at = blockIdx.x * 32 + warp;
+    a.dw[at / D][at % D] = x;
+  }
+}
+
+// cos and sin of p base^(-2 i / rot), the angle in 64 bits: at p = 131071 fp32 would hold
+// it to 2^-7 only.
+__global__ void __launch_bounds__(256) rope_table_kernel(float* cos_, float* sin_, long long n, int half,
+                                                         double log_base) {
+  grid_dep_wait();
+  grid_dep_launch();
+  for (long long x = (long long)blockIdx.x * 256 + threadIdx.x; x < n; x += (long long)gridDim.x * 256) {
+    const long long p = x / half;
+    const int i = (int)(x - p * half);
+    double s, c;
+    sincos((double)p * exp(-log_base * i / half), &s, &c);
+    cos_[x] = (float)c;
+    sin_[x] = (float)s;
+  }
+}
+
+bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+int check_shape(int T, int Hq, int Hkv, int D, int P, int rot, float eps) {
+  if (T < 0 || Hq < 1 || Hkv < 1 || P < 1 || !std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (rot < 16 || rot > D || rot % 16) return FA_ERR_INVALID_ARG;
+  // units of eight heads, and warps of blocks, are counted in 32 bits
+  if ((long long)T * (Hq / kHeads + Hkv / kHeads + 2) >= (1LL << 31) || Hq > (1 << 20) || Hkv > (1 << 20))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+// Rows and heads apart by non-negative multiples of 8 elements; outputs by D at least.
+int strides(const fa_packed_stride* s, int H, int D, bool written, long long* token, long long* head) {
+  *token = s ? (long long)s->token : (long long)H * D;
+  *head = s ? (long long)s->head : (long long)D;
+  const long long least = written ? D : 0;
+  if (*token < least || *head < least || *token > (1LL << 36) || *head > (1LL << 36))
+    return FA_ERR_INVALID_ARG;
+  return (*token & 7) || (*head & 7) ? FA_ERR_MISALIGNED : FA_OK;
+}
+
+int grad_blocks(int sms, int T, int Hq, int Hkv) {
+  const long long q = (long long)T * ((Hq + kHeads - 1) / kHeads), k = (long long)T * ((Hkv + kHeads - 1) / kHeads);
+  const long long most = ((q > k ? q : k) + kWarps - 1) / kWarps;
+  const long long grid = (long long)sms * kGradBlocks;
+  return (int)(most < grid ? (most > 0 ? most : 1) : grid);
+}
+
+template <typename... A>
+int launch(void (*kernel)(A...), long long grid, int threads, cudaStream_t stream, const NormRopeArgs& a) {
+  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, a) != cudaSuccess) return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
+
+}  // namespace
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+int fa_rope_table(float* cos, float* sin, int64_t positions, int rot, double base, fa_stream_t stream) {
+  reset_launches();
+  if (positions < 1 || positions > INT32_MAX || rot < 16 || rot > 128 || rot % 16 || !std::isfinite(base) ||
+      base <= 0.0)
+    return FA_ERR_INVALID_ARG;
+  if (!cos || !sin) return FA_ERR_INVALID_ARG;
+  if (misaligned(cos, 16) || misaligned(sin, 16)) return FA_ERR_MISALIGNED;
+  int rc = check_device();
+  if (rc) return rc;
+  const long long n = positions * (rot / 2), blocks = (n + 255) / 256;
+  if (launch_pdl(rope_table_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0,
+                 static_cast<cudaStream_t>(stream), cos, sin, n, rot / 2, std::log(base)) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
+
+int fa_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                     const void* k_weight, int weight_bf16, const float* cos, const float* sin,
+                     const int* positions, int T, int Hq, int Hkv, int D, int table_rows, int rot,
+                     int interleaved, float eps, const fa_packed_stride* q_stride,
+                     const fa_packed_stride* k_stride, const fa_packed_stride* q_out_stride,
+                     const fa_packed_stride* k_out_stride, int zero_skipped, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_shape(T, Hq, Hkv, D, table_rows, rot, eps);
+  if (rc) return rc;
+  NormRopeArgs a{};
+  if ((rc = strides(q_stride, Hq, D, false, &a.in[0].token, &a.in[0].head)) ||
+      (rc = strides(k_stride, Hkv, D, false, &a.in[1].token, &a.in[1].head)) ||
+      (rc = strides(q_out_stride, Hq, D, true, &a.out[0].token, &a.out[0].head)) ||
+      (rc = strides(k_out_stride, Hkv, D, true, &a.out[1].token, &a.out[1].head)))
+    return rc;
+  if (T == 0) return FA_OK;
+  for (const void* p : {q, k, (const void*)q_out, (const void*)k_out, q_weight, k_weight, (const void*)cos,
+                        (const void*)sin}) {
+    if (!p) return FA_ERR_INVALID_ARG;
+    if (misaligned(p, 16)) return FA_ERR_MISALIGNED;
+  }
+  if (!positions) return FA_ERR_INVALID_ARG;
+  if (misaligned(positions, 4)) return FA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  a.in[0].x = static_cast<const __nv_bfloat16*>(q);
+  a.in[1].x = static_cast<const __nv_bfloat16*>(k);
+  a.out[0].x = static_cast<__nv_bfloat16*>(q_out);
+  a.out[1].x = static_cast<__nv_bfloat16*>(k_out);
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.w_bf16 = weight_bf16 ? 1 : 0;
+  a.cos = cos;
+  a.sin = sin;
+  a.pos = positions;
+  a.T = T;
+  a.H[0] = Hq;
+  a.H[1] = Hkv;
+  a.P = table_rows;
+  a.rot = rot;
+  a.zero = zero_skipped ? 1 : 0;
+  a.eps = eps;
+  a.status = fwd_status_word();
+  if (!a.status) return FA_ERR_CUDA;
+  const long long units = (long long)T * ((Hq + kHeads - 1) / kHeads + (Hkv + kHeads - 1) / kHeads);
+  const auto kernel = D == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
+                               : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>);
+  return launch(kernel, (units + kWarps - 1) / kWarps, kWarps * 32, static_cast<cudaStream_t>(stream), a);
+}
+
+size_t fa_norm_rope_workspace_bytes(int T, int Hq, int Hkv, int D) {
+  if (check_shape(T, Hq, Hkv, D, 1, 16, 0.f) != FA_OK) return 0;
+  int dev;
+  DeviceInfo info;
+  const int sms = current_device(&dev, &info) ? info.sm_count : 0;
+  return sms < 1 ? 0 : (size_t)grad_blocks(sms, T, Hq, Hkv) * 2 * D * sizeof(float);
+}
+
+int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq,
+                     void* dk, float* dq_weight, float* dk_weight, const void* q_weight,
+                     const void* k_weight, int weight_bf16, const float* cos, const float* sin,
+                     const int* positions, int T, int Hq, int Hkv, int D, int table_rows, int rot,
+                     int interleaved, float eps, const fa_packed_stride* q_stride,
+                     const fa_packed_stride* k_stride, const fa_packed_stride* dq_out_stride,
+                     const fa_packed_stride* dk_out_stride, const fa_packed_stride* dq_stride,
+                     const fa_packed_stride* dk_stride, int zero_skipped, void* workspace,
+                     size_t workspace_bytes, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_shape(T, Hq, Hkv, D, table_rows, rot, eps);
+  if (rc) return rc;
+  NormRopeArgs a{};
+  if ((rc = strides(q_stride, Hq, D, false, &a.in[0].token, &a.in[0].head)) ||
+      (rc = strides(k_stride, Hkv, D, false, &a.in[1].token, &a.in[1].head)) ||
+      (rc = strides(dq_out_stride, Hq, D, false, &a.dy[0].token, &a.dy[0].head)) ||
+      (rc = strides(dk_out_stride, Hkv, D, false, &a.dy[1].token, &a.dy[1].head)) ||
+      (rc = strides(dq_stride, Hq, D, true, &a.out[0].token, &a.out[0].head)) ||
+      (rc = strides(dk_stride, Hkv, D, true, &a.out[1].token, &a.out[1].head)))
+    return rc;
+  if (!dq_weight || !dk_weight || !q_weight || !k_weight) return FA_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !k || !dq_out || !dk_out || !dq || !dk || !cos || !sin || !positions))
+    return FA_ERR_INVALID_ARG;
+  for (const void* p : {q, k, dq_out, dk_out, (const void*)dq, (const void*)dk, q_weight, k_weight,
+                        (const void*)cos, (const void*)sin})
+    if (misaligned(p, 16)) return FA_ERR_MISALIGNED;
+  if (misaligned(dq_weight, 4) || misaligned(dk_weight, 4) || misaligned(positions, 4)) return FA_ERR_MISALIGNED;
+  if (!workspace || misaligned(workspace, 16)) return FA_ERR_WORKSPACE;
+  if ((rc = check_device())) return rc;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
+  a.blocks = grad_blocks(info.sm_count, T, Hq, Hkv);
+  if (workspace_bytes < (size_t)a.blocks * 2 * D * sizeof(float)) return FA_ERR_WORKSPACE;
+  a.in[0].x = static_cast<const __nv_bfloat16*>(q);
+  a.in[1].x = static_cast<const __nv_bfloat16*>(k);
+  a.dy[0].x = static_cast<const __nv_bfloat16*>(dq_out);
+  a.dy[1].x = static_cast<const __nv_bfloat16*>(dk_out);
+  a.out[0].x = static_cast<__nv_bfloat16*>(dq);
+  a.out[1].x = static_cast<__nv_bfloat16*>(dk);
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.w_bf16 = weight_bf16 ? 1 : 0;
+  a.cos = cos;
+  a.sin = sin;
+  a.pos = positions;
+  a.T = T;
+  a.H[0] = Hq;
+  a.H[1] = Hkv;
+  a.P = table_rows;
+  a.rot = rot;
+  a.zero = zero_skipped ? 1 : 0;
+  a.eps = eps;
+  a.part = static_cast<float*>(workspace);
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  a.status = fwd_status_word();
+  if (!a.status) return FA_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const auto kernel =
+      D == 128 ? (interleaved ? norm_rope_grad_kernel<128, true> : norm_rope_grad_kernel<128, false>)
+               : (interleaved ? norm_rope_grad_kernel<64, true> : norm_rope_grad_kernel<64, false>);
+  if ((rc = launch(kernel, a.blocks, kWarps * 32, st, a))) return rc;
+  return D == 128 ? launch(norm_rope_sum_kernel<128>, 2 * 128 / 32, 1024, st, a)
+                  : launch(norm_rope_sum_kernel<64>, 2 * 64 / 32, 1024, st, a);
+}
+
+}  // extern "C"

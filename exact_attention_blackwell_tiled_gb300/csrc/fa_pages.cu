@@ -1,0 +1,340 @@
+// fa_pages.cu -- page tables of a paged cache brought up to date on the device for the
+// lengths that its sequences are about to have.
+//
+// Sequence b holds L = lens[b] tokens and will hold N = new_lens[b]; entry e of its table
+// is the page of tokens e s .. e s + s - 1.  Under a window of wl tokens with sinks,
+//   hidden(e) = (e + 1) s <= N - 1 - wl and e s >= sinks
+// (no query from N - 1 on sees it), entries [hs, he).  With n0 = ceil(L / s), n1 = ceil(N / s):
+//   back to the pool  e < n0 with a page of the pool, and hidden or e >= n1; becomes -1
+//   from the pool     n0 <= e < n1, not hidden
+// The pool is a stack; what comes back goes on top of it in (b, e) order, and what is taken
+// then comes from the top, in that order too.  So all places are prefix sums over the
+// sequences.  New tokens are packed in (b, position) order; a token's slot is page s +
+// position % s, or -1 where its entry has no page.
+//
+// A few kilobytes move: the time is a launch and a chain of dependent steps.  One cluster
+// of blocks does it all, so that no second launch stands between the sums and what needs
+// them: a warp counts a sequence's entries, the blocks' sums meet in shared memory of the
+// cluster, and two barriers of the cluster stand where a page that came back may be taken
+// by another block's sequence.
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "cache4.cuh"
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kMaxSequences = 65536;  // their sums lie in shared memory
+// Blocks of the cluster: one where a warp has at most two sequences and a thread few
+// tokens, else the eight that every device grants.
+constexpr int kCluster = 8;
+
+struct PageArgs {
+  int* table;  // [B, width]
+  int width, shift, B;
+  int* stack;   // [pages]
+  int* height;  // [1]
+  int pages;
+  const int *lens, *new_lens;
+  int wl, sinks;
+  int T;
+  int* cu;           // [B + 1]
+  int* pos;          // [T]
+  long long* slots;  // [T]
+  int* status;
+};
+
+// What a sequence's lengths say about its entries.
+struct Sequence {
+  int L, N, n0, n1, hs, he;
+  __device__ __forceinline__ bool hidden(int e) const { return e >= hs && e < he; }
+  // entries taken from the pool: [n0, n1) without [hs, he)
+  __device__ __forceinline__ int taken() const {
+    const int all = max(0, n1 - n0), skip = max(0, min(he, n1) - max(hs, n0));
+    return all - min(all, skip);
+  }
+};
+
+__device__ __forceinline__ Sequence read_sequence(const PageArgs& a, int b, bool* bad) {
+  const long long most = (long long)a.width << a.shift;
+  const int l = a.lens[b], n = a.new_lens[b];
+  Sequence s;
+  s.L = l < 0 ? 0 : (int)min((long long)l, most);
+  s.N = n < 0 ? 0 : (int)min((long long)n, most);
+  *bad |= s.L != l || s.N != n;
+  const int page = 1 << a.shift;
+  s.n0 = (s.L + page - 1) >> a.shift;
+  s.n1 = (s.N + page - 1) >> a.shift;
+  s.hs = s.he = 0;
+  if (a.wl >= 0 && s.N - 1 - a.wl > 0) {
+    s.hs = (int)(((long long)a.sinks + page - 1) >> a.shift);
+    s.he = (s.N - 1 - a.wl) >> a.shift;
+  }
+  return s;
+}
+
+// Sums of entries taken and returned, and of new tokens (which stay at INT_MAX).
+struct Sums {
+  int taken, back, tokens;
+};
+__device__ __forceinline__ Sums operator+(const Sums& x, const Sums& y) {
+  return {x.taken + y.taken, x.back + y.back,
+          (int)min((long long)x.tokens + y.tokens, (long long)INT_MAX)};
+}
+__device__ __forceinline__ Sums shfl_up(const Sums& x, int o) {
+  return {__shfl_up_sync(0xffffffffu, x.taken, o), __shfl_up_sync(0xffffffffu, x.back, o),
+          __shfl_up_sync(0xffffffffu, x.tokens, o)};
+}
+
+// Visits the entries that go back to the pool, in order, by a whole warp: f(e, page, rank)
+// for the lanes that hold one; returns their number.
+template <typename F>
+__device__ __forceinline__ int returned(const PageArgs& a, int b, const Sequence& s, F f) {
+  const int lane = threadIdx.x & 31;
+  const int* row = a.table + (size_t)b * a.width;
+  int count = 0;
+  // hidden ones, then those behind the new length (he <= n1)
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int lo = part ? s.n1 : s.hs, hi = part ? s.n0 : min(s.he, s.n0);
+#pragma unroll 1
+    for (int e0 = lo; e0 < hi; e0 += 32) {
+      const int e = e0 + lane;
+      const int page = e < hi ? row[e] : -1;
+      const bool on = page >= 0 && page < a.pages;
+      const unsigned m = __ballot_sync(0xffffffffu, on);
+      if (on) f(e, page, count + __popc(m & ((1u << lane) - 1)));
+      count += __popc(m);
+    }
+  }
+  return count;
+}
+
+template <bool kOne>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (kOne) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+template <bool kOne>
+__global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
+  extern __shared__ int s_taken[];  // [per] each: taken, back, tokens, of the block's sequences
+  __shared__ Sums s_warp[32], s_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t rank = 0;
+  if constexpr (!kOne) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  constexpr int kBlocks = kOne ? 1 : kCluster;
+  const int per = (a.B + kBlocks - 1) / kBlocks;
+  int* s_back = s_taken + per;
+  int* s_tokens = s_back + per;
+  const int b0 = min(a.B, (int)rank * per), n = min(a.B, b0 + per) - b0;
+  grid_dep_wait();
+  grid_dep_launch();
+  bool bad = false;
+  int height = *a.height;
+  if (height < 0 || height > a.pages) {
+    bad = true;
+    height = height < 0 ? 0 : a.pages;
+  }
+  // ---- counts, a warp per sequence
+  for (int i = warp; i < n; i += 32) {
+    const Sequence s = read_sequence(a, b0 + i, &bad);
+    const int back = returned(a, b0 + i, s, [](int, int, int) {});
+    if (lane == 0) {
+      s_taken[i] = s.taken();
+      s_back[i] = back;
+      s_tokens[i] = max(0, s.N - s.L);
+    }
+  }
+  __syncthreads();
+  // ---- sums before each sequence, in the block
+  const int each = (n + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
+  Sums own = {0, 0, 0};
+  for (int i = i0; i < i1; ++i) own = own + Sums{s_taken[i], s_back[i], s_tokens[i]};
+  Sums inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums y = shfl_up(inc, o);
+    if (lane >= o) inc = y + inc;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    Sums w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums y = shfl_up(w, o);
+      if (lane >= o) w = y + w;
+    }
+    s_warp[lane] = w;
+    if (lane == 31) s_total = w;
+  }
+  __syncthreads();
+  sync_all<kOne>();
+  // ... and over the blocks before it
+  Sums before = {0, 0, 0}, total = {0, 0, 0};
+  if constexpr (kOne) {
+    total = s_total;
+  } else {
+    for (int r = 0; r < kBlocks; ++r) {
+      Sums x;
+      uint32_t at;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&s_total)), "r"(r));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x.taken) : "r"(at));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x.back) : "r"(at + 4));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x.tokens) : "r"(at + 8));
+      if (r < (int)rank) before = before + x;
+      total = total + x;
+    }
+  }
+  // the sums before the thread's sequences: the warps before, the lanes before
+  {
+    Sums at = before;
+    if (warp > 0) at = at + s_warp[warp - 1];
+    const Sums lanes = shfl_up(inc, 1);
+    if (lane > 0) at = at + lanes;
+    for (int i = i0; i < i1; ++i) {
+      const Sums x = {s_taken[i], s_back[i], s_tokens[i]};
+      s_taken[i] = at.taken;
+      s_back[i] = at.back;
+      s_tokens[i] = at.tokens;
+      a.cu[b0 + i] = min(at.tokens, a.T);
+      at = at + x;
+    }
+  }
+  if (rank == 0 && tid == 0) {
+    a.cu[a.B] = min(total.tokens, a.T);
+    bad |= total.tokens > a.T;
+  }
+  __syncthreads();
+  // ---- back to the pool
+  for (int i = warp; i < n && total.back > 0; i += 32) {
+    const Sequence s = read_sequence(a, b0 + i, &bad);
+    int* row = a.table + (size_t)(b0 + i) * a.width;
+    const int first = height + s_back[i];
+    returned(a, b0 + i, s, [&](int e, int page, int r) {
+      if (first + r < a.pages) a.stack[first + r] = page;
+      else bad = true;  // more pages than the pool has: one was held twice
+      row[e] = -1;
+    });
+  }
+  sync_all<kOne>();
+  // ---- from the pool
+  const int top = height + total.back;  // (both at most the pool's and the tables' entries)
+  for (int i = warp; i < n && total.taken > 0; i += 32) {
+    const Sequence s = read_sequence(a, b0 + i, &bad);
+    int* row = a.table + (size_t)(b0 + i) * a.width;
+    // entries in front of the hidden ones and behind them
+    const int lo1 = s.n0, hi1 = min(s.n1, max(s.n0, s.hs < s.he ? s.hs : s.n1));
+    const int lo2 = s.hs < s.he ? max(s.n0, s.he) : s.n1, hi2 = s.n1;
+    const int c1 = max(0, hi1 - lo1), c = c1 + max(0, hi2 - lo2);
+    for (int x = lane; x < c; x += 32) {
+      const int e = x < c1 ? lo1 + x : lo2 + x - c1;
+      const int at = top - 1 - (s_taken[i] + x);
+      const bool there = at >= 0 && at < a.pages;
+      row[e] = there ? __ldcg(a.stack + at) : -1;
+      bad |= !there;
+    }
+  }
+  if (rank == 0 && tid == 0) {
+    const int left = top - total.taken;
+    *a.height = left < 0 ? 0 : min(left, a.pages);
+  }
+  __syncthreads();
+  // ---- positions and slots of the block's new tokens
+  const int lo = min(a.T, before.tokens), hi = n > 0 ? min(a.T, (before + s_total).tokens) : lo;
+  const int mask = (1 << a.shift) - 1;
+  for (int t = lo + tid; t < hi; t += kThreads) {
+    int x = 0, m = n;  // the last sequence that begins at or before token t
+    while (m > 1) {
+      const int half = m >> 1;
+      if (s_tokens[x + half] <= t) {
+        x += half;
+        m -= half;
+      } else {
+        m = half;
+      }
+    }
+    const int p = a.lens[b0 + x] + t - s_tokens[x];
+    const int pos = p < 0 ? t - s_tokens[x] : p;  // (a negative length counts as none)
+    const int page = a.table[(size_t)(b0 + x) * a.width + (pos >> a.shift)];
+    a.pos[t] = pos;
+    a.slots[t] = page >= 0 ? ((long long)page << a.shift) + (pos & mask) : -1;
+  }
+  for (int t = min(a.T, total.tokens) + rank * kThreads + tid; t < a.T; t += kBlocks * kThreads) {
+    a.pos[t] = -1;
+    a.slots[t] = -1;
+  }
+  if (bad) atomicExch(a.status, 1);
+}
+
+bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" int fa_page_update(int* page_table, int table_width, int* free_pages, int* free_count,
+                              int num_pages, const int* lens, const int* new_lens, int B, int page_size,
+                              int window_left, int sinks, int T, int* cu_seqlens, int* positions,
+                              int64_t* slots, fa_stream_t stream) {
+  reset_launches();
+  int rc = check_cache4(num_pages, 1, 64, page_size, B, table_width);
+  if (rc) return rc;
+  if (B > kMaxSequences || (long long)B * table_width >= (1LL << 30) || num_pages > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (T < 0 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (!page_table || !free_pages || !free_count || !lens || !new_lens || !cu_seqlens ||
+      (T > 0 && (!positions || !slots)))
+    return FA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)page_table, (const void*)free_pages, (const void*)free_count,
+                        (const void*)lens, (const void*)new_lens, (const void*)cu_seqlens, (const void*)positions})
+    if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
+  if (misaligned(slots, 8)) return FA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
+  int* status = cache4_status_word();
+  if (!status) return FA_ERR_CUDA;
+  const PageArgs a{page_table, table_width, c4_shift(page_size) + 4, B, free_pages, free_count, num_pages,
+                   lens, new_lens, window_left < 0 ? -1 : window_left, sinks, T, cu_seqlens, positions,
+                   reinterpret_cast<long long*>(slots), status};
+  static bool attr_done[64] = {};
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(page_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             3 * (kMaxSequences / kCluster) * (int)sizeof(int)) != cudaSuccess)
+      return FA_ERR_CUDA;
+    attr_done[dev] = true;
+  }
+  const bool one = B <= 64 && T <= 4096;
+  const int blocks = one ? 1 : kCluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 3 * (size_t)((B + blocks - 1) / blocks) * sizeof(int);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = one ? 1 : 2;
+  if (cudaLaunchKernelEx(&cfg, one ? page_kernel<true> : page_kernel<false>, a) != cudaSuccess)
+    return FA_ERR_CUDA;
+  note_launches(1);
+  return FA_OK;
+}
