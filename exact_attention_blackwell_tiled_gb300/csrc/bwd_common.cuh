@@ -326,13 +326,10 @@ __device__ __forceinline__ size_t sink_slot(const BwdArgs& a, int row0, int tile
              : (size_t)(row0 / kTile + tile) * a.sinks + row0;
 }
 
-// The list positions (head, item) of the sinks' kernel, head by head, are dealt in equal
-// contiguous shares.
-__device__ __forceinline__ int sink_shares(const BwdArgs& a, long long total) {
-  return total < a.sink_grid ? (int)total : a.sink_grid;
-}
-__device__ __forceinline__ long long sink_share(long long total, int shares, int k) {
-  return k * total / shares;
+// The list positions (head, item) of the sinks' kernel, head by head, are dealt in
+// contiguous shares of this many.
+__device__ __forceinline__ int sink_share(const BwdArgs& a, int n_items) {
+  return max(1, (n_items * a.Hq + a.sink_grid - 1) / a.sink_grid);
 }
 
 // 32 columns (32 c ..) of rows row0 .. row0 + 3, held by the lanes of a group of four, as

@@ -87,11 +87,12 @@ namespace fa {
 
 constexpr int kQB = 64;  // query rows per backward block
 
-// bwd_main warp roles.  The score-modified kernel (masks, bias: more softmax
+// bwd_main warp roles.  The dense score-modified kernel (masks, bias: more softmax
 // work per score) and the D = 64 kernels (half the tensor work per score) run
 // 16 softmax warps of 16 query columns each, 768 threads at 80 registers; the
-// plain D = 128 kernel 8 of 32 columns, 512 threads at 128 registers, which
-// measured faster there.
+// plain D = 128 kernel and the packed one with a window, which has no bias, 8 of 32
+// columns, 512 threads at 128 registers, which measured faster there.
+__host__ __device__ constexpr bool bwd_wide(int D, bool mod, bool var) { return D == 64 || (mod && !var); }
 template <bool kWide>
 struct BwdRoles {
   static constexpr int kSmxWarps = kWide ? 16 : 8;  // warps 0..: P^T / dS^T
@@ -340,13 +341,13 @@ __device__ __forceinline__ void red_add(float* p, float x) {
 // (D = 64; at D = 128 it is the 128-row kernel's); a kernel of its own, since the
 // atomic mode's adds lost 13% of its rate to code that it does not run.
 template <int D, bool kMod, bool kVar, bool kDet>
-__global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
+__global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1)
     bwd_main(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
              const BwdArgs a, const __grid_constant__ Tails<kVar, 4> tails) {
   using L = BwdSmem<D>;
   static_assert(!kDet || D == 64, "D = 128 deterministic calls run the 128-row kernel");
-  using R = BwdRoles<kMod || D == 64>;
+  using R = BwdRoles<bwd_wide(D, kMod, kVar)>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -722,8 +723,8 @@ __global__ void __launch_bounds__(BwdRoles<kMod || D == 64>::kThreads, 1)
         const int c_lo = wr >= 0 ? kv - wr - q0 : INT_MIN;
         const int c_hi = wl >= 0 ? kv + wl - q0 : INT_MAX;
         // -LSE2 plus the relative-position bias slope*log2(e)*(kv - q) per column
-        // (zero bias: exactly -LSE2)
-        if (kMod) {
+        // (zero bias: exactly -LSE2; packed calls have none)
+        if (kMod && !kVar) {
           const float slope2 =
               a.alibi ? a.alibi[w.hk * group + gi] * 1.4426950408889634f : 0.f;
 #pragma unroll
@@ -1119,8 +1120,7 @@ __device__ void sum_sinks(const BwdArgs& a, int n_items, int item, const VarItem
   const int groups = kSlots / at_once;
   const int c8 = threadIdx.x % kPerRow, slot = threadIdx.x / kPerRow;
   const int my_row = slot % at_once, my_group = slot / at_once;
-  const long long total = (long long)n_items * a.Hq;
-  const int shares = sink_shares(a, total);
+  const int share = sink_share(a, n_items);
   const int first = sink_first_tile(a), last = (it.len - 1) / kTile;
   // the shares of the group's q heads, one after the other
   for (int r0 = 0; r0 < rows; r0 += at_once) {
@@ -1130,17 +1130,18 @@ __device__ void sum_sinks(const BwdArgs& a, int n_items, int item, const VarItem
     for (int g = 0; g < group; ++g) {
       const int h = hk * group + g;
       const float* parts = (is_v ? a.sink_dv : a.sink_dk) + (size_t)h * a.sink_rows * D;
-      const long long x0 = (long long)h * n_items + item;  // the sequence's tile 0
-      int k = (int)((x0 + first) * shares / total);  // the share that holds it
-      while (sink_share(total, shares, k + 1) <= x0 + first) ++k;
-      while (sink_share(total, shares, k) > x0 + first) --k;
-      int tile = first;
-      do {
-        if (part++ % groups == my_group && r < rows)
+      // runs begin at the first tile with sinks behind the window and at the shares'
+      // multiples; tiles count from the sequence's tile 0, at position x0
+      const int x0 = h * n_items + item;
+      int tile = first, next = (x0 + first) / share * share + share - x0;
+      while (tile <= last) {
+        if ((part & (groups - 1)) == my_group && r < rows)
           add_eight(x, reinterpret_cast<const float4*>(parts + (sink_slot(a, it.row0, tile) + r) * D +
                                                        c8 * 8));
-        tile = (int)(sink_share(total, shares, ++k) - x0);
-      } while (tile <= last);
+        ++part;
+        tile = next;
+        next += share;
+      }
     }
     __syncthreads();
     s_sum[threadIdx.x][0] = x[0];
@@ -1307,7 +1308,7 @@ static int launch_bwd_d(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream)
                             ? (mod ? bwd_main<D, true, false, kDet> : bwd_main<D, false, false, kDet>)
                             : (mod ? bwd_main<D, true, false, false> : bwd_main<D, false, false, false>);
     const int threads =
-        (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
+        bwd_wide(D, mod, false) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
     record_timing(false, stream);
     if (a.qblk_rows == 128) {
       // the deterministic mode deals units from the global counter in the
@@ -1419,7 +1420,8 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaS
   const auto kernel = kDet && a.deterministic
                           ? (mod ? bwd_main<D, true, true, kDet> : bwd_main<D, false, true, kDet>)
                           : (mod ? bwd_main<D, true, true, false> : bwd_main<D, false, true, false>);
-  const int threads = (mod || D == 64) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
+  const int threads =
+      bwd_wide(D, mod, true) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
   record_timing(false, stream);
   if (a.qblk_rows == 128) {
     const int rc = launch_bwd_main_q128_var(m, a, mod, grid, stream);

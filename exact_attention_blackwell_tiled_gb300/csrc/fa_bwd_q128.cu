@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
         const int c_lo = wr >= 0 ? kv - wr - q0 : INT_MIN;
         const int c_hi = wl >= 0 ? kv + wl - q0 : INT_MAX;
         // relative-position bias slope*log2(e)*(kv - q) per column (none in
-        // the plain kernel)
+        // the plain kernel and in packed calls)
         const float slope2 =
             (kMod && a.alibi) ? a.alibi[w.hk * group + gi] * 1.4426950408889634f : 0.f;
         if (!warp_wait_b(bar(L::kBarSFull), it & 1, abort_flag)) {
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
               const int c = 4 * q + e;
-              const float b0 = kMod ? slope2 * (float)(kv - q0 - c) : 0.f;
-              const float b1 = kMod ? slope2 * (float)(kv - q0 - c - 1) : 0.f;
+              const float b0 = kMod && !kVar ? slope2 * (float)(kv - q0 - c) : 0.f;
+              const float b1 = kMod && !kVar ? slope2 * (float)(kv - q0 - c - 1) : 0.f;
               const float2 t2 = __ffma2_rn(make_float2(u2f(v[c]), u2f(v[c + 1])), c2,
                                            make_float2(b0 - lq[e], b1 - lq[e + 1]));
               const float x0 = ex2_mufu(t2.x), x1 = ex2_mufu(t2.y);

@@ -142,11 +142,9 @@ __global__ void __launch_bounds__(192, 1)
   SinkWalk walk;
   walk.n_items = *a.n_items;
   {
-    const long long total = (long long)walk.n_items * a.Hq;
-    const int shares = sink_shares(a, total);
-    const bool mine = (int)blockIdx.x < shares;
-    walk.x = mine ? sink_share(total, shares, blockIdx.x) : 0;
-    walk.end = mine ? sink_share(total, shares, blockIdx.x + 1) : 0;
+    const long long total = (long long)walk.n_items * a.Hq, share = sink_share(a, walk.n_items);
+    walk.x = blockIdx.x * share;
+    walk.end = walk.x + share < total ? walk.x + share : total;
   }
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer

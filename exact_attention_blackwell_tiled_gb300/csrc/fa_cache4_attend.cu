@@ -133,11 +133,9 @@ struct View {
   int lo, front, gap, sinks;  // (kWin) keys from lo on and below `sinks` are visible
   __device__ __forceinline__ int block(int i) const { return !kWin || i < front ? i : i + gap; }
   __device__ __forceinline__ bool key(int j) const { return j < len && (!kWin || j >= lo || j < sinks); }
-  // whether all keys of block `blk` are visible
-  __device__ __forceinline__ bool whole(int blk) const {
-    const int j = blk * kC4Block;
-    return j + kC4Block <= len && (!kWin || j >= lo || j + kC4Block <= sinks);
-  }
+  // (kWin) blocks [in0, in1) lie behind one another and all their keys are visible
+  __device__ __forceinline__ int in0() const { return front + (lo % kC4Block ? 1 : 0); }
+  __device__ __forceinline__ int in1() const { return len / kC4Block - gap; }
 };
 template <bool kWin>
 __device__ __forceinline__ View<kWin> seq_view(const AttendArgs& a, int b) {
@@ -480,6 +478,7 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
       score = a.scores +
               (((size_t)row_b * a.Hkv + hk) * a.cap + (kWin ? 0 : blk0) * kC4Block + slot_i) * a.group +
               tile * 8 * NT + 2 * t;
+    const int in0 = kWin ? view.in0() : 0, in1 = kWin ? min(view.in1(), blk1) : 0;
     // ---- its blocks, two at a time: their chains of dependent steps interleave
 #pragma unroll 1
     for (int at = blk0; at < blk1; at += 2) {
@@ -552,20 +551,19 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
       // slots behind the last key, and blocks whose page is out of range
       const uint32_t miss = (bad >> (st * R::kBlocks + x)) & 3u;
       const int ends = min(len, blk1 * kC4Block) - at * kC4Block;  // the share's keys from here on
-      int key0[2] = {0, 0};  // (kWin) the blocks' first keys
-      bool full;
-      bool live[2][2];
+      const bool full = miss == 0 && (kWin ? at >= in0 && at + 2 <= in1 : ends >= 2 * kC4Block);
+      bool live[2][2] = {{true, true}, {true, true}};
       if constexpr (kWin) {
-        key0[0] = view.block(at) * kC4Block;
-        key0[1] = view.block(at + 1) * kC4Block;
-        full = miss == 0 && at + 1 < blk1 && view.whole(key0[0] / kC4Block) && view.whole(key0[1] / kC4Block);
+        if (!full) {
+          asm volatile("" ::: "memory");  // a branch
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int z = 0; z < 2; ++z)
-            live[y][z] = !((miss >> y) & 1) && at + y < blk1 && view.key(key0[y] + slot_i + 8 * z);
+            for (int z = 0; z < 2; ++z)
+              live[y][z] = !((miss >> y) & 1) && at + y < blk1 &&
+                           view.key(view.block(at + y) * kC4Block + slot_i + 8 * z);
+        }
       } else {
-        full = miss == 0 && ends >= 2 * kC4Block;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -598,11 +596,13 @@ __global__ void __launch_bounds__((kOwn ? kOwnWarps : kWarps) * 32, kOwn ? 1 : b
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             if constexpr (kWin) {
-              if (at + y >= blk1 || key0[y] + slot_i + 8 * z >= len) continue;
+              // keys out of sight have no score, in these blocks and in others
+              if (!full && !(at + y < blk1 && view.key(view.block(at + y) * kC4Block + slot_i + 8 * z))) continue;
             } else {
               if (mine <= y * kC4Block + 8 * z) continue;
             }
-            float* dst = score + ((kWin ? (size_t)key0[y] : (size_t)(y * kC4Block)) + 8 * z) * a.group;
+            float* dst = score + (kWin ? (size_t)view.block(at + y) * kC4Block + 8 * z
+                                       : (size_t)(y * kC4Block + 8 * z)) * a.group;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const int col = nt * 8 + 2 * t;

@@ -28,8 +28,9 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kHeads = 8;       // heads of a token that a warp takes at a time
-constexpr int kGradBlocks = 2;  // of the backward kernel per SM
+constexpr int kBlocks = 3, kGradBlocks = 2;  // per SM, forward and backward
+constexpr int kDepth = 2, kGradDepth = 1;     // steps whose rows are on their way, of a warp
+constexpr int kHeads = 8;  // heads of a unit where tokens are few
 
 struct Rows {
   const __nv_bfloat16* x;
@@ -48,6 +49,7 @@ struct NormRopeArgs {
   const float *cos, *sin;  // [P, rot / 2]
   const int* pos;          // [T]
   int T, H[2], P, rot;
+  int heads;  // of a unit
   int zero;  // rows of no sequence get zeros
   float eps;
   int* status;
@@ -81,7 +83,6 @@ template <int D, bool kPairs>
 struct Lane {
   static constexpr int kPerRow = D / 16;       // lanes
   static constexpr int kRows = 32 / kPerRow;   // rows of a warp
-  static constexpr int kSteps = kHeads / kRows < 1 ? 1 : kHeads / kRows;
   int l, sub, a0, b0;
   bool turns;  // the lane's elements are rotated
   __device__ __forceinline__ Lane(int rot) {
@@ -158,70 +159,127 @@ __device__ __forceinline__ int position(const NormRopeArgs& a, int token) {
   return p < a.P ? p : -1;
 }
 
+// A step is kRows heads of one token; a warp takes its units' steps one after the other,
+// the next one's rows on their way while it turns the present one's.  A unit is a token and
+// `heads` of its heads.
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeArgs a) {
+struct Walk {
+  using L = Lane<D, kPairs>;
+  int token, h, end;  // the step's heads: h .. min(end, h + kRows) - 1
+  uint32_t u, stride, units;  // units are below 2^31
+  int per_token, heads, H;
+  __device__ __forceinline__ void start(const NormRopeArgs& a, int kind, uint32_t first, uint32_t by) {
+    H = a.H[kind];
+    heads = a.heads;
+    per_token = (H + heads - 1) / heads;
+    units = (uint32_t)a.T * per_token;
+    u = first;
+    stride = by;
+    place();
+  }
+  __device__ __forceinline__ void place() {
+    token = (int)(u / (uint32_t)per_token);
+    h = (int)(u - (uint32_t)token * per_token) * heads;
+    end = min(H, h + heads);
+  }
+  __device__ __forceinline__ bool more() const { return u < units; }
+  __device__ __forceinline__ void next() {
+    h += L::kRows;
+    if (h >= end) {
+      u += stride;
+      place();
+    }
+  }
+};
+
+// One row's part of a lane.
+struct Piece {
+  uint4 a, b;
+};
+template <int D, bool kPairs>
+__device__ __forceinline__ Piece load_row(const Rows& x, const Walk<D, kPairs>& w, const Lane<D, kPairs>& lane) {
+  Piece p;
+  p.a = p.b = make_uint4(0u, 0u, 0u, 0u);
+  const int h = w.h + lane.sub;
+  if (w.more() && h < w.end) {
+    const __nv_bfloat16* row = x.x + w.token * x.token + h * x.head;
+    p.a = load16(row + lane.a0);
+    p.b = load16(row + lane.b0);
+  }
+  return p;
+}
+
+template <int D, bool kPairs>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
   const L lane(a.rot);
   grid_dep_wait();
   grid_dep_launch();
-  const int units_q = (a.H[0] + kHeads - 1) / kHeads;
-  const int per_token = units_q + (a.H[1] + kHeads - 1) / kHeads;
-  const long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int token = (int)(u / per_token), part = (int)(u - (long long)token * per_token);
-  if (token >= a.T) return;
-  const int kind = part >= units_q ? 1 : 0;
-  const int h0 = (kind ? part - units_q : part) * kHeads;
-  const Rows& in = a.in[kind];
-  const RowsOut& out = a.out[kind];
-  uint4 xa[L::kSteps], xb[L::kSteps];
+  const uint32_t first = (threadIdx.x >> 5) * gridDim.x + blockIdx.x, by = kWarps * gridDim.x;
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    Walk<D, kPairs> w;
+    // (the other kind's units begin where these end, so that few units spread over all warps)
+    const uint32_t shift = kind ? (uint32_t)a.T * ((a.H[0] + a.heads - 1) / a.heads) % by : 0u;
+    w.start(a, kind, first >= shift ? first - shift : first - shift + by, by);
+    if (!w.more()) continue;
+    const RowsOut& out = a.out[kind];
+    float2 c[4], s[4], wa[4], wb[4];
+    Piece x[kDepth];
+    Walk<D, kPairs> ahead = w;
 #pragma unroll
-  for (int n = 0; n < L::kSteps; ++n) {
-    const int h = h0 + n * L::kRows + lane.sub;
-    xa[n] = xb[n] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < a.H[kind]) {
-      const __nv_bfloat16* row = in.x + token * in.token + h * in.head;
-      xa[n] = load16(row + lane.a0);
-      xb[n] = load16(row + lane.b0);
+    for (int n = 0; n < kDepth; ++n) {
+      x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
+      ahead.next();
     }
-  }
-  const int p = position(a, token);
-  if (p < 0 && !a.zero) return;
-  float2 c[4], s[4], wa[4], wb[4];
-  load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
-  load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
-  load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
+    load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
+    load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
+    int token = -1, p = -1;
+#pragma unroll 1
+    while (w.more()) {
 #pragma unroll
-  for (int n = 0; n < L::kSteps; ++n) {
-    const int h = h0 + n * L::kRows + lane.sub;
-    float2 fa_[4], fb[4], sum = make_float2(0.f, 0.f);
-    widen(xa[n], fa_);
-    widen(xb[n], fb);
+      for (int n = 0; n < kDepth; ++n) {
+        if (!w.more()) break;
+        if (w.token != token) {
+          token = w.token;
+          p = position(a, token);
+          load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
+        }
+        float2 fa_[4], fb[4], sum = make_float2(0.f, 0.f);
+        widen(x[n].a, fa_);
+        widen(x[n].b, fb);
+        x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
+        ahead.next();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sum = __ffma2_rn(fa_[e], fa_[e], sum);
-      sum = __ffma2_rn(fb[e], fb[e], sum);
-    }
-    float ss = sum.x + sum.y;
+        for (int e = 0; e < 4; ++e) {
+          sum = __ffma2_rn(fa_[e], fa_[e], sum);
+          sum = __ffma2_rn(fb[e], fb[e], sum);
+        }
+        float ss = sum.x + sum.y;
 #pragma unroll
-    for (int o = L::kPerRow / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-    const float2 r2 = make_float2(r, r);
+        for (int o = L::kPerRow / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        const float2 r2 = make_float2(r, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      fa_[e] = __fmul2_rn(__fmul2_rn(fa_[e], r2), wa[e]);
-      fb[e] = __fmul2_rn(__fmul2_rn(fb[e], r2), wb[e]);
-    }
-    if (lane.turns) turn<kPairs, false>(fa_, fb, c, s);
-    if (h < a.H[kind]) {
-      __nv_bfloat16* row = out.x + token * out.token + h * out.head;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(row + lane.a0) = p < 0 ? zero : narrow(fa_);
-      *reinterpret_cast<uint4*>(row + lane.b0) = p < 0 ? zero : narrow(fb);
+        for (int e = 0; e < 4; ++e) {
+          fa_[e] = __fmul2_rn(__fmul2_rn(fa_[e], r2), wa[e]);
+          fb[e] = __fmul2_rn(__fmul2_rn(fb[e], r2), wb[e]);
+        }
+        if (lane.turns) turn<kPairs, false>(fa_, fb, c, s);
+        const int h = w.h + lane.sub;
+        if (h < w.end && (p >= 0 || a.zero)) {
+          __nv_bfloat16* row = out.x + w.token * out.token + h * out.head;
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(row + lane.a0) = p < 0 ? zero : narrow(fa_);
+          *reinterpret_cast<uint4*>(row + lane.b0) = p < 0 ? zero : narrow(fb);
+        }
+        w.next();
+      }
     }
   }
 }
 
-// A persistent grid: its warps walk q's units, then k's, and sum dw as they go.
+// The warps walk q's units, then k's, and sum dw as they go.
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
@@ -232,44 +290,41 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
   grid_dep_launch();
 #pragma unroll 1
   for (int kind = 0; kind < 2; ++kind) {
-    const Rows &in = a.in[kind], &dy = a.dy[kind];
     const RowsOut& out = a.out[kind];
-    const int H = a.H[kind], per_token = (H + kHeads - 1) / kHeads;
-    const long long units = (long long)a.T * per_token;
-    float2 wa[4], wb[4], da[4], db[4];
+    Walk<D, kPairs> w;
+    w.start(a, kind, warp * gridDim.x + blockIdx.x, kWarps * gridDim.x);
+    float2 wa[4], wb[4], da[4], db[4], c[4], s[4];
+    Piece x[kGradDepth], g[kGradDepth];
+    Walk<D, kPairs> ahead = w;
+#pragma unroll
+    for (int n = 0; n < kGradDepth; ++n) {
+      x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
+      g[n] = load_row<D, kPairs>(a.dy[kind], ahead, lane);
+      ahead.next();
+    }
     load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
     load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
 #pragma unroll
     for (int e = 0; e < 4; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
+    int token = -1, p = -1;
 #pragma unroll 1
-    for (long long u = (long long)warp * gridDim.x + blockIdx.x; u < units; u += (long long)kWarps * gridDim.x) {
-      const int token = (int)(u / per_token), h0 = (int)(u - (long long)token * per_token) * kHeads;
-      uint4 xa[L::kSteps], xb[L::kSteps], ga[L::kSteps], gb[L::kSteps];
+    while (w.more()) {
 #pragma unroll
-      for (int n = 0; n < L::kSteps; ++n) {
-        const int h = h0 + n * L::kRows + lane.sub;
-        xa[n] = xb[n] = ga[n] = gb[n] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < H) {
-          const __nv_bfloat16* row = in.x + token * in.token + h * in.head;
-          const __nv_bfloat16* grad = dy.x + token * dy.token + h * dy.head;
-          xa[n] = load16(row + lane.a0);
-          xb[n] = load16(row + lane.b0);
-          ga[n] = load16(grad + lane.a0);
-          gb[n] = load16(grad + lane.b0);
+      for (int n = 0; n < kGradDepth; ++n) {
+        if (!w.more()) break;
+        if (w.token != token) {
+          token = w.token;
+          p = position(a, token);
+          load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
         }
-      }
-      const int p = position(a, token);
-      if (p < 0 && !a.zero) continue;
-      float2 c[4], s[4];
-      load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
-#pragma unroll
-      for (int n = 0; n < L::kSteps; ++n) {
-        const int h = h0 + n * L::kRows + lane.sub;
         float2 fa_[4], fb[4], ha[4], hb[4];
-        widen(xa[n], fa_);
-        widen(xb[n], fb);
-        widen(ga[n], ha);
-        widen(gb[n], hb);
+        widen(x[n].a, fa_);
+        widen(x[n].b, fb);
+        widen(g[n].a, ha);
+        widen(g[n].b, hb);
+        x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
+        g[n] = load_row<D, kPairs>(a.dy[kind], ahead, lane);
+        ahead.next();
         if (lane.turns) turn<kPairs, true>(ha, hb, c, s);
         // sums of x^2 and of h x, h = g w
         float2 sx = make_float2(0.f, 0.f), sh = make_float2(0.f, 0.f);
@@ -290,26 +345,25 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
           hx += __shfl_xor_sync(0xffffffffu, hx, o);
         }
         const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        if (p < 0 || h >= H) {
-          if (h < H) {
-            __nv_bfloat16* row = out.x + token * out.token + h * out.head;
-            *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          continue;
-        }
-        const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
-        const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+        const int h = w.h + lane.sub;
+        __nv_bfloat16* row = out.x + w.token * out.token + h * out.head;
+        if (p >= 0 && h < w.end) {
+          const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
+          const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          da[e] = __ffma2_rn(ta[e], r2, da[e]);
-          db[e] = __ffma2_rn(tb[e], r2, db[e]);
-          ha[e] = __ffma2_rn(__fmul2_rn(ha[e], wa[e]), r2, __fmul2_rn(fa_[e], m2));
-          hb[e] = __ffma2_rn(__fmul2_rn(hb[e], wb[e]), r2, __fmul2_rn(fb[e], m2));
+          for (int e = 0; e < 4; ++e) {
+            da[e] = __ffma2_rn(ta[e], r2, da[e]);
+            db[e] = __ffma2_rn(tb[e], r2, db[e]);
+            ha[e] = __ffma2_rn(__fmul2_rn(ha[e], wa[e]), r2, __fmul2_rn(fa_[e], m2));
+            hb[e] = __ffma2_rn(__fmul2_rn(hb[e], wb[e]), r2, __fmul2_rn(fb[e], m2));
+          }
+          *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ha);
+          *reinterpret_cast<uint4*>(row + lane.b0) = narrow(hb);
+        } else if (a.zero && h < w.end) {
+          *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
         }
-        __nv_bfloat16* row = out.x + token * out.token + h * out.head;
-        *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ha);
-        *reinterpret_cast<uint4*>(row + lane.b0) = narrow(hb);
+        w.next();
       }
     }
     // the warp's sums over its rows, then the block's over its warps
@@ -334,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
     if (threadIdx.x < D) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += s_dw[w][threadIdx.x];
+      for (int w2 = 0; w2 < kWarps; ++w2) sum += s_dw[w2][threadIdx.x];
       a.part[((size_t)blockIdx.x * 2 + kind) * D + threadIdx.x] = sum;
     }
   }
@@ -400,11 +454,23 @@ int strides(const fa_packed_stride* s, int H, int D, bool written, long long* to
   return (*token & 7) || (*head & 7) ? FA_ERR_MISALIGNED : FA_OK;
 }
 
+// A unit's heads: few where that gives no warp more than kFew units, else a token's, so
+// that its angles are loaded once.  Returns the grid, at most `most` blocks.
+constexpr int kFew = 4;
+int set_units(NormRopeArgs* a, long long most) {
+  const int H = a->H[0] > a->H[1] ? a->H[0] : a->H[1];
+  const auto count = [&](int heads) {
+    return (long long)a->T * ((a->H[0] + heads - 1) / heads + (a->H[1] + heads - 1) / heads);
+  };
+  a->heads = count(kHeads) <= kFew * most * kWarps ? kHeads : (H + 7) / 8 * 8;
+  const long long blocks = (count(a->heads) + kWarps - 1) / kWarps;
+  return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+}
+
 int grad_blocks(int sms, int T, int Hq, int Hkv) {
-  const long long q = (long long)T * ((Hq + kHeads - 1) / kHeads), k = (long long)T * ((Hkv + kHeads - 1) / kHeads);
-  const long long most = ((q > k ? q : k) + kWarps - 1) / kWarps;
-  const long long grid = (long long)sms * kGradBlocks;
-  return (int)(most < grid ? (most > 0 ? most : 1) : grid);
+  NormRopeArgs a{};
+  a.T = T, a.H[0] = Hq, a.H[1] = Hkv;
+  return set_units(&a, (long long)sms * kGradBlocks);
 }
 
 template <typename... A>
@@ -481,11 +547,12 @@ int fa_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, con
   a.zero = zero_skipped ? 1 : 0;
   a.eps = eps;
   a.status = fwd_status_word();
-  if (!a.status) return FA_ERR_CUDA;
-  const long long units = (long long)T * ((Hq + kHeads - 1) / kHeads + (Hkv + kHeads - 1) / kHeads);
+  int dev;
+  DeviceInfo info;
+  if (!a.status || !current_device(&dev, &info)) return FA_ERR_CUDA;
   const auto kernel = D == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
                                : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>);
-  return launch(kernel, (units + kWarps - 1) / kWarps, kWarps * 32, static_cast<cudaStream_t>(stream), a);
+  return launch(kernel, set_units(&a, (long long)info.sm_count * kBlocks), kWarps * 32, static_cast<cudaStream_t>(stream), a);
 }
 
 size_t fa_norm_rope_workspace_bytes(int T, int Hq, int Hkv, int D) {
@@ -528,7 +595,10 @@ int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
-  a.blocks = grad_blocks(info.sm_count, T, Hq, Hkv);
+  a.T = T;
+  a.H[0] = Hq;
+  a.H[1] = Hkv;
+  a.blocks = set_units(&a, (long long)info.sm_count * kGradBlocks);
   if (workspace_bytes < (size_t)a.blocks * 2 * D * sizeof(float)) return FA_ERR_WORKSPACE;
   a.in[0].x = static_cast<const __nv_bfloat16*>(q);
   a.in[1].x = static_cast<const __nv_bfloat16*>(k);

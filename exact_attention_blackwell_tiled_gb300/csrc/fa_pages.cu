@@ -31,9 +31,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxSequences = 65536;  // their sums lie in shared memory
-// Blocks of the cluster: one where a warp has at most two sequences and a thread few
-// tokens, else the eight that every device grants.
-constexpr int kCluster = 8;
+// One block where a warp has at most two sequences, else a cluster of the eight that every
+// device grants.
+constexpr int kOneBlock = 64, kCluster = 8;
+constexpr int kApart = 8192;  // more new tokens than this are written by a launch of their own
 
 struct PageArgs {
   int* table;  // [B, width]
@@ -48,6 +49,7 @@ struct PageArgs {
   int* pos;          // [T]
   long long* slots;  // [T]
   int* status;
+  int apart;  // slot_kernel writes positions and slots
 };
 
 // What a sequence's lengths say about its entries.
@@ -61,13 +63,15 @@ struct Sequence {
   }
 };
 
-__device__ __forceinline__ Sequence read_sequence(const PageArgs& a, int b, bool* bad) {
+__device__ __forceinline__ int cut_length(const PageArgs& a, int n) {
   const long long most = (long long)a.width << a.shift;
-  const int l = a.lens[b], n = a.new_lens[b];
+  return n < 0 ? 0 : (int)min((long long)n, most);
+}
+
+__device__ __forceinline__ Sequence make_sequence(const PageArgs& a, int L, int N) {
   Sequence s;
-  s.L = l < 0 ? 0 : (int)min((long long)l, most);
-  s.N = n < 0 ? 0 : (int)min((long long)n, most);
-  *bad |= s.L != l || s.N != n;
+  s.L = L;
+  s.N = N;
   const int page = 1 << a.shift;
   s.n0 = (s.L + page - 1) >> a.shift;
   s.n1 = (s.N + page - 1) >> a.shift;
@@ -93,7 +97,9 @@ __device__ __forceinline__ Sums shfl_up(const Sums& x, int o) {
 }
 
 // Visits the entries that go back to the pool, in order, by a whole warp: f(e, page, rank)
-// for the lanes that hold one; returns their number.
+// for the lanes that hold one; returns their number.  A lane loads several entries at a time,
+// for it is the loads' latency that counts.
+constexpr int kAtOnce = 8;
 template <typename F>
 __device__ __forceinline__ int returned(const PageArgs& a, int b, const Sequence& s, F f) {
   const int lane = threadIdx.x & 31;
@@ -104,16 +110,47 @@ __device__ __forceinline__ int returned(const PageArgs& a, int b, const Sequence
   for (int part = 0; part < 2; ++part) {
     const int lo = part ? s.n1 : s.hs, hi = part ? s.n0 : min(s.he, s.n0);
 #pragma unroll 1
-    for (int e0 = lo; e0 < hi; e0 += 32) {
-      const int e = e0 + lane;
-      const int page = e < hi ? row[e] : -1;
-      const bool on = page >= 0 && page < a.pages;
-      const unsigned m = __ballot_sync(0xffffffffu, on);
-      if (on) f(e, page, count + __popc(m & ((1u << lane) - 1)));
-      count += __popc(m);
+    for (int e0 = lo; e0 < hi; e0 += 32 * kAtOnce) {
+      int page[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int e = e0 + 32 * x + lane;
+        page[x] = e < hi ? row[e] : -1;
+      }
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const bool on = page[x] >= 0 && page[x] < a.pages;
+        const unsigned m = __ballot_sync(0xffffffffu, on);
+        if (on) f(e0 + 32 * x + lane, page[x], count + __popc(m & ((1u << lane) - 1)));
+        count += __popc(m);
+      }
     }
   }
   return count;
+}
+
+// The last of the ascending numbers x[lo .. lo + n - 1] that is at most t.
+__device__ __forceinline__ int last_at_or_before(const int* x, int lo, int n, int t) {
+  while (n > 1) {
+    const int half = n >> 1;
+    if (x[lo + half] <= t) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void write_token(const PageArgs& a, int t, int b, int pos) {
+  const int page = a.table[(size_t)b * a.width + (pos >> a.shift)];
+  a.pos[t] = pos;
+  a.slots[t] = page >= 0 ? ((long long)page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
+}
+__device__ __forceinline__ void write_no_token(const PageArgs& a, int t) {
+  a.pos[t] = -1;
+  a.slots[t] = -1;
 }
 
 template <bool kOne>
@@ -128,7 +165,8 @@ __device__ __forceinline__ void sync_all() {
 
 template <bool kOne>
 __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
-  extern __shared__ int s_taken[];  // [per] each: taken, back, tokens, of the block's sequences
+  // [per] each: taken, back, tokens (counts, then sums before), lengths, of the block's sequences
+  extern __shared__ int s_taken[];
   __shared__ Sums s_warp[32], s_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank = 0;
@@ -137,6 +175,8 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
   const int per = (a.B + kBlocks - 1) / kBlocks;
   int* s_back = s_taken + per;
   int* s_tokens = s_back + per;
+  int* s_old = s_tokens + per;
+  int* s_new = s_old + per;
   const int b0 = min(a.B, (int)rank * per), n = min(a.B, b0 + per) - b0;
   grid_dep_wait();
   grid_dep_launch();
@@ -146,9 +186,17 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
     bad = true;
     height = height < 0 ? 0 : a.pages;
   }
+  for (int i = tid; i < n; i += kThreads) {
+    const int l = a.lens[b0 + i], m = a.new_lens[b0 + i];
+    s_old[i] = cut_length(a, l);
+    s_new[i] = cut_length(a, m);
+    bad |= s_old[i] != l || s_new[i] != m;
+  }
+  __syncthreads();
+  auto sequence = [&](int i) { return make_sequence(a, s_old[i], s_new[i]); };
   // ---- counts, a warp per sequence
   for (int i = warp; i < n; i += 32) {
-    const Sequence s = read_sequence(a, b0 + i, &bad);
+    const Sequence s = sequence(i);
     const int back = returned(a, b0 + i, s, [](int, int, int) {});
     if (lane == 0) {
       s_taken[i] = s.taken();
@@ -218,8 +266,10 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
   }
   __syncthreads();
   // ---- back to the pool
-  for (int i = warp; i < n && total.back > 0; i += 32) {
-    const Sequence s = read_sequence(a, b0 + i, &bad);
+  const Sums end = before + s_total;
+  for (int i = warp; i < n; i += 32) {
+    if ((i + 1 < n ? s_back[i + 1] : end.back) == s_back[i]) continue;
+    const Sequence s = sequence(i);
     int* row = a.table + (size_t)(b0 + i) * a.width;
     const int first = height + s_back[i];
     returned(a, b0 + i, s, [&](int e, int page, int r) {
@@ -231,8 +281,9 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
   sync_all<kOne>();
   // ---- from the pool
   const int top = height + total.back;  // (both at most the pool's and the tables' entries)
-  for (int i = warp; i < n && total.taken > 0; i += 32) {
-    const Sequence s = read_sequence(a, b0 + i, &bad);
+  for (int i = warp; i < n; i += 32) {
+    if ((i + 1 < n ? s_taken[i + 1] : end.taken) == s_taken[i]) continue;
+    const Sequence s = sequence(i);
     int* row = a.table + (size_t)(b0 + i) * a.width;
     // entries in front of the hidden ones and behind them
     const int lo1 = s.n0, hi1 = min(s.n1, max(s.n0, s.hs < s.he ? s.hs : s.n1));
@@ -250,32 +301,62 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
     const int left = top - total.taken;
     *a.height = left < 0 ? 0 : min(left, a.pages);
   }
+  if (bad) atomicExch(a.status, 1);
+  if (a.apart) return;
   __syncthreads();
   // ---- positions and slots of the block's new tokens
-  const int lo = min(a.T, before.tokens), hi = n > 0 ? min(a.T, (before + s_total).tokens) : lo;
-  const int mask = (1 << a.shift) - 1;
+  const int lo = min(a.T, before.tokens), hi = n > 0 ? min(a.T, end.tokens) : lo;
   for (int t = lo + tid; t < hi; t += kThreads) {
-    int x = 0, m = n;  // the last sequence that begins at or before token t
-    while (m > 1) {
-      const int half = m >> 1;
-      if (s_tokens[x + half] <= t) {
-        x += half;
-        m -= half;
-      } else {
-        m = half;
-      }
+    const int x = last_at_or_before(s_tokens, 0, n, t);
+    write_token(a, t, b0 + x, s_old[x] + t - s_tokens[x]);
+  }
+  for (int t = min(a.T, total.tokens) + rank * kThreads + tid; t < a.T; t += kBlocks * kThreads)
+    write_no_token(a, t);
+}
+
+// The same for many tokens, in a launch of its own over the whole GPU: a block takes 1024
+// of them, whose sequences lie in a stretch of cu.
+constexpr int kChunk = 1024, kStretch = 2048;
+
+__global__ void __launch_bounds__(256) slot_kernel(const PageArgs a) {
+  __shared__ int s_cu[kStretch];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int total = a.cu[a.B];
+  const int t0 = blockIdx.x * kChunk, t1 = min(t0 + kChunk, total);
+  const int lane = threadIdx.x & 31;
+  // the sequences of the first and the last token, each by a whole warp's search
+  auto find = [&](int t) {
+    int lo = 0, n = a.B;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = lo + lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, at < lo + n && a.cu[at] <= t);
+      const int piece = 31 - __clz(m | 1);
+      n = min(step, n - piece * step);
+      lo += piece * step;
     }
-    const int p = a.lens[b0 + x] + t - s_tokens[x];
-    const int pos = p < 0 ? t - s_tokens[x] : p;  // (a negative length counts as none)
-    const int page = a.table[(size_t)(b0 + x) * a.width + (pos >> a.shift)];
-    a.pos[t] = pos;
-    a.slots[t] = page >= 0 ? ((long long)page << a.shift) + (pos & mask) : -1;
+    return lo;
+  };
+  int b0 = 0, b1 = 0;
+  if (t0 < t1) {
+    b0 = find(t0);
+    b1 = find(t1 - 1);
   }
-  for (int t = min(a.T, total.tokens) + rank * kThreads + tid; t < a.T; t += kBlocks * kThreads) {
-    a.pos[t] = -1;
-    a.slots[t] = -1;
+  const int n = b1 - b0 + 1;
+  const bool near = n <= kStretch;
+  for (int i = threadIdx.x; near && i < n; i += 256) s_cu[i] = a.cu[b0 + i];
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < kChunk / 256; ++x) {
+    const int t = t0 + 256 * x + threadIdx.x;
+    if (t < t1) {
+      const int i = last_at_or_before(near ? s_cu : a.cu + b0, 0, n, t);
+      const int first = near ? s_cu[i] : a.cu[b0 + i];
+      write_token(a, t, b0 + i, cut_length(a, a.lens[b0 + i]) + t - first);
+    } else if (t < a.T) {
+      write_no_token(a, t);
+    }
   }
-  if (bad) atomicExch(a.status, 1);
 }
 
 bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -310,20 +391,20 @@ extern "C" int fa_page_update(int* page_table, int table_width, int* free_pages,
   if (!status) return FA_ERR_CUDA;
   const PageArgs a{page_table, table_width, c4_shift(page_size) + 4, B, free_pages, free_count, num_pages,
                    lens, new_lens, window_left < 0 ? -1 : window_left, sinks, T, cu_seqlens, positions,
-                   reinterpret_cast<long long*>(slots), status};
+                   reinterpret_cast<long long*>(slots), status, T > kApart ? 1 : 0};
   static bool attr_done[64] = {};
   if (!attr_done[dev]) {
     if (cudaFuncSetAttribute(page_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             3 * (kMaxSequences / kCluster) * (int)sizeof(int)) != cudaSuccess)
+                             5 * (kMaxSequences / kCluster) * (int)sizeof(int)) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  const bool one = B <= 64 && T <= 4096;
+  const bool one = B <= kOneBlock;
   const int blocks = one ? 1 : kCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 3 * (size_t)((B + blocks - 1) / blocks) * sizeof(int);
+  cfg.dynamicSmemBytes = 5 * (size_t)((B + blocks - 1) / blocks) * sizeof(int);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -336,5 +417,11 @@ extern "C" int fa_page_update(int* page_table, int table_width, int* free_pages,
   if (cudaLaunchKernelEx(&cfg, one ? page_kernel<true> : page_kernel<false>, a) != cudaSuccess)
     return FA_ERR_CUDA;
   note_launches(1);
+  if (a.apart) {
+    if (launch_pdl(slot_kernel, dim3((unsigned)((T + kChunk - 1) / kChunk)), dim3(256), 0, cfg.stream, a) !=
+        cudaSuccess)
+      return FA_ERR_CUDA;
+    note_launches(1);
+  }
   return FA_OK;
 }

@@ -121,6 +121,16 @@ def test_a_bad_page_in_sight_is_reported(gpu):
     r = ref.attend(q[0], k[j], v[j])
     assert_within(o[0], r["o"], r["o_tol"], "o")
     assert_within(lse[0], r["lse"], r["lse_tol"], "lse")
+    # its tokens weigh nothing
+    w = torch.full((1, 1, 400), 0.5, device="cuda")
+    ws = torch.full((fa.cache4_attend_workspace_bytes(1, 2, 1, 64, 400),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    fa.cache4_attend(q.cuda(), cache, table, n, window_left=100, sinks=20, weights=w, workspace=ws)
+    assert fa.cache4_status() == 1
+    p, tol = (torch.zeros(1, 400, dtype=torch.float64) for _ in range(2))
+    p[:, j], tol[:, j] = r["p"], r["p_tol"]
+    assert_within(w[0], 0.5 + p, tol + 2.0 ** -23 * (0.5 + p), "weights")
+    assert bool((w[0, 0, 384:] == 0.5).all()) and bool((w[0, 0, 20:299] == 0.5).all())
 
 
 @pytest.mark.gpu
