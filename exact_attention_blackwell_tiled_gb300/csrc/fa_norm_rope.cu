@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kBlocks = 3, kGradBlocks = 2;  // per SM, forward and backward
-constexpr int kDepth = 2, kGradDepth = 1;     // steps whose rows are on their way, of a warp
+constexpr int kDepth = 4, kGradDepth = 3;     // steps whose rows are on their way, of a warp
 constexpr int kHeads = 8;  // heads of a unit where tokens are few
 
 struct Rows {
@@ -57,14 +57,6 @@ struct NormRopeArgs {
   float* dw[2];   // [D]
   int blocks;
 };
-
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
-  uint4 x;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "l"(p));
-  return x;
-}
 
 // Eight bf16 numbers as pairs of fp32.
 __device__ __forceinline__ void widen(const uint4& x, float2 (&f)[4]) {
@@ -192,26 +184,35 @@ struct Walk {
   }
 };
 
-// One row's part of a lane.
-struct Piece {
-  uint4 a, b;
-};
+// A lane's two pieces of its row of a step, on their way to shared memory: slots of its own,
+// which no other lane reads, so that its own wait is all that orders them.  Zeros where
+// the step has no row for it.
+__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
 template <int D, bool kPairs>
-__device__ __forceinline__ Piece load_row(const Rows& x, const Walk<D, kPairs>& w, const Lane<D, kPairs>& lane) {
-  Piece p;
-  p.a = p.b = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void copy_row(uint32_t dst, const Rows& x, const Walk<D, kPairs>& w,
+                                         const Lane<D, kPairs>& lane) {
   const int h = w.h + lane.sub;
-  if (w.more() && h < w.end) {
-    const __nv_bfloat16* row = x.x + w.token * x.token + h * x.head;
-    p.a = load16(row + lane.a0);
-    p.b = load16(row + lane.b0);
-  }
-  return p;
+  const bool on = w.more() && h < w.end;
+  const __nv_bfloat16* row = x.x + (on ? w.token * x.token + h * x.head : 0);
+  copy16(dst, row + lane.a0, on);
+  copy16(dst + kWarps * 32 * 16, row + lane.b0, on);
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All groups but the latest n have arrived.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
+  extern __shared__ uint4 s_rows[];  // [kDepth][2][threads]
+  constexpr uint32_t kStep = 2 * kWarps * 32 * 16;  // bytes
+  const uint32_t mine = smem_u32(s_rows + threadIdx.x);
   const L lane(a.rot);
   grid_dep_wait();
   grid_dep_launch();
@@ -225,11 +226,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const N
     if (!w.more()) continue;
     const RowsOut& out = a.out[kind];
     float2 c[4], s[4], wa[4], wb[4];
-    Piece x[kDepth];
     Walk<D, kPairs> ahead = w;
 #pragma unroll
     for (int n = 0; n < kDepth; ++n) {
-      x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
+      copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
+      end_copies();
       ahead.next();
     }
     load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
@@ -246,10 +247,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const N
           load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
         }
         float2 fa_[4], fb[4], sum = make_float2(0.f, 0.f);
-        widen(x[n].a, fa_);
-        widen(x[n].b, fb);
-        x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
-        ahead.next();
+        wait_copies<kDepth - 1>();
+        const uint4* at = s_rows + n * (kStep / 16) + threadIdx.x;
+        widen(at[0], fa_);
+        widen(at[kWarps * 32], fb);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           sum = __ffma2_rn(fa_[e], fa_[e], sum);
@@ -266,6 +267,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const N
           fb[e] = __fmul2_rn(__fmul2_rn(fb[e], r2), wb[e]);
         }
         if (lane.turns) turn<kPairs, false>(fa_, fb, c, s);
+        copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
+        end_copies();
+        ahead.next();
         const int h = w.h + lane.sub;
         if (h < w.end && (p >= 0 || a.zero)) {
           __nv_bfloat16* row = out.x + w.token * out.token + h * out.head;
@@ -276,6 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const N
         w.next();
       }
     }
+    wait_copies<0>();  // (the next kind's take the same slots)
   }
 }
 
@@ -283,6 +288,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const N
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
+  extern __shared__ uint4 s_rows[];  // [kGradDepth][x, dy][2][threads]
+  constexpr uint32_t kStep = 4 * kWarps * 32 * 16;  // bytes
+  const uint32_t mine = smem_u32(s_rows + threadIdx.x);
   __shared__ float s_dw[kWarps][D];
   const L lane(a.rot);
   const int warp = threadIdx.x >> 5;
@@ -294,12 +302,12 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
     Walk<D, kPairs> w;
     w.start(a, kind, warp * gridDim.x + blockIdx.x, kWarps * gridDim.x);
     float2 wa[4], wb[4], da[4], db[4], c[4], s[4];
-    Piece x[kGradDepth], g[kGradDepth];
     Walk<D, kPairs> ahead = w;
 #pragma unroll
     for (int n = 0; n < kGradDepth; ++n) {
-      x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
-      g[n] = load_row<D, kPairs>(a.dy[kind], ahead, lane);
+      copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
+      copy_row<D, kPairs>(mine + n * kStep + kStep / 2, a.dy[kind], ahead, lane);
+      end_copies();
       ahead.next();
     }
     load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
@@ -318,13 +326,12 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
           load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
         }
         float2 fa_[4], fb[4], ha[4], hb[4];
-        widen(x[n].a, fa_);
-        widen(x[n].b, fb);
-        widen(g[n].a, ha);
-        widen(g[n].b, hb);
-        x[n] = load_row<D, kPairs>(a.in[kind], ahead, lane);
-        g[n] = load_row<D, kPairs>(a.dy[kind], ahead, lane);
-        ahead.next();
+        wait_copies<kGradDepth - 1>();
+        const uint4* at = s_rows + n * (kStep / 16) + threadIdx.x;
+        widen(at[0], fa_);
+        widen(at[kWarps * 32], fb);
+        widen(at[2 * kWarps * 32], ha);
+        widen(at[3 * kWarps * 32], hb);
         if (lane.turns) turn<kPairs, true>(ha, hb, c, s);
         // sums of x^2 and of h x, h = g w
         float2 sx = make_float2(0.f, 0.f), sh = make_float2(0.f, 0.f);
@@ -345,6 +352,10 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
           hx += __shfl_xor_sync(0xffffffffu, hx, o);
         }
         const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
+        copy_row<D, kPairs>(mine + n * kStep + kStep / 2, a.dy[kind], ahead, lane);
+        end_copies();
+        ahead.next();
         const int h = w.h + lane.sub;
         __nv_bfloat16* row = out.x + w.token * out.token + h * out.head;
         if (p >= 0 && h < w.end) {
@@ -366,6 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
         w.next();
       }
     }
+    wait_copies<0>();
     // the warp's sums over its rows, then the block's over its warps
 #pragma unroll
     for (int o = L::kPerRow; o < 32; o <<= 1)
@@ -473,10 +485,29 @@ int grad_blocks(int sms, int T, int Hq, int Hkv) {
   return set_units(&a, (long long)sms * kGradBlocks);
 }
 
-template <typename... A>
-int launch(void (*kernel)(A...), long long grid, int threads, cudaStream_t stream, const NormRopeArgs& a) {
-  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, a) != cudaSuccess) return FA_ERR_CUDA;
+int launch(void (*kernel)(NormRopeArgs), long long grid, int threads, int smem, cudaStream_t stream,
+           const NormRopeArgs& a) {
+  if (launch_pdl(kernel, dim3((unsigned)grid), dim3(threads), smem, stream, a) != cudaSuccess) return FA_ERR_CUDA;
   note_launches(1);
+  return FA_OK;
+}
+
+// Shared memory of the kernels' rows on their way.
+constexpr int kSmem = kDepth * 2 * kWarps * 32 * 16, kGradSmem = kGradDepth * 4 * kWarps * 32 * 16;
+
+// The kernels' shared memory, once per device: 0 forward, 1 backward.
+int allow_smem(int dev) {
+  static bool done[64] = {};
+  if (done[dev]) return FA_OK;
+  const auto set = [](void (*kernel)(NormRopeArgs), int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  if (!set(norm_rope_kernel<64, false>, kSmem) || !set(norm_rope_kernel<64, true>, kSmem) ||
+      !set(norm_rope_kernel<128, false>, kSmem) || !set(norm_rope_kernel<128, true>, kSmem) ||
+      !set(norm_rope_grad_kernel<64, false>, kGradSmem) || !set(norm_rope_grad_kernel<64, true>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<128, false>, kGradSmem) || !set(norm_rope_grad_kernel<128, true>, kGradSmem))
+    return FA_ERR_CUDA;
+  done[dev] = true;
   return FA_OK;
 }
 
@@ -549,10 +580,11 @@ int fa_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, con
   a.status = fwd_status_word();
   int dev;
   DeviceInfo info;
-  if (!a.status || !current_device(&dev, &info)) return FA_ERR_CUDA;
+  if (!a.status || !current_device(&dev, &info) || allow_smem(dev) != FA_OK) return FA_ERR_CUDA;
   const auto kernel = D == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
                                : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>);
-  return launch(kernel, set_units(&a, (long long)info.sm_count * kBlocks), kWarps * 32, static_cast<cudaStream_t>(stream), a);
+  return launch(kernel, set_units(&a, (long long)info.sm_count * kBlocks), kWarps * 32, kSmem,
+                static_cast<cudaStream_t>(stream), a);
 }
 
 size_t fa_norm_rope_workspace_bytes(int T, int Hq, int Hkv, int D) {
@@ -628,9 +660,10 @@ int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
   const auto kernel =
       D == 128 ? (interleaved ? norm_rope_grad_kernel<128, true> : norm_rope_grad_kernel<128, false>)
                : (interleaved ? norm_rope_grad_kernel<64, true> : norm_rope_grad_kernel<64, false>);
-  if ((rc = launch(kernel, a.blocks, kWarps * 32, st, a))) return rc;
-  return D == 128 ? launch(norm_rope_sum_kernel<128>, 2 * 128 / 32, 1024, st, a)
-                  : launch(norm_rope_sum_kernel<64>, 2 * 64 / 32, 1024, st, a);
+  if (allow_smem(dev) != FA_OK) return FA_ERR_CUDA;
+  if ((rc = launch(kernel, a.blocks, kWarps * 32, kGradSmem, st, a))) return rc;
+  return D == 128 ? launch(norm_rope_sum_kernel<128>, 2 * 128 / 32, 1024, 0, st, a)
+                  : launch(norm_rope_sum_kernel<64>, 2 * 64 / 32, 1024, 0, st, a);
 }
 
 }  // extern "C"
