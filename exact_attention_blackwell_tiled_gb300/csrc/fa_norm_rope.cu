@@ -27,10 +27,9 @@ namespace fa {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kBlocks = 3, kGradBlocks = 2;  // per SM, forward and backward
-constexpr int kDepth = 4, kGradDepth = 3;     // steps whose rows are on their way, of a warp
-constexpr int kHeads = 8;  // heads of a unit where tokens are few
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kBlocks = 2;                // per SM
+constexpr int kDepth = 8, kGradDepth = 4;  // steps whose rows are on their way, of a warp
 
 struct Rows {
   const __nv_bfloat16* x;
@@ -41,7 +40,15 @@ struct RowsOut {
   long long token, head;
 };
 
+// How the rows are dealt to warps: a unit is a token's steps of kRows heads, q's before k's, or
+// one of `split` parts of them.
+struct Plan {
+  int steps[2], split, per;  // steps of q and of k; parts of a token, their steps
+  uint32_t units;            // below 2^31
+};
+
 struct NormRopeArgs {
+  Plan plan;
   Rows in[2], dy[2];  // q, k; the gradients of the results
   RowsOut out[2];     // the results, or the inputs' gradients
   const void* w[2];
@@ -49,12 +56,11 @@ struct NormRopeArgs {
   const float *cos, *sin;  // [P, rot / 2]
   const int* pos;          // [T]
   int T, H[2], P, rot;
-  int heads;  // of a unit
   int zero;  // rows of no sequence get zeros
   float eps;
   int* status;
-  float* part;    // [blocks, 2, D] sums of dw
-  float* dw[2];   // [D]
+  float* part;   // [blocks, 2, D] sums of dw
+  float* dw[2];  // [D]
   int blocks;
 };
 
@@ -69,12 +75,19 @@ __device__ __forceinline__ uint4 narrow(const float2 (&f)[4]) {
   return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
                     pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
+__device__ __forceinline__ void load8(const float* p, float2 (&f)[4]) {
+  const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+  f[0] = make_float2(x.x, x.y), f[1] = make_float2(x.z, x.w);
+  f[2] = make_float2(y.x, y.y), f[3] = make_float2(y.z, y.w);
+}
+__device__ __forceinline__ float2 swapped(float2 x) { return make_float2(x.y, x.x); }
+__device__ __forceinline__ float2 negated(float2 x) { return make_float2(-x.x, -x.y); }
 
 // What a lane holds of a row: elements a0 .. a0 + 7 and b0 .. b0 + 7.
 template <int D, bool kPairs>
 struct Lane {
-  static constexpr int kPerRow = D / 16;       // lanes
-  static constexpr int kRows = 32 / kPerRow;   // rows of a warp
+  static constexpr int kPerRow = D / 16;      // lanes
+  static constexpr int kRows = 32 / kPerRow;  // rows of a warp's step
   int l, sub, a0, b0;
   bool turns;  // the lane's elements are rotated
   __device__ __forceinline__ Lane(int rot) {
@@ -87,298 +100,353 @@ struct Lane {
   }
 };
 
-// 8 numbers at p, fp32 or bf16.
-__device__ __forceinline__ void load_weights(const void* w, int bf16, int at, float2 (&f)[4]) {
-  if (bf16) {
-    widen(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + at), f);
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
-    const float4 x = p[0], y = p[1];
-    f[0] = make_float2(x.x, x.y), f[1] = make_float2(x.z, x.w);
-    f[2] = make_float2(y.x, y.y), f[3] = make_float2(y.z, y.w);
-  }
-}
-
-// The lane's cosines and sines at position p: of its 8 pairs.
+// The rotation's factors for what a lane holds, at position p: an element times `own`, plus
+// its pair's other element (halves: the one of the other eight; neighbours: the one
+// beside it) times `other`.
 template <int D, bool kPairs>
-__device__ __forceinline__ void load_angles(const NormRopeArgs& a, const Lane<D, kPairs>& L, int p,
-                                            float2 (&c)[4], float2 (&s)[4]) {
+__device__ __forceinline__ void load_factors(const NormRopeArgs& a, const Lane<D, kPairs>& L, int p,
+                                             float2 (&own_a)[4], float2 (&own_b)[4],
+                                             float2 (&other_a)[4], float2 (&other_b)[4]) {
+  float2 c[4], s[4];  // of the lane's eight pairs
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] = make_float2(1.f, 1.f), s[e] = make_float2(0.f, 0.f);
-  if (!L.turns) return;
-  const size_t at = (size_t)p * (a.rot / 2) + 8 * L.l;
-#pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    const float4 x = *reinterpret_cast<const float4*>(a.cos + at + 4 * y);
-    const float4 z = *reinterpret_cast<const float4*>(a.sin + at + 4 * y);
-    c[2 * y] = make_float2(x.x, x.y), c[2 * y + 1] = make_float2(x.z, x.w);
-    s[2 * y] = make_float2(z.x, z.y), s[2 * y + 1] = make_float2(z.z, z.w);
+  if (L.turns) {
+    const size_t at = (size_t)p * (a.rot / 2) + 8 * L.l;
+    load8(a.cos + at, c);
+    load8(a.sin + at, s);
   }
-}
-
-// Rotates the lane's 8 pairs by the angle (kBack: its negative).  Halves: (a, b) element by
-// element.  Neighbours: pair e of a's four uses angle e, of b's 4 + e.
-template <bool kPairs, bool kBack>
-__device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const float2 (&c)[4],
-                                     const float2 (&s)[4]) {
-  if constexpr (kPairs) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float ca = (e & 1) ? c[e / 2].y : c[e / 2].x, sa = (e & 1) ? s[e / 2].y : s[e / 2].x;
-      const float cb = (e & 1) ? c[2 + e / 2].y : c[2 + e / 2].x;
-      const float sb = (e & 1) ? s[2 + e / 2].y : s[2 + e / 2].x;
-      const float2 x = a[e], y = b[e];
-      const float ta = kBack ? -sa : sa, tb = kBack ? -sb : sb;
-      a[e] = make_float2(fmaf(x.x, ca, -x.y * ta), fmaf(x.y, ca, x.x * ta));
-      b[e] = make_float2(fmaf(y.x, cb, -y.y * tb), fmaf(y.y, cb, y.x * tb));
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 t = kBack ? make_float2(-s[e].x, -s[e].y) : s[e];
-      const float2 n = make_float2(-t.x, -t.y);
-      const float2 x = a[e], y = b[e];
-      a[e] = __ffma2_rn(x, c[e], __fmul2_rn(y, n));
-      b[e] = __ffma2_rn(y, c[e], __fmul2_rn(x, t));
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (kPairs) {
+      // pairs 0 .. 3 are a's, 4 .. 7 b's
+      const float2 ca = c[e / 2], cb = c[2 + e / 2], sa = s[e / 2], sb = s[2 + e / 2];
+      const float x = (e & 1) ? ca.y : ca.x, y = (e & 1) ? cb.y : cb.x;
+      const float u = (e & 1) ? sa.y : sa.x, v = (e & 1) ? sb.y : sb.x;
+      own_a[e] = make_float2(x, x), own_b[e] = make_float2(y, y);
+      other_a[e] = make_float2(-u, u), other_b[e] = make_float2(-v, v);
+    } else {
+      own_a[e] = own_b[e] = c[e];
+      other_a[e] = negated(s[e]), other_b[e] = s[e];
     }
   }
 }
 
-// Token of a unit's rows: -1 where it is of no sequence, or its position has no angles.
+// The pair's other elements of a and of b.
+template <bool kPairs>
+__device__ __forceinline__ float2 other(const float2& own, const float2& across) {
+  return kPairs ? swapped(own) : across;
+}
+
+// A warp's work: units of a token's steps, kRows heads each, q's before k's.  Rows of the
+// next steps are on their way to shared memory meanwhile, in a ring of a thread's own
+// 16-byte slots: no other thread reads them, so its own wait is all that orders them.
+template <int D>
+struct Cursor {
+  static constexpr int kRows = 32 / (D / 16);
+  uint32_t u;
+  int token, i, end;  // step i of [.., end) of the token; q's come first
+  __device__ __forceinline__ bool more(const Plan& p) const { return u < p.units; }
+  __device__ __forceinline__ void place(const Plan& p) {
+    token = p.split == 1 ? (int)u : (int)(u / (uint32_t)p.split);
+    i = (int)(u - (uint32_t)token * p.split) * p.per;
+    end = min(i + p.per, p.steps[0] + p.steps[1]);
+  }
+  // Whether the next step is of another unit.
+  __device__ __forceinline__ bool next(const Plan& p, uint32_t by) {
+    if (++i < end) return false;
+    u += by;
+    place(p);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The lane's place in row (token, first head of a step + sub).
+template <typename R>
+__device__ __forceinline__ auto row_of(const R& x, int token, int h) {
+  return x.x + (token * x.token + h * x.head);
+}
+
+// A token's position; -1 where it is of no sequence, or has no angles.
 __device__ __forceinline__ int position(const NormRopeArgs& a, int token) {
   const int p = __ldg(a.pos + token);
   if (p >= a.P && (threadIdx.x & 31) == 0) atomicExch(a.status, (int)FA_ERR_INVALID_ARG);
   return p < a.P ? p : -1;
 }
 
-// A step is kRows heads of one token; a warp takes its units' steps one after the other,
-// the next one's rows on their way while it turns the present one's.  A unit is a token and
-// `heads` of its heads.
-template <int D, bool kPairs>
-struct Walk {
-  using L = Lane<D, kPairs>;
-  int token, h, end;  // the step's heads: h .. min(end, h + kRows) - 1
-  uint32_t u, stride, units;  // units are below 2^31
-  int per_token, heads, H;
-  __device__ __forceinline__ void start(const NormRopeArgs& a, int kind, uint32_t first, uint32_t by) {
-    H = a.H[kind];
-    heads = a.heads;
-    per_token = (H + heads - 1) / heads;
-    units = (uint32_t)a.T * per_token;
-    u = first;
-    stride = by;
-    place();
+// Both weight vectors as fp32 in shared memory.
+template <int D>
+__device__ __forceinline__ void load_weights(const NormRopeArgs& a, float (&s_w)[2][D]) {
+  if (threadIdx.x < 2 * D) {
+    const int kind = threadIdx.x / D, d = threadIdx.x % D;
+    s_w[kind][d] = a.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w[kind])[d])
+                            : static_cast<const float*>(a.w[kind])[d];
   }
-  __device__ __forceinline__ void place() {
-    token = (int)(u / (uint32_t)per_token);
-    h = (int)(u - (uint32_t)token * per_token) * heads;
-    end = min(H, h + heads);
-  }
-  __device__ __forceinline__ bool more() const { return u < units; }
-  __device__ __forceinline__ void next() {
-    h += L::kRows;
-    if (h >= end) {
-      u += stride;
-      place();
-    }
-  }
-};
-
-// A lane's two pieces of its row of a step, on their way to shared memory: slots of its own,
-// which no other lane reads, so that its own wait is all that orders them.  Zeros where
-// the step has no row for it.
-__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
-               : "memory");
-}
-template <int D, bool kPairs>
-__device__ __forceinline__ void copy_row(uint32_t dst, const Rows& x, const Walk<D, kPairs>& w,
-                                         const Lane<D, kPairs>& lane) {
-  const int h = w.h + lane.sub;
-  const bool on = w.more() && h < w.end;
-  const __nv_bfloat16* row = x.x + (on ? w.token * x.token + h * x.head : 0);
-  copy16(dst, row + lane.a0, on);
-  copy16(dst + kWarps * 32 * 16, row + lane.b0, on);
-}
-__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All groups but the latest n have arrived.
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32, kBlocks) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
-  extern __shared__ uint4 s_rows[];  // [kDepth][2][threads]
-  constexpr uint32_t kStep = 2 * kWarps * 32 * 16;  // bytes
-  const uint32_t mine = smem_u32(s_rows + threadIdx.x);
+  extern __shared__ uint4 s_rows[];  // [kDepth][2][kThreads]
+  __shared__ __align__(16) float s_w[2][D];
   const L lane(a.rot);
+  const uint32_t mine = smem_u32(s_rows + threadIdx.x);
   grid_dep_wait();
   grid_dep_launch();
-  const uint32_t first = (threadIdx.x >> 5) * gridDim.x + blockIdx.x, by = kWarps * gridDim.x;
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    Walk<D, kPairs> w;
-    // (the other kind's units begin where these end, so that few units spread over all warps)
-    const uint32_t shift = kind ? (uint32_t)a.T * ((a.H[0] + a.heads - 1) / a.heads) % by : 0u;
-    w.start(a, kind, first >= shift ? first - shift : first - shift + by, by);
-    if (!w.more()) continue;
-    const RowsOut& out = a.out[kind];
-    float2 c[4], s[4], wa[4], wb[4];
-    Walk<D, kPairs> ahead = w;
-#pragma unroll
-    for (int n = 0; n < kDepth; ++n) {
-      copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
-      end_copies();
-      ahead.next();
+  const uint32_t by = kWarps * gridDim.x;
+  const Plan& plan = a.plan;
+  Cursor<D> at, ahead;
+  at.u = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  at.place(plan);
+  ahead = at;
+  uint32_t slot = 0, fill = 0;  // of the ring
+  auto copy = [&]() {           // step `ahead`
+    if (ahead.more(plan)) {
+      const int kind = ahead.i >= plan.steps[0] ? 1 : 0;
+      const int h = (ahead.i - (kind ? plan.steps[0] : 0)) * L::kRows + lane.sub;
+      const bool on = h < a.H[kind];
+      const __nv_bfloat16* row = row_of(a.in[kind], ahead.token, on ? h : 0);
+      const uint32_t dst = mine + fill * (2 * kThreads * 16);
+      copy16(dst, row + lane.a0, on);
+      copy16(dst + kThreads * 16, row + lane.b0, on);
+      fill = (fill + 1) & (kDepth - 1);
+      ahead.next(plan, by);
     }
-    load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
-    load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
-    int token = -1, p = -1;
+    end_copies();
+  };
 #pragma unroll 1
-    while (w.more()) {
-#pragma unroll
-      for (int n = 0; n < kDepth; ++n) {
-        if (!w.more()) break;
-        if (w.token != token) {
-          token = w.token;
-          p = position(a, token);
-          load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
-        }
-        float2 fa_[4], fb[4], sum = make_float2(0.f, 0.f);
-        wait_copies<kDepth - 1>();
-        const uint4* at = s_rows + n * (kStep / 16) + threadIdx.x;
-        widen(at[0], fa_);
-        widen(at[kWarps * 32], fb);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum = __ffma2_rn(fa_[e], fa_[e], sum);
-          sum = __ffma2_rn(fb[e], fb[e], sum);
-        }
-        float ss = sum.x + sum.y;
-#pragma unroll
-        for (int o = L::kPerRow / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        const float2 r2 = make_float2(r, r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          fa_[e] = __fmul2_rn(__fmul2_rn(fa_[e], r2), wa[e]);
-          fb[e] = __fmul2_rn(__fmul2_rn(fb[e], r2), wb[e]);
-        }
-        if (lane.turns) turn<kPairs, false>(fa_, fb, c, s);
-        copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
-        end_copies();
-        ahead.next();
-        const int h = w.h + lane.sub;
-        if (h < w.end && (p >= 0 || a.zero)) {
-          __nv_bfloat16* row = out.x + w.token * out.token + h * out.head;
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(row + lane.a0) = p < 0 ? zero : narrow(fa_);
-          *reinterpret_cast<uint4*>(row + lane.b0) = p < 0 ? zero : narrow(fb);
-        }
-        w.next();
+  for (int n = 0; n < kDepth; ++n) copy();
+  load_weights<D>(a, s_w);
+  __syncthreads();
+  int p = at.more(plan) ? position(a, at.token) : -1;
+#pragma unroll 1
+  while (at.more(plan)) {
+    const int token = at.token, end = at.end;
+    // the next unit's position, and its angles on their way to L2
+    int p_next = -1;
+    if (at.u + by < plan.units) {
+      Cursor<D> then = at;
+      then.u += by;
+      then.place(plan);
+      p_next = position(a, then.token);
+      if (p_next >= 0 && lane.sub == 0 && lane.turns) {
+        const size_t to = (size_t)p_next * (a.rot / 2) + 8 * lane.l;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.cos + to));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.sin + to));
       }
     }
-    wait_copies<0>();  // (the next kind's take the same slots)
+    float2 own_a[4], own_b[4], other_a[4], other_b[4];
+#pragma unroll 1
+    while (at.i < end) {
+      const int kind = at.i >= plan.steps[0] ? 1 : 0;
+      {
+        // the rotation's factors times the weights
+        float2 wa[4], wb[4];
+        load_factors<D, kPairs>(a, lane, p < 0 ? 0 : p, own_a, own_b, other_a, other_b);
+        load8(&s_w[kind][lane.a0], wa);
+        load8(&s_w[kind][lane.b0], wb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          own_a[e] = __fmul2_rn(own_a[e], wa[e]);
+          own_b[e] = __fmul2_rn(own_b[e], wb[e]);
+          other_a[e] = __fmul2_rn(other_a[e], other<kPairs>(wa[e], wb[e]));
+          other_b[e] = __fmul2_rn(other_b[e], other<kPairs>(wb[e], wa[e]));
+        }
+      }
+      const int stop = kind ? end : min(end, plan.steps[0]);
+      int h = (at.i - (kind ? plan.steps[0] : 0)) * L::kRows + lane.sub;
+      const RowsOut& out = a.out[kind];
+      __nv_bfloat16* row = row_of(out, token, h);
+      const long long step = L::kRows * out.head;
+      const int H = p >= 0 || a.zero ? a.H[kind] : 0;
+#pragma unroll 1
+      for (; at.i < stop; ++at.i, h += L::kRows, row += step) {
+        wait_copies<kDepth - 1>();
+        float2 xa[4], xb[4], sum = make_float2(0.f, 0.f), more = sum;
+        const uint4* src = s_rows + slot * (2 * kThreads) + threadIdx.x;
+        widen(src[0], xa);
+        widen(src[kThreads], xb);
+        slot = (slot + 1) & (kDepth - 1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum = __ffma2_rn(xa[e], xa[e], sum);
+          more = __ffma2_rn(xb[e], xb[e], more);
+        }
+        float ss = (sum.x + sum.y) + (more.x + more.y);
+#pragma unroll
+        for (int o = L::kPerRow / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        copy();
+        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        const float2 r2 = make_float2(r, r);
+        float2 ya[4], yb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 za = __fmul2_rn(xa[e], own_a[e]), zb = __fmul2_rn(xb[e], own_b[e]);
+          ya[e] = __fmul2_rn(__ffma2_rn(other<kPairs>(xa[e], xb[e]), other_a[e], za), r2);
+          yb[e] = __fmul2_rn(__ffma2_rn(other<kPairs>(xb[e], xa[e]), other_b[e], zb), r2);
+        }
+        if (h < H) {
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(row + lane.a0) = p < 0 ? zero : narrow(ya);
+          *reinterpret_cast<uint4*>(row + lane.b0) = p < 0 ? zero : narrow(yb);
+        }
+      }
+    }
+    at.u += by;
+    at.place(plan);
+    p = p_next;
   }
 }
 
-// The warps walk q's units, then k's, and sum dw as they go.
+// The same walk over q's units, then over k's; a warp sums dw over its rows of a kind, and
+// the sums of its lanes, then of the block's warps, meet in shared memory.
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
-  extern __shared__ uint4 s_rows[];  // [kGradDepth][x, dy][2][threads]
-  constexpr uint32_t kStep = 4 * kWarps * 32 * 16;  // bytes
-  const uint32_t mine = smem_u32(s_rows + threadIdx.x);
-  __shared__ float s_dw[kWarps][D];
+  extern __shared__ uint4 s_rows[];  // [kGradDepth][x, dy][2][kThreads]
+  __shared__ __align__(16) float s_w[2][D], s_dw[kWarps][D];
   const L lane(a.rot);
+  const uint32_t mine = smem_u32(s_rows + threadIdx.x);
   const int warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
+  const uint32_t by = kWarps * gridDim.x;
+  load_weights<D>(a, s_w);
+  __syncthreads();
 #pragma unroll 1
   for (int kind = 0; kind < 2; ++kind) {
-    const RowsOut& out = a.out[kind];
-    Walk<D, kPairs> w;
-    w.start(a, kind, warp * gridDim.x + blockIdx.x, kWarps * gridDim.x);
-    float2 wa[4], wb[4], da[4], db[4], c[4], s[4];
-    Walk<D, kPairs> ahead = w;
-#pragma unroll
-    for (int n = 0; n < kGradDepth; ++n) {
-      copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
-      copy_row<D, kPairs>(mine + n * kStep + kStep / 2, a.dy[kind], ahead, lane);
+    Plan plan = a.plan;
+    plan.steps[0] = a.plan.steps[kind];
+    plan.steps[1] = 0;
+    plan.per = (plan.steps[0] + plan.split - 1) / plan.split;
+    Cursor<D> at, ahead;
+    at.u = warp * gridDim.x + blockIdx.x;
+    at.place(plan);
+    ahead = at;
+    // (a part of a token may have no steps: then it is passed over)
+    uint32_t slot = 0, fill = 0;
+    auto copy = [&]() {
+      while (ahead.more(plan) && ahead.i >= ahead.end) {
+        ahead.u += by;
+        ahead.place(plan);
+      }
+      if (ahead.more(plan)) {
+        const int h = ahead.i * L::kRows + lane.sub;
+        const bool on = h < a.H[kind];
+        const __nv_bfloat16* x = row_of(a.in[kind], ahead.token, on ? h : 0);
+        const __nv_bfloat16* g = row_of(a.dy[kind], ahead.token, on ? h : 0);
+        const uint32_t dst = mine + fill * (4 * kThreads * 16);
+        copy16(dst, x + lane.a0, on);
+        copy16(dst + kThreads * 16, x + lane.b0, on);
+        copy16(dst + 2 * kThreads * 16, g + lane.a0, on);
+        copy16(dst + 3 * kThreads * 16, g + lane.b0, on);
+        fill = (fill + 1) & (kGradDepth - 1);
+        ++ahead.i;
+      }
       end_copies();
-      ahead.next();
-    }
-    load_weights(a.w[kind], a.w_bf16, lane.a0, wa);
-    load_weights(a.w[kind], a.w_bf16, lane.b0, wb);
+    };
+#pragma unroll 1
+    for (int n = 0; n < kGradDepth; ++n) copy();
+    float2 wa[4], wb[4], da[4], db[4];
+    load8(&s_w[kind][lane.a0], wa);
+    load8(&s_w[kind][lane.b0], wb);
 #pragma unroll
     for (int e = 0; e < 4; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
-    int token = -1, p = -1;
+    int p = at.more(plan) ? position(a, at.token) : -1;
 #pragma unroll 1
-    while (w.more()) {
-#pragma unroll
-      for (int n = 0; n < kGradDepth; ++n) {
-        if (!w.more()) break;
-        if (w.token != token) {
-          token = w.token;
-          p = position(a, token);
-          load_angles<D, kPairs>(a, lane, p < 0 ? 0 : p, c, s);
+    while (at.more(plan)) {
+      const int token = at.token;
+      int p_next = -1;
+      if (at.u + by < plan.units) {
+        Cursor<D> then = at;
+        then.u += by;
+        then.place(plan);
+        p_next = position(a, then.token);
+        if (p_next >= 0 && lane.sub == 0 && lane.turns) {
+          const size_t to = (size_t)p_next * (a.rot / 2) + 8 * lane.l;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.cos + to));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.sin + to));
         }
-        float2 fa_[4], fb[4], ha[4], hb[4];
+      }
+      // the transposed rotation: the same factors, the other one's sign turned
+      float2 own_a[4], own_b[4], other_a[4], other_b[4];
+      load_factors<D, kPairs>(a, lane, p < 0 ? 0 : p, own_a, own_b, other_a, other_b);
+      int h = at.i * L::kRows + lane.sub;
+      const RowsOut& out = a.out[kind];
+      __nv_bfloat16* row = row_of(out, token, h);
+      const long long step = L::kRows * out.head;
+      const int H = a.H[kind];
+#pragma unroll 1
+      for (; at.i < at.end; ++at.i, h += L::kRows, row += step) {
         wait_copies<kGradDepth - 1>();
-        const uint4* at = s_rows + n * (kStep / 16) + threadIdx.x;
-        widen(at[0], fa_);
-        widen(at[kWarps * 32], fb);
-        widen(at[2 * kWarps * 32], ha);
-        widen(at[3 * kWarps * 32], hb);
-        if (lane.turns) turn<kPairs, true>(ha, hb, c, s);
-        // sums of x^2 and of h x, h = g w
-        float2 sx = make_float2(0.f, 0.f), sh = make_float2(0.f, 0.f);
-        float2 ta[4], tb[4];  // g x
+        float2 xa[4], xb[4], ga[4], gb[4];
+        const uint4* src = s_rows + slot * (4 * kThreads) + threadIdx.x;
+        {
+          float2 ya[4], yb[4];
+          widen(src[2 * kThreads], ya);
+          widen(src[3 * kThreads], yb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 za = __fmul2_rn(ya[e], own_a[e]), zb = __fmul2_rn(yb[e], own_b[e]);
+            ga[e] = __ffma2_rn(other<kPairs>(ya[e], yb[e]), kPairs ? swapped(other_a[e]) : other_b[e], za);
+            gb[e] = __ffma2_rn(other<kPairs>(yb[e], ya[e]), kPairs ? swapped(other_b[e]) : other_a[e], zb);
+          }
+        }
+        widen(src[0], xa);
+        widen(src[kThreads], xb);
+        slot = (slot + 1) & (kGradDepth - 1);
+        // sums of x^2 and of h x, h = g w; g x
+        float2 sx = make_float2(0.f, 0.f), sy = sx, sh = sx, sg = sx, ta[4], tb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sx = __ffma2_rn(fa_[e], fa_[e], sx);
-          sx = __ffma2_rn(fb[e], fb[e], sx);
-          ta[e] = __fmul2_rn(ha[e], fa_[e]);
-          tb[e] = __fmul2_rn(hb[e], fb[e]);
+          sx = __ffma2_rn(xa[e], xa[e], sx);
+          sy = __ffma2_rn(xb[e], xb[e], sy);
+          ta[e] = __fmul2_rn(ga[e], xa[e]);
+          tb[e] = __fmul2_rn(gb[e], xb[e]);
           sh = __ffma2_rn(ta[e], wa[e], sh);
-          sh = __ffma2_rn(tb[e], wb[e], sh);
+          sg = __ffma2_rn(tb[e], wb[e], sg);
         }
-        float ss = sx.x + sx.y, hx = sh.x + sh.y;
+        float ss = (sx.x + sx.y) + (sy.x + sy.y), hx = (sh.x + sh.y) + (sg.x + sg.y);
 #pragma unroll
         for (int o = L::kPerRow / 2; o > 0; o >>= 1) {
           ss += __shfl_xor_sync(0xffffffffu, ss, o);
           hx += __shfl_xor_sync(0xffffffffu, hx, o);
         }
+        copy();
         const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        copy_row<D, kPairs>(mine + n * kStep, a.in[kind], ahead, lane);
-        copy_row<D, kPairs>(mine + n * kStep + kStep / 2, a.dy[kind], ahead, lane);
-        end_copies();
-        ahead.next();
-        const int h = w.h + lane.sub;
-        __nv_bfloat16* row = out.x + w.token * out.token + h * out.head;
-        if (p >= 0 && h < w.end) {
-          const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
-          const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+        if (h < H) {
+          if (p >= 0) {
+            const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
+            const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            da[e] = __ffma2_rn(ta[e], r2, da[e]);
-            db[e] = __ffma2_rn(tb[e], r2, db[e]);
-            ha[e] = __ffma2_rn(__fmul2_rn(ha[e], wa[e]), r2, __fmul2_rn(fa_[e], m2));
-            hb[e] = __ffma2_rn(__fmul2_rn(hb[e], wb[e]), r2, __fmul2_rn(fb[e], m2));
+            for (int e = 0; e < 4; ++e) {
+              da[e] = __ffma2_rn(ta[e], r2, da[e]);
+              db[e] = __ffma2_rn(tb[e], r2, db[e]);
+              ga[e] = __ffma2_rn(__fmul2_rn(ga[e], wa[e]), r2, __fmul2_rn(xa[e], m2));
+              gb[e] = __ffma2_rn(__fmul2_rn(gb[e], wb[e]), r2, __fmul2_rn(xb[e], m2));
+            }
+            *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ga);
+            *reinterpret_cast<uint4*>(row + lane.b0) = narrow(gb);
+          } else if (a.zero) {
+            *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
           }
-          *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ha);
-          *reinterpret_cast<uint4*>(row + lane.b0) = narrow(hb);
-        } else if (a.zero && h < w.end) {
-          *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
         }
-        w.next();
       }
+      at.u += by;
+      at.place(plan);
+      p = p_next;
     }
-    wait_copies<0>();
-    // the warp's sums over its rows, then the block's over its warps
+    wait_copies<0>();  // (the next kind's take the same slots)
 #pragma unroll
     for (int o = L::kPerRow; o < 32; o <<= 1)
 #pragma unroll
@@ -400,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradBlocks) norm_rope_grad_kerne
     if (threadIdx.x < D) {
       float sum = 0.f;
 #pragma unroll
-      for (int w2 = 0; w2 < kWarps; ++w2) sum += s_dw[w2][threadIdx.x];
+      for (int w = 0; w < kWarps; ++w) sum += s_dw[w][threadIdx.x];
       a.part[((size_t)blockIdx.x * 2 + kind) * D + threadIdx.x] = sum;
     }
   }
@@ -414,7 +482,7 @@ __global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const NormRopeArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 10
   for (int b = warp; b < a.blocks; b += 32) sum += a.part[(size_t)b * 2 * D + col];
   s_sum[warp][lane] = sum;
   __syncthreads();
@@ -450,9 +518,8 @@ int check_shape(int T, int Hq, int Hkv, int D, int P, int rot, float eps) {
   if (T < 0 || Hq < 1 || Hkv < 1 || P < 1 || !std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (rot < 16 || rot > D || rot % 16) return FA_ERR_INVALID_ARG;
-  // units of eight heads, and warps of blocks, are counted in 32 bits
-  if ((long long)T * (Hq / kHeads + Hkv / kHeads + 2) >= (1LL << 31) || Hq > (1 << 20) || Hkv > (1 << 20))
-    return FA_ERR_INVALID_ARG;
+  // (units, and those a warp looks ahead, are counted in 32 bits: T where it is large)
+  if (T > (1 << 30) || Hq > (1 << 20) || Hkv > (1 << 20)) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -466,24 +533,26 @@ int strides(const fa_packed_stride* s, int H, int D, bool written, long long* to
   return (*token & 7) || (*head & 7) ? FA_ERR_MISALIGNED : FA_OK;
 }
 
-// A unit's heads: few where that gives no warp more than kFew units, else a token's, so
-// that its angles are loaded once.  Returns the grid, at most `most` blocks.
-constexpr int kFew = 4;
-int set_units(NormRopeArgs* a, long long most) {
-  const int H = a->H[0] > a->H[1] ? a->H[0] : a->H[1];
-  const auto count = [&](int heads) {
-    return (long long)a->T * ((a->H[0] + heads - 1) / heads + (a->H[1] + heads - 1) / heads);
-  };
-  a->heads = count(kHeads) <= kFew * most * kWarps ? kHeads : (H + 7) / 8 * 8;
-  const long long blocks = (count(a->heads) + kWarps - 1) / kWarps;
-  return (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
+// Splits tokens where they are fewer than the warps of the grid, into parts of two steps at
+// least; returns the grid: a warp of every SM before a second one of any.
+int set_plan(NormRopeArgs* a, int D, int sms, bool backward) {
+  const int rows = 32 / (D / 16);
+  Plan& p = a->plan;
+  for (int i = 0; i < 2; ++i) p.steps[i] = (a->H[i] + rows - 1) / rows;
+  const int steps = backward ? (p.steps[0] > p.steps[1] ? p.steps[0] : p.steps[1]) : p.steps[0] + p.steps[1];
+  const long long warps = (long long)sms * kBlocks * kWarps;
+  long long split = a->T > 0 ? warps / a->T : 1;
+  if (split > steps / 2) split = steps / 2;
+  p.split = split < 1 ? 1 : (int)split;
+  p.per = (steps + p.split - 1) / p.split;
+  if (!backward) p.split = (steps + p.per - 1) / p.per;  // (no part without steps)
+  p.units = (uint32_t)((long long)a->T * p.split);
+  const long long grid = p.units < 1 ? 1 : p.units, most = (long long)sms * kBlocks;
+  return (int)(grid < most ? grid : most);
 }
 
-int grad_blocks(int sms, int T, int Hq, int Hkv) {
-  NormRopeArgs a{};
-  a.T = T, a.H[0] = Hq, a.H[1] = Hkv;
-  return set_units(&a, (long long)sms * kGradBlocks);
-}
+// Shared memory of the rings.
+constexpr int kSmem = kDepth * 2 * kThreads * 16, kGradSmem = kGradDepth * 4 * kThreads * 16;
 
 int launch(void (*kernel)(NormRopeArgs), long long grid, int threads, int smem, cudaStream_t stream,
            const NormRopeArgs& a) {
@@ -492,9 +561,6 @@ int launch(void (*kernel)(NormRopeArgs), long long grid, int threads, int smem, 
   return FA_OK;
 }
 
-// Shared memory of the kernels' rows on their way.
-constexpr int kSmem = kDepth * 2 * kWarps * 32 * 16, kGradSmem = kGradDepth * 4 * kWarps * 32 * 16;
-
 // The kernels' shared memory, once per device: 0 forward, 1 backward.
 int allow_smem(int dev) {
   static bool done[64] = {};
@@ -502,10 +568,14 @@ int allow_smem(int dev) {
   const auto set = [](void (*kernel)(NormRopeArgs), int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  if (!set(norm_rope_kernel<64, false>, kSmem) || !set(norm_rope_kernel<64, true>, kSmem) ||
-      !set(norm_rope_kernel<128, false>, kSmem) || !set(norm_rope_kernel<128, true>, kSmem) ||
-      !set(norm_rope_grad_kernel<64, false>, kGradSmem) || !set(norm_rope_grad_kernel<64, true>, kGradSmem) ||
-      !set(norm_rope_grad_kernel<128, false>, kGradSmem) || !set(norm_rope_grad_kernel<128, true>, kGradSmem))
+  if (!set(norm_rope_kernel<64, false>, kSmem) ||
+      !set(norm_rope_kernel<64, true>, kSmem) ||
+      !set(norm_rope_kernel<128, false>, kSmem) ||
+      !set(norm_rope_kernel<128, true>, kSmem) ||
+      !set(norm_rope_grad_kernel<64, false>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<64, true>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<128, false>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<128, true>, kGradSmem))
     return FA_ERR_CUDA;
   done[dev] = true;
   return FA_OK;
@@ -583,7 +653,8 @@ int fa_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, con
   if (!a.status || !current_device(&dev, &info) || allow_smem(dev) != FA_OK) return FA_ERR_CUDA;
   const auto kernel = D == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
                                : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>);
-  return launch(kernel, set_units(&a, (long long)info.sm_count * kBlocks), kWarps * 32, kSmem,
+  return launch(kernel, set_plan(&a, D, info.sm_count, false), kThreads,
+                kSmem,
                 static_cast<cudaStream_t>(stream), a);
 }
 
@@ -592,7 +663,10 @@ size_t fa_norm_rope_workspace_bytes(int T, int Hq, int Hkv, int D) {
   int dev;
   DeviceInfo info;
   const int sms = current_device(&dev, &info) ? info.sm_count : 0;
-  return sms < 1 ? 0 : (size_t)grad_blocks(sms, T, Hq, Hkv) * 2 * D * sizeof(float);
+  if (sms < 1) return 0;
+  NormRopeArgs a{};
+  a.T = T, a.H[0] = Hq, a.H[1] = Hkv;
+  return (size_t)set_plan(&a, D, sms, true) * 2 * D * sizeof(float);
 }
 
 int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq,
@@ -630,7 +704,7 @@ int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
   a.T = T;
   a.H[0] = Hq;
   a.H[1] = Hkv;
-  a.blocks = set_units(&a, (long long)info.sm_count * kGradBlocks);
+  a.blocks = set_plan(&a, D, info.sm_count, true);
   if (workspace_bytes < (size_t)a.blocks * 2 * D * sizeof(float)) return FA_ERR_WORKSPACE;
   a.in[0].x = static_cast<const __nv_bfloat16*>(q);
   a.in[1].x = static_cast<const __nv_bfloat16*>(k);
@@ -661,7 +735,8 @@ int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
       D == 128 ? (interleaved ? norm_rope_grad_kernel<128, true> : norm_rope_grad_kernel<128, false>)
                : (interleaved ? norm_rope_grad_kernel<64, true> : norm_rope_grad_kernel<64, false>);
   if (allow_smem(dev) != FA_OK) return FA_ERR_CUDA;
-  if ((rc = launch(kernel, a.blocks, kWarps * 32, kGradSmem, st, a))) return rc;
+  if ((rc = launch(kernel, a.blocks, kThreads, kGradSmem,
+                   st, a))) return rc;
   return D == 128 ? launch(norm_rope_sum_kernel<128>, 2 * 128 / 32, 1024, 0, st, a)
                   : launch(norm_rope_sum_kernel<64>, 2 * 64 / 32, 1024, 0, st, a);
 }

@@ -490,8 +490,8 @@ int fa_cache4_status(fa_stream_t stream);
  *     not written (zero_skipped != 0: become zeros); one from table_rows on counts as such
  *     and is recorded: fa_fwd_status returns FA_ERR_INVALID_ARG.
  * T >= 0; D in {64, 128}; rot a multiple of 16 up to D; eps >= 0 (a row of zeros with eps 0
- * is NaN); Hq, Hkv at most 2^20 and T (Hq / 8 + Hkv / 8 + 2) below 2^31.  Tensors 16-byte
- * aligned, positions 4-byte.
+ * is NaN); Hq, Hkv at most 2^20 and T at most 2^30.  Tensors 16-byte aligned, positions
+ * 4-byte.
  */
 int fa_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
                      const void* k_weight, int weight_bf16, const float* cos, const float* sin,

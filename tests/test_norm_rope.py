@@ -106,7 +106,7 @@ def test_refusals(L):
     assert fwd(s=(-128, 64)) == 1
     assert fwd(s=(128, 56)) == 1            # the results' heads would overlap
     assert fwd(T=0, q=None, pos=None) == 0
-    assert fwd(T=1 << 30, Hq=64) == 1
+    assert fwd(T=(1 << 30) + 1) == 1 and fwd(Hq=(1 << 20) + 1) == 1
 
     def bwd(dw=P, dy=P, ws=P, T=4):
         return L.fa_norm_rope_bwd(P, P, dy, P, P, P, dw, P, P, P, 0, P, P, P, T, 2, 1, 64, 8, 64, 0,
