@@ -59,9 +59,9 @@ struct NormRopeArgs {
   int zero;  // rows of no sequence get zeros
   float eps;
   int* status;
-  float* part;   // [blocks, 2, D] sums of dw
+  float* part;   // [blocks, D] sums of dw, the first blocks_q of them q's
   float* dw[2];  // [D]
-  int blocks;
+  int blocks, blocks_q;
 };
 
 // Eight bf16 numbers as pairs of fp32.
@@ -307,8 +307,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const Norm
   }
 }
 
-// The same walk over q's units, then over k's; a warp sums dw over its rows of a kind, and
-// the sums of its lanes, then of the block's warps, meet in shared memory.
+// The same walk, by blocks of their own for q and for k (one after the other in every block,
+// the second would wait for its first rows again).  A warp sums dw over its rows, and the
+// sums of its lanes, then of the block's warps, meet in shared memory.
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
@@ -319,171 +320,169 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_grad_kernel(const
   const int warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  const uint32_t by = kWarps * gridDim.x;
+  const int kind = (int)blockIdx.x >= a.blocks_q ? 1 : 0;
+  const uint32_t blocks = kind ? gridDim.x - a.blocks_q : a.blocks_q;
+  const uint32_t by = kWarps * blocks;
+  Plan plan = a.plan;
+  plan.steps[0] = a.plan.steps[kind];
+  plan.steps[1] = 0;
+  plan.per = (plan.steps[0] + plan.split - 1) / plan.split;
+  Cursor<D> at, ahead;
+  at.u = warp * blocks + blockIdx.x - (kind ? a.blocks_q : 0);
+  at.place(plan);
+  ahead = at;
+  // (a part of a token may have no steps: then it is passed over)
+  uint32_t slot = 0, fill = 0;
+  auto copy = [&]() {
+    while (ahead.more(plan) && ahead.i >= ahead.end) {
+      ahead.u += by;
+      ahead.place(plan);
+    }
+    if (ahead.more(plan)) {
+      const int h = ahead.i * L::kRows + lane.sub;
+      const bool on = h < a.H[kind];
+      const __nv_bfloat16* x = row_of(a.in[kind], ahead.token, on ? h : 0);
+      const __nv_bfloat16* g = row_of(a.dy[kind], ahead.token, on ? h : 0);
+      const uint32_t dst = mine + fill * (4 * kThreads * 16);
+      copy16(dst, x + lane.a0, on);
+      copy16(dst + kThreads * 16, x + lane.b0, on);
+      copy16(dst + 2 * kThreads * 16, g + lane.a0, on);
+      copy16(dst + 3 * kThreads * 16, g + lane.b0, on);
+      fill = (fill + 1) & (kGradDepth - 1);
+      ++ahead.i;
+    }
+    end_copies();
+  };
+#pragma unroll 1
+  for (int n = 0; n < kGradDepth; ++n) copy();
   load_weights<D>(a, s_w);
   __syncthreads();
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    Plan plan = a.plan;
-    plan.steps[0] = a.plan.steps[kind];
-    plan.steps[1] = 0;
-    plan.per = (plan.steps[0] + plan.split - 1) / plan.split;
-    Cursor<D> at, ahead;
-    at.u = warp * gridDim.x + blockIdx.x;
-    at.place(plan);
-    ahead = at;
-    // (a part of a token may have no steps: then it is passed over)
-    uint32_t slot = 0, fill = 0;
-    auto copy = [&]() {
-      while (ahead.more(plan) && ahead.i >= ahead.end) {
-        ahead.u += by;
-        ahead.place(plan);
-      }
-      if (ahead.more(plan)) {
-        const int h = ahead.i * L::kRows + lane.sub;
-        const bool on = h < a.H[kind];
-        const __nv_bfloat16* x = row_of(a.in[kind], ahead.token, on ? h : 0);
-        const __nv_bfloat16* g = row_of(a.dy[kind], ahead.token, on ? h : 0);
-        const uint32_t dst = mine + fill * (4 * kThreads * 16);
-        copy16(dst, x + lane.a0, on);
-        copy16(dst + kThreads * 16, x + lane.b0, on);
-        copy16(dst + 2 * kThreads * 16, g + lane.a0, on);
-        copy16(dst + 3 * kThreads * 16, g + lane.b0, on);
-        fill = (fill + 1) & (kGradDepth - 1);
-        ++ahead.i;
-      }
-      end_copies();
-    };
-#pragma unroll 1
-    for (int n = 0; n < kGradDepth; ++n) copy();
-    float2 wa[4], wb[4], da[4], db[4];
-    load8(&s_w[kind][lane.a0], wa);
-    load8(&s_w[kind][lane.b0], wb);
+  float2 wa[4], wb[4], da[4], db[4];
+  load8(&s_w[kind][lane.a0], wa);
+  load8(&s_w[kind][lane.b0], wb);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
-    int p = at.more(plan) ? position(a, at.token) : -1;
+  for (int e = 0; e < 4; ++e) da[e] = db[e] = make_float2(0.f, 0.f);
+  int p = at.more(plan) ? position(a, at.token) : -1;
 #pragma unroll 1
-    while (at.more(plan)) {
-      const int token = at.token;
-      int p_next = -1;
-      if (at.u + by < plan.units) {
-        Cursor<D> then = at;
-        then.u += by;
-        then.place(plan);
-        p_next = position(a, then.token);
-        if (p_next >= 0 && lane.sub == 0 && lane.turns) {
-          const size_t to = (size_t)p_next * (a.rot / 2) + 8 * lane.l;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.cos + to));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.sin + to));
-        }
+  while (at.more(plan)) {
+    const int token = at.token;
+    int p_next = -1;
+    if (at.u + by < plan.units) {
+      Cursor<D> then = at;
+      then.u += by;
+      then.place(plan);
+      p_next = position(a, then.token);
+      if (p_next >= 0 && lane.sub == 0 && lane.turns) {
+        const size_t to = (size_t)p_next * (a.rot / 2) + 8 * lane.l;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.cos + to));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.sin + to));
       }
-      // the transposed rotation: the same factors, the other one's sign turned
-      float2 own_a[4], own_b[4], other_a[4], other_b[4];
-      load_factors<D, kPairs>(a, lane, p < 0 ? 0 : p, own_a, own_b, other_a, other_b);
-      int h = at.i * L::kRows + lane.sub;
-      const RowsOut& out = a.out[kind];
-      __nv_bfloat16* row = row_of(out, token, h);
-      const long long step = L::kRows * out.head;
-      const int H = a.H[kind];
+    }
+    // the transposed rotation: the same factors, the other one's sign turned
+    float2 own_a[4], own_b[4], other_a[4], other_b[4];
+    load_factors<D, kPairs>(a, lane, p < 0 ? 0 : p, own_a, own_b, other_a, other_b);
+    int h = at.i * L::kRows + lane.sub;
+    const RowsOut& out = a.out[kind];
+    __nv_bfloat16* row = row_of(out, token, h);
+    const long long step = L::kRows * out.head;
+    const int H = a.H[kind];
 #pragma unroll 1
-      for (; at.i < at.end; ++at.i, h += L::kRows, row += step) {
-        wait_copies<kGradDepth - 1>();
-        float2 xa[4], xb[4], ga[4], gb[4];
-        const uint4* src = s_rows + slot * (4 * kThreads) + threadIdx.x;
-        {
-          float2 ya[4], yb[4];
-          widen(src[2 * kThreads], ya);
-          widen(src[3 * kThreads], yb);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 za = __fmul2_rn(ya[e], own_a[e]), zb = __fmul2_rn(yb[e], own_b[e]);
-            ga[e] = __ffma2_rn(other<kPairs>(ya[e], yb[e]), kPairs ? swapped(other_a[e]) : other_b[e], za);
-            gb[e] = __ffma2_rn(other<kPairs>(yb[e], ya[e]), kPairs ? swapped(other_b[e]) : other_a[e], zb);
-          }
-        }
-        widen(src[0], xa);
-        widen(src[kThreads], xb);
-        slot = (slot + 1) & (kGradDepth - 1);
-        // sums of x^2 and of h x, h = g w; g x
-        float2 sx = make_float2(0.f, 0.f), sy = sx, sh = sx, sg = sx, ta[4], tb[4];
+    for (; at.i < at.end; ++at.i, h += L::kRows, row += step) {
+      wait_copies<kGradDepth - 1>();
+      float2 xa[4], xb[4], ga[4], gb[4];
+      const uint4* src = s_rows + slot * (4 * kThreads) + threadIdx.x;
+      {
+        float2 ya[4], yb[4];
+        widen(src[2 * kThreads], ya);
+        widen(src[3 * kThreads], yb);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sx = __ffma2_rn(xa[e], xa[e], sx);
-          sy = __ffma2_rn(xb[e], xb[e], sy);
-          ta[e] = __fmul2_rn(ga[e], xa[e]);
-          tb[e] = __fmul2_rn(gb[e], xb[e]);
-          sh = __ffma2_rn(ta[e], wa[e], sh);
-          sg = __ffma2_rn(tb[e], wb[e], sg);
+          const float2 za = __fmul2_rn(ya[e], own_a[e]), zb = __fmul2_rn(yb[e], own_b[e]);
+          ga[e] = __ffma2_rn(other<kPairs>(ya[e], yb[e]), kPairs ? swapped(other_a[e]) : other_b[e], za);
+          gb[e] = __ffma2_rn(other<kPairs>(yb[e], ya[e]), kPairs ? swapped(other_b[e]) : other_a[e], zb);
         }
-        float ss = (sx.x + sx.y) + (sy.x + sy.y), hx = (sh.x + sh.y) + (sg.x + sg.y);
+      }
+      widen(src[0], xa);
+      widen(src[kThreads], xb);
+      slot = (slot + 1) & (kGradDepth - 1);
+      // sums of x^2 and of h x, h = g w; g x
+      float2 sx = make_float2(0.f, 0.f), sy = sx, sh = sx, sg = sx, ta[4], tb[4];
 #pragma unroll
-        for (int o = L::kPerRow / 2; o > 0; o >>= 1) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          hx += __shfl_xor_sync(0xffffffffu, hx, o);
-        }
-        copy();
-        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-        if (h < H) {
-          if (p >= 0) {
-            const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
-            const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+      for (int e = 0; e < 4; ++e) {
+        sx = __ffma2_rn(xa[e], xa[e], sx);
+        sy = __ffma2_rn(xb[e], xb[e], sy);
+        ta[e] = __fmul2_rn(ga[e], xa[e]);
+        tb[e] = __fmul2_rn(gb[e], xb[e]);
+        sh = __ffma2_rn(ta[e], wa[e], sh);
+        sg = __ffma2_rn(tb[e], wb[e], sg);
+      }
+      float ss = (sx.x + sx.y) + (sy.x + sy.y), hx = (sh.x + sh.y) + (sg.x + sg.y);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              da[e] = __ffma2_rn(ta[e], r2, da[e]);
-              db[e] = __ffma2_rn(tb[e], r2, db[e]);
-              ga[e] = __ffma2_rn(__fmul2_rn(ga[e], wa[e]), r2, __fmul2_rn(xa[e], m2));
-              gb[e] = __ffma2_rn(__fmul2_rn(gb[e], wb[e]), r2, __fmul2_rn(xb[e], m2));
-            }
-            *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ga);
-            *reinterpret_cast<uint4*>(row + lane.b0) = narrow(gb);
-          } else if (a.zero) {
-            *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
+      for (int o = L::kPerRow / 2; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        hx += __shfl_xor_sync(0xffffffffu, hx, o);
+      }
+      copy();
+      const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+      if (h < H) {
+        if (p >= 0) {
+          const float m = -(hx * r * (1.f / D)) * (r * r);  // (r^3 may leave fp32's range)
+          const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            da[e] = __ffma2_rn(ta[e], r2, da[e]);
+            db[e] = __ffma2_rn(tb[e], r2, db[e]);
+            ga[e] = __ffma2_rn(__fmul2_rn(ga[e], wa[e]), r2, __fmul2_rn(xa[e], m2));
+            gb[e] = __ffma2_rn(__fmul2_rn(gb[e], wb[e]), r2, __fmul2_rn(xb[e], m2));
           }
+          *reinterpret_cast<uint4*>(row + lane.a0) = narrow(ga);
+          *reinterpret_cast<uint4*>(row + lane.b0) = narrow(gb);
+        } else if (a.zero) {
+          *reinterpret_cast<uint4*>(row + lane.a0) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(row + lane.b0) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      at.u += by;
-      at.place(plan);
-      p = p_next;
     }
-    wait_copies<0>();  // (the next kind's take the same slots)
+    at.u += by;
+    at.place(plan);
+    p = p_next;
+  }
 #pragma unroll
-    for (int o = L::kPerRow; o < 32; o <<= 1)
+  for (int o = L::kPerRow; o < 32; o <<= 1)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        da[e].x += __shfl_xor_sync(0xffffffffu, da[e].x, o);
-        da[e].y += __shfl_xor_sync(0xffffffffu, da[e].y, o);
-        db[e].x += __shfl_xor_sync(0xffffffffu, db[e].x, o);
-        db[e].y += __shfl_xor_sync(0xffffffffu, db[e].y, o);
-      }
-    __syncthreads();
-    if (lane.sub == 0) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        *reinterpret_cast<float2*>(&s_dw[warp][lane.a0 + 2 * e]) = da[e];
-        *reinterpret_cast<float2*>(&s_dw[warp][lane.b0 + 2 * e]) = db[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      da[e].x += __shfl_xor_sync(0xffffffffu, da[e].x, o);
+      da[e].y += __shfl_xor_sync(0xffffffffu, da[e].y, o);
+      db[e].x += __shfl_xor_sync(0xffffffffu, db[e].x, o);
+      db[e].y += __shfl_xor_sync(0xffffffffu, db[e].y, o);
     }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float sum = 0.f;
+  if (lane.sub == 0) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += s_dw[w][threadIdx.x];
-      a.part[((size_t)blockIdx.x * 2 + kind) * D + threadIdx.x] = sum;
+    for (int e = 0; e < 4; ++e) {
+      *reinterpret_cast<float2*>(&s_dw[warp][lane.a0 + 2 * e]) = da[e];
+      *reinterpret_cast<float2*>(&s_dw[warp][lane.b0 + 2 * e]) = db[e];
     }
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_dw[w][threadIdx.x];
+    a.part[(size_t)blockIdx.x * D + threadIdx.x] = sum;
   }
 }
 
-// dw from the blocks' sums: 32 of the 2 D columns a block, 32 warps over the rows.
+// dw from the blocks' sums: 32 of q's or k's D columns a block, 32 warps over the rows.
 template <int D>
 __global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const NormRopeArgs a) {
   __shared__ float s_sum[32][33];
   grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  const int kind = blockIdx.x * 32 / D, col = blockIdx.x * 32 % D + lane;
+  const int b0 = kind ? a.blocks_q : 0, b1 = kind ? a.blocks : a.blocks_q;
   float sum = 0.f;
 #pragma unroll 10
-  for (int b = warp; b < a.blocks; b += 32) sum += a.part[(size_t)b * 2 * D + col];
+  for (int b = b0 + warp; b < b1; b += 32) sum += a.part[(size_t)b * D + col];
   s_sum[warp][lane] = sum;
   __syncthreads();
   // column `warp` of the block's, its 32 partial sums a lane each
@@ -491,8 +490,7 @@ __global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const NormRopeArgs 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   if (lane == 0) {
-    const int at = blockIdx.x * 32 + warp;
-    a.dw[at / D][at % D] = x;
+    a.dw[kind][blockIdx.x * 32 % D + warp] = x;
   }
 }
 
@@ -548,7 +546,15 @@ int set_plan(NormRopeArgs* a, int D, int sms, bool backward) {
   if (!backward) p.split = (steps + p.per - 1) / p.per;  // (no part without steps)
   p.units = (uint32_t)((long long)a->T * p.split);
   const long long grid = p.units < 1 ? 1 : p.units, most = (long long)sms * kBlocks;
-  return (int)(grid < most ? grid : most);
+  if (!backward) return (int)(grid < most ? grid : most);
+  // q's and k's blocks by their steps, and one for a token's angles
+  const long long q = p.steps[0] + 1, all = q + p.steps[1] + 1;
+  a->blocks = (int)(2 * grid < most ? 2 * grid : most);
+  long long share = (a->blocks * q + all / 2) / all;
+  if (share < 1) share = 1;
+  if (share > a->blocks - 1) share = a->blocks - 1;
+  a->blocks_q = (int)share;
+  return a->blocks;
 }
 
 // Shared memory of the rings.
@@ -666,7 +672,7 @@ size_t fa_norm_rope_workspace_bytes(int T, int Hq, int Hkv, int D) {
   if (sms < 1) return 0;
   NormRopeArgs a{};
   a.T = T, a.H[0] = Hq, a.H[1] = Hkv;
-  return (size_t)set_plan(&a, D, sms, true) * 2 * D * sizeof(float);
+  return (size_t)set_plan(&a, D, sms, true) * D * sizeof(float);
 }
 
 int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq,
@@ -704,8 +710,8 @@ int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
   a.T = T;
   a.H[0] = Hq;
   a.H[1] = Hkv;
-  a.blocks = set_plan(&a, D, info.sm_count, true);
-  if (workspace_bytes < (size_t)a.blocks * 2 * D * sizeof(float)) return FA_ERR_WORKSPACE;
+  set_plan(&a, D, info.sm_count, true);
+  if (workspace_bytes < (size_t)a.blocks * D * sizeof(float)) return FA_ERR_WORKSPACE;
   a.in[0].x = static_cast<const __nv_bfloat16*>(q);
   a.in[1].x = static_cast<const __nv_bfloat16*>(k);
   a.dy[0].x = static_cast<const __nv_bfloat16*>(dq_out);
