@@ -30,6 +30,8 @@
 // Scores are handled in base 2: t = s * scale * log2(e), P = 2^(t - m).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "exp2.cuh"
 #include "fa_internal.h"
 #include "fwd_common.cuh"
@@ -39,7 +41,12 @@ namespace fa {
 
 __device__ int g_fwd_status = 0;
 
-template <int D>
+// At most this many sinks in front of the window take a step of so many columns (GEMM 1 with
+// N, GEMM 2 with K of 32, a quarter of the softmax), from keys and values of their own
+// in shared memory, so that the ring's tiles are the window's.
+constexpr int kFewSinks = 32;
+
+template <int D, int kMod = 0>
 struct FwdLayout {
   static constexpr int kColBlocks = D / 64;         // 64-element (128-byte) column blocks
   static constexpr int kBlockBytes = kTile * 128;   // one 128-row x 64-col block
@@ -54,7 +61,10 @@ struct FwdLayout {
   static constexpr int kKVStages = (D == 128) ? 4 : 6;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kOffQ + kQStages * 2 * kTileBytes;
-  static constexpr int kOffBar = kOffKV + kKVStages * kTileBytes;
+  static constexpr int kOffSink = kOffKV + kKVStages * kTileBytes;  // (kMod 3) K, then V
+  static constexpr int kSinkBlock = kFewSinks * 128;
+  static constexpr int kSinkBytes = kMod == 3 ? kSinkBlock * kColBlocks : 0;
+  static constexpr int kOffBar = kOffSink + 2 * kSinkBytes;
   static constexpr int kBarQFull = 0;
   static constexpr int kBarQEmpty = kBarQFull + kQStages;
   static constexpr int kBarKVFull = kBarQEmpty + kQStages;
@@ -64,7 +74,8 @@ struct FwdLayout {
   static constexpr int kBarOFinal = kBarPFull + 2;           // per tile: last GEMM 2 done
   static constexpr int kBarOFree = kBarOFinal + 2;           // per tile: epilogue done with O
   static constexpr int kBarDrain = kBarOFree + 2;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarSinkFull = kBarDrain + 1, kBarSinkEmpty = kBarSinkFull + 1;
+  static constexpr int kNumBars = kBarDrain + (kMod == 3 ? 3 : 1);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM base slot, abort flag
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAllocBytes = kBytes + 1024;  // slack for 1024-byte alignment
@@ -76,10 +87,6 @@ struct FwdLayout {
   // Chosen by measurement on GB300, whose MUFU rate is twice B200's.
   static constexpr int kPolyPairs = (D == 64) ? 1 : 0;
 };
-
-// At most this many sinks in front of the window take a step of so many columns: GEMM 1
-// with N, GEMM 2 with K of 32, a quarter of the softmax.
-constexpr int kFewSinks = 32;
 
 // Bit i: key k0 + i is visible, in [lo, lim) or below sinks (and lim).
 __device__ __forceinline__ uint32_t seen_bits(int k0, int lo, int lim, int sinks) {
@@ -93,7 +100,8 @@ __device__ __forceinline__ uint32_t seen_bits(int k0, int lo, int lim, int sinks
 
 // kMod: 0 plain (no mask or the causal one), 1 a sliding window, 2 a window
 // and the relative-position bias (a.alibi) added to every score, 3 (packed) a window
-// with sinks: kv tile 0 first, then the window's tiles, what lies between left out.  kSplit: a
+// with or without sinks: kv tile 0 first, then the window's tiles, what lies between left
+// out.  kSplit: a
 // unit covers one split of the kv tiles and writes fp32 parts for the merge.
 // kVar: a packed batch.  Its tensor maps go over the rows of all sequences.  Rows of
 // Q and K past the sequence's last one (another sequence's, or uninitialised) only
@@ -103,8 +111,8 @@ template <int D, int kMod, bool kSplit, bool kVar>
 __global__ void __launch_bounds__(320, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdArgs a,
-               const __grid_constant__ Tails<kVar, 1> tails) {
-  using L = FwdLayout<D>;
+               const __grid_constant__ Tails<kVar, kMod == 3 ? 2 : 1> tails) {
+  using L = FwdLayout<D, kMod>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -131,6 +139,10 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(bar(L::kBarOFree + t), 128);
     }
     mbar_init(bar(L::kBarDrain), 1);
+    if (kMod == 3) {
+      mbar_init(bar(L::kBarSinkFull), 1);
+      mbar_init(bar(L::kBarSinkEmpty), 1);
+    }
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -164,10 +176,11 @@ __global__ void __launch_bounds__(320, 1)
   // the window; plain calls carry only the causal flag
   const int wl = kWin ? a.wl : -1;
   const int wr = kWin ? a.wr : (a.causal ? 0 : -1);
+  const bool few_sinks = kSink && a.sinks <= kFewSinks && a.scale_log2 > 0.f;
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      uint32_t kv_it = 0, q_it = 0;
+      uint32_t kv_it = 0, q_it = 0, sink_it = 0;
       bool ok = true;
       // kv tile j of K or V, its first row `row` of head bhk; `valid` rows exist (kVar)
       auto load_kv = [&](const CUtensorMap* tm, int bhk, int row, int valid) -> bool {
@@ -194,7 +207,7 @@ __global__ void __launch_bounds__(320, 1)
         int lo[2], hi[2], jlo, nmax;
         SinkSpan span;
         if constexpr (kSink) {
-          span = sink_kv_span(w.Sq, wl, wr, pair);
+          span = sink_kv_span(w.Sq, wl, wr, a.sinks, pair);
           jlo = 0;
           nmax = span.n;
         } else {
@@ -202,6 +215,38 @@ __global__ void __launch_bounds__(320, 1)
                                jlo, nmax);
         }
         if (nmax == 0) continue;
+        int p = jlo;
+        // position p's K and V
+        auto load_position = [&]() -> bool {
+          const int j = kSink ? span.tile(p) : p;
+          const int row = w.row0 + j * kTile;
+          ++p;
+          return load_kv(&tm_k, bhk, row, kTile) && load_kv(&tm_v, bhk, row, w.Sq - j * kTile);
+        };
+        if constexpr (kSink) {
+          if (span.first && few_sinks) {
+            if (!mbar_wait(bar(L::kBarSinkEmpty), (sink_it & 1) ^ 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            ++sink_it;
+            mbar_arrive_expect_tx(bar(L::kBarSinkFull), 2 * L::kSinkBytes);
+            // (the sequence is longer than a tile: all these rows are its own)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              for (int r = 0; r < kFewSinks; r += 16)
+#pragma unroll
+                for (int cb = 0; cb < L::kColBlocks; ++cb)
+                  tma_load_3d(sbase + L::kOffSink + x * L::kSinkBytes + cb * L::kSinkBlock + r * 128,
+                              &tails.of[x ? 0 : 1].box[1], bar(L::kBarSinkFull), cb * 64, w.row0 + r, bhk);
+            p = 1;
+          }
+          // the first tiles before Q, whose place the unit before holds longer
+          if (!load_position()) {
+            ok = false;
+            break;
+          }
+        }
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQEmpty + qs), ((q_it / L::kQStages) & 1) ^ 1, abort_flag)) {
           ok = false;
@@ -219,10 +264,8 @@ __global__ void __launch_bounds__(320, 1)
                         bar(L::kBarQFull + qs), cb * 64, row, w.bh);
         }
         ++q_it;
-        for (int p = jlo; p < jlo + nmax; ++p) {
-          const int j = kSink ? span.tile(p) : p;
-          const int row = w.row0 + j * kTile;
-          if (!load_kv(&tm_k, bhk, row, kTile) || !load_kv(&tm_v, bhk, row, w.Sq - j * kTile)) {
+        while (p < jlo + nmax) {
+          if (!load_position()) {
             ok = false;
             break;
           }
@@ -233,6 +276,7 @@ __global__ void __launch_bounds__(320, 1)
         drain_wait(bar(L::kBarKVFull + n % L::kKVStages), (n / L::kKVStages) & 1);
       for (uint32_t n = (q_it > (uint32_t)L::kQStages ? q_it - L::kQStages : 0); n < q_it; ++n)
         drain_wait(bar(L::kBarQFull + n % L::kQStages), (n / L::kQStages) & 1);
+      if (kSink && sink_it > 0) drain_wait(bar(L::kBarSinkFull), (sink_it - 1) & 1);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
@@ -241,7 +285,7 @@ __global__ void __launch_bounds__(320, 1)
       constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D, false, true);
       constexpr uint32_t kHi = sdesc_hi(1024);  // SBO 1024 B, version 1, 128B swizzle
       constexpr uint32_t kIdescFew = idesc_bf16_f32(kTile, kFewSinks, false, false);
-      uint32_t kv_it = 0, q_it = 0;
+      uint32_t kv_it = 0, q_it = 0, sink_it = 0;
       uint32_t p_seen[2] = {0u, 0u};  // P-ready phases consumed, per tile
       uint32_t units_t[2] = {0u, 0u};  // units with work, per tile (O-free phases)
       bool ok = true;
@@ -252,12 +296,21 @@ __global__ void __launch_bounds__(320, 1)
         // (sinks: position 0 and the window's, SinkSpan)
         int plo[2], phi[2], jlo, nmax;
         SinkSpan span;
+        struct {
+          int plo[2];
+          bool first[2];
+          __device__ __forceinline__ bool active(int t, int p, int hi) const {
+            return p < hi && (p >= plo[t] || (p == 0 && first[t]));
+          }
+        } gap;
         if constexpr (kSink) {
-          span = sink_kv_span(w.Sq, wl, wr, w.pair);
+          span = sink_kv_span(w.Sq, wl, wr, a.sinks, w.pair);
           nmax = span.n;
           for (int t = 0; t < 2; ++t) {
-            plo[t] = 0;  // the first position
+            plo[t] = span.begin(t);
             phi[t] = span.phi[t];
+            gap.first[t] = span.has;
+            gap.plo[t] = span.plo[t];
           }
         } else {
           pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), w.pair, w.split, plo,
@@ -268,10 +321,12 @@ __global__ void __launch_bounds__(320, 1)
           plo[t] -= jlo;
           phi[t] -= jlo;
         }
-        auto active = [&](int t, int p) {
-          return kSink ? span.active(t, p) : p >= plo[t] && p < phi[t];
-        };
-        const bool few = kSink && span.first && a.sinks <= kFewSinks && a.scale_log2 > 0.f;
+        // position 0 is the sinks' own step
+        const bool few = kSink && span.first && few_sinks;
+        if (few && !mbar_wait(bar(L::kBarSinkFull), sink_it & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
         const uint32_t qs = q_it % L::kQStages;
         if (!mbar_wait(bar(L::kBarQFull + qs), (q_it / L::kQStages) & 1, abort_flag)) {
           ok = false;
@@ -280,74 +335,80 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_after();
         const uint32_t q_base = sbase + L::kOffQ + qs * 2 * L::kTileBytes;
         const uint32_t base_it = kv_it;  // ring position of K_0; V_j sits right after K_j
-        for (int j = 0; ok && j <= nmax; ++j) {
-          const bool need_v = j >= 1;
-          const bool need_k = j < nmax;
-          const uint32_t v_pos = base_it + 2 * (j - 1) + 1, k_pos = base_it + 2 * j;
+        // Step j: GEMM 2 of position j - 1 and GEMM 1 of position j, which sit in the ring
+        // `shift` places earlier.  kKind 0: any step; 1, 2: the sinks' GEMM 1 and GEMM 2
+        auto step = [&](int j, int shift, auto kind) -> bool {
+          constexpr int kKind = decltype(kind)::value;
+          const bool need_v = kKind == 0 && j >= 1, need_k = kKind != 1 && j < nmax;
+          const uint32_t v_pos = base_it + 2 * (j - shift - 1) + 1, k_pos = base_it + 2 * (j - shift);
           const uint32_t v_st = v_pos % L::kKVStages, k_st = k_pos % L::kKVStages;
-          if (need_v && !mbar_wait(bar(L::kBarKVFull + v_st), (v_pos / L::kKVStages) & 1,
-                                   abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (need_k && !mbar_wait(bar(L::kBarKVFull + k_st), (k_pos / L::kKVStages) & 1,
-                                   abort_flag)) {
-            ok = false;
-            break;
-          }
+          if (need_v && !mbar_wait(bar(L::kBarKVFull + v_st), (v_pos / L::kKVStages) & 1, abort_flag))
+            return false;
+          if (need_k && !mbar_wait(bar(L::kBarKVFull + k_st), (k_pos / L::kKVStages) & 1, abort_flag))
+            return false;
           tc_fence_after();
           const uint32_t v_base = sbase + L::kOffKV + v_st * L::kTileBytes;
           const uint32_t k_base = sbase + L::kOffKV + k_st * L::kTileBytes;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (kSink ? j >= 1 && active(t, j - 1) : j >= plo[t] + 1 && j <= phi[t]) {
+            // (sinks: a tile whose window begins behind position 1 is idle there)
+            const bool old = kSink ? j >= 1 && (kKind == 2 ? phi[t] > 0 : gap.active(t, j - 1, phi[t]))
+                                   : j >= plo[t] + 1 && j <= phi[t];
+            if (old) {
               // GEMM 2: O_t += P_t(j-1) V_{j-1}
-              if (!mbar_wait(bar(L::kBarPFull + t), p_seen[t] & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
+              if (!mbar_wait(bar(L::kBarPFull + t), p_seen[t] & 1, abort_flag)) return false;
               ++p_seen[t];
               if (j == plo[t] + 1 && units_t[t] > 0 &&
-                  !mbar_wait(bar(L::kBarOFree + t), (units_t[t] - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
+                  !mbar_wait(bar(L::kBarOFree + t), (units_t[t] - 1) & 1, abort_flag))
+                return false;
               tc_fence_after();
-              const uint32_t v_lo = sdesc_lo(v_base, L::kBlockBytes);
+              const uint32_t v_lo = kKind == 2 ? sdesc_lo(sbase + L::kOffSink + L::kSinkBytes, L::kSinkBlock)
+                                               : sdesc_lo(v_base, L::kBlockBytes);
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk) {
-                if (kSink && few && j == 1 && kk == kFewSinks / 16) break;
+              for (int kk = 0; kk < (kKind == 2 ? kFewSinks : kTile) / 16; ++kk)
                 umma_ts_w(tmem + L::kColO + t * D, tmem + t * kTile + kk * 8,
                           v_lo + ((kk * 16 * 128) >> 4), kHi, kIdescO,
-                          (j > plo[t] + 1 || kk > 0) ? 1u : 0u);
-              }
+                          (kKind != 2 && j > plo[t] + 1) || kk > 0 ? 1u : 0u);
               if (j == phi[t]) umma_commit(bar(L::kBarOFinal + t));
             }
-            if (active(t, j)) {
+            const bool now = kSink ? (kKind == 1 ? phi[t] > 0 : gap.active(t, j, phi[t]))
+                                   : j >= plo[t] && j < phi[t];
+            if (now) {
               // GEMM 1: S_t = Q_t K_j^T
               const uint32_t q_lo = sdesc_lo(q_base + t * L::kTileBytes, 16);
-              const uint32_t k_lo = sdesc_lo(k_base, 16);
+              const uint32_t k_lo = sdesc_lo(kKind == 1 ? sbase + L::kOffSink : k_base, 16);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * L::kBlockBytes + (kk & 3) * 32) >> 4;
-                const uint32_t idesc = kSink && few && j == 0 ? kIdescFew : kIdescS;
+                const uint32_t at = ((kk >> 2) * (kKind == 1 ? L::kSinkBlock : L::kBlockBytes) + (kk & 3) * 32) >> 4;
+                constexpr uint32_t kIdesc = kKind == 1 ? kIdescFew : kIdescS;
                 if (kk == 0)
-                  umma_ss_w<0>(tmem + t * kTile, q_lo + off, kHi, k_lo + off, kHi, idesc);
+                  umma_ss_w<0>(tmem + t * kTile, q_lo + off, kHi, k_lo + at, kHi, kIdesc);
                 else
-                  umma_ss_w<1>(tmem + t * kTile, q_lo + off, kHi, k_lo + off, kHi, idesc);
+                  umma_ss_w<1>(tmem + t * kTile, q_lo + off, kHi, k_lo + at, kHi, kIdesc);
               }
               umma_commit(bar(L::kBarSFull + t));
             }
           }
-          if (!ok) break;
           // stages are released in ring order: V_{j-1} then K_j
           if (need_v) umma_commit(bar(L::kBarKVEmpty + v_st));
           if (need_k) umma_commit(bar(L::kBarKVEmpty + k_st));
+          if (kKind == 2) umma_commit(bar(L::kBarSinkEmpty));
           // the Q stage is free once the unit's last GEMM 1 has run
           if (j == nmax - 1) umma_commit(bar(L::kBarQEmpty + qs));
+          return true;
+        };
+        int j0 = 0;
+        if constexpr (kSink) {
+          if (few) {
+            ok = step(0, 1, std::integral_constant<int, 1>{}) && step(1, 1, std::integral_constant<int, 2>{});
+            j0 = 2;
+          }
         }
+        for (int j = j0; ok && j <= nmax; ++j) ok = step(j, j0 / 2, std::integral_constant<int, 0>{});
         if (!ok) break;
-        kv_it = base_it + 2 * nmax;
+        kv_it = base_it + 2 * (nmax - (few ? 1 : 0));
+        if (few) ++sink_it;
         ++q_it;
         for (int t = 0; t < 2; ++t)
           if (phi[t] > plo[t]) ++units_t[t];
@@ -372,8 +433,8 @@ __global__ void __launch_bounds__(320, 1)
       int jlo, jhi;
       SinkSpan span;
       if constexpr (kSink) {
-        span = sink_kv_span(Sq, wl, wr, w.pair);
-        jlo = 0;  // positions
+        span = sink_kv_span(Sq, wl, wr, a.sinks, w.pair);
+        jlo = span.begin(t);  // positions
         jhi = span.phi[t];
       } else {
         split_kv_range<kSplit>(a, Sq, wl, wr, kv_len, qt, split, jlo, jhi);
@@ -411,14 +472,14 @@ __global__ void __launch_bounds__(320, 1)
       const float kslope = kBias ? slope2 / a.scale_log2 : 0.f;
       const bool kslope_ok = kBias && a.scale_log2 > 0.f && fabsf(kslope) < 1e30f;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int p = jlo; p < jhi; p = kSink ? max(p + 1, span.plo[t]) : p + 1) {
+      for (int p = jlo; p < jhi; p = kSink ? span.next(t, p) : p + 1) {
         const int j = kSink ? span.tile(p) : p;
         if (!warp_wait(bar(L::kBarSFull + t), g & 1, abort_flag)) { ok = false; break; }
         ++g;
         tc_fence_after();
         const int kv0 = j * kTile;
         if constexpr (kSink) {
-          if (p == 0 && span.first && sinks <= kFewSinks && a.scale_log2 > 0.f) {
+          if (p == 0 && span.first && few_sinks) {
             // the sinks in front of the window: only their columns were computed
             uint32_t v[kFewSinks], pk[kFewSinks / 2];
             tmem_ld32(t_row + col_s, v);
@@ -820,21 +881,20 @@ static int launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 
 template <int D>
 static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                            const TailMaps& v_tails, FwdArgs a, int max_items,
+                            const Tails<true, 2>& tails, FwdArgs a, int max_items,
                             cudaStream_t stream) {
   using L = FwdLayout<D>;
+  using LW = FwdLayout<D, 3>;
   int dev;
   DeviceInfo info;
   if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   static bool attr_done[64] = {};
   if (dev < 64 && !attr_done[dev]) {
-    const void* kernels[] = {(const void*)fwd_kernel<D, 0, false, true>,
-                             (const void*)fwd_kernel<D, 1, false, true>,
-                             (const void*)fwd_kernel<D, 3, false, true>};
-    for (const void* k : kernels)
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAllocBytes) !=
-          cudaSuccess)
-        return FA_ERR_CUDA;
+    if (cudaFuncSetAttribute(fwd_kernel<D, 0, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::kAllocBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(fwd_kernel<D, 3, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             LW::kAllocBytes) != cudaSuccess)
+      return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
   // the plan lists the longest items first; dealt in a snake as in the dense
@@ -843,14 +903,16 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
   const long long units = (long long)max_items * a.Hq;
   const int grid = (int)(units < info.sm_count ? units : info.sm_count);
   const bool plain = a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal));
-  const auto kernel = plain ? fwd_kernel<D, 0, false, true>
-                     : a.sinks ? fwd_kernel<D, 3, false, true> : fwd_kernel<D, 1, false, true>;
   record_timing(false, stream);
   // D = 64 without a window: the ring of score buffers, as in the dense call
   if (fwd_ring64_eligible(a, D, plain ? 0 : 1)) {
-    if (launch_fwd_ring64_var(tq, tk, tv, v_tails, a, grid, stream) != FA_OK) return FA_ERR_CUDA;
-  } else if (launch_pdl(kernel, dim3(grid), dim3(320), L::kAllocBytes, stream, tq, tk, tv, a,
-                        Tails<true, 1>{{v_tails}}) != cudaSuccess) {
+    if (launch_fwd_ring64_var(tq, tk, tv, tails.of[0], a, grid, stream) != FA_OK) return FA_ERR_CUDA;
+  } else if (plain) {
+    if (launch_pdl(fwd_kernel<D, 0, false, true>, dim3(grid), dim3(320), L::kAllocBytes, stream, tq, tk,
+                   tv, a, Tails<true, 1>{{tails.of[0]}}) != cudaSuccess)
+      return FA_ERR_CUDA;
+  } else if (launch_pdl(fwd_kernel<D, 3, false, true>, dim3(grid), dim3(320), LW::kAllocBytes, stream, tq,
+                        tk, tv, a, tails) != cudaSuccess) {
     return FA_ERR_CUDA;
   }
   record_timing(true, stream);
@@ -859,10 +921,10 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
 }
 
 int launch_fwd_var(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const TailMaps& v_tails, const FwdArgs& a, int D, int max_items,
+                   const Tails<true, 2>& tails, const FwdArgs& a, int D, int max_items,
                    cudaStream_t stream) {
-  if (D == 128) return launch_fwd_var_d<128>(tq, tk, tv, v_tails, a, max_items, stream);
-  if (D == 64) return launch_fwd_var_d<64>(tq, tk, tv, v_tails, a, max_items, stream);
+  if (D == 128) return launch_fwd_var_d<128>(tq, tk, tv, tails, a, max_items, stream);
+  if (D == 64) return launch_fwd_var_d<64>(tq, tk, tv, tails, a, max_items, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

@@ -129,9 +129,9 @@ int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
                const FwdArgs& a, int D, cudaStream_t stream);
 
 // The same kernel over a packed batch (maps over all its rows) of at most max_items
-// items; v_tails: v's smaller boxes.
+// items; tails: v's and k's smaller boxes.
 int launch_fwd_var(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const TailMaps& v_tails, const FwdArgs& a, int D, int max_items,
+                   const Tails<true, 2>& tails, const FwdArgs& a, int D, int max_items,
                    cudaStream_t stream);
 int* fwd_status_word();  // on the current device; null if it cannot be found
 

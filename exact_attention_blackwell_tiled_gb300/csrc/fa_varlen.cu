@@ -319,10 +319,14 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   if ((rc = check_device())) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   CUtensorMap maps[3];
-  TailMaps v_tails;
+  Tails<true, 2> tails;  // of v and k
   for (int i = 0; i < 3; ++i)
     if (!full_map(t[i], T, D, &maps[i])) return FA_ERR_CUDA;
-  if (!tail_maps(t[2], T, D, &v_tails)) return FA_ERR_CUDA;
+  // (k's are the sinks' in front of a window)
+  if (!tail_maps(t[2], T, D, &tails.of[0])) return FA_ERR_CUDA;
+  tails.of[1] = tails.of[0];
+  if (window_sinks(sinks, window_side(window_left, T), T) && !tail_maps(t[1], T, D, &tails.of[1]))
+    return FA_ERR_CUDA;
   PlanArgs p{};
   FwdArgs a{};
   a.wl = window_side(window_left, T);
@@ -354,7 +358,7 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   a.T = T;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((rc = launch_plan(p, st))) return rc;
-  return launch_fwd_var(maps[0], maps[1], maps[2], v_tails, a, D, L.max_items, st);
+  return launch_fwd_var(maps[0], maps[1], maps[2], tails, a, D, L.max_items, st);
 }
 
 int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const void* dO,

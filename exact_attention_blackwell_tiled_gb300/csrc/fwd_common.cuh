@@ -148,31 +148,36 @@ __device__ __forceinline__ void pair_kv_span(const FwdArgs& a, int Sq, int wl, i
   if (e1) lo[1] = hi[1] = jlo;
 }
 
-// The same with sinks: kv tile 0 comes first for every query tile with rows.  Position
-// p of the unit is tile 0 where p == 0, else jlo + p - first, so that the tiles between
-// the sinks and the window are left out; plo[t] .. phi[t] are the positions of tile t's
-// window.  Returns false where the unit has no rows (never: the plan lists none).
+// The same with sinks (has), as positions: kv tile 0 is position 0 for every query tile with
+// rows, and where the windows begin behind it (first), theirs follow from position 1 on, so
+// that the tiles between the sinks and the window are left out.  plo[t] .. phi[t] are the
+// positions of tile t's window.  (A packed unit has rows and sees itself: n is not 0.)
 struct SinkSpan {
   int plo[2], phi[2];  // phi 0: no rows
-  int jlo, first, n;
-  __device__ __forceinline__ int tile(int p) const { return p == 0 ? 0 : jlo + p - first; }
+  int jlo, n;
+  bool has, first;
+  __device__ __forceinline__ int tile(int p) const { return first && p == 0 ? 0 : jlo + p - (first ? 1 : 0); }
   __device__ __forceinline__ bool active(int t, int p) const {
-    return p == 0 ? phi[t] > 0 : p >= plo[t] && p < phi[t];
+    return has && p == 0 ? phi[t] > 0 : p >= plo[t] && p < phi[t];
   }
+  // tile t's first position, and the next one
+  __device__ __forceinline__ int begin(int t) const { return has ? 0 : plo[t]; }
+  __device__ __forceinline__ int next(int t, int p) const { return max(p + 1, plo[t]); }
 };
-__device__ __forceinline__ SinkSpan sink_kv_span(int Sq, int wl, int wr, int pair) {
+__device__ __forceinline__ SinkSpan sink_kv_span(int Sq, int wl, int wr, int sinks, int pair) {
   SinkSpan s;
+  s.has = sinks > 0;
   int lo[2], hi[2];
   tile_kv_range(Sq, wl, wr, Sq, 2 * pair, lo[0], hi[0]);
   tile_kv_range(Sq, wl, wr, Sq, 2 * pair + 1, lo[1], hi[1]);
   s.jlo = lo[0];
-  s.first = s.jlo > 0 ? 1 : 0;
-  s.n = s.first;
+  s.first = s.has && s.jlo > 0;
+  s.n = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const bool rows = hi[t] > lo[t];
-    s.plo[t] = rows ? lo[t] - s.jlo + s.first : 0;
-    s.phi[t] = rows ? hi[t] - s.jlo + s.first : 0;
+    s.plo[t] = rows ? lo[t] - s.jlo + (s.first ? 1 : 0) : 0;
+    s.phi[t] = rows ? hi[t] - s.jlo + (s.first ? 1 : 0) : 0;
     s.n = max(s.n, s.phi[t]);
   }
   return s;
