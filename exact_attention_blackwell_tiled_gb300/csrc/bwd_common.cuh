@@ -63,9 +63,9 @@ __device__ __forceinline__ int qblk_first_contributor(int wl, int iq) {
 }
 
 template <bool kMod, int QB>
-__device__ __forceinline__ bool tile_adds_to(const BwdArgs& a, int j, int kv_len, int iq) {
+__device__ __forceinline__ bool tile_adds_to(const BwdArgs& a, int Sq, int j, int kv_len, int iq) {
   int lo, hi;
-  bwd_qblk_range<kMod, QB>(a, a.Sq, j, kv_len, lo, hi);
+  bwd_qblk_range<kMod, QB>(a, Sq, j, kv_len, lo, hi);
   return lo <= iq && iq < hi;
 }
 
@@ -76,12 +76,12 @@ __device__ __forceinline__ bool tile_adds_to(const BwdArgs& a, int j, int kv_len
 // block that some tile adds into, so the contiguous run of contributors stops
 // the descent within a step or two.
 template <bool kMod, int QB>
-__device__ __forceinline__ int qblk_last_contributor(const BwdArgs& a, int iq, int kv_len) {
+__device__ __forceinline__ int qblk_last_contributor(const BwdArgs& a, int Sq, int iq, int kv_len) {
   const int wl = win_left<kMod>(a), wr = win_right<kMod>(a);
   const int n_kt = (kv_len + kTile - 1) / kTile;
   const int first = qblk_first_contributor<QB>(wl, iq);
   int last = wr >= 0 ? min(n_kt - 1, (iq * QB + QB - 1 + wr) / kTile) : n_kt - 1;
-  while (last > first && !tile_adds_to<kMod, QB>(a, last, kv_len, iq)) --last;
+  while (last > first && !tile_adds_to<kMod, QB>(a, Sq, last, kv_len, iq)) --last;
   return last;
 }
 

@@ -849,7 +849,8 @@ __global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1
     // before this one:
     auto turn_of = [&](const BwdUnit& w, int iq) -> int {
       const int g = w.j % a.dq_groups;
-      return a.desc ? (group_last(qblk_last_contributor<kMod, kQB>(a, iq, w.kv_len), g, a.dq_groups) -
+      return a.desc ? (group_last(qblk_last_contributor<kMod, kQB>(a, kVar ? w.kv_len : a.Sq, iq, w.kv_len), g,
+                                a.dq_groups) -
                        w.j) / a.dq_groups
                     : (w.j - group_first(qblk_first_contributor<kQB>(win_left<kMod>(a), iq), g,
                                          a.dq_groups)) / a.dq_groups;
@@ -1130,16 +1131,17 @@ __device__ void sum_sinks(const BwdArgs& a, int n_items, int item, const VarItem
     for (int g = 0; g < group; ++g) {
       const int h = hk * group + g;
       const float* parts = (is_v ? a.sink_dv : a.sink_dk) + (size_t)h * a.sink_rows * D;
-      // runs begin at the first tile with sinks behind the window and at the shares'
-      // multiples; tiles count from the sequence's tile 0, at position x0
-      const int x0 = h * n_items + item;
-      int tile = first, next = (x0 + first) / share * share + share - x0;
-      while (tile <= last) {
+      // runs begin at the sequence's first position whose tile has sinks behind the window
+      // and at the shares' multiples; positions count from there
+      const int x0 = h * n_items + item + (a.desc ? -last : first);
+      int at = 0, next = x0 / share * share + share - x0;
+      while (at <= last - first) {
+        const int tile = a.desc ? last - at : first + at;
         if ((part & (groups - 1)) == my_group && r < rows)
           add_eight(x, reinterpret_cast<const float4*>(parts + (sink_slot(a, it.row0, tile) + r) * D +
                                                        c8 * 8));
         ++part;
-        tile = next;
+        at = next;
         next += share;
       }
     }
@@ -1407,8 +1409,8 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaS
   if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
     return FA_ERR_CUDA;
   if (a.sinks) {
-    const long long shares = q_units < sms ? q_units : sms;
-    a.sink_grid = (int)shares;
+    const int most = bwd_sink_blocks(D, a.sinks, sms);
+    a.sink_grid = (int)(q_units < most ? q_units : most);
     const int rc = launch_bwd_sink(m, a, stream);
     if (rc != FA_OK) return rc;
   }

@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           // with head-major dealing), the first of them storing
           g = w.j % a.dq_groups;
           turn = a.desc
-                     ? (group_last(qblk_last_contributor<kMod, kQB2>(a, iq, w.kv_len), g,
+                     ? (group_last(qblk_last_contributor<kMod, kQB2>(a, kVar ? w.kv_len : a.Sq, iq, w.kv_len), g,
                                    a.dq_groups) -
                         w.j) / a.dq_groups
                      : (w.j - group_first(qblk_first_contributor<kQB2>(win_left<kMod>(a), iq), g,

@@ -14,7 +14,7 @@
 // with P and dS rounded to bf16 for the products, as in the main kernels.  It needs Q, dO
 // and the row vectors once and writes dQ in fp32: 4 D + 4 D bytes per query and head, a
 // memory-bound pass.  The list of (head, tile) positions is cut into one contiguous share
-// per SM; a run ends with its sequence, head or share and leaves one fp32 part of dK_s
+// per block, one or two of which an SM holds; a run ends with its sequence, head or share and leaves one fp32 part of dK_s
 // and dV_s, which the last kernel of the call adds up.
 //
 // Warps 0-3: a query row per thread (TMEM lane); warp 4: TMA; warp 5: TMEM and MMAs.
@@ -60,11 +60,12 @@ struct SinkSmem {
   static constexpr int kNumBars = kBarDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
-  static constexpr int kAllocBytes = kBytes + 1024;
+  static constexpr int kBlocks = D == 64 && !kWide ? 2 : 1;  // per SM
   static constexpr uint32_t kColDP = kRowsKV, kColDV = 2 * kRowsKV < D ? D : 2 * kRowsKV,
                             kColDK = kColDV + D;
   static constexpr uint32_t kTmemCols = kColDK + D <= 256 ? 256 : 512;
-  static_assert(kColDK + D <= 512, "TMEM columns");
+  static_assert(kColDK + D <= 512 && kTmemCols * kBlocks <= 512, "TMEM columns");
+  static_assert(kBlocks * (kBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 // A share's tiles that have sinks behind the window, in order.
@@ -98,12 +99,10 @@ __device__ __forceinline__ bool same_run(const SinkTile& a, const SinkTile& b) {
 }
 
 template <int D, bool kWide>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(192, SinkSmem<D, kWide>::kBlocks)
     bwd_sink_kernel(const BwdArgs a, const __grid_constant__ Tails<true, 4> tails) {
   using L = SinkSmem<D, kWide>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (no room for two blocks of D = 64 with slack)
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
@@ -163,8 +162,10 @@ __global__ void __launch_bounds__(192, 1)
         if (first) {
           if (!mbar_wait(bar(L::kBarKVEmpty), (runs & 1) ^ 1, abort_flag)) break;
           mbar_arrive_expect_tx(bar(L::kBarKVFull), 2 * L::kKVBytes);
-          load(sbase + L::kOffK, L::kKVBlock, L::kRowsKV, 1, bar(L::kBarKVFull), t.it.row0, t.it.len, hk);
-          load(sbase + L::kOffV, L::kKVBlock, L::kRowsKV, 2, bar(L::kBarKVFull), t.it.row0, t.it.len, hk);
+          // (zeros behind the sinks: what lies there is out of sight)
+          const int keys = min(a.sinks, t.it.len);
+          load(sbase + L::kOffK, L::kKVBlock, L::kRowsKV, 1, bar(L::kBarKVFull), t.it.row0, keys, hk);
+          load(sbase + L::kOffV, L::kKVBlock, L::kRowsKV, 2, bar(L::kBarKVFull), t.it.row0, keys, hk);
           ++runs;
         }
         const uint32_t st = it % L::kStages;
@@ -381,17 +382,21 @@ int launch(const BwdVarMaps& m, const BwdArgs& a, cudaStream_t stream) {
   static bool attr_done[64] = {};
   if (!attr_done[dev]) {
     if (cudaFuncSetAttribute(bwd_sink_kernel<D, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::kAllocBytes) != cudaSuccess)
+                             L::kBytes) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  if (launch_pdl(bwd_sink_kernel<D, kWide>, dim3(a.sink_grid), dim3(192), L::kAllocBytes, stream, a,
+  if (launch_pdl(bwd_sink_kernel<D, kWide>, dim3(a.sink_grid), dim3(192), L::kBytes, stream, a,
                  m.tails) != cudaSuccess)
     return FA_ERR_CUDA;
   return FA_OK;
 }
 
 }  // namespace
+
+int bwd_sink_blocks(int D, int sinks, int sms) {
+  return sms * (D == 64 && sinks <= 64 ? SinkSmem<64, false>::kBlocks : 1);
+}
 
 int launch_bwd_sink(const BwdVarMaps& m, const BwdArgs& a, cudaStream_t stream) {
   if (a.D == 128) return a.sinks > 64 ? launch<128, true>(m, a, stream) : launch<128, false>(m, a, stream);

@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(320, 1)
           const int j = kSink ? span.tile(p) : p;
           const int row = w.row0 + j * kTile;
           ++p;
-          return load_kv(&tm_k, bhk, row, kTile) && load_kv(&tm_v, bhk, row, w.Sq - j * kTile);
+          // (sinks in front of the window: the rows behind them are out of sight)
+          const int valid = kSink && span.first && j == 0 ? min(a.sinks, w.Sq) : w.Sq - j * kTile;
+          return load_kv(&tm_k, bhk, row, kTile) && load_kv(&tm_v, bhk, row, valid);
         };
         if constexpr (kSink) {
           if (span.first && few_sinks) {
@@ -231,14 +233,11 @@ __global__ void __launch_bounds__(320, 1)
             }
             ++sink_it;
             mbar_arrive_expect_tx(bar(L::kBarSinkFull), 2 * L::kSinkBytes);
-            // (the sequence is longer than a tile: all these rows are its own)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              for (int r = 0; r < kFewSinks; r += 16)
-#pragma unroll
-                for (int cb = 0; cb < L::kColBlocks; ++cb)
-                  tma_load_3d(sbase + L::kOffSink + x * L::kSinkBytes + cb * L::kSinkBlock + r * 128,
-                              &tails.of[x ? 0 : 1].box[1], bar(L::kBarSinkFull), cb * 64, w.row0 + r, bhk);
+            // keys and, with zeros behind the sinks, values
+            load_pieces<kFewSinks, L::kColBlocks>(sbase + L::kOffSink, L::kSinkBlock, tails.of[1],
+                                                  bar(L::kBarSinkFull), w.row0, kFewSinks, a.T, bhk);
+            load_pieces<kFewSinks, L::kColBlocks>(sbase + L::kOffSink + L::kSinkBytes, L::kSinkBlock,
+                                                  tails.of[0], bar(L::kBarSinkFull), w.row0, a.sinks, a.T, bhk);
             p = 1;
           }
           // the first tiles before Q, whose place the unit before holds longer

@@ -78,6 +78,7 @@ struct PlanArgs {
   int B, T;
   int item_rows;  // 256 (forward: pairs of query tiles) or 128 (backward: kv tiles)
   int causal;
+  int desc;  // without a causal mask: each sequence's tiles from the last down
   int pad;  // VarItem::pad0 counts sequences padded to this many rows (a power of two)
   VarItem* items;
   int max_items;
@@ -188,7 +189,8 @@ struct BwdArgs {
   int n_ktiles;  // 128-row kv tiles of Sk
   int n_units;
   int snake;     // 1: units dealt longest-first (ascending kv tile) in a snake
-  int desc;      // 1: each head's kv tiles dealt in descending order (deterministic mode)
+  int desc;      // 1: each head's kv tiles dealt in descending order (deterministic mode);
+                 // packed: the plan lists each sequence's so (PlanArgs::desc)
   // Dynamic dealing (bwd_main with the snake order): a CTA takes its next unit
   // from an atomic counter, in an order that runs over groups of head_group kv
   // heads, each group's longest units (lowest kv tile) first, so that the
@@ -271,6 +273,7 @@ struct BwdVarMaps {
 int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, int max_items, cudaStream_t stream);
 
 // The pairs of queries and sinks behind the window (a.sinks > 0), before the main kernel.
+int bwd_sink_blocks(int D, int sinks, int sms);  // that are resident at once
 int launch_bwd_sink(const BwdVarMaps& m, const BwdArgs& a, cudaStream_t stream);
 
 // Rows of sink_dk and its like, per head, for T packed rows (sink_slot's largest and

@@ -41,7 +41,7 @@ __device__ __forceinline__ int warp_add(int x) {
 //   forward, causal: pair t attends to 2 t + 2 kv tiles: by t, descending;
 //   backward, causal: kv tile t is seen by blocks64 - 2 t query blocks;
 //   otherwise: the longest sequence first, its items in order.
-// Ties go to the lower sequence.  Within a sequence the backward's tiles ascend.
+// Ties go to the lower sequence.  Within a sequence the backward's tiles ascend (desc: descend).
 __device__ __forceinline__ int items_before(int mode, int t, int n_own, int blk_own, int n_other,
                                             int blk_other, bool lower) {
   if (mode == 0) {  // forward, causal
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const PlanArgs p)
     return items_before(mode, t, n_own, blk_own, (n + p.item_rows - 1) >> shift, (n + 63) >> 6, i < b);
   };
   auto place = [&](int t, int before) {
-    before += mode == 0 ? n_own - 1 - t : t;
+    before += mode == 0 || (mode == 2 && p.desc) ? n_own - 1 - t : t;
     if (before >= p.max_items) return;
     int4* dst = reinterpret_cast<int4*>(p.items + before);
     dst[0] = make_int4(row0, len, t, b);
@@ -441,7 +441,15 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
     a.sink_dv = reinterpret_cast<float*>(ws + L.off_sink[1]);
     a.sink_dk0 = reinterpret_cast<float*>(ws + L.off_sink[2]);
     a.sink_dv0 = reinterpret_cast<float*>(ws + L.off_sink[3]);
-    if (deterministic) a.dq_sink = reinterpret_cast<float*>(ws + L.off_dq_sink);
+    if (deterministic) {
+      a.dq_sink = reinterpret_cast<float*>(ws + L.off_dq_sink);
+      // Under a window tile j adds to blocks from 2 j (64 rows) on: from the last tile down
+      // the one before has been at a block two steps earlier, so that a chain never
+      // waits; upwards each waits for the one before to be two blocks ahead, and the last
+      // of those that run at a time for all of them (16384 tokens in one sequence, 32 heads
+      // of 64 under 256: 690 us so, atomic 314).
+      p.desc = a.desc = 1;
+    }
   }
   a.status = p.status;
   a.unit_counter = p.counter;
@@ -461,7 +469,8 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
     // 820 tokens, 16 / 4 heads, of 128 139 / 140 / 149, of 64 99 / 95 / 97; without a
     // mask of 128 555 / 545 / 567 and 186 / 181 / 187, of 64 493 / 474 / 439 and 148 /
     // 138 / 135.
-    const int most = a.causal ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
+    // (chains that do not wait, a.desc: one)
+    const int most = a.desc ? (D == 128 ? 1 : 2) : a.causal ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
     a.dq_groups = L.groups < most ? L.groups : most;
   } else {
     a.dq_groups = 1;

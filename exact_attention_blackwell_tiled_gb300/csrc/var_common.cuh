@@ -25,6 +25,32 @@ __device__ __forceinline__ void prefetch_tails(const Tails<true, N>& tails, int 
   if (lane < N * kTailBoxes) tma_prefetch_desc(&tails.of[lane / kTailBoxes].box[lane % kTailBoxes]);
 }
 
+// Rows row .. row + valid - 1 of head `head` of a packed tensor into a tile of kRows rows (128
+// bytes each, kColBlocks blocks of 64 columns) in pieces of 64, 16, 4 and 1 rows, then
+// rows T .., which do not exist and arrive as zeros.
+template <int kRows, int kColBlocks>
+__device__ __forceinline__ void load_pieces(uint32_t dst, uint32_t block_bytes, const TailMaps& tails,
+                                            uint32_t bar, int row, int valid, int T, int head) {
+  int at = 0, from = row, n = valid;
+#pragma unroll 1
+  for (int zeros = 0; zeros < 2; ++zeros) {
+#pragma unroll 1
+    for (int x = 0; x < kTailBoxes; ++x) {
+      const int rows = 64 >> (2 * x);
+#pragma unroll 1
+      for (; n >= rows; n -= rows) {
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb)
+          tma_load_3d(dst + cb * block_bytes + at * 128, &tails.box[x], bar, cb * 64, from, head);
+        at += rows;
+        if (!zeros) from += rows;
+      }
+    }
+    from = T;
+    n = kRows - at;
+  }
+}
+
 // Rows row .. row + valid - 1 of head `head` of a packed tensor into a tile of kRows
 // rows (128 bytes each, kColBlocks blocks of 64 columns), zeros behind them: one box
 // where the tile is full, pieces of 64, 16, 4 and 1 rows where the sequence ends in
@@ -46,24 +72,7 @@ __device__ __forceinline__ void load_rows(uint32_t dst, uint32_t block_bytes, co
       tma_load_3d(dst + cb * block_bytes, full, bar, cb * 64, row, head);
     return;
   }
-  int at = 0, from = row, n = valid;
-#pragma unroll 1
-  for (int zeros = 0; zeros < 2; ++zeros) {
-#pragma unroll 1
-    for (int x = 0; x < kTailBoxes; ++x) {
-      const int rows = 64 >> (2 * x);
-#pragma unroll 1
-      for (; n >= rows; n -= rows) {
-#pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb)
-          tma_load_3d(dst + cb * block_bytes + at * 128, &tails.box[x], bar, cb * 64, from, head);
-        at += rows;
-        if (!zeros) from += rows;
-      }
-    }
-    from = T;
-    n = kRows - at;
-  }
+  load_pieces<kRows, kColBlocks>(dst, block_bytes, tails, bar, row, valid, T, head);
 }
 
 }  // namespace fa

@@ -212,6 +212,33 @@ def test_large_scores_and_strides(D, det):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sinks", [4, 40])
+@pytest.mark.parametrize("det", [False, True])
+def test_nan_and_infinity_out_of_sight(D, sinks, det):
+    """Keys behind the sinks, in their tile, reach no query whose tiles of the window begin
+    further on: neither through a weight of zero nor through a masked score."""
+    __graft_entry__.build()
+    n, window = 700, (100, 0)
+    q, k, v, do = _inputs(n, 2, 1, D, 23)
+    r = packed_sinks(q, k, v, [(0, n)], window, sinks, do=do)
+    far = 384                                  # queries from here on see keys from 284 on
+    for bad in (math.nan, math.inf):
+        kb, vb = k.clone(), v.clone()
+        kb[sinks], kb[100] = bad, -bad
+        vb[sinks + 1], vb[127] = bad, -bad
+        d = [x.cuda() for x in (q, kb, vb, do)]
+        cu = _cu([(0, n)])
+        o, lse = fa.fwd_varlen(*d[:3], cu, window=window, sinks=sinks)
+        assert_within(o[far:], r["o"][far:], r["o_tol"][far:], "o")
+        assert_within(lse[:, far:], r["lse"][:, far:], r["lse_tol"][:, far:], "lse")
+        dq, dk, dv = fa.bwd_varlen(*d[:3], o, d[3], lse, cu, window=window, sinks=sinks, deterministic=det)
+        assert_within(dq[far:], r["dq"][far:], r["dq_tol"][far:], "dq")
+        for name, x in (("dk", dk), ("dv", dv)):
+            assert_within(x[far:], r[name][far:], r[name + "_tol"][far:], name)
+
+
+@pytest.mark.gpu
 def test_a_window_that_hides_nothing_is_the_plain_call():
     __graft_entry__.build()
     q, k, v, do = (x.cuda() for x in _inputs(500, 4, 2, 128, 1))
