@@ -80,7 +80,7 @@ def _build_binding() -> None:
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{d}" for d in inc], BINDING_SOURCE,
           "-o", tmp, f"-L{PKG}", "-l:libfa.so", "-Wl,-rpath,$ORIGIN",
-          "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+          "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
          "g++ for binding.cpp")
     os.replace(tmp, BINDING_PATH)
     os.makedirs(BUILD_DIR, exist_ok=True)

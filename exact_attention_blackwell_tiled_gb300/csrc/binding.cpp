@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -162,7 +162,8 @@ struct Place {
 };
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const Place& place) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(c10::Device(at::kCUDA, place.device)));
+  // (what at::empty comes to on a CUDA device, without its way there: 0.5 us of 1.3 a tensor)
+  return at::Tensor(at::detail::empty_cuda(shape, dtype, c10::Device(at::kCUDA, place.device), std::nullopt));
 }
 
 // The same, or for None a new one, whose memory stays until the caller's stream, where
