@@ -873,6 +873,16 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, int unit, float* s_ls
   const View<kWin> view = seq_view<kWin>(a, b);
   const int len = view.len;
   if (first >= len) return;
+  if (kWin && first >= view.sinks && first + kWeightKeys <= view.lo) {
+    // out of sight as a whole: nothing to add
+    if (a.w_in == a.w_out) return;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {  // (its keys are below lo, and so below len)
+      const size_t at = (size_t)bh * a.w_stride + j0 + x * kW * 32;
+      a.w_out[at] = a.w_in ? a.w_in[at] : 0.f;
+    }
+    return;
+  }
   const float* src = a.scores + ((size_t)bh * a.cap + j0) * a.group;
   const size_t step = (size_t)kW * 32 * a.group, at = (size_t)bh * a.w_stride + j0;
   const bool four = (a.group & 3) == 0;

@@ -289,12 +289,22 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
     const int lo1 = s.n0, hi1 = min(s.n1, max(s.n0, s.hs < s.he ? s.hs : s.n1));
     const int lo2 = s.hs < s.he ? max(s.n0, s.he) : s.n1, hi2 = s.n1;
     const int c1 = max(0, hi1 - lo1), c = c1 + max(0, hi2 - lo2);
-    for (int x = lane; x < c; x += 32) {
-      const int e = x < c1 ? lo1 + x : lo2 + x - c1;
-      const int at = top - 1 - (s_taken[i] + x);
-      const bool there = at >= 0 && at < a.pages;
-      row[e] = there ? __ldcg(a.stack + at) : -1;
-      bad |= !there;
+    const int first = top - 1 - s_taken[i];
+#pragma unroll 1
+    for (int x0 = lane; x0 < c; x0 += 32 * kAtOnce) {
+      int page[kAtOnce];
+#pragma unroll
+      for (int y = 0; y < kAtOnce; ++y) {
+        const int x = x0 + 32 * y, at = first - x;
+        const bool there = at >= 0 && at < a.pages;
+        page[y] = x < c && there ? __ldcg(a.stack + at) : -1;
+        bad |= x < c && !there;
+      }
+#pragma unroll
+      for (int y = 0; y < kAtOnce; ++y) {
+        const int x = x0 + 32 * y;
+        if (x < c) row[x < c1 ? lo1 + x : lo2 + x - c1] = page[y];
+      }
     }
   }
   if (rank == 0 && tid == 0) {
