@@ -576,6 +576,8 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda", s
     """cos and sin fp32 [positions, rot/2] of the angles p base^(-2i/rot), taken in 64 bits
     (fa_rope_table)."""
     device = torch.device(device)
+    if device.type != "cuda":
+        raise TypeError("rope_table fills CUDA tensors")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
@@ -699,7 +701,8 @@ def page_update(page_table: torch.Tensor, free_pages: torch.Tensor, free_count: 
     ``page_table`` int32 [B,width]; ``free_pages``, ``free_count``: the pool (page_pool);
     ``lens``, ``new_lens`` int32 [B]: tokens held and to be held.  Entries past the new
     length, and those that a window of ``window_left`` tokens with ``sinks`` hides from the
-    last token's query on, give their pages back; entries for new tokens take pages.
+    last token's query on, give their pages back; entries for new tokens take pages.  A
+    page belongs to one entry: tables that share pages are not for this call.
     Returns (cu_seqlens int32 [B+1], positions int32 [T], slots int64 [T]) of the new
     tokens, packed in order; ``T`` is the rows they have, and rows past the last get -1.
     cache4_status() reports a pool or T that was too small, and lengths past the table.

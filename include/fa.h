@@ -302,7 +302,10 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
  *   j <= i + window_right (any j where it is negative) and
  *   (window_left < 0 or j >= i - window_left or j < sinks).
  * 0 <= sinks <= 128 (more: FA_ERR_UNSUPPORTED); 0 is fa_fwd_varlen / fa_bwd_varlen.  Same
- * tensors, sizes, pointer rules, roundings and errors as those calls.  The forward's
+ * tensors, sizes, pointer rules, roundings and errors as those calls.  (As there, an infinity
+ * or NaN in a row of k or v may reach the queries whose tiles of 128 see that row's tile; the
+ * rows of a sequence's first tile behind its sinks do not count for later queries.)  The
+ * deterministic mode adds the tiles of a sequence from the last one down.  The forward's
  * workspace is fa_varlen_workspace_bytes(..., 0, 0) bytes, the backward's
  * fa_varlen_sink_workspace_bytes(..., 1, deterministic, window_left, sinks).
  */
@@ -389,9 +392,10 @@ int fa_cache4_append_slots(void* cache, int num_pages, int page_size, const void
  * there once the tokens are stored.  A length outside [0, table_width * page_size] or a
  * free_count outside [0, num_pages] is cut and recorded; fa_cache4_status returns
  * FA_ERR_INVALID_ARG for all of these.
+ * A page belongs to one entry of one table: one that two entries hold comes back twice.
  * page_size 16, 32, 64 or 128; 1 <= B <= 65536; B * table_width below 2^30, num_pages at most
- * 2^30; int32 arrays 4-byte, slots 8-byte aligned.  One launch, no workspace; calls on
- * the same tables or stack follow one another.
+ * 2^30; int32 arrays 4-byte, slots 8-byte aligned.  One launch (two from 8193 rows on), no
+ * workspace; calls on the same tables or stack follow one another.
  */
 int fa_page_update(int* page_table, int table_width, int* free_pages, int* free_count,
                    int num_pages, const int* lens, const int* new_lens, int B, int page_size,

@@ -79,6 +79,10 @@ def test_attend(gpu, D, lens, page, Hkv, group, wl, sinks):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     step = torch.full_like(wd, 7.0)
     fa.cache4_attend(q.cuda(), cache, table, n, weights_out=step, **kw)
+    apart = torch.full_like(wd, 7.0)
+    fa.cache4_attend(q.cuda(), cache, table, n, weights=w0.cuda(), weights_out=apart, **kw)
+    live = (torch.arange(slots) < torch.tensor(lens)[:, None]).cuda()[:, None].expand_as(wd)
+    assert torch.equal(apart[live], wd[live]) and bool((apart[~live] == 7).all())
     assert fa.cache4_status() == fa.FA_OK
     for b, m in enumerate(lens):
         j = visible(m, wl, sinks)

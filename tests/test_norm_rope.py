@@ -380,3 +380,31 @@ def test_capture_and_streams(gpu):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gpu):
+    """Rows 2^26 elements apart: the last ones lie behind 2^32 elements."""
+    T, D, step = 70, 64, 1 << 26
+    try:
+        far = torch.zeros(T * step, dtype=torch.bfloat16, device="cuda")
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("not enough memory")
+    gen = torch.Generator().manual_seed(1)
+    q, k = _rows(T, 2, D, gen).cuda(), _rows(T, 1, D, gen).cuda()
+    qf, kf = far.as_strided((T, 2, D), (step, D, 1)), far.as_strided((T, 1, D), (step, D, 1), 4 * D)
+    qf.copy_(q)
+    kf.copy_(k)
+    w = torch.ones(D, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    cos, sin = fa.rope_table(T, D)
+    want = fa.norm_rope_fwd(q, k, w, w, cos, sin, pos)
+    got = fa.norm_rope_fwd(qf, kf, w, w, cos, sin, pos, q_out=qf, k_out=kf)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    del far, qf, kf, got
+    torch.cuda.empty_cache()
+
+
+def test_table_refuses_host_memory():
+    with pytest.raises(TypeError):
+        fa.rope_table(4, 64, device="cpu")

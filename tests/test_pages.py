@@ -189,6 +189,37 @@ def test_lengths_and_counts_out_of_range(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [8192, 8193, 50000])
+def test_many_new_tokens(gpu, T):
+    """Prompts of many tokens, more than the one launch writes, some of them empty."""
+    rng = random.Random(T)
+    new, left = [], T
+    while left:
+        n = min(left, rng.choice([0, 1, 3, 200, 3000]))
+        new.append(n)
+        left -= n
+    B, width = len(new), 3000 // 16 + 1
+    pages = sum(-(-n // 16) for n in new)
+    _check([[-1] * width for _ in new], list(range(pages)), pages, [0] * B, new, 16, -1, 0, T)
+    _check([[-1] * width for _ in new], list(range(pages)), pages, [0] * B, new, 16, 100, 5, T + 1500)
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_a_stretch(gpu):
+    """A thousand tokens of more sequences than one block of the second launch keeps."""
+    B = 30000
+    table = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    free, count = fa.page_pool(B)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    new = (torch.arange(B, device="cuda") % 3 == 1).int()
+    T = 10000
+    cu, pos, slots = fa.page_update(table, free, count, lens, new, 16, T)
+    assert fa.cache4_status() == fa.FA_OK and int(cu[-1]) == T == int(new.sum())
+    at = torch.arange(T, device="cuda")
+    assert torch.equal(slots, (B - 1 - at) * 16) and bool((pos == 0).all())
+
+
+@pytest.mark.gpu
 def test_many_sequences(gpu):
     """The most there can be, in closed form: a page and a token each."""
     B = 65536
@@ -205,16 +236,18 @@ def test_many_sequences(gpu):
 
 
 @pytest.mark.gpu
-def test_a_captured_step_replays(gpu):
+@pytest.mark.parametrize("B", [10, 70])
+def test_a_captured_step_replays(gpu, B):
     """Many steps of one graph against the simulation: windows, ends and starts."""
     rng = random.Random(9)
-    B, page, wl, sinks, width = 10, 16, 40, 3, 12
+    page, wl, sinks, width, pages = 16, 40, 3, 12, 5 * B
+    T = 6 * B
     table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
-    free, count = fa.page_pool(50)
+    free, count = fa.page_pool(pages)
     lens, new = _i32([0] * B), _i32([0] * B)
 
     def step():
-        out = fa.page_update(table, free, count, lens, new, page, 64, window_left=wl, sinks=sinks)
+        out = fa.page_update(table, free, count, lens, new, page, T, window_left=wl, sinks=sinks)
         lens.copy_(new)
         return out
     step()
@@ -226,7 +259,7 @@ def test_a_captured_step_replays(gpu):
     old = [0] * B
     for i in range(60):
         nxt = [0 if rng.random() < 0.05 else min(n + rng.choice([1, 1, 1, 6]), width * page) for n in old]
-        want = simulate(*state, old, nxt, page, wl, sinks, 64)
+        want = simulate(*state, old, nxt, page, wl, sinks, T)
         new.copy_(_i32(nxt))
         graph.replay()
         assert out[0].tolist() == want[3] and out[1].tolist() == want[4] and out[2].tolist() == want[5]
@@ -234,7 +267,7 @@ def test_a_captured_step_replays(gpu):
         assert table.tolist() == want[0] and count.item() == want[2]
     assert fa.cache4_status() == fa.FA_OK
     held = [p for row in state[0] for p in row if p >= 0]
-    assert sorted(held + state[1][:state[2]]) == list(range(50))  # no page lost, none twice
+    assert sorted(held + state[1][:state[2]]) == list(range(pages))  # no page lost, none twice
 
 
 @pytest.mark.gpu

@@ -195,7 +195,7 @@ def test_large_scores_and_strides(D, det):
     dev = fused.cuda()
     parts = dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:]
     cu = _cu(bounds)
-    for scale in (None, -0.05):
+    for scale in (None, -0.05, 0.0):
         r = packed_sinks(*(x.cpu() for x in parts), bounds, window, sinks, scale=scale, do=do)
         o = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
         lse = torch.full((Hq, T), 7.0, device="cuda")
@@ -313,3 +313,51 @@ def test_two_streams():
     for w, runs in zip(want, got):
         for g in runs:
             assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("det", [False, True])
+def test_long_sequences_in_many_shares(D, det):
+    """A sequence whose sinks' parts come from many blocks, next to short ones; sampled rows
+    and the sinks' gradients against the plain form."""
+    __graft_entry__.build()
+    Hq, Hkv, window, sinks = 4, 2, (300, 0), 6
+    bounds = _bounds([50, 5000, 1, 700])
+    T = bounds[-1][1]
+    q, k, v, do = (x.cuda() for x in _inputs(T, Hq, Hkv, D, 77))
+    cu = _cu(bounds)
+    o, lse = fa.fwd_varlen(q, k, v, cu, window=window, sinks=sinks)
+    g = fa.bwd_varlen(q, k, v, o, do, lse, cu, window=window, sinks=sinks, deterministic=det)
+    # the long sequence by itself, in fp64 on the GPU, and the bounds of its sinks' rows
+    lo, hi = bounds[1]
+    n = hi - lo
+    i = torch.arange(n, device="cuda")
+    mask = (i[None] <= i[:, None]) & ((i[None] >= i[:, None] - window[0]) | (i[None] < sinks))
+    scale, u = 1 / math.sqrt(D), 2.0 ** -8
+    dk, dv = (torch.zeros(n, Hkv, D, dtype=torch.float64, device="cuda") for _ in range(2))
+    dk_tol, dv_tol = torch.zeros_like(dk), torch.zeros_like(dv)
+    for h in range(Hq):
+        qh, doh = q[lo:hi, h].double(), do[lo:hi, h].double()
+        kh, vh = k[lo:hi, h // 2].double(), v[lo:hi, h // 2].double()
+        s = (qh @ kh.T * scale).masked_fill(~mask, -math.inf)
+        z = torch.logsumexp(s, 1, keepdim=True)
+        p = (s - z).exp()
+        out = p @ vh
+        e_s = (D + 8) * 2.0 ** -23 * scale * (qh.abs() @ kh.abs().T).masked_fill(~mask, 0).amax(1, keepdim=True)
+        o_tol = u * out.abs() + (u + 2 * e_s + n * 2.0 ** -23) * (p @ vh.abs())
+        assert bool(((o[lo:hi, h].double() - out).abs() <= o_tol).all())
+        dp = doh @ vh.T
+        ds = p * (dp - (doh * out).sum(1, keepdim=True))
+        e_dp = (D + 2) * 2.0 ** -23 * (doh.abs() @ vh.abs().T)
+        e_delta = (doh.abs() * o_tol).sum(1, keepdim=True) + (D + 2) * 2.0 ** -23 * (doh * out).abs().sum(1, keepdim=True)
+        e_ds = (u + 2 * e_s + n * 2.0 ** -23) * ds.abs() + p * (e_delta + e_dp)
+        dq = ds @ kh * scale
+        dq_tol = u * dq.abs() + scale * (e_ds @ kh.abs())
+        assert bool(((g[0][lo:hi, h].double() - dq).abs() <= dq_tol).all())
+        dv[:, h // 2] += p.T @ doh
+        dv_tol[:, h // 2] += (p * (u + 2 * e_s + n * 2.0 ** -23)).T @ doh.abs()
+        dk[:, h // 2] += ds.T @ qh * scale
+        dk_tol[:, h // 2] += scale * (e_ds.T @ qh.abs())
+    for x, ref, tol in ((g[1], dk, dk_tol), (g[2], dv, dv_tol)):
+        assert bool(((x[lo:hi].double() - ref).abs() <= tol + u * ref.abs()).all())
