@@ -12,11 +12,16 @@
 // sequences.  New tokens are packed in (b, position) order; a token's slot is page s +
 // position % s, or -1 where its entry has no page.
 //
-// A few kilobytes move: the time is a launch and a chain of dependent steps.  One cluster
-// of blocks does it all, so that no second launch stands between the sums and what needs
-// them: a warp counts a sequence's entries, the blocks' sums meet in shared memory of the
-// cluster, and two barriers of the cluster stand where a page that came back may be taken
-// by another block's sequence.
+// A few kilobytes move: the time is a launch and a chain of dependent steps.  One block or
+// one cluster of blocks does all that the sums are needed for, so that no second launch
+// stands between: a warp counts a sequence's entries, the blocks' sums meet in shared memory
+// of the cluster, and two barriers of the cluster stand where a page that came back may be
+// taken by another block's sequence.  Only many new tokens' positions and slots take a
+// second launch, for the whole GPU's stores.
+//
+// Measured: 64 sequences that grow by a token under a window of 4,096 (one block) 5 us, 8
+// cold; 1,024 sequences, 244,000 new tokens, 17 us and 9 for the second launch (one launch
+// for all: 48).
 #include <cuda_runtime.h>
 
 #include <climits>
