@@ -198,18 +198,37 @@ __global__ void __launch_bounds__(256) bwd_preprocess(const BwdArgs a) {
 // rows with few keys that moves dS about as much as its own rounding to bf16 for the
 // products does (2^-9 of it each).
 template <int D>
-__global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a) {
+__global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a, const PlanArgs p) {
+  __shared__ VarItem s_items[kBlockPlanItems];
   grid_dep_wait();
   grid_dep_launch();
   constexpr int kLanesPerRow = D / 8;
   constexpr int kRowsPerStep = 32 / kLanesPerRow;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanesPerRow, seg = lane % kLanesPerRow;
-  const int n_units = *a.n_items * a.Hq;
+  const VarItem* items = a.items;
+  int n_items;
+  if (p.cu) {
+    // the plan, here for the block itself and by block 0 for the kernels that follow
+    n_items = plan_in_block(p, warp, 8, [&](int at, const VarItem& it) {
+      s_items[at] = it;
+      if (blockIdx.x == 0) p.items[at] = it;
+    });
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      *p.status = n_items < 0 ? (int)FA_ERR_INVALID_ARG : 0;
+      *p.counter = 0;
+      *p.n_items = max(n_items, 0);
+    }
+    items = s_items;
+    __syncthreads();
+  } else {
+    n_items = *a.n_items;
+  }
+  const int n_units = n_items * a.Hq;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int item = u / a.Hq, h = u - item * a.Hq;
-    const VarItem it = load_item(a.items, item);
-    const int pad0 = a.items[item].pad0;
+    const VarItem it = load_item(items, item);
+    const int pad0 = items[item].pad0;
     const int i0 = it.tile * kTile;
     const int i1 = min(i0 + kTile, (it.len + a.qblk_rows - 1) / a.qblk_rows * a.qblk_rows);
     // kTile / 8 = 16 rows per warp, kPreUnroll steps of them in flight
@@ -1384,7 +1403,8 @@ int launch_bwd(const BwdMaps& m, const BwdArgs& a, cudaStream_t stream) {
 }
 
 template <int D>
-static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaStream_t stream) {
+static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, const PlanArgs& p, int max_items,
+                            cudaStream_t stream) {
   constexpr bool kDet = D == 64;
   using L = BwdSmem<D>;
   int dev;
@@ -1406,7 +1426,7 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaS
   const int small_grid = (int)(q_units < 8LL * sms ? q_units : 8LL * sms);
   const long long units = a.dk_part ? q_units : kv_units;
   const int grid = (int)(units < sms ? units : sms);
-  if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a) != cudaSuccess)
+  if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a, p) != cudaSuccess)
     return FA_ERR_CUDA;
   if (a.sinks) {
     const int most = bwd_sink_blocks(D, a.sinks, sms);
@@ -1453,9 +1473,10 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, int max_items, cudaS
   return FA_OK;
 }
 
-int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, int max_items, cudaStream_t stream) {
-  if (a.D == 128) return launch_bwd_var_d<128>(m, a, max_items, stream);
-  if (a.D == 64) return launch_bwd_var_d<64>(m, a, max_items, stream);
+int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, const PlanArgs& p, int max_items,
+                   cudaStream_t stream) {
+  if (a.D == 128) return launch_bwd_var_d<128>(m, a, p, max_items, stream);
+  if (a.D == 64) return launch_bwd_var_d<64>(m, a, p, max_items, stream);
   return FA_ERR_UNSUPPORTED;
 }
 

@@ -118,7 +118,9 @@ __device__ __forceinline__ uint32_t seen_bits(int k0, int lo, int lim, int sinks
 // Q and K past the sequence's last one (another sequence's, or uninitialised) only
 // reach scores that are masked or rows that are not stored; rows of V have to be zeros
 // there, since infinities or NaN would survive a weight of zero in GEMM 2 (load_rows).
-template <int D, int kMod, bool kSplit, bool kVar>
+// kPlan: the block plans the packed batch itself (a form of its own: a choice at run time
+// cost the others 2.5%).
+template <int D, int kMod, bool kSplit, bool kVar, bool kPlan = false>
 __global__ void __launch_bounds__(320, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdArgs a,
@@ -178,8 +180,21 @@ __global__ void __launch_bounds__(320, 1)
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
-  const int n_units = kVar ? *a.n_items * a.Hq : a.n_units;
   constexpr bool kWin = kMod >= 1, kBias = kMod == 2, kSink = kMod == 3;
+  static_assert(!kPlan || kSink, "a window's items do not depend on their tile");
+  __shared__ VarItem s_items[kPlan ? kBlockPlanItems : 1];
+  const VarItem* items = kPlan ? s_items : a.items;
+  int n_units;
+  if constexpr (kPlan) {
+    PlanArgs p{};
+    p.cu = a.cu, p.B = a.B, p.T = a.T, p.item_rows = 2 * kTile, p.pad = 1;
+    const int n = plan_in_block(p, warp, 10, [&](int at, const VarItem& it) { s_items[at] = it; });
+    if (n < 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, (int)FA_ERR_INVALID_ARG);
+    n_units = max(n, 0) * a.Hq;
+    __syncthreads();
+  } else {
+    n_units = kVar ? *a.n_items * a.Hq : a.n_units;
+  }
   static_assert(!kSink || kVar, "sinks: packed calls");
   // packed calls keep every exponential on MUFU: the cubic's 7.5e-5 would be
   // the largest error of their LSE by two orders of magnitude
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(320, 1)
         return true;
       };
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const FwdUnit w = fwd_unit<kVar>(a, items, u);
         const int pair = w.pair;
         const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(320, 1)
       uint32_t units_t[2] = {0u, 0u};  // units with work, per tile (O-free phases)
       bool ok = true;
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const FwdUnit w = fwd_unit<kVar>(a, items, u);
         // kv tile j sits at position p = j - jlo of the pair's range; tile t
         // computes S for positions [plo[t], phi[t]) and O one position behind
         // (sinks: position 0 and the window's, SinkSpan)
@@ -436,7 +451,7 @@ __global__ void __launch_bounds__(320, 1)
     uint32_t g = 0, nu = 0;  // S-full phases and units consumed by this group
     bool ok = true;
     for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-      const FwdUnit w = fwd_unit<kVar>(a, u);
+      const FwdUnit w = fwd_unit<kVar>(a, items, u);
       const int bh = w.bh, split = w.split, Sq = w.Sq;
       const int qt = 2 * w.pair + t;
       const int kv_len = unit_kv_len<kWin, kVar>(a, w);
@@ -903,7 +918,9 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
     if (cudaFuncSetAttribute(fwd_kernel<D, 0, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kAllocBytes) != cudaSuccess ||
         cudaFuncSetAttribute(fwd_kernel<D, 3, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             LW::kAllocBytes) != cudaSuccess)
+                             LW::kAllocBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(fwd_kernel<D, 3, false, true, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, LW::kAllocBytes) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
@@ -921,8 +938,9 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
     if (launch_pdl(fwd_kernel<D, 0, false, true>, dim3(grid), dim3(320), L::kAllocBytes, stream, tq, tk,
                    tv, a, Tails<true, 1>{{tails.of[0]}}) != cudaSuccess)
       return FA_ERR_CUDA;
-  } else if (launch_pdl(fwd_kernel<D, 3, false, true>, dim3(grid), dim3(320), LW::kAllocBytes, stream, tq,
-                        tk, tv, a, tails) != cudaSuccess) {
+  } else if (launch_pdl(a.cu ? fwd_kernel<D, 3, false, true, true> : fwd_kernel<D, 3, false, true>,
+                        dim3(grid), dim3(320), LW::kAllocBytes, stream, tq, tk, tv, a, tails) !=
+             cudaSuccess) {
     return FA_ERR_CUDA;
   }
   record_timing(true, stream);

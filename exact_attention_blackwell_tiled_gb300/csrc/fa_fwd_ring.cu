@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         return true;
       };
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const FwdUnit w = fwd_unit<kVar>(a, a.items, u);
         const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
         pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       uint32_t gs = 0;  // score halves issued for this tile (all units)
       bool ok = true;
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const FwdUnit w = fwd_unit<kVar>(a, a.items, u);
         int lo[2], hi[2], jlo, nmax;
         pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
                             nmax);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       uint32_t units = 0;  // units in which this tile had keys (O-free phases)
       bool ok = true;
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, u);
+        const FwdUnit w = fwd_unit<kVar>(a, a.items, u);
         int lo[2], hi[2], jlo, nmax;
         pair_kv_span<false>(a, w.Sq, -1, wr, unit_kv_len<false, kVar>(a, w), w.pair, 0, lo, hi, jlo,
                             nmax);
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const float c = a.scale_log2;  // > 0 for this kernel
     const float2 c2 = make_float2(c, c);
     for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-      const FwdUnit w = fwd_unit<kVar>(a, u);
+      const FwdUnit w = fwd_unit<kVar>(a, a.items, u);
       const int qt = 2 * w.pair + t, Sq = w.Sq, kv_len = unit_kv_len<false, kVar>(a, w);
       int jlo, jhi;
       split_kv_range<false>(a, Sq, -1, wr, kv_len, qt, 0, jlo, jhi);

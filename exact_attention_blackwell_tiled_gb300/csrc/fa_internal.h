@@ -89,6 +89,18 @@ struct PlanArgs {
 };
 int launch_plan(const PlanArgs& p, cudaStream_t stream);
 
+// Calls of so few sequences and items are planned by each block of their first kernel for
+// itself, in shared memory.  Measured, us with the plan kernel / so, window 256 with 4
+// sinks, 8 / 2 heads of 64: forward 10 sequences of 44 tokens 8.7 / 7.4, 16 of 100 8.9 / 8.3,
+// 32 of 60 12.0 / 11.5, 32 of 400 (82 items) 34.8 / 35.9; backward 1 of 437 38.3 / 35.2, 5 of 820
+// 56.4 / 53.5, 10 of 44 22.4 / 21.2, causal 16 of 100 24.1 / 24.5, 32 of 60 28.0 / 37.7 (each
+// item counts all sequences in turn), 2 of 8000 (127 items) 137.8 / 139.6.
+// (The forward without sinks keeps its two launches.)
+constexpr int kBlockPlanItems = 64;
+inline bool plan_fits_block(int B, int max_items, bool backward) {
+  return B <= (backward ? 10 : 16) && max_items <= kBlockPlanItems;
+}
+
 struct FwdArgs {
   void* o;
   float* lse;
@@ -121,6 +133,7 @@ struct FwdArgs {
   const VarItem* items;
   const int* n_items;
   int T;
+  const int* cu;  // or the sequences' first rows [B + 1], for a block's own plan (kMod 3)
   // packed calls with a window: the keys j < sinks of a sequence stay visible behind
   // it (at most kTile, so tile 0 holds them)
   int sinks;
@@ -270,7 +283,8 @@ struct BwdVarMaps {
   CUtensorMap q, k, v, dO;
   Tails<true, 4> tails;  // of q, k, v and dO
 };
-int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, int max_items, cudaStream_t stream);
+int launch_bwd_var(const BwdVarMaps& m, const BwdArgs& a, const PlanArgs& p, int max_items,
+                   cudaStream_t stream);
 
 // The pairs of queries and sinks behind the window (a.sinks > 0), before the main kernel.
 int bwd_sink_blocks(int D, int sinks, int sms);  // that are resident at once

@@ -14,6 +14,8 @@
 //     var_common.cuh).
 // The plan costs one launch of a warp per sequence and no pass over the data; it
 // overlaps the end of the kernel before it and the attention kernel's prologue.
+// A few sequences are planned by every block of the call's first kernel for itself
+// (plan_in_block, var_common.cuh).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -22,6 +24,7 @@
 
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "var_common.cuh"
 
 namespace fa {
 
@@ -29,33 +32,6 @@ namespace {
 
 constexpr int kPlanWarps = 4;
 constexpr int kPlanCache = 4096;  // sequences whose lengths a block keeps
-
-__device__ __forceinline__ int warp_add(int x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Items of sequence `other` that go before item `t` of the sequence `own` with
-// n_own blocks of item_rows rows; len_other / len_own in 64-row blocks.
-//   forward, causal: pair t attends to 2 t + 2 kv tiles: by t, descending;
-//   backward, causal: kv tile t is seen by blocks64 - 2 t query blocks;
-//   otherwise: the longest sequence first, its items in order.
-// Ties go to the lower sequence.  Within a sequence the backward's tiles ascend (desc: descend).
-__device__ __forceinline__ int items_before(int mode, int t, int n_own, int blk_own, int n_other,
-                                            int blk_other, bool lower) {
-  if (mode == 0) {  // forward, causal
-    const int more = max(0, n_other - 1 - t);
-    return more + (lower && n_other > t ? 1 : 0);
-  }
-  if (mode == 1) {  // backward, causal: blk_other - 2 t' > blk_own - 2 t
-    const int d = blk_other - (blk_own - 2 * t);  // 2 t' < d
-    const int more = d > 0 ? min(n_other, (d + 1) / 2) : 0;
-    const bool tie = d >= 0 && (d & 1) == 0 && d / 2 < n_other;
-    return more + (lower && tie ? 1 : 0);
-  }
-  return n_other > n_own || (n_other == n_own && lower) ? n_other : 0;
-}
 
 // One warp per sequence.  Bound by the latency of reading cu once and by the
 // counting: B steps for every 32 items of a sequence (lanes are items), or B / 32
@@ -103,13 +79,13 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const PlanArgs p)
   for (int i = lane; i < b; i += 32) pad0 += (len_of(i) + p.pad - 1) & -p.pad;
   pad0 = warp_add(pad0);
   const int n_own = (len + p.item_rows - 1) >> shift, blk_own = (len + 63) >> 6;
-  const int mode = p.causal ? (p.item_rows == 256 ? 0 : 1) : 2;
+  const int mode = plan_mode(p);
   auto count = [&](int t, int i) {
     const int n = len_of(i);
     return items_before(mode, t, n_own, blk_own, (n + p.item_rows - 1) >> shift, (n + 63) >> 6, i < b);
   };
   auto place = [&](int t, int before) {
-    before += mode == 0 || (mode == 2 && p.desc) ? n_own - 1 - t : t;
+    before += plan_descends(p) ? n_own - 1 - t : t;
     if (before >= p.max_items) return;
     int4* dst = reinterpret_cast<int4*>(p.items + before);
     dst[0] = make_int4(row0, len, t, b);
@@ -357,7 +333,10 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   a.n_items = p.n_items;
   a.T = T;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_plan(p, st))) return rc;
+  if (a.sinks && plan_fits_block(B, L.max_items, false))
+    a.cu = cu_seqlens;
+  else if ((rc = launch_plan(p, st)))
+    return rc;
   return launch_fwd_var(maps[0], maps[1], maps[2], tails, a, D, L.max_items, st);
 }
 
@@ -495,8 +474,11 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
   a.T = T;
   a.T_pad = (int)L.t_pad;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_plan(p, st))) return rc;
-  return launch_bwd_var(m, a, L.max_items, st);
+  if (!plan_fits_block(B, L.max_items, true)) {
+    if ((rc = launch_plan(p, st))) return rc;
+    p.cu = nullptr;
+  }
+  return launch_bwd_var(m, a, p, L.max_items, st);
 }
 
 }  // extern "C"

@@ -64,12 +64,12 @@ struct FwdUnit {
 };
 
 template <bool kVar>
-__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
+__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, const VarItem* items, int u) {
   FwdUnit w;
   w.row0 = 0;
   if constexpr (kVar) {
     const int item = u / a.Hq;
-    const VarItem it = load_item(a.items, item);
+    const VarItem it = load_item(items, item);
     w.h = w.bh = u - item * a.Hq;
     w.b = it.b;
     w.pair = it.tile;
