@@ -142,6 +142,24 @@ struct VarLayout {
 // 8 T Hq D bytes, at most 80 MB times the group at D = 128: T Hkv is below 77,824.)
 constexpr long long kSplitUnits = 608;
 
+// Whether a call with sinks takes those parts.  Under a window a unit has at most about (128 + wl
+// + wr) / 64 blocks per head, and units are alike: what counts is how many an SM gets, and
+// what each costs besides its blocks: its ends, its parts written and read again, some 4 blocks
+// at D = 128, 2 at D = 64.  Measured, us of the whole backward, with parts / without: 4099
+// tokens in 5 sequences, 16 / 4 heads, window 300, of 64 88.9 / 74.6, of 128 131.8 / 99.4;
+// 9000 tokens in one 160 / 131 and 234 / 175, under 2000 350 / 360 (the rule's worst here)
+// and 446 / 426; 4000 in two, 14 / 2 heads, 100, 66.8 / 72.8 (taken) and 122.8 / 92.1.
+// (Calls without sinks keep theirs, and the order of their sums.)
+bool split_pays(int max_items, int Hq, int Hkv, int T, int D, int wl, int wr) {
+  if (wr < 0) return true;  // (units of any number of blocks)
+  const long long sms = 152, start = D == 128 ? 4 : 2;
+  long long blocks = (128LL + wl + wr) / 64 + 1;
+  if (blocks > T / 64 + 1) blocks = T / 64 + 1;
+  const long long one = (max_items * (long long)Hkv + sms - 1) / sms * (Hq / Hkv * blocks + start);
+  const long long parts = (max_items * (long long)Hq + sms - 1) / sms * (blocks + start);
+  return parts < one;
+}
+
 int check_var(int B, int T, int Hq, int Hkv, int D) {
   if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
@@ -189,7 +207,7 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
     L.sink_rows = sink_row_count(T, wl, sinks);
     for (int i = 0; i < 4; ++i) {  // dK, dV of the sinks' kernel; of the main kernel
       L.off_sink[i] = L.total;
-      const int heads = i < 2 ? Hq : (L.split ? 0 : Hkv);
+      const int heads = i < 2 ? Hq : Hkv;
       L.total = up256(L.total + (size_t)heads * L.sink_rows * D * sizeof(float));
     }
     L.off_dq_sink = L.total;
@@ -409,7 +427,8 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
   a.delta = reinterpret_cast<float*>(ws + L.off_delta);
   a.lse2 = reinterpret_cast<float*>(ws + L.off_lse2);
   a.sem = reinterpret_cast<int*>(ws + L.off_sem);
-  if (L.split) {
+  const bool split = L.split && (seen == 0 || split_pays(L.max_items, Hq, Hkv, T, D, a.wl, a.wr));
+  if (split) {
     a.dk_part = reinterpret_cast<float*>(ws + L.off_dk);
     a.dv_part = reinterpret_cast<float*>(ws + L.off_dv);
   }
@@ -467,7 +486,7 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
     const double per_kv_head = (double)(Hq / Hkv) * T * D * (4.0 + 4.0) + (double)T * D * 4.0;
     const double fit = kBwdGroupBytes / per_kv_head;
     const int hg = deterministic || fit >= Hkv ? Hkv : (fit < 1.0 ? 1 : (int)fit);
-    a.head_group = hg * (L.split ? Hq / Hkv : 1);
+    a.head_group = hg * (split ? Hq / Hkv : 1);
   }
   a.items = p.items;
   a.n_items = p.n_items;
