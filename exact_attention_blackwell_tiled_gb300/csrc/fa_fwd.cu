@@ -119,8 +119,10 @@ __device__ __forceinline__ uint32_t seen_bits(int k0, int lo, int lim, int sinks
 // reach scores that are masked or rows that are not stored; rows of V have to be zeros
 // there, since infinities or NaN would survive a weight of zero in GEMM 2 (load_rows).
 // kPlan: the block plans the packed batch itself (a form of its own: a choice at run time
-// cost the others 2.5%).
-template <int D, int kMod, bool kSplit, bool kVar, bool kPlan = false>
+// cost the others 2.5%).  kHeads: a unit is a tile of two query heads of one kv head
+// instead of two tiles of one: both see the same kv tiles, so that no step is one tile's
+// alone, and a sequence's last unit is not half empty.
+template <int D, int kMod, bool kSplit, bool kVar, bool kPlan = false, bool kHeads = false>
 __global__ void __launch_bounds__(320, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdArgs a,
@@ -181,19 +183,21 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t tmem = *tmem_slot;
   const int group = a.Hq / a.Hkv;
   constexpr bool kWin = kMod >= 1, kBias = kMod == 2, kSink = kMod == 3;
-  static_assert(!kPlan || kSink, "a window's items do not depend on their tile");
+  static_assert((!kPlan && !kHeads) || kSink, "under a window");
   __shared__ VarItem s_items[kPlan ? kBlockPlanItems : 1];
   const VarItem* items = kPlan ? s_items : a.items;
   int n_units;
   if constexpr (kPlan) {
     PlanArgs p{};
-    p.cu = a.cu, p.B = a.B, p.T = a.T, p.item_rows = 2 * kTile, p.pad = 1;
-    const int n = plan_in_block(p, warp, 10, [&](int at, const VarItem& it) { s_items[at] = it; });
+    p.cu = a.cu, p.B = a.B, p.T = a.T, p.item_rows = kHeads ? kTile : 2 * kTile, p.pad = 1;
+    const int n = plan_in_block(p, warp, 10, [&](int at, const VarItem& it) {
+      reinterpret_cast<int4*>(s_items)[kHeads ? at : 2 * at] = make_int4(it.row0, it.len, it.tile, it.b);
+    });
     if (n < 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, (int)FA_ERR_INVALID_ARG);
-    n_units = max(n, 0) * a.Hq;
+    n_units = max(n, 0) * (kHeads ? a.Hq / 2 : a.Hq);
     __syncthreads();
   } else {
-    n_units = kVar ? *a.n_items * a.Hq : a.n_units;
+    n_units = kVar ? *a.n_items * (kHeads ? a.Hq / 2 : a.Hq) : a.n_units;
   }
   static_assert(!kSink || kVar, "sinks: packed calls");
   // packed calls keep every exponential on MUFU: the cubic's 7.5e-5 would be
@@ -227,13 +231,13 @@ __global__ void __launch_bounds__(320, 1)
         return true;
       };
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, items, u);
+        const FwdUnit w = fwd_unit<kVar, kHeads>(a, items, u);
         const int pair = w.pair;
         const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
         SinkSpan span;
         if constexpr (kSink) {
-          span = sink_kv_span(w.Sq, wl, wr, a.sinks, pair);
+          span = sink_kv_span<kHeads>(w.Sq, wl, wr, a.sinks, pair);
           jlo = 0;
           nmax = span.n;
         } else {
@@ -282,11 +286,11 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           // (a packed tile that the sequence does not reach: zeros)
-          const int q0 = (2 * pair + t) * kTile, row = !kVar ? q0 : (q0 < w.Sq ? w.row0 + q0 : a.T);
+          const int q0 = (kHeads ? pair : 2 * pair + t) * kTile, row = !kVar ? q0 : (q0 < w.Sq ? w.row0 + q0 : a.T);
 #pragma unroll
           for (int cb = 0; cb < L::kColBlocks; ++cb)
             tma_load_3d(qdst + t * L::kTileBytes + cb * L::kBlockBytes, &tm_q,
-                        bar(L::kBarQFull + qs), cb * 64, row, w.bh);
+                        bar(L::kBarQFull + qs), cb * 64, row, w.bh + (kHeads ? t : 0));
         }
         ++q_it;
         while (p < jlo + nmax) {
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(320, 1)
       uint32_t units_t[2] = {0u, 0u};  // units with work, per tile (O-free phases)
       bool ok = true;
       for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-        const FwdUnit w = fwd_unit<kVar>(a, items, u);
+        const FwdUnit w = fwd_unit<kVar, kHeads>(a, items, u);
         // kv tile j sits at position p = j - jlo of the pair's range; tile t
         // computes S for positions [plo[t], phi[t]) and O one position behind
         // (sinks: position 0 and the window's, SinkSpan)
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(320, 1)
           }
         } gap;
         if constexpr (kSink) {
-          span = sink_kv_span(w.Sq, wl, wr, a.sinks, w.pair);
+          span = sink_kv_span<kHeads>(w.Sq, wl, wr, a.sinks, w.pair);
           nmax = span.n;
           for (int t = 0; t < 2; ++t) {
             plo[t] = span.begin(t);
@@ -377,7 +381,8 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             // (sinks: a tile whose window begins behind position 1 is idle there)
-            const bool old = kSink ? j >= 1 && (kKind == 2 ? phi[t] > 0 : gap.active(t, j - 1, phi[t]))
+            const bool old = kHeads ? j >= 1
+                             : kSink ? j >= 1 && (kKind == 2 ? phi[t] > 0 : gap.active(t, j - 1, phi[t]))
                                    : j >= plo[t] + 1 && j <= phi[t];
             if (old) {
               // GEMM 2: O_t += P_t(j-1) V_{j-1}
@@ -396,7 +401,8 @@ __global__ void __launch_bounds__(320, 1)
                           (kKind != 2 && j > plo[t] + 1) || kk > 0 ? 1u : 0u);
               if (j == phi[t]) umma_commit(bar(L::kBarOFinal + t));
             }
-            const bool now = kSink ? (kKind == 1 ? phi[t] > 0 : gap.active(t, j, phi[t]))
+            const bool now = kHeads ? kKind == 1 || j < nmax
+                             : kSink ? (kKind == 1 ? phi[t] > 0 : gap.active(t, j, phi[t]))
                                    : j >= plo[t] && j < phi[t];
             if (now) {
               // GEMM 1: S_t = Q_t K_j^T
@@ -451,14 +457,14 @@ __global__ void __launch_bounds__(320, 1)
     uint32_t g = 0, nu = 0;  // S-full phases and units consumed by this group
     bool ok = true;
     for (int ri = 0, u = cta_unit(a, n_units, 0); ok && u >= 0; u = cta_unit(a, n_units, ++ri)) {
-      const FwdUnit w = fwd_unit<kVar>(a, items, u);
+      const FwdUnit w = fwd_unit<kVar, kHeads>(a, items, u);
       const int bh = w.bh, split = w.split, Sq = w.Sq;
-      const int qt = 2 * w.pair + t;
+      const int qt = kHeads ? w.pair : 2 * w.pair + t, head = w.h + (kHeads ? t : 0);
       const int kv_len = unit_kv_len<kWin, kVar>(a, w);
       int jlo, jhi;
       SinkSpan span;
       if constexpr (kSink) {
-        span = sink_kv_span(Sq, wl, wr, a.sinks, w.pair);
+        span = sink_kv_span<kHeads>(Sq, wl, wr, a.sinks, w.pair);
         jlo = span.begin(t);  // positions
         jhi = span.phi[t];
       } else {
@@ -467,10 +473,10 @@ __global__ void __launch_bounds__(320, 1)
       const int q_row = qt * kTile + r;
       const size_t part_row = ((size_t)split * a.B * a.Hq + bh) * Sq + q_row;
       // O rows of the unit: element offset of row 0 and from row to row
-      const size_t o_off = kVar ? ((size_t)w.row0 * a.Hq + w.h) * D : (size_t)bh * Sq * D;
+      const size_t o_off = kVar ? ((size_t)w.row0 * a.Hq + head) * D : (size_t)bh * Sq * D;
       const size_t o_row = kVar ? (size_t)a.Hq * D : (size_t)D;
       // its LSE values: [Hq, T] in packed calls
-      float* lse_u = a.lse + (kVar ? (size_t)w.h * a.T + w.row0 : (size_t)bh * Sq);
+      float* lse_u = a.lse + (kVar ? (size_t)head * a.T + w.row0 : (size_t)bh * Sq);
       if (jhi == jlo) {
         // no key (of this split) reaches the tile: an empty part, or with a
         // window or padding the whole tile sees no key: O = 0, LSE = -inf
@@ -920,6 +926,10 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
         cudaFuncSetAttribute(fwd_kernel<D, 3, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              LW::kAllocBytes) != cudaSuccess ||
         cudaFuncSetAttribute(fwd_kernel<D, 3, false, true, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, LW::kAllocBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(fwd_kernel<D, 3, false, true, false, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, LW::kAllocBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(fwd_kernel<D, 3, false, true, true, true>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, LW::kAllocBytes) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
@@ -927,7 +937,7 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
   // the plan lists the longest items first; dealt in a snake as in the dense
   // causal call
   a.sched = 2;
-  const long long units = (long long)max_items * a.Hq;
+  const long long units = (long long)max_items * (a.head_pairs ? a.Hq / 2 : a.Hq);
   const int grid = (int)(units < info.sm_count ? units : info.sm_count);
   const bool plain = a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal));
   record_timing(false, stream);
@@ -938,7 +948,10 @@ static int launch_fwd_var_d(const CUtensorMap& tq, const CUtensorMap& tk, const 
     if (launch_pdl(fwd_kernel<D, 0, false, true>, dim3(grid), dim3(320), L::kAllocBytes, stream, tq, tk,
                    tv, a, Tails<true, 1>{{tails.of[0]}}) != cudaSuccess)
       return FA_ERR_CUDA;
-  } else if (launch_pdl(a.cu ? fwd_kernel<D, 3, false, true, true> : fwd_kernel<D, 3, false, true>,
+  } else if (launch_pdl(a.head_pairs ? (a.cu ? fwd_kernel<D, 3, false, true, true, true>
+                                             : fwd_kernel<D, 3, false, true, false, true>)
+                                     : (a.cu ? fwd_kernel<D, 3, false, true, true>
+                                             : fwd_kernel<D, 3, false, true>),
                         dim3(grid), dim3(320), LW::kAllocBytes, stream, tq, tk, tv, a, tails) !=
              cudaSuccess) {
     return FA_ERR_CUDA;

@@ -81,6 +81,7 @@ struct PlanArgs {
   int desc;  // without a causal mask: each sequence's tiles from the last down
   int pad;  // VarItem::pad0 counts sequences padded to this many rows (a power of two)
   VarItem* items;
+  int narrow;  // items of 16 bytes, without pad0
   int max_items;
   int* n_items;
   int* status;   // gets FA_ERR_INVALID_ARG where cu is not ascending within [0, T]
@@ -134,6 +135,8 @@ struct FwdArgs {
   const int* n_items;
   int T;
   const int* cu;  // or the sequences' first rows [B + 1], for a block's own plan (kMod 3)
+  // units are a query tile of two heads of one kv head (kMod 3), and items 16 bytes apart
+  int head_pairs;
   // packed calls with a window: the keys j < sinks of a sequence stay visible behind
   // it (at most kTile, so tile 0 holds them)
   int sinks;

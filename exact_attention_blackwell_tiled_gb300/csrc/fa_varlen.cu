@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const PlanArgs p)
   auto place = [&](int t, int before) {
     before += plan_descends(p) ? n_own - 1 - t : t;
     if (before >= p.max_items) return;
-    int4* dst = reinterpret_cast<int4*>(p.items + before);
+    int4* dst = reinterpret_cast<int4*>(p.items) + (p.narrow ? before : 2 * before);
     dst[0] = make_int4(row0, len, t, b);
-    dst[1] = make_int4(pad0, 0, 0, 0);
+    if (!p.narrow) dst[1] = make_int4(pad0, 0, 0, 0);
   };
   if (n_own < 8) {
     for (int t = 0; t < n_own; ++t) {
@@ -168,6 +168,18 @@ int check_var(int B, int T, int Hq, int Hkv, int D) {
   const long long t_pad = ((long long)T + 127) / 128 * 128 + 128LL * B;
   if (t_pad * Hq > INT32_MAX) return FA_ERR_INVALID_ARG;
   return FA_OK;
+}
+
+// Forward calls under a window with an even number of q heads to a kv head: a unit is one
+// tile of 128 query rows of two heads, not two tiles of one.  Its items are more, but of 16
+// bytes, as many as the others' room holds.  Measured, us, two tiles / two heads, 4 sinks:
+// 16384 tokens in one sequence, 32 / 8 heads, window 1024, of 128 299 / 273, of 64 259 / 243; 256
+// 154 / 136 and 136 / 124; 4099 tokens in 5, 16 / 4 heads, 300, 31.5 / 28.3 and 27.2 / 24.7; 40 of
+// 100 23.6 / 19.3 and 20.7 / 18.2; 437 in one, 8 / 1 heads 13.6 / 11.9 and 11.7 / 10.5.  Where
+// sequences of one tile leave SMs without a unit, a unit of one head is done sooner: 10 of 44
+// tokens, 4 / 2 heads, 8.0 / 9.1 and 6.8 / 7.5.
+bool head_pairs(int B, int T, int Hq, int Hkv) {
+  return Hq / Hkv % 2 == 0 && (T >= 128LL * B || (T / 256 + (long long)B) * Hq > 152);
 }
 
 // The sinks of a call that count: none where no window hides a key from any query.
@@ -308,6 +320,8 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
       misaligned(lse, 4) || misaligned(cu_seqlens, 4))
     return FA_ERR_MISALIGNED;
+  const int wl = window_side(window_left, T), wr = window_side(window_right, T);
+  const int seen = window_sinks(sinks, wl, T);
   const VarLayout L = var_layout(B, T, Hq, Hkv, D, false, false, -1, 0);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
@@ -319,22 +333,23 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   // (k's are the sinks' in front of a window)
   if (!tail_maps(t[2], T, D, &tails.of[0])) return FA_ERR_CUDA;
   tails.of[1] = tails.of[0];
-  if (window_sinks(sinks, window_side(window_left, T), T) && !tail_maps(t[1], T, D, &tails.of[1]))
-    return FA_ERR_CUDA;
+  if (seen && !tail_maps(t[1], T, D, &tails.of[1])) return FA_ERR_CUDA;
   PlanArgs p{};
   FwdArgs a{};
-  a.wl = window_side(window_left, T);
-  a.wr = window_side(window_right, T);
-  a.causal = (a.wl < 0 && a.wr == 0) ? 1 : 0;
-  a.sinks = window_sinks(sinks, a.wl, T);
+  a.wl = wl;
+  a.wr = wr;
+  a.causal = (wl < 0 && wr == 0) ? 1 : 0;
+  a.sinks = seen;
+  a.head_pairs = (wl >= 0 || wr > 0) && head_pairs(B, T, Hq, Hkv) ? 1 : 0;
   p.cu = cu_seqlens;
   p.B = B;
   p.T = T;
-  p.item_rows = 256;
+  p.item_rows = a.head_pairs ? 128 : 256;
   p.pad = 64;
   p.causal = a.causal;
   p.items = reinterpret_cast<VarItem*>(ws + L.off_items);
-  p.max_items = L.max_items;
+  p.max_items = a.head_pairs ? T / 128 + B : L.max_items;
+  p.narrow = a.head_pairs;
   p.n_items = reinterpret_cast<int*>(ws + 64);
   p.status = fwd_status_word();
   p.counter = reinterpret_cast<int*>(ws + 128);
@@ -351,11 +366,11 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   a.n_items = p.n_items;
   a.T = T;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.sinks && plan_fits_block(B, L.max_items, false))
+  if (a.sinks && plan_fits_block(B, p.max_items, false))
     a.cu = cu_seqlens;
   else if ((rc = launch_plan(p, st)))
     return rc;
-  return launch_fwd_var(maps[0], maps[1], maps[2], tails, a, D, L.max_items, st);
+  return launch_fwd_var(maps[0], maps[1], maps[2], tails, a, D, p.max_items, st);
 }
 
 int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const void* dO,

@@ -55,7 +55,8 @@ __device__ __forceinline__ void unit_coords(const FwdArgs& a, int u, int& bh, in
 // 2 * pair and 2 * pair + 1, its split of the kv tiles, and the sizes of its
 // sequence.  Packed calls (kVar): units are (item, head) with the head running
 // fastest, an item of the plan names a sequence (rows row0 .. row0 + Sq - 1 of
-// the packed tensors) and a pair of its query tiles, and bh is the head alone.
+// the packed tensors) and a pair of its query tiles, and bh is the head alone.  kHeads: an
+// item names one query tile, and the pair is that tile of two heads of one kv head.
 struct FwdUnit {
   int bh, pair, split;
   int b, h;   // batch entry and query head
@@ -63,14 +64,14 @@ struct FwdUnit {
   int row0;   // its first packed row (kVar)
 };
 
-template <bool kVar>
+template <bool kVar, bool kHeads = false>
 __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, const VarItem* items, int u) {
   FwdUnit w;
   w.row0 = 0;
   if constexpr (kVar) {
-    const int item = u / a.Hq;
-    const VarItem it = load_item(items, item);
-    w.h = w.bh = u - item * a.Hq;
+    const int per = kHeads ? a.Hq / 2 : a.Hq, item = u / per;
+    const VarItem it = load_item<kHeads>(items, item);
+    w.h = w.bh = (u - item * per) * (kHeads ? 2 : 1);
     w.b = it.b;
     w.pair = it.tile;
     w.split = 0;
@@ -164,12 +165,17 @@ struct SinkSpan {
   __device__ __forceinline__ int begin(int t) const { return has ? 0 : plo[t]; }
   __device__ __forceinline__ int next(int t, int p) const { return max(p + 1, plo[t]); }
 };
+template <bool kHeads>
 __device__ __forceinline__ SinkSpan sink_kv_span(int Sq, int wl, int wr, int sinks, int pair) {
   SinkSpan s;
   s.has = sinks > 0;
   int lo[2], hi[2];
-  tile_kv_range(Sq, wl, wr, Sq, 2 * pair, lo[0], hi[0]);
-  tile_kv_range(Sq, wl, wr, Sq, 2 * pair + 1, lo[1], hi[1]);
+  tile_kv_range(Sq, wl, wr, Sq, kHeads ? pair : 2 * pair, lo[0], hi[0]);
+  if constexpr (kHeads) {
+    lo[1] = lo[0], hi[1] = hi[0];
+  } else {
+    tile_kv_range(Sq, wl, wr, Sq, 2 * pair + 1, lo[1], hi[1]);
+  }
   s.jlo = lo[0];
   s.first = s.has && s.jlo > 0;
   s.n = 0;

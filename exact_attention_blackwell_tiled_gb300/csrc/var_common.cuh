@@ -93,9 +93,10 @@ __device__ __forceinline__ int plan_in_block(const PlanArgs& p, int warp, int wa
   return warp_add(n);
 }
 
-// The part of an item every kernel reads, in one 16-byte load.
+// The part of an item every kernel reads, in one 16-byte load (kNarrow: all there is of it).
+template <bool kNarrow = false>
 __device__ __forceinline__ VarItem load_item(const VarItem* items, int i) {
-  const int4 x = *reinterpret_cast<const int4*>(items + i);
+  const int4 x = reinterpret_cast<const int4*>(items)[kNarrow ? i : 2 * i];
   VarItem it;
   it.row0 = x.x;
   it.len = x.y;
