@@ -19,7 +19,10 @@
 // taken by another block's sequence.  Only many new tokens' positions and slots take a
 // second launch, for the whole GPU's stores.
 //
-// Measured: 64 sequences that grow by a token under a window of 4,096 (one block) 5 us, 8
+// The hidden entries are read in every call, for any of them may still hold a page (it
+// may have been taken without the window): 4 bytes for each page's tokens of the past.
+//
+// Measured: 64 sequences that grow by a token under a window of 4,096 (one block) 5.7 us, 8
 // cold; 1,024 sequences, 244,000 new tokens, 17 us and 9 for the second launch (one launch
 // for all: 48).
 #include <cuda_runtime.h>
@@ -36,9 +39,12 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxSequences = 65536;  // their sums lie in shared memory
-// One block where a warp has at most two sequences, else a cluster of the eight that every
-// device grants.
+// One block where a warp has at most two sequences and a window's hidden entries are not too
+// many to read, else a cluster of the eight that every device grants.  Measured, us, one block / cluster, a window of 4,096:
+// 64 sequences, tables of 524,352 entries in all 17.0 / 9.6, 131,136 9.5 / 8.3, 65,600 8.0 /
+// 7.7, 16,448 5.7 / 7.6; one sequence of 65,537 6.4 / 9.3; 524,352 without a window 4.5 / 6.6.
 constexpr int kOneBlock = 64, kCluster = 8;
+constexpr long long kOneBlockEntries = 131072;
 constexpr int kApart = 8192;  // more new tokens than this are written by a launch of their own
 
 struct PageArgs {
@@ -101,19 +107,74 @@ __device__ __forceinline__ Sums shfl_up(const Sums& x, int o) {
           __shfl_up_sync(0xffffffffu, x.tokens, o)};
 }
 
-// Visits the entries that go back to the pool, in order, by a whole warp: f(e, page, rank)
-// for the lanes that hold one; returns their number.  A lane loads several entries at a time,
-// for it is the loads' latency that counts.
-constexpr int kAtOnce = 8;
-template <typename F>
-__device__ __forceinline__ int returned(const PageArgs& a, int b, const Sequence& s, F f) {
+// The entries that may go back to the pool are hidden ones, [hs, min(he, n0)), and those
+// behind the new length, [n1, n0) (he <= n1).  2^log warps share a sequence's: the first
+// ones in equal parts, the others the last warp's.
+struct Stretch {
+  int lo, hi;
+};
+__device__ __forceinline__ Stretch stretch(const Sequence& s, int part, int slice, int log) {
+  if (part) return slice == (1 << log) - 1 ? Stretch{s.n1, s.n0} : Stretch{0, 0};
+  const long long n = max(0, min(s.he, s.n0) - s.hs);
+  return {s.hs + (int)(n * slice >> log), s.hs + (int)(n * (slice + 1) >> log)};
+}
+
+// A lane loads several entries at a time, for it is the loads' latency that counts.
+constexpr int kAtOnce = 8, kPieces = 4;
+
+// The number of pages among them, by a whole warp, 16 bytes a load.
+__device__ __forceinline__ int count_returned(const PageArgs& a, int b, const Sequence& s, int slice,
+                                              int log) {
   const int lane = threadIdx.x & 31;
   const int* row = a.table + (size_t)b * a.width;
   int count = 0;
-  // hidden ones, then those behind the new length (he <= n1)
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    const int lo = part ? s.n1 : s.hs, hi = part ? s.n0 : min(s.he, s.n0);
+    const Stretch x = stretch(s, part, slice, log);
+    int lo = x.lo;
+    const unsigned pages = a.pages;  // (a negative entry is none)
+    if (x.hi - lo > 32 * kAtOnce) {
+      // a long one: 16 bytes a load, behind the entries in front of the first such piece
+      const int edge = (int)(-(reinterpret_cast<uintptr_t>(row + lo) >> 2) & 3);
+      if (lane < edge) count += (unsigned)row[lo + lane] < pages;
+      lo += edge;
+#pragma unroll 1
+      for (; lo + 128 * kPieces <= x.hi; lo += 128 * kPieces) {
+        int4 page[kPieces];
+#pragma unroll
+        for (int y = 0; y < kPieces; ++y) page[y] = *reinterpret_cast<const int4*>(row + lo + 128 * y + 4 * lane);
+#pragma unroll
+        for (int y = 0; y < kPieces; ++y)
+          count += ((unsigned)page[y].x < pages) + ((unsigned)page[y].y < pages) +
+                   ((unsigned)page[y].z < pages) + ((unsigned)page[y].w < pages);
+      }
+    }
+#pragma unroll 1
+    for (; lo < x.hi; lo += 32 * kAtOnce) {
+      int page[kAtOnce];
+#pragma unroll
+      for (int y = 0; y < kAtOnce; ++y) {
+        const int e = lo + 32 * y + lane;
+        page[y] = e < x.hi ? row[e] : -1;
+      }
+#pragma unroll
+      for (int y = 0; y < kAtOnce; ++y) count += (unsigned)page[y] < pages;
+    }
+  }
+  return __reduce_add_sync(0xffffffffu, count);
+}
+
+// Visits those entries in order, by a whole warp: f(e, page, rank) for the lanes that hold one.
+template <typename F>
+__device__ __forceinline__ void returned(const PageArgs& a, int b, const Sequence& s, int slice, int log,
+                                         F f) {
+  const int lane = threadIdx.x & 31;
+  const int* row = a.table + (size_t)b * a.width;
+  int count = 0;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const Stretch range = stretch(s, part, slice, log);
+    const int lo = range.lo, hi = range.hi;
 #pragma unroll 1
     for (int e0 = lo; e0 < hi; e0 += 32 * kAtOnce) {
       int page[kAtOnce];
@@ -131,7 +192,6 @@ __device__ __forceinline__ int returned(const PageArgs& a, int b, const Sequence
       }
     }
   }
-  return count;
 }
 
 // The last of the ascending numbers x[lo .. lo + n - 1] that is at most t.
@@ -173,6 +233,7 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
   // [per] each: taken, back, tokens (counts, then sums before), lengths, of the block's sequences
   extern __shared__ int s_taken[];
   __shared__ Sums s_warp[32], s_total;
+  __shared__ int s_slice[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank = 0;
   if constexpr (!kOne) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -199,17 +260,31 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
   }
   __syncthreads();
   auto sequence = [&](int i) { return make_sequence(a, s_old[i], s_new[i]); };
-  // ---- counts, a warp per sequence
-  for (int i = warp; i < n; i += 32) {
+  // ---- counts, a warp per sequence, or a group of 2^log where the block has few
+  int log = 0;
+  while (n > 0 && log < 5 && (n << (log + 1)) <= 32) ++log;
+  const int slice = warp & ((1 << log) - 1);
+  for (int i = warp >> log; i < n; i += 32 >> log) {
     const Sequence s = sequence(i);
-    const int back = returned(a, b0 + i, s, [](int, int, int) {});
+    const int back = count_returned(a, b0 + i, s, slice, log);
     if (lane == 0) {
-      s_taken[i] = s.taken();
-      s_back[i] = back;
-      s_tokens[i] = max(0, s.N - s.L);
+      s_slice[warp] = back;
+      if (slice == 0) {
+        s_taken[i] = s.taken();
+        s_back[i] = back;
+        s_tokens[i] = max(0, s.N - s.L);
+      }
     }
   }
   __syncthreads();
+  if (log > 0) {  // (one sequence to a group)
+    if (tid < n) {
+      int sum = 0;
+      for (int x = 0; x < 1 << log; ++x) sum += s_slice[(tid << log) + x];
+      s_back[tid] = sum;
+    }
+    __syncthreads();
+  }
   // ---- sums before each sequence, in the block
   const int each = (n + kThreads - 1) / kThreads, i0 = min(n, tid * each), i1 = min(n, i0 + each);
   Sums own = {0, 0, 0};
@@ -272,12 +347,14 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
   __syncthreads();
   // ---- back to the pool
   const Sums end = before + s_total;
-  for (int i = warp; i < n; i += 32) {
+  for (int i = warp >> log; i < n; i += 32 >> log) {
     if ((i + 1 < n ? s_back[i + 1] : end.back) == s_back[i]) continue;
+    if (log > 0 && s_slice[warp] == 0) continue;
     const Sequence s = sequence(i);
     int* row = a.table + (size_t)(b0 + i) * a.width;
-    const int first = height + s_back[i];
-    returned(a, b0 + i, s, [&](int e, int page, int r) {
+    int first = height + s_back[i];
+    for (int x = 0; x < slice; ++x) first += s_slice[warp - slice + x];
+    returned(a, b0 + i, s, slice, log, [&](int e, int page, int r) {
       if (first + r < a.pages) a.stack[first + r] = page;
       else bad = true;  // more pages than the pool has: one was held twice
       row[e] = -1;
@@ -414,7 +491,8 @@ extern "C" int fa_page_update(int* page_table, int table_width, int* free_pages,
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  const bool one = B <= kOneBlock;
+  const bool one =
+      B <= kOneBlock && (window_left < 0 || (long long)B * table_width <= kOneBlockEntries);
   const int blocks = one ? 1 : kCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);

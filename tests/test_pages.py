@@ -189,6 +189,28 @@ def test_lengths_and_counts_out_of_range(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,width", [(1, 9001), (3, 2501), (40, 2050), (70, 1283), (64, 2049)])
+def test_long_tables_under_a_window(gpu, B, width):
+    """Many pages behind a window at once, in rows that begin at any 4 bytes, with holes; then
+    the next step, which finds them gone."""
+    rng = random.Random(B)
+    lens, table, used = [], [], 0
+    for b in range(B):
+        n = rng.choice([width * 16 - 3, width * 16 // 2, rng.randrange(1, width * 16 - 2), 5])
+        row = [-1] * width
+        for e in range(-(-n // 16)):
+            if rng.random() < 0.9:
+                row[e], used = used, used + 1
+        lens.append(n)
+        table.append(row)
+    stack = list(range(used, used + 9 * B))
+    new = [n + rng.randrange(0, 3) for n in lens]
+    _check(table, stack + [0] * used, len(stack), lens, new, 16, 1000, 20, 3 * B)
+    new = [rng.choice([0, n, n // 3]) for n in lens]  # shorter ones give back both ends
+    _check(table, stack + [0] * used, len(stack), lens, new, 16, 777, 0, 3)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [8192, 8193, 50000])
 def test_many_new_tokens(gpu, T):
     """Prompts of many tokens, more than the one launch writes, some of them empty."""
