@@ -361,3 +361,47 @@ def test_long_sequences_in_many_shares(D, det):
         dk_tol[:, h // 2] += scale * (e_ds.T @ qh.abs())
     for x, ref, tol in ((g[1], dk, dk_tol), (g[2], dv, dv_tol)):
         assert bool(((x[lo:hi].double() - ref).abs() <= tol + u * ref.abs()).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Hq,Hkv,D,window,sinks", [
+    ([700, 300], 7, 1, 64, (100, 0), 4),              # an odd group
+    ([40] * 30 + [500], 8, 2, 64, (37, 0), 3),        # many short sequences, an even one
+    ([40] * 30 + [500], 8, 2, 128, (37, 0), 40),
+    ([90] * 16, 4, 2, 128, (20, 0), 2),               # the most sequences that a block plans
+    ([90] * 17, 4, 2, 128, (20, 0), 2),
+    ([200] * 10, 4, 1, 64, (50, 0), 2),
+    ([200] * 11, 4, 1, 64, (50, 0), 2),
+    ([500, 300], 4, 2, 128, (-1, 7), 0),              # windows without sinks, open to the left
+    ([500, 300], 4, 2, 64, (30, -1), 0),              # and to the right
+    ([500, 300], 4, 4, 64, (30, 9), 0),
+])
+def test_units_of_every_kind(lens, Hq, Hkv, D, window, sinks):
+    """Two tiles of a head or two heads of a tile, planned by a launch or by each block."""
+    test_forward_and_backward(lens, Hq, Hkv, D, window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [3, 40])
+@pytest.mark.parametrize("group", [1, 2])
+def test_boundaries_out_of_order(B, group):
+    """Recorded, and nothing is written, whoever plans the call."""
+    __graft_entry__.build()
+    T, D, window, sinks = 40 * B, 64, (20, 0), 3
+    q, k, v, do = (x.cuda() for x in _inputs(T, 2 * group, 2, D, B))
+    for bad in (T + 1, -1, 41):
+        cu = _cu(_bounds([40] * B))
+        cu[B if bad > T else 1 if bad < 0 else 2] = bad if bad != 41 else 39
+        o = torch.full_like(q, 7.0)
+        lse = torch.full((2 * group, T), 7.0, device="cuda")
+        fa.fwd_varlen(q, k, v, cu, window=window, sinks=sinks, out=o, lse=lse)
+        assert fa.fwd_status() == 1
+        assert bool((o == 7).all()) and bool((lse == 7).all())
+        for det in (False, True):
+            ws = torch.empty(fa.varlen_workspace_bytes(B, T, 2 * group, 2, D, True, det, window=window,
+                                                       sinks=sinks), dtype=torch.uint8, device="cuda")
+            g = [torch.full_like(x, 7.0) for x in (q, k, v)]
+            fa.bwd_varlen(q, k, v, o, do, lse, cu, window=window, sinks=sinks, deterministic=det,
+                          workspace=ws, dq=g[0], dk=g[1], dv=g[2])
+            assert fa.bwd_status(ws) == 1
+            assert all(bool((x == 7).all()) for x in g)
