@@ -18,9 +18,11 @@
 // and leaves one fp32 part of dK_s and dV_s, which the last kernel of the call adds up.
 //
 // Measured, 16,384 tokens of 16 heads of 128, 16 sinks: 55 us, 4.8 TB/s of the 264 MB (of dQ
-// half stays in L2); one block per SM (shared memory) and its chain of load, products,
-// exponentials, products and stores bound it, not memory (38% of it busy).  At head dimension
-// 64, 4,099 tokens of 16 heads, two blocks per SM: 12 us, 16 with one.
+// half stays in L2); one block per SM (shared memory), a chain of load, products,
+// exponentials, products and stores, 38% of DRAM busy.  Slower: two groups of warps with
+// buffers of their own (65), or with the preprocess kernel's work in it (115 against 55 and
+// 31 for both).  At head dimension 64, 4,099 tokens of 16 heads, two blocks per SM: 12 us,
+// 16 with one.
 //
 // Warps 0-3: a query row per thread (TMEM lane); warp 4: TMA; warp 5: TMEM and MMAs.
 // The dQ columns lie over those of S and dP, which are read before dQ is issued; the next

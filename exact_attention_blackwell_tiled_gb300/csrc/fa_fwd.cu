@@ -50,11 +50,12 @@ __device__ int g_fwd_status = 0;
 // N, GEMM 2 with K of 32, a quarter of the softmax), from keys and values of their own
 // in shared memory, so that the ring's tiles are the window's.
 // Measured, 16,384 tokens in sequences of up to 8,192, 32 query and 8 kv heads of 128, a window
-// of 1,024 with 4 sinks: 266 us, 44% of tensor cycles (the plain causal kernel 57%);
-// one sequence of 16,384: 310, 300 without sinks, 391 before this form.  It is bound by a
-// step's chain as the plain kernel is, and by 9,000 of a unit's 43,000 cycles at its ends.
-// Slower: two Q stages and three for K/V (304 against 280 for the first), an issuing thread per tile
-// (338 against 310 for the second), K/V waits between the tiles (334), a whole-row epilogue (325).
+// of 1,024 with 4 sinks: 249 us with two heads a unit (kHeads), 49% of tensor cycles (the
+// plain causal kernel 57%), 270 and 44% with two tiles; one sequence of 16,384: 272, 258
+// without sinks, 391 before this form.  It is bound by a step's chain as the plain kernel
+// is, and by some 9,000 of a unit's 40,000 cycles at its ends.  Slower: two Q stages and three
+// for K/V (304 against 280), an issuing thread per tile (338 against 310), K/V waits between
+// the tiles (334), a whole-row epilogue (325), GEMM 2 begun on half of P (362 against 272).
 constexpr int kFewSinks = 32;
 
 template <int D, int kMod = 0>
