@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess(const BwdArgs a) {
 // rows with few keys that moves dS about as much as its own rounding to bf16 for the
 // products does (2^-9 of it each).
 template <int D>
-__global__ void __launch_bounds__(256) bwd_preprocess_var(const BwdArgs a, const PlanArgs p) {
+__global__ void __launch_bounds__(256, 4) bwd_preprocess_var(const BwdArgs a, const PlanArgs p) {
   __shared__ VarItem s_items[kBlockPlanItems];
   grid_dep_wait();
   grid_dep_launch();
