@@ -120,7 +120,7 @@ __device__ __forceinline__ Stretch stretch(const Sequence& s, int part, int slic
 }
 
 // A lane loads several entries at a time, for it is the loads' latency that counts.
-constexpr int kAtOnce = 8, kPieces = 4;
+constexpr int kAtOnce = 8, kPieces = 4, kTakes = 4;
 
 // The number of pages among them, by a whole warp, 16 bytes a load.
 __device__ __forceinline__ int count_returned(const PageArgs& a, int b, const Sequence& s, int slice,
@@ -361,32 +361,30 @@ __global__ void __launch_bounds__(kThreads) page_kernel(const PageArgs a) {
     });
   }
   sync_all<kOne>();
-  // ---- from the pool
+  // ---- from the pool: the block's entries, dealt to its threads
   const int top = height + total.back;  // (both at most the pool's and the tables' entries)
-  for (int i = warp; i < n; i += 32) {
-    if ((i + 1 < n ? s_taken[i + 1] : end.taken) == s_taken[i]) continue;
-    const Sequence s = sequence(i);
-    int* row = a.table + (size_t)(b0 + i) * a.width;
-    // entries in front of the hidden ones and behind them
-    const int lo1 = s.n0, hi1 = min(s.n1, max(s.n0, s.hs < s.he ? s.hs : s.n1));
-    const int lo2 = s.hs < s.he ? max(s.n0, s.he) : s.n1, hi2 = s.n1;
-    const int c1 = max(0, hi1 - lo1), c = c1 + max(0, hi2 - lo2);
-    const int first = top - 1 - s_taken[i];
 #pragma unroll 1
-    for (int x0 = lane; x0 < c; x0 += 32 * kAtOnce) {
-      int page[kAtOnce];
+  for (int y0 = before.taken + tid; y0 < end.taken; y0 += kTakes * kThreads) {
+    int page[kTakes];
 #pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) {
-        const int x = x0 + 32 * y, at = first - x;
-        const bool there = at >= 0 && at < a.pages;
-        page[y] = x < c && there ? __ldcg(a.stack + at) : -1;
-        bad |= x < c && !there;
-      }
-#pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) {
-        const int x = x0 + 32 * y;
-        if (x < c) row[x < c1 ? lo1 + x : lo2 + x - c1] = page[y];
-      }
+    for (int z = 0; z < kTakes; ++z) {
+      const int y = y0 + z * kThreads, at = top - 1 - y;
+      const bool there = at >= 0 && at < a.pages;
+      page[z] = y < end.taken && there ? __ldcg(a.stack + at) : -1;
+      bad |= y < end.taken && !there;
+    }
+#pragma unroll 1
+    for (int z = 0; z < kTakes; ++z) {
+      const int y = y0 + z * kThreads;
+      if (y >= end.taken) break;
+      const int i = last_at_or_before(s_taken, 0, n, y), x = y - s_taken[i];
+      const Sequence s = sequence(i);
+      // entries in front of the hidden ones, then those behind them
+      const int lo1 = s.n0, hi1 = min(s.n1, max(s.n0, s.hs < s.he ? s.hs : s.n1));
+      const int lo2 = s.hs < s.he ? max(s.n0, s.he) : s.n1;
+      const int c1 = max(0, hi1 - lo1);
+      a.table[(size_t)(b0 + i) * a.width + (x < c1 ? lo1 + x : lo2 + x - c1)] =
+          z == 0 ? page[0] : z == 1 ? page[1] : z == 2 ? page[2] : page[3];
     }
   }
   if (rank == 0 && tid == 0) {
