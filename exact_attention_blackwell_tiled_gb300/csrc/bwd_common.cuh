@@ -311,6 +311,12 @@ __device__ __forceinline__ bool sink_sequence(const BwdArgs& a, int len) {
 __device__ __forceinline__ bool sink_tile(const BwdArgs& a, int len, int tile) {
   return a.sinks > 0 && min(len, (tile + 1) * kTile) > a.wl + 1;
 }
+// The first block of QB queries whose accumulator holds dQ of the sinks already, in a
+// sequence of len rows; INT_MAX: none.
+template <bool kMod, bool kVar, int QB>
+__device__ __forceinline__ int sink_first_block(const BwdArgs& a, int len) {
+  return kMod && kVar && sink_sequence(a, len) ? (a.wl + 1) / kTile * (kTile / QB) : INT_MAX;
+}
 // The first such tile.
 __device__ __forceinline__ int sink_first_tile(const BwdArgs& a) { return (a.wl + 1) / kTile; }
 

@@ -922,6 +922,7 @@ __global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1
           if (!ok) break;
         }
       }
+      const int sunk = kDet ? sink_first_block<kMod, kVar, kQB>(a, w.kv_len) : INT_MAX;
       for (int t = 0; t < (helper ? 0 : w.n_it); ++t, ++it) {
         const int gi = t / w.n_blk;
         const int iq = w.lo + (t - gi * w.n_blk);
@@ -939,7 +940,7 @@ __global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1
         bool first = false;  // this tile stores (deterministic mode)
         if (kDet) {
           dst += (size_t)(w.j % a.dq_groups) * a.dq_group_stride;
-          first = turn_of(w, iq) == 0;
+          first = turn_of(w, iq) == 0 && iq < sunk;
           if (!first) ok = warp_wait_b(bar(L::kBarSemOk + (it & 1)), (it >> 1) & 1, abort_flag);
           if (!ok) break;
         }
@@ -1219,13 +1220,6 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
       float4 x[kPieces][2];
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) x[e][0] = x[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.dq_sink && sink_tile(a, it.len, it.tile)) {
-        const float* sinks = a.dq_sink + ((size_t)h * a.T + it.row0 + i0) * D + c8 * 8;
-#pragma unroll
-        for (int e = 0; e < kPieces; ++e)
-          if (r0 + e * kRows < rows)
-            add_eight(x[e], reinterpret_cast<const float4*>(sinks + (size_t)e * kRows * D));
-      }
       // (deterministic: in fixed order, the groups that some kv tile wrote for this
       // block; otherwise the one accumulator, cleared before the main kernel)
 #pragma unroll 2

@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
         // query rows of the block that exist (kVar)
         const int n_rows = kVar ? w.kv_len - iq * kQB2 : kQB2;
         if (good) {
-          if (a.deterministic && turn == 0) {
+          if (a.deterministic && turn == 0 && iq < sink_first_block<kMod, kVar, kQB2>(a, w.kv_len)) {
 #pragma unroll
             for (int e = 0; e < kQB2; ++e)
               if (!kVar || e < n_rows) dst[(size_t)e * D] = u2f(v[e]);

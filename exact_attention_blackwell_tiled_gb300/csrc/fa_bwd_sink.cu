@@ -8,8 +8,7 @@
 // go the other way round, a tile of 128 queries against the few sinks:
 //   S = Q K_s^T, dP = dO V_s^T      (128 x N, N = s rounded up to 16)
 //   P = 2^(S scale log2 e - LSE2), dS = P (dP - Delta), 0 where i - j <= wl or j >= s
-//   dQ  = dS K_s                    stored as the accumulator's first value (or apart, in
-//                                   the deterministic mode)
+//   dQ  = dS K_s                    stored as the accumulator's first value
 //   dV_s += P^T dO, dK_s += dS^T Q  in TMEM over a run of tiles of one head and sequence
 // with P and dS rounded to bf16 for the products, as in the main kernels.  It needs Q, dO
 // and the row vectors once and writes dQ in fp32: 4 D + 4 D bytes per query and head, a
@@ -330,8 +329,7 @@ __global__ void __launch_bounds__(192, SinkSmem<D, kWide>::kBlocks)
       if (!warp_wait_b(bar(L::kBarDQFull), it & 1, abort_flag)) break;
       tc_fence_after();
       // the tile's rows of dQ
-      float* dst = (a.dq_sink ? a.dq_sink : a.dq_acc) +
-                   ((size_t)t.h * a.T + t.it.row0 + t.it.tile * kTile) * D;
+      float* dst = a.dq_acc + ((size_t)t.h * a.T + t.it.row0 + t.it.tile * kTile) * D;
       const int rows = min(kTile, t.it.len - t.it.tile * kTile);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {

@@ -233,16 +233,14 @@ struct BwdArgs {
   // packed calls with a window: the keys j < sinks of a sequence stay visible behind it
   // (at most kTile).  Pairs of a query and a sink behind its window are a kernel of
   // their own (fa_bwd_sink.cu), which leaves parts of dK and dV [Hq, sink_rows, D] (one
-  // per run of query tiles, at sink_slot) and its share of dQ, in the accumulator or, in
-  // the deterministic mode, in dq_sink [Hq, T, D].  The main kernel leaves the sinks'
-  // dK and dV over the window in fp32 too, [Hkv, sink_rows, D], unless dk_part holds
-  // them; the last kernel sums.
+  // per run of query tiles, at sink_slot) and its share of dQ in the accumulator (one, in
+  // the deterministic mode too).  The main kernel leaves the sinks' dK and dV over the window
+  // in fp32 too, [Hkv, sink_rows, D], unless dk_part holds them; the last kernel sums.
   int sinks;
   long long sink_rows;
   int sink_grid;           // blocks of that kernel
   float *sink_dk, *sink_dv;
   float *sink_dk0, *sink_dv0;
-  float* dq_sink;
   int qblk_rows;           // query rows per block of the main kernel (64 or 128):
                            // semaphore i of a head counts the writers of block i
 };

@@ -132,7 +132,7 @@ struct VarLayout {
   long long t_pad;
   bool split;  // q heads are units of their own (BwdArgs::dk_part)
   long long sink_rows;  // BwdArgs::sink_rows
-  size_t off_sink[4], off_dq_sink;
+  size_t off_sink[4];
   size_t off_items, off_acc, off_delta, off_lse2, off_sem, off_dk, off_dv, total;
 };
 
@@ -222,8 +222,6 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
       const int heads = i < 2 ? Hq : Hkv;
       L.total = up256(L.total + (size_t)heads * L.sink_rows * D * sizeof(float));
     }
-    L.off_dq_sink = L.total;
-    if (deterministic) L.total = up256(L.total + (size_t)Hq * T * D * sizeof(float));
   }
   return L;
 }
@@ -455,7 +453,6 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
     a.sink_dk0 = reinterpret_cast<float*>(ws + L.off_sink[2]);
     a.sink_dv0 = reinterpret_cast<float*>(ws + L.off_sink[3]);
     if (deterministic) {
-      a.dq_sink = reinterpret_cast<float*>(ws + L.off_dq_sink);
       // Under a window tile j adds to blocks from 2 j (64 rows) on: from the last tile down
       // the one before has been at a block two steps earlier, so that a chain never
       // waits; upwards each waits for the one before to be two blocks ahead, and the last
@@ -482,8 +479,9 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
     // 820 tokens, 16 / 4 heads, of 128 139 / 140 / 149, of 64 99 / 95 / 97; without a
     // mask of 128 555 / 545 / 567 and 186 / 181 / 187, of 64 493 / 474 / 439 and 148 /
     // 138 / 135.
-    // (chains that do not wait, a.desc: one)
-    const int most = a.desc ? (D == 128 ? 1 : 2) : a.causal ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
+    // (chains that do not wait, a.desc: one; 4099 tokens, 16 / 4 heads of 64 under 300, sinks: 87.7 /
+    // 90.1 / 93.2, of 128 133 / - / 148)
+    const int most = a.desc ? 1 : a.causal ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
     a.dq_groups = L.groups < most ? L.groups : most;
   } else {
     a.dq_groups = 1;
