@@ -197,9 +197,9 @@ VarLayout var_layout(int B, int T, int Hq, int Hkv, int D, bool backward, bool d
   L.total = up256(up256(L.off_items + (size_t)L.max_items * sizeof(VarItem)) + maps);
   if (!backward) return L;
   // as many accumulators as a dense call of twice the mean length would take (at most;
-  // the causal mask and D = 128 use fewer, see fa_bwd_varlen)
+  // the causal mask and D = 128 use fewer, sinks one, see fa_bwd_varlen_sink)
   const long long twice = 2LL * T / B + 1;
-  L.groups = dq_group_count((int)(twice < T ? twice : T), deterministic);
+  L.groups = sinks > 0 ? 1 : dq_group_count((int)(twice < T ? twice : T), deterministic);
   L.pad = bwd_qblk_rows(D, deterministic);
   L.t_pad = ((long long)T + L.pad - 1) / L.pad * L.pad + (long long)L.pad * B;
   L.off_acc = L.total;
@@ -479,9 +479,9 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
     // 820 tokens, 16 / 4 heads, of 128 139 / 140 / 149, of 64 99 / 95 / 97; without a
     // mask of 128 555 / 545 / 567 and 186 / 181 / 187, of 64 493 / 474 / 439 and 148 /
     // 138 / 135.
-    // (chains that do not wait, a.desc: one; 4099 tokens, 16 / 4 heads of 64 under 300, sinks: 87.7 /
-    // 90.1 / 93.2, of 128 133 / - / 148)
-    const int most = a.desc ? 1 : a.causal ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
+    // (Sinks, whose chains do not wait: one, L.groups.  4099 tokens, 16 / 4 heads of 64 under
+    // 300, 1 / 2 / 4: 87.7 / 90.1 / 93.2, of 128 1 / 4: 133 / 148.)
+    const int most = a.causal ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 4);
     a.dq_groups = L.groups < most ? L.groups : most;
   } else {
     a.dq_groups = 1;
