@@ -1429,8 +1429,8 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, const PlanArgs& p, i
     if (rc != FA_OK) return rc;
   }
   // units come from the global counter in the plan's order (longest first, each
-  // sequence's kv tiles ascending, which is also the order of the deterministic
-  // mode's chain)
+  // sequence's kv tiles ascending, with sinks descending in the deterministic mode, which
+  // is also the order of that mode's chain)
   a.dyn = 1;
   const bool mod = !(a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal)));
   const auto kernel = kDet && a.deterministic
