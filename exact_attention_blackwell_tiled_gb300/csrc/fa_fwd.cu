@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(320, 1)
   const int group = a.Hq / a.Hkv;
   constexpr bool kWin = kMod >= 1, kBias = kMod == 2, kSink = kMod == 3;
   static_assert((!kPlan && !kHeads) || kSink, "under a window");
-  __shared__ VarItem s_items[kPlan ? kBlockPlanItems : 1];
+  __shared__ VarItem s_items[kPlan ? kBlockPlanItemsFwd : 1];
   const VarItem* items = kPlan ? s_items : a.items;
   int n_units;
   if constexpr (kPlan) {

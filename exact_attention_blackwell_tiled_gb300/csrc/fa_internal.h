@@ -91,15 +91,19 @@ struct PlanArgs {
 int launch_plan(const PlanArgs& p, cudaStream_t stream);
 
 // Calls of so few sequences and items are planned by each block of their first kernel for
-// itself, in shared memory.  Measured, us with the plan kernel / so, window 256 with 4
-// sinks, 8 / 2 heads of 64: forward 10 sequences of 44 tokens 8.7 / 7.4, 16 of 100 8.9 / 8.3,
-// 32 of 60 12.0 / 11.5, 32 of 400 (82 items) 34.8 / 35.9; backward 1 of 437 38.3 / 35.2, 5 of 820
-// 56.4 / 53.5, 10 of 44 22.4 / 21.2, causal 16 of 100 24.1 / 24.5, 32 of 60 28.0 / 37.7 (each
-// item counts all sequences in turn), 2 of 8000 (127 items) 137.8 / 139.6.
-// (The forward without sinks keeps its two launches.)
-constexpr int kBlockPlanItems = 64;
-inline bool plan_fits_block(int B, int max_items, bool backward) {
-  return B <= (backward ? 10 : 16) && max_items <= kBlockPlanItems;
+// itself, in shared memory.  Measured, us with the plan kernel / so, 4 sinks:
+// backward, window 256, 8 / 2 heads of 64: 1 sequence of 437 tokens 38.3 / 35.2, 5 of 820 56.4 /
+// 53.5, 10 of 44 22.4 / 21.2, causal 16 of 100 24.1 / 24.5, 32 of 60 28.0 / 37.7 (each item
+// counts all sequences in turn), 2 of 8000 (127 items) 137.8 / 139.6;
+// forward, where all blocks plan at once: window 256, 8 / 2 heads of 64: 10 of 44 8.7 / 7.4, 16 of
+// 100 8.9 / 8.3, 32 of 60 12.0 / 11.5, 32 of 400 34.8 / 35.9; 16 of 500, 4 / 1 heads, 100, 13.6 /
+// 12.1; of 128: 9000, 16 / 4 heads, 300 (568 units) 54.3 / 51.3; 16,384, 16 / 16, 1,024 (1,040) 160
+// / 156; 16 of 1300, 32 / 8, 300 (2,848) 189 / 192; 6 sequences of 16,384 in all, 1,024 (2,144) 248.5 /
+// 251.  (The forward without sinks keeps its two launches.)
+constexpr int kBlockPlanItems = 64, kBlockPlanItemsFwd = 192;
+inline bool bwd_plan_fits_block(int B, int max_items) { return B <= 10 && max_items <= kBlockPlanItems; }
+inline bool fwd_plan_fits_block(int B, int max_items, long long units) {
+  return B <= 16 && max_items <= kBlockPlanItemsFwd && units <= 2048;
 }
 
 struct FwdArgs {

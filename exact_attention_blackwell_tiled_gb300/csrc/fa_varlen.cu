@@ -364,7 +364,8 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   a.n_items = p.n_items;
   a.T = T;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.sinks && plan_fits_block(B, p.max_items, false))
+  const long long units = (long long)p.max_items * Hq / (a.head_pairs ? 2 : 1);
+  if (a.sinks && fwd_plan_fits_block(B, p.max_items, units))
     a.cu = cu_seqlens;
   else if ((rc = launch_plan(p, st)))
     return rc;
@@ -506,7 +507,7 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
   a.T = T;
   a.T_pad = (int)L.t_pad;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!plan_fits_block(B, L.max_items, true)) {
+  if (!bwd_plan_fits_block(B, L.max_items)) {
     if ((rc = launch_plan(p, st))) return rc;
     p.cu = nullptr;
   }
