@@ -405,3 +405,67 @@ def test_boundaries_out_of_order(B, group):
                           workspace=ws, dq=g[0], dk=g[1], dv=g[2])
             assert fa.bwd_status(ws) == 1
             assert all(bool((x == 7).all()) for x in g)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [2, 30])
+@pytest.mark.parametrize("Hq", [2, 4])
+def test_nothing_but_empty_sequences(B, Hq):
+    """Rows of no sequence are left as they were, in every result."""
+    __graft_entry__.build()
+    T, D, window, sinks = 3000, 128, (20, 0), 3  # (the window hides keys in T rows)
+    q, k, v, do = (x.cuda() for x in _inputs(T, Hq, 2, D, 4))
+    for at in (0, 7, T):
+        cu = torch.full((B + 1,), at, dtype=torch.int32, device="cuda")
+        o, lse = torch.full_like(q, 7.0), torch.full((Hq, T), 7.0, device="cuda")
+        fa.fwd_varlen(q, k, v, cu, window=window, sinks=sinks, out=o, lse=lse)
+        assert fa.fwd_status() == fa.FA_OK and bool((o == 7).all()) and bool((lse == 7).all())
+        for det in (False, True):
+            g = [torch.full_like(x, 7.0) for x in (q, k, v)]
+            fa.bwd_varlen(q, k, v, o, do, lse, cu, window=window, sinks=sinks, deterministic=det,
+                          dq=g[0], dk=g[1], dv=g[2])
+            assert all(bool((x == 7).all()) for x in g)
+
+
+@pytest.mark.gpu
+def test_a_captured_call_follows_its_boundaries():
+    """One graph, replayed for other boundaries, planned by its blocks and by a launch."""
+    __graft_entry__.build()
+    Hq, Hkv, D, window, sinks, T = 4, 2, 64, (40, 0), 5, 600
+    q, k, v, do = (x.cuda() for x in _inputs(T, Hq, Hkv, D, 8))
+    for B in (4, 24):
+        cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+        o, lse = torch.zeros_like(q), torch.zeros(Hq, T, device="cuda")
+        g = [torch.zeros_like(x) for x in (q, k, v)]
+
+        def step():
+            fa.fwd_varlen(q, k, v, cu, window=window, sinks=sinks, out=o, lse=lse)
+            fa.bwd_varlen(q, k, v, o, do, lse, cu, window=window, sinks=sinks, deterministic=True,
+                          dq=g[0], dk=g[1], dv=g[2])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        gen = torch.Generator().manual_seed(B)
+        for _ in range(4):
+            cuts = torch.randint(0, T + 1, (B + 1,), generator=gen).sort().values.to(torch.int32)
+            cu.copy_(cuts.cuda())
+            for x in (o, lse, *g):
+                x.fill_(3.0)
+            graph.replay()
+            got = [x.clone() for x in (o, lse, *g)]
+            for x in (o, lse, *g):
+                x.fill_(3.0)
+            step()
+            assert all(torch.equal(x, y) for x, y in zip(got, (o, lse, *g)))
+            bounds = list(zip(cuts[:-1].tolist(), cuts[1:].tolist()))
+            r = packed_sinks(q.cpu(), k.cpu(), v.cpu(), bounds, window, sinks, do=do.cpu())
+            assert_within(o, r["o"], r["o_tol"], "o")
+            for name, x in zip(("dq", "dk", "dv"), g):
+                assert_within(x, r[name], r[name + "_tol"], name)
+        del graph
+    assert fa.fwd_status() == fa.FA_OK
