@@ -173,9 +173,9 @@ int check_var(int B, int T, int Hq, int Hkv, int D) {
 // Forward calls under a window with an even number of q heads to a kv head: a unit is one
 // tile of 128 query rows of two heads, not two tiles of one.  Its items are more, but of 16
 // bytes, as many as the others' room holds.  Measured, us, two tiles / two heads, 4 sinks:
-// 16384 tokens in one sequence, 32 / 8 heads, window 1024, of 128 299 / 273, of 64 259 / 243; 256
-// 154 / 136 and 136 / 124; 4099 tokens in 5, 16 / 4 heads, 300, 31.5 / 28.3 and 27.2 / 24.7; 40 of
-// 100 23.6 / 19.3 and 20.7 / 18.2; 437 in one, 8 / 1 heads 13.6 / 11.9 and 11.7 / 10.5.  Where
+// 16384 tokens in one sequence, 32 / 8 heads, window 1024, of 128 299 / 273, of 64 259 / 234; 256
+// 154 / 136 and 136 / 116; 4099 tokens in 5, 16 / 4 heads, 300, 31.5 / 28.1 and 27.2 / 24.2; 40 of
+// 100 23.6 / 19.5 and 20.7 / 17.5; 437 in one, 8 / 1 heads 13.6 / 11.8 and 11.7 / 10.2.  Where
 // sequences of one tile leave SMs without a unit, a unit of one head is done sooner: 10 of 44
 // tokens, 4 / 2 heads, 8.0 / 9.1 and 6.8 / 7.5.
 bool head_pairs(int B, int T, int Hq, int Hkv) {
