@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(320, 1)
         const int pair = w.pair;
         const int bhk = (kVar ? 0 : w.b * a.Hkv) + w.h / group;
         int lo[2], hi[2], jlo, nmax;
-        SinkSpan span;
+        SinkSpan<kHeads> span;
         if constexpr (kSink) {
           span = sink_kv_span<kHeads>(w.Sq, wl, wr, a.sinks, pair);
           jlo = 0;
@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(320, 1)
         auto load_position = [&]() -> bool {
           const int j = kSink ? span.tile(p) : p;
           const int row = w.row0 + j * kTile;
-          ++p;
           // (sinks in front of the window: the rows behind them are out of sight)
-          const int valid = kSink && span.first && j == 0 ? min(a.sinks, w.Sq) : w.Sq - j * kTile;
+          const int valid = kSink && span.first && p == 0 ? min(a.sinks, w.Sq) : w.Sq - j * kTile;
+          ++p;
           return load_kv(&tm_k, bhk, row, kTile) && load_kv(&tm_v, bhk, row, valid);
         };
         if constexpr (kSink) {
@@ -325,22 +325,13 @@ __global__ void __launch_bounds__(320, 1)
         // computes S for positions [plo[t], phi[t]) and O one position behind
         // (sinks: position 0 and the window's, SinkSpan)
         int plo[2], phi[2], jlo, nmax;
-        SinkSpan span;
-        struct {
-          int plo[2];
-          bool first[2];
-          __device__ __forceinline__ bool active(int t, int p, int hi) const {
-            return p < hi && (p >= plo[t] || (p == 0 && first[t]));
-          }
-        } gap;
+        SinkSpan<kHeads> span;
         if constexpr (kSink) {
           span = sink_kv_span<kHeads>(w.Sq, wl, wr, a.sinks, w.pair);
           nmax = span.n;
           for (int t = 0; t < 2; ++t) {
             plo[t] = span.begin(t);
             phi[t] = span.phi[t];
-            gap.first[t] = span.has;
-            gap.plo[t] = span.plo[t];
           }
         } else {
           pair_kv_span<kSplit>(a, w.Sq, wl, wr, unit_kv_len<kWin, kVar>(a, w), w.pair, w.split, plo,
@@ -365,6 +356,8 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_after();
         const uint32_t q_base = sbase + L::kOffQ + qs * 2 * L::kTileBytes;
         const uint32_t base_it = kv_it;  // ring position of K_0; V_j sits right after K_j
+        // whether tile t has a part in the sinks' step
+        auto front = [&](int t) { return t == 0 ? !span.twice : phi[1] > 0; };
         // Step j: GEMM 2 of position j - 1 and GEMM 1 of position j, which sit in the ring
         // `shift` places earlier.  kKind 0: any step; 1, 2: the sinks' GEMM 1 and GEMM 2
         auto step = [&](int j, int shift, auto kind) -> bool {
@@ -383,7 +376,7 @@ __global__ void __launch_bounds__(320, 1)
           for (int t = 0; t < 2; ++t) {
             // (sinks: a tile whose window begins behind position 1 is idle there)
             const bool old = kHeads ? j >= 1
-                             : kSink ? j >= 1 && (kKind == 2 ? phi[t] > 0 : gap.active(t, j - 1, phi[t]))
+                             : kSink ? j >= 1 && (kKind == 2 ? front(t) : span.active(t, j - 1))
                                    : j >= plo[t] + 1 && j <= phi[t];
             if (old) {
               // GEMM 2: O_t += P_t(j-1) V_{j-1}
@@ -403,7 +396,7 @@ __global__ void __launch_bounds__(320, 1)
               if (j == phi[t]) umma_commit(bar(L::kBarOFinal + t));
             }
             const bool now = kHeads ? kKind == 1 || j < nmax
-                             : kSink ? (kKind == 1 ? phi[t] > 0 : gap.active(t, j, phi[t]))
+                             : kSink ? (kKind == 1 ? front(t) : span.active(t, j))
                                    : j >= plo[t] && j < phi[t];
             if (now) {
               // GEMM 1: S_t = Q_t K_j^T
@@ -463,7 +456,7 @@ __global__ void __launch_bounds__(320, 1)
       const int qt = kHeads ? w.pair : 2 * w.pair + t, head = w.h + (kHeads ? t : 0);
       const int kv_len = unit_kv_len<kWin, kVar>(a, w);
       int jlo, jhi;
-      SinkSpan span;
+      SinkSpan<kHeads> span;
       if constexpr (kSink) {
         span = sink_kv_span<kHeads>(Sq, wl, wr, a.sinks, w.pair);
         jlo = span.begin(t);  // positions

@@ -150,41 +150,53 @@ __device__ __forceinline__ void pair_kv_span(const FwdArgs& a, int Sq, int wl, i
 }
 
 // The same with sinks (has), as positions: kv tile 0 is position 0 for every query tile with
-// rows, and where the windows begin behind it (first), theirs follow from position 1 on, so
-// that the tiles between the sinks and the window are left out.  plo[t] .. phi[t] are the
-// positions of tile t's window.  (A packed unit has rows and sees itself: n is not 0.)
+// rows, and where a window begins behind it (first), the windows' tiles follow from position
+// 1 on, so that the tiles between the sinks and the window are left out.  Position 0 then
+// has zeros for the values behind the sinks, lest a weight of zero meets an infinity there;
+// if the first tile's window begins in kv tile 0 all the same (twice), that tile comes
+// again at position 1, where the first query tile begins.  plo1 is the first position of
+// the second one's window, phi[t] the end of tile t's.  (A packed unit has rows and sees
+// itself: n is not 0.)
+template <bool kHeads>
 struct SinkSpan {
-  int plo[2], phi[2];  // phi 0: no rows
+  int plo1, phi[2];  // phi 0: no rows (the second tile's)
   int jlo, n;
-  bool has, first;
+  bool has, first, twice;
   __device__ __forceinline__ int tile(int p) const { return first && p == 0 ? 0 : jlo + p - (first ? 1 : 0); }
+  // Whether tile t computes at position p, its first position, and the next one.
   __device__ __forceinline__ bool active(int t, int p) const {
-    return has && p == 0 ? phi[t] > 0 : p >= plo[t] && p < phi[t];
+    if (kHeads) return p < n;
+    return p < phi[t] && (t == 0 ? p > 0 || !twice : p >= plo1 || (p == 0 && has));
   }
-  // tile t's first position, and the next one
-  __device__ __forceinline__ int begin(int t) const { return has ? 0 : plo[t]; }
-  __device__ __forceinline__ int next(int t, int p) const { return max(p + 1, plo[t]); }
+  __device__ __forceinline__ int begin(int t) const {
+    return kHeads ? 0 : t == 0 ? (twice ? 1 : 0) : has ? 0 : plo1;
+  }
+  __device__ __forceinline__ int next(int t, int p) const {
+    return kHeads || t == 0 ? p + 1 : max(p + 1, plo1);
+  }
 };
 template <bool kHeads>
-__device__ __forceinline__ SinkSpan sink_kv_span(int Sq, int wl, int wr, int sinks, int pair) {
-  SinkSpan s;
+__device__ __forceinline__ SinkSpan<kHeads> sink_kv_span(int Sq, int wl, int wr, int sinks, int pair) {
+  SinkSpan<kHeads> s;
   s.has = sinks > 0;
-  int lo[2], hi[2];
-  tile_kv_range(Sq, wl, wr, Sq, kHeads ? pair : 2 * pair, lo[0], hi[0]);
+  int lo0, hi0;
+  tile_kv_range(Sq, wl, wr, Sq, kHeads ? pair : 2 * pair, lo0, hi0);
+  s.jlo = lo0;
   if constexpr (kHeads) {
-    lo[1] = lo[0], hi[1] = hi[0];
+    s.first = s.has && lo0 > 0;
+    s.twice = false;
+    s.plo1 = 0;
+    s.n = s.phi[0] = s.phi[1] = hi0 - lo0 + (s.first ? 1 : 0);
   } else {
-    tile_kv_range(Sq, wl, wr, Sq, 2 * pair + 1, lo[1], hi[1]);
-  }
-  s.jlo = lo[0];
-  s.first = s.has && s.jlo > 0;
-  s.n = 0;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const bool rows = hi[t] > lo[t];
-    s.plo[t] = rows ? lo[t] - s.jlo + (s.first ? 1 : 0) : 0;
-    s.phi[t] = rows ? hi[t] - s.jlo + (s.first ? 1 : 0) : 0;
-    s.n = max(s.n, s.phi[t]);
+    int lo1, hi1;
+    tile_kv_range(Sq, wl, wr, Sq, 2 * pair + 1, lo1, hi1);  // (no rows: both are 0)
+    s.first = s.has && max(lo0, lo1) > 0;
+    s.twice = s.first && lo0 == 0;
+    const int shift = (s.first ? 1 : 0) - lo0;
+    s.phi[0] = hi0 + shift;
+    s.plo1 = hi1 > lo1 ? lo1 + shift : 0;
+    s.phi[1] = hi1 > lo1 ? hi1 + shift : 0;
+    s.n = max(s.phi[0], s.phi[1]);
   }
   return s;
 }
