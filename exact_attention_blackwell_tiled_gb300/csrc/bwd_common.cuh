@@ -29,7 +29,7 @@ __device__ __forceinline__ int win_right(const BwdArgs& a) {
 template <bool kMod>
 __device__ __forceinline__ int bwd_kv_len(const BwdArgs& a, int b) {
   if (!kMod || !a.seqlens_k) return a.Sk;
-  const int n = __ldg(a.seqlens_k + b);
+  const int n = a.seqlens_k[b];
   return n < 0 ? 0 : (n < a.Sk ? n : a.Sk);
 }
 

@@ -68,11 +68,12 @@ inline int c4_shift(int page_size) {
   return s;
 }
 
-// The page of block blk of sequence b, or -1.
+// The page of block blk of sequence b, or -1.  (A plain load: a kernel may be resident while
+// the one before it still writes the table, so this is not memory that is read only.)
 __device__ __forceinline__ int c4_page(const C4Table& t, int b, int blk) {
   const int e = blk >> t.shift;
   if (e >= t.width) return -1;
-  const int p = __ldg(t.pages + (size_t)b * t.width + e);
+  const int p = t.pages[(size_t)b * t.width + e];
   return p >= 0 && p < t.num_pages ? p : -1;
 }
 

@@ -1095,9 +1095,9 @@ __global__ void __launch_bounds__(256) bwd_dq_convert(const BwdArgs a) {
       // wrote for this query block (its semaphore, the count of warps that
       // added, is 0) holds stale memory and is skipped
       const int* sem = a.sem + (size_t)bh * a.n_qblk + i / (uint32_t)a.qblk_rows;
-      if (__ldg(sem) == 0) x0 = x1 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (*sem == 0) x0 = x1 = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int g = 1; g < a.dq_groups; ++g) {
-        if (__ldg(sem + (size_t)g * a.sem_group_stride) == 0) continue;
+        if (sem[(size_t)g * a.sem_group_stride] == 0) continue;
         const float4* src = reinterpret_cast<const float4*>(base + (size_t)g * a.dq_group_stride);
         const float4 y0 = src[0], y1 = src[1];
         x0.x += y0.x, x0.y += y0.y, x0.z += y0.z, x0.w += y0.w;

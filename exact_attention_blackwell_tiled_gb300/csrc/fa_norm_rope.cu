@@ -188,7 +188,7 @@ __device__ __forceinline__ auto row_of(const R& x, int token, int h) {
 
 // A token's position; -1 where it is of no sequence, or has no angles.
 __device__ __forceinline__ int position(const NormRopeArgs& a, int token) {
-  const int p = __ldg(a.pos + token);
+  const int p = a.pos[token];
   if (p >= a.P && (threadIdx.x & 31) == 0) atomicExch(a.status, (int)FA_ERR_INVALID_ARG);
   return p < a.P ? p : -1;
 }

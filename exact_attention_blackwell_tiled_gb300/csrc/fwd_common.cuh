@@ -91,7 +91,7 @@ __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, const VarItem* ite
 template <bool kWin>
 __device__ __forceinline__ int batch_kv_len(const FwdArgs& a, int b) {
   if (!kWin || !a.seqlens_k) return a.Sk;
-  const int n = __ldg(a.seqlens_k + b);
+  const int n = a.seqlens_k[b];
   return n < 0 ? 0 : (n < a.Sk ? n : a.Sk);
 }
 
