@@ -7,8 +7,10 @@
 // default).
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -171,7 +173,12 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const Place& place
 at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType dtype, const Place& place,
                   const char* name) {
   if (o != Py_None) return given(o, shape, dtype, place.device, name);
-  at::Tensor t = fresh(shape, dtype, place);
+  // (torch's deterministic algorithms want new memory filled, which at::empty does: rows
+  // that a call does not write are NaN then)
+  const at::Context& c = at::globalContext();
+  at::Tensor t = c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory()
+                     ? at::empty(shape, at::TensorOptions().dtype(dtype).device(c10::Device(at::kCUDA, place.device)))
+                     : fresh(shape, dtype, place);
   if (place.elsewhere()) t.record_stream(place.caller.unwrap());
   return t;
 }
