@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(256) slot_kernel(const PageArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int total = a.cu[a.B];
-  const int t0 = blockIdx.x * kChunk, t1 = min(t0 + kChunk, total);
+  const int t0 = blockIdx.x * kChunk, t1 = t0 + min(kChunk, total - t0);  // (up to INT_MAX)
   const int lane = threadIdx.x & 31;
   // the sequences of the first and the last token, each by a whole warp's search
   auto find = [&](int t) {
@@ -509,7 +509,7 @@ extern "C" int fa_page_update(int* page_table, int table_width, int* free_pages,
     return FA_ERR_CUDA;
   note_launches(1);
   if (a.apart) {
-    if (launch_pdl(slot_kernel, dim3((unsigned)((T + kChunk - 1) / kChunk)), dim3(256), 0, cfg.stream, a) !=
+    if (launch_pdl(slot_kernel, dim3((unsigned)(((long long)T + kChunk - 1) / kChunk)), dim3(256), 0, cfg.stream, a) !=
         cudaSuccess)
       return FA_ERR_CUDA;
     note_launches(1);
