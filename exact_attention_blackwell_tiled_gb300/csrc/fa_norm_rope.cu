@@ -112,7 +112,8 @@ struct Lane {
 
 // The rotation's factors for what a lane holds, at position p: an element times `own`, plus
 // its pair's other element (halves: the one of the other eight; neighbours: the one
-// beside it) times `other`.
+// beside it) times `other`.  (Elements that are not rotated have no other one: a product of
+// zero and an infinity there would be NaN.)
 template <int D, bool kPairs>
 __device__ __forceinline__ void load_factors(const NormRopeArgs& a, const Lane<D, kPairs>& L, int p,
                                              float2 (&own_a)[4], float2 (&own_b)[4],
@@ -300,9 +301,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const Norm
         float2 ya[4], yb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 za = __fmul2_rn(xa[e], own_a[e]), zb = __fmul2_rn(xb[e], own_b[e]);
-          ya[e] = __fmul2_rn(__ffma2_rn(other<kPairs>(xa[e], xb[e]), other_a[e], za), r2);
-          yb[e] = __fmul2_rn(__ffma2_rn(other<kPairs>(xb[e], xa[e]), other_b[e], zb), r2);
+          float2 za = __fmul2_rn(xa[e], own_a[e]), zb = __fmul2_rn(xb[e], own_b[e]);
+          if (lane.turns) {
+            za = __ffma2_rn(other<kPairs>(xa[e], xb[e]), other_a[e], za);
+            zb = __ffma2_rn(other<kPairs>(xb[e], xa[e]), other_b[e], zb);
+          }
+          ya[e] = __fmul2_rn(za, r2);
+          yb[e] = __fmul2_rn(zb, r2);
         }
         if (h < H) {
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -319,8 +324,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const Norm
 
 // The same walk, by blocks of their own for q and for k (one after the other in every block,
 // the second would wait for its first rows again).  A warp sums dw over its rows, and the
-// sums of its lanes, then of the block's warps, meet in shared memory.
-template <int D, bool kPairs>
+// sums of its lanes, then of the block's warps, meet in shared memory.  kAll: all of a row is
+// rotated, in halves (asked per lane, that takes registers that are not there: 70 -> 71 us for
+// 16,384 tokens of 32 heads of 128).
+template <int D, bool kPairs, bool kAll>
 __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_grad_kernel(const NormRopeArgs a) {
   using L = Lane<D, kPairs>;
   extern __shared__ uint4 s_rows[];  // [kGradDepth][x, dy][2][kThreads]
@@ -407,9 +414,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_grad_kernel(const
         widen(src[3 * kThreads], yb);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 za = __fmul2_rn(ya[e], own_a[e]), zb = __fmul2_rn(yb[e], own_b[e]);
-          ga[e] = __ffma2_rn(other<kPairs>(ya[e], yb[e]), kPairs ? swapped(other_a[e]) : other_b[e], za);
-          gb[e] = __ffma2_rn(other<kPairs>(yb[e], ya[e]), kPairs ? swapped(other_b[e]) : other_a[e], zb);
+          ga[e] = __fmul2_rn(ya[e], own_a[e]);
+          gb[e] = __fmul2_rn(yb[e], own_b[e]);
+          if (kAll || lane.turns) {
+            ga[e] = __ffma2_rn(other<kPairs>(ya[e], yb[e]), kPairs ? swapped(other_a[e]) : other_b[e], ga[e]);
+            gb[e] = __ffma2_rn(other<kPairs>(yb[e], ya[e]), kPairs ? swapped(other_b[e]) : other_a[e], gb[e]);
+          }
         }
       }
       widen(src[0], xa);
@@ -588,10 +598,12 @@ int allow_smem(int dev) {
       !set(norm_rope_kernel<64, true>, kSmem) ||
       !set(norm_rope_kernel<128, false>, kSmem) ||
       !set(norm_rope_kernel<128, true>, kSmem) ||
-      !set(norm_rope_grad_kernel<64, false>, kGradSmem) ||
-      !set(norm_rope_grad_kernel<64, true>, kGradSmem) ||
-      !set(norm_rope_grad_kernel<128, false>, kGradSmem) ||
-      !set(norm_rope_grad_kernel<128, true>, kGradSmem))
+      !set(norm_rope_grad_kernel<64, false, false>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<64, false, true>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<64, true, false>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<128, false, false>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<128, false, true>, kGradSmem) ||
+      !set(norm_rope_grad_kernel<128, true, false>, kGradSmem))
     return FA_ERR_CUDA;
   done[dev] = true;
   return FA_OK;
@@ -746,9 +758,12 @@ int fa_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
   a.status = fwd_status_word();
   if (!a.status) return FA_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const auto kernel =
-      D == 128 ? (interleaved ? norm_rope_grad_kernel<128, true> : norm_rope_grad_kernel<128, false>)
-               : (interleaved ? norm_rope_grad_kernel<64, true> : norm_rope_grad_kernel<64, false>);
+  const auto kernel = D == 128 ? (interleaved  ? norm_rope_grad_kernel<128, true, false>
+                                  : rot == D ? norm_rope_grad_kernel<128, false, true>
+                                             : norm_rope_grad_kernel<128, false, false>)
+                               : (interleaved  ? norm_rope_grad_kernel<64, true, false>
+                                  : rot == D ? norm_rope_grad_kernel<64, false, true>
+                                             : norm_rope_grad_kernel<64, false, false>);
   if (allow_smem(dev) != FA_OK) return FA_ERR_CUDA;
   if ((rc = launch(kernel, a.blocks, kThreads, kGradSmem, st, a))) return rc;
   return D == 128 ? launch(norm_rope_sum_kernel<128>, 2 * 128 / 32, 1024, 0, st, a)
