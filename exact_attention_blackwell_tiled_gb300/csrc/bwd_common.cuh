@@ -313,9 +313,9 @@ __device__ __forceinline__ bool sink_tile(const BwdArgs& a, int len, int tile) {
 }
 // The first block of QB queries whose accumulator holds dQ of the sinks already, in a
 // sequence of len rows; INT_MAX: none.
-template <bool kMod, bool kVar, int QB>
+template <bool kSink, int QB>
 __device__ __forceinline__ int sink_first_block(const BwdArgs& a, int len) {
-  return kMod && kVar && sink_sequence(a, len) ? (a.wl + 1) / kTile * (kTile / QB) : INT_MAX;
+  return kSink && sink_sequence(a, len) ? (a.wl + 1) / kTile * (kTile / QB) : INT_MAX;
 }
 // The first such tile.
 __device__ __forceinline__ int sink_first_tile(const BwdArgs& a) { return (a.wl + 1) / kTile; }

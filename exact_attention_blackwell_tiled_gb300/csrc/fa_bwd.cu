@@ -358,14 +358,18 @@ __device__ __forceinline__ void red_add(float* p, float x) {
 // zeros (load_rows); the dQ accumulators hold no padding rows, so a block's rows past
 // the end are not added.  kDet: the deterministic mode
 // (D = 64; at D = 128 it is the 128-row kernel's); a kernel of its own, since the
-// atomic mode's adds lost 13% of its rate to code that it does not run.
-template <int D, bool kMod, bool kVar, bool kDet>
+// atomic mode's adds lost 13% of its rate to code that it does not run.  kSink: a packed call
+// with sinks, an instance of its own for the same reason (16,384 tokens in 5 sequences, 16
+// heads of 128 under 1,023: 452 us of the whole backward with that code in every instance, 437
+// without).
+template <int D, bool kMod, bool kVar, bool kDet, bool kSink = false>
 __global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1)
     bwd_main(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
              const BwdArgs a, const __grid_constant__ Tails<kVar, 4> tails) {
   using L = BwdSmem<D>;
   static_assert(!kDet || D == 64, "D = 128 deterministic calls run the 128-row kernel");
+  static_assert(!kSink || (kMod && kVar), "sinks: packed calls under a window");
   using R = BwdRoles<bwd_wide(D, kMod, kVar)>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -922,7 +926,7 @@ __global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1
           if (!ok) break;
         }
       }
-      const int sunk = kDet ? sink_first_block<kMod, kVar, kQB>(a, w.kv_len) : INT_MAX;
+      const int sunk = kDet ? sink_first_block<kSink, kQB>(a, w.kv_len) : INT_MAX;
       for (int t = 0; t < (helper ? 0 : w.n_it); ++t, ++it) {
         const int gi = t / w.n_blk;
         const int iq = w.lo + (t - gi * w.n_blk);
@@ -1037,7 +1041,7 @@ __global__ void __launch_bounds__(BwdRoles<bwd_wide(D, kMod, kVar)>::kThreads, 1
           bwd_store_part(a, w, group, is_v, c, D, vk, sc, row0, Sk, lane);
           continue;
         }
-        if (kVar && kMod && w.j == 0 && wq * 32 < a.sinks && sink_sequence(a, w.kv_len))
+        if (kSink && w.j == 0 && wq * 32 < a.sinks && sink_sequence(a, w.kv_len))
           bwd_store_sinks(a, w, is_v, c, D, vk, sc, row0, lane);
         uint32_t wk[16];
 #pragma unroll
@@ -1411,7 +1415,8 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, const PlanArgs& p, i
                                   L::kAllocBytes) == cudaSuccess;
     };
     if (!set(bwd_main<D, false, true, false>) || !set(bwd_main<D, true, true, false>) ||
-        !set(bwd_main<D, false, true, kDet>) || !set(bwd_main<D, true, true, kDet>))
+        !set(bwd_main<D, false, true, kDet>) || !set(bwd_main<D, true, true, kDet>) ||
+        !set(bwd_main<D, true, true, false, true>) || !set(bwd_main<D, true, true, kDet, true>))
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
@@ -1433,9 +1438,12 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, const PlanArgs& p, i
   // is also the order of that mode's chain)
   a.dyn = 1;
   const bool mod = !(a.wl < 0 && (a.wr < 0 || (a.wr == 0 && a.causal)));
-  const auto kernel = kDet && a.deterministic
-                          ? (mod ? bwd_main<D, true, true, kDet> : bwd_main<D, false, true, kDet>)
-                          : (mod ? bwd_main<D, true, true, false> : bwd_main<D, false, true, false>);
+  const auto kernel = kDet && a.deterministic ? (a.sinks ? bwd_main<D, true, true, kDet, true>
+                                                 : mod   ? bwd_main<D, true, true, kDet>
+                                                         : bwd_main<D, false, true, kDet>)
+                                              : (a.sinks ? bwd_main<D, true, true, false, true>
+                                                 : mod   ? bwd_main<D, true, true, false>
+                                                         : bwd_main<D, false, true, false>);
   const int threads =
       bwd_wide(D, mod, true) ? BwdRoles<true>::kThreads : BwdRoles<false>::kThreads;
   record_timing(false, stream);

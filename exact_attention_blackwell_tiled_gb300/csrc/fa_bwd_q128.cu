@@ -133,8 +133,8 @@ static_assert(Q128Layout::kBytes <= kQ128MaxSmem, "q128 backward layout exceeds 
 
 }  // namespace
 
-// kVar: a packed batch, as in bwd_main.
-template <bool kMod, bool kVar>
+// kVar, kSink: a packed batch, and one with sinks, as in bwd_main.
+template <bool kMod, bool kVar, bool kSink = false>
 __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
     bwd_main_q128(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v,
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
         // query rows of the block that exist (kVar)
         const int n_rows = kVar ? w.kv_len - iq * kQB2 : kQB2;
         if (good) {
-          if (a.deterministic && turn == 0 && iq < sink_first_block<kMod, kVar, kQB2>(a, w.kv_len)) {
+          if (a.deterministic && turn == 0 && iq < sink_first_block<kSink, kQB2>(a, w.kv_len)) {
 #pragma unroll
             for (int e = 0; e < kQB2; ++e)
               if (!kVar || e < n_rows) dst[(size_t)e * D] = u2f(v[e]);
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(Q128Layout::kThreads, 1)
           bwd_store_part(a, w, group, is_v, c, D, vk, sc, row0, Sk, lane);
           continue;
         }
-        if (kVar && kMod && w.j == 0 && wq * 32 < a.sinks && sink_sequence(a, w.kv_len))
+        if (kSink && w.j == 0 && wq * 32 < a.sinks && sink_sequence(a, w.kv_len))
           bwd_store_sinks(a, w, is_v, c, D, vk, sc, row0, lane);
         uint32_t wk[16];
 #pragma unroll
@@ -807,20 +807,26 @@ static int launch_q128(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     if (cudaFuncSetAttribute(bwd_main_q128<false, kVar>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess ||
         cudaFuncSetAttribute(bwd_main_q128<true, kVar>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
+                             smem) != cudaSuccess ||
+        cudaFuncSetAttribute(bwd_main_q128<true, kVar, kVar>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return FA_ERR_CUDA;
     attr_done[dev] = true;
   }
-  const auto kernel = mod ? bwd_main_q128<true, kVar> : bwd_main_q128<false, kVar>;
+  const bool sinks = kVar && a.sinks > 0;
+  const auto kernel = sinks ? bwd_main_q128<true, kVar, kVar>
+                      : mod ? bwd_main_q128<true, kVar>
+                            : bwd_main_q128<false, kVar>;
   // the setmaxnreg split assumes exactly kRegsLaunch registers per thread at
   // launch: a different count could leave the drain warpgroup's request
   // unserved, so such a build is refused
-  static bool regs_ok[2] = {false, false};
-  if (!regs_ok[mod ? 1 : 0]) {
+  static bool regs_ok[3] = {false, false, false};
+  bool& ok = regs_ok[sinks ? 2 : mod ? 1 : 0];
+  if (!ok) {
     cudaFuncAttributes fattr;
     if (cudaFuncGetAttributes(&fattr, kernel) != cudaSuccess) return FA_ERR_CUDA;
     if (fattr.numRegs != Q128Layout::kRegsLaunch) return FA_ERR_UNSUPPORTED;
-    regs_ok[mod ? 1 : 0] = true;
+    ok = true;
   }
   cudaError_t e;
   if (a.deterministic) {
