@@ -197,9 +197,9 @@ __global__ void __launch_bounds__(256) bwd_preprocess(const BwdArgs a) {
 // taken, in fp32, from the O that the forward returned, which is rounded to bf16: for
 // rows with few keys that moves dS about as much as its own rounding to bf16 for the
 // products does (2^-9 of it each).
-template <int D>
+// kPlan: the plan too.
+template <int D, bool kPlan>
 __global__ void __launch_bounds__(256, 4) bwd_preprocess_var(const BwdArgs a, const PlanArgs p) {
-  __shared__ VarItem s_items[kBlockPlanItems];
   grid_dep_wait();
   grid_dep_launch();
   constexpr int kLanesPerRow = D / 8;
@@ -208,7 +208,10 @@ __global__ void __launch_bounds__(256, 4) bwd_preprocess_var(const BwdArgs a, co
   const int sub = lane / kLanesPerRow, seg = lane % kLanesPerRow;
   const VarItem* items = a.items;
   int n_items;
-  if (p.cu) {
+  if constexpr (kPlan) {
+    // (an instance of its own: 32 sequences of 60 tokens, 16 heads of 128, deterministic, whose
+    // plan is a launch, 58.1 -> 56.6 us)
+    __shared__ VarItem s_items[kBlockPlanItems];
     // the plan, here for the block itself and by block 0 for the kernels that follow
     n_items = plan_in_block(p, warp, 8, [&](int at, const VarItem& it) {
       s_items[at] = it;
@@ -1274,7 +1277,7 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_var(const BwdArgs a) {
             add_eight(x[e], reinterpret_cast<const float4*>(base + ((size_t)g * a.T + e * kRows) * D));
       __nv_bfloat16* out =
           reinterpret_cast<__nv_bfloat16*>(is_v ? a.dv : a.dk) + (i0 * a.Hkv + hk) * D + c8 * 8;
-      const int first = it.tile == 0 && sink_sequence(a, it.len) ? a.sinks : 0;  // (sum_sinks)
+      const int first = kSink && it.tile == 0 && sink_sequence(a, it.len) ? a.sinks : 0;  // (sum_sinks)
 #pragma unroll
       for (int e = 0; e < kPieces; ++e)
         if (r0 + e * kRows < rows && r0 + e * kRows >= first)
@@ -1425,7 +1428,8 @@ static int launch_bwd_var_d(const BwdVarMaps& m, BwdArgs a, const PlanArgs& p, i
   const int small_grid = (int)(q_units < 8LL * sms ? q_units : 8LL * sms);
   const long long units = a.dk_part ? q_units : kv_units;
   const int grid = (int)(units < sms ? units : sms);
-  if (launch_pdl(bwd_preprocess_var<D>, dim3(small_grid), dim3(256), 0, stream, a, p) != cudaSuccess)
+  const auto preprocess = p.cu ? bwd_preprocess_var<D, true> : bwd_preprocess_var<D, false>;
+  if (launch_pdl(preprocess, dim3(small_grid), dim3(256), 0, stream, a, p) != cudaSuccess)
     return FA_ERR_CUDA;
   if (a.sinks) {
     const int most = bwd_sink_blocks(D, a.sinks, sms);
