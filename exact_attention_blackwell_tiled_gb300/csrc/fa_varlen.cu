@@ -150,9 +150,9 @@ constexpr long long kSplitUnits = 608;
 // 9000 tokens in one 160 / 131 and 234 / 175, under 2000 350 / 360 (the rule's worst here)
 // and 446 / 426; 4000 in two, 14 / 2 heads, 100, 66.8 / 72.8 (taken) and 122.8 / 92.1.
 // (Calls without sinks keep theirs, and the order of their sums.)
-bool split_pays(int max_items, int Hq, int Hkv, int T, int D, int wl, int wr) {
+bool split_pays(int max_items, int Hq, int Hkv, int T, int D, int wl, int wr, long long sms) {
   if (wr < 0) return true;  // (units of any number of blocks)
-  const long long sms = 152, start = D == 128 ? 4 : 2;
+  const long long start = D == 128 ? 4 : 2;
   long long blocks = (128LL + wl + wr) / 64 + 1;
   if (blocks > T / 64 + 1) blocks = T / 64 + 1;
   const long long one = (max_items * (long long)Hkv + sms - 1) / sms * (Hq / Hkv * blocks + start);
@@ -178,8 +178,8 @@ int check_var(int B, int T, int Hq, int Hkv, int D) {
 // 100 23.6 / 19.5 and 20.7 / 17.5; 437 in one, 8 / 1 heads 13.6 / 11.8 and 11.7 / 10.2.  Where
 // sequences of one tile leave SMs without a unit, a unit of one head is done sooner: 10 of 44
 // tokens, 4 / 2 heads, 8.0 / 9.1 and 6.8 / 7.5.
-bool head_pairs(int B, int T, int Hq, int Hkv) {
-  return Hq / Hkv % 2 == 0 && (T >= 128LL * B || (T / 256 + (long long)B) * Hq > 152);
+bool head_pairs(int B, int T, int Hq, int Hkv, int sms) {
+  return Hq / Hkv % 2 == 0 && (T >= 128LL * B || (T / 256 + (long long)B) * Hq > sms);
 }
 
 // The sinks of a call that count: none where no window hides a key from any query.
@@ -323,6 +323,9 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   const VarLayout L = var_layout(B, T, Hq, Hkv, D, false, false, -1, 0);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   CUtensorMap maps[3];
   Tails<true, 2> tails;  // of v and k
@@ -338,7 +341,7 @@ int fa_fwd_varlen_sink(const void* q, const void* k, const void* v, void* o, flo
   a.wr = wr;
   a.causal = (wl < 0 && wr == 0) ? 1 : 0;
   a.sinks = seen;
-  a.head_pairs = (wl >= 0 || wr > 0) && head_pairs(B, T, Hq, Hkv) ? 1 : 0;
+  a.head_pairs = (wl >= 0 || wr > 0) && head_pairs(B, T, Hq, Hkv, info.sm_count) ? 1 : 0;
   p.cu = cu_seqlens;
   p.B = B;
   p.T = T;
@@ -409,6 +412,9 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
   const VarLayout L = var_layout(B, T, Hq, Hkv, D, true, deterministic != 0, wl, seen);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < L.total) return FA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
+  int dev;
+  DeviceInfo info;
+  if (!current_device(&dev, &info)) return FA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   BwdVarMaps m;
   CUtensorMap* const maps[4] = {&m.q, &m.k, &m.v, &m.dO};
@@ -441,7 +447,7 @@ int fa_bwd_varlen_sink(const void* q, const void* k, const void* v, const void* 
   a.delta = reinterpret_cast<float*>(ws + L.off_delta);
   a.lse2 = reinterpret_cast<float*>(ws + L.off_lse2);
   a.sem = reinterpret_cast<int*>(ws + L.off_sem);
-  const bool split = L.split && (seen == 0 || split_pays(L.max_items, Hq, Hkv, T, D, a.wl, a.wr));
+  const bool split = L.split && (seen == 0 || split_pays(L.max_items, Hq, Hkv, T, D, a.wl, a.wr, info.sm_count));
   if (split) {
     a.dk_part = reinterpret_cast<float*>(ws + L.off_dk);
     a.dv_part = reinterpret_cast<float*>(ws + L.off_dv);
