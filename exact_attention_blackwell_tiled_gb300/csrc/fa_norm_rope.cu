@@ -16,7 +16,7 @@
 // multiplied by the weights, once for all their heads (once a step: 73 us instead of 64 for
 // the prompt below); where tokens are few their steps are dealt to several warps.  The
 // grid stays, and each warp keeps the rows of its next 8 (backward 4) steps on their way to
-// shared memory, some 64 KB an SM.  dw: sums per lane over all rows that it meets, then over
+// shared memory, 64 KB a block, 128 KB an SM.  dw: sums per lane over all rows that it meets, then over
 // the lanes and warps of a block in shared memory; a second kernel adds the blocks', always
 // in the same order.
 //

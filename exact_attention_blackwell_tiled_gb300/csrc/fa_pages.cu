@@ -14,16 +14,16 @@
 //
 // A few kilobytes move: the time is a launch and a chain of dependent steps.  One block or
 // one cluster of blocks does all that the sums are needed for, so that no second launch
-// stands between: a warp counts a sequence's entries, the blocks' sums meet in shared memory
-// of the cluster, and two barriers of the cluster stand where a page that came back may be
-// taken by another block's sequence.  Only many new tokens' positions and slots take a
+// stands between: a warp counts a sequence's entries (up to 32 warps share one where a block has
+// few), the blocks' sums meet in shared memory of the cluster, and two barriers of the
+// cluster stand where a page that came back may be taken by another block's sequence.  Only many new tokens' positions and slots take a
 // second launch, for the whole GPU's stores.
 //
 // The hidden entries are read in every call, for any of them may still hold a page (it
 // may have been taken without the window): 4 bytes for each page's tokens of the past.
 //
-// Measured: 64 sequences that grow by a token under a window of 4,096 (one block) 5.7 us, 8
-// cold; 1,024 sequences, 244,000 new tokens, 17 us and 9 for the second launch (one launch
+// Measured: 64 sequences that grow by a token under a window of 4,096 (one block) 5.2 us, 8
+// cold; 1,024 sequences, 244,000 new tokens, 15 us and 8 for the second launch (one launch
 // for all: 48).
 #include <cuda_runtime.h>
 

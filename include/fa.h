@@ -393,8 +393,9 @@ int fa_cache4_append_slots(void* cache, int num_pages, int page_size, const void
  * free_count outside [0, num_pages] is cut and recorded; fa_cache4_status returns
  * FA_ERR_INVALID_ARG for all of these.
  * A page belongs to one entry of one table: one that two entries hold comes back twice.
+ * A table begins as -1 throughout.
  * page_size 16, 32, 64 or 128; 1 <= B <= 65536; B * table_width below 2^30, num_pages at most
- * 2^30; int32 arrays 4-byte, slots 8-byte aligned.  One launch (two from 8193 rows on), no
+ * 2^30, T any; int32 arrays 4-byte, slots 8-byte aligned.  One launch (two from 8193 rows on), no
  * workspace; calls on the same tables or stack follow one another.
  */
 int fa_page_update(int* page_table, int table_width, int* free_pages, int* free_count,
