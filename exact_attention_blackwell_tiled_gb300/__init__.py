@@ -650,8 +650,9 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight
               interleaved: bool = False):
     """norm_rope_fwd as a differentiable op: gradients for q, k and the weights (those in the
     weights' type).  Tokens with a negative position get zeros in the results and in every
-    gradient.  The gradients cannot be differentiated again (RuntimeError).  Returns (q, k)
-    bf16, contiguous."""
+    gradient.  A training step can be captured into a CUDA graph, as with attention_varlen.
+    The gradients cannot be differentiated again (RuntimeError).  Returns (q, k) bf16,
+    contiguous."""
     return _NormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
 
 
@@ -702,7 +703,8 @@ def page_update(page_table: torch.Tensor, free_pages: torch.Tensor, free_count: 
     ``lens``, ``new_lens`` int32 [B]: tokens held and to be held.  Entries past the new
     length, and those that a window of ``window_left`` tokens with ``sinks`` hides from the
     last token's query on, give their pages back; entries for new tokens take pages.  A
-    page belongs to one entry: tables that share pages are not for this call.
+    page belongs to one entry: tables that share pages are not for this call.  A table
+    begins as -1 everywhere.
     Returns (cu_seqlens int32 [B+1], positions int32 [T], slots int64 [T]) of the new
     tokens, packed in order; ``T`` is the rows they have, and rows past the last get -1.
     cache4_status() reports a pool or T that was too small, and lengths past the table.
