@@ -485,7 +485,8 @@ int fa_cache4_status(fa_stream_t stream);
  *   r = 1 / sqrt(mean_d x_d^2 + eps),  n_d = x_d r w_d, and of the first `rot` elements the
  *   pairs (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) where interleaved != 0, i < rot / 2:
  *   y_a = n_a cos[p][i] - n_b sin[p][i],  y_b = n_b cos[p][i] + n_a sin[p][i];  y_d = n_d beyond
- * in fp32, rounded once to bf16.
+ * in fp32, rounded once to bf16 (the squares' sum too, which is infinite from elements of some
+ * 2^60 on: such a row's results are zeros).
  *   q [T, Hq, D], k [T, Hkv, D] bf16, rows and heads apart by *_stride (multiples of 8
  *     elements; null: contiguous), and q_out, k_out likewise (at least D apart); q_out may be
  *     q itself and k_out k, with the same strides;
