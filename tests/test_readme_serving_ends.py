@@ -12,13 +12,14 @@ from test_readme_serving import README, _loop
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("padded", [False, True])  # a row for every sequence in every step
 @pytest.mark.parametrize("lens,ends,count", [
     ([300, 17, 129], [40, 20, 60], 60),      # the second one ends first, then the first
     ([300, 17, 129], [60, 60, 1], 60),       # the last one after a single token
     ([2, 0], [30, 30], 30),                  # prompts of two tokens in all, for two sequences
     ([1, 1, 1, 1], [5, 100, 7, 9], 100),     # one is left on its own
 ])
-def test_sequences_that_end(lens, ends, count):
+def test_sequences_that_end(lens, ends, count, padded):
     __graft_entry__.build()
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
@@ -44,8 +45,9 @@ def test_sequences_that_end(lens, ends, count):
         for i in range(count):
             going = [b for b in range(B) if i < ends[b]]
             new = [len(held[b][0]) + 1 if b in going else 0 for b in range(B)]
-            yield len(going), i32(new), projection(len(going))
-            assert ns["o"].shape[0] == len(going)
+            T = B if padded else len(going)
+            yield T, i32(new), projection(T)
+            assert ns["o"].shape[0] == T
             for row, b in enumerate(going):
                 held[b] = tuple(torch.cat((x, ns[y][row:row + 1].cpu())) for x, y in zip(held[b], "kv"))
                 kk, vv = held[b]
