@@ -15,6 +15,8 @@ def gpu():
         pytest.skip("no CUDA device")
     if torch.cuda.mem_get_info()[0] < 40 * 2 ** 30:
         pytest.skip("less than 40 GB free")
+    yield
+    torch.cuda.empty_cache()
 
 
 def _sample(n):
